@@ -504,6 +504,160 @@ idx_status idx_q_rope_quant(const uint16_t *q, const int32_t *positions, const f
                             float *weights_out, idx_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Latent attention: the layer the ragged slots are for.  A token is cached
+ * as one latent vector of L = 512 elements, which serves every head as key
+ * and as value, and rope_dim = 64 rotated elements, which are key only.
+ * These calls have no counterpart in the pages (their latent attention is a
+ * vendor library's); layouts and conventions follow the indexer's own cache.
+ *
+ * Block-flat pages, page p at kv_pages + p * page_stride_bytes (16-byte
+ * aligned, stride a multiple of 16 and at least the page's bytes):
+ *   IDX_LATENT_BF16      page_size * 576 bf16 (token-major: latents, then
+ *                        the rotated elements): 1152 bytes a token.
+ *   IDX_LATENT_FP8_E4M3  page_size * 512 e4m3, then page_size * 64 bf16
+ *                        rotated elements, then page_size * 8 e8m0 scales
+ *                        (one per 64 latents): 648 bytes a token.  The value
+ *                        of a code is code * 2^(scale - 127); the reader
+ *                        takes it in bf16, which holds it exactly.
+ * ---------------------------------------------------------------------- */
+typedef enum { IDX_LATENT_BF16 = 0, IDX_LATENT_FP8_E4M3 = 1 } idx_latent_format;
+
+/* ------------------------------------------------------------------------
+ * idx_latent_store -- normalise, rotate, quantise and write new tokens into
+ * their cache slots.
+ *
+ *   kv          bf16 bits [T, ld_kv], ld_kv >= 576: 512 latents, then 64
+ *               elements to rotate.  16-byte aligned, ld_kv a multiple of 8.
+ *   positions, cos_sin, ld_cos_sin, num_positions  as idx_k_norm_rope_store
+ *               (rows cos | sin of rope_dim / 2 each, pairs (2i, 2i + 1));
+ *               cos_sin NULL: the elements are stored as they are, positions
+ *               are not read.
+ *   norm_weight fp32 [512], 16-byte aligned; eps >= 0: the latents become
+ *               x / sqrt(mean(x^2) + eps) * norm_weight.  NULL: no norm.
+ *   slot_mapping [T] int64: page * page_size + offset; negative skips.
+ *   FP8: one exponent per 64 latents, bits = clamp(ceil(log2(max(amax,
+ *   2^-126) / 448)) + 127, 0, 254), codes of y * 2^(127 - bits) to nearest
+ *   even; a group holding a NaN or an infinity gets the e8m0 NaN (255).
+ * Supported: L = 512, rope_dim = 64.  A slot outside the pool sets
+ * IDX_DEV_BAD_PAGE, a position outside the table IDX_DEV_BAD_POSITION; those
+ * tokens are skipped.  Two tokens with one slot race.
+ * ---------------------------------------------------------------------- */
+idx_status idx_latent_store(const uint16_t *kv, int64_t ld_kv, const int32_t *positions,
+                            const float *cos_sin, int64_t ld_cos_sin, int num_positions,
+                            const float *norm_weight, float eps, int T, int L, int rope_dim,
+                            idx_latent_format fmt, uint8_t *kv_pages, int64_t page_stride_bytes,
+                            int num_pages, int page_size, const int64_t *slot_mapping,
+                            idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_latent_gather -- read cached tokens back as rows of bf16, for the
+ * up-projection of the expanded form.
+ *
+ *   block_table [B, bt_stride], max_blocks columns of it valid.
+ *   cu_lens     int32 [B + 1], ascending from 0: rows [cu_lens[b],
+ *               cu_lens[b + 1]) of out are the tokens seq_starts[b],
+ *               seq_starts[b] + 1, ... of sequence b.
+ *   seq_starts  int32 [B] or NULL (0).
+ *   N           rows of out; rows at or past cu_lens[B] are not written.
+ *   out         bf16 bits [N, ld_out], ld_out >= 576 a multiple of 8,
+ *               16-byte aligned: latents, then the rotated elements.
+ * A token whose page is outside the table or the pool is written as zeros
+ * and sets IDX_DEV_BAD_PAGE.  Supported: L = 512, rope_dim = 64.
+ * ---------------------------------------------------------------------- */
+idx_status idx_latent_gather(const uint8_t *kv_pages, int64_t page_stride_bytes, int num_pages,
+                             int page_size, idx_latent_format fmt, int L, int rope_dim,
+                             const int32_t *block_table, int64_t bt_stride, int max_blocks,
+                             const int32_t *cu_lens, const int32_t *seq_starts, int B, int N,
+                             uint16_t *out, int64_t ld_out, idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_latent_attention -- absorbed latent attention over ragged slots (the
+ * output of idx_topk_ragged_slots):
+ *     s = scale * (q[r, h, :] . token),  out[r, h, :] = sum softmax(s) token[:512]
+ *
+ *   q         bf16 bits [R, H, 576] with strides ldq_row, ldq_head (elements,
+ *             multiples of 8; 16-byte aligned): 512 latents, 64 rotated.
+ *   slots     int32, num_slots of them; row r attends to slots[indptr[r]]
+ *             .. slots[indptr[r + 1] - 1] (a slot listed twice counts twice).
+ *   indptr    int32 [R + 1], ascending; values are clamped to [0, num_slots].
+ *   scale     multiplies the scores, > 0.
+ *   out       bf16 bits [R, H, 512] with strides ldo_row, ldo_head (multiples
+ *             of 8, 16-byte aligned).
+ *   lse       fp32 [R, ld_lse] natural logarithm of the sum of exp(s), or
+ *             NULL.  A row with no token gets zeros and -inf.
+ *   ws, ws_bytes  device scratch, 16-byte aligned, of at least
+ *             idx_latent_attention_workspace_size(R, H) bytes.  Calls that
+ *             share one ws must not overlap in time.
+ * A slot outside the pool is left out of its row and sets IDX_DEV_BAD_PAGE.
+ * The sums run in fp32, the weights enter the second product in bf16; the
+ * order of the sums depends on the arguments and the lengths alone.
+ * Supported: L = 512, rope_dim = 64, 1 <= H <= 128.
+ * Errors: IDX_ERR_INVALID_ARG, IDX_ERR_UNSUPPORTED (sizes, alignment),
+ * IDX_ERR_WORKSPACE (ws missing or too small), IDX_ERR_CUDA.
+ * ---------------------------------------------------------------------- */
+idx_status idx_latent_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                                const uint8_t *kv_pages, int64_t page_stride_bytes, int num_pages,
+                                int page_size, idx_latent_format fmt, const int32_t *slots,
+                                const int32_t *indptr, int64_t num_slots, int R, int H, int L,
+                                int rope_dim, float scale, uint16_t *out, int64_t ldo_row,
+                                int64_t ldo_head, float *lse, int64_t ld_lse, void *ws,
+                                size_t ws_bytes, idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_paged_latent_attention -- the same over whole contexts: row j of
+ * sequence b (B * next_n rows) attends to its tokens [0, ke), ke as in
+ * idx_paged_mqa_logits (context_lens, ctx_per_row), clamped to
+ * [0, max_model_len]; token t is in page block_table[b, t / page_size],
+ * bt_stride >= ceil(max_model_len / page_size).  Tokens of a page outside
+ * the pool are left out and set IDX_DEV_BAD_PAGE.
+ * ---------------------------------------------------------------------- */
+idx_status idx_paged_latent_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                                      const uint8_t *kv_pages, int64_t page_stride_bytes,
+                                      int num_pages, int page_size, idx_latent_format fmt,
+                                      const int32_t *block_table, int64_t bt_stride,
+                                      const int32_t *context_lens, int ctx_per_row, int B,
+                                      int next_n, int max_model_len, int H, int L, int rope_dim,
+                                      float scale, uint16_t *out, int64_t ldo_row,
+                                      int64_t ldo_head, float *lse, int64_t ld_lse, void *ws,
+                                      size_t ws_bytes, idx_stream_t stream);
+
+/* Bytes of ws for R rows of H heads on the current device (its SM count). */
+size_t idx_latent_attention_workspace_size(int R, int H);
+
+/* ------------------------------------------------------------------------
+ * idx_latent_prefill -- the expanded form: attention of ragged sequences
+ * with keys of 128 own elements a head and 64 rotated ones shared by all
+ * heads, and values of 128 elements a head.
+ *
+ *   q       bf16 bits [Tq, H, 192] (128, then 64 rotated), strides ldq_row,
+ *           ldq_head.
+ *   k       bf16 bits [Tk, H, 128], strides ldk_row, ldk_head.
+ *   k_rope  bf16 bits [Tk, 64], row stride ld_rope.
+ *   v       bf16 bits [Tk, H, 128], strides ldv_row, ldv_head.
+ *   cu_q, cu_k  int32 [B + 1], ascending from 0, ends at most Tq and Tk: the
+ *           rows of each sequence.  causal: query i of a sequence with Lq
+ *           queries and Lk keys attends to keys [0, i + Lk - Lq], so the
+ *           last query sees every key; otherwise to all Lk.
+ *   out     bf16 bits [Tq, H, 128], strides ldo_row, ldo_head.
+ *   lse     fp32 [Tq, ld_lse] (ld_lse >= H) or NULL, as idx_latent_attention.
+ *           A query with no key gets zeros and -inf; rows of q outside every
+ *           sequence are not written.
+ * Every stride is a multiple of 8 elements and every pointer 16-byte
+ * aligned.  Keys and values past a sequence's end (another sequence's) never
+ * enter its results, whatever they hold; within a sequence a value that is
+ * not finite may reach queries that the causal mask hides it from.
+ * Supported: d_nope = d_v = 128, d_rope = 64, H <= 65535.
+ * ---------------------------------------------------------------------- */
+idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                              const uint16_t *k, int64_t ldk_row, int64_t ldk_head,
+                              const uint16_t *k_rope, int64_t ld_rope, const uint16_t *v,
+                              int64_t ldv_row, int64_t ldv_head, const int32_t *cu_q,
+                              const int32_t *cu_k, int B, int Tq, int Tk, int H, int d_nope,
+                              int d_rope, int d_v, float scale, int causal, uint16_t *out,
+                              int64_t ldo_row, int64_t ldo_head, float *lse, int64_t ld_lse,
+                              idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * idx_get_device_status -- read and clear the sticky device status word of
  * the current device (IDX_DEV_* bits).  Synchronises `stream`; it is the
  * only call that does.  *out receives the bits.

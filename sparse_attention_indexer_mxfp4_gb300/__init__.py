@@ -10,15 +10,24 @@ from ._binding import (  # noqa: F401
     FMT_FP8,
     FMT_MXFP4,
     IndexerError,
+    LATENT_BF16,
+    LATENT_FP8,
     idx_apply_candidate_mask,
     idx_fill_logits_tail,
     idx_get_device_status,
+    idx_latent_attention,
+    idx_latent_gather,
+    idx_latent_prefill,
+    idx_latent_store,
     idx_mqa_logits,
+    idx_paged_latent_attention,
     idx_paged_mqa_logits,
     idx_row_ends,
     idx_topk,
     idx_topk_ragged_slots,
     idx_topk_to_ragged_slots,
+    latent_attention_workspace_size,
+    latent_page_bytes,
     lib,
     library_path,
     version,

@@ -18,6 +18,10 @@ from . import build as _build
 
 FMT_FP8 = 0
 FMT_MXFP4 = 1
+LATENT_BF16 = 0
+LATENT_FP8 = 1
+LATENT_DIM = 512  # latents of a cached token
+LATENT_ROPE = 64  # its rotated elements
 
 IDX_OK = 0
 _ERRORS = {1: "IDX_ERR_INVALID_ARG", 2: "IDX_ERR_UNSUPPORTED", 3: "IDX_ERR_WORKSPACE",
@@ -54,6 +58,15 @@ _SIGNATURES = {
                               _L, _I, _I, _P, _P],
     "idx_q_rope_quant": [_P, _P, _P, _L, _I, _I, _P, ctypes.c_float, _I, _I, _I, _I, _P, _P, _P,
                          _P],
+    "idx_latent_store": [_P, _L, _P, _P, _L, _I, _P, ctypes.c_float, _I, _I, _I, _I, _P, _L, _I,
+                         _I, _P, _P],
+    "idx_latent_gather": [_P, _L, _I, _I, _I, _I, _I, _P, _L, _I, _P, _P, _I, _I, _P, _L, _P],
+    "idx_latent_attention": [_P, _L, _L, _P, _L, _I, _I, _I, _P, _P, _L, _I, _I, _I, _I,
+                             ctypes.c_float, _P, _L, _L, _P, _L, _P, _S, _P],
+    "idx_paged_latent_attention": [_P, _L, _L, _P, _L, _I, _I, _I, _P, _L, _P, _I, _I, _I, _I, _I,
+                                   _I, _I, ctypes.c_float, _P, _L, _L, _P, _L, _P, _S, _P],
+    "idx_latent_prefill": [_P, _L, _L, _P, _L, _L, _P, _L, _P, _L, _L, _P, _P, _I, _I, _I, _I, _I,
+                           _I, _I, ctypes.c_float, _I, _P, _L, _L, _P, _L, _P],
     "idx_get_device_status": [_P, ctypes.POINTER(ctypes.c_uint32)],
     "idx_debug_wait_expiry": [_I, ctypes.c_uint64, _P],
     "idx_row_ends": [_P, _I, _I, _I, _I, _P, _P],
@@ -87,6 +100,8 @@ def lib() -> ctypes.CDLL:
             L.idx_version.restype = ctypes.c_char_p
             L.idx_topk_workspace_size.argtypes = [_I, _L, _I]
             L.idx_topk_workspace_size.restype = _S
+            L.idx_latent_attention_workspace_size.argtypes = [_I, _I]
+            L.idx_latent_attention_workspace_size.restype = _S
             L.idx_paged_mqa_logits_workspace_size.argtypes = [_I, _I, _I, _I]
             L.idx_paged_mqa_logits_workspace_size.restype = _S
             _lib = L
@@ -566,6 +581,226 @@ def idx_fill_logits_tail(logits, row_ends, width=None, stream=None):
     _check(lib().idx_fill_logits_tail(_ptr(logits), logits.stride(0), logits.shape[0],
                                       _ptr(row_ends), width, _stream(stream)),
            "idx_fill_logits_tail")
+
+
+def latent_page_bytes(page_size, fmt) -> int:
+    """Bytes of a latent-cache page, rounded up to the 16 bytes a page stride needs."""
+    token = 2 * (LATENT_DIM + LATENT_ROPE) if fmt == LATENT_BF16 else (
+        LATENT_DIM + 2 * LATENT_ROPE + LATENT_DIM // 64)
+    return -(-page_size * token // 16) * 16
+
+
+def _need_pages(t):
+    if t.dtype != torch.uint8 or t.dim() != 2 or t.stride(1) != 1:
+        raise ValueError("kv_pages must be uint8 [num_pages, page_stride] with unit byte stride")
+
+
+def _need_heads(t, dims, dim, name):
+    """bf16, `dims` dimensions, the last one of `dim` contiguous elements."""
+    if t.dtype != torch.bfloat16 or t.dim() != dims or t.shape[-1] != dim or t.stride(-1) != 1:
+        raise ValueError(f"{name} must be bfloat16 [..., {dim}] of {dims} dimensions with unit "
+                         "last stride")
+
+
+def _out_lse(out, lse, rows, heads, dim, device):
+    """The outputs of an attention call, made here unless given; lse False: none."""
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=device)
+    else:
+        _need_heads(out, 3, dim, "out")
+        if out.shape[0] != rows or out.shape[1] != heads:
+            raise ValueError(f"out must be [{rows}, {heads}, {dim}]")
+    if lse is False:
+        return out, None
+    if lse is None:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
+    elif (lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.stride(1) != 1):
+        raise ValueError(f"lse must be float32 [{rows}, {heads}] with unit column stride")
+    return out, lse
+
+
+def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
+                         slot_mapping, fmt):
+    """New tokens into the latent cache.  kv bf16 [T, 576] (512 latents, 64
+    elements to rotate; row stride free); positions int32 [T] and cos_sin fp32
+    [P, 64] (both None: stored as they are); norm_weight fp32 [512] (None: no
+    norm); slot_mapping int64 [T], negative skips."""
+    _need_heads(kv, 2, LATENT_DIM + LATENT_ROPE, "kv")
+    _need(slot_mapping, torch.int64, "slot_mapping")
+    _need_pages(kv_pages)
+    T = kv.shape[0]
+    if slot_mapping.numel() != T:
+        raise ValueError(f"slot_mapping must hold {T} entries")
+    if (cos_sin is None) != (positions is None):
+        raise ValueError("positions and cos_sin come together")
+    rows, ld = 0, 0
+    if cos_sin is not None:
+        _need(positions, torch.int32, "positions")
+        if positions.numel() != T:
+            raise ValueError(f"positions must hold {T} entries")
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.stride(1) != 1 or (
+                cos_sin.shape[1] < LATENT_ROPE):
+            raise ValueError(f"cos_sin must be float32 [positions, {LATENT_ROPE}]")
+        rows, ld = cos_sin.shape[0], cos_sin.stride(0)
+    if norm_weight is not None:
+        _need(norm_weight, torch.float32, "norm_weight")
+        if norm_weight.numel() != LATENT_DIM:
+            raise ValueError(f"norm_weight must hold {LATENT_DIM} entries")
+    args = (_ptr(kv), kv.stride(0), _ptr(positions), _ptr(cos_sin), ld, rows, _ptr(norm_weight),
+            float(eps), T, LATENT_DIM, LATENT_ROPE, fmt, _ptr(kv_pages), kv_pages.stride(0),
+            kv_pages.shape[0], page_size, _ptr(slot_mapping))
+    return Prepared("idx_latent_store", args,
+                    (kv, positions, cos_sin, norm_weight, kv_pages, slot_mapping))
+
+
+def idx_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size, slot_mapping,
+                     fmt, stream=None):
+    prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
+                         slot_mapping, fmt)(stream)
+
+
+def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None):
+    """Cached tokens back as rows of out (bf16 [N, 576], row stride free):
+    rows cu_lens[b] .. cu_lens[b + 1] are sequence b's tokens from
+    seq_starts[b] (None: 0) on.  cu_lens int32 [B + 1], seq_starts int32 [B]."""
+    _need_pages(kv_pages)
+    _need_heads(out, 2, LATENT_DIM + LATENT_ROPE, "out")
+    _need(block_table, torch.int32, "block_table")
+    _need(cu_lens, torch.int32, "cu_lens")
+    B_ = cu_lens.numel() - 1
+    if block_table.dim() != 2 or block_table.shape[0] < B_ or B_ < 0:
+        raise ValueError("block_table must be [B, blocks] and cu_lens [B + 1]")
+    if seq_starts is not None:
+        _need(seq_starts, torch.int32, "seq_starts")
+        if seq_starts.numel() != B_:
+            raise ValueError(f"seq_starts must hold {B_} entries")
+    args = (_ptr(kv_pages), kv_pages.stride(0), kv_pages.shape[0], page_size, fmt, LATENT_DIM,
+            LATENT_ROPE, _ptr(block_table), block_table.stride(0), block_table.shape[1],
+            _ptr(cu_lens), _ptr(seq_starts), B_, out.shape[0], _ptr(out), out.stride(0))
+    return Prepared("idx_latent_gather", args, (kv_pages, block_table, cu_lens, seq_starts, out))
+
+
+def idx_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None,
+                      stream=None):
+    prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts)(stream)
+    return out
+
+
+def latent_attention_workspace_size(rows, heads) -> int:
+    """Bytes of device scratch of the absorbed attention on the current device."""
+    return int(lib().idx_latent_attention_workspace_size(rows, heads))
+
+
+def _latent_ws(workspace, rows, heads, device):
+    if workspace is True:
+        return torch.empty(latent_attention_workspace_size(rows, heads), dtype=torch.uint8,
+                           device=device)
+    return workspace
+
+
+def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
+                             workspace=True):
+    """Absorbed latent attention over ragged slots.  q bf16 [R, H, 576] (row
+    and head strides free); slots int32, indptr int32 [R + 1]; out bf16
+    [R, H, 512] and lse fp32 [R, H] are made here when None (lse False:
+    none).  workspace: True allocates the scratch here, or a uint8 tensor of
+    latent_attention_workspace_size(R, H) bytes."""
+    _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
+    _need_pages(kv_pages)
+    _need(slots, torch.int32, "slots")
+    _need(indptr, torch.int32, "indptr")
+    R, H = q.shape[0], q.shape[1]
+    if indptr.numel() != R + 1:
+        raise ValueError(f"indptr must hold {R + 1} entries")
+    out, lse = _out_lse(out, lse, R, H, LATENT_DIM, q.device)
+    ws = _latent_ws(workspace, R, H, q.device)
+    args = (_ptr(q), q.stride(0), q.stride(1), _ptr(kv_pages), kv_pages.stride(0),
+            kv_pages.shape[0], page_size, fmt, _ptr(slots), _ptr(indptr), slots.numel(), R, H,
+            LATENT_DIM, LATENT_ROPE, scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
+            0 if lse is None else lse.stride(0), _ptr(ws), 0 if ws is None else ws.numel())
+    return Prepared("idx_latent_attention", args, (q, kv_pages, slots, indptr, out, lse, ws))
+
+
+def idx_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
+                         workspace=True, stream=None):
+    """(out, lse) of the absorbed attention over ragged slots."""
+    call = prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out, lse,
+                                    workspace)
+    call(stream)
+    return call.keep[4], call.keep[5]
+
+
+def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
+                                   scale, max_model_len, ctx_per_row=False, out=None, lse=None,
+                                   workspace=True):
+    """Absorbed latent attention over whole paged contexts: row j of sequence
+    b attends to its first context_lens[b] - next_n + j + 1 tokens (or
+    context_lens[row] with ctx_per_row).  q bf16 [B * next_n, H, 576]."""
+    _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
+    _need_pages(kv_pages)
+    _need(block_table, torch.int32, "block_table")
+    _need(context_lens, torch.int32, "context_lens")
+    R, H = q.shape[0], q.shape[1]
+    if next_n <= 0 or R % next_n:
+        raise ValueError("q must hold B * next_n rows")
+    B_ = R // next_n
+    want = R if ctx_per_row else B_
+    if context_lens.numel() != want:
+        raise ValueError(f"context_lens must hold {want} entries")
+    if block_table.dim() != 2 or block_table.shape[0] < B_:
+        raise ValueError(f"block_table must be [{B_}, blocks]")
+    out, lse = _out_lse(out, lse, R, H, LATENT_DIM, q.device)
+    ws = _latent_ws(workspace, R, H, q.device)
+    args = (_ptr(q), q.stride(0), q.stride(1), _ptr(kv_pages), kv_pages.stride(0),
+            kv_pages.shape[0], page_size, fmt, _ptr(block_table), block_table.stride(0),
+            _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len, H, LATENT_DIM,
+            LATENT_ROPE, scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
+            0 if lse is None else lse.stride(0), _ptr(ws), 0 if ws is None else ws.numel())
+    return Prepared("idx_paged_latent_attention", args,
+                    (q, kv_pages, block_table, context_lens, out, lse, ws))
+
+
+def idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
+                               scale, max_model_len, ctx_per_row=False, out=None, lse=None,
+                               workspace=True, stream=None):
+    """(out, lse) of the absorbed attention over whole paged contexts."""
+    call = prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens,
+                                          next_n, scale, max_model_len, ctx_per_row, out, lse,
+                                          workspace)
+    call(stream)
+    return call.keep[4], call.keep[5]
+
+
+def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None):
+    """Expanded latent attention of ragged sequences.  q bf16 [Tq, H, 192]
+    (128, then 64 rotated), k bf16 [Tk, H, 128], k_rope bf16 [Tk, 64], v bf16
+    [Tk, H, 128], every outer stride free; cu_q, cu_k int32 [B + 1]; out bf16
+    [Tq, H, 128] and lse fp32 [Tq, H] as in prepare_latent_attention."""
+    _need_heads(q, 3, 192, "q")
+    _need_heads(k, 3, 128, "k")
+    _need_heads(k_rope, 2, LATENT_ROPE, "k_rope")
+    _need_heads(v, 3, 128, "v")
+    _need(cu_q, torch.int32, "cu_q")
+    _need(cu_k, torch.int32, "cu_k")
+    Tq, H, Tk = q.shape[0], q.shape[1], k.shape[0]
+    if k.shape[1] != H or v.shape[1] != H or v.shape[0] != Tk or k_rope.shape[0] != Tk:
+        raise ValueError("k, k_rope and v must hold the same tokens, and the heads of q")
+    if cu_q.numel() != cu_k.numel() or cu_q.numel() < 1:
+        raise ValueError("cu_q and cu_k must both hold B + 1 entries")
+    out, lse = _out_lse(out, lse, Tq, H, 128, q.device)
+    args = (_ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), k.stride(1), _ptr(k_rope),
+            k_rope.stride(0), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k),
+            cu_q.numel() - 1, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal), _ptr(out),
+            out.stride(0), out.stride(1), _ptr(lse), 0 if lse is None else lse.stride(0))
+    return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse))
+
+
+def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                       stream=None):
+    """(out, lse) of the expanded attention of ragged sequences."""
+    call = prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse)
+    call(stream)
+    return call.keep[6], call.keep[7]
 
 
 def idx_debug_wait_expiry(which: int, limit_ns: int, stream=None):

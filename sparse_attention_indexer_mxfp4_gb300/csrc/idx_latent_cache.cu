@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kCacheThreads)
         const float a = lo_float(rope), b = hi_float(rope);
         const uint32_t turned = pack_bf16(a * c - b * s, b * c + a * s);
         uint8_t *page = const_cast<uint8_t *>(pool.base) + page_byte;
-        if (!FP8) {
+        if constexpr (!FP8) {
             uint8_t *tok = page + (int64_t)off * kLatBf16TokBytes;
             #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -135,44 +135,44 @@ __global__ void __launch_bounds__(kCacheThreads)
                                pack_bf16(y[8 * h + 4], y[8 * h + 5]),
                                pack_bf16(y[8 * h + 6], y[8 * h + 7]));
             *reinterpret_cast<uint32_t *>(tok + 2 * kLatent + 4 * lane) = turned;
-            continue;
-        }
-        int bits[2];
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float amax = 0.0f;
-            bool bad = false;
+        } else {
+            int bits[2];
             #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                amax = fmaxf(amax, fabsf(y[8 * h + i]));
-                bad |= y[8 * h + i] != y[8 * h + i];  // fmaxf drops a NaN
+            for (int h = 0; h < 2; ++h) {
+                float amax = 0.0f;
+                bool bad = false;
+                #pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    amax = fmaxf(amax, fabsf(y[8 * h + i]));
+                    bad |= y[8 * h + i] != y[8 * h + i];  // fmaxf drops a NaN
+                }
+                amax = bad ? __int_as_float(0x7f800000) : amax;
+                #pragma unroll
+                for (int o = 1; o < 8; o <<= 1)
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                bits[h] = group_bits(amax);
+                const float inv = group_inverse(bits[h]);
+                uint32_t code[2];
+                #pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float *v = y + 8 * h + 4 * q;
+                    const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv),
+                                                                __NV_SATFINITE, __NV_E4M3);
+                    const uint32_t u = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv),
+                                                                __NV_SATFINITE, __NV_E4M3);
+                    code[q] = l | u << 16;
+                }
+                *reinterpret_cast<uint2 *>(page + (int64_t)off * kLatent + 256 * h + 8 * lane) =
+                    make_uint2(code[0], code[1]);
             }
-            amax = bad ? __int_as_float(0x7f800000) : amax;
-            #pragma unroll
-            for (int o = 1; o < 8; o <<= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-            bits[h] = group_bits(amax);
-            const float inv = group_inverse(bits[h]);
-            uint32_t code[2];
-            #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float *v = y + 8 * h + 4 * q;
-                const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv),
-                                                            __NV_SATFINITE, __NV_E4M3);
-                const uint32_t u = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv),
-                                                            __NV_SATFINITE, __NV_E4M3);
-                code[q] = l | u << 16;
+            *reinterpret_cast<uint32_t *>(page + (int64_t)pool.page_size * kLatent +
+                                          (int64_t)off * 2 * kLatRope + 4 * lane) = turned;
+            uint8_t *scales = page + (int64_t)pool.page_size * (kLatent + 2 * kLatRope) +
+                              (int64_t)off * kLatGroups;
+            if ((lane & 7) == 0) {
+                scales[lane >> 3] = (uint8_t)bits[0];
+                scales[4 + (lane >> 3)] = (uint8_t)bits[1];
             }
-            *reinterpret_cast<uint2 *>(page + (int64_t)off * kLatent + 256 * h + 8 * lane) =
-                make_uint2(code[0], code[1]);
-        }
-        *reinterpret_cast<uint32_t *>(page + (int64_t)pool.page_size * kLatent +
-                                      (int64_t)off * 2 * kLatRope + 4 * lane) = turned;
-        uint8_t *scales = page + (int64_t)pool.page_size * (kLatent + 2 * kLatRope) +
-                          (int64_t)off * kLatGroups;
-        if ((lane & 7) == 0) {
-            scales[lane >> 3] = (uint8_t)bits[0];
-            scales[4 + (lane >> 3)] = (uint8_t)bits[1];
         }
     }
 }

@@ -610,6 +610,7 @@ idx_status idx_latent_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_
  * [0, max_model_len]; token t is in page block_table[b, t / page_size],
  * bt_stride >= ceil(max_model_len / page_size).  Tokens of a page outside
  * the pool are left out and set IDX_DEV_BAD_PAGE.
+ * Supported: as above, and next_n * ceil(H / 64) at most the SMs (152).
  * ---------------------------------------------------------------------- */
 idx_status idx_paged_latent_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
                                       const uint8_t *kv_pages, int64_t page_stride_bytes,

@@ -496,11 +496,11 @@ IDX_DEVFN void stmatrix_x4_trans(uint32_t saddr, uint32_t a, uint32_t b, uint32_
                  : "memory");
 }
 
-// 16 bytes global -> shared, zeros when !live (the source is not read then).
-IDX_DEVFN void cp_async16(uint32_t saddr, const void *src, bool live)
+// 16 bytes global -> shared.
+IDX_DEVFN void cp_async16(uint32_t saddr, const void *src)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(live ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr),
+                 "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
 }
 

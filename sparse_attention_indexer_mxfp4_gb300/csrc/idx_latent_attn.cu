@@ -8,17 +8,20 @@
 //     O^T [512 latents x heads] += K[:, :512]^T . P^T         (4 x 4 MMAs, M = 128)
 //
 // with the tokens (first product) and the latents (second) on the MMA's M and
-// the heads on its N: 16, 32 or 64 of them a CTA, so few heads waste no tensor
+// the heads on its N: 16, 32 or 64 columns a CTA, so few heads waste no tensor
 // work, the running sums O^T stay in tensor memory for a row's whole length
 // (4 N columns), and the tile is read in place both times, K-major by its
 // token rows and M-major by its latent columns (the same 128-byte swizzled
-// rows describe both).  More than 64 heads are two groups, each a unit of its
-// own; the second reads the tokens from L2.
+// rows describe both).  In the paged form the heads of several rows of a
+// sequence share the columns (each row with its own end), so their tokens are
+// read once.  What 64 columns do not hold is further groups; the CTAs of one
+// share's groups run side by side and find each other's tokens in L2.
 //
-// Work is split over a flat list of (row, head group, tile): every CTA (one
-// per SM) takes an equal contiguous share, whatever the rows' lengths.  Rows
-// that lie in one share are finished there; the others leave unnormalised sums
-// with their maximum in scratch and a second kernel joins them in share order.
+// Work is split over the flat list of (row, tile): every share is an equal
+// contiguous part, whatever the rows' lengths (a row: a ragged row, or a
+// sequence of the paged form).  Rows that lie in one share are finished there;
+// the others leave unnormalised sums with their maximum in scratch and a
+// second kernel joins them in share order.
 //
 // Warps: 0-3 softmax and epilogue; 4-11 bring tokens in (slot -> page ->
 // global loads; 8-bit codes are widened to bf16 on the way, exactly, by two
@@ -54,23 +57,35 @@ struct AttnArgs {
     int64_t num_slots;
     const int32_t *block_table, *context_lens;
     int64_t bt_stride;
-    int ctx_per_row, next_n, max_len;
-    int R, H, groups;
+    int ctx_per_row, max_len;
+    int rows, next;            // rows of the list; query rows in each (paged: next_n)
+    int H, groups, hgroups;    // head groups, times groups of query rows
+    int hpg, rpg;              // heads and query rows of a group's columns
+    uint32_t inv_hpg;          // column / hpg = column * inv_hpg >> 16
     float scale_log2;  // scale * log2(e)
     uint16_t *out;
     int64_t ldo_row, ldo_head;
     float *lse;
     int64_t ld_lse;
-    void *ws_place;  // int4 a CTA: the row, group and tile its share begins at
+    void *ws_place;  // int2 a share: the row and tile it begins at
     float *ws_part;  // two segments a CTA: O^T, then maxima, then sums
     unsigned int *status;
 };
 
-// Where a row's tokens are listed, and how many it has.
+// Where a row's tokens are listed, and how many it has (paged: the most any
+// of its query rows sees).
 struct Row {
     int64_t first;
     int n;
 };
+
+// Paged: how many tokens query row j of sequence b sees.
+__device__ __forceinline__ int query_end(const AttnArgs &a, int b, int j)
+{
+    const int end = a.ctx_per_row ? a.context_lens[b * a.next + j]
+                                  : a.context_lens[b] - a.next + j + 1;
+    return min(max(end, 0), a.max_len);
+}
 
 __device__ __forceinline__ Row row_of(const AttnArgs &a, int r)
 {
@@ -79,9 +94,11 @@ __device__ __forceinline__ Row row_of(const AttnArgs &a, int r)
         const int64_t hi = min((int64_t)max(a.indptr[r + 1], 0), a.num_slots);
         return {lo, (int)max((int64_t)0, hi - lo)};
     }
-    const int b = r / a.next_n, j = r - b * a.next_n;
-    const int end = a.ctx_per_row ? a.context_lens[r] : a.context_lens[b] - a.next_n + j + 1;
-    return {b * a.bt_stride, min(max(end, 0), a.max_len)};
+    int n = query_end(a, r, a.next - 1);
+    if (a.ctx_per_row)
+        for (int j = 0; j + 1 < a.next; ++j)
+            n = max(n, query_end(a, r, j));
+    return {r * a.bt_stride, n};
 }
 
 // A row without tokens still takes one (empty) tile: it has outputs.
@@ -100,23 +117,33 @@ __device__ __forceinline__ int64_t slot_of(const AttnArgs &a, const Row &w, int 
     return id < 0 ? -1 : (int64_t)id * a.pool.page_size + (t - p * a.pool.page_size);
 }
 
-// First unit of CTA c's share.
-__device__ __forceinline__ int64_t share_start(int64_t c, int64_t units, int64_t ctas)
+// First tile of share p.
+__device__ __forceinline__ int64_t share_start(int64_t p, int64_t tiles, int64_t shares)
 {
-    return c * units / ctas;
+    return p * tiles / shares;
 }
 
-// The walk of a share: segments of consecutive tiles of one row and group.
-// The next row's length is fetched a segment ahead.
+// Query row (within the list's row) and head of a group's column; false for a
+// column that has none.
+__device__ __forceinline__ bool column_place(const AttnArgs &a, int g, int col, int *j, int *h)
+{
+    const int q = (int)(col * a.inv_hpg >> 16);
+    *j = g / a.hgroups * a.rpg + q;
+    *h = g % a.hgroups * a.hpg + col - q * a.hpg;
+    return q < a.rpg && *j < a.next && *h < a.H;
+}
+
+// The walk of a share: segments of consecutive tiles of one row.  The next
+// row's length is fetched a segment ahead.
 struct Walk {
     int64_t left;
-    int r, g, t;
+    int r, t;
     Row row;
 };
 
 struct Seg {
     Row row;
-    int r, g, t0, t1, tiles;
+    int r, t0, t1, tiles;
 };
 
 __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
@@ -125,7 +152,6 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
         return false;
     s.row = w.row;
     s.r = w.r;
-    s.g = w.g;
     s.t0 = w.t;
     s.tiles = tiles_of(w.row.n);
     s.t1 = (int)min((int64_t)s.tiles, w.t + w.left);
@@ -133,12 +159,9 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
     w.t = s.t1;
     if (s.t1 == s.tiles) {
         w.t = 0;
-        if (++w.g == a.groups) {
-            w.g = 0;
-            ++w.r;
-            if (w.left > 0)
-                w.row = row_of(a, w.r);
-        }
+        ++w.r;
+        if (w.left > 0)
+            w.row = row_of(a, w.r);
     }
     return true;
 }
@@ -151,7 +174,8 @@ struct Cfg {
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
     static constexpr int OFF_MAX = OFF_P + P_BYTES;     // [4][N] floats
     static constexpr int OFF_HEAD = OFF_MAX + 16 * N;   // [N] floats
-    static constexpr int OFF_VALID = OFF_HEAD + 4 * N;  // [2][8] uint16
+    static constexpr int OFF_END = OFF_HEAD + 4 * N;    // [N] int
+    static constexpr int OFF_VALID = OFF_END + 4 * N;   // [2][4] uint16
     static constexpr int OFF_BAR = OFF_VALID + 32;
     static constexpr int BARS = 15;
     static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;  // tmem base, abort, start place
@@ -162,63 +186,33 @@ struct Cfg {
     static constexpr int PART = kLatent * N + 2 * N;  // floats of a partial result
 };
 
-__device__ __forceinline__ uint32_t tile_unit(uint32_t stage, int chunk, int key, int unit)
+// Four e4m3 codes to bf16 times `mul`.  A code's bits placed at bf16's sign,
+// low exponent and high mantissa bits (two bytes: s0000eee emmm0000) are its
+// value times 2^-120, subnormal codes included; the multiplier carries 2^120.
+__device__ __forceinline__ uint2 widen4(uint32_t w, uint32_t mul)
 {
-    return stage + chunk * kChunkBytes + key * 128 + ((unit ^ (key & 7)) << 4);
-}
-
-// Four e4m3 codes to bf16 times 2^(scale - 127).  A code's bits placed at
-// bf16's sign, low exponent and high mantissa bits are its value times 2^-120,
-// subnormal codes included; the multiplier carries the 2^120.
-__device__ __forceinline__ uint2 widen4(uint32_t w, __nv_bfloat162 mul)
-{
-    const uint32_t lo = __byte_perm(w, 0, 0x1404), hi = __byte_perm(w, 0, 0x3424);
-    uint32_t a = (lo & 0x80008000u) | ((lo >> 4) & 0x07f007f0u);
-    uint32_t b = (hi & 0x80008000u) | ((hi >> 4) & 0x07f007f0u);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a), mul);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&b), mul);
+    const uint32_t hi = (w & 0x80808080u) | ((w >> 4) & 0x07070707u);
+    const uint32_t lo = (w << 4) & 0xf0f0f0f0u;
+    uint32_t a = __byte_perm(lo, hi, 0x5140), b = __byte_perm(lo, hi, 0x7362);
+    const __nv_bfloat162 m = *reinterpret_cast<__nv_bfloat162 *>(&mul);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&a), m);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&b), m);
     return make_uint2(*reinterpret_cast<const uint32_t *>(&x),
                       *reinterpret_cast<const uint32_t *>(&y));
 }
 
-__device__ __forceinline__ uint32_t bf16_pair_of_bits(uint32_t b)
+// An e8m0 scale as the multiplier of widen4: 2^(scale - 7) twice, up to 2^127
+// (scale 134); fix_scales does the rest.
+constexpr uint32_t kPlainScale = 134;
+
+__device__ __forceinline__ uint32_t widen_mul(uint32_t scale)
 {
-    return b | b << 16;
+    return min(scale, kPlainScale) * 0x00800080u + 120u * 0x00800080u;
 }
 
-__device__ __forceinline__ uint32_t scale_pair(uint32_t w, uint32_t mul)
-{
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&w),
-                                     *reinterpret_cast<__nv_bfloat162 *>(&mul));
-    return *reinterpret_cast<const uint32_t *>(&x);
-}
-
-// Sixteen codes of one key (latents 16 u .. 16 u + 15) into a stage.  Lanes
-// of odd chunks store their second half first, so eight neighbouring lanes
-// cover all the banks.
-__device__ __forceinline__ void put_codes(uint32_t stage, int key, int u, const uint4 &c,
-                                          uint32_t scale)
-{
-    // 2^(scale - 7): bf16's exponent field holds it up to 2^127
-    const uint32_t field = min(scale + 120u, 254u);
-    uint32_t m = bf16_pair_of_bits(scale == 255u ? 0x7fc0u : field << 7);
-    const __nv_bfloat162 mul = *reinterpret_cast<__nv_bfloat162 *>(&m);
-    uint2 v[4] = {widen4(c.x, mul), widen4(c.y, mul), widen4(c.z, mul), widen4(c.w, mul)};
-    if (__any_sync(0xffffffffu, scale > 134u)) {
-        // what the first multiplier could not hold
-        const uint32_t rest =
-            bf16_pair_of_bits((scale > 134u && scale < 255u ? scale - 134u + 127u : 127u) << 7);
-        #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = make_uint2(scale_pair(v[i].x, rest), scale_pair(v[i].y, rest));
-    }
-    const int chunk = u >> 2, unit = 2 * (u & 3), odd = chunk & 1;
-    const uint4 h0 = make_uint4(v[0].x, v[0].y, v[1].x, v[1].y);
-    const uint4 h1 = make_uint4(v[2].x, v[2].y, v[3].x, v[3].y);
-    const uint4 a = odd ? h1 : h0, b = odd ? h0 : h1;
-    st_shared_v4(tile_unit(stage, chunk, key, unit + odd), a.x, a.y, a.z, a.w);
-    st_shared_v4(tile_unit(stage, chunk, key, unit + 1 - odd), b.x, b.y, b.z, b.w);
-}
+// The slots' tokens of nothing: what a loading warp reads for a place without
+// a token.
+__device__ uint4 g_no_token[kLatBf16TokBytes / 16];
 
 // A loading warp's place in the share: its tokens of the next tile.
 struct Feed {
@@ -279,45 +273,148 @@ __device__ __forceinline__ uint4 ld_stream16(const uint8_t *p)
     return v;
 }
 
-// What a loading warp holds of a tile of 8-bit tokens: eight token rows (lane
-// u: latents 16 u ..), their rotated elements (eight lanes a token) and their
-// scales (four lanes a token, two each).
-struct Codes {
-    uint4 row[8];
-    uint4 rope[2];
-    uint32_t scales;
+__device__ __forceinline__ const uint8_t *shfl_ptr(const uint8_t *p, int src)
+{
+    return reinterpret_cast<const uint8_t *>(
+        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
+}
+
+// The sixteen tokens that a loading warp brings of a tile: token i of warp w
+// is the tile's key 8 (i / 2) + 2 w + i % 2, and lane i < 16 holds its place.
+// Pairs of keys that differ in the lowest bit are handled together, eight
+// lanes at a time reach all banks and every shared address is a constant of
+// the lane plus a constant.
+struct Places {
+    const uint8_t *row, *rope, *scale;  // lanes 0..15
+    uint32_t ok;                        // which of the sixteen exist
 };
 
-__device__ __forceinline__ int64_t shfl64(int64_t v, int src)
+template <bool FP8>
+__device__ __forceinline__ Places places_of(const AttnArgs &a, int64_t slot)
 {
-    return __shfl_sync(0xffffffffu, v, src);
+    int off;
+    const int64_t pb = place_slot(a, slot, &off);
+    Places p;
+    p.ok = __ballot_sync(0xffffffffu, pb >= 0);
+    p.row = p.rope = p.scale = reinterpret_cast<const uint8_t *>(g_no_token);
+    if (pb >= 0) {
+        const uint8_t *page = a.pool.base + pb;
+        if (FP8) {
+            p.row = page + (int64_t)off * kLatent;
+            page += (int64_t)a.pool.page_size * kLatent;
+            p.rope = page + (int64_t)off * (2 * kLatRope);
+            page += (int64_t)a.pool.page_size * (2 * kLatRope);
+            p.scale = page + (int64_t)off * kLatGroups;
+        } else {
+            p.row = page + (int64_t)off * kLatBf16TokBytes;
+            p.rope = p.row + 2 * kLatent;
+        }
+    }
+    return p;
 }
 
-__device__ __forceinline__ uint4 load_row8(const AttnArgs &a, int64_t pb, int off, int j, int lane)
+// 8-bit tokens on their way through registers.  Lane: key bit (lane / 4) % 2,
+// chunks lane / 8 and 4 more, sixteen codes at 16 (lane % 4) of each.
+struct Codes {
+    uint4 row[8][2];  // pairs of tokens, halves of the latents
+    uint4 rope[4];    // eight lanes a token
+    uint32_t scales;  // lane 2 i + half: that half's four scales of token i
+};
+
+__device__ __forceinline__ void load_codes(const Places &p, int lane, Codes &c)
 {
-    const int64_t p = shfl64(pb, j);
-    const int o = __shfl_sync(0xffffffffu, off, j);
-    return p >= 0 ? ld_stream16(a.pool.base + p + (int64_t)o * kLatent + 16 * lane)
-                  : make_uint4(0u, 0u, 0u, 0u);
+    c.scales = *reinterpret_cast<const uint32_t *>(shfl_ptr(p.scale, lane >> 1) + 4 * (lane & 1));
+    const int at = 64 * (lane >> 3) + 16 * (lane & 3);
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint8_t *src = shfl_ptr(p.row, 2 * j + ((lane >> 2) & 1)) + at;
+        c.row[j][0] = ld_stream16(src);
+        c.row[j][1] = ld_stream16(src + 256);
+    }
+    #pragma unroll
+    for (int q = 0; q < 4; ++q)
+        c.rope[q] = ld_stream16(shfl_ptr(p.rope, 4 * q + (lane >> 3)) + 16 * (lane & 7));
 }
 
-__device__ __forceinline__ uint4 load_rope8(const AttnArgs &a, int64_t pb, int off, int i, int lane)
+// Into the stage as bf16.
+__device__ __forceinline__ void put_codes(uint32_t stage, int wl, int lane, const Codes &c)
 {
-    const int64_t p = shfl64(pb, 4 * i + (lane >> 3));
-    const int o = __shfl_sync(0xffffffffu, off, 4 * i + (lane >> 3));
-    return p >= 0 ? ld_stream16(a.pool.base + p + (int64_t)a.pool.page_size * kLatent +
-                                (int64_t)o * 2 * kLatRope + 16 * (lane & 7))
-                  : make_uint4(0u, 0u, 0u, 0u);
+    const int k7 = 2 * wl + ((lane >> 2) & 1);  // key % 8 of all this lane's keys
+    const uint32_t at = stage + (lane >> 3) * kChunkBytes + k7 * 128;
+    const uint32_t u0 = at + (((2 * (lane & 3)) ^ k7) << 4), u1 = u0 ^ 16;
+    #pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        #pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t four =
+                __shfl_sync(0xffffffffu, c.scales, 4 * j + 2 * ((lane >> 2) & 1) + h);
+            const uint32_t mul = widen_mul(__byte_perm(four, 0, 0x4440 | (lane >> 3)));
+            const uint4 v = c.row[j][h];
+            const uint2 a = widen4(v.x, mul), b = widen4(v.y, mul);
+            const uint2 d = widen4(v.z, mul), e = widen4(v.w, mul);
+            const uint32_t to = j * 1024 + h * 4 * kChunkBytes;
+            st_shared_v4(u0 + to, a.x, a.y, b.x, b.y);
+            st_shared_v4(u1 + to, d.x, d.y, e.x, e.y);
+        }
+    }
+    const int kr = 2 * wl + ((lane >> 3) & 1);
+    const uint32_t ur = stage + (kChunks - 1) * kChunkBytes + (8 * (lane >> 4) + kr) * 128 +
+                        (((lane & 7) ^ kr) << 4);
+    #pragma unroll
+    for (int q = 0; q < 4; ++q)
+        st_shared_v4(ur + q * 2048, c.rope[q].x, c.rope[q].y, c.rope[q].z, c.rope[q].w);
 }
 
-__device__ __forceinline__ uint32_t load_scales8(const AttnArgs &a, int64_t pb, int off, int lane)
+// Scales over 2^7 and the NaN scale: multiplies the warp's own part of the
+// stage by what widen_mul left out.  Rare (latents beyond 57344).
+__device__ __noinline__ void fix_scales(uint32_t stage, int wl, int lane, uint32_t scales)
 {
-    const int64_t p = shfl64(pb, lane >> 2);
-    const int o = __shfl_sync(0xffffffffu, off, lane >> 2);
-    return p >= 0 ? *reinterpret_cast<const uint16_t *>(
-                        a.pool.base + p + (int64_t)a.pool.page_size * (kLatent + 2 * kLatRope) +
-                        (int64_t)o * kLatGroups + 2 * (lane & 3))
-                  : 0x7f7fu;
+    const int k7 = 2 * wl + ((lane >> 2) & 1);
+    const uint32_t at = stage + (lane >> 3) * kChunkBytes + k7 * 128;
+    for (int j = 0; j < 16; ++j) {
+        const int h = j & 1;
+        const uint32_t four =
+            __shfl_sync(0xffffffffu, scales, 4 * (j >> 1) + 2 * ((lane >> 2) & 1) + h);
+        const uint32_t s = four >> (8 * (lane >> 3)) & 0xffu;
+        if (s <= kPlainScale)
+            continue;
+        const uint32_t bits = s == 255u ? 0x7fc0u : (s - kPlainScale + 127u) << 7;
+        uint32_t mul = bits | bits << 16;
+        const __nv_bfloat162 m = *reinterpret_cast<__nv_bfloat162 *>(&mul);
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t to = at + (j >> 1) * 1024 + h * 4 * kChunkBytes +
+                                (((2 * (lane & 3) + e) ^ k7) << 4);
+            uint32_t v[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(to));
+            for (int q = 0; q < 4; ++q) {
+                const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162 *>(&v[q]), m);
+                v[q] = *reinterpret_cast<const uint32_t *>(&y);
+            }
+            st_shared_v4(to, v[0], v[1], v[2], v[3]);
+        }
+    }
+}
+
+// bf16 tokens straight into the stage.
+__device__ __forceinline__ void copy_tokens(uint32_t stage, int wl, int lane, const Places &p)
+{
+    #pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int k = 8 * (i >> 1) + 2 * wl + (i & 1);
+        const uint8_t *src = shfl_ptr(p.row, i) + 16 * lane;
+        const uint32_t to = stage + (lane >> 3) * kChunkBytes + k * 128 +
+                            (((lane & 7) ^ (2 * wl + (i & 1))) << 4);
+        cp_async16(to, src);
+        cp_async16(to + 4 * kChunkBytes, src + 512);
+    }
+    const int kr = 2 * wl + ((lane >> 3) & 1);
+    const uint32_t ur = stage + (kChunks - 1) * kChunkBytes + (8 * (lane >> 4) + kr) * 128 +
+                        (((lane & 7) ^ kr) << 4);
+    #pragma unroll
+    for (int q = 0; q < 4; ++q)
+        cp_async16(ur + q * 2048, shfl_ptr(p.rope, 4 * q + (lane >> 3)) + 16 * (lane & 7));
 }
 
 template <int N, bool FP8>
@@ -326,8 +423,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using C = Cfg<N>;
     constexpr int NH = N / 8;           // fragments of eight heads
-    constexpr int WPT = FP8 ? 8 : 4;    // loading warps of a tile
-    constexpr int KPW = kTile / WPT;    // tokens a loading warp brings
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
@@ -344,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], WPT);
+            mbar_init(&full[i], kLoadWarps / 2);
             mbar_init(&empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], kSoftWarps);
@@ -367,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
 
     // this CTA's share: a prefix sum of the rows' tiles over the threads
-    const int chunk = (a.R + kThreads - 1) / kThreads;
-    const int r0 = min(a.R, tid * chunk), r1 = min(a.R, r0 + chunk);
+    const int chunk = (a.rows + kThreads - 1) / kThreads;
+    const int r0 = min(a.rows, tid * chunk), r1 = min(a.rows, r0 + chunk);
     int64_t mine = 0;
     for (int r = r0; r < r1; ++r)
         mine += tiles_of(row_of(a, r).n);
@@ -387,35 +482,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         total += wsum[i];
         before += i < warp ? wsum[i] : 0;
     }
-    const int64_t units = total * a.groups;
-    const int64_t ctas = min((int64_t)gridDim.x, units);
-    const int c = blockIdx.x;
-    const int64_t u0 = c < ctas ? share_start(c, units, ctas) : units;
-    const int64_t left = c < ctas ? share_start(c + 1, units, ctas) - u0 : 0;
-    int4 *place = reinterpret_cast<int4 *>(a.ws_place);
-    if (left > 0 && u0 >= before * a.groups && u0 < (before + mine) * a.groups) {
-        int64_t p = before * a.groups;
+    const int c = blockIdx.x, g = c % a.groups, p = c / a.groups;
+    const int64_t shares = min((int64_t)(gridDim.x / a.groups), total);
+    const int64_t u0 = p < shares ? share_start(p, total, shares) : total;
+    const int64_t left = p < shares ? share_start(p + 1, total, shares) - u0 : 0;
+    int2 *place = reinterpret_cast<int2 *>(a.ws_place);
+    if (left > 0 && u0 >= before && u0 < before + mine) {
+        int64_t q = before;
         int r = r0, tl = tiles_of(row_of(a, r).n);
-        while (u0 >= p + (int64_t)tl * a.groups) {
-            p += (int64_t)tl * a.groups;
+        while (u0 >= q + tl) {
+            q += tl;
             tl = tiles_of(row_of(a, ++r).n);
         }
-        const int g = (int)((u0 - p) / tl), t = (int)((u0 - p) % tl);
         misc[2] = r;
-        misc[3] = g;
-        misc[4] = t;
-        place[c] = make_int4(r, g, t, 0);
+        misc[3] = (uint32_t)(u0 - q);
+        if (g == 0)
+            place[p] = make_int2(r, (int)(u0 - q));
     }
-    if (left == 0 && tid == 0)
-        place[c] = make_int4(-1, 0, 0, 0);
+    if (left == 0 && g == 0 && tid == 0)
+        place[p] = make_int2(-1, 0);
+    if (a.hpg * a.rpg < N) {
+        // columns without a head: their query rows are zeros
+        for (int e = tid; e < C::Q_BYTES / 16; e += kThreads)
+            st_shared_v4(sbase + C::OFF_Q + 16 * e, 0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
     Walk w;
     w.left = left;
     w.r = misc[2];
-    w.g = misc[3];
-    w.t = misc[4];
+    w.t = misc[3];
     if (left > 0)
         w.row = row_of(a, w.r);
     Seg s;
@@ -424,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ softmax, epilogue
         const int g8 = lane >> 2, c2 = 2 * (lane & 3);
         const int key0 = 16 * warp + g8;  // and key0 + 8
+        const int *send = reinterpret_cast<const int *>(smem + C::OFF_END);
         const uint32_t lanes = (uint32_t)(warp * 32) << 16;
         const uint32_t p_addr = sbase + C::OFF_P;
         const float sl = a.scale_log2;
@@ -434,6 +533,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 2 * NH; ++e) {
                 m[e] = -INFINITY;
                 l[e] = 0.0f;
+            }
+            // paged: each column's end; before the first of them nothing is masked
+            int first_end = INT_MAX;
+            if (!a.indptr) {
+                if (tid < N) {
+                    int j, h;
+                    reinterpret_cast<int *>(smem + C::OFF_END)[tid] =
+                        column_place(a, g, tid, &j, &h) ? query_end(a, s.r, j) : s.row.n;
+                }
+                if (a.next > 1)
+                    for (int j = 0; j < a.rpg; ++j)
+                        first_end = min(first_end,
+                                        query_end(a, s.r, min(g / a.hgroups * a.rpg + j,
+                                                              a.next - 1)));
+                named_bar_sync(1, 32 * kSoftWarps);
             }
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int st = i & 1;
@@ -455,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 #pragma unroll
                 for (int e = 0; e < 4 * NH; ++e)
                     x[e] = __uint_as_float(sr[e]);
-                const bool v0 = valid[8 * st + key0 % WPT] >> (key0 / WPT) & 1;
-                const bool v1 = valid[8 * st + key0 % WPT] >> ((key0 + 8) / WPT) & 1;
+                const uint32_t ok = valid[4 * st + (g8 >> 1)] >> (4 * warp + (g8 & 1));
+                const bool v0 = ok & 1, v1 = ok & 4;
                 if (!(v0 && v1)) {
                     #pragma unroll
                     for (int j = 0; j < NH; ++j) {
@@ -464,6 +578,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         x[4 * j + 1] = v0 ? x[4 * j + 1] : -INFINITY;
                         x[4 * j + 2] = v1 ? x[4 * j + 2] : -INFINITY;
                         x[4 * j + 3] = v1 ? x[4 * j + 3] : -INFINITY;
+                    }
+                }
+                if ((t + 1) * kTile > first_end) {
+                    #pragma unroll
+                    for (int e = 0; e < 2 * NH; ++e) {
+                        const int lim = send[8 * (e >> 1) + c2 + (e & 1)] - t * kTile;
+                        const int q = 4 * (e >> 1) + (e & 1);
+                        x[q] = key0 < lim ? x[q] : -INFINITY;
+                        x[q + 2] = key0 + 8 < lim ? x[q + 2] : -INFINITY;
                     }
                 }
                 // heads 8 j + c2 + e are entries 2 j + e of m and l
@@ -565,14 +688,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             named_bar_sync(1, 32 * kSoftWarps);
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
             float *part = a.ws_part + (int64_t)(2 * c + (k > 0)) * C::PART;
-            const int h0 = s.g * 64;
             if (tid < N) {
                 const float sum = smax[tid] + smax[N + tid] + smax[2 * N + tid] + smax[3 * N + tid];
                 const float mm = shead[tid];
                 if (whole) {
                     shead[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
-                    if (a.lse && h0 + tid < a.H)
-                        a.lse[s.r * a.ld_lse + h0 + tid] =
+                    int j, h;
+                    if (column_place(a, g, tid, &j, &h) && a.lse)
+                        a.lse[((int64_t)s.r * a.next + j) * a.ld_lse + h] =
                             sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
                 } else {
                     part[kLatent * N + tid] = mm;
@@ -599,10 +722,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
                         const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, y1)
                                                      : __floats2bfloat162_rn(y0, got);
-                        const int h = h0 + hq + e + odd;
-                        if (h < a.H)
-                            *reinterpret_cast<__nv_bfloat162 *>(a.out + s.r * a.ldo_row +
-                                                                h * a.ldo_head + d) = v;
+                        int j, h;
+                        if (column_place(a, g, hq + e + odd, &j, &h))
+                            *reinterpret_cast<__nv_bfloat162 *>(
+                                a.out + ((int64_t)s.r * a.next + j) * a.ldo_row + h * a.ldo_head +
+                                d) = v;
                     }
                 } else {
                     #pragma unroll
@@ -615,115 +739,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp < kWarpS) {
         // ------------------------------------------------------ token feed
+        // four warps bring the even tiles, four the odd ones, so that one
+        // group's loads are in flight while the other fills its stage
+        const int wl = (warp - kSoftWarps) & 3, st = (warp - kSoftWarps) >> 2;
+        const int key = 8 * (lane >> 1) + 2 * wl + (lane & 1);
+        const bool on = lane < 16;
+        const uint32_t stage = sbase + st * kStageBytes;
         Feed f;
         feed_start(a, f, w);
-        if constexpr (FP8) {
-            const int wl = warp - kSoftWarps;
-            const int key = wl + WPT * lane;
-            const bool on = lane < KPW;
-            int off;
-            int64_t pb = place_slot(a, feed_slot(a, f, key, on), &off);
+        if (st == 1)
             feed_next(a, f);
-            int64_t slot = feed_slot(a, f, key, on);
-            Codes cd;
-            #pragma unroll
-            for (int j = 0; j < KPW; ++j)
-                cd.row[j] = load_row8(a, pb, off, j, lane);
-            cd.scales = load_scales8(a, pb, off, lane);
-            cd.rope[0] = load_rope8(a, pb, off, 0, lane);
-            cd.rope[1] = load_rope8(a, pb, off, 1, lane);
-            uint32_t ok = __ballot_sync(0xffffffffu, pb >= 0);
-            for (int i = 0; i < (int)left; ++i) {
-                const int st = i & 1;
-                const uint32_t stage = sbase + st * kStageBytes;
-                // the next tile's places (its slots were fetched a tile ago)
-                pb = place_slot(a, slot, &off);
-                feed_next(a, f);
-                slot = feed_slot(a, f, key, on);
-                if (i >= 2 && !mbar_wait(&empty[st], ((i >> 1) - 1) & 1, abort_flag, a.status))
-                    break;
-                __syncwarp();
-                if (lane == 0)
-                    valid[8 * st + wl] = (uint16_t)ok;
-                const uint32_t scales = cd.scales;
-                cd.scales = load_scales8(a, pb, off, lane);
-                // each register is filled for the next tile as soon as it is free
-                #pragma unroll
-                for (int j = 0; j < KPW; ++j) {
-                    const uint32_t both =
-                        __shfl_sync(0xffffffffu, scales, 4 * j + (lane >> 3));
-                    put_codes(stage, wl + WPT * j, lane, cd.row[j],
-                              lane & 4 ? both >> 8 : both & 0xffu);
-                    cd.row[j] = load_row8(a, pb, off, j, lane);
+        Places pl = places_of<FP8>(a, feed_slot(a, f, key, on));
+        feed_next(a, f);
+        feed_next(a, f);
+        int64_t slot = feed_slot(a, f, key, on);
+        Codes cd;
+        if constexpr (FP8)
+            load_codes(pl, lane, cd);
+        for (int i = st; i < (int)left; i += 2) {
+            if (i >= 2 && !mbar_wait(&empty[st], ((i >> 1) - 1) & 1, abort_flag, a.status))
+                break;
+            __syncwarp();
+            if (lane == 0)
+                valid[4 * st + wl] = (uint16_t)pl.ok;
+            if constexpr (FP8) {
+                // widen what came in while the stage was busy
+                put_codes(stage, wl, lane, cd);
+                const bool big = __vcmpgtu4(cd.scales, kPlainScale * 0x01010101u) != 0;
+                if (__any_sync(0xffffffffu, big)) {
+                    __syncwarp();
+                    fix_scales(stage, wl, lane, cd.scales);
                 }
-                #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const uint4 v = cd.rope[q];
-                    st_shared_v4(tile_unit(stage, kChunks - 1, wl + WPT * (4 * q + (lane >> 3)),
-                                           lane & 7), v.x, v.y, v.z, v.w);
-                    cd.rope[q] = load_rope8(a, pb, off, q, lane);
-                }
-                ok = __ballot_sync(0xffffffffu, pb >= 0);
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&full[st]);
-            }
-        } else {
-            // four warps bring the even tiles, four the odd ones, straight
-            // into the stage: a group waits for its own copies alone
-            const int wl = (warp - kSoftWarps) & 3, st = (warp - kSoftWarps) >> 2;
-            const int key = wl + WPT * lane;
-            const bool on = lane < KPW;
-            const uint32_t stage = sbase + st * kStageBytes;
-            if (st == 1)
-                feed_next(a, f);
-            int64_t slot = feed_slot(a, f, key, on);
-            for (int i = st; i < (int)left; i += 2) {
-                int off;
-                const int64_t pb = place_slot(a, slot, &off);
-                feed_next(a, f);
-                feed_next(a, f);
-                slot = feed_slot(a, f, key, on);
-                if (i >= 2 && !mbar_wait(&empty[st], ((i >> 1) - 1) & 1, abort_flag, a.status))
-                    break;
-                __syncwarp();
-                const uint32_t ok = __ballot_sync(0xffffffffu, pb >= 0);
-                if (lane == 0)
-                    valid[8 * st + wl] = (uint16_t)ok;
-                #pragma unroll
-                for (int j = 0; j < KPW; ++j) {
-                    const int64_t p = shfl64(pb, j);
-                    const int o = __shfl_sync(0xffffffffu, off, j);
-                    const uint8_t *src =
-                        a.pool.base + (p >= 0 ? p + (int64_t)o * kLatBf16TokBytes + 16 * lane : 0);
-                    const int k = wl + WPT * j;
-                    cp_async16(tile_unit(stage, lane >> 3, k, lane & 7), src, p >= 0);
-                    cp_async16(tile_unit(stage, 4 + (lane >> 3), k, lane & 7),
-                               p >= 0 ? src + 512 : src, p >= 0);
-                }
-                #pragma unroll
-                for (int q = 0; q < KPW / 4; ++q) {
-                    const int j = 4 * q + (lane >> 3);
-                    const int64_t p = shfl64(pb, j);
-                    const int o = __shfl_sync(0xffffffffu, off, j);
-                    const uint8_t *src =
-                        a.pool.base + (p >= 0 ? p + (int64_t)o * kLatBf16TokBytes + 2 * kLatent +
-                                                    16 * (lane & 7)
-                                              : 0);
-                    cp_async16(tile_unit(stage, kChunks - 1, wl + WPT * j, lane & 7), src, p >= 0);
-                }
+            } else {
+                copy_tokens(stage, wl, lane, pl);
                 cp_async_wait_all();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&full[st]);
             }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&full[st]);
+            // the group's next tile (its slots were fetched a tile ago)
+            pl = places_of<FP8>(a, slot);
+            feed_next(a, f);
+            feed_next(a, f);
+            slot = feed_slot(a, f, key, on);
+            if constexpr (FP8)
+                load_codes(pl, lane, cd);
         }
     } else if (warp == kWarpS) {
         // -------------------------------------------- queries, S^T = K Q^T
         const bool one = elect_one();
         const uint32_t id = idesc_bf16(kTile, N, false, false);
+        const uint32_t q_bytes = kChunks * a.hpg * a.rpg * 128;
+        const int qh = g % a.hgroups * a.hpg, qj = g / a.hgroups * a.rpg;
         int i = 0, k = 0;
         bool ok = true, q_flying = false;
         for (; ok && next_seg(a, w, s); ++k) {
@@ -731,11 +799,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 break;
             __syncwarp();
             if (one) {
-                mbar_arrive_expect_tx(q_full, C::Q_BYTES);
+                mbar_arrive_expect_tx(q_full, q_bytes);
                 #pragma unroll 1
                 for (int ch = 0; ch < kChunks; ++ch)
-                    tma_load_3d(smem + C::OFF_Q + ch * N * 128, &tm_q, q_full, ch * 128, s.g * 64,
-                                s.r);
+                    tma_load_3d(smem + C::OFF_Q + ch * N * 128, &tm_q, q_full, ch * 128, qh,
+                                s.r * a.next + qj);
             }
             __syncwarp();
             q_flying = true;
@@ -828,9 +896,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial results of a row that several shares hold: the CTAs of
-// boundary c (blockIdx.x + 1) act if it is the first that cuts its (row,
-// group), the shares before and after it holding the pieces.  Threads: 128
-// latents x 2 of the group's quads of heads.
+// boundary p (blockIdx.x + 1) act if it is the first that cuts its row, the
+// shares before and after it holding the pieces.  Threads: 128 latents x 2 of
+// a group's quads of columns; blockIdx.z: the group.
 constexpr int kJoinThreads = 256;
 
 template <int N>
@@ -839,33 +907,30 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
     using C = Cfg<N>;
     pdl_wait();
     pdl_launch_dependents();
-    const int4 *place = reinterpret_cast<const int4 *>(a.ws_place);
-    const int c = blockIdx.x + 1, ctas = gridDim.x + 1;
-    const int4 here = place[c], prev = place[c - 1];
-    const bool prev_same = prev.x == here.x && prev.y == here.y;
-    if (here.x < 0 || here.z == 0 || (prev_same && prev.z > 0))
+    const int2 *place = reinterpret_cast<const int2 *>(a.ws_place);
+    const int p = blockIdx.x + 1, shares = gridDim.x + 1, g = blockIdx.z;
+    const int2 here = place[p], prev = place[p - 1];
+    const bool prev_same = prev.x == here.x;
+    if (here.x < 0 || here.y == 0 || (prev_same && prev.y > 0))
         return;
-    int pieces = 0;  // shares c, c + 1, .. that hold more of the row
-    for (int b = c; b < ctas; b += kJoinThreads) {
+    int pieces = 0;  // shares p, p + 1, .. that hold more of the row
+    for (int b = p; b < shares; b += kJoinThreads) {
         const int q = b + (int)threadIdx.x;
-        bool more = false;
-        if (q < ctas) {
-            const int4 p = place[q];
-            more = p.x == here.x && p.y == here.y && p.z > 0;
-        }
-        pieces += __syncthreads_count(more);
+        pieces += __syncthreads_count(q < shares && place[q].x == here.x && place[q].y > 0);
     }
     const int d = threadIdx.x & 127, mt = blockIdx.y & 3;
     const int quad = 2 * (blockIdx.y >> 2) + (threadIdx.x >> 7);
-    // the first piece is the share's first segment if that began with it
-    const float *first = a.ws_part + (int64_t)(2 * (c - 1) + !prev_same) * C::PART;
-    const float *rest = a.ws_part + (int64_t)2 * c * C::PART;
+    const int64_t step = (int64_t)2 * a.groups * C::PART;
+    // the first piece is its share's first segment if the share began with it
+    const float *first =
+        a.ws_part + (int64_t)(2 * ((p - 1) * a.groups + g) + !prev_same) * C::PART;
+    const float *rest = a.ws_part + (int64_t)2 * (p * a.groups + g) * C::PART;
     const int at = (mt * N + 4 * quad) * 128 + 4 * d;
     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    #pragma unroll 4
+    #pragma unroll 8
     for (int q = 0; q <= pieces; ++q) {
-        const float *p = q == 0 ? first : rest + (int64_t)(q - 1) * 2 * C::PART;
-        const float4 v = *reinterpret_cast<const float4 *>(p + kLatent * N + 4 * quad);
+        const float *f = q == 0 ? first : rest + (q - 1) * step;
+        const float4 v = *reinterpret_cast<const float4 *>(f + kLatent * N + 4 * quad);
         top[0] = fmaxf(top[0], v.x);
         top[1] = fmaxf(top[1], v.y);
         top[2] = fmaxf(top[2], v.z);
@@ -875,12 +940,12 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
     for (int e = 0; e < 4; ++e)
         top[e] = top[e] == -INFINITY ? 0.0f : top[e];
     float acc[4] = {}, sum[4] = {};
-    #pragma unroll 4
+    #pragma unroll 8
     for (int q = 0; q <= pieces; ++q) {
-        const float *p = q == 0 ? first : rest + (int64_t)(q - 1) * 2 * C::PART;
-        const float4 v = *reinterpret_cast<const float4 *>(p + at);
-        const float4 m = *reinterpret_cast<const float4 *>(p + kLatent * N + 4 * quad);
-        const float4 l = *reinterpret_cast<const float4 *>(p + kLatent * N + N + 4 * quad);
+        const float *f = q == 0 ? first : rest + (q - 1) * step;
+        const float4 v = *reinterpret_cast<const float4 *>(f + at);
+        const float4 m = *reinterpret_cast<const float4 *>(f + kLatent * N + 4 * quad);
+        const float4 l = *reinterpret_cast<const float4 *>(f + kLatent * N + N + 4 * quad);
         const float vv[4] = {v.x, v.y, v.z, v.w}, mm[4] = {m.x, m.y, m.z, m.w};
         const float ll[4] = {l.x, l.y, l.z, l.w};
         #pragma unroll
@@ -890,28 +955,28 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
             sum[e] = fmaf(wt, ll[e], sum[e]);
         }
     }
-    const int h0 = here.y * 64 + 4 * quad;
     #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        if (h0 + e >= a.H)
-            break;
-        reinterpret_cast<__nv_bfloat16 *>(a.out)[here.x * a.ldo_row + (h0 + e) * a.ldo_head +
-                                                 128 * mt + d] =
+        int j, h;
+        if (!column_place(a, g, 4 * quad + e, &j, &h))
+            continue;
+        const int64_t r = (int64_t)here.x * a.next + j;
+        reinterpret_cast<__nv_bfloat16 *>(a.out)[r * a.ldo_row + h * a.ldo_head + 128 * mt + d] =
             __float2bfloat16(sum[e] == 0.0f ? 0.0f : acc[e] / sum[e]);
         if (a.lse && mt == 0 && d == 0)
-            a.lse[here.x * a.ld_lse + h0 + e] =
+            a.lse[r * a.ld_lse + h] =
                 sum[e] == 0.0f ? -INFINITY : (top[e] + log2f(sum[e])) * kLn2;
     }
 }
 
-int head_columns(int H)
+int columns_of(int n)
 {
-    return H <= 16 ? 16 : H <= 32 ? 32 : 64;
+    return n <= 16 ? 16 : n <= 32 ? 32 : 64;
 }
 
 size_t place_bytes()
 {
-    return ((size_t)sm_count() * sizeof(int4) + 255) / 256 * 256;
+    return ((size_t)sm_count() * sizeof(int2) + 255) / 256 * 256;
 }
 
 template <int N, bool FP8>
@@ -932,9 +997,10 @@ idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int ctas, cudaS
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::SMEM, s, tm, a);
-    if (e == cudaSuccess && ctas > 1)
-        e = launch_pdl(latent_join_kernel<N>, dim3(ctas - 1, 4 * (N / 8)), dim3(kJoinThreads), 0, s,
-                       a);
+    const int shares = ctas / a.groups;
+    if (e == cudaSuccess && shares > 1)
+        e = launch_pdl(latent_join_kernel<N>, dim3(shares - 1, 4 * (N / 8), a.groups),
+                       dim3(kJoinThreads), 0, s, a);
     return launch_status(e);
 }
 
@@ -957,22 +1023,32 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
                     idx_latent_format fmt, int64_t most, void *ws, size_t ws_bytes,
                     cudaStream_t s)
 {
-    if (!ws || !aligned16(ws) || ws_bytes < idx_latent_attention_workspace_size(a.R, a.H))
+    const int R = a.rows * a.next;
+    if (!ws || !aligned16(ws) || ws_bytes < idx_latent_attention_workspace_size(R, a.H))
         return IDX_ERR_WORKSPACE;
     a.status = device_status_ptr();
     if (!a.status)
         return IDX_ERR_CUDA;
-    const int n = head_columns(a.H);
-    a.groups = (a.H + n - 1) / n;
+    // columns: up to 64 heads, and as many query rows of them as 64 hold
+    a.hpg = std::min(a.H, 64);
+    a.rpg = std::min(a.next, 64 / a.hpg);
+    a.inv_hpg = 65536 / a.hpg + 1;
+    a.hgroups = (a.H + a.hpg - 1) / a.hpg;
+    a.groups = a.hgroups * ((a.next + a.rpg - 1) / a.rpg);
+    if (a.groups > sm_count())
+        return IDX_ERR_UNSUPPORTED;
+    const int n = columns_of(a.hpg * a.rpg);
     a.ws_place = ws;
     a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + place_bytes());
-    const int ctas = (int)std::min<int64_t>(sm_count(), most * a.groups);
+    // one CTA per SM, the same number for every group
+    const int shares = (int)std::min<int64_t>(sm_count() / a.groups, most);
+    const int ctas = shares * a.groups;
     CUtensorMap tm;
     // bytes of a head row, heads, rows; a stride over one element is free
-    const uint64_t dims[3] = {2 * kLatTok, (uint64_t)a.H, (uint64_t)a.R};
+    const uint64_t dims[3] = {2 * kLatTok, (uint64_t)a.H, (uint64_t)R};
     const uint64_t str[2] = {(uint64_t)(a.H > 1 ? 2 * ldq_head : 2 * kLatTok),
-                             (uint64_t)(a.R > 1 ? 2 * ldq_row : 2 * kLatTok)};
-    const uint32_t box[3] = {128, (uint32_t)n, 1};
+                             (uint64_t)(R > 1 ? 2 * ldq_row : 2 * kLatTok)};
+    const uint32_t box[3] = {128, (uint32_t)a.hpg, (uint32_t)a.rpg};
     if (!encode_tma_u8(&tm, 3, q, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
         return IDX_ERR_UNSUPPORTED;
     const bool fp8 = fmt == IDX_LATENT_FP8_E4M3;
@@ -992,8 +1068,10 @@ extern "C" size_t idx_latent_attention_workspace_size(int R, int H)
 {
     if (R <= 0 || H <= 0)
         return 0;
-    const int n = head_columns(H);
-    return place_bytes() + (size_t)2 * sm_count() * (kLatent * n + 2 * n) * sizeof(float);
+    // at most a CTA per SM, each with two segments of at most 64 columns (which
+    // rows of a sequence share whatever H is)
+    const int64_t columns = columns_of((int)std::min<int64_t>(64, (int64_t)R * H));
+    return place_bytes() + (size_t)(2 * sm_count() * (kLatent + 2) * columns) * sizeof(float);
 }
 
 extern "C" idx_status idx_latent_attention(
@@ -1021,8 +1099,8 @@ extern "C" idx_status idx_latent_attention(
     a.slots = slots;
     a.indptr = indptr;
     a.num_slots = num_slots;
-    a.next_n = 1;
-    a.R = R;
+    a.rows = R;
+    a.next = 1;
     a.H = H;
     a.scale_log2 = scale * kLog2e;
     a.out = out;
@@ -1063,9 +1141,9 @@ extern "C" idx_status idx_paged_latent_attention(
     a.bt_stride = bt_stride;
     a.context_lens = context_lens;
     a.ctx_per_row = ctx_per_row;
-    a.next_n = next_n;
+    a.next = next_n;
     a.max_len = max_model_len;
-    a.R = B * next_n;
+    a.rows = B;
     a.H = H;
     a.scale_log2 = scale * kLog2e;
     a.out = out;
@@ -1074,6 +1152,6 @@ extern "C" idx_status idx_paged_latent_attention(
     a.lse = lse;
     a.ld_lse = ld_lse;
     const int64_t row_tiles = std::max(1, (int)(((int64_t)max_model_len + kTile - 1) / kTile));
-    return run_attn(a, q, ldq_row, ldq_head, fmt, row_tiles * a.R, ws, ws_bytes,
+    return run_attn(a, q, ldq_row, ldq_head, fmt, row_tiles * B, ws, ws_bytes,
                     (cudaStream_t)stream);
 }

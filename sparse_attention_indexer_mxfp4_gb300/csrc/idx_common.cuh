@@ -129,6 +129,35 @@ IDX_DEVFN bool mbar_wait(uint64_t *bar, uint32_t parity, volatile int *abort,
     return mbar_wait_slow(bar, parity, abort, status, limit_ns);
 }
 
+// mbar_wait and mbar_wait_drain without a call, for kernels that move
+// registers between warpgroups: a called function has one register count.
+IDX_DEVFN bool mbar_wait_here(uint64_t *bar, uint32_t parity, volatile int *abort,
+                              unsigned int *status, uint64_t limit_ns = 2000000000ull)
+{
+    if (mbar_try_wait(bar, parity))
+        return true;
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+        if (*abort)
+            return false;
+        if (globaltimer_ns() - t0 > limit_ns) {
+            *abort = 1;
+            atomicOr(status, kDevTimeout);
+            return false;
+        }
+    }
+    return true;
+}
+
+IDX_DEVFN bool mbar_drain_here(uint64_t *bar, uint32_t parity, uint64_t limit_ns = 20000000ull)
+{
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait_sleep(bar, parity, 20000u))
+        if (globaltimer_ns() - t0 > limit_ns)
+            return false;
+    return true;
+}
+
 // Order-preserving 32-bit key of a float: a larger float gives a larger key;
 // non-finite values give 0, below the key of every finite value.  The
 // top-k's radix digits and the logits kernel's digit-1 histograms both use
@@ -259,14 +288,17 @@ IDX_DEVFN void mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uin
                  : "memory");
 }
 
-// The same with bf16 operands (kind::f16).
+// The same with bf16 operands (kind::f16), issued by the thread with `issue`
+// set: the warp stays converged around it, so that the descriptors can be
+// computed once for the warp.
 IDX_DEVFN void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                       uint32_t accumulate)
+                       uint32_t accumulate, uint32_t issue)
 {
-    asm volatile("{\n\t.reg .pred p;\n\t"
+    asm volatile("{\n\t.reg .pred p, q;\n\t"
                  "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+                 "setp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
                  : "memory");
 }
 
@@ -458,6 +490,21 @@ IDX_DEVFN float2 fma2(float2 a, float2 b, float2 c)
     return __ffma2_rn(a, b, c);
 }
 
+// Move registers between the warpgroups of a block: every warp of an aligned
+// group of four executes the same one, and the shares may not add up to more
+// than the block was launched with.
+template <int REGS>
+IDX_DEVFN void regs_give()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+template <int REGS>
+IDX_DEVFN void regs_take()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 IDX_DEVFN void named_bar_sync(int id, int nthreads)
 {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
@@ -504,9 +551,16 @@ IDX_DEVFN void cp_async16(uint32_t saddr, const void *src)
                  : "memory");
 }
 
-IDX_DEVFN void cp_async_wait_all()
+IDX_DEVFN void cp_async_commit()
 {
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Waits until at most N of the thread's groups are still in flight.
+template <int N>
+IDX_DEVFN void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 IDX_DEVFN void st_shared_v4(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)

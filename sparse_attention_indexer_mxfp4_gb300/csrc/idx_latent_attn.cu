@@ -44,7 +44,10 @@ constexpr int kTile = 64;                          // tokens of a tile
 constexpr int kChunks = kLatTok / 64;              // 128-byte columns of a token row
 constexpr int kChunkBytes = kTile * 128;           // one column of all 64 tokens
 constexpr int kStageBytes = kChunks * kChunkBytes; // 73728
-constexpr int kSoftWarps = 4, kLoadWarps = 8;
+constexpr int kSoftWarps = 4;
+constexpr int kFeedWarps = 4;              // loading warps of a tile
+constexpr int kToks = kTile / kFeedWarps;  // tokens each brings
+constexpr int kLoadWarps = 2 * kFeedWarps; // even tiles, odd tiles
 constexpr int kWarpS = kSoftWarps + kLoadWarps, kWarpPV = kWarpS + 1;
 constexpr int kThreads = (kWarpPV + 1) * 32;
 constexpr int kMaxHeads = 128;
@@ -54,7 +57,7 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 struct AttnArgs {
     LatentPool pool;
     const int32_t *slots, *indptr;  // ragged rows (indptr null: paged)
-    int64_t num_slots;
+    int num_slots;
     const int32_t *block_table, *context_lens;
     int64_t bt_stride;
     int ctx_per_row, max_len;
@@ -69,6 +72,7 @@ struct AttnArgs {
     int64_t ld_lse;
     void *ws_place;  // int2 a share: the row and tile it begins at
     float *ws_part;  // two segments a CTA: O^T, then maxima, then sums
+    int page_stride;  // pool.stride in 32 bits: one multiplication
     unsigned int *status;
 };
 
@@ -90,9 +94,9 @@ __device__ __forceinline__ int query_end(const AttnArgs &a, int b, int j)
 __device__ __forceinline__ Row row_of(const AttnArgs &a, int r)
 {
     if (a.indptr) {
-        const int64_t lo = min((int64_t)max(a.indptr[r], 0), a.num_slots);
-        const int64_t hi = min((int64_t)max(a.indptr[r + 1], 0), a.num_slots);
-        return {lo, (int)max((int64_t)0, hi - lo)};
+        const int lo = min(max(a.indptr[r], 0), a.num_slots);
+        const int hi = min(max(a.indptr[r + 1], 0), a.num_slots);
+        return {lo, max(0, hi - lo)};
     }
     int n = query_end(a, r, a.next - 1);
     if (a.ctx_per_row)
@@ -107,36 +111,32 @@ __device__ __forceinline__ int tiles_of(int n)
     return n > kTile ? (n + kTile - 1) / kTile : 1;
 }
 
-// The slot of token t of a row; -1 when its page is negative.
-__device__ __forceinline__ int64_t slot_of(const AttnArgs &a, const Row &w, int t)
-{
-    if (a.indptr)
-        return a.slots[w.first + t];
-    const int p = page_of(a.pool, t);
-    const int id = a.block_table[w.first + p];
-    return id < 0 ? -1 : (int64_t)id * a.pool.page_size + (t - p * a.pool.page_size);
-}
+// A group's first query row and head.
+struct Group {
+    int j0, h0;
+};
 
-// First tile of share p.
-__device__ __forceinline__ int64_t share_start(int64_t p, int64_t tiles, int64_t shares)
+__device__ __forceinline__ Group group_of(const AttnArgs &a, int g)
 {
-    return p * tiles / shares;
+    const int q = g / a.hgroups;
+    return {q * a.rpg, (g - q * a.hgroups) * a.hpg};
 }
 
 // Query row (within the list's row) and head of a group's column; false for a
 // column that has none.
-__device__ __forceinline__ bool column_place(const AttnArgs &a, int g, int col, int *j, int *h)
+__device__ __forceinline__ bool column_place(const AttnArgs &a, const Group &g, int col, int *j,
+                                             int *h)
 {
     const int q = (int)(col * a.inv_hpg >> 16);
-    *j = g / a.hgroups * a.rpg + q;
-    *h = g % a.hgroups * a.hpg + col - q * a.hpg;
+    *j = g.j0 + q;
+    *h = g.h0 + col - q * a.hpg;
     return q < a.rpg && *j < a.next && *h < a.H;
 }
 
 // The walk of a share: segments of consecutive tiles of one row.  The next
 // row's length is fetched a segment ahead.
 struct Walk {
-    int64_t left;
+    int left;
     int r, t;
     Row row;
 };
@@ -154,7 +154,7 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
     s.r = w.r;
     s.t0 = w.t;
     s.tiles = tiles_of(w.row.n);
-    s.t1 = (int)min((int64_t)s.tiles, w.t + w.left);
+    s.t1 = min(s.tiles, w.t + w.left);
     w.left -= s.t1 - s.t0;
     w.t = s.t1;
     if (s.t1 == s.tiles) {
@@ -169,15 +169,16 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
 template <int N>
 struct Cfg {
     static constexpr int Q_BYTES = kChunks * N * 128;
-    static constexpr int P_BYTES = N * 128;  // 64 tokens a head row
+    // 64 tokens a head row; the epilogue turns 1 KB a warp over in it
+    static constexpr int P_BYTES = N * 128 > 4096 ? N * 128 : 4096;
     static constexpr int OFF_Q = 2 * kStageBytes;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
     static constexpr int OFF_MAX = OFF_P + P_BYTES;     // [4][N] floats
     static constexpr int OFF_HEAD = OFF_MAX + 16 * N;   // [N] floats
     static constexpr int OFF_END = OFF_HEAD + 4 * N;    // [N] int
-    static constexpr int OFF_VALID = OFF_END + 4 * N;   // [2][4] uint16
+    static constexpr int OFF_VALID = OFF_END + 4 * N;   // [2][8] uint16
     static constexpr int OFF_BAR = OFF_VALID + 32;
-    static constexpr int BARS = 15;
+    static constexpr int BARS = 19;
     static constexpr int OFF_MISC = OFF_BAR + 8 * BARS;  // tmem base, abort, start place
     static constexpr int BYTES = OFF_MISC + 40;
     static constexpr int SMEM = BYTES + 1024;  // the base is aligned to 1024 in the kernel
@@ -214,53 +215,71 @@ __device__ __forceinline__ uint32_t widen_mul(uint32_t scale)
 // a token.
 __device__ uint4 g_no_token[kLatBf16TokBytes / 16];
 
-// A loading warp's place in the share: its tokens of the next tile.
+// A loading warp's place in the share: tile t of a row of which the share
+// holds the tiles before `end`, and the tiles left after them.
 struct Feed {
-    Walk w;
-    Seg s;
-    int t;
-    bool live;
+    Row row;
+    int r, t, end, left;
 };
 
-__device__ __forceinline__ void feed_start(const AttnArgs &a, Feed &f, const Walk &w)
+__device__ __forceinline__ void feed_row(Feed &f)
 {
-    f.w = w;
-    f.live = next_seg(a, f.w, f.s);
-    f.t = f.live ? f.s.t0 : 0;
-}
-
-// The slot of token k of the feed's tile; kNoSlot past the row's end.
-constexpr int64_t kNoSlot = INT64_MIN;
-
-__device__ __forceinline__ int64_t feed_slot(const AttnArgs &a, Feed &f, int k, bool lane_on)
-{
-    int64_t slot = kNoSlot;
-    const int t = f.t * kTile + k;
-    if (f.live && lane_on && t < f.s.row.n)
-        slot = slot_of(a, f.s.row, t);
-    return slot;
+    f.end = min(tiles_of(f.row.n), f.t + f.left);
+    f.left -= f.end - f.t;
 }
 
 __device__ __forceinline__ void feed_next(const AttnArgs &a, Feed &f)
 {
-    if (f.live && ++f.t == f.s.t1) {
-        f.live = next_seg(a, f.w, f.s);
-        f.t = f.s.t0;
+    if (++f.t < f.end)
+        return;
+    f.t = f.end = 0;
+    f.row.n = 0;
+    if (f.left > 0) {
+        f.row = row_of(a, ++f.r);
+        feed_row(f);
     }
 }
 
-// Page byte and offset of a slot (-1: no token), telling of bad slots.
-__device__ __forceinline__ int64_t place_slot(const AttnArgs &a, int64_t slot, int *off)
+// A token on its way: what its table holds (a slot, or a page's id) and, for
+// the paged form, its offset in the page.  The entry is only fetched here;
+// place_of, a tile later, is the first to look at it.
+struct Entry {
+    int32_t id;
+    int off;  // -1: no token (past the row's end, or another lane's)
+};
+
+__device__ __forceinline__ Entry feed_entry(const AttnArgs &a, const Feed &f, int k, bool lane_on)
 {
-    int64_t pb = -1;
-    *off = 0;
-    if (slot == kNoSlot)
-        return -1;
-    if (!slot_place(a.pool, slot, &pb, off)) {
-        atomicOr(a.status, kDevBadPage);
-        return -1;
+    Entry e = {0, -1};
+    const int t = f.t * kTile + k;
+    if (lane_on && t < f.row.n) {
+        const int32_t *at = a.slots + f.row.first + t;
+        e.off = 0;
+        if (!a.indptr) {
+            const int p = page_of(a.pool, t);
+            e.off = t - p * a.pool.page_size;
+            at = a.block_table + f.row.first + p;
+        }
+        e.id = *at;
     }
-    return pb;
+    return e;
+}
+
+// Page byte and offset of an entry (-1: no token), telling of bad ones.
+__device__ __forceinline__ int64_t place_of(const AttnArgs &a, const Entry &e, int *off)
+{
+    if (e.off < 0)
+        return -1;
+    *off = e.off;
+    int page = e.id;
+    if (a.indptr) {
+        page = page_of(a.pool, e.id);
+        *off = e.id - page * a.pool.page_size;
+    }
+    if (e.id >= 0 && page < a.pool.num_pages)
+        return (int64_t)page * a.page_stride;
+    atomicOr(a.status, kDevBadPage);
+    return -1;
 }
 
 // Feed of the loading warps' codes and scales: bypass L1, nothing is read twice.
@@ -279,21 +298,21 @@ __device__ __forceinline__ const uint8_t *shfl_ptr(const uint8_t *p, int src)
         __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), src));
 }
 
-// The sixteen tokens that a loading warp brings of a tile: token i of warp w
-// is the tile's key 8 (i / 2) + 2 w + i % 2, and lane i < 16 holds its place.
-// Pairs of keys that differ in the lowest bit are handled together, eight
-// lanes at a time reach all banks and every shared address is a constant of
+// The kToks tokens that a loading warp brings of a tile: token i of warp w is
+// the tile's key 2 kFeedWarps (i / 2) + 2 w + i % 2, and lane i holds its place.
+// Pairs of keys that differ in the lowest bit are handled together: eight
+// lanes at a time reach all banks, and every shared address is a constant of
 // the lane plus a constant.
 struct Places {
-    const uint8_t *row, *rope, *scale;  // lanes 0..15
-    uint32_t ok;                        // which of the sixteen exist
+    const uint8_t *row, *rope, *scale;  // lanes below kToks
+    uint32_t ok;                        // which of the tokens exist
 };
 
 template <bool FP8>
-__device__ __forceinline__ Places places_of(const AttnArgs &a, int64_t slot)
+__device__ __forceinline__ Places places_of(const AttnArgs &a, const Entry &e)
 {
     int off;
-    const int64_t pb = place_slot(a, slot, &off);
+    const int64_t pb = place_of(a, e, &off);
     Places p;
     p.ok = __ballot_sync(0xffffffffu, pb >= 0);
     p.row = p.rope = p.scale = reinterpret_cast<const uint8_t *>(g_no_token);
@@ -316,74 +335,89 @@ __device__ __forceinline__ Places places_of(const AttnArgs &a, int64_t slot)
 // 8-bit tokens on their way through registers.  Lane: key bit (lane / 4) % 2,
 // chunks lane / 8 and 4 more, sixteen codes at 16 (lane % 4) of each.
 struct Codes {
-    uint4 row[8][2];  // pairs of tokens, halves of the latents
-    uint4 rope[4];    // eight lanes a token
-    uint32_t scales;  // lane 2 i + half: that half's four scales of token i
+    uint4 row[kToks / 2][2];  // pairs of tokens, halves of the latents
+    uint4 rope[kToks / 4];    // eight lanes a token
+    uint32_t scales;          // lane 2 i + half: that half's four scales of token i
 };
 
 __device__ __forceinline__ void load_codes(const Places &p, int lane, Codes &c)
 {
-    c.scales = *reinterpret_cast<const uint32_t *>(shfl_ptr(p.scale, lane >> 1) + 4 * (lane & 1));
+    c.scales = *reinterpret_cast<const uint32_t *>(shfl_ptr(p.scale, (lane >> 1) & (kToks - 1)) +
+                                                   4 * (lane & 1));
     const int at = 64 * (lane >> 3) + 16 * (lane & 3);
     #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kToks / 2; ++j) {
         const uint8_t *src = shfl_ptr(p.row, 2 * j + ((lane >> 2) & 1)) + at;
         c.row[j][0] = ld_stream16(src);
         c.row[j][1] = ld_stream16(src + 256);
     }
     #pragma unroll
-    for (int q = 0; q < 4; ++q)
+    for (int q = 0; q < kToks / 4; ++q)
         c.rope[q] = ld_stream16(shfl_ptr(p.rope, 4 * q + (lane >> 3)) + 16 * (lane & 7));
 }
 
-// Into the stage as bf16.
-__device__ __forceinline__ void put_codes(uint32_t stage, int wl, int lane, const Codes &c)
+constexpr int kPairBytes = 2 * kFeedWarps * 128;  // between a warp's pairs of keys
+
+// Shared address of this lane's codes of pair 0 in its first chunk (the second
+// sixteen bytes are at ^ 16), and of its rotated elements.
+__device__ __forceinline__ uint32_t codes_at(uint32_t stage, int wl, int lane)
 {
-    const int k7 = 2 * wl + ((lane >> 2) & 1);  // key % 8 of all this lane's keys
-    const uint32_t at = stage + (lane >> 3) * kChunkBytes + k7 * 128;
-    const uint32_t u0 = at + (((2 * (lane & 3)) ^ k7) << 4), u1 = u0 ^ 16;
+    const int k = 2 * wl + ((lane >> 2) & 1);
+    return stage + (lane >> 3) * kChunkBytes + k * 128 + (((2 * (lane & 3)) ^ (k & 7)) << 4);
+}
+
+__device__ __forceinline__ uint32_t rope_at(uint32_t stage, int wl, int lane)
+{
+    const int k = 2 * wl + ((lane >> 3) & 1);
+    return stage + (kChunks - 1) * kChunkBytes + (2 * kFeedWarps * (lane >> 4) + k) * 128 +
+           (((lane & 7) ^ (k & 7)) << 4);
+}
+
+// Half h (chunks 4 h .., the rotated elements with the second) as bf16 into
+// the stage.
+__device__ __forceinline__ void put_codes(uint32_t stage, int wl, int lane, const Codes &c,
+                                          int h)
+{
+    const uint32_t u0 = codes_at(stage, wl, lane), u1 = u0 ^ 16;
     #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t four =
-                __shfl_sync(0xffffffffu, c.scales, 4 * j + 2 * ((lane >> 2) & 1) + h);
-            const uint32_t mul = widen_mul(__byte_perm(four, 0, 0x4440 | (lane >> 3)));
-            const uint4 v = c.row[j][h];
-            const uint2 a = widen4(v.x, mul), b = widen4(v.y, mul);
-            const uint2 d = widen4(v.z, mul), e = widen4(v.w, mul);
-            const uint32_t to = j * 1024 + h * 4 * kChunkBytes;
-            st_shared_v4(u0 + to, a.x, a.y, b.x, b.y);
-            st_shared_v4(u1 + to, d.x, d.y, e.x, e.y);
-        }
+    for (int j = 0; j < kToks / 2; ++j) {
+        const uint32_t four =
+            __shfl_sync(0xffffffffu, c.scales, 4 * j + 2 * ((lane >> 2) & 1) + h);
+        const uint32_t mul = widen_mul(__byte_perm(four, 0, 0x4440 | (lane >> 3)));
+        const uint4 v = c.row[j][h];
+        const uint2 a = widen4(v.x, mul), b = widen4(v.y, mul);
+        const uint2 d = widen4(v.z, mul), e = widen4(v.w, mul);
+        const uint32_t to = j * kPairBytes + h * 4 * kChunkBytes;
+        st_shared_v4(u0 + to, a.x, a.y, b.x, b.y);
+        st_shared_v4(u1 + to, d.x, d.y, e.x, e.y);
     }
-    const int kr = 2 * wl + ((lane >> 3) & 1);
-    const uint32_t ur = stage + (kChunks - 1) * kChunkBytes + (8 * (lane >> 4) + kr) * 128 +
-                        (((lane & 7) ^ kr) << 4);
+    if (h == 0)
+        return;
+    const uint32_t ur = rope_at(stage, wl, lane);
     #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        st_shared_v4(ur + q * 2048, c.rope[q].x, c.rope[q].y, c.rope[q].z, c.rope[q].w);
+    for (int q = 0; q < kToks / 4; ++q)
+        st_shared_v4(ur + 2 * q * kPairBytes, c.rope[q].x, c.rope[q].y, c.rope[q].z, c.rope[q].w);
 }
 
 // Scales over 2^7 and the NaN scale: multiplies the warp's own part of the
 // stage by what widen_mul left out.  Rare (latents beyond 57344).
-__device__ __noinline__ void fix_scales(uint32_t stage, int wl, int lane, uint32_t scales)
+__device__ __forceinline__ void fix_scales(uint32_t stage, int wl, int lane, uint32_t scales,
+                                           int h)
 {
-    const int k7 = 2 * wl + ((lane >> 2) & 1);
-    const uint32_t at = stage + (lane >> 3) * kChunkBytes + k7 * 128;
-    for (int j = 0; j < 16; ++j) {
-        const int h = j & 1;
+    #pragma unroll 1
+    for (int j = 0; j < kToks / 2; ++j) {
         const uint32_t four =
-            __shfl_sync(0xffffffffu, scales, 4 * (j >> 1) + 2 * ((lane >> 2) & 1) + h);
+            __shfl_sync(0xffffffffu, scales, 4 * j + 2 * ((lane >> 2) & 1) + h);
         const uint32_t s = four >> (8 * (lane >> 3)) & 0xffu;
         if (s <= kPlainScale)
             continue;
         const uint32_t bits = s == 255u ? 0x7fc0u : (s - kPlainScale + 127u) << 7;
         uint32_t mul = bits | bits << 16;
         const __nv_bfloat162 m = *reinterpret_cast<__nv_bfloat162 *>(&mul);
+        #pragma unroll 1
         for (int e = 0; e < 2; ++e) {
-            const uint32_t to = at + (j >> 1) * 1024 + h * 4 * kChunkBytes +
-                                (((2 * (lane & 3) + e) ^ k7) << 4);
+            const uint32_t to =
+                (codes_at(stage, wl, lane) ^ (16 * e)) + j * kPairBytes + h * 4 * kChunkBytes;
             uint32_t v[4];
             asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
@@ -397,24 +431,23 @@ __device__ __noinline__ void fix_scales(uint32_t stage, int wl, int lane, uint32
     }
 }
 
-// bf16 tokens straight into the stage.
-__device__ __forceinline__ void copy_tokens(uint32_t stage, int wl, int lane, const Places &p)
+// The same halves of bf16 tokens, straight into the stage.
+__device__ __forceinline__ void copy_tokens(uint32_t stage, int wl, int lane, const Places &p,
+                                            int h)
 {
     #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int k = 8 * (i >> 1) + 2 * wl + (i & 1);
-        const uint8_t *src = shfl_ptr(p.row, i) + 16 * lane;
-        const uint32_t to = stage + (lane >> 3) * kChunkBytes + k * 128 +
-                            (((lane & 7) ^ (2 * wl + (i & 1))) << 4);
-        cp_async16(to, src);
-        cp_async16(to + 4 * kChunkBytes, src + 512);
+    for (int i = 0; i < kToks; ++i) {
+        const int k = 2 * kFeedWarps * (i >> 1) + 2 * wl + (i & 1);
+        cp_async16(stage + (4 * h + (lane >> 3)) * kChunkBytes + k * 128 +
+                       (((lane & 7) ^ (k & 7)) << 4),
+                   shfl_ptr(p.row, i) + 512 * h + 16 * lane);
     }
-    const int kr = 2 * wl + ((lane >> 3) & 1);
-    const uint32_t ur = stage + (kChunks - 1) * kChunkBytes + (8 * (lane >> 4) + kr) * 128 +
-                        (((lane & 7) ^ kr) << 4);
+    if (h == 0)
+        return;
+    const uint32_t ur = rope_at(stage, wl, lane);
     #pragma unroll
-    for (int q = 0; q < 4; ++q)
-        cp_async16(ur + q * 2048, shfl_ptr(p.rope, 4 * q + (lane >> 3)) + 16 * (lane & 7));
+    for (int q = 0; q < kToks / 4; ++q)
+        cp_async16(ur + 2 * q * kPairBytes, shfl_ptr(p.rope, 4 * q + (lane >> 3)) + 16 * (lane & 7));
 }
 
 template <int N, bool FP8>
@@ -427,9 +460,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + C::OFF_BAR);
-    uint64_t *full = bar, *empty = bar + 2, *s_full = bar + 4, *s_empty = bar + 6;
-    uint64_t *q_full = bar + 8, *q_empty = bar + 9, *p_full = bar + 10, *p_empty = bar + 11;
-    uint64_t *o_full = bar + 12, *drain = bar + 13;  // drain[2]: the MMA warps' last commits
+    // full, empty [2 stage + half]: a stage's chunks 0-3, and the rest
+    uint64_t *full = bar, *empty = bar + 4, *s_full = bar + 8, *s_empty = bar + 10;
+    uint64_t *q_full = bar + 12, *q_empty = bar + 13, *p_full = bar + 14, *p_empty = bar + 15;
+    uint64_t *o_full = bar + 16, *drain = bar + 17;  // drain[2]: the MMA warps' last commits
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + C::OFF_MISC);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
     float *smax = reinterpret_cast<float *>(smem + C::OFF_MAX);
@@ -438,9 +472,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&full[i], kLoadWarps / 2);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&full[i], kFeedWarps);
             mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&s_empty[i], kSoftWarps);
             mbar_init(&drain[i], 1);
@@ -464,42 +500,44 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this CTA's share: a prefix sum of the rows' tiles over the threads
     const int chunk = (a.rows + kThreads - 1) / kThreads;
     const int r0 = min(a.rows, tid * chunk), r1 = min(a.rows, r0 + chunk);
-    int64_t mine = 0;
+    int mine = 0;
     for (int r = r0; r < r1; ++r)
         mine += tiles_of(row_of(a, r).n);
-    int64_t upto = mine;
+    int upto = mine;
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
         upto += lane >= o ? v : 0;
     }
-    int64_t *wsum = reinterpret_cast<int64_t *>(smax);
+    int *wsum = reinterpret_cast<int *>(smax);
     if (lane == 31)
         wsum[warp] = upto;
     __syncthreads();
-    int64_t total = 0, before = upto - mine;
+    int total = 0, before = upto - mine;
+    #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) {
         total += wsum[i];
         before += i < warp ? wsum[i] : 0;
     }
-    const int c = blockIdx.x, g = c % a.groups, p = c / a.groups;
-    const int64_t shares = min((int64_t)(gridDim.x / a.groups), total);
-    const int64_t u0 = p < shares ? share_start(p, total, shares) : total;
-    const int64_t left = p < shares ? share_start(p + 1, total, shares) - u0 : 0;
+    // equal shares, the first ones a tile longer
+    const Group group = group_of(a, blockIdx.x);
+    const int p = blockIdx.y, shares = min((int)gridDim.y, total);
+    const int each = total / shares, more = total - each * shares;
+    const int u0 = p * each + min(p, more);
+    const int left = p < shares ? each + (p < more) : 0;
     int2 *place = reinterpret_cast<int2 *>(a.ws_place);
     if (left > 0 && u0 >= before && u0 < before + mine) {
-        int64_t q = before;
-        int r = r0, tl = tiles_of(row_of(a, r).n);
+        int q = before, r = r0, tl = tiles_of(row_of(a, r).n);
         while (u0 >= q + tl) {
             q += tl;
             tl = tiles_of(row_of(a, ++r).n);
         }
         misc[2] = r;
-        misc[3] = (uint32_t)(u0 - q);
-        if (g == 0)
-            place[p] = make_int2(r, (int)(u0 - q));
+        misc[3] = u0 - q;
+        if (blockIdx.x == 0)
+            place[p] = make_int2(r, u0 - q);
     }
-    if (left == 0 && g == 0 && tid == 0)
+    if (left == 0 && blockIdx.x == 0 && tid == 0)
         place[p] = make_int2(-1, 0);
     if (a.hpg * a.rpg < N) {
         // columns without a head: their query rows are zeros
@@ -510,12 +548,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = misc[0];
-    Walk w;
-    w.left = left;
-    w.r = misc[2];
-    w.t = misc[3];
-    if (left > 0)
+    Walk w = {left, 0, 0, {0, 0}};  // a CTA without a share has an empty walk
+    if (left > 0) {
+        w.r = misc[2];
+        w.t = misc[3];
         w.row = row_of(a, w.r);
+    }
     Seg s;
 
     if (warp < kSoftWarps) {
@@ -540,13 +578,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (tid < N) {
                     int j, h;
                     reinterpret_cast<int *>(smem + C::OFF_END)[tid] =
-                        column_place(a, g, tid, &j, &h) ? query_end(a, s.r, j) : s.row.n;
+                        column_place(a, group, tid, &j, &h) ? query_end(a, s.r, j) : s.row.n;
                 }
                 if (a.next > 1)
                     for (int j = 0; j < a.rpg; ++j)
                         first_end = min(first_end,
-                                        query_end(a, s.r, min(g / a.hgroups * a.rpg + j,
-                                                              a.next - 1)));
+                                        query_end(a, s.r, min(group.j0 + j, a.next - 1)));
                 named_bar_sync(1, 32 * kSoftWarps);
             }
             for (int t = s.t0; t < s.t1; ++t, ++i) {
@@ -554,8 +591,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t ph = (i >> 1) & 1;
                 // after an abort the waits return at once and the loops run
                 // out: every barrier below is still reached by all
-                (void)mbar_wait(&full[st], ph, abort_flag, a.status);
-                (void)mbar_wait(&s_full[st], ph, abort_flag, a.status);
+                (void)mbar_wait_here(&full[2 * st], ph, abort_flag, a.status);
+                (void)mbar_wait_here(&s_full[st], ph, abort_flag, a.status);
                 __syncwarp();
                 tc_fence_after();
                 uint32_t sr[4 * NH];
@@ -569,8 +606,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 #pragma unroll
                 for (int e = 0; e < 4 * NH; ++e)
                     x[e] = __uint_as_float(sr[e]);
-                const uint32_t ok = valid[4 * st + (g8 >> 1)] >> (4 * warp + (g8 & 1));
-                const bool v0 = ok & 1, v1 = ok & 4;
+                const auto exists = [&](int key) {
+                    const int pair = key / (2 * kFeedWarps), in = key % (2 * kFeedWarps);
+                    return (valid[8 * st + (in >> 1)] >> (2 * pair + (in & 1)) & 1) != 0;
+                };
+                const bool v0 = exists(key0), v1 = exists(key0 + 8);
                 if (!(v0 && v1)) {
                     #pragma unroll
                     for (int j = 0; j < NH; ++j) {
@@ -590,6 +630,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 // heads 8 j + c2 + e are entries 2 j + e of m and l
+                if (t == s.t0) {
+                    // the reference of each head begins as its first token's
+                    // score: it only has to be within range of the others
+                    if (warp == 0 && g8 == 0) {
+                        #pragma unroll
+                        for (int e = 0; e < 2 * NH; ++e)
+                            shead[8 * (e >> 1) + c2 + (e & 1)] = x[4 * (e >> 1) + (e & 1)];
+                    }
+                    named_bar_sync(1, 32 * kSoftWarps);
+                    #pragma unroll
+                    for (int e = 0; e < 2 * NH; ++e)
+                        m[e] = shead[8 * (e >> 1) + c2 + (e & 1)] * sl;
+                }
                 bool over = false;
                 #pragma unroll
                 for (int e = 0; e < 2 * NH; ++e) {
@@ -622,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (t > s.t0) {
                         // O^T of the row so far, once its last product is in
-                        (void)mbar_wait(p_empty, (i - 1) & 1, abort_flag, a.status);
+                        (void)mbar_wait_here(p_empty, (i - 1) & 1, abort_flag, a.status);
                         named_bar_sync(1, 32 * kSoftWarps);
                         tc_fence_after();
                         #pragma unroll 1
@@ -650,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P^T as bf16 (half a step of 2^-8 a weight), head rows of 64
                 // tokens, once the product before has read the last ones
                 if (i > 0)
-                    (void)mbar_wait(p_empty, (i - 1) & 1, abort_flag, a.status);
+                    (void)mbar_wait_here(p_empty, (i - 1) & 1, abort_flag, a.status);
                 __syncwarp();
                 #pragma unroll
                 for (int j = 0; j < NH; j += 2) {
@@ -687,14 +740,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             named_bar_sync(1, 32 * kSoftWarps);
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
-            float *part = a.ws_part + (int64_t)(2 * c + (k > 0)) * C::PART;
+            float *part = a.ws_part +
+                          (int64_t)(2 * (p * a.groups + (int)blockIdx.x) + (k > 0)) * C::PART;
+            int *at_col = reinterpret_cast<int *>(smem + C::OFF_END);  // whole: places in out
             if (tid < N) {
                 const float sum = smax[tid] + smax[N + tid] + smax[2 * N + tid] + smax[3 * N + tid];
                 const float mm = shead[tid];
                 if (whole) {
                     shead[tid] = sum == 0.0f ? 0.0f : 1.0f / sum;
                     int j, h;
-                    if (column_place(a, g, tid, &j, &h) && a.lse)
+                    const bool is = column_place(a, group, tid, &j, &h);
+                    at_col[tid] = is ? (int)((j * a.ldo_row + h * a.ldo_head) >> 3) : -1;
+                    if (is && a.lse)
                         a.lse[((int64_t)s.r * a.next + j) * a.ld_lse + h] =
                             sum == 0.0f ? -INFINITY : (mm + log2f(sum)) * kLn2;
                 } else {
@@ -702,136 +759,191 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[kLatent * N + N + tid] = sum;
                 }
             }
-            (void)mbar_wait(o_full, k & 1, abort_flag, a.status);
+            (void)mbar_wait_here(o_full, k & 1, abort_flag, a.status);
             named_bar_sync(1, 32 * kSoftWarps);
             tc_fence_after();
-            #pragma unroll 1
-            for (int q = 0; q < 4 * N; q += 16) {
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(tmem + lanes + q, o);
-                tmem_ld_wait();
-                const int mt = q / N, hq = q % N;  // latents 128 mt .., heads hq ..
-                if (whole) {
-                    // neighbouring lanes swap, so each stores two latents of a head
-                    const int d = 128 * mt + 32 * warp + (lane & ~1);
+            if (whole) {
+                // 32 latents (this warp's) x 16 heads at a time, turned over in
+                // the warp's part of the P buffer (free: the last product is in)
+                // so that four lanes store 64 bytes of a head
+                const uint32_t turn = p_addr + warp * 1024;
+                uint16_t *to = a.out + (int64_t)s.r * a.next * a.ldo_row + 32 * warp +
+                               8 * (lane & 3);
+                #pragma unroll 1
+                for (int q = 0; q < 4 * N; q += 16) {
+                    uint32_t o[2][8];
+                    tmem_ld_16x256b<2>(tmem + lanes + q, o[0]);
+                    tmem_ld_16x256b<2>(tmem + lanes + (16u << 16) + q, o[1]);
+                    tmem_ld_wait();
+                    const int hq = q % N;
+                    uint32_t f[2][4];  // eight heads each: latents 8 i ..
                     #pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const float y0 = __uint_as_float(o[e]) * shead[hq + e];
-                        const float y1 = __uint_as_float(o[e + 1]) * shead[hq + e + 1];
-                        const bool odd = lane & 1;
-                        const float got = __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
-                        const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(got, y1)
-                                                     : __floats2bfloat162_rn(y0, got);
-                        int j, h;
-                        if (column_place(a, g, hq + e + odd, &j, &h))
-                            *reinterpret_cast<__nv_bfloat162 *>(
-                                a.out + ((int64_t)s.r * a.next + j) * a.ldo_row + h * a.ldo_head +
-                                d) = v;
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 inv =
+                            *reinterpret_cast<const float2 *>(shead + hq + 8 * e + c2);
+                        #pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const __nv_bfloat162 v = __floats2bfloat162_rn(
+                                __uint_as_float(o[i >> 1][4 * e + 2 * (i & 1)]) * inv.x,
+                                __uint_as_float(o[i >> 1][4 * e + 2 * (i & 1) + 1]) * inv.y);
+                            f[e][i] = *reinterpret_cast<const uint32_t *>(&v);
+                        }
                     }
-                } else {
+                    __syncwarp();
+                    // head rows of 64 bytes, 16-byte pieces rotated against bank conflicts
+                    #pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        stmatrix_x4_trans(turn + (8 * e + (lane & 7)) * 64 +
+                                              (((lane >> 3) ^ ((lane >> 1) & 3)) << 4),
+                                          f[e][0], f[e][1], f[e][2], f[e][3]);
+                    __syncwarp();
+                    #pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int row = 8 * e + (lane >> 2);
+                        uint4 v;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(turn + row * 64 +
+                                           (((lane & 3) ^ ((row >> 1) & 3)) << 4)));
+                        const int off = at_col[hq + row];
+                        if (off >= 0)
+                            *reinterpret_cast<uint4 *>(to + ((int64_t)off << 3) + 128 * (q / N)) =
+                                v;
+                    }
+                }
+            } else {
+                #pragma unroll 1
+                for (int q = 0; q < 4 * N; q += 16) {
+                    uint32_t o[16];
+                    tmem_ld_32x32b_x16(tmem + lanes + q, o);
+                    tmem_ld_wait();
                     #pragma unroll
                     for (int e = 0; e < 16; e += 4)
                         *reinterpret_cast<uint4 *>(part + (int64_t)((q + e) * 128 + 4 * tid)) =
                             make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
             }
+            named_bar_sync(1, 32 * kSoftWarps);  // the next row's columns go where these were
             tc_fence_before();
         }
     } else if (warp < kWarpS) {
         // ------------------------------------------------------ token feed
-        // four warps bring the even tiles, four the odd ones, so that one
+        // half of the warps bring the even tiles, half the odd ones, so that one
         // group's loads are in flight while the other fills its stage
-        const int wl = (warp - kSoftWarps) & 3, st = (warp - kSoftWarps) >> 2;
-        const int key = 8 * (lane >> 1) + 2 * wl + (lane & 1);
-        const bool on = lane < 16;
+        const int wl = (warp - kSoftWarps) % kFeedWarps, st = (warp - kSoftWarps) / kFeedWarps;
+        const int key = 2 * kFeedWarps * (lane >> 1) + 2 * wl + (lane & 1);
+        const bool on = lane < kToks;
         const uint32_t stage = sbase + st * kStageBytes;
-        Feed f;
-        feed_start(a, f, w);
+        Feed f = {w.row, w.r, w.t, 0, left};
+        if (left > 0)
+            feed_row(f);
         if (st == 1)
             feed_next(a, f);
-        Places pl = places_of<FP8>(a, feed_slot(a, f, key, on));
-        feed_next(a, f);
-        feed_next(a, f);
-        int64_t slot = feed_slot(a, f, key, on);
+        Entry entry = feed_entry(a, f, key, on);
+        Places pl;
         Codes cd;
-        if constexpr (FP8)
-            load_codes(pl, lane, cd);
-        for (int i = st; i < (int)left; i += 2) {
-            if (i >= 2 && !mbar_wait(&empty[st], ((i >> 1) - 1) & 1, abort_flag, a.status))
-                break;
-            __syncwarp();
-            if (lane == 0)
-                valid[4 * st + wl] = (uint16_t)pl.ok;
-            if constexpr (FP8) {
-                // widen what came in while the stage was busy
-                put_codes(stage, wl, lane, cd);
-                const bool big = __vcmpgtu4(cd.scales, kPlainScale * 0x01010101u) != 0;
-                if (__any_sync(0xffffffffu, big)) {
+        for (int i = st - 2; i < left; i += 2) {
+            bool ok = true;
+            if (i >= 0) {
+                const uint32_t ph = ((i >> 1) - 1) & 1;
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    ok = ok && (i < 2 || mbar_wait_here(&empty[2 * st + h], ph, abort_flag,
+                                                        a.status));
+                    if (!ok)
+                        break;
                     __syncwarp();
-                    fix_scales(stage, wl, lane, cd.scales);
+                    if (h == 0 && lane == 0)
+                        valid[8 * st + wl] = (uint16_t)pl.ok;
+                    if constexpr (FP8) {
+                        put_codes(stage, wl, lane, cd, h);  // in registers since the last tile
+                        if (__any_sync(0xffffffffu,
+                                       __vcmpgtu4(cd.scales, kPlainScale * 0x01010101u) != 0)) {
+                            __syncwarp();
+                            fix_scales(stage, wl, lane, cd.scales, h);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&full[2 * st + h]);
+                    } else {
+                        copy_tokens(stage, wl, lane, pl, h);
+                        cp_async_commit();
+                    }
                 }
-            } else {
-                copy_tokens(stage, wl, lane, pl);
-                cp_async_wait_all();
+                if (!ok)
+                    break;
+                if constexpr (!FP8) {
+                    cp_async_wait<1>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&full[2 * st]);
+                    cp_async_wait<0>();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&full[2 * st + 1]);
+                }
             }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&full[st]);
-            // the group's next tile (its slots were fetched a tile ago)
-            pl = places_of<FP8>(a, slot);
+            // the group's next tile (its entries were fetched a tile ago)
+            pl = places_of<FP8>(a, entry);
             feed_next(a, f);
             feed_next(a, f);
-            slot = feed_slot(a, f, key, on);
+            entry = feed_entry(a, f, key, on);
             if constexpr (FP8)
                 load_codes(pl, lane, cd);
         }
+        if constexpr (!FP8)
+            cp_async_wait<0>();  // after an abort
     } else if (warp == kWarpS) {
         // -------------------------------------------- queries, S^T = K Q^T
         const bool one = elect_one();
         const uint32_t id = idesc_bf16(kTile, N, false, false);
         const uint32_t q_bytes = kChunks * a.hpg * a.rpg * 128;
-        const int qh = g % a.hgroups * a.hpg, qj = g / a.hgroups * a.rpg;
         int i = 0, k = 0;
         bool ok = true, q_flying = false;
         for (; ok && next_seg(a, w, s); ++k) {
-            if (k > 0 && !mbar_wait(q_empty, (k - 1) & 1, abort_flag, a.status))
+            if (k > 0 && !mbar_wait_here(q_empty, (k - 1) & 1, abort_flag, a.status))
                 break;
             __syncwarp();
             if (one) {
                 mbar_arrive_expect_tx(q_full, q_bytes);
                 #pragma unroll 1
                 for (int ch = 0; ch < kChunks; ++ch)
-                    tma_load_3d(smem + C::OFF_Q + ch * N * 128, &tm_q, q_full, ch * 128, qh,
-                                s.r * a.next + qj);
+                    tma_load_3d(smem + C::OFF_Q + ch * N * 128, &tm_q, q_full, ch * 128,
+                                group.h0, s.r * a.next + group.j0);
             }
             __syncwarp();
             q_flying = true;
-            if (!mbar_wait(q_full, k & 1, abort_flag, a.status))
+            if (!mbar_wait_here(q_full, k & 1, abort_flag, a.status))
                 break;
             q_flying = false;
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int st = i & 1;
                 const uint32_t ph = (i >> 1) & 1;
-                ok = mbar_wait(&full[st], ph, abort_flag, a.status) &&
-                     (i < 2 || mbar_wait(&s_empty[st], ph ^ 1, abort_flag, a.status));
+                ok = i < 2 || mbar_wait_here(&s_empty[st], ph ^ 1, abort_flag, a.status);
+                uint64_t kd = make_smem_desc(sbase + st * kStageBytes, 16, 1024, kLayoutSw128);
+                uint64_t qd = make_smem_desc(sbase + C::OFF_Q, 16, 1024, kLayoutSw128);
+                #pragma unroll 1
+                for (int ch = 0; ok && ch < kChunks; ++ch) {
+                    if (ch == 0 || ch == 4) {
+                        ok = mbar_wait_here(&full[2 * st + (ch >> 2)], ph, abort_flag, a.status);
+                        if (!ok)
+                            break;
+                        __syncwarp();
+                        tc_fence_after();
+                    }
+                    #pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + C::COL_S + st * N, kd + 2 * kk, qd + 2 * kk, id,
+                                ch + kk > 0 ? 1u : 0u, one);
+                    kd += kChunkBytes >> 4;
+                    qd += N * 128 >> 4;
+                }
                 if (!ok)
                     break;
-                __syncwarp();
-                tc_fence_after();
                 if (one) {
-                    const uint32_t ka = sbase + st * kStageBytes, qa = sbase + C::OFF_Q;
-                    #pragma unroll 1
-                    for (int ch = 0; ch < kChunks; ++ch) {
-                        #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + C::COL_S + st * N,
-                                    make_smem_desc(ka + ch * kChunkBytes + kk * 32, 16, 1024,
-                                                   kLayoutSw128),
-                                    make_smem_desc(qa + ch * N * 128 + kk * 32, 16, 1024,
-                                                   kLayoutSw128),
-                                    id, ch + kk > 0 ? 1u : 0u);
-                    }
                     mma_commit(&s_full[st]);
                     if (t + 1 == s.t1)
                         mma_commit(q_empty);
@@ -844,8 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&drain[0]);
             __syncwarp();
             if (q_flying)
-                (void)mbar_wait_drain(q_full, k & 1);
-            (void)mbar_wait_drain(&drain[0], 0);
+                (void)mbar_drain_here(q_full, k & 1);
+            (void)mbar_drain_here(&drain[0], 0);
         }
     } else {
         // --------------------------------------------- O^T += K^T P^T
@@ -856,24 +968,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && next_seg(a, w, s)) {
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int st = i & 1;
-                ok = mbar_wait(p_full, i & 1, abort_flag, a.status);
+                ok = mbar_wait_here(p_full, i & 1, abort_flag, a.status);
                 if (!ok)
                     break;
                 __syncwarp();
                 tc_fence_after();
+                uint64_t vd =
+                    make_smem_desc(sbase + st * kStageBytes, kChunkBytes, 1024, kLayoutSw128);
+                const uint64_t pd = make_smem_desc(sbase + C::OFF_P, 16, 1024, kLayoutSw128);
+                #pragma unroll
+                for (int mt = 0; mt < 4; ++mt) {
+                    #pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16(tmem + mt * N, vd + kk * (2048 >> 4), pd + 2 * kk, id,
+                                t > s.t0 || kk > 0 ? 1u : 0u, one);
+                    vd += 2 * kChunkBytes >> 4;
+                    if ((mt & 1) && one)
+                        mma_commit(&empty[2 * st + (mt >> 1)]);
+                }
                 if (one) {
-                    const uint32_t va = sbase + st * kStageBytes, pa = sbase + C::OFF_P;
-                    #pragma unroll 1
-                    for (int mt = 0; mt < 4; ++mt) {
-                        #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_f16(tmem + mt * N,
-                                    make_smem_desc(va + 2 * mt * kChunkBytes + kk * 2048,
-                                                   kChunkBytes, 1024, kLayoutSw128),
-                                    make_smem_desc(pa + kk * 32, 16, 1024, kLayoutSw128), id,
-                                    t > s.t0 || kk > 0 ? 1u : 0u);
-                    }
-                    mma_commit(&empty[st]);
                     mma_commit(p_empty);
                     if (t + 1 == s.t1)
                         mma_commit(o_full);
@@ -885,7 +998,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one)
                 mma_commit(&drain[1]);
             __syncwarp();
-            (void)mbar_wait_drain(&drain[1], 0);
+            (void)mbar_drain_here(&drain[1], 0);
         }
     }
     tc_fence_before();
@@ -909,6 +1022,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
     pdl_launch_dependents();
     const int2 *place = reinterpret_cast<const int2 *>(a.ws_place);
     const int p = blockIdx.x + 1, shares = gridDim.x + 1, g = blockIdx.z;
+    const Group group = group_of(a, g);
     const int2 here = place[p], prev = place[p - 1];
     const bool prev_same = prev.x == here.x;
     if (here.x < 0 || here.y == 0 || (prev_same && prev.y > 0))
@@ -958,7 +1072,7 @@ __global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArg
     #pragma unroll
     for (int e = 0; e < 4; ++e) {
         int j, h;
-        if (!column_place(a, g, 4 * quad + e, &j, &h))
+        if (!column_place(a, group, 4 * quad + e, &j, &h))
             continue;
         const int64_t r = (int64_t)here.x * a.next + j;
         reinterpret_cast<__nv_bfloat16 *>(a.out)[r * a.ldo_row + h * a.ldo_head + 128 * mt + d] =
@@ -980,7 +1094,7 @@ size_t place_bytes()
 }
 
 template <int N, bool FP8>
-idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int ctas, cudaStream_t s)
+idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int shares, cudaStream_t s)
 {
     using C = Cfg<N>;
     static_assert(C::SMEM <= 227 * 1024, "shared memory of a CTA");
@@ -996,8 +1110,7 @@ idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int ctas, cudaS
             return IDX_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaError_t e = launch_pdl(kern, dim3(ctas), dim3(kThreads), C::SMEM, s, tm, a);
-    const int shares = ctas / a.groups;
+    cudaError_t e = launch_pdl(kern, dim3(a.groups, shares), dim3(kThreads), C::SMEM, s, tm, a);
     if (e == cudaSuccess && shares > 1)
         e = launch_pdl(latent_join_kernel<N>, dim3(shares - 1, 4 * (N / 8), a.groups),
                        dim3(kJoinThreads), 0, s, a);
@@ -1035,14 +1148,17 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
     a.inv_hpg = 65536 / a.hpg + 1;
     a.hgroups = (a.H + a.hpg - 1) / a.hpg;
     a.groups = a.hgroups * ((a.next + a.rpg - 1) / a.rpg);
-    if (a.groups > sm_count())
+    // places in out are kept in units of eight elements, in 32 bits
+    const int64_t span = (a.next - 1) * a.ldo_row + (a.H - 1) * a.ldo_head;
+    if (a.groups > sm_count() || most > INT32_MAX || a.pool.stride > INT32_MAX ||
+        span / 8 > INT32_MAX)
         return IDX_ERR_UNSUPPORTED;
+    a.page_stride = (int)a.pool.stride;
     const int n = columns_of(a.hpg * a.rpg);
     a.ws_place = ws;
     a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + place_bytes());
     // one CTA per SM, the same number for every group
     const int shares = (int)std::min<int64_t>(sm_count() / a.groups, most);
-    const int ctas = shares * a.groups;
     CUtensorMap tm;
     // bytes of a head row, heads, rows; a stride over one element is free
     const uint64_t dims[3] = {2 * kLatTok, (uint64_t)a.H, (uint64_t)R};
@@ -1053,9 +1169,9 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
         return IDX_ERR_UNSUPPORTED;
     const bool fp8 = fmt == IDX_LATENT_FP8_E4M3;
     switch (n) {
-    case 16: return fp8 ? launch_attn<16, true>(tm, a, ctas, s) : launch_attn<16, false>(tm, a, ctas, s);
-    case 32: return fp8 ? launch_attn<32, true>(tm, a, ctas, s) : launch_attn<32, false>(tm, a, ctas, s);
-    default: return fp8 ? launch_attn<64, true>(tm, a, ctas, s) : launch_attn<64, false>(tm, a, ctas, s);
+    case 16: return fp8 ? launch_attn<16, true>(tm, a, shares, s) : launch_attn<16, false>(tm, a, shares, s);
+    case 32: return fp8 ? launch_attn<32, true>(tm, a, shares, s) : launch_attn<32, false>(tm, a, shares, s);
+    default: return fp8 ? launch_attn<64, true>(tm, a, shares, s) : launch_attn<64, false>(tm, a, shares, s);
     }
 }
 
@@ -1098,7 +1214,7 @@ extern "C" idx_status idx_latent_attention(
     a.pool = make_pool(kv_pages, page_stride_bytes, num_pages, page_size);
     a.slots = slots;
     a.indptr = indptr;
-    a.num_slots = num_slots;
+    a.num_slots = (int)std::min<int64_t>(num_slots, INT32_MAX);
     a.rows = R;
     a.next = 1;
     a.H = H;

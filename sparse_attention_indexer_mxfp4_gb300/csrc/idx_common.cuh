@@ -289,28 +289,44 @@ IDX_DEVFN void mma_f8f6f4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uin
 }
 
 // The same with bf16 operands (kind::f16), issued by the thread with `issue`
-// set: the warp stays converged around it, so that the descriptors can be
-// computed once for the warp.
-IDX_DEVFN void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+// set: the warp stays converged around it, so that the operands are computed
+// once for the warp (in uniform registers, where the instruction wants them).
+// The matrices come as the low words of their descriptors (desc_lo) and the
+// high word both share: only the low word moves from one MMA to the next.
+IDX_DEVFN void mma_f16(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                        uint32_t accumulate, uint32_t issue)
 {
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "setp.ne.b32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\t"
+                 "setp.ne.b32 q, %6, 0;\n\t"
+                 "mov.b64 a, {%1, %3};\n\t"
+                 "mov.b64 b, {%2, %3};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(issue)
                  : "memory");
 }
 
 // The same with A (M x K, two bf16 a column) in tensor memory.
-IDX_DEVFN void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                          uint32_t accumulate, uint32_t issue)
+IDX_DEVFN void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi,
+                          uint32_t idesc, uint32_t accumulate, uint32_t issue)
 {
-    asm volatile("{\n\t.reg .pred p, q;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "setp.ne.b32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-                 "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(issue)
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\t"
+                 "setp.ne.b32 q, %6, 0;\n\t"
+                 "mov.b64 b, {%2, %3};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+                 "r"(a_tmem), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(issue)
+                 : "memory");
+}
+
+// mma_commit by the thread with `issue` set.
+IDX_DEVFN void mma_commit_if(uint64_t *bar, uint32_t issue)
+{
+    asm volatile("{\n\t.reg .pred q;\n\t"
+                 "setp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+                     smem_u32(bar)),
+                 "r"(issue)
                  : "memory");
 }
 
@@ -489,6 +505,16 @@ IDX_DEVFN uint64_t make_smem_desc(uint32_t saddr, uint32_t lbo_bytes, uint32_t s
     d |= layout << 61;
     return d;
 }
+
+// The two words of make_smem_desc for 128-byte swizzled rows in groups of
+// eight (1024 bytes); lbo: bytes between columns of 64 elements where the
+// matrix is not K-major.
+IDX_DEVFN uint32_t desc_lo(uint32_t saddr, uint32_t lbo_bytes = 16)
+{
+    return ((saddr & 0x3FFFF) >> 4) | ((lbo_bytes >> 4) << 16);
+}
+
+constexpr uint32_t kDescHiSw128 = (1024u >> 4) | (1u << 14) | ((uint32_t)kLayoutSw128 << 29);
 
 // ------------------------------------------------------------- misc helpers
 

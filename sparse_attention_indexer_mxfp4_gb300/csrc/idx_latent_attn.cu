@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *smax = reinterpret_cast<float *>(smem + C::OFF_MAX);
     float *shead = reinterpret_cast<float *>(smem + C::OFF_HEAD);
     uint16_t *valid = reinterpret_cast<uint16_t *>(smem + C::OFF_VALID);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     if (tid == 0) {
         for (int i = 0; i < 4; ++i) {
@@ -547,7 +548,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
+    // one value for the warp, as the compiler sees it too
+    const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     Walk w = {left, 0, 0, {0, 0}};  // a CTA without a share has an empty walk
     if (left > 0) {
         w.r = misc[2];
@@ -923,9 +925,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int st = i & 1;
                 const uint32_t ph = (i >> 1) & 1;
                 ok = i < 2 || mbar_wait_here(&s_empty[st], ph ^ 1, abort_flag, a.status);
-                uint64_t kd = make_smem_desc(sbase + st * kStageBytes, 16, 1024, kLayoutSw128);
-                uint64_t qd = make_smem_desc(sbase + C::OFF_Q, 16, 1024, kLayoutSw128);
-                #pragma unroll 1
+                const uint32_t kd = desc_lo(sbase + st * kStageBytes);
+                const uint32_t qd = desc_lo(sbase + C::OFF_Q);
+                #pragma unroll
                 for (int ch = 0; ok && ch < kChunks; ++ch) {
                     if (ch == 0 || ch == 4) {
                         ok = mbar_wait_here(&full[2 * st + (ch >> 2)], ph, abort_flag, a.status);
@@ -936,18 +938,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + C::COL_S + st * N, kd + 2 * kk, qd + 2 * kk, id,
+                        mma_f16(tmem + C::COL_S + st * N, kd + (ch * kChunkBytes >> 4) + 2 * kk,
+                                qd + (ch * N * 128 >> 4) + 2 * kk, kDescHiSw128, id,
                                 ch + kk > 0 ? 1u : 0u, one);
-                    kd += kChunkBytes >> 4;
-                    qd += N * 128 >> 4;
                 }
                 if (!ok)
                     break;
-                if (one) {
-                    mma_commit(&s_full[st]);
-                    if (t + 1 == s.t1)
-                        mma_commit(q_empty);
-                }
+                mma_commit_if(&s_full[st], one);
+                mma_commit_if(q_empty, one && t + 1 == s.t1);
                 __syncwarp();
             }
         }
@@ -973,24 +971,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 __syncwarp();
                 tc_fence_after();
-                uint64_t vd =
-                    make_smem_desc(sbase + st * kStageBytes, kChunkBytes, 1024, kLayoutSw128);
-                const uint64_t pd = make_smem_desc(sbase + C::OFF_P, 16, 1024, kLayoutSw128);
+                const uint32_t vd = desc_lo(sbase + st * kStageBytes, kChunkBytes);
+                const uint32_t pd = desc_lo(sbase + C::OFF_P);
                 #pragma unroll
                 for (int mt = 0; mt < 4; ++mt) {
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + mt * N, vd + kk * (2048 >> 4), pd + 2 * kk, id,
-                                t > s.t0 || kk > 0 ? 1u : 0u, one);
-                    vd += 2 * kChunkBytes >> 4;
-                    if ((mt & 1) && one)
-                        mma_commit(&empty[2 * st + (mt >> 1)]);
+                        mma_f16(tmem + mt * N, vd + (2 * mt * kChunkBytes >> 4) + kk * (2048 >> 4),
+                                pd + 2 * kk, kDescHiSw128, id, t > s.t0 || kk > 0 ? 1u : 0u, one);
+                    if (mt & 1)
+                        mma_commit_if(&empty[2 * st + (mt >> 1)], one);
                 }
-                if (one) {
-                    mma_commit(p_empty);
-                    if (t + 1 == s.t1)
-                        mma_commit(o_full);
-                }
+                mma_commit_if(p_empty, one);
+                mma_commit_if(o_full, one && t + 1 == s.t1);
                 __syncwarp();
             }
         }

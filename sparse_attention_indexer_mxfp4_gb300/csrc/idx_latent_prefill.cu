@@ -132,7 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *q_full = s_full + 6, *tail = s_full + 7, *drain = s_full + 8;
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int head = blockIdx.y;
 
     if (tid == 0) {
@@ -159,15 +160,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_launch_dependents();
     Block k;
     const bool some = find_block(a, blockIdx.x, a.tiles * kTile, k);
-    int nt[2] = {0, 0};
-    if (some) {
-        nt[0] = key_tiles(a, k, 0);
-        nt[1] = key_tiles(a, k, 1);
-    }
-    const int most = max(nt[0], nt[1]);
+    // key tiles of the two query tiles
+    const int nt0 = some ? key_tiles(a, k, 0) : 0, nt1 = some ? key_tiles(a, k, 1) : 0;
+    const int most = max(nt0, nt1);
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = misc[0];
+    // one value for the warp, as the compiler sees it too
+    const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
 
     if (!some) {
         // nothing here: only the tensor memory to give back
@@ -182,8 +181,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int seen = row < k.nq ? keys_seen(a, k, row) : 0;
         const int seen_first = __shfl_sync(0xffffffffu, seen, 0);  // the warp's fewest, if it has them
         const bool whole_warp = __all_sync(0xffffffffu, row < k.nq);
+        const int nt = q ? nt1 : nt0;
         float m = -INFINITY, l = 0.0f;
-        for (int j = 0; j < nt[q]; ++j) {
+        for (int j = 0; j < nt; ++j) {
             // after an abort the waits return at once and the loop runs out
             (void)mbar_wait(&s_full[q], j & 1, abort_flag, a.status);
             __syncwarp();
@@ -258,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive(&p_full[q]);
         }
-        if (nt[q] > 0) {
-            (void)mbar_wait(&pv_done[q], (nt[q] - 1) & 1, abort_flag, a.status);
+        if (nt > 0) {
+            (void)mbar_wait(&pv_done[q], (nt - 1) & 1, abort_flag, a.status);
             __syncwarp();
             tc_fence_after();
         }
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         #pragma unroll 1
         for (int c = 0; c < 128; c += 16) {
             uint32_t o[16];
-            if (nt[q] > 0) {
+            if (nt > 0) {
                 tmem_ld_32x32b_x16(col_o + c, o);
                 tmem_ld_wait();
             } else {
@@ -299,11 +299,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;           // pieces issued
         bool q_flying = false, ok = most > 0;
         if (ok && one) {
-            mbar_arrive_expect_tx(q_full, (nt[1] > 0 ? 2 : 1) * kQPieces * kPiece);
+            mbar_arrive_expect_tx(q_full, (nt1 > 0 ? 2 : 1) * kQPieces * kPiece);
             #pragma unroll 1
-            for (int q = 0; q < 2; ++q) {
-                if (nt[q] == 0 && q == 1)
-                    break;
+            for (int q = 0; q < (nt1 > 0 ? 2 : 1); ++q) {
                 #pragma unroll 1
                 for (int c = 0; c < kQPieces; ++c)
                     tma_load_3d(smem + (q * kQPieces + c) * kPiece, &tm_q, q_full, 128 * c, head,
@@ -370,62 +368,57 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = most > 0 && mbar_wait(q_full, 0, abort_flag, a.status);
         // S of query tile q and key tile j; the last query tile frees the keys
         const auto scores = [&](int q, int j) {
-            #pragma unroll 1
+            const bool last = q == 1 || nt1 <= j;
+            const uint32_t qd = desc_lo(sbase + q * kQPieces * kPiece);
+            #pragma unroll
             for (int c = 0; c < kQPieces; ++c) {
                 const int n = j * kPieces + c, slot = n & (kRing - 1);
                 if (!mbar_wait(&full[slot], (n >> 3) & 1, abort_flag, a.status))
                     return false;
                 __syncwarp();
                 tc_fence_after();
-                const uint64_t qd = make_smem_desc(sbase + (q * kQPieces + c) * kPiece, 16, 1024,
-                                                   kLayoutSw128);
-                const uint64_t kd =
-                    make_smem_desc(sbase + kOffRing + slot * kPiece, 16, 1024, kLayoutSw128);
+                const uint32_t kd = desc_lo(sbase + kOffRing + slot * kPiece);
                 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    mma_f16(tmem + kColS + q * 128, qd + 2 * e, kd + 2 * e, id_s,
-                            c + e > 0 ? 1u : 0u, one);
-                if (one && (q == 1 || nt[1] <= j))
-                    mma_commit(&empty[slot]);
+                    mma_f16(tmem + kColS + q * 128, qd + (c * kPiece >> 4) + 2 * e, kd + 2 * e,
+                            kDescHiSw128, id_s, c + e > 0 ? 1u : 0u, one);
+                mma_commit_if(&empty[slot], one && last);
             }
-            if (one)
-                mma_commit(&s_full[q]);
-            __syncwarp();
+            mma_commit_if(&s_full[q], one);
             return true;
         };
         const auto values = [&](int q, int j) {
+            const bool last = q == 1 || nt1 <= j;
             if (!mbar_wait(&p_full[q], j & 1, abort_flag, a.status))
                 return false;
-            #pragma unroll 1
+            #pragma unroll
             for (int c = 0; c < kVPieces; ++c) {
                 const int n = j * kPieces + kQPieces + c, slot = n & (kRing - 1);
                 if (!mbar_wait(&full[slot], (n >> 3) & 1, abort_flag, a.status))
                     return false;
                 __syncwarp();
                 tc_fence_after();
-                const uint64_t vd =
-                    make_smem_desc(sbase + kOffRing + slot * kPiece, kPiece, 1024, kLayoutSw128);
+                const uint32_t vd = desc_lo(sbase + kOffRing + slot * kPiece);
                 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     mma_f16_ts(tmem + kColO + q * 128 + 64 * c, tmem + kColS + q * 128 + 8 * e,
-                               vd + e * (2048 >> 4), id_v, j + e > 0 ? 1u : 0u, one);
-                if (one && (q == 1 || nt[1] <= j))
-                    mma_commit(&empty[slot]);
+                               vd + e * (2048 >> 4), kDescHiSw128, id_v, j + e > 0 ? 1u : 0u, one);
+                mma_commit_if(&empty[slot], one && last);
             }
-            if (one)
-                mma_commit(&pv_done[q]);
-            __syncwarp();
+            mma_commit_if(&pv_done[q], one);
             return true;
         };
-        for (int q = 0; q < 2; ++q)
-            if (ok && nt[q] > 0)
-                ok = scores(q, 0);
+        if (ok && nt0 > 0)
+            ok = scores(0, 0);
+        if (ok && nt1 > 0)
+            ok = scores(1, 0);
         for (int j = 0; ok && j < most; ++j) {
-            #pragma unroll 1
-            for (int q = 0; ok && q < 2; ++q) {
-                if (j < nt[q])
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int nt = q ? nt1 : nt0;
+                if (ok && j < nt)
                     ok = values(q, j);
-                if (ok && j + 1 < nt[q])
+                if (ok && j + 1 < nt)
                     ok = scores(q, j + 1);
             }
         }

@@ -85,6 +85,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load libidx.so (building it first if the sources are newer)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build() if not os.environ.get("IDX_NO_BUILD") else _build.LIB
@@ -121,10 +123,17 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (a tenth of
+# the time, which a decode step's calls notice), where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _u8(t):
@@ -591,32 +600,40 @@ def latent_page_bytes(page_size, fmt) -> int:
 
 
 def _need_pages(t):
-    if t.dtype != torch.uint8 or t.dim() != 2 or t.stride(1) != 1:
+    """The number of pages and the bytes between them."""
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.uint8 or len(shape) != 2 or stride[1] != 1:
         raise ValueError("kv_pages must be uint8 [num_pages, page_stride] with unit byte stride")
+    return shape[0], stride[0]
 
 
 def _need_heads(t, dims, dim, name):
     """bf16, `dims` dimensions, the last one of `dim` contiguous elements."""
-    if t.dtype != torch.bfloat16 or t.dim() != dims or t.shape[-1] != dim or t.stride(-1) != 1:
+    shape, stride = t.shape, t.stride()
+    if t.dtype != torch.bfloat16 or len(shape) != dims or shape[-1] != dim or stride[-1] != 1:
         raise ValueError(f"{name} must be bfloat16 [..., {dim}] of {dims} dimensions with unit "
                          "last stride")
+    return shape, stride
 
 
 def _out_lse(out, lse, rows, heads, dim, device):
-    """The outputs of an attention call, made here unless given; lse False: none."""
+    """The outputs of an attention call, made here unless given (lse False:
+    none), and their strides: row and head of out, row of lse."""
     if out is None:
         out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=device)
+        ldo = (heads * dim, dim)
     else:
-        _need_heads(out, 3, dim, "out")
-        if out.shape[0] != rows or out.shape[1] != heads:
+        shape, ldo = _need_heads(out, 3, dim, "out")
+        if shape[0] != rows or shape[1] != heads:
             raise ValueError(f"out must be [{rows}, {heads}, {dim}]")
     if lse is False:
-        return out, None
+        return out, None, ldo[0], ldo[1], 0
     if lse is None:
         lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
-    elif (lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.stride(1) != 1):
+        return out, lse, ldo[0], ldo[1], heads
+    if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.stride(1) != 1:
         raise ValueError(f"lse must be float32 [{rows}, {heads}] with unit column stride")
-    return out, lse
+    return out, lse, ldo[0], ldo[1], lse.stride(0)
 
 
 def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
@@ -625,10 +642,9 @@ def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, pag
     elements to rotate; row stride free); positions int32 [T] and cos_sin fp32
     [P, 64] (both None: stored as they are); norm_weight fp32 [512] (None: no
     norm); slot_mapping int64 [T], negative skips."""
-    _need_heads(kv, 2, LATENT_DIM + LATENT_ROPE, "kv")
+    (T, _), (ld_kv, _) = _need_heads(kv, 2, LATENT_DIM + LATENT_ROPE, "kv")
     _need(slot_mapping, torch.int64, "slot_mapping")
-    _need_pages(kv_pages)
-    T = kv.shape[0]
+    pages, stride = _need_pages(kv_pages)
     if slot_mapping.numel() != T:
         raise ValueError(f"slot_mapping must hold {T} entries")
     if (cos_sin is None) != (positions is None):
@@ -646,9 +662,9 @@ def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, pag
         _need(norm_weight, torch.float32, "norm_weight")
         if norm_weight.numel() != LATENT_DIM:
             raise ValueError(f"norm_weight must hold {LATENT_DIM} entries")
-    args = (_ptr(kv), kv.stride(0), _ptr(positions), _ptr(cos_sin), ld, rows, _ptr(norm_weight),
-            float(eps), T, LATENT_DIM, LATENT_ROPE, fmt, _ptr(kv_pages), kv_pages.stride(0),
-            kv_pages.shape[0], page_size, _ptr(slot_mapping))
+    args = (_ptr(kv), ld_kv, _ptr(positions), _ptr(cos_sin), ld, rows, _ptr(norm_weight), eps, T,
+            LATENT_DIM, LATENT_ROPE, fmt, _ptr(kv_pages), stride, pages, page_size,
+            _ptr(slot_mapping))
     return Prepared("idx_latent_store", args,
                     (kv, positions, cos_sin, norm_weight, kv_pages, slot_mapping))
 
@@ -663,20 +679,21 @@ def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, s
     """Cached tokens back as rows of out (bf16 [N, 576], row stride free):
     rows cu_lens[b] .. cu_lens[b + 1] are sequence b's tokens from
     seq_starts[b] (None: 0) on.  cu_lens int32 [B + 1], seq_starts int32 [B]."""
-    _need_pages(kv_pages)
-    _need_heads(out, 2, LATENT_DIM + LATENT_ROPE, "out")
+    pages, stride = _need_pages(kv_pages)
+    (rows, _), (ld_out, _) = _need_heads(out, 2, LATENT_DIM + LATENT_ROPE, "out")
     _need(block_table, torch.int32, "block_table")
     _need(cu_lens, torch.int32, "cu_lens")
     B_ = cu_lens.numel() - 1
-    if block_table.dim() != 2 or block_table.shape[0] < B_ or B_ < 0:
+    table = block_table.shape
+    if len(table) != 2 or table[0] < B_ or B_ < 0:
         raise ValueError("block_table must be [B, blocks] and cu_lens [B + 1]")
     if seq_starts is not None:
         _need(seq_starts, torch.int32, "seq_starts")
         if seq_starts.numel() != B_:
             raise ValueError(f"seq_starts must hold {B_} entries")
-    args = (_ptr(kv_pages), kv_pages.stride(0), kv_pages.shape[0], page_size, fmt, LATENT_DIM,
-            LATENT_ROPE, _ptr(block_table), block_table.stride(0), block_table.shape[1],
-            _ptr(cu_lens), _ptr(seq_starts), B_, out.shape[0], _ptr(out), out.stride(0))
+    args = (_ptr(kv_pages), stride, pages, page_size, fmt, LATENT_DIM, LATENT_ROPE,
+            _ptr(block_table), table[1], table[1], _ptr(cu_lens), _ptr(seq_starts), B_, rows,
+            _ptr(out), ld_out)
     return Prepared("idx_latent_gather", args, (kv_pages, block_table, cu_lens, seq_starts, out))
 
 
@@ -692,10 +709,11 @@ def latent_attention_workspace_size(rows, heads) -> int:
 
 
 def _latent_ws(workspace, rows, heads, device):
+    """The scratch of an absorbed attention call and its bytes."""
     if workspace is True:
-        return torch.empty(latent_attention_workspace_size(rows, heads), dtype=torch.uint8,
-                           device=device)
-    return workspace
+        n = lib().idx_latent_attention_workspace_size(rows, heads)
+        return torch.empty(n, dtype=torch.uint8, device=device), n
+    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
@@ -705,19 +723,18 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
     [R, H, 512] and lse fp32 [R, H] are made here when None (lse False:
     none).  workspace: True allocates the scratch here, or a uint8 tensor of
     latent_attention_workspace_size(R, H) bytes."""
-    _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
-    _need_pages(kv_pages)
+    (R, H, _), (ldq, ldqh, _) = _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
+    pages, stride = _need_pages(kv_pages)
     _need(slots, torch.int32, "slots")
     _need(indptr, torch.int32, "indptr")
-    R, H = q.shape[0], q.shape[1]
     if indptr.numel() != R + 1:
         raise ValueError(f"indptr must hold {R + 1} entries")
-    out, lse = _out_lse(out, lse, R, H, LATENT_DIM, q.device)
-    ws = _latent_ws(workspace, R, H, q.device)
-    args = (_ptr(q), q.stride(0), q.stride(1), _ptr(kv_pages), kv_pages.stride(0),
-            kv_pages.shape[0], page_size, fmt, _ptr(slots), _ptr(indptr), slots.numel(), R, H,
-            LATENT_DIM, LATENT_ROPE, scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
-            0 if lse is None else lse.stride(0), _ptr(ws), 0 if ws is None else ws.numel())
+    device = q.device
+    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
+    ws, ws_bytes = _latent_ws(workspace, R, H, device)
+    args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(slots),
+            _ptr(indptr), slots.numel(), R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
+            ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
     return Prepared("idx_latent_attention", args, (q, kv_pages, slots, indptr, out, lse, ws))
 
 
@@ -736,11 +753,10 @@ def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, con
     """Absorbed latent attention over whole paged contexts: row j of sequence
     b attends to its first context_lens[b] - next_n + j + 1 tokens (or
     context_lens[row] with ctx_per_row).  q bf16 [B * next_n, H, 576]."""
-    _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
-    _need_pages(kv_pages)
+    (R, H, _), (ldq, ldqh, _) = _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
+    pages, stride = _need_pages(kv_pages)
     _need(block_table, torch.int32, "block_table")
     _need(context_lens, torch.int32, "context_lens")
-    R, H = q.shape[0], q.shape[1]
     if next_n <= 0 or R % next_n:
         raise ValueError("q must hold B * next_n rows")
     B_ = R // next_n
@@ -749,13 +765,13 @@ def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, con
         raise ValueError(f"context_lens must hold {want} entries")
     if block_table.dim() != 2 or block_table.shape[0] < B_:
         raise ValueError(f"block_table must be [{B_}, blocks]")
-    out, lse = _out_lse(out, lse, R, H, LATENT_DIM, q.device)
-    ws = _latent_ws(workspace, R, H, q.device)
-    args = (_ptr(q), q.stride(0), q.stride(1), _ptr(kv_pages), kv_pages.stride(0),
-            kv_pages.shape[0], page_size, fmt, _ptr(block_table), block_table.stride(0),
-            _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len, H, LATENT_DIM,
-            LATENT_ROPE, scale, _ptr(out), out.stride(0), out.stride(1), _ptr(lse),
-            0 if lse is None else lse.stride(0), _ptr(ws), 0 if ws is None else ws.numel())
+    device = q.device
+    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
+    ws, ws_bytes = _latent_ws(workspace, R, H, device)
+    args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(block_table),
+            block_table.shape[1], _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len,
+            H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws),
+            ws_bytes)
     return Prepared("idx_paged_latent_attention", args,
                     (q, kv_pages, block_table, context_lens, out, lse, ws))
 
@@ -776,22 +792,21 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
     (128, then 64 rotated), k bf16 [Tk, H, 128], k_rope bf16 [Tk, 64], v bf16
     [Tk, H, 128], every outer stride free; cu_q, cu_k int32 [B + 1]; out bf16
     [Tq, H, 128] and lse fp32 [Tq, H] as in prepare_latent_attention."""
-    _need_heads(q, 3, 192, "q")
-    _need_heads(k, 3, 128, "k")
-    _need_heads(k_rope, 2, LATENT_ROPE, "k_rope")
-    _need_heads(v, 3, 128, "v")
+    (Tq, H, _), (ldq, ldqh, _) = _need_heads(q, 3, 192, "q")
+    (Tk, Hk, _), (ldk, ldkh, _) = _need_heads(k, 3, 128, "k")
+    (Tr, _), (ldr, _) = _need_heads(k_rope, 2, LATENT_ROPE, "k_rope")
+    (Tv, Hv, _), (ldv, ldvh, _) = _need_heads(v, 3, 128, "v")
     _need(cu_q, torch.int32, "cu_q")
     _need(cu_k, torch.int32, "cu_k")
-    Tq, H, Tk = q.shape[0], q.shape[1], k.shape[0]
-    if k.shape[1] != H or v.shape[1] != H or v.shape[0] != Tk or k_rope.shape[0] != Tk:
+    if Hk != H or Hv != H or Tv != Tk or Tr != Tk:
         raise ValueError("k, k_rope and v must hold the same tokens, and the heads of q")
-    if cu_q.numel() != cu_k.numel() or cu_q.numel() < 1:
+    B_ = cu_q.numel() - 1
+    if cu_k.numel() != B_ + 1 or B_ < 0:
         raise ValueError("cu_q and cu_k must both hold B + 1 entries")
-    out, lse = _out_lse(out, lse, Tq, H, 128, q.device)
-    args = (_ptr(q), q.stride(0), q.stride(1), _ptr(k), k.stride(0), k.stride(1), _ptr(k_rope),
-            k_rope.stride(0), _ptr(v), v.stride(0), v.stride(1), _ptr(cu_q), _ptr(cu_k),
-            cu_q.numel() - 1, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal), _ptr(out),
-            out.stride(0), out.stride(1), _ptr(lse), 0 if lse is None else lse.stride(0))
+    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, Tq, H, 128, q.device)
+    args = (_ptr(q), ldq, ldqh, _ptr(k), ldk, ldkh, _ptr(k_rope), ldr, _ptr(v), ldv, ldvh,
+            _ptr(cu_q), _ptr(cu_k), B_, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal),
+            _ptr(out), ldo, ldoh, _ptr(lse), ldl)
     return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse))
 
 

@@ -815,12 +815,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             } else {
                 #pragma unroll 1
-                for (int q = 0; q < 4 * N; q += 16) {
-                    uint32_t o[16];
-                    tmem_ld_32x32b_x16(tmem + lanes + q, o);
+                for (int q = 0; q < 4 * N; q += 32) {
+                    uint32_t o[32];
+                    tmem_ld_32x32b_x32(tmem + lanes + q, o);
                     tmem_ld_wait();
                     #pragma unroll
-                    for (int e = 0; e < 16; e += 4)
+                    for (int e = 0; e < 32; e += 4)
                         *reinterpret_cast<uint4 *>(part + (int64_t)((q + e) * 128 + 4 * tid)) =
                             make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                 }
@@ -1001,78 +1001,137 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tmem, C::TM_COLS);
 }
 
-// Joins the partial results of a row that several shares hold: the CTAs of
-// boundary p (blockIdx.x + 1) act if it is the first that cuts its row, the
-// shares before and after it holding the pieces.  Threads: 128 latents x 2 of
-// a group's quads of columns; blockIdx.z: the group.
-constexpr int kJoinThreads = 256;
+// Joins the partial results of a row that several shares hold:
+//     out = sum_q 2^(m_q - m) O_q / sum_q 2^(m_q - m) l_q,   m = max_q m_q.
+// blockIdx.x: the row, or (more rows than shares) a boundary between shares,
+// which acts if it is the first that cuts its row; blockIdx.y: an equal part of
+// the group's slices (128 latents x a quad of columns); blockIdx.z: the group.
+// With few pieces the four groups of 128 threads take a slice each, with many
+// each takes every fourth piece of one, so that the loads are in flight
+// together: the pieces lie in L2 and the kernel is a chain of their latencies.
+constexpr int kJoinThreads = 512;
+constexpr int kJoinFew = 8;
+constexpr int kMaxShares = 152;
 
 template <int N>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArgs a)
+__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArgs a, int shares)
 {
     using C = Cfg<N>;
+    constexpr int kRuns = kJoinThreads / N;  // threads a column in the first phase
+    __shared__ int s_first, s_count;
+    __shared__ __align__(16) float wt[kMaxShares * N];  // a piece's weight for each column
+    __shared__ float run[kRuns][N], inv[N];
+    __shared__ float4 part[3][128];
+    const int tid = threadIdx.x, g = blockIdx.z;
+    if (tid == 0) {
+        s_first = INT_MAX;
+        s_count = 0;
+    }
     pdl_wait();
     pdl_launch_dependents();
     const int2 *place = reinterpret_cast<const int2 *>(a.ws_place);
-    const int p = blockIdx.x + 1, shares = gridDim.x + 1, g = blockIdx.z;
-    const Group group = group_of(a, g);
-    const int2 here = place[p], prev = place[p - 1];
-    const bool prev_same = prev.x == here.x;
-    if (here.x < 0 || here.y == 0 || (prev_same && prev.y > 0))
+    const bool by_row = a.rows < shares;
+    const int2 mine = tid < shares ? place[tid] : make_int2(-1, 0);
+    const int row = by_row ? (int)blockIdx.x : place[blockIdx.x + 1].x;
+    __syncthreads();
+    // shares that begin inside the row: they and the one before hold its pieces
+    if (tid > 0 && row >= 0 && mine.x == row && mine.y > 0) {
+        atomicMin(&s_first, tid);
+        atomicAdd(&s_count, 1);
+    }
+    __syncthreads();
+    const int first = s_first, pieces = s_count + 1;
+    if (pieces < 2 || (!by_row && first != (int)blockIdx.x + 1))
         return;
-    int pieces = 0;  // shares p, p + 1, .. that hold more of the row
-    for (int b = p; b < shares; b += kJoinThreads) {
-        const int q = b + (int)threadIdx.x;
-        pieces += __syncthreads_count(q < shares && place[q].x == here.x && place[q].y > 0);
-    }
-    const int d = threadIdx.x & 127, mt = blockIdx.y & 3;
-    const int quad = 2 * (blockIdx.y >> 2) + (threadIdx.x >> 7);
-    const int64_t step = (int64_t)2 * a.groups * C::PART;
-    // the first piece is its share's first segment if the share began with it
-    const float *first =
-        a.ws_part + (int64_t)(2 * ((p - 1) * a.groups + g) + !prev_same) * C::PART;
-    const float *rest = a.ws_part + (int64_t)2 * (p * a.groups + g) * C::PART;
-    const int at = (mt * N + 4 * quad) * 128 + 4 * d;
-    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-    #pragma unroll 8
-    for (int q = 0; q <= pieces; ++q) {
-        const float *f = q == 0 ? first : rest + (q - 1) * step;
-        const float4 v = *reinterpret_cast<const float4 *>(f + kLatent * N + 4 * quad);
-        top[0] = fmaxf(top[0], v.x);
-        top[1] = fmaxf(top[1], v.y);
-        top[2] = fmaxf(top[2], v.z);
-        top[3] = fmaxf(top[3], v.w);
-    }
-    #pragma unroll
-    for (int e = 0; e < 4; ++e)
-        top[e] = top[e] == -INFINITY ? 0.0f : top[e];
-    float acc[4] = {}, sum[4] = {};
-    #pragma unroll 8
-    for (int q = 0; q <= pieces; ++q) {
-        const float *f = q == 0 ? first : rest + (q - 1) * step;
-        const float4 v = *reinterpret_cast<const float4 *>(f + at);
-        const float4 m = *reinterpret_cast<const float4 *>(f + kLatent * N + 4 * quad);
-        const float4 l = *reinterpret_cast<const float4 *>(f + kLatent * N + N + 4 * quad);
-        const float vv[4] = {v.x, v.y, v.z, v.w}, mm[4] = {m.x, m.y, m.z, m.w};
-        const float ll[4] = {l.x, l.y, l.z, l.w};
-        #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float wt = ex2(mm[e] - top[e]);
-            acc[e] = fmaf(wt, vv[e], acc[e]);
-            sum[e] = fmaf(wt, ll[e], sum[e]);
+    // a share leaves its first segment at 2 (share, group), its last after it
+    const bool late = place[first - 1].x != row;
+    const auto piece = [&](int q) {
+        const int64_t at = 2 * ((int64_t)(first - 1 + q) * a.groups + g);
+        return a.ws_part + (at + (q == 0 && late)) * C::PART;
+    };
+    const Group group = group_of(a, g);
+    {
+        const int col = tid % N, r = tid / N;
+        float top = -INFINITY;
+        for (int q = r; q < pieces; q += kRuns) {
+            const float m = piece(q)[kLatent * N + col];
+            wt[q * N + col] = m;
+            top = fmaxf(top, m);
         }
+        run[r][col] = top;
+        __syncthreads();
+        #pragma unroll
+        for (int i = 0; i < kRuns; ++i)
+            top = fmaxf(top, run[i][col]);
+        top = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f;
+        for (int q = r; q < pieces; q += kRuns) {
+            const float w = ex2(wt[q * N + col] - top);
+            wt[q * N + col] = w;
+            sum = fmaf(w, piece(q)[kLatent * N + N + col], sum);
+        }
+        __syncthreads();
+        run[r][col] = sum;
+        __syncthreads();
+        if (r == 0) {
+            #pragma unroll
+            for (int i = 1; i < kRuns; ++i)
+                sum += run[i][col];
+            inv[col] = sum == 0.0f ? 0.0f : 1.0f / sum;
+            int j, h;
+            if (blockIdx.y == 0 && a.lse && column_place(a, group, col, &j, &h))
+                a.lse[((int64_t)row * a.next + j) * a.ld_lse + h] =
+                    sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+        }
+        __syncthreads();
     }
-    #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        int j, h;
-        if (!column_place(a, group, 4 * quad + e, &j, &h))
-            continue;
-        const int64_t r = (int64_t)here.x * a.next + j;
-        reinterpret_cast<__nv_bfloat16 *>(a.out)[r * a.ldo_row + h * a.ldo_head + 128 * mt + d] =
-            __float2bfloat16(sum[e] == 0.0f ? 0.0f : acc[e] / sum[e]);
-        if (a.lse && mt == 0 && d == 0)
-            a.lse[r * a.ld_lse + h] =
-                sum[e] == 0.0f ? -INFINITY : (top[e] + log2f(sum[e])) * kLn2;
+    const int d = tid & 127, team = tid >> 7;
+    const bool few = pieces <= kJoinFew;
+    const int last = (blockIdx.y + 1) * N / gridDim.y;
+    for (int s0 = blockIdx.y * N / gridDim.y; s0 < last; s0 += few ? 4 : 1) {
+        const int slice = s0 + (few ? team : 0), mt = slice & 3, quad = slice >> 2;
+        const int at = (mt * N + 4 * quad) * 128 + 4 * d;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (slice < last) {
+            #pragma unroll 4
+            for (int q = few ? 0 : team; q < pieces; q += few ? 1 : 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(piece(q) + at);
+                const float4 u = *reinterpret_cast<const float4 *>(wt + q * N + 4 * quad);
+                acc.x = fmaf(u.x, v.x, acc.x);
+                acc.y = fmaf(u.y, v.y, acc.y);
+                acc.z = fmaf(u.z, v.z, acc.z);
+                acc.w = fmaf(u.w, v.w, acc.w);
+            }
+        }
+        if (!few) {
+            if (team > 0)
+                part[team - 1][d] = acc;
+            __syncthreads();
+            if (team == 0) {
+                #pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    acc.x += part[i][d].x;
+                    acc.y += part[i][d].y;
+                    acc.z += part[i][d].z;
+                    acc.w += part[i][d].w;
+                }
+            }
+        }
+        if (slice < last && (few || team == 0)) {
+            const float y[4] = {acc.x, acc.y, acc.z, acc.w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                int j, h;
+                if (!column_place(a, group, 4 * quad + e, &j, &h))
+                    continue;
+                const int64_t r = (int64_t)row * a.next + j;
+                reinterpret_cast<__nv_bfloat16 *>(
+                    a.out)[r * a.ldo_row + h * a.ldo_head + 128 * mt + d] =
+                    __float2bfloat16(y[e] * inv[4 * quad + e]);
+            }
+        }
+        if (!few)
+            __syncthreads();  // part is written again
     }
 }
 
@@ -1105,8 +1164,13 @@ idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int shares, cud
     }
     cudaError_t e = launch_pdl(kern, dim3(a.groups, shares), dim3(kThreads), C::SMEM, s, tm, a);
     if (e == cudaSuccess && shares > 1)
-        e = launch_pdl(latent_join_kernel<N>, dim3(shares - 1, 4 * (N / 8), a.groups),
-                       dim3(kJoinThreads), 0, s, a);
+    {
+        // a few CTAs per SM over all rows that may be cut
+        const int rows = std::min(a.rows, shares - 1) * a.groups;
+        const int parts = std::min(N, std::max(2, 4 * sm_count() / rows));
+        e = launch_pdl(latent_join_kernel<N>, dim3(rows / a.groups, parts, a.groups),
+                       dim3(kJoinThreads), 0, s, a, shares);
+    }
     return launch_status(e);
 }
 
@@ -1151,7 +1215,8 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
     a.ws_place = ws;
     a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + place_bytes());
     // one CTA per SM, the same number for every group
-    const int shares = (int)std::min<int64_t>(sm_count() / a.groups, most);
+    const int shares =
+        (int)std::min<int64_t>(std::min(sm_count(), kMaxShares) / a.groups, most);
     CUtensorMap tm;
     // bytes of a head row, heads, rows; a stride over one element is free
     const uint64_t dims[3] = {2 * kLatTok, (uint64_t)a.H, (uint64_t)R};

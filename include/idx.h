@@ -643,6 +643,8 @@ size_t idx_latent_attention_workspace_size(int R, int H);
  *   lse     fp32 [Tq, ld_lse] (ld_lse >= H) or NULL, as idx_latent_attention.
  *           A query with no key gets zeros and -inf; rows of q outside every
  *           sequence are not written.
+ *   ws, ws_bytes  device scratch as for idx_latent_attention, of
+ *           idx_latent_prefill_workspace_size(Tq, H) bytes.
  * Every stride is a multiple of 8 elements and every pointer 16-byte
  * aligned.  Keys and values past a sequence's end (another sequence's) never
  * enter its results, whatever they hold; within a sequence a value that is
@@ -656,7 +658,10 @@ idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_he
                               const int32_t *cu_k, int B, int Tq, int Tk, int H, int d_nope,
                               int d_rope, int d_v, float scale, int causal, uint16_t *out,
                               int64_t ldo_row, int64_t ldo_head, float *lse, int64_t ld_lse,
-                              idx_stream_t stream);
+                              void *ws, size_t ws_bytes, idx_stream_t stream);
+
+/* Bytes of ws for Tq query rows of H heads. */
+size_t idx_latent_prefill_workspace_size(int Tq, int H);
 
 /* ------------------------------------------------------------------------
  * idx_get_device_status -- read and clear the sticky device status word of

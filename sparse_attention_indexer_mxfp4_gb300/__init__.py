@@ -28,6 +28,7 @@ from ._binding import (  # noqa: F401
     idx_topk_to_ragged_slots,
     latent_attention_workspace_size,
     latent_page_bytes,
+    latent_prefill_workspace_size,
     lib,
     library_path,
     version,

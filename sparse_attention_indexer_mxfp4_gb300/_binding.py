@@ -66,7 +66,7 @@ _SIGNATURES = {
     "idx_paged_latent_attention": [_P, _L, _L, _P, _L, _I, _I, _I, _P, _L, _P, _I, _I, _I, _I, _I,
                                    _I, _I, ctypes.c_float, _P, _L, _L, _P, _L, _P, _S, _P],
     "idx_latent_prefill": [_P, _L, _L, _P, _L, _L, _P, _L, _P, _L, _L, _P, _P, _I, _I, _I, _I, _I,
-                           _I, _I, ctypes.c_float, _I, _P, _L, _L, _P, _L, _P],
+                           _I, _I, ctypes.c_float, _I, _P, _L, _L, _P, _L, _P, _S, _P],
     "idx_get_device_status": [_P, ctypes.POINTER(ctypes.c_uint32)],
     "idx_debug_wait_expiry": [_I, ctypes.c_uint64, _P],
     "idx_row_ends": [_P, _I, _I, _I, _I, _P, _P],
@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
             L.idx_topk_workspace_size.restype = _S
             L.idx_latent_attention_workspace_size.argtypes = [_I, _I]
             L.idx_latent_attention_workspace_size.restype = _S
+            L.idx_latent_prefill_workspace_size.argtypes = [_I, _I]
+            L.idx_latent_prefill_workspace_size.restype = _S
             L.idx_paged_mqa_logits_workspace_size.argtypes = [_I, _I, _I, _I]
             L.idx_paged_mqa_logits_workspace_size.restype = _S
             _lib = L
@@ -708,10 +710,15 @@ def latent_attention_workspace_size(rows, heads) -> int:
     return int(lib().idx_latent_attention_workspace_size(rows, heads))
 
 
-def _latent_ws(workspace, rows, heads, device):
-    """The scratch of an absorbed attention call and its bytes."""
+def latent_prefill_workspace_size(rows, heads) -> int:
+    """Bytes of device scratch of the expanded attention."""
+    return int(lib().idx_latent_prefill_workspace_size(rows, heads))
+
+
+def _latent_ws(workspace, size, rows, heads, device):
+    """The scratch of an attention call and its bytes."""
     if workspace is True:
-        n = lib().idx_latent_attention_workspace_size(rows, heads)
+        n = size(rows, heads)
         return torch.empty(n, dtype=torch.uint8, device=device), n
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
@@ -731,7 +738,7 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
         raise ValueError(f"indptr must hold {R + 1} entries")
     device = q.device
     out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
-    ws, ws_bytes = _latent_ws(workspace, R, H, device)
+    ws, ws_bytes = _latent_ws(workspace, lib().idx_latent_attention_workspace_size, R, H, device)
     args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(slots),
             _ptr(indptr), slots.numel(), R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
             ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
@@ -767,7 +774,7 @@ def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, con
         raise ValueError(f"block_table must be [{B_}, blocks]")
     device = q.device
     out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
-    ws, ws_bytes = _latent_ws(workspace, R, H, device)
+    ws, ws_bytes = _latent_ws(workspace, lib().idx_latent_attention_workspace_size, R, H, device)
     args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(block_table),
             block_table.shape[1], _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len,
             H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws),
@@ -787,11 +794,13 @@ def idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context
     return call.keep[4], call.keep[5]
 
 
-def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None):
+def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                           workspace=True):
     """Expanded latent attention of ragged sequences.  q bf16 [Tq, H, 192]
     (128, then 64 rotated), k bf16 [Tk, H, 128], k_rope bf16 [Tk, 64], v bf16
     [Tk, H, 128], every outer stride free; cu_q, cu_k int32 [B + 1]; out bf16
-    [Tq, H, 128] and lse fp32 [Tq, H] as in prepare_latent_attention."""
+    [Tq, H, 128], lse fp32 [Tq, H] and workspace as in prepare_latent_attention
+    (the size is latent_prefill_workspace_size(Tq, H))."""
     (Tq, H, _), (ldq, ldqh, _) = _need_heads(q, 3, 192, "q")
     (Tk, Hk, _), (ldk, ldkh, _) = _need_heads(k, 3, 128, "k")
     (Tr, _), (ldr, _) = _need_heads(k_rope, 2, LATENT_ROPE, "k_rope")
@@ -803,17 +812,20 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
     B_ = cu_q.numel() - 1
     if cu_k.numel() != B_ + 1 or B_ < 0:
         raise ValueError("cu_q and cu_k must both hold B + 1 entries")
-    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, Tq, H, 128, q.device)
+    device = q.device
+    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, Tq, H, 128, device)
+    ws, ws_bytes = _latent_ws(workspace, lib().idx_latent_prefill_workspace_size, Tq, H, device)
     args = (_ptr(q), ldq, ldqh, _ptr(k), ldk, ldkh, _ptr(k_rope), ldr, _ptr(v), ldv, ldvh,
             _ptr(cu_q), _ptr(cu_k), B_, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal),
-            _ptr(out), ldo, ldoh, _ptr(lse), ldl)
-    return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse))
+            _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
+    return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws))
 
 
 def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
-                       stream=None):
+                       workspace=True, stream=None):
     """(out, lse) of the expanded attention of ragged sequences."""
-    call = prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse)
+    call = prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
+                                  workspace)
     call(stream)
     return call.keep[6], call.keep[7]
 

@@ -1,7 +1,7 @@
 // idx_latent_prefill.cu -- expanded latent attention of ragged sequences:
 // s = scale * (q[:128] . k + q[128:] . k_rope), out = softmax(s) . v.
 //
-// A CTA takes up to two tiles of 128 queries of one head and walks the keys
+// A block is up to two tiles of 128 queries of one head; a CTA walks the keys
 // they see, 128 at a time, with a running maximum and sum:
 //
 //     S [128 queries x 128 keys] = Q [128 x 192] . K^T   (12 MMAs, 128 x 128 x 16)
@@ -20,8 +20,15 @@
 // (32-bit sums lose nothing by that), so rescaling O is rare after a row's
 // first tile.
 //
+// Work is the flat list of (head, block, key tile); every CTA (one per SM)
+// takes an equal contiguous share of it, so causal blocks of any length fill
+// the GPU evenly and few queries on many keys are spread over it.  The next
+// block's queries and keys come in while the last one's epilogue runs.  A block
+// that shares cut leaves unnormalised sums in scratch for a second kernel.
+//
 // Warps: 0-3 and 4-7 softmax of the two tiles, a thread a query; 8 issues TMA;
 // 9 issues the products.
+#include <algorithm>
 #include <atomic>
 #include <cuda_bf16.h>
 
@@ -37,12 +44,19 @@ constexpr int kPiece = kTile * 128;             // bytes of 64 elements of a til
 constexpr int kQPieces = kQk / 64, kVPieces = kV / 64, kPieces = kQPieces + kVPieces;
 constexpr int kRing = 8;
 constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // whole warpgroups: two warps only help to start
+// Registers of a thread: as launched, then of the two softmax warpgroups (a
+// row of scores each thread) and of the third.
+constexpr int kRegs = 168, kRegsSoft = 216, kRegsRest = 72;
+static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegs && kRegs * kThreads <= 65536,
+              "the warpgroups' registers come from the launch's");
 constexpr int kOffRing = 2 * kQPieces * kPiece;
 constexpr int kOffBar = kOffRing + kRing * kPiece;
-constexpr int kBars = 2 * kRing + 9;
-constexpr int kOffMisc = kOffBar + 8 * kBars;  // tmem base, abort flag
-constexpr int kSmem = kOffMisc + 16 + 1024;    // the base is aligned to 1024 in the kernel
+constexpr int kBars = 2 * kRing + 12;
+constexpr int kOffMisc = kOffBar + 8 * kBars;  // tmem base, abort flag, the share's place
+constexpr int kOffCu = kOffMisc + 64;          // the sequences' bounds, where they fit
+constexpr int kMaxCu = 128;
+constexpr int kSmem = kOffCu + 8 * (kMaxCu + 1) + 1024;  // the base is aligned to 1024
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 constexpr uint32_t kColS = 0, kColO = 256;     // tensor memory columns, 128 a query tile
 constexpr float kLazy = 40.0f;                 // a score may exceed its running maximum by 2^40
@@ -51,70 +65,145 @@ constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 struct PrefillArgs {
     const int32_t *cu_q, *cu_k;
     int B, Tq, Tk, H;
-    int tiles;  // query tiles of a CTA (1 or 2)
     float scale_log2;
     int causal;
     __nv_bfloat16 *out;
     int64_t ldo_row, ldo_head;
     float *lse;
     int64_t ld_lse;
+    int4 *ws_place;  // a share's first head, sequence, block, tile
+    float *ws_part;  // two segments a share: for each query tile O, maxima, sums
     unsigned int *status;
 };
 
-// A CTA's queries: rows q0 .. of a sequence of nq queries and nk keys.
+constexpr int kRows = 2 * kTile;                        // queries of a block
+constexpr int kPartTile = kTile * kV + 2 * kTile;       // floats of a query tile's partial result
+constexpr int kMaxShares = 152;
+
+// A block: queries kRows i .. of sequence b, for one head.
 struct Block {
-    int seq_q, seq_k, nq, nk, q0;
+    int head, b, i;
+    int seq_q, nq, seq_k, nk;
 };
 
-// Finds block t of all sequences' blocks of `rows` queries, the last of a
-// sequence first (causal: they see the most keys).  One warp; false past the end.
-__device__ __forceinline__ bool find_block(const PrefillArgs &a, int t, int rows, Block &k)
+// The sequence's rows (bounds outside the tensors are clamped).
+__device__ __forceinline__ void block_seq(const PrefillArgs &a, const int32_t *cq,
+                                          const int32_t *ck, Block &k)
 {
-    const int lane = lane_id();
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-        const int b = b0 + lane;
-        int lo = 0, n = 0;
-        if (b < a.B) {
-            lo = min(max(a.cu_q[b], 0), a.Tq);
-            n = max(0, min(a.cu_q[b + 1], a.Tq) - lo);
-        }
-        const int blocks = (n + rows - 1) / rows;
-        int upto = blocks;
-        #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
-            upto += lane >= o ? v : 0;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, upto > t);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            const int first = __shfl_sync(0xffffffffu, upto - blocks, src);
-            const int count = __shfl_sync(0xffffffffu, blocks, src);
-            k.seq_q = __shfl_sync(0xffffffffu, lo, src);
-            k.nq = __shfl_sync(0xffffffffu, n, src);
-            k.q0 = (count - 1 - (t - first)) * rows;
-            k.seq_k = min(max(a.cu_k[b0 + src], 0), a.Tk);
-            k.nk = max(0, min(a.cu_k[b0 + src + 1], a.Tk) - k.seq_k);
-            return true;
-        }
-        t -= __shfl_sync(0xffffffffu, upto, 31);
-    }
-    return false;
+    k.seq_q = min(max(cq[k.b], 0), a.Tq);
+    k.nq = max(0, min(cq[k.b + 1], a.Tq) - k.seq_q);
+    k.seq_k = min(max(ck[k.b], 0), a.Tk);
+    k.nk = max(0, min(ck[k.b + 1], a.Tk) - k.seq_k);
 }
 
-// Keys that query row i of the sequence sees.
-__device__ __forceinline__ int keys_seen(const PrefillArgs &a, const Block &k, int i)
+// The next block: of the sequence, of the next one that has queries, of the
+// next head.  Only called when there is one.
+__device__ __forceinline__ void block_next(const PrefillArgs &a, const int32_t *cq,
+                                           const int32_t *ck, Block &k)
 {
-    return a.causal ? min(k.nk, max(0, i + k.nk - k.nq + 1)) : k.nk;
+    ++k.i;
+    while (k.i * kRows >= k.nq) {
+        k.i = 0;
+        if (++k.b == a.B) {
+            k.b = 0;
+            ++k.head;
+        }
+        block_seq(a, cq, ck, k);
+    }
+}
+
+// Keys that query row r of the sequence sees.
+__device__ __forceinline__ int keys_seen(const PrefillArgs &a, const Block &k, int r)
+{
+    return a.causal ? min(k.nk, max(0, r + k.nk - k.nq + 1)) : k.nk;
 }
 
 // Key tiles of query tile q of the block (0: it has no queries, or they no keys).
 __device__ __forceinline__ int key_tiles(const PrefillArgs &a, const Block &k, int q)
 {
-    const int first = k.q0 + q * kTile, last = min(first + kTile, k.nq) - 1;
-    if (q >= a.tiles || last < first)
+    const int first = k.i * kRows + q * kTile, last = min(first + kTile, k.nq) - 1;
+    return last < first ? 0 : (keys_seen(a, k, last) + kTile - 1) / kTile;
+}
+
+// Tiles of the first n blocks of a sequence, its last not among them; a block
+// counts at least one, its outputs are written (causal: block i sees kRows / kTile (i + 1) + ceil((nk - nq) /
+// kTile) tiles).
+__device__ __forceinline__ int tiles_before(const PrefillArgs &a, int nq, int nk, int n)
+{
+    if (!a.causal)
+        return n * max(1, (nk + kTile - 1) / kTile);
+    constexpr int rho = kRows / kTile;
+    const int d = nk - nq;
+    const int delta = d >= 0 ? (d + kTile - 1) / kTile : -(-d / kTile);
+    const int z = min(n, max(0, -delta / rho));  // blocks that see nothing
+    return z + rho * (n * (n + 1) - z * (z + 1)) / 2 + delta * (n - z);
+}
+
+// All of a sequence's tiles.
+__device__ __forceinline__ int tiles_of_seq(const PrefillArgs &a, int nq, int nk)
+{
+    if (nq <= 0)
         return 0;
-    return (keys_seen(a, k, last) + kTile - 1) / kTile;
+    const int blocks = (nq + kRows - 1) / kRows;
+    return tiles_before(a, nq, nk, blocks - 1) + max(1, (nk + kTile - 1) / kTile);
+}
+
+// The walk of a share: segments of a block's tiles.
+struct Walk {
+    Block k;
+    int t, left;
+};
+
+struct Seg {
+    Block k;
+    int t0, t1, tiles;
+    int nt[2];  // unrolled uses only
+};
+
+__device__ __forceinline__ bool next_seg(const PrefillArgs &a, const int32_t *cq,
+                                         const int32_t *ck, Walk &w, Seg &s)
+{
+    if (w.left <= 0)
+        return false;
+    if (w.t < 0) {
+        block_next(a, cq, ck, w.k);
+        w.t = 0;
+    }
+    s.k = w.k;
+    s.t0 = w.t;
+    s.nt[0] = key_tiles(a, w.k, 0);
+    s.nt[1] = key_tiles(a, w.k, 1);
+    s.tiles = max(1, max(s.nt[0], s.nt[1]));
+    s.t1 = min(s.tiles, w.t + w.left);
+    w.left -= s.t1 - s.t0;
+    w.t = s.t1 < s.tiles ? s.t1 : -1;
+    return true;
+}
+
+// Two bf16 of scaled sums.
+__device__ __forceinline__ uint32_t pack2(uint32_t a, uint32_t b, float f)
+{
+    const __nv_bfloat162 v =
+        __floats2bfloat162_rn(__uint_as_float(a) * f, __uint_as_float(b) * f);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// 4 x 4 words turned over among the four lanes of a quad: word x of lane c
+// becomes word c of lane x.
+__device__ __forceinline__ void turn_quad(uint32_t (&w)[4], int c)
+{
+    #pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, c & 1 ? w[e] : w[e + 1], 1);
+        w[e] = c & 1 ? got : w[e];
+        w[e + 1] = c & 1 ? w[e + 1] : got;
+    }
+    #pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, c & 2 ? w[e] : w[e + 2], 2);
+        w[e] = c & 2 ? got : w[e];
+        w[e + 2] = c & 2 ? w[e + 2] : got;
+    }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -129,12 +218,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
     uint64_t *full = bar, *empty = bar + kRing;
     uint64_t *s_full = bar + 2 * kRing, *p_full = s_full + 2, *pv_done = s_full + 4;
-    uint64_t *q_full = s_full + 6, *tail = s_full + 7, *drain = s_full + 8;
-    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + kOffMisc);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(misc + 1);
+    uint64_t *q_full = s_full + 6, *q_free = s_full + 8, *tail = s_full + 10, *drain = s_full + 11;
+    int *misc = reinterpret_cast<int *>(smem + kOffMisc);
+    volatile int *abort_flag = misc + 1;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-    const int head = blockIdx.y;
 
     if (tid == 0) {
         for (int i = 0; i < kRing; ++i) {
@@ -145,235 +233,368 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_free[i], 1);
         }
-        mbar_init(q_full, 1);
         mbar_init(tail, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == kWarpMma) {
-        tmem_alloc(misc, 512);
+        tmem_alloc(reinterpret_cast<uint32_t *>(misc), 512);
         tmem_relinquish();
     }
     pdl_wait();
     pdl_launch_dependents();
-    Block k;
-    const bool some = find_block(a, blockIdx.x, a.tiles * kTile, k);
-    // key tiles of the two query tiles
-    const int nt0 = some ? key_tiles(a, k, 0) : 0, nt1 = some ? key_tiles(a, k, 1) : 0;
-    const int most = max(nt0, nt1);
+
+    // ---- this CTA's share: the tiles of a head are those of all sequences
+    const int32_t *cq = a.cu_q, *ck = a.cu_k;
+    if (a.B <= kMaxCu) {
+        int32_t *cu = reinterpret_cast<int32_t *>(smem + kOffCu);
+        for (int i = tid; i <= a.B; i += kThreads) {
+            cu[i] = a.cu_q[i];
+            cu[kMaxCu + 1 + i] = a.cu_k[i];
+        }
+        cq = cu;
+        ck = cu + kMaxCu + 1;
+    }
+    __syncthreads();
+    int *wsum = misc + 4;
+    const auto seq_tiles = [&](int b) {
+        Block k;
+        k.b = b;
+        if (b >= a.B)
+            return 0;
+        block_seq(a, cq, ck, k);
+        return tiles_of_seq(a, k.nq, k.nk);
+    };
+    int head_tiles = 0, mine, before;
+    const auto scan = [&](int b0) {  // of sequences b0 + thread; adds up head_tiles
+        mine = seq_tiles(b0 + tid);
+        int upto = mine;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? v : 0;
+        }
+        __syncthreads();
+        if (lane == 31)
+            wsum[warp] = upto;
+        __syncthreads();
+        before = head_tiles + upto - mine;
+        #pragma unroll
+        for (int i = 0; i < kThreads / 32; ++i) {
+            before += i < warp ? wsum[i] : 0;
+            head_tiles += wsum[i];
+        }
+    };
+    for (int b0 = 0; b0 < a.B; b0 += kThreads)
+        scan(b0);
+    const int total = head_tiles * a.H;
+    // two tiles a share at least: a cut costs about as much as a tile
+    const int p = blockIdx.x, shares = max(1, min((int)gridDim.x, total / 2));
+    const int each = total / shares, more = total - each * shares;
+    const int u0 = p * each + min(p, more);
+    Walk w;
+    w.left = p < shares && total > 0 ? each + (p < more) : 0;
+    w.k.head = w.left > 0 ? u0 / head_tiles : 0;
+    const int at = u0 - w.k.head * head_tiles;
+    if (a.B > kThreads) {
+        // many sequences: the chunk that holds the place, once more
+        head_tiles = 0;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            scan(b0);
+            if (w.left > 0 && at >= before && at < before + mine) {
+                misc[2] = b0 + tid;
+                misc[3] = at - before;
+            }
+        }
+    } else if (w.left > 0 && at >= before && at < before + mine) {
+        misc[2] = tid;
+        misc[3] = at - before;
+    }
     __syncthreads();
     tc_fence_after();
     // one value for the warp, as the compiler sees it too
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
+    w.t = 0;
+    if (w.left > 0) {
+        w.k.b = __shfl_sync(0xffffffffu, misc[2], 0);
+        int rest = __shfl_sync(0xffffffffu, misc[3], 0);
+        block_seq(a, cq, ck, w.k);
+        int lo = 0, hi = (w.k.nq + kRows - 1) / kRows - 1;  // the last i with tiles_before <= rest
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (tiles_before(a, w.k.nq, w.k.nk, mid) <= rest)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        w.k.i = lo;
+        w.t = rest - tiles_before(a, w.k.nq, w.k.nk, lo);
+    }
+    if (tid == 0)
+        a.ws_place[p] = w.left > 0 ? make_int4(w.k.head, w.k.b, w.k.i, w.t) : make_int4(-1, 0, 0, 0);
+    Seg s;
 
-    if (!some) {
-        // nothing here: only the tensor memory to give back
-    } else if (warp < kWarpLoad) {
+    if (warp < kWarpLoad) {
         // ------------------------------------------------ softmax, epilogue
+        regs_take<kRegsSoft>();
         const int q = warp >> 2;
-        const int row = k.q0 + q * kTile + (tid & 127);
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lanes + kColS + q * 128, col_o = tmem + lanes + kColO + q * 128;
         const float sl = a.scale_log2;
-        // rows past the sequence's queries take part with no key
-        const int seen = row < k.nq ? keys_seen(a, k, row) : 0;
-        const int seen_first = __shfl_sync(0xffffffffu, seen, 0);  // the warp's fewest, if it has them
-        const bool whole_warp = __all_sync(0xffffffffu, row < k.nq);
-        const int nt = q ? nt1 : nt0;
-        float m = -INFINITY, l = 0.0f;
-        for (int j = 0; j < nt; ++j) {
-            // after an abort the waits return at once and the loop runs out
-            (void)mbar_wait(&s_full[q], j & 1, abort_flag, a.status);
-            __syncwarp();
-            tc_fence_after();
-            uint32_t r[4][32];
-            #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                tmem_ld_32x32b_x32(col_s + 32 * c, r[c]);
-            tmem_ld_wait();
-            if (!whole_warp || (j + 1) * kTile > seen_first) {
-                const int lim = seen - j * kTile;
+        int i = 0;  // tiles of this query tile so far
+        for (int seg = 0; next_seg(a, cq, ck, w, s); ++seg) {
+            const int row = s.k.i * kRows + q * kTile + (tid & 127);
+            // rows past the sequence's queries take part with no key
+            const int seen = row < s.k.nq ? keys_seen(a, s.k, row) : 0;
+            // the warp's fewest, if it has all its rows
+            const int seen_first = __shfl_sync(0xffffffffu, seen, 0);
+            const bool whole_warp = __all_sync(0xffffffffu, row < s.k.nq);
+            const int t1 = min(s.t1, q ? s.nt[1] : s.nt[0]);
+            float m = -INFINITY, l = 0.0f;
+            for (int j = s.t0; j < t1; ++j, ++i) {
+                // after an abort the waits return at once and the loop runs out
+                (void)mbar_wait_here(&s_full[q], i & 1, abort_flag, a.status);
+                __syncwarp();
+                tc_fence_after();
+                uint32_t r[4][32];
+                #pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    tmem_ld_32x32b_x32(col_s + 32 * c, r[c]);
+                tmem_ld_wait();
+                if (!whole_warp || (j + 1) * kTile > seen_first) {
+                    const int lim = seen - j * kTile;
+                    #pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        #pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            r[c][e] = 32 * c + e < lim ? r[c][e] : 0xff800000u;
+                    }
+                }
+                float mx[4];
                 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    mx[c] = __uint_as_float(r[c][0]);
                     #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        r[c][e] = 32 * c + e < lim ? r[c][e] : 0xff800000u;
+                    for (int e = 1; e < 32; ++e)
+                        mx[c] = fmaxf(mx[c], __uint_as_float(r[c][e]));
                 }
-            }
-            float mx[4];
-            #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                mx[c] = __uint_as_float(r[c][0]);
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+                // -inf - -inf (no key so far) is no reason to raise it
+                if (__any_sync(0xffffffffu, top - m > kLazy)) {
+                    const float nm = fmaxf(m, top);
+                    const float al = nm == m ? 1.0f : ex2(m - nm);
+                    m = nm;
+                    l *= al;
+                    if (j > s.t0) {
+                        (void)mbar_wait_here(&pv_done[q], (i - 1) & 1, abort_flag, a.status);
+                        __syncwarp();
+                        tc_fence_after();
+                        #pragma unroll 1
+                        for (int c = 0; c < 128; c += 16) {
+                            uint32_t o[16];
+                            tmem_ld_32x32b_x16(col_o + c, o);
+                            tmem_ld_wait();
+                            #pragma unroll
+                            for (int e = 0; e < 16; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
+                            tmem_st_32x32b_x16(col_o + c, o);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float nm = m == -INFINITY ? 0.0f : -m;
+                float sum[4] = {};
                 #pragma unroll
-                for (int e = 1; e < 32; ++e)
-                    mx[c] = fmaxf(mx[c], __uint_as_float(r[c][e]));
+                for (int c = 0; c < 2; ++c) {
+                    // weights as bf16 (half a step of 2^-8 each), two a column
+                    uint32_t v[32];
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int at2 = 2 * e & 31;
+                        const float x = ex2(fmaf(__uint_as_float(r[2 * c + (e >> 4)][at2]), sl, nm));
+                        const float y =
+                            ex2(fmaf(__uint_as_float(r[2 * c + (e >> 4)][at2 + 1]), sl, nm));
+                        sum[e & 3] += x + y;
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+                        v[e] = *reinterpret_cast<const uint32_t *>(&b2);
+                    }
+                    tmem_st_32x32b_x32(col_s + 32 * c, v);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&p_full[q]);
             }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-            // -inf - -inf (no key so far) is no reason to raise it
-            if (__any_sync(0xffffffffu, top - m > kLazy)) {
-                const float nm = fmaxf(m, top);
-                const float al = nm == m ? 1.0f : ex2(m - nm);
-                m = nm;
-                l *= al;
-                if (j > 0) {
-                    (void)mbar_wait(&pv_done[q], (j - 1) & 1, abort_flag, a.status);
-                    __syncwarp();
-                    tc_fence_after();
+            // ---- the segment's sums
+            const bool some = t1 > s.t0;
+            if (some) {
+                (void)mbar_wait_here(&pv_done[q], (i - 1) & 1, abort_flag, a.status);
+                __syncwarp();
+                tc_fence_after();
+            }
+            if (s.t0 > 0 || s.t1 < s.tiles) {
+                // a part of the block: scratch, rows side by side
+                float *part = a.ws_part + ((int64_t)(2 * p + (seg > 0)) * 2 + q) * kPartTile;
+                const int r4 = 4 * (tid & 127);
+                if (some) {
                     #pragma unroll 1
-                    for (int c = 0; c < 128; c += 16) {
-                        uint32_t o[16];
-                        tmem_ld_32x32b_x16(col_o + c, o);
+                    for (int c = 0; c < 128; c += 32) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(col_o + c, o);
                         tmem_ld_wait();
                         #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * al);
-                        tmem_st_32x32b_x16(col_o + c, o);
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4 *>(part + (c + e) * kTile + r4) =
+                                make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
-                    tmem_st_wait();
+                }
+                part[kTile * kV + (tid & 127)] = m;
+                part[kTile * kV + kTile + (tid & 127)] = l;
+            } else if (__any_sync(0xffffffffu, row < s.k.nq)) {
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (a.lse && row < s.k.nq)
+                    a.lse[(int64_t)(s.k.seq_q + row) * a.ld_lse + s.k.head] =
+                        l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2;
+                // rows g, g + 8 of each half warp's sixteen; a quad of lanes
+                // holds 64 contiguous bytes of each after turning over
+                const int g = lane >> 2, c4 = lane & 3;
+                __nv_bfloat16 *to = a.out + (int64_t)s.k.seq_q * a.ldo_row +
+                                    s.k.head * a.ldo_head + 8 * c4;
+                const int row0 = row - lane;
+                #pragma unroll 1
+                for (int hc = 0; hc < 4; ++hc) {
+                    const int half = hc >> 1, c0 = 64 * (hc & 1);
+                    uint32_t o[32];
+                    #pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = 0;
+                    if (some) {
+                        tmem_ld_16x256b<8>(col_o + ((uint32_t)(16 * half) << 16) + c0, o);
+                        tmem_ld_wait();
+                    }
+                    #pragma unroll
+                    for (int up = 0; up < 2; ++up) {
+                        const int r = row0 + 16 * half + 8 * up + g;
+                        const float f = __shfl_sync(0xffffffffu, inv, 16 * half + 8 * up + g);
+                        #pragma unroll
+                        for (int x = 0; x < 8; x += 4) {
+                            uint32_t v[4];
+                            #pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                v[e] = pack2(o[4 * (x + e) + 2 * up], o[4 * (x + e) + 2 * up + 1], f);
+                            turn_quad(v, c4);
+                            if (r < s.k.nq)
+                                *reinterpret_cast<uint4 *>(to + (int64_t)r * a.ldo_row + c0 +
+                                                           8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
+                        }
+                    }
                 }
             }
-            const float nm = m == -INFINITY ? 0.0f : -m;
-            float sum[4] = {};
-            #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                // weights as bf16 (half a step of 2^-8 each), two a column
-                uint32_t w[32];
-                #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int at = 2 * e & 31;
-                    const float x = ex2(fmaf(__uint_as_float(r[2 * c + (e >> 4)][at]), sl, nm));
-                    const float y = ex2(fmaf(__uint_as_float(r[2 * c + (e >> 4)][at + 1]), sl, nm));
-                    sum[e & 3] += x + y;
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-                    w[e] = *reinterpret_cast<const uint32_t *>(&v);
-                }
-                tmem_st_32x32b_x32(col_s + 32 * c, w);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tmem_st_wait();
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&p_full[q]);
         }
-        if (nt > 0) {
-            (void)mbar_wait(&pv_done[q], (nt - 1) & 1, abort_flag, a.status);
-            __syncwarp();
-            tc_fence_after();
-        }
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const bool mine = q < a.tiles && row < k.nq;
-        __nv_bfloat16 *to = a.out + (int64_t)(k.seq_q + row) * a.ldo_row + head * a.ldo_head;
-        #pragma unroll 1
-        for (int c = 0; c < 128; c += 16) {
-            uint32_t o[16];
-            if (nt > 0) {
-                tmem_ld_32x32b_x16(col_o + c, o);
-                tmem_ld_wait();
-            } else {
-                #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    o[e] = 0;
-            }
-            uint32_t w[8];
-            #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(o[2 * e]) * inv,
-                                                               __uint_as_float(o[2 * e + 1]) * inv);
-                w[e] = *reinterpret_cast<const uint32_t *>(&v);
-            }
-            if (mine) {
-                *reinterpret_cast<uint4 *>(to + c) = make_uint4(w[0], w[1], w[2], w[3]);
-                *reinterpret_cast<uint4 *>(to + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-        }
-        if (mine && a.lse)
-            a.lse[(int64_t)(k.seq_q + row) * a.ld_lse + head] =
-                l == 0.0f ? -INFINITY : ((m == -INFINITY ? 0.0f : m) + log2f(l)) * kLn2;
-        tc_fence_before();
-    } else if (warp == kWarpLoad) {
+    } else if (regs_give<kRegsRest>(), warp == kWarpLoad) {
         // ------------------------------------------------------------- TMA
         const bool one = elect_one();
-        int n = 0;           // pieces issued
-        bool q_flying = false, ok = most > 0;
-        if (ok && one) {
-            mbar_arrive_expect_tx(q_full, (nt1 > 0 ? 2 : 1) * kQPieces * kPiece);
-            #pragma unroll 1
-            for (int q = 0; q < (nt1 > 0 ? 2 : 1); ++q) {
-                #pragma unroll 1
-                for (int c = 0; c < kQPieces; ++c)
-                    tma_load_3d(smem + (q * kQPieces + c) * kPiece, &tm_q, q_full, 128 * c, head,
-                                k.seq_q + k.q0 + q * kTile);
-            }
-        }
-        q_flying = ok;
-        bool tail_flying = false;
-        for (int j = 0; ok && j < most; ++j) {
-            const int t0 = k.seq_k + j * kTile, rem = k.nk - j * kTile;
-            #pragma unroll 1
-            for (int c = 0; c < kPieces; ++c, ++n) {
-                const int slot = n & (kRing - 1);
-                if (n >= kRing) {
-                    ok = mbar_wait(&empty[slot], ((n >> 3) - 1) & 1, abort_flag, a.status);
-                    if (!ok)
-                        break;
-                }
+        int n = 0, tails = 0;     // pieces issued, tiles cut off at a sequence's end
+        int loads[2] = {0, 0};    // of each query tile
+        bool ok = true, tail_flying = false;
+        while (ok && next_seg(a, cq, ck, w, s)) {
+            #pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (!ok || s.nt[q] <= s.t0)
+                    continue;
+                // the last segment's products have read the queries before
+                if (loads[q] > 0)
+                    ok = mbar_wait_here(&q_free[q], (loads[q] - 1) & 1, abort_flag, a.status);
+                if (!ok)
+                    continue;
                 __syncwarp();
-                uint8_t *to = smem + kOffRing + slot * kPiece;
-                const bool cut = c >= kQPieces && rem < kTile;  // values past the sequence
                 if (one) {
-                    uint64_t *b = cut ? tail : &full[slot];
-                    mbar_arrive_expect_tx(b, kPiece);
-                    if (c < 2)
-                        tma_load_3d(to, &tm_k, b, 128 * c, head, t0);
-                    else if (c == 2)
-                        tma_load_2d(to, &tm_r, b, 0, t0);
-                    else
-                        tma_load_3d(to, &tm_v, b, 128 * (c - kQPieces), head, t0);
+                    mbar_arrive_expect_tx(&q_full[q], kQPieces * kPiece);
+                    #pragma unroll 1
+                    for (int c = 0; c < kQPieces; ++c)
+                        tma_load_3d(smem + (q * kQPieces + c) * kPiece, &tm_q, &q_full[q], 128 * c,
+                                    s.k.head, s.k.seq_q + s.k.i * kRows + q * kTile);
                 }
-                __syncwarp();
-                if (cut) {
-                    // a weight of zero does not hide what is not finite:
-                    // another sequence's values become zeros here
-                    tail_flying = true;
-                    ok = mbar_wait(tail, c - kQPieces, abort_flag, a.status);
-                    if (!ok)
-                        break;
-                    tail_flying = false;
-                    for (int e = rem * 8 + lane; e < kTile * 8; e += 32)
-                        st_shared_v4(smem_u32(to) + 16 * e, 0, 0, 0, 0);
-                    fence_proxy_async_smem();
+                ++loads[q];
+            }
+            const int most = min(s.t1, max(s.nt[0], s.nt[1]));
+            for (int j = s.t0; ok && j < most; ++j) {
+                const int t0 = s.k.seq_k + j * kTile, rem = s.k.nk - j * kTile;
+                #pragma unroll 1
+                for (int c = 0; c < kPieces; ++c, ++n) {
+                    const int slot = n & (kRing - 1);
+                    if (n >= kRing) {
+                        ok = mbar_wait_here(&empty[slot], ((n >> 3) - 1) & 1, abort_flag, a.status);
+                        if (!ok)
+                            break;
+                    }
                     __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&full[slot]);
+                    uint8_t *to = smem + kOffRing + slot * kPiece;
+                    const bool cut = c >= kQPieces && rem < kTile;  // values past the sequence
+                    if (one) {
+                        uint64_t *b = cut ? tail : &full[slot];
+                        mbar_arrive_expect_tx(b, kPiece);
+                        if (c < 2)
+                            tma_load_3d(to, &tm_k, b, 128 * c, s.k.head, t0);
+                        else if (c == 2)
+                            tma_load_2d(to, &tm_r, b, 0, t0);
+                        else
+                            tma_load_3d(to, &tm_v, b, 128 * (c - kQPieces), s.k.head, t0);
+                    }
+                    __syncwarp();
+                    if (cut) {
+                        // a weight of zero does not hide what is not finite:
+                        // another sequence's values become zeros here
+                        tail_flying = true;
+                        ok = mbar_wait_here(tail, tails & 1, abort_flag, a.status);
+                        if (!ok)
+                            break;
+                        tail_flying = false;
+                        ++tails;
+                        for (int e = rem * 8 + lane; e < kTile * 8; e += 32)
+                            st_shared_v4(smem_u32(to) + 16 * e, 0, 0, 0, 0);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&full[slot]);
+                    }
                 }
             }
         }
         if (*abort_flag) {
             // the copies in flight land before the CTA leaves
-            if (q_flying)
-                (void)mbar_wait_drain(q_full, 0);
+            #pragma unroll
+            for (int q = 0; q < 2; ++q)
+                if (loads[q] > 0)
+                    (void)mbar_drain_here(&q_full[q], (loads[q] - 1) & 1);
             if (tail_flying)
-                (void)mbar_wait_drain(tail, 0);
+                (void)mbar_drain_here(tail, tails & 1);
             for (int i = n > kRing ? n - kRing : 0; i < n; ++i)
-                (void)mbar_wait_drain(&full[i & (kRing - 1)], (i >> 3) & 1);
+                (void)mbar_drain_here(&full[i & (kRing - 1)], (i >> 3) & 1);
         }
-    } else {
+    } else if (warp == kWarpMma) {
         // ------------------------------------------------------------ MMAs
-        const bool one = elect_one();
+        const uint32_t one = elect_one();
         const uint32_t id_s = idesc_bf16(kTile, kTile, false, false);
         const uint32_t id_v = idesc_bf16(kTile, 64, false, true);
-        bool ok = most > 0 && mbar_wait(q_full, 0, abort_flag, a.status);
-        // S of query tile q and key tile j; the last query tile frees the keys
-        const auto scores = [&](int q, int j) {
-            const bool last = q == 1 || nt1 <= j;
+        int n0 = 0;            // ring piece of the segment's first tile
+        int fills = 0;         // segments whose queries came, two bits a query tile
+        int done0 = 0, done1 = 0;  // tiles of each query tile before the segment
+        // S of query tile q and key tile j (the segment's k-th); the last query
+        // tile of a key tile frees its pieces
+        const auto scores = [&](int q, int k, bool last, bool end) {
             const uint32_t qd = desc_lo(sbase + q * kQPieces * kPiece);
             #pragma unroll
             for (int c = 0; c < kQPieces; ++c) {
-                const int n = j * kPieces + c, slot = n & (kRing - 1);
-                if (!mbar_wait(&full[slot], (n >> 3) & 1, abort_flag, a.status))
+                const int n = n0 + k * kPieces + c, slot = n & (kRing - 1);
+                if (!mbar_wait_here(&full[slot], (n >> 3) & 1, abort_flag, a.status))
                     return false;
                 __syncwarp();
                 tc_fence_after();
@@ -385,16 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit_if(&empty[slot], one && last);
             }
             mma_commit_if(&s_full[q], one);
+            mma_commit_if(&q_free[q], one && end);
             return true;
         };
-        const auto values = [&](int q, int j) {
-            const bool last = q == 1 || nt1 <= j;
-            if (!mbar_wait(&p_full[q], j & 1, abort_flag, a.status))
+        const auto values = [&](int q, int k, int done, bool last) {
+            if (!mbar_wait_here(&p_full[q], (done + k) & 1, abort_flag, a.status))
                 return false;
             #pragma unroll
             for (int c = 0; c < kVPieces; ++c) {
-                const int n = j * kPieces + kQPieces + c, slot = n & (kRing - 1);
-                if (!mbar_wait(&full[slot], (n >> 3) & 1, abort_flag, a.status))
+                const int n = n0 + k * kPieces + kQPieces + c, slot = n & (kRing - 1);
+                if (!mbar_wait_here(&full[slot], (n >> 3) & 1, abort_flag, a.status))
                     return false;
                 __syncwarp();
                 tc_fence_after();
@@ -402,31 +623,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     mma_f16_ts(tmem + kColO + q * 128 + 64 * c, tmem + kColS + q * 128 + 8 * e,
-                               vd + e * (2048 >> 4), kDescHiSw128, id_v, j + e > 0 ? 1u : 0u, one);
+                               vd + e * (2048 >> 4), kDescHiSw128, id_v, k + e > 0 ? 1u : 0u, one);
                 mma_commit_if(&empty[slot], one && last);
             }
             mma_commit_if(&pv_done[q], one);
             return true;
         };
-        if (ok && nt0 > 0)
-            ok = scores(0, 0);
-        if (ok && nt1 > 0)
-            ok = scores(1, 0);
-        for (int j = 0; ok && j < most; ++j) {
+        bool ok = true;
+        while (ok && next_seg(a, cq, ck, w, s)) {
+            // tiles of the segment that each query tile takes
+            const int c0 = max(0, min(s.t1, s.nt[0]) - s.t0);
+            const int c1 = max(0, min(s.t1, s.nt[1]) - s.t0);
+            const int most = max(c0, c1);
             #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                const int nt = q ? nt1 : nt0;
-                if (ok && j < nt)
-                    ok = values(q, j);
-                if (ok && j + 1 < nt)
-                    ok = scores(q, j + 1);
+                const int cnt = q ? c1 : c0;
+                if (!ok || cnt == 0)
+                    continue;
+                ok = mbar_wait_here(&q_full[q], (fills >> q) & 1, abort_flag, a.status);
+                fills ^= 1 << q;
+                if (ok)
+                    ok = scores(q, 0, q == 1 || c1 <= 0, cnt == 1);
             }
+            for (int k = 0; ok && k < most; ++k) {
+                #pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int cnt = q ? c1 : c0;
+                    if (ok && k < cnt)
+                        ok = values(q, k, q ? done1 : done0, q == 1 || c1 <= k);
+                    if (ok && k + 1 < cnt)
+                        ok = scores(q, k + 1, q == 1 || c1 <= k + 1, k + 2 == cnt);
+                }
+            }
+            n0 += most * kPieces;
+            done0 += c0;
+            done1 += c1;
         }
         if (*abort_flag) {
-            if (one)
-                mma_commit(drain);
+            mma_commit_if(drain, one);
             __syncwarp();
-            (void)mbar_wait_drain(drain, 0);
+            (void)mbar_drain_here(drain, 0);
         }
     }
     tc_fence_before();
@@ -434,6 +670,88 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (warp == kWarpMma)
         tmem_dealloc(tmem, 512);
+}
+
+// Joins the partial results of a block that several shares hold, as the
+// absorbed kernel's: blockIdx.x is the boundary between shares (+ 1), which
+// acts if it is the first that cuts its block; blockIdx.y: the query tile and
+// a quarter of the 128 elements.  A thread a row.
+__global__ void __launch_bounds__(kTile) latent_prefill_join_kernel(const PrefillArgs a, int shares)
+{
+    pdl_wait();
+    pdl_launch_dependents();
+    const auto same = [](const int4 &x, const int4 &y) {
+        return x.x == y.x && x.y == y.y && x.z == y.z;
+    };
+    const int first = blockIdx.x + 1;
+    const int4 here = a.ws_place[first], prev = a.ws_place[first - 1];
+    if (here.x < 0 || here.w == 0 || (same(here, prev) && prev.w > 0))
+        return;
+    int pieces = 1;  // shares first, first + 1, .. that begin inside the block
+    for (int b = first; b < shares; b += kTile) {
+        const int c = b + (int)threadIdx.x;
+        bool in = false;
+        if (c < shares) {
+            const int4 x = a.ws_place[c];
+            in = same(x, here) && x.w > 0;
+        }
+        pieces += __syncthreads_count(in);
+    }
+    Block k;
+    k.head = here.x;
+    k.b = here.y;
+    k.i = here.z;
+    block_seq(a, a.cu_q, a.cu_k, k);
+    const int q = blockIdx.y >> 2, c0 = 32 * (blockIdx.y & 3);
+    const int t = threadIdx.x, row = k.i * kRows + q * kTile + t;
+    if (row >= k.nq)
+        return;
+    // a share leaves its first segment at 2 p, its last after it
+    const bool late = !same(here, prev);
+    const auto piece = [&](int i) {
+        return a.ws_part +
+               ((int64_t)(2 * (first - 1 + i) + (i == 0 && late)) * 2 + q) * kPartTile;
+    };
+    float top = -INFINITY;
+    #pragma unroll 4
+    for (int i = 0; i < pieces; ++i)
+        top = fmaxf(top, piece(i)[kTile * kV + t]);
+    top = top == -INFINITY ? 0.0f : top;
+    float acc[32] = {}, sum = 0.0f;
+    for (int i = 0; i < pieces; ++i) {
+        const float *f = piece(i);
+        const float l = f[kTile * kV + kTile + t];
+        const float wt = ex2(f[kTile * kV + t] - top);
+        if (l == 0.0f)
+            continue;  // no key here: its O was not written
+        sum = fmaf(wt, l, sum);
+        #pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float4 v = *reinterpret_cast<const float4 *>(f + (c0 + 4 * e) * kTile + 4 * t);
+            acc[4 * e] = fmaf(wt, v.x, acc[4 * e]);
+            acc[4 * e + 1] = fmaf(wt, v.y, acc[4 * e + 1]);
+            acc[4 * e + 2] = fmaf(wt, v.z, acc[4 * e + 2]);
+            acc[4 * e + 3] = fmaf(wt, v.w, acc[4 * e + 3]);
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    __nv_bfloat16 *to = a.out + (int64_t)(k.seq_q + row) * a.ldo_row + k.head * a.ldo_head + c0;
+    #pragma unroll
+    for (int e = 0; e < 32; e += 8) {
+        uint32_t v[4];
+        #pragma unroll
+        for (int x = 0; x < 4; ++x)
+            v[x] = pack2(__float_as_uint(acc[e + 2 * x]), __float_as_uint(acc[e + 2 * x + 1]), inv);
+        *reinterpret_cast<uint4 *>(to + e) = make_uint4(v[0], v[1], v[2], v[3]);
+    }
+    if (a.lse && c0 == 0)
+        a.lse[(int64_t)(k.seq_q + row) * a.ld_lse + k.head] =
+            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+size_t place_bytes()
+{
+    return ((size_t)kMaxShares * sizeof(int4) + 255) / 256 * 256;
 }
 
 // bf16 [rows, H, dim] with these strides (elements) as bytes; boxes of 64
@@ -453,6 +771,13 @@ bool encode_rows(CUtensorMap *map, const uint16_t *p, int dim, int H, int rows, 
 
 using namespace idx;
 
+extern "C" size_t idx_latent_prefill_workspace_size(int Tq, int H)
+{
+    if (Tq <= 0 || H <= 0)
+        return 0;
+    return place_bytes() + (size_t)2 * kMaxShares * 2 * kPartTile * sizeof(float);
+}
+
 extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
                                          const uint16_t *k, int64_t ldk_row, int64_t ldk_head,
                                          const uint16_t *k_rope, int64_t ld_rope,
@@ -460,8 +785,8 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
                                          const int32_t *cu_q, const int32_t *cu_k, int B, int Tq,
                                          int Tk, int H, int d_nope, int d_rope, int d_v,
                                          float scale, int causal, uint16_t *out, int64_t ldo_row,
-                                         int64_t ldo_head, float *lse, int64_t ld_lse,
-                                         idx_stream_t stream)
+                                         int64_t ldo_head, float *lse, int64_t ld_lse, void *ws,
+                                         size_t ws_bytes, idx_stream_t stream)
 {
     IDX_NVTX_RANGE("idx_latent_prefill");
     if (B < 0 || Tq < 0 || Tk < 0 || H <= 0 || d_nope <= 0 || d_rope < 0 || d_v <= 0)
@@ -477,6 +802,12 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
         !aligned16(k) || !aligned16(k_rope) || !aligned16(v) || !aligned16(out) ||
         (ldq_row | ldq_head | ldk_row | ldk_head | ld_rope | ldv_row | ldv_head | ldo_row |
          ldo_head) % 8 != 0)
+        return IDX_ERR_UNSUPPORTED;
+    if (!ws || !aligned16(ws) || ws_bytes < idx_latent_prefill_workspace_size(Tq, H))
+        return IDX_ERR_WORKSPACE;
+    // an upper bound of the list: every block and the most keys it may see
+    const int64_t bound = ((int64_t)Tq / kRows + B) * ((int64_t)Tk / kTile + 1) * H;
+    if (bound > INT32_MAX || Tq / kRows > 32768)
         return IDX_ERR_UNSUPPORTED;
     CUtensorMap tq, tk, tr, tv;
     const uint64_t rdims[2] = {2 * kRope, (uint64_t)Tk};
@@ -509,8 +840,8 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
     a.status = device_status_ptr();
     if (!a.status)
         return IDX_ERR_CUDA;
-    // two query tiles a CTA unless that leaves SMs without one
-    a.tiles = (int64_t)(Tq / (2 * kTile)) * H >= sm_count() ? 2 : 1;
+    a.ws_place = static_cast<int4 *>(ws);
+    a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + place_bytes());
     static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
@@ -522,11 +853,12 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
             return IDX_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    // every sequence ends in at most one block that is not full
-    const int64_t blocks = (int64_t)Tq / (a.tiles * kTile) + B;
-    if (blocks > INT32_MAX)
-        return IDX_ERR_UNSUPPORTED;
-    return launch_status(launch_pdl(latent_prefill_kernel, dim3((unsigned)blocks, H),
-                                    dim3(kThreads), kSmem, (cudaStream_t)stream, tq, tk, tr, tv,
-                                    a));
+    const int shares =
+        (int)std::min<int64_t>(std::min(sm_count(), kMaxShares), std::max<int64_t>(1, bound / 2));
+    cudaError_t e = launch_pdl(latent_prefill_kernel, dim3(shares), dim3(kThreads), kSmem,
+                               (cudaStream_t)stream, tq, tk, tr, tv, a);
+    if (e == cudaSuccess && shares > 1)
+        e = launch_pdl(latent_prefill_join_kernel, dim3(shares - 1, 8), dim3(kTile), 0,
+                       (cudaStream_t)stream, a, shares);
+    return launch_status(e);
 }

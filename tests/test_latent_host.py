@@ -117,9 +117,9 @@ def test_paged_attention_refusals():
 
 def test_prefill_refusals():
     base = [FAKE, 64 * 192, 192, FAKE, 64 * 256, 256, FAKE, 576, FAKE, 64 * 256, 256, FAKE, FAKE, 2, 100,
-            100, 64, 128, 64, 128, 0.1, 1, FAKE, 64 * 128, 128, FAKE, 64, None]
+            100, 64, 128, 64, 128, 0.1, 1, FAKE, 64 * 128, 128, FAKE, 64, FAKE, 1 << 30, None]
     p = dict(q=0, qr=1, qh=2, k=3, kr=4, kh=5, rope=6, ldr=7, v=8, vr=9, vh=10, cq=11, ck=12, B=13, Tq=14,
-             Tk=15, H=16, dn=17, dr=18, dv=19, scale=20, out=22, outr=23, oh=24, lse=25, ldl=26)
+             Tk=15, H=16, dn=17, dr=18, dv=19, scale=20, out=22, outr=23, oh=24, lse=25, ldl=26, ws=27, wsb=28)
     call = _caller("idx_latent_prefill", base, p)
     assert call(B=0) == 0 and call(Tq=0) == 0
     for kw in (dict(B=-1), dict(Tq=-1), dict(Tk=-1), dict(H=0), dict(q=None), dict(k=None), dict(rope=None),
@@ -129,6 +129,7 @@ def test_prefill_refusals():
     for kw in (dict(dn=64), dict(dr=32), dict(dv=64), dict(q=FAKE + 2), dict(kr=64 * 256 + 4), dict(ldr=572),
                dict(v=FAKE + 8), dict(H=65536, ldl=65536)):
         assert call(**kw) == UNSUPPORTED, kw
+    assert call(ws=None) == WORKSPACE and call(wsb=0) == WORKSPACE and call(ws=FAKE + 8) == WORKSPACE
 
 
 def test_binding_refusals():
@@ -169,4 +170,6 @@ def test_binding_refusals():
 
 def test_workspace_size_of_nothing():
     f = B.lib().idx_latent_attention_workspace_size
+    g = B.lib().idx_latent_prefill_workspace_size
+    assert g(0, 64) == 0 and g(4, 0) == 0 and g(1, 1) > 0
     assert f(0, 64) == 0 and f(4, 0) == 0 and isinstance(f(1, 1), int) and ctypes.sizeof(ctypes.c_size_t) == 8

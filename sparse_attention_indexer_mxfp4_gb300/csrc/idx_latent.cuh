@@ -24,15 +24,24 @@ struct LatentPool {
     int64_t stride;  // bytes between pages
     int num_pages;
     int page_size;
-    int page_shift;  // log2(page_size), or -1
+    // slot / page_size = __umulhi(slot, magic) >> shift for slots below 2^31
+    // (magic = 0: page_size is 1)
+    uint32_t magic;
+    int shift;
 };
 
 inline LatentPool make_pool(const uint8_t *base, int64_t stride, int num_pages, int page_size)
 {
-    LatentPool p = {base, stride, num_pages, page_size, -1};
-    for (int s = 0; s < 31; ++s)
-        if (page_size == 1 << s)
-            p.page_shift = s;
+    // rounding up: with l = ceil(log2 d), m = floor(2^(31 + l) / d) + 1 is below
+    // 2^32 and n m / 2^(31 + l) exceeds n / d by less than 1 / d for n < 2^31
+    LatentPool p = {base, stride, num_pages, page_size, 0, 0};
+    if (page_size > 1) {
+        int l = 1;
+        while ((1ll << l) < page_size)
+            ++l;
+        p.magic = (uint32_t)((1ull << (31 + l)) / (uint64_t)page_size + 1);
+        p.shift = l - 1;
+    }
     return p;
 }
 
@@ -51,26 +60,10 @@ inline idx_status check_pool(const uint8_t *base, int64_t stride, int num_pages,
     return IDX_OK;
 }
 
-// Slot -> page and offset; false for a slot outside the pool.
-IDX_DEVFN bool slot_place(const LatentPool &p, int64_t slot, int64_t *page_byte, int *off)
+// Page of a slot (or of a token within its sequence), below 2^31.
+IDX_DEVFN int page_of(const LatentPool &p, int slot)
 {
-    if (slot < 0)
-        return false;
-    int64_t page;
-    if (p.page_shift >= 0) {
-        page = slot >> p.page_shift;
-        *off = (int)(slot & (p.page_size - 1));
-    } else {
-        page = slot / p.page_size;
-        *off = (int)(slot - page * p.page_size);
-    }
-    *page_byte = page * p.stride;
-    return page < p.num_pages;
-}
-
-IDX_DEVFN int page_of(const LatentPool &p, int t)
-{
-    return p.page_shift >= 0 ? t >> p.page_shift : t / p.page_size;
+    return p.magic ? (int)(__umulhi((uint32_t)slot, p.magic) >> p.shift) : slot;
 }
 
 } // namespace idx

@@ -91,7 +91,8 @@ __device__ __forceinline__ int query_end(const AttnArgs &a, int b, int j)
     return min(max(end, 0), a.max_len);
 }
 
-__device__ __forceinline__ Row row_of(const AttnArgs &a, int r)
+// Out of line: every role asks, once a row.
+__device__ __noinline__ Row row_of(const AttnArgs &a, int r)
 {
     if (a.indptr) {
         const int lo = min(max(a.indptr[r], 0), a.num_slots);
@@ -100,6 +101,7 @@ __device__ __forceinline__ Row row_of(const AttnArgs &a, int r)
     }
     int n = query_end(a, r, a.next - 1);
     if (a.ctx_per_row)
+        #pragma unroll 1
         for (int j = 0; j + 1 < a.next; ++j)
             n = max(n, query_end(a, r, j));
     return {r * a.bt_stride, n};
@@ -375,21 +377,20 @@ __device__ __forceinline__ uint32_t rope_at(uint32_t stage, int wl, int lane)
 
 // Half h (chunks 4 h .., the rotated elements with the second) as bf16 into
 // the stage.
-__device__ __forceinline__ void put_codes(uint32_t stage, int wl, int lane, const Codes &c,
-                                          int h)
+__device__ __forceinline__ void put_codes(uint32_t stage, int wl, int lane, Codes &c, int h)
 {
-    const uint32_t u0 = codes_at(stage, wl, lane), u1 = u0 ^ 16;
+    const uint32_t u0 = codes_at(stage, wl, lane), u1 = u0 ^ 16, half = h * 4 * kChunkBytes;
     #pragma unroll
     for (int j = 0; j < kToks / 2; ++j) {
         const uint32_t four =
             __shfl_sync(0xffffffffu, c.scales, 4 * j + 2 * ((lane >> 2) & 1) + h);
         const uint32_t mul = widen_mul(__byte_perm(four, 0, 0x4440 | (lane >> 3)));
-        const uint4 v = c.row[j][h];
+        const uint4 v = c.row[j][0];
+        c.row[j][0] = c.row[j][1];  // the second half's turn: one code for both
         const uint2 a = widen4(v.x, mul), b = widen4(v.y, mul);
         const uint2 d = widen4(v.z, mul), e = widen4(v.w, mul);
-        const uint32_t to = j * kPairBytes + h * 4 * kChunkBytes;
-        st_shared_v4(u0 + to, a.x, a.y, b.x, b.y);
-        st_shared_v4(u1 + to, d.x, d.y, e.x, e.y);
+        st_shared_v4(u0 + half + j * kPairBytes, a.x, a.y, b.x, b.y);
+        st_shared_v4(u1 + half + j * kPairBytes, d.x, d.y, e.x, e.y);
     }
     if (h == 0)
         return;
@@ -401,7 +402,7 @@ __device__ __forceinline__ void put_codes(uint32_t stage, int wl, int lane, cons
 
 // Scales over 2^7 and the NaN scale: multiplies the warp's own part of the
 // stage by what widen_mul left out.  Rare (latents beyond 57344).
-__device__ __forceinline__ void fix_scales(uint32_t stage, int wl, int lane, uint32_t scales,
+__device__ __noinline__ void fix_scales(uint32_t stage, int wl, int lane, uint32_t scales,
                                            int h)
 {
     #pragma unroll 1
@@ -502,6 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int chunk = (a.rows + kThreads - 1) / kThreads;
     const int r0 = min(a.rows, tid * chunk), r1 = min(a.rows, r0 + chunk);
     int mine = 0;
+    #pragma unroll 1
     for (int r = r0; r < r1; ++r)
         mine += tiles_of(row_of(a, r).n);
     int upto = mine;
@@ -529,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int2 *place = reinterpret_cast<int2 *>(a.ws_place);
     if (left > 0 && u0 >= before && u0 < before + mine) {
         int q = before, r = r0, tl = tiles_of(row_of(a, r).n);
+        #pragma unroll 1
         while (u0 >= q + tl) {
             q += tl;
             tl = tiles_of(row_of(a, ++r).n);
@@ -542,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         place[p] = make_int2(-1, 0);
     if (a.hpg * a.rpg < N) {
         // columns without a head: their query rows are zeros
+        #pragma unroll 1
         for (int e = tid; e < C::Q_BYTES / 16; e += kThreads)
             st_shared_v4(sbase + C::OFF_Q + 16 * e, 0, 0, 0, 0);
         fence_proxy_async_smem();
@@ -583,18 +587,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                         column_place(a, group, tid, &j, &h) ? query_end(a, s.r, j) : s.row.n;
                 }
                 if (a.next > 1)
+                    #pragma unroll 1
                     for (int j = 0; j < a.rpg; ++j)
                         first_end = min(first_end,
                                         query_end(a, s.r, min(group.j0 + j, a.next - 1)));
                 named_bar_sync(1, 32 * kSoftWarps);
             }
+            #pragma unroll 1
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int st = i & 1;
                 const uint32_t ph = (i >> 1) & 1;
                 // after an abort the waits return at once and the loops run
                 // out: every barrier below is still reached by all
-                (void)mbar_wait_here(&full[2 * st], ph, abort_flag, a.status);
-                (void)mbar_wait_here(&s_full[st], ph, abort_flag, a.status);
+                (void)mbar_wait(&full[2 * st], ph, abort_flag, a.status);
+                (void)mbar_wait(&s_full[st], ph, abort_flag, a.status);
                 __syncwarp();
                 tc_fence_after();
                 uint32_t sr[4 * NH];
@@ -677,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     if (t > s.t0) {
                         // O^T of the row so far, once its last product is in
-                        (void)mbar_wait_here(p_empty, (i - 1) & 1, abort_flag, a.status);
+                        (void)mbar_wait(p_empty, (i - 1) & 1, abort_flag, a.status);
                         named_bar_sync(1, 32 * kSoftWarps);
                         tc_fence_after();
                         #pragma unroll 1
@@ -705,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P^T as bf16 (half a step of 2^-8 a weight), head rows of 64
                 // tokens, once the product before has read the last ones
                 if (i > 0)
-                    (void)mbar_wait_here(p_empty, (i - 1) & 1, abort_flag, a.status);
+                    (void)mbar_wait(p_empty, (i - 1) & 1, abort_flag, a.status);
                 __syncwarp();
                 #pragma unroll
                 for (int j = 0; j < NH; j += 2) {
@@ -761,7 +767,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     part[kLatent * N + N + tid] = sum;
                 }
             }
-            (void)mbar_wait_here(o_full, k & 1, abort_flag, a.status);
+            (void)mbar_wait(o_full, k & 1, abort_flag, a.status);
             named_bar_sync(1, 32 * kSoftWarps);
             tc_fence_after();
             if (whole) {
@@ -839,19 +845,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         Feed f = {w.row, w.r, w.t, 0, left};
         if (left > 0)
             feed_row(f);
-        if (st == 1)
-            feed_next(a, f);
-        Entry entry = feed_entry(a, f, key, on);
+        Entry entry = {0, -1};
         Places pl;
         Codes cd;
-        for (int i = st - 2; i < left; i += 2) {
-            bool ok = true;
+        int skip = st;  // tiles to pass over: the other half's
+        #pragma unroll 1
+        for (int i = st - 4; i < left; i += 2) {
             if (i >= 0) {
                 const uint32_t ph = ((i >> 1) - 1) & 1;
-                #pragma unroll
+                bool ok = true;
+                #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
-                    ok = ok && (i < 2 || mbar_wait_here(&empty[2 * st + h], ph, abort_flag,
-                                                        a.status));
+                    ok = i < 2 || mbar_wait(&empty[2 * st + h], ph, abort_flag, a.status);
                     if (!ok)
                         break;
                     __syncwarp();
@@ -888,13 +893,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         mbar_arrive(&full[2 * st + 1]);
                 }
             }
-            // the group's next tile (its entries were fetched a tile ago)
+            // the half's next tile (its entries were fetched a tile ago)
             pl = places_of<FP8>(a, entry);
-            feed_next(a, f);
-            feed_next(a, f);
-            entry = feed_entry(a, f, key, on);
             if constexpr (FP8)
                 load_codes(pl, lane, cd);
+            #pragma unroll 1
+            for (; skip > 0; --skip)
+                feed_next(a, f);
+            skip = 2;
+            entry = feed_entry(a, f, key, on);
         }
         if constexpr (!FP8)
             cp_async_wait<0>();  // after an abort
@@ -906,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int i = 0, k = 0;
         bool ok = true, q_flying = false;
         for (; ok && next_seg(a, w, s); ++k) {
-            if (k > 0 && !mbar_wait_here(q_empty, (k - 1) & 1, abort_flag, a.status))
+            if (k > 0 && !mbar_wait(q_empty, (k - 1) & 1, abort_flag, a.status))
                 break;
             __syncwarp();
             if (one) {
@@ -918,19 +925,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             q_flying = true;
-            if (!mbar_wait_here(q_full, k & 1, abort_flag, a.status))
+            if (!mbar_wait(q_full, k & 1, abort_flag, a.status))
                 break;
             q_flying = false;
+            #pragma unroll 1
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int st = i & 1;
                 const uint32_t ph = (i >> 1) & 1;
-                ok = i < 2 || mbar_wait_here(&s_empty[st], ph ^ 1, abort_flag, a.status);
-                const uint32_t kd = desc_lo(sbase + st * kStageBytes);
-                const uint32_t qd = desc_lo(sbase + C::OFF_Q);
-                #pragma unroll
+                ok = i < 2 || mbar_wait(&s_empty[st], ph ^ 1, abort_flag, a.status);
+                uint32_t kd = desc_lo(sbase + st * kStageBytes), qd = desc_lo(sbase + C::OFF_Q);
+                #pragma unroll 1
                 for (int ch = 0; ok && ch < kChunks; ++ch) {
                     if (ch == 0 || ch == 4) {
-                        ok = mbar_wait_here(&full[2 * st + (ch >> 2)], ph, abort_flag, a.status);
+                        ok = mbar_wait(&full[2 * st + (ch >> 2)], ph, abort_flag, a.status);
                         if (!ok)
                             break;
                         __syncwarp();
@@ -938,9 +945,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + C::COL_S + st * N, kd + (ch * kChunkBytes >> 4) + 2 * kk,
-                                qd + (ch * N * 128 >> 4) + 2 * kk, kDescHiSw128, id,
-                                ch + kk > 0 ? 1u : 0u, one);
+                        mma_f16(tmem + C::COL_S + st * N, kd + 2 * kk, qd + 2 * kk, kDescHiSw128,
+                                id, kk > 0 ? 1u : (ch > 0 ? 1u : 0u), one);
+                    kd += kChunkBytes >> 4;
+                    qd += N * 128 >> 4;
                 }
                 if (!ok)
                     break;
@@ -954,8 +962,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit(&drain[0]);
             __syncwarp();
             if (q_flying)
-                (void)mbar_drain_here(q_full, k & 1);
-            (void)mbar_drain_here(&drain[0], 0);
+                (void)mbar_wait_drain(q_full, k & 1);
+            (void)mbar_wait_drain(&drain[0], 0);
         }
     } else {
         // --------------------------------------------- O^T += K^T P^T
@@ -964,21 +972,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         int i = 0;
         bool ok = true;
         while (ok && next_seg(a, w, s)) {
+            #pragma unroll 1
             for (int t = s.t0; t < s.t1; ++t, ++i) {
                 const int st = i & 1;
-                ok = mbar_wait_here(p_full, i & 1, abort_flag, a.status);
+                ok = mbar_wait(p_full, i & 1, abort_flag, a.status);
                 if (!ok)
                     break;
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t vd = desc_lo(sbase + st * kStageBytes, kChunkBytes);
+                uint32_t vd = desc_lo(sbase + st * kStageBytes, kChunkBytes);
                 const uint32_t pd = desc_lo(sbase + C::OFF_P);
-                #pragma unroll
+                #pragma unroll 1
                 for (int mt = 0; mt < 4; ++mt) {
                     #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_f16(tmem + mt * N, vd + (2 * mt * kChunkBytes >> 4) + kk * (2048 >> 4),
-                                pd + 2 * kk, kDescHiSw128, id, t > s.t0 || kk > 0 ? 1u : 0u, one);
+                        mma_f16(tmem + mt * N, vd + kk * (2048 >> 4), pd + 2 * kk, kDescHiSw128,
+                                id, kk > 0 ? 1u : (t > s.t0 ? 1u : 0u), one);
+                    vd += 2 * kChunkBytes >> 4;
                     if (mt & 1)
                         mma_commit_if(&empty[2 * st + (mt >> 1)], one);
                 }
@@ -991,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (one)
                 mma_commit(&drain[1]);
             __syncwarp();
-            (void)mbar_drain_here(&drain[1], 0);
+            (void)mbar_wait_drain(&drain[1], 0);
         }
     }
     tc_fence_before();

@@ -78,9 +78,10 @@ __global__ void __launch_bounds__(kCacheThreads)
         const uint32_t rope = *reinterpret_cast<const uint32_t *>(row + kLatent + 2 * lane);
         if (slot < 0)
             continue;
-        int64_t page_byte;
-        int off;
-        const bool in_pool = slot_place(pool, slot, &page_byte, &off);
+        const bool in_pool = slot < (int64_t)pool.num_pages * pool.page_size;
+        const int page_id = in_pool ? page_of(pool, (int)slot) : 0;
+        const int off = (int)slot - page_id * pool.page_size;
+        const int64_t page_byte = page_id * pool.stride;
         const bool in_table = !cos_sin || (pos >= 0 && pos < num_pos);
         if (!in_pool || !in_table) {
             if (lane == 0)

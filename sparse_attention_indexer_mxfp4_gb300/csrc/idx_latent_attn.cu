@@ -19,7 +19,8 @@
 //
 // Work is split over the flat list of (row, tile): every share is an equal
 // contiguous part, whatever the rows' lengths (a row: a ragged row, or a
-// sequence of the paged form).  Rows that lie in one share are finished there;
+// sequence of the paged form).  A row counts a few tiles more than it has: what
+// a CTA that begins it pays for the end of the row before.  Rows that lie in one share are finished there;
 // the others leave unnormalised sums with their maximum in scratch and a
 // second kernel joins them in share order.
 //
@@ -64,6 +65,7 @@ struct AttnArgs {
     int rows, next;            // rows of the list; query rows in each (paged: next_n)
     int H, groups, hgroups;    // head groups, times groups of query rows
     int hpg, rpg;              // heads and query rows of a group's columns
+    int charge;                // tiles a row counts besides its own
     uint32_t inv_hpg;          // column / hpg = column * inv_hpg >> 16
     float scale_log2;  // scale * log2(e)
     uint16_t *out;
@@ -166,6 +168,32 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
             w.row = row_of(a, w.r);
     }
     return true;
+}
+
+// Reduces each of CNT values over the eight lanes that differ in bits 2-4,
+// halving the values a lane carries at every step (CNT - 1 exchanges, not 3
+// CNT).  Lane l is left with CNT / 8 results (one, for fewer than eight) in
+// v[0 ..]; returns which value v[0] is.
+template <int CNT, typename Op>
+__device__ __forceinline__ int reduce_rows(float (&v)[CNT], int lane, Op op)
+{
+    int base = 0;
+    #pragma unroll
+    for (int o = 16, n = CNT; o >= 4; o >>= 1) {
+        if (n > 1) {
+            n >>= 1;
+            const bool up = lane & o;
+            #pragma unroll
+            for (int e = 0; e < n; ++e) {
+                const float got = __shfl_xor_sync(0xffffffffu, up ? v[e] : v[e + n], o);
+                v[e] = op(up ? v[e + n] : v[e], got);
+            }
+            base += up ? n : 0;
+        } else {
+            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
+        }
+    }
+    return base;
 }
 
 template <int N>
@@ -457,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using C = Cfg<N>;
     constexpr int NH = N / 8;           // fragments of eight heads
+    constexpr int KEPT = 2 * NH > 8 ? NH / 4 : 1;  // what reduce_rows leaves a lane
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
@@ -499,13 +528,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_wait();
     pdl_launch_dependents();
 
-    // this CTA's share: a prefix sum of the rows' tiles over the threads
+    // this CTA's share: a prefix sum of the rows' tiles, and what each row
+    // counts besides, over the threads
     const int chunk = (a.rows + kThreads - 1) / kThreads;
     const int r0 = min(a.rows, tid * chunk), r1 = min(a.rows, r0 + chunk);
     int mine = 0;
     #pragma unroll 1
     for (int r = r0; r < r1; ++r)
-        mine += tiles_of(row_of(a, r).n);
+        mine += tiles_of(row_of(a, r).n) + a.charge;
     int upto = mine;
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -526,23 +556,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Group group = group_of(a, blockIdx.x);
     const int p = blockIdx.y, shares = min((int)gridDim.y, total);
     const int each = total / shares, more = total - each * shares;
-    const int u0 = p * each + min(p, more);
-    const int left = p < shares ? each + (p < more) : 0;
     int2 *place = reinterpret_cast<int2 *>(a.ws_place);
-    if (left > 0 && u0 >= before && u0 < before + mine) {
-        int q = before, r = r0, tl = tiles_of(row_of(a, r).n);
-        #pragma unroll 1
-        while (u0 >= q + tl) {
-            q += tl;
-            tl = tiles_of(row_of(a, ++r).n);
+    // the share's bounds as places in the list and as tiles (a place within a
+    // row's charge is its first tile)
+    #pragma unroll 1
+    for (int e = 0; e < 2; ++e) {
+        const int u = (p + e) * each + min(p + e, more);
+        if (p + e <= shares && u >= before && u < before + mine) {
+            int q = before, r = r0, n = tiles_of(row_of(a, r).n) + a.charge;
+            #pragma unroll 1
+            while (u >= q + n) {
+                q += n;
+                n = tiles_of(row_of(a, ++r).n) + a.charge;
+            }
+            const int t = max(0, u - q - a.charge);
+            misc[2 + e] = q - r * a.charge + t;
+            if (e == 0) {
+                misc[4] = r;
+                misc[5] = t;
+            }
         }
-        misc[2] = r;
-        misc[3] = u0 - q;
-        if (blockIdx.x == 0)
-            place[p] = make_int2(r, u0 - q);
     }
-    if (left == 0 && blockIdx.x == 0 && tid == 0)
-        place[p] = make_int2(-1, 0);
+    __syncthreads();
+    const int tiles1 = p + 1 < shares ? (int)misc[3] : total - a.rows * a.charge;
+    const int left = p < shares ? tiles1 - (int)misc[2] : 0;
+    if (blockIdx.x == 0 && tid == 0)
+        place[p] = left > 0 ? make_int2(misc[4], misc[5]) : make_int2(-1, 0);
     if (a.hpg * a.rpg < N) {
         // columns without a head: their query rows are zeros
         #pragma unroll 1
@@ -556,8 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     Walk w = {left, 0, 0, {0, 0}};  // a CTA without a share has an empty walk
     if (left > 0) {
-        w.r = misc[2];
-        w.t = misc[3];
+        w.r = misc[4];
+        w.t = misc[5];
         w.row = row_of(a, w.r);
     }
     Seg s;
@@ -658,16 +697,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     over |= fmaf(fmaxf(x[q], x[q + 2]), sl, -m[e]) > kLazy;
                 }
                 if (named_bar_or(1, 32 * kSoftWarps, over)) {
+                    float v[2 * NH];
                     #pragma unroll
                     for (int e = 0; e < 2 * NH; ++e) {
                         const int q = 4 * (e >> 1) + (e & 1);
-                        float v = fmaxf(x[q], x[q + 2]);
-                        #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1)
-                            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                        if (g8 == 0)
-                            smax[warp * N + 8 * (e >> 1) + c2 + (e & 1)] = v;
+                        v[e] = fmaxf(x[q], x[q + 2]);
                     }
+                    const int b = reduce_rows(v, lane, [](float y, float z) { return fmaxf(y, z); });
+                    #pragma unroll
+                    for (int e = 0; e < KEPT; ++e)
+                        smax[warp * N + 8 * ((b + e) >> 1) + c2 + ((b + e) & 1)] = v[e];
                     named_bar_sync(1, 32 * kSoftWarps);
                     #pragma unroll
                     for (int e = 0; e < 2 * NH; ++e) {
@@ -734,17 +773,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the segment's sums, then its O^T
             named_bar_sync(1, 32 * kSoftWarps);
+            const int b = reduce_rows(l, lane, [](float y, float z) { return y + z; });
             #pragma unroll
-            for (int e = 0; e < 2 * NH; ++e) {
+            for (int e = 0; e < KEPT; ++e)
+                smax[warp * N + 8 * ((b + e) >> 1) + c2 + ((b + e) & 1)] = l[e];
+            if (warp == 0 && g8 == 0) {
                 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1)
-                    l[e] += __shfl_xor_sync(0xffffffffu, l[e], o);
-                const int h = 8 * (e >> 1) + c2 + (e & 1);
-                if (g8 == 0) {
-                    smax[warp * N + h] = l[e];
-                    if (warp == 0)
-                        shead[h] = m[e];
-                }
+                for (int e = 0; e < 2 * NH; ++e)
+                    shead[8 * (e >> 1) + c2 + (e & 1)] = m[e];
             }
             named_bar_sync(1, 32 * kSoftWarps);
             const bool whole = s.t0 == 0 && s.t1 == s.tiles;
@@ -895,7 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // the half's next tile (its entries were fetched a tile ago)
             pl = places_of<FP8>(a, entry);
-            if constexpr (FP8)
+            if (FP8 && i >= st - 2)
                 load_codes(pl, lane, cd);
             #pragma unroll 1
             for (; skip > 0; --skip)
@@ -1217,7 +1253,7 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
     a.groups = a.hgroups * ((a.next + a.rpg - 1) / a.rpg);
     // places in out are kept in units of eight elements, in 32 bits
     const int64_t span = (a.next - 1) * a.ldo_row + (a.H - 1) * a.ldo_head;
-    if (a.groups > sm_count() || most > INT32_MAX || a.pool.stride > INT32_MAX ||
+    if (a.groups > sm_count() || most > INT32_MAX / 4 || a.pool.stride > INT32_MAX ||
         span / 8 > INT32_MAX)
         return IDX_ERR_UNSUPPORTED;
     a.page_stride = (int)a.pool.stride;
@@ -1227,6 +1263,9 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
     // one CTA per SM, the same number for every group
     const int shares =
         (int)std::min<int64_t>(std::min(sm_count(), kMaxShares) / a.groups, most);
+    // the end of a row (its sums, its output, the next row's first scores) costs
+    // a CTA about as much as this many tiles; short shares are left equal
+    a.charge = most >= 8ll * shares ? (n == 64 ? 3 : 2) : 0;
     CUtensorMap tm;
     // bytes of a head row, heads, rows; a stride over one element is free
     const uint64_t dims[3] = {2 * kLatTok, (uint64_t)a.H, (uint64_t)R};

@@ -22,7 +22,8 @@
 //
 // Work is the flat list of (head, block, key tile); every CTA (one per SM)
 // takes an equal contiguous share of it, so causal blocks of any length fill
-// the GPU evenly and few queries on many keys are spread over it.  The next
+// the GPU evenly and few queries on many keys are spread over it; a block
+// counts a tile more than it has, for the end of the one before.  The next
 // block's queries and keys come in while the last one's epilogue runs.  A block
 // that shares cut leaves unnormalised sums in scratch for a second kernel.
 //
@@ -79,6 +80,7 @@ struct PrefillArgs {
 constexpr int kRows = 2 * kTile;                        // queries of a block
 constexpr int kPartTile = kTile * kV + 2 * kTile;       // floats of a query tile's partial result
 constexpr int kMaxShares = 152;
+constexpr int kCharge = 1;  // tiles that a block counts besides its own
 
 // A block: queries kRows i .. of sequence b, for one head.
 struct Block {
@@ -139,19 +141,21 @@ __device__ __forceinline__ int tiles_before(const PrefillArgs &a, int nq, int nk
     return z + rho * (n * (n + 1) - z * (z + 1)) / 2 + delta * (n - z);
 }
 
-// All of a sequence's tiles.
+// All of a sequence's tiles and its blocks' charges.
 __device__ __forceinline__ int tiles_of_seq(const PrefillArgs &a, int nq, int nk)
 {
     if (nq <= 0)
         return 0;
     const int blocks = (nq + kRows - 1) / kRows;
-    return tiles_before(a, nq, nk, blocks - 1) + max(1, (nk + kTile - 1) / kTile);
+    return tiles_before(a, nq, nk, blocks - 1) + max(1, (nk + kTile - 1) / kTile) +
+           blocks * kCharge;
 }
 
 // The walk of a share: segments of a block's tiles.
 struct Walk {
     Block k;
-    int t, left;
+    int t, left;  // left: tiles and charges
+    int pay;      // of the block's charge
 };
 
 struct Seg {
@@ -163,12 +167,15 @@ struct Seg {
 __device__ __forceinline__ bool next_seg(const PrefillArgs &a, const int32_t *cq,
                                          const int32_t *ck, Walk &w, Seg &s)
 {
-    if (w.left <= 0)
-        return false;
-    if (w.t < 0) {
+    if (w.t < 0 && w.left > kCharge) {
         block_next(a, cq, ck, w.k);
         w.t = 0;
+        w.pay = kCharge;
     }
+    w.left -= w.pay;
+    w.pay = 0;
+    if (w.left <= 0 || w.t < 0)
+        return false;
     s.k = w.k;
     s.t0 = w.t;
     s.nt[0] = key_tiles(a, w.k, 0);
@@ -318,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     // one value for the warp, as the compiler sees it too
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
-    w.t = 0;
+    w.t = w.pay = 0;
     if (w.left > 0) {
         w.k.b = __shfl_sync(0xffffffffu, misc[2], 0);
         int rest = __shfl_sync(0xffffffffu, misc[3], 0);
@@ -326,16 +333,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lo = 0, hi = (w.k.nq + kRows - 1) / kRows - 1;  // the last i with tiles_before <= rest
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tiles_before(a, w.k.nq, w.k.nk, mid) <= rest)
+            if (tiles_before(a, w.k.nq, w.k.nk, mid) + mid * kCharge <= rest)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         w.k.i = lo;
-        w.t = rest - tiles_before(a, w.k.nq, w.k.nk, lo);
+        rest -= tiles_before(a, w.k.nq, w.k.nk, lo) + lo * kCharge;
+        w.t = max(0, rest - kCharge);
+        w.pay = max(0, kCharge - rest);
     }
     if (tid == 0)
-        a.ws_place[p] = w.left > 0 ? make_int4(w.k.head, w.k.b, w.k.i, w.t) : make_int4(-1, 0, 0, 0);
+        a.ws_place[p] = w.left > w.pay ? make_int4(w.k.head, w.k.b, w.k.i, w.t) : make_int4(-1, 0, 0, 0);
     Seg s;
 
     if (warp < kWarpLoad) {
@@ -806,7 +815,7 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
     if (!ws || !aligned16(ws) || ws_bytes < idx_latent_prefill_workspace_size(Tq, H))
         return IDX_ERR_WORKSPACE;
     // an upper bound of the list: every block and the most keys it may see
-    const int64_t bound = ((int64_t)Tq / kRows + B) * ((int64_t)Tk / kTile + 1) * H;
+    const int64_t bound = ((int64_t)Tq / kRows + B) * ((int64_t)Tk / kTile + 1 + kCharge) * H;
     if (bound > INT32_MAX || Tq / kRows > 32768)
         return IDX_ERR_UNSUPPORTED;
     CUtensorMap tq, tk, tr, tv;

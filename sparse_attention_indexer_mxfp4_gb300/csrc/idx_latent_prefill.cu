@@ -15,7 +15,7 @@
 //
 // Keys and values come by TMA in pieces of 64 elements of 128 tokens (16 KB,
 // 128-byte swizzled), five a tile (three of K, the last shared by all heads,
-// two of V), through a ring of eight: K^T is read K-major, V M-major, as they
+// two of V), around a ring of eight places: K^T is read K-major, V M-major, as they
 // lie.  The running maximum is only raised when a score exceeds it by 2^40
 // (32-bit sums lose nothing by that), so rescaling O is rare after a row's
 // first tile.
@@ -53,7 +53,7 @@ static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegs && kRegs * kThreads <= 6553
               "the warpgroups' registers come from the launch's");
 constexpr int kOffRing = 2 * kQPieces * kPiece;
 constexpr int kOffBar = kOffRing + kRing * kPiece;
-constexpr int kBars = 2 * kRing + 12;
+constexpr int kBars = kRing + 18;
 constexpr int kOffMisc = kOffBar + 8 * kBars;  // tmem base, abort flag, the share's place
 constexpr int kOffCu = kOffMisc + 64;          // the sequences' bounds, where they fit
 constexpr int kMaxCu = 128;
@@ -223,27 +223,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     const uint32_t sbase = smem_u32(smem);
     uint64_t *bar = reinterpret_cast<uint64_t *>(smem + kOffBar);
-    uint64_t *full = bar, *empty = bar + kRing;
-    uint64_t *s_full = bar + 2 * kRing, *p_full = s_full + 2, *pv_done = s_full + 4;
-    uint64_t *q_full = s_full + 6, *q_free = s_full + 8, *tail = s_full + 10, *drain = s_full + 11;
+    // a piece of the ring came in; the keys and the values of even and odd tiles
+    // were read by their last product
+    uint64_t *full = bar, *k_free = bar + kRing, *v_free = k_free + 2;
+    uint64_t *s_full = k_free + 4, *p_full = k_free + 6, *pv_done = k_free + 8;
+    uint64_t *q_full = k_free + 10, *q_free = k_free + 12, *tail = k_free + 14;  // tail[2]
+    uint64_t *drain = k_free + 16;
     int *misc = reinterpret_cast<int *>(smem + kOffMisc);
     volatile int *abort_flag = misc + 1;
     const int tid = threadIdx.x, lane = tid & 31;
     const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     if (tid == 0) {
-        for (int i = 0; i < kRing; ++i) {
+        for (int i = 0; i < kRing; ++i)
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
-        }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&tail[i], 1);
+            mbar_init(&k_free[i], 1);
+            mbar_init(&v_free[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_full[i], 1);
             mbar_init(&q_free[i], 1);
         }
-        mbar_init(tail, 1);
         mbar_init(drain, 1);
         *abort_flag = 0;
         fence_mbar_init();
@@ -510,9 +513,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (regs_give<kRegsRest>(), warp == kWarpLoad) {
         // ------------------------------------------------------------- TMA
         const bool one = elect_one();
-        int n = 0, tails = 0;     // pieces issued, tiles cut off at a sequence's end
+        int n = 0, pieces = 0;    // tiles and pieces issued
+        int tails = 0;            // tiles whose values a sequence's end cuts
         int loads[2] = {0, 0};    // of each query tile
-        bool ok = true, tail_flying = false;
+        bool ok = true;
         while (ok && next_seg(a, cq, ck, w, s)) {
             #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -534,21 +538,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++loads[q];
             }
             const int most = min(s.t1, max(s.nt[0], s.nt[1]));
-            for (int j = s.t0; ok && j < most; ++j) {
+            for (int j = s.t0; ok && j < most; ++j, ++n) {
                 const int t0 = s.k.seq_k + j * kTile, rem = s.k.nk - j * kTile;
+                const bool cut = rem < kTile;  // values past the sequence
                 #pragma unroll 1
-                for (int c = 0; c < kPieces; ++c, ++n) {
-                    const int slot = n & (kRing - 1);
-                    if (n >= kRing) {
-                        ok = mbar_wait_here(&empty[slot], ((n >> 3) - 1) & 1, abort_flag, a.status);
-                        if (!ok)
-                            break;
-                    }
+                for (int c = 0; ok && c < kPieces; ++c) {
+                    // Piece 5 n + c takes the place of 5 n + c - 8: the last of tile
+                    // n - 2's keys (c = 0), its values (1, 2), tile n - 1's first
+                    // keys (3, 4).
+                    const int m = n * kPieces + c, slot = m & (kRing - 1);
+                    if (c == 0 && n >= 2)
+                        ok = mbar_wait_here(&k_free[n & 1], ((n >> 1) - 1) & 1, abort_flag,
+                                            a.status);
+                    else if (c == 1 && n >= 2)
+                        ok = mbar_wait_here(&v_free[n & 1], ((n >> 1) - 1) & 1, abort_flag,
+                                            a.status);
+                    else if (c == kQPieces && n >= 1)
+                        ok = mbar_wait_here(&k_free[(n - 1) & 1], ((n - 1) >> 1) & 1, abort_flag,
+                                            a.status);
+                    if (!ok)
+                        break;
                     __syncwarp();
                     uint8_t *to = smem + kOffRing + slot * kPiece;
-                    const bool cut = c >= kQPieces && rem < kTile;  // values past the sequence
                     if (one) {
-                        uint64_t *b = cut ? tail : &full[slot];
+                        uint64_t *b = cut && c >= kQPieces ? &tail[c - kQPieces] : &full[slot];
                         mbar_arrive_expect_tx(b, kPiece);
                         if (c < 2)
                             tma_load_3d(to, &tm_k, b, 128 * c, s.k.head, t0);
@@ -557,24 +570,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else
                             tma_load_3d(to, &tm_v, b, 128 * (c - kQPieces), s.k.head, t0);
                     }
-                    __syncwarp();
-                    if (cut) {
-                        // a weight of zero does not hide what is not finite:
-                        // another sequence's values become zeros here
-                        tail_flying = true;
-                        ok = mbar_wait_here(tail, tails & 1, abort_flag, a.status);
-                        if (!ok)
-                            break;
-                        tail_flying = false;
-                        ++tails;
-                        for (int e = rem * 8 + lane; e < kTile * 8; e += 32)
-                            st_shared_v4(smem_u32(to) + 16 * e, 0, 0, 0, 0);
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&full[slot]);
-                    }
+                    pieces = m + 1;
                 }
+                __syncwarp();
+                // a weight of zero does not hide what is not finite: another
+                // sequence's values become zeros here
+                #pragma unroll 1
+                for (int c = 0; ok && cut && c < kVPieces; ++c) {
+                    ok = mbar_wait_here(&tail[c], tails & 1, abort_flag, a.status);
+                    const int slot = (n * kPieces + kQPieces + c) & (kRing - 1);
+                    const uint32_t to = smem_u32(smem + kOffRing + slot * kPiece);
+                    for (int e = rem * 8 + lane; e < kTile * 8; e += 32)
+                        st_shared_v4(to + 16 * e, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&full[slot]);
+                }
+                tails += cut;
             }
         }
         if (*abort_flag) {
@@ -583,9 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 2; ++q)
                 if (loads[q] > 0)
                     (void)mbar_drain_here(&q_full[q], (loads[q] - 1) & 1);
-            if (tail_flying)
-                (void)mbar_drain_here(tail, tails & 1);
-            for (int i = n > kRing ? n - kRing : 0; i < n; ++i)
+            for (int c = 0; c < kVPieces; ++c)
+                if (tails > 0)
+                    (void)mbar_drain_here(&tail[c], (tails - 1) & 1);
+            for (int i = max(0, pieces - kRing); i < pieces; ++i)
                 (void)mbar_drain_here(&full[i & (kRing - 1)], (i >> 3) & 1);
         }
     } else if (warp == kWarpMma) {
@@ -593,49 +607,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t one = elect_one();
         const uint32_t id_s = idesc_bf16(kTile, kTile, false, false);
         const uint32_t id_v = idesc_bf16(kTile, 64, false, true);
-        int n0 = 0;            // ring piece of the segment's first tile
-        int fills = 0;         // segments whose queries came, two bits a query tile
+        int n0 = 0;            // tiles before the segment
+        int fills = 0;         // parity of the segments that each query tile had, a bit each
         int done0 = 0, done1 = 0;  // tiles of each query tile before the segment
-        // S of query tile q and key tile j (the segment's k-th); the last query
-        // tile of a key tile frees its pieces
-        const auto scores = [&](int q, int k, bool last, bool end) {
+        // S of query tile q and the segment's k-th key tile; the last query tile
+        // of a key tile frees it
+        const auto scores = [&](int q, int k, bool first, bool last, bool end) {
+            const int n = n0 + k, slot = n * kPieces;
             const uint32_t qd = desc_lo(sbase + q * kQPieces * kPiece);
             #pragma unroll
             for (int c = 0; c < kQPieces; ++c) {
-                const int n = n0 + k * kPieces + c, slot = n & (kRing - 1);
-                if (!mbar_wait_here(&full[slot], (n >> 3) & 1, abort_flag, a.status))
+                const int m = slot + c;
+                if (first && !mbar_wait_here(&full[m & (kRing - 1)], (m >> 3) & 1, abort_flag,
+                                             a.status))
                     return false;
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t kd = desc_lo(sbase + kOffRing + slot * kPiece);
+                const uint32_t kd = desc_lo(sbase + kOffRing + (m & (kRing - 1)) * kPiece);
                 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                     mma_f16(tmem + kColS + q * 128, qd + (c * kPiece >> 4) + 2 * e, kd + 2 * e,
                             kDescHiSw128, id_s, c + e > 0 ? 1u : 0u, one);
-                mma_commit_if(&empty[slot], one && last);
             }
             mma_commit_if(&s_full[q], one);
+            mma_commit_if(&k_free[n & 1], one && last);
             mma_commit_if(&q_free[q], one && end);
             return true;
         };
-        const auto values = [&](int q, int k, int done, bool last) {
+        const auto values = [&](int q, int k, int done, bool first, bool last) {
+            const int n = n0 + k, slot = n * kPieces + kQPieces;
             if (!mbar_wait_here(&p_full[q], (done + k) & 1, abort_flag, a.status))
                 return false;
             #pragma unroll
             for (int c = 0; c < kVPieces; ++c) {
-                const int n = n0 + k * kPieces + kQPieces + c, slot = n & (kRing - 1);
-                if (!mbar_wait_here(&full[slot], (n >> 3) & 1, abort_flag, a.status))
+                const int m = slot + c;
+                if (first && !mbar_wait_here(&full[m & (kRing - 1)], (m >> 3) & 1, abort_flag,
+                                             a.status))
                     return false;
                 __syncwarp();
                 tc_fence_after();
-                const uint32_t vd = desc_lo(sbase + kOffRing + slot * kPiece);
+                const uint32_t vd = desc_lo(sbase + kOffRing + (m & (kRing - 1)) * kPiece);
                 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     mma_f16_ts(tmem + kColO + q * 128 + 64 * c, tmem + kColS + q * 128 + 8 * e,
                                vd + e * (2048 >> 4), kDescHiSw128, id_v, k + e > 0 ? 1u : 0u, one);
-                mma_commit_if(&empty[slot], one && last);
             }
             mma_commit_if(&pv_done[q], one);
+            mma_commit_if(&v_free[n & 1], one && last);
             return true;
         };
         bool ok = true;
@@ -652,19 +670,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait_here(&q_full[q], (fills >> q) & 1, abort_flag, a.status);
                 fills ^= 1 << q;
                 if (ok)
-                    ok = scores(q, 0, q == 1 || c1 <= 0, cnt == 1);
+                    ok = scores(q, 0, q == 0 || c0 <= 0, q == 1 || c1 <= 0, cnt == 1);
             }
             for (int k = 0; ok && k < most; ++k) {
                 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int cnt = q ? c1 : c0;
                     if (ok && k < cnt)
-                        ok = values(q, k, q ? done1 : done0, q == 1 || c1 <= k);
+                        ok = values(q, k, q ? done1 : done0, q == 0 || c0 <= k, q == 1 || c1 <= k);
                     if (ok && k + 1 < cnt)
-                        ok = scores(q, k + 1, q == 1 || c1 <= k + 1, k + 2 == cnt);
+                        ok = scores(q, k + 1, q == 0 || c0 <= k + 1, q == 1 || c1 <= k + 1,
+                                    k + 2 == cnt);
                 }
             }
-            n0 += most * kPieces;
+            n0 += most;
             done0 += c0;
             done1 += c1;
         }

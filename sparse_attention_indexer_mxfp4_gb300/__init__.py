@@ -34,3 +34,4 @@ from ._binding import (  # noqa: F401
     version,
 )
 from .pipeline import IndexerStep, ProducerStep  # noqa: F401
+from .latent import LatentLayer, SparseDecodeStep  # noqa: F401

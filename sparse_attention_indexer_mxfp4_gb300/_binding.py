@@ -742,7 +742,9 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
     args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(slots),
             _ptr(indptr), slots.numel(), R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
             ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
-    return Prepared("idx_latent_attention", args, (q, kv_pages, slots, indptr, out, lse, ws))
+    # the attention, and the joining kernel unless one tile may be all
+    return Prepared("idx_latent_attention", args, (q, kv_pages, slots, indptr, out, lse, ws),
+                    2 if slots.numel() // 64 + R > 1 else 1)
 
 
 def idx_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
@@ -780,7 +782,8 @@ def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, con
             H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws),
             ws_bytes)
     return Prepared("idx_paged_latent_attention", args,
-                    (q, kv_pages, block_table, context_lens, out, lse, ws))
+                    (q, kv_pages, block_table, context_lens, out, lse, ws),
+                    2 if B_ * max(1, -(-max_model_len // 64)) > 1 else 1)
 
 
 def idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
@@ -818,7 +821,10 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
     args = (_ptr(q), ldq, ldqh, _ptr(k), ldk, ldkh, _ptr(k_rope), ldr, _ptr(v), ldv, ldvh,
             _ptr(cu_q), _ptr(cu_k), B_, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal),
             _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
-    return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws))
+    # the attention, and the joining kernel unless one share holds everything
+    bound = (Tq // 256 + B_) * (Tk // 128 + 2) * H
+    return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws),
+                    2 if bound >= 4 else 1)
 
 
 def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,

@@ -120,9 +120,9 @@ def _check(rc: int, name: str):
 def _ptr(t):
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("indexer tensors must live on a CUDA device")
-    return t.data_ptr()
+    if t.is_cuda:
+        return t.data_ptr()
+    raise ValueError("indexer tensors must live on a CUDA device")
 
 
 # the current stream's handle without a Stream object around it (a tenth of
@@ -168,6 +168,13 @@ class Prepared:
 
     def __call__(self, stream=None):
         _check(self.fn(*self.args, _stream(stream)), self.name)
+
+
+def _run(name, args, stream):
+    """A call made once: what Prepared does, without the object."""
+    rc = getattr(_lib or lib(), name)(*args, _stream(stream))
+    if rc != IDX_OK:
+        _check(rc, name)
 
 
 def prepare_mqa_logits(q, q_scale, weights, k, k_scale, row_ks, row_ke, fmt, logits):
@@ -638,12 +645,8 @@ def _out_lse(out, lse, rows, heads, dim, device):
     return out, lse, ldo[0], ldo[1], lse.stride(0)
 
 
-def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
+def _latent_store_args(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
                          slot_mapping, fmt):
-    """New tokens into the latent cache.  kv bf16 [T, 576] (512 latents, 64
-    elements to rotate; row stride free); positions int32 [T] and cos_sin fp32
-    [P, 64] (both None: stored as they are); norm_weight fp32 [512] (None: no
-    norm); slot_mapping int64 [T], negative skips."""
     (T, _), (ld_kv, _) = _need_heads(kv, 2, LATENT_DIM + LATENT_ROPE, "kv")
     _need(slot_mapping, torch.int64, "slot_mapping")
     pages, stride = _need_pages(kv_pages)
@@ -667,20 +670,27 @@ def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, pag
     args = (_ptr(kv), ld_kv, _ptr(positions), _ptr(cos_sin), ld, rows, _ptr(norm_weight), eps, T,
             LATENT_DIM, LATENT_ROPE, fmt, _ptr(kv_pages), stride, pages, page_size,
             _ptr(slot_mapping))
-    return Prepared("idx_latent_store", args,
-                    (kv, positions, cos_sin, norm_weight, kv_pages, slot_mapping))
+    return args, (kv, positions, cos_sin, norm_weight, kv_pages, slot_mapping), 1
+
+
+def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
+                         slot_mapping, fmt):
+    """New tokens into the latent cache.  kv bf16 [T, 576] (512 latents, 64
+    elements to rotate; row stride free); positions int32 [T] and cos_sin fp32
+    [P, 64] (both None: stored as they are); norm_weight fp32 [512] (None: no
+    norm); slot_mapping int64 [T], negative skips."""
+    return Prepared("idx_latent_store",
+                    *_latent_store_args(kv, positions, cos_sin, norm_weight, eps, kv_pages,
+                                        page_size, slot_mapping, fmt))
 
 
 def idx_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size, slot_mapping,
                      fmt, stream=None):
-    prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
-                         slot_mapping, fmt)(stream)
+    _run("idx_latent_store", _latent_store_args(kv, positions, cos_sin, norm_weight, eps, kv_pages,
+                                                page_size, slot_mapping, fmt)[0], stream)
 
 
-def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None):
-    """Cached tokens back as rows of out (bf16 [N, 576], row stride free):
-    rows cu_lens[b] .. cu_lens[b + 1] are sequence b's tokens from
-    seq_starts[b] (None: 0) on.  cu_lens int32 [B + 1], seq_starts int32 [B]."""
+def _latent_gather_args(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None):
     pages, stride = _need_pages(kv_pages)
     (rows, _), (ld_out, _) = _need_heads(out, 2, LATENT_DIM + LATENT_ROPE, "out")
     _need(block_table, torch.int32, "block_table")
@@ -696,12 +706,22 @@ def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, s
     args = (_ptr(kv_pages), stride, pages, page_size, fmt, LATENT_DIM, LATENT_ROPE,
             _ptr(block_table), table[1], table[1], _ptr(cu_lens), _ptr(seq_starts), B_, rows,
             _ptr(out), ld_out)
-    return Prepared("idx_latent_gather", args, (kv_pages, block_table, cu_lens, seq_starts, out))
+    return args, (kv_pages, block_table, cu_lens, seq_starts, out), 1
+
+
+def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None):
+    """Cached tokens back as rows of out (bf16 [N, 576], row stride free):
+    rows cu_lens[b] .. cu_lens[b + 1] are sequence b's tokens from
+    seq_starts[b] (None: 0) on.  cu_lens int32 [B + 1], seq_starts int32 [B]."""
+    return Prepared("idx_latent_gather",
+                    *_latent_gather_args(kv_pages, page_size, fmt, block_table, cu_lens, out,
+                                         seq_starts))
 
 
 def idx_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None,
                       stream=None):
-    prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts)(stream)
+    _run("idx_latent_gather", _latent_gather_args(kv_pages, page_size, fmt, block_table, cu_lens,
+                                                  out, seq_starts)[0], stream)
     return out
 
 
@@ -723,13 +743,8 @@ def _latent_ws(workspace, size, rows, heads, device):
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
-def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
-                             workspace=True):
-    """Absorbed latent attention over ragged slots.  q bf16 [R, H, 576] (row
-    and head strides free); slots int32, indptr int32 [R + 1]; out bf16
-    [R, H, 512] and lse fp32 [R, H] are made here when None (lse False:
-    none).  workspace: True allocates the scratch here, or a uint8 tensor of
-    latent_attention_workspace_size(R, H) bytes."""
+def _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
+                           workspace=True):
     (R, H, _), (ldq, ldqh, _) = _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
     pages, stride = _need_pages(kv_pages)
     _need(slots, torch.int32, "slots")
@@ -743,25 +758,34 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
             _ptr(indptr), slots.numel(), R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
             ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
     # the attention, and the joining kernel unless one tile may be all
-    return Prepared("idx_latent_attention", args, (q, kv_pages, slots, indptr, out, lse, ws),
-                    2 if slots.numel() // 64 + R > 1 else 1)
+    kernels = 2 if slots.numel() // 64 + R > 1 else 1
+    return args, (q, kv_pages, slots, indptr, out, lse, ws), kernels
+
+
+def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
+                             workspace=True):
+    """Absorbed latent attention over ragged slots.  q bf16 [R, H, 576] (row
+    and head strides free); slots int32, indptr int32 [R + 1]; out bf16
+    [R, H, 512] and lse fp32 [R, H] are made here when None (lse False:
+    none).  workspace: True allocates the scratch here, or a uint8 tensor of
+    latent_attention_workspace_size(R, H) bytes."""
+    return Prepared("idx_latent_attention",
+                    *_latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out,
+                                            lse, workspace))
 
 
 def idx_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
                          workspace=True, stream=None):
     """(out, lse) of the absorbed attention over ragged slots."""
-    call = prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out, lse,
-                                    workspace)
-    call(stream)
-    return call.keep[4], call.keep[5]
+    args, keep, _ = _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out,
+                                           lse, workspace)
+    _run("idx_latent_attention", args, stream)
+    return keep[4], keep[5]
 
 
-def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
-                                   scale, max_model_len, ctx_per_row=False, out=None, lse=None,
-                                   workspace=True):
-    """Absorbed latent attention over whole paged contexts: row j of sequence
-    b attends to its first context_lens[b] - next_n + j + 1 tokens (or
-    context_lens[row] with ctx_per_row).  q bf16 [B * next_n, H, 576]."""
+def _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
+                                 scale, max_model_len, ctx_per_row=False, out=None, lse=None,
+                                 workspace=True):
     (R, H, _), (ldq, ldqh, _) = _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
     pages, stride = _need_pages(kv_pages)
     _need(block_table, torch.int32, "block_table")
@@ -781,29 +805,35 @@ def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, con
             block_table.shape[1], _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len,
             H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws),
             ws_bytes)
-    return Prepared("idx_paged_latent_attention", args,
-                    (q, kv_pages, block_table, context_lens, out, lse, ws),
-                    2 if B_ * max(1, -(-max_model_len // 64)) > 1 else 1)
+    kernels = 2 if B_ * max(1, -(-max_model_len // 64)) > 1 else 1
+    return args, (q, kv_pages, block_table, context_lens, out, lse, ws), kernels
+
+
+def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
+                                   scale, max_model_len, ctx_per_row=False, out=None, lse=None,
+                                   workspace=True):
+    """Absorbed latent attention over whole paged contexts: row j of sequence
+    b attends to its first context_lens[b] - next_n + j + 1 tokens (or
+    context_lens[row] with ctx_per_row).  q bf16 [B * next_n, H, 576]."""
+    return Prepared("idx_paged_latent_attention",
+                    *_paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table,
+                                                  context_lens, next_n, scale, max_model_len,
+                                                  ctx_per_row, out, lse, workspace))
 
 
 def idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
                                scale, max_model_len, ctx_per_row=False, out=None, lse=None,
                                workspace=True, stream=None):
     """(out, lse) of the absorbed attention over whole paged contexts."""
-    call = prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens,
-                                          next_n, scale, max_model_len, ctx_per_row, out, lse,
-                                          workspace)
-    call(stream)
-    return call.keep[4], call.keep[5]
+    args, keep, _ = _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table,
+                                                 context_lens, next_n, scale, max_model_len,
+                                                 ctx_per_row, out, lse, workspace)
+    _run("idx_paged_latent_attention", args, stream)
+    return keep[4], keep[5]
 
 
-def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
-                           workspace=True):
-    """Expanded latent attention of ragged sequences.  q bf16 [Tq, H, 192]
-    (128, then 64 rotated), k bf16 [Tk, H, 128], k_rope bf16 [Tk, 64], v bf16
-    [Tk, H, 128], every outer stride free; cu_q, cu_k int32 [B + 1]; out bf16
-    [Tq, H, 128], lse fp32 [Tq, H] and workspace as in prepare_latent_attention
-    (the size is latent_prefill_workspace_size(Tq, H))."""
+def _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                         workspace=True):
     (Tq, H, _), (ldq, ldqh, _) = _need_heads(q, 3, 192, "q")
     (Tk, Hk, _), (ldk, ldkh, _) = _need_heads(k, 3, 128, "k")
     (Tr, _), (ldr, _) = _need_heads(k_rope, 2, LATENT_ROPE, "k_rope")
@@ -823,17 +853,28 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
             _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
     # the attention, and the joining kernel unless one share holds everything
     bound = (Tq // 256 + B_) * (Tk // 128 + 2) * H
-    return Prepared("idx_latent_prefill", args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws),
-                    2 if bound >= 4 else 1)
+    return args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws), 2 if bound >= 4 else 1
+
+
+def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                           workspace=True):
+    """Expanded latent attention of ragged sequences.  q bf16 [Tq, H, 192]
+    (128, then 64 rotated), k bf16 [Tk, H, 128], k_rope bf16 [Tk, 64], v bf16
+    [Tk, H, 128], every outer stride free; cu_q, cu_k int32 [B + 1]; out bf16
+    [Tq, H, 128], lse fp32 [Tq, H] and workspace as in prepare_latent_attention
+    (the size is latent_prefill_workspace_size(Tq, H))."""
+    return Prepared("idx_latent_prefill",
+                    *_latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
+                                          workspace))
 
 
 def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
                        workspace=True, stream=None):
     """(out, lse) of the expanded attention of ragged sequences."""
-    call = prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
-                                  workspace)
-    call(stream)
-    return call.keep[6], call.keep[7]
+    args, keep, _ = _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
+                                         workspace)
+    _run("idx_latent_prefill", args, stream)
+    return keep[6], keep[7]
 
 
 def idx_debug_wait_expiry(which: int, limit_ns: int, stream=None):

@@ -72,7 +72,10 @@ struct AttnArgs {
     int64_t ldo_row, ldo_head;
     float *lse;
     int64_t ld_lse;
-    void *ws_place;  // int2 a share: the row and tile it begins at
+    // By row (by_row), or by the share that begins the row: the row, that share,
+    // its pieces (fewer than two: whole), whether a segment lies before it.
+    int4 *ws_cut;
+    int by_row;
     float *ws_part;  // two segments a CTA: O^T, then maxima, then sums
     int page_stride;  // pool.stride in 32 bits: one multiplication
     unsigned int *status;
@@ -556,18 +559,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     const Group group = group_of(a, blockIdx.x);
     const int p = blockIdx.y, shares = min((int)gridDim.y, total);
     const int each = total / shares, more = total - each * shares;
-    int2 *place = reinterpret_cast<int2 *>(a.ws_place);
     // the share's bounds as places in the list and as tiles (a place within a
     // row's charge is its first tile)
     #pragma unroll 1
     for (int e = 0; e < 2; ++e) {
         const int u = (p + e) * each + min(p + e, more);
         if (p + e <= shares && u >= before && u < before + mine) {
-            int q = before, r = r0, n = tiles_of(row_of(a, r).n) + a.charge;
-            #pragma unroll 1
-            while (u >= q + n) {
-                q += n;
-                n = tiles_of(row_of(a, ++r).n) + a.charge;
+            int q = before, r = r0, n = mine;  // of one row, usually
+            if (chunk > 1) {
+                n = tiles_of(row_of(a, r).n) + a.charge;
+                #pragma unroll 1
+                while (u >= q + n) {
+                    q += n;
+                    n = tiles_of(row_of(a, ++r).n) + a.charge;
+                }
             }
             const int t = max(0, u - q - a.charge);
             misc[2 + e] = q - r * a.charge + t;
@@ -577,11 +582,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    if (!a.by_row && blockIdx.x == 0 && tid == 0)
+        a.ws_cut[p] = make_int4(-1, 0, 0, 0);
     __syncthreads();
     const int tiles1 = p + 1 < shares ? (int)misc[3] : total - a.rows * a.charge;
     const int left = p < shares ? tiles1 - (int)misc[2] : 0;
-    if (blockIdx.x == 0 && tid == 0)
-        place[p] = left > 0 ? make_int2(misc[4], misc[5]) : make_int2(-1, 0);
     if (a.hpg * a.rpg < N) {
         // columns without a head: their query rows are zeros
         #pragma unroll 1
@@ -801,6 +806,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 } else {
                     part[kLatent * N + tid] = mm;
                     part[kLatent * N + N + tid] = sum;
+                }
+                if (tid == 0 && blockIdx.x == 0 && s.t0 == 0 && (a.by_row || !whole)) {
+                    // the shares that hold the rest: `more - p - 1` longer ones first
+                    const int rest = s.tiles - s.t1, longer = max(0, more - p - 1);
+                    const int in = min(rest, longer * (each + 1));
+                    a.ws_cut[a.by_row ? s.r : p] = make_int4(
+                        s.r, p, 1 + (in + each) / (each + 1) + (rest - in + each - 1) / each, k > 0);
                 }
             }
             (void)mbar_wait(o_full, k & 1, abort_flag, a.status);
@@ -1049,135 +1061,117 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of a row that several shares hold:
 //     out = sum_q 2^(m_q - m) O_q / sum_q 2^(m_q - m) l_q,   m = max_q m_q.
-// blockIdx.x: the row, or (more rows than shares) a boundary between shares,
-// which acts if it is the first that cuts its row; blockIdx.y: an equal part of
-// the group's slices (128 latents x a quad of columns); blockIdx.z: the group.
-// With few pieces the four groups of 128 threads take a slice each, with many
-// each takes every fourth piece of one, so that the loads are in flight
-// together: the pieces lie in L2 and the kernel is a chain of their latencies.
-constexpr int kJoinThreads = 512;
-constexpr int kJoinFew = 8;
-constexpr int kMaxShares = 152;
+// blockIdx.x: the row's entry of ws_cut; blockIdx.y: a quad of columns (MANY:
+// and 128 latents); blockIdx.z: the group.  The pieces lie in L2, a thousand
+// cycles away or more, so a thread asks for four pieces at once, a thread a
+// latent (of all four tiles of them), and where a row has many, eight teams of
+// threads take four pieces each.
+constexpr int kTeams = 8;
 
-template <int N>
-__global__ void __launch_bounds__(kJoinThreads) latent_join_kernel(const AttnArgs a, int shares)
+template <int N, bool MANY>
+__global__ void __launch_bounds__(MANY ? 128 * kTeams : 128) latent_join_kernel(const AttnArgs a)
 {
     using C = Cfg<N>;
-    constexpr int kRuns = kJoinThreads / N;  // threads a column in the first phase
-    __shared__ int s_first, s_count;
-    __shared__ __align__(16) float wt[kMaxShares * N];  // a piece's weight for each column
-    __shared__ float run[kRuns][N], inv[N];
-    __shared__ float4 part[3][128];
-    const int tid = threadIdx.x, g = blockIdx.z;
-    if (tid == 0) {
-        s_first = INT_MAX;
-        s_count = 0;
-    }
+    constexpr int MT = MANY ? 1 : 4, TEAMS = MANY ? kTeams : 1;
+    __shared__ float4 s_top[TEAMS], s_sum[TEAMS], s_acc[TEAMS][MANY ? 128 : 1];
     pdl_wait();
     pdl_launch_dependents();
-    const int2 *place = reinterpret_cast<const int2 *>(a.ws_place);
-    const bool by_row = a.rows < shares;
-    const int2 mine = tid < shares ? place[tid] : make_int2(-1, 0);
-    const int row = by_row ? (int)blockIdx.x : place[blockIdx.x + 1].x;
-    __syncthreads();
-    // shares that begin inside the row: they and the one before hold its pieces
-    if (tid > 0 && row >= 0 && mine.x == row && mine.y > 0) {
-        atomicMin(&s_first, tid);
-        atomicAdd(&s_count, 1);
-    }
-    __syncthreads();
-    const int first = s_first, pieces = s_count + 1;
-    if (pieces < 2 || (!by_row && first != (int)blockIdx.x + 1))
+    const int4 cut = a.ws_cut[blockIdx.x];
+    const int pieces = cut.z;
+    if (pieces < 2)
         return;
+    const int d = threadIdx.x & 127, team = threadIdx.x >> 7;
+    const int quad = MANY ? blockIdx.y >> 2 : blockIdx.y, mt0 = MANY ? blockIdx.y & 3 : 0;
+    const int64_t step = (int64_t)2 * a.groups * C::PART;
     // a share leaves its first segment at 2 (share, group), its last after it
-    const bool late = place[first - 1].x != row;
-    const auto piece = [&](int q) {
-        const int64_t at = 2 * ((int64_t)(first - 1 + q) * a.groups + g);
-        return a.ws_part + (at + (q == 0 && late)) * C::PART;
-    };
-    const Group group = group_of(a, g);
-    {
-        const int col = tid % N, r = tid / N;
-        float top = -INFINITY;
-        for (int q = r; q < pieces; q += kRuns) {
-            const float m = piece(q)[kLatent * N + col];
-            wt[q * N + col] = m;
-            top = fmaxf(top, m);
-        }
-        run[r][col] = top;
-        __syncthreads();
+    const float *rest = a.ws_part + cut.y * step + (int64_t)blockIdx.z * 2 * C::PART;
+    const int at_m = kLatent * N + 4 * quad, at_o = (mt0 * N + 4 * quad) * 128 + 4 * d;
+    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, sum[4] = {}, acc[MT][4] = {};
+    #pragma unroll 1
+    for (int q0 = 4 * team; q0 < pieces; q0 += 4 * TEAMS) {
+        float4 m[4], l[4], o[4][MT];
         #pragma unroll
-        for (int i = 0; i < kRuns; ++i)
-            top = fmaxf(top, run[i][col]);
-        top = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f;
-        for (int q = r; q < pieces; q += kRuns) {
-            const float w = ex2(wt[q * N + col] - top);
-            wt[q * N + col] = w;
-            sum = fmaf(w, piece(q)[kLatent * N + N + col], sum);
-        }
-        __syncthreads();
-        run[r][col] = sum;
-        __syncthreads();
-        if (r == 0) {
+        for (int i = 0; i < 4; ++i) {
+            const int q = q0 + i;
+            const float *f = rest + (q == 0 ? cut.w * C::PART : q * step);
+            m[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            l[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             #pragma unroll
-            for (int i = 1; i < kRuns; ++i)
-                sum += run[i][col];
-            inv[col] = sum == 0.0f ? 0.0f : 1.0f / sum;
-            int j, h;
-            if (blockIdx.y == 0 && a.lse && column_place(a, group, col, &j, &h))
-                a.lse[((int64_t)row * a.next + j) * a.ld_lse + h] =
-                    sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
-        }
-        __syncthreads();
-    }
-    const int d = tid & 127, team = tid >> 7;
-    const bool few = pieces <= kJoinFew;
-    const int last = (blockIdx.y + 1) * N / gridDim.y;
-    for (int s0 = blockIdx.y * N / gridDim.y; s0 < last; s0 += few ? 4 : 1) {
-        const int slice = s0 + (few ? team : 0), mt = slice & 3, quad = slice >> 2;
-        const int at = (mt * N + 4 * quad) * 128 + 4 * d;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (slice < last) {
-            #pragma unroll 4
-            for (int q = few ? 0 : team; q < pieces; q += few ? 1 : 4) {
-                const float4 v = *reinterpret_cast<const float4 *>(piece(q) + at);
-                const float4 u = *reinterpret_cast<const float4 *>(wt + q * N + 4 * quad);
-                acc.x = fmaf(u.x, v.x, acc.x);
-                acc.y = fmaf(u.y, v.y, acc.y);
-                acc.z = fmaf(u.z, v.z, acc.z);
-                acc.w = fmaf(u.w, v.w, acc.w);
-            }
-        }
-        if (!few) {
-            if (team > 0)
-                part[team - 1][d] = acc;
-            __syncthreads();
-            if (team == 0) {
+            for (int x = 0; x < MT; ++x)
+                o[i][x] = l[i];
+            if (q < pieces) {
+                m[i] = *reinterpret_cast<const float4 *>(f + at_m);
+                l[i] = *reinterpret_cast<const float4 *>(f + at_m + N);
                 #pragma unroll
-                for (int i = 0; i < 3; ++i) {
-                    acc.x += part[i][d].x;
-                    acc.y += part[i][d].y;
-                    acc.z += part[i][d].z;
-                    acc.w += part[i][d].w;
-                }
+                for (int x = 0; x < MT; ++x)
+                    o[i][x] = *reinterpret_cast<const float4 *>(f + at_o + x * N * 128);
             }
         }
-        if (slice < last && (few || team == 0)) {
-            const float y[4] = {acc.x, acc.y, acc.z, acc.w};
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const auto of = [e](const float4 &v) {
+                return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+            };
+            const float nt = fmaxf(fmaxf(fmaxf(of(m[0]), of(m[1])), fmaxf(of(m[2]), of(m[3]))), top[e]);
+            const float ref = nt == -INFINITY ? 0.0f : nt;
+            const float c = ex2(top[e] - ref);
+            top[e] = nt;
+            sum[e] *= c;
             #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                int j, h;
-                if (!column_place(a, group, 4 * quad + e, &j, &h))
-                    continue;
-                const int64_t r = (int64_t)row * a.next + j;
-                reinterpret_cast<__nv_bfloat16 *>(
-                    a.out)[r * a.ldo_row + h * a.ldo_head + 128 * mt + d] =
-                    __float2bfloat16(y[e] * inv[4 * quad + e]);
+            for (int x = 0; x < MT; ++x)
+                acc[x][e] *= c;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = ex2(of(m[i]) - ref);
+                sum[e] = fmaf(w, of(l[i]), sum[e]);
+                #pragma unroll
+                for (int x = 0; x < MT; ++x)
+                    acc[x][e] = fmaf(w, of(o[i][x]), acc[x][e]);
             }
         }
-        if (!few)
-            __syncthreads();  // part is written again
+    }
+    if constexpr (MANY) {
+        s_acc[team][d] = make_float4(acc[0][0], acc[0][1], acc[0][2], acc[0][3]);
+        if (d == 0) {
+            s_top[team] = make_float4(top[0], top[1], top[2], top[3]);
+            s_sum[team] = make_float4(sum[0], sum[1], sum[2], sum[3]);
+        }
+        __syncthreads();
+        if (team > 0)
+            return;
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            top[e] = -INFINITY;
+            #pragma unroll
+            for (int i = 0; i < TEAMS; ++i)
+                top[e] = fmaxf(top[e], reinterpret_cast<const float *>(&s_top[i])[e]);
+            const float ref = top[e] == -INFINITY ? 0.0f : top[e];
+            sum[e] = acc[0][e] = 0.0f;
+            #pragma unroll
+            for (int i = 0; i < TEAMS; ++i) {
+                const float w = ex2(reinterpret_cast<const float *>(&s_top[i])[e] - ref);
+                sum[e] = fmaf(w, reinterpret_cast<const float *>(&s_sum[i])[e], sum[e]);
+                acc[0][e] = fmaf(w, reinterpret_cast<const float *>(&s_acc[i][d])[e], acc[0][e]);
+            }
+        }
+    }
+    const Group group = group_of(a, blockIdx.z);
+    #pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        int j, h;
+        if (!column_place(a, group, 4 * quad + e, &j, &h))
+            continue;
+        const int64_t r = (int64_t)cut.x * a.next + j;
+        __nv_bfloat16 *to = reinterpret_cast<__nv_bfloat16 *>(a.out) + r * a.ldo_row +
+                            h * a.ldo_head + 128 * mt0 + d;
+        const float inv = sum[e] == 0.0f ? 0.0f : 1.0f / sum[e];
+        #pragma unroll
+        for (int x = 0; x < MT; ++x)
+            to[128 * x] = __float2bfloat16(acc[x][e] * inv);
+        if (a.lse && mt0 == 0 && d == 0)
+            a.lse[r * a.ld_lse + h] =
+                sum[e] == 0.0f ? -INFINITY
+                               : ((top[e] == -INFINITY ? 0.0f : top[e]) + log2f(sum[e])) * kLn2;
     }
 }
 
@@ -1186,9 +1180,9 @@ int columns_of(int n)
     return n <= 16 ? 16 : n <= 32 ? 32 : 64;
 }
 
-size_t place_bytes()
+size_t cut_bytes()
 {
-    return ((size_t)sm_count() * sizeof(int2) + 255) / 256 * 256;
+    return ((size_t)sm_count() * sizeof(int4) + 255) / 256 * 256;
 }
 
 template <int N, bool FP8>
@@ -1209,13 +1203,15 @@ idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int shares, cud
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     cudaError_t e = launch_pdl(kern, dim3(a.groups, shares), dim3(kThreads), C::SMEM, s, tm, a);
-    if (e == cudaSuccess && shares > 1)
-    {
-        // a few CTAs per SM over all rows that may be cut
-        const int rows = std::min(a.rows, shares - 1) * a.groups;
-        const int parts = std::min(N, std::max(2, 4 * sm_count() / rows));
-        e = launch_pdl(latent_join_kernel<N>, dim3(rows / a.groups, parts, a.groups),
-                       dim3(kJoinThreads), 0, s, a, shares);
+    if (e == cudaSuccess && shares > 1) {
+        const int entries = a.by_row ? a.rows : shares - 1;
+        // teams from about eight pieces a row on
+        if (shares >= 8 * a.rows)
+            e = launch_pdl(latent_join_kernel<N, true>, dim3(entries, N, a.groups),
+                           dim3(128 * kTeams), 0, s, a);
+        else
+            e = launch_pdl(latent_join_kernel<N, false>, dim3(entries, N / 4, a.groups), dim3(128),
+                           0, s, a);
     }
     return launch_status(e);
 }
@@ -1258,11 +1254,12 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
         return IDX_ERR_UNSUPPORTED;
     a.page_stride = (int)a.pool.stride;
     const int n = columns_of(a.hpg * a.rpg);
-    a.ws_place = ws;
-    a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + place_bytes());
+    a.ws_cut = static_cast<int4 *>(ws);
+    a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + cut_bytes());
     // one CTA per SM, the same number for every group
     const int shares =
-        (int)std::min<int64_t>(std::min(sm_count(), kMaxShares) / a.groups, most);
+        (int)std::min<int64_t>(sm_count() / a.groups, most);
+    a.by_row = a.rows < shares;
     // the end of a row (its sums, its output, the next row's first scores) costs
     // a CTA about as much as this many tiles; short shares are left equal
     a.charge = most >= 8ll * shares ? (n == 64 ? 3 : 2) : 0;
@@ -1294,7 +1291,7 @@ extern "C" size_t idx_latent_attention_workspace_size(int R, int H)
     // at most a CTA per SM, each with two segments of at most 64 columns (which
     // rows of a sequence share whatever H is)
     const int64_t columns = columns_of((int)std::min<int64_t>(64, (int64_t)R * H));
-    return place_bytes() + (size_t)(2 * sm_count() * (kLatent + 2) * columns) * sizeof(float);
+    return cut_bytes() + (size_t)(2 * sm_count() * (kLatent + 2) * columns) * sizeof(float);
 }
 
 extern "C" idx_status idx_latent_attention(

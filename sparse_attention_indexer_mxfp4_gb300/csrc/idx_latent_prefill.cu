@@ -72,7 +72,8 @@ struct PrefillArgs {
     int64_t ldo_row, ldo_head;
     float *lse;
     int64_t ld_lse;
-    int4 *ws_place;  // a share's first head, sequence, block, tile
+    int4 *ws_cut;    // two a share: the block it begins and leaves to the next (head, sequence,
+                     // block, pieces; no pieces: none), whether a segment lies before it
     float *ws_part;  // two segments a share: for each query tile O, maxima, sums
     unsigned int *status;
 };
@@ -270,6 +271,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ck = cu + kMaxCu + 1;
     }
     __syncthreads();
+    if (tid == 0)
+        a.ws_cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
     int *wsum = misc + 4;
     const auto seq_tiles = [&](int b) {
         Block k;
@@ -346,8 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.t = max(0, rest - kCharge);
         w.pay = max(0, kCharge - rest);
     }
-    if (tid == 0)
-        a.ws_place[p] = w.left > w.pay ? make_int4(w.k.head, w.k.b, w.k.i, w.t) : make_int4(-1, 0, 0, 0);
     Seg s;
 
     if (warp < kWarpLoad) {
@@ -465,6 +466,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                             *reinterpret_cast<uint4 *>(part + (c + e) * kTile + r4) =
                                 make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
                     }
+                }
+                if (tid == 0 && s.t0 == 0) {
+                    // the shares that hold the rest: `more - p - 1` longer ones first
+                    const int rest = s.tiles - s.t1, longer = max(0, more - p - 1);
+                    const int in = min(rest, longer * (each + 1));
+                    a.ws_cut[2 * p] = make_int4(
+                        s.k.head, s.k.b, s.k.i,
+                        1 + (in + each) / (each + 1) + (rest - in + each - 1) / each);
+                    a.ws_cut[2 * p + 1] = make_int4(seg > 0, 0, 0, 0);
                 }
                 part[kTile * kV + (tid & 127)] = m;
                 part[kTile * kV + kTile + (tid & 127)] = l;
@@ -701,71 +711,56 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins the partial results of a block that several shares hold, as the
-// absorbed kernel's: blockIdx.x is the boundary between shares (+ 1), which
-// acts if it is the first that cuts its block; blockIdx.y: the query tile and
-// a quarter of the 128 elements.  A thread a row.
-__global__ void __launch_bounds__(kTile) latent_prefill_join_kernel(const PrefillArgs a, int shares)
+// absorbed kernel's: blockIdx.x is the share that begins the block,
+// blockIdx.y the query tile and an eighth of the 128 elements.  A thread a row.
+constexpr int kJoinDims = 16;
+
+__global__ void __launch_bounds__(kTile) latent_prefill_join_kernel(const PrefillArgs a)
 {
     pdl_wait();
     pdl_launch_dependents();
-    const auto same = [](const int4 &x, const int4 &y) {
-        return x.x == y.x && x.y == y.y && x.z == y.z;
-    };
-    const int first = blockIdx.x + 1;
-    const int4 here = a.ws_place[first], prev = a.ws_place[first - 1];
-    if (here.x < 0 || here.w == 0 || (same(here, prev) && prev.w > 0))
+    const int4 cut = a.ws_cut[2 * blockIdx.x];
+    const int pieces = cut.w;
+    if (pieces < 2)
         return;
-    int pieces = 1;  // shares first, first + 1, .. that begin inside the block
-    for (int b = first; b < shares; b += kTile) {
-        const int c = b + (int)threadIdx.x;
-        bool in = false;
-        if (c < shares) {
-            const int4 x = a.ws_place[c];
-            in = same(x, here) && x.w > 0;
-        }
-        pieces += __syncthreads_count(in);
-    }
+    constexpr int kParts = kV / kJoinDims;
+    const int q = blockIdx.y / kParts, c0 = kJoinDims * (blockIdx.y % kParts), t = threadIdx.x;
     Block k;
-    k.head = here.x;
-    k.b = here.y;
-    k.i = here.z;
+    k.b = cut.y;
     block_seq(a, a.cu_q, a.cu_k, k);
-    const int q = blockIdx.y >> 2, c0 = 32 * (blockIdx.y & 3);
-    const int t = threadIdx.x, row = k.i * kRows + q * kTile + t;
+    const int row = cut.z * kRows + q * kTile + t;
     if (row >= k.nq)
         return;
     // a share leaves its first segment at 2 p, its last after it
-    const bool late = !same(here, prev);
-    const auto piece = [&](int i) {
-        return a.ws_part +
-               ((int64_t)(2 * (first - 1 + i) + (i == 0 && late)) * 2 + q) * kPartTile;
-    };
+    constexpr int64_t step = 4 * kPartTile;
+    const float *rest = a.ws_part + blockIdx.x * step + q * kPartTile;
+    const float *first = rest + a.ws_cut[2 * blockIdx.x + 1].x * 2 * kPartTile;
     float top = -INFINITY;
     #pragma unroll 4
     for (int i = 0; i < pieces; ++i)
-        top = fmaxf(top, piece(i)[kTile * kV + t]);
+        top = fmaxf(top, (i == 0 ? first : rest + i * step)[kTile * kV + t]);
     top = top == -INFINITY ? 0.0f : top;
-    float acc[32] = {}, sum = 0.0f;
+    float acc[kJoinDims] = {}, sum = 0.0f;
+    #pragma unroll 2
     for (int i = 0; i < pieces; ++i) {
-        const float *f = piece(i);
-        const float l = f[kTile * kV + kTile + t];
-        const float wt = ex2(f[kTile * kV + t] - top);
-        if (l == 0.0f)
-            continue;  // no key here: its O was not written
-        sum = fmaf(wt, l, sum);
+        const float *f = i == 0 ? first : rest + i * step;
+        const float l = f[kTile * kV + kTile + t], w = ex2(f[kTile * kV + t] - top);
+        sum = fmaf(w, l, sum);
         #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float4 v = *reinterpret_cast<const float4 *>(f + (c0 + 4 * e) * kTile + 4 * t);
-            acc[4 * e] = fmaf(wt, v.x, acc[4 * e]);
-            acc[4 * e + 1] = fmaf(wt, v.y, acc[4 * e + 1]);
-            acc[4 * e + 2] = fmaf(wt, v.z, acc[4 * e + 2]);
-            acc[4 * e + 3] = fmaf(wt, v.w, acc[4 * e + 3]);
+        for (int e = 0; e < kJoinDims; e += 4) {
+            float4 v = *reinterpret_cast<const float4 *>(f + (c0 + e) * kTile + 4 * t);
+            if (l == 0.0f)  // no key here: O was not written
+                v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            acc[e] = fmaf(w, v.x, acc[e]);
+            acc[e + 1] = fmaf(w, v.y, acc[e + 1]);
+            acc[e + 2] = fmaf(w, v.z, acc[e + 2]);
+            acc[e + 3] = fmaf(w, v.w, acc[e + 3]);
         }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    __nv_bfloat16 *to = a.out + (int64_t)(k.seq_q + row) * a.ldo_row + k.head * a.ldo_head + c0;
+    __nv_bfloat16 *to = a.out + (int64_t)(k.seq_q + row) * a.ldo_row + cut.x * a.ldo_head + c0;
     #pragma unroll
-    for (int e = 0; e < 32; e += 8) {
+    for (int e = 0; e < kJoinDims; e += 8) {
         uint32_t v[4];
         #pragma unroll
         for (int x = 0; x < 4; ++x)
@@ -773,13 +768,13 @@ __global__ void __launch_bounds__(kTile) latent_prefill_join_kernel(const Prefil
         *reinterpret_cast<uint4 *>(to + e) = make_uint4(v[0], v[1], v[2], v[3]);
     }
     if (a.lse && c0 == 0)
-        a.lse[(int64_t)(k.seq_q + row) * a.ld_lse + k.head] =
+        a.lse[(int64_t)(k.seq_q + row) * a.ld_lse + cut.x] =
             sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
-size_t place_bytes()
+size_t cut_bytes()
 {
-    return ((size_t)kMaxShares * sizeof(int4) + 255) / 256 * 256;
+    return ((size_t)2 * kMaxShares * sizeof(int4) + 255) / 256 * 256;
 }
 
 // bf16 [rows, H, dim] with these strides (elements) as bytes; boxes of 64
@@ -803,7 +798,7 @@ extern "C" size_t idx_latent_prefill_workspace_size(int Tq, int H)
 {
     if (Tq <= 0 || H <= 0)
         return 0;
-    return place_bytes() + (size_t)2 * kMaxShares * 2 * kPartTile * sizeof(float);
+    return cut_bytes() + (size_t)2 * kMaxShares * 2 * kPartTile * sizeof(float);
 }
 
 extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
@@ -868,8 +863,8 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
     a.status = device_status_ptr();
     if (!a.status)
         return IDX_ERR_CUDA;
-    a.ws_place = static_cast<int4 *>(ws);
-    a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + place_bytes());
+    a.ws_cut = static_cast<int4 *>(ws);
+    a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + cut_bytes());
     static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
@@ -886,7 +881,7 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
     cudaError_t e = launch_pdl(latent_prefill_kernel, dim3(shares), dim3(kThreads), kSmem,
                                (cudaStream_t)stream, tq, tk, tr, tv, a);
     if (e == cudaSuccess && shares > 1)
-        e = launch_pdl(latent_prefill_join_kernel, dim3(shares - 1, 8), dim3(kTile), 0,
-                       (cudaStream_t)stream, a, shares);
+        e = launch_pdl(latent_prefill_join_kernel, dim3(shares - 1, 2 * kV / kJoinDims), dim3(kTile),
+                       0, (cudaStream_t)stream, a);
     return launch_status(e);
 }

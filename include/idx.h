@@ -586,7 +586,8 @@ idx_status idx_latent_gather(const uint8_t *kv_pages, int64_t page_stride_bytes,
  *   lse       fp32 [R, ld_lse] natural logarithm of the sum of exp(s), or
  *             NULL.  A row with no token gets zeros and -inf.
  *   ws, ws_bytes  device scratch, 16-byte aligned, of at least
- *             idx_latent_attention_workspace_size(R, H) bytes.  Calls that
+ *             idx_latent_attention_workspace_size(R, H, num_slots) bytes
+ *             (the paged form: max_model_len); NULL where that is 0.  Calls that
  *             share one ws must not overlap in time.
  * A slot outside the pool is left out of its row and sets IDX_DEV_BAD_PAGE.
  * The sums run in fp32, the weights enter the second product in bf16; the
@@ -622,8 +623,10 @@ idx_status idx_paged_latent_attention(const uint16_t *q, int64_t ldq_row, int64_
                                       int64_t ldo_head, float *lse, int64_t ld_lse, void *ws,
                                       size_t ws_bytes, idx_stream_t stream);
 
-/* Bytes of ws for R rows of H heads on the current device (its SM count). */
-size_t idx_latent_attention_workspace_size(int R, int H);
+/* Bytes of ws for R rows of H heads on the current device (its SM count), where
+ * no row has more than max_keys keys (num_slots, or max_model_len); 0 where they
+ * are so few that rows are not split. */
+size_t idx_latent_attention_workspace_size(int R, int H, int64_t max_keys);
 
 /* ------------------------------------------------------------------------
  * idx_latent_prefill -- the expanded form: attention of ragged sequences
@@ -644,7 +647,7 @@ size_t idx_latent_attention_workspace_size(int R, int H);
  *           A query with no key gets zeros and -inf; rows of q outside every
  *           sequence are not written.
  *   ws, ws_bytes  device scratch as for idx_latent_attention, of
- *           idx_latent_prefill_workspace_size(Tq, H) bytes.
+ *           idx_latent_prefill_workspace_size(Tq, Tk, H) bytes.
  * Every stride is a multiple of 8 elements and every pointer 16-byte
  * aligned.  Keys and values past a sequence's end (another sequence's) never
  * enter its results, whatever they hold; within a sequence a value that is
@@ -660,8 +663,9 @@ idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_he
                               int64_t ldo_row, int64_t ldo_head, float *lse, int64_t ld_lse,
                               void *ws, size_t ws_bytes, idx_stream_t stream);
 
-/* Bytes of ws for Tq query rows of H heads. */
-size_t idx_latent_prefill_workspace_size(int Tq, int H);
+/* Bytes of ws for Tq query rows of H heads on Tk key rows; 0 where these are so
+ * few that queries are not split over the keys. */
+size_t idx_latent_prefill_workspace_size(int Tq, int Tk, int H);
 
 /* ------------------------------------------------------------------------
  * idx_get_device_status -- read and clear the sticky device status word of

@@ -8,6 +8,7 @@ library raises at import of this module's first call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -102,9 +103,9 @@ def lib() -> ctypes.CDLL:
             L.idx_version.restype = ctypes.c_char_p
             L.idx_topk_workspace_size.argtypes = [_I, _L, _I]
             L.idx_topk_workspace_size.restype = _S
-            L.idx_latent_attention_workspace_size.argtypes = [_I, _I]
+            L.idx_latent_attention_workspace_size.argtypes = [_I, _I, _L]
             L.idx_latent_attention_workspace_size.restype = _S
-            L.idx_latent_prefill_workspace_size.argtypes = [_I, _I]
+            L.idx_latent_prefill_workspace_size.argtypes = [_I, _I, _I]
             L.idx_latent_prefill_workspace_size.restype = _S
             L.idx_paged_mqa_logits_workspace_size.argtypes = [_I, _I, _I, _I]
             L.idx_paged_mqa_logits_workspace_size.restype = _S
@@ -175,6 +176,12 @@ def _run(name, args, stream):
     rc = getattr(_lib or lib(), name)(*args, _stream(stream))
     if rc != IDX_OK:
         _check(rc, name)
+
+
+def _on(stream):
+    """The context a call's outputs and scratch are made in: memory of the
+    current stream may still be in use there when another stream writes it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def prepare_mqa_logits(q, q_scale, weights, k, k_scale, row_ks, row_ke, fmt, logits):
@@ -725,21 +732,21 @@ def idx_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_s
     return out
 
 
-def latent_attention_workspace_size(rows, heads) -> int:
-    """Bytes of device scratch of the absorbed attention on the current device."""
-    return int(lib().idx_latent_attention_workspace_size(rows, heads))
+def latent_attention_workspace_size(rows, heads, max_keys) -> int:
+    """Bytes of device scratch of the absorbed attention on the current device
+    for rows of at most max_keys keys (0: none needed)."""
+    return int(lib().idx_latent_attention_workspace_size(rows, heads, max_keys))
 
 
-def latent_prefill_workspace_size(rows, heads) -> int:
-    """Bytes of device scratch of the expanded attention."""
-    return int(lib().idx_latent_prefill_workspace_size(rows, heads))
+def latent_prefill_workspace_size(rows, keys, heads) -> int:
+    """Bytes of device scratch of the expanded attention (0: none needed)."""
+    return int(lib().idx_latent_prefill_workspace_size(rows, keys, heads))
 
 
-def _latent_ws(workspace, size, rows, heads, device):
+def _latent_ws(workspace, size, device):
     """The scratch of an attention call and its bytes."""
     if workspace is True:
-        n = size(rows, heads)
-        return torch.empty(n, dtype=torch.uint8, device=device), n
+        return (torch.empty(size, dtype=torch.uint8, device=device), size) if size else (None, 0)
     return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
@@ -753,13 +760,14 @@ def _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, ou
         raise ValueError(f"indptr must hold {R + 1} entries")
     device = q.device
     out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
-    ws, ws_bytes = _latent_ws(workspace, lib().idx_latent_attention_workspace_size, R, H, device)
+    n = slots.numel()
+    size = lib().idx_latent_attention_workspace_size(R, H, n)
+    ws, ws_bytes = _latent_ws(workspace, size, device)
     args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(slots),
-            _ptr(indptr), slots.numel(), R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
+            _ptr(indptr), n, R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
             ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
-    # the attention, and the joining kernel unless one tile may be all
-    kernels = 2 if slots.numel() // 64 + R > 1 else 1
-    return args, (q, kv_pages, slots, indptr, out, lse, ws), kernels
+    # the attention, and with scratch the joining kernel
+    return args, (q, kv_pages, slots, indptr, out, lse, ws), 2 if size else 1
 
 
 def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
@@ -768,7 +776,7 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
     and head strides free); slots int32, indptr int32 [R + 1]; out bf16
     [R, H, 512] and lse fp32 [R, H] are made here when None (lse False:
     none).  workspace: True allocates the scratch here, or a uint8 tensor of
-    latent_attention_workspace_size(R, H) bytes."""
+    latent_attention_workspace_size(R, H, slots.numel()) bytes."""
     return Prepared("idx_latent_attention",
                     *_latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out,
                                             lse, workspace))
@@ -777,9 +785,10 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
 def idx_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
                          workspace=True, stream=None):
     """(out, lse) of the absorbed attention over ragged slots."""
-    args, keep, _ = _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out,
-                                           lse, workspace)
-    _run("idx_latent_attention", args, stream)
+    with _on(stream):
+        args, keep, _ = _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale,
+                                               out, lse, workspace)
+        _run("idx_latent_attention", args, None)
     return keep[4], keep[5]
 
 
@@ -800,13 +809,13 @@ def _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table, conte
         raise ValueError(f"block_table must be [{B_}, blocks]")
     device = q.device
     out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
-    ws, ws_bytes = _latent_ws(workspace, lib().idx_latent_attention_workspace_size, R, H, device)
+    size = lib().idx_latent_attention_workspace_size(R, H, max_model_len)
+    ws, ws_bytes = _latent_ws(workspace, size, device)
     args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(block_table),
             block_table.shape[1], _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len,
             H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws),
             ws_bytes)
-    kernels = 2 if B_ * max(1, -(-max_model_len // 64)) > 1 else 1
-    return args, (q, kv_pages, block_table, context_lens, out, lse, ws), kernels
+    return args, (q, kv_pages, block_table, context_lens, out, lse, ws), 2 if size else 1
 
 
 def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
@@ -825,10 +834,11 @@ def idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context
                                scale, max_model_len, ctx_per_row=False, out=None, lse=None,
                                workspace=True, stream=None):
     """(out, lse) of the absorbed attention over whole paged contexts."""
-    args, keep, _ = _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table,
-                                                 context_lens, next_n, scale, max_model_len,
-                                                 ctx_per_row, out, lse, workspace)
-    _run("idx_paged_latent_attention", args, stream)
+    with _on(stream):
+        args, keep, _ = _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table,
+                                                     context_lens, next_n, scale, max_model_len,
+                                                     ctx_per_row, out, lse, workspace)
+        _run("idx_paged_latent_attention", args, None)
     return keep[4], keep[5]
 
 
@@ -847,13 +857,12 @@ def _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=No
         raise ValueError("cu_q and cu_k must both hold B + 1 entries")
     device = q.device
     out, lse, ldo, ldoh, ldl = _out_lse(out, lse, Tq, H, 128, device)
-    ws, ws_bytes = _latent_ws(workspace, lib().idx_latent_prefill_workspace_size, Tq, H, device)
+    size = lib().idx_latent_prefill_workspace_size(Tq, Tk, H)
+    ws, ws_bytes = _latent_ws(workspace, size, device)
     args = (_ptr(q), ldq, ldqh, _ptr(k), ldk, ldkh, _ptr(k_rope), ldr, _ptr(v), ldv, ldvh,
             _ptr(cu_q), _ptr(cu_k), B_, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal),
             _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
-    # the attention, and the joining kernel unless one share holds everything
-    bound = (Tq // 256 + B_) * (Tk // 128 + 2) * H
-    return args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws), 2 if bound >= 4 else 1
+    return args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws), 2 if size else 1
 
 
 def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
@@ -862,7 +871,7 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
     (128, then 64 rotated), k bf16 [Tk, H, 128], k_rope bf16 [Tk, 64], v bf16
     [Tk, H, 128], every outer stride free; cu_q, cu_k int32 [B + 1]; out bf16
     [Tq, H, 128], lse fp32 [Tq, H] and workspace as in prepare_latent_attention
-    (the size is latent_prefill_workspace_size(Tq, H))."""
+    (the size is latent_prefill_workspace_size(Tq, Tk, H))."""
     return Prepared("idx_latent_prefill",
                     *_latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
                                           workspace))
@@ -871,9 +880,10 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
 def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
                        workspace=True, stream=None):
     """(out, lse) of the expanded attention of ragged sequences."""
-    args, keep, _ = _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
-                                         workspace)
-    _run("idx_latent_prefill", args, stream)
+    with _on(stream):
+        args, keep, _ = _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
+                                             workspace)
+        _run("idx_latent_prefill", args, None)
     return keep[6], keep[7]
 
 

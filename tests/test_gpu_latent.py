@@ -201,9 +201,10 @@ def _check_sparse(pool, fmt, page, slots, indptr, q, out, lse, rows=None):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("H", [1, 3, 8, 16, 17, 32, 40, 64, 65, 96, 128])
-def test_sparse_heads(fmt, H):
+@pytest.mark.parametrize("longest", [130, 700])  # rows that stay whole, and a row cut into pieces
+def test_sparse_heads(fmt, H, longest):
     rng = np.random.default_rng(H)
-    pool, slots, indptr, qt, q = _sparse_case(rng, fmt, [130, 0, 64, 1], H, 64)
+    pool, slots, indptr, qt, q = _sparse_case(rng, fmt, [longest, 0, 64, 1], H, 64)
     out, lse = B.idx_latent_attention(qt, _dev(pool), 64, fmt, _dev(slots), _dev(indptr), SCALE)
     _clean()
     _check_sparse(pool, fmt, 64, slots, indptr, q, out, lse)
@@ -253,7 +254,7 @@ def test_sparse_strides_outputs_and_repeats(fmt):
     big, q = _bf16(rng.standard_normal((3, 30, 584)))
     o = torch.full((3, 30, 520), 3.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full((3, 28), 3.0, device="cuda")
-    ws = torch.empty(B.latent_attention_workspace_size(3, 24) + 8, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(B.latent_attention_workspace_size(3, 24, 300) + 8, dtype=torch.uint8, device="cuda")
     got, gl = B.idx_latent_attention(big[:, 2:26, :576], _dev(pool), 64, fmt, _dev(slots), _dev(indptr), SCALE,
                                      out=o[:, 3:27, :512], lse=lse[:, :24], workspace=ws)
     _clean()
@@ -375,6 +376,10 @@ def test_same_bits_again_other_stream_and_graph(fmt):
         call()
     side.synchronize()
     assert torch.equal(call.keep[4], first) and torch.equal(call.keep[5], lse)
+    for _ in range(3):  # outputs and scratch made for the stream they are written on
+        other, _ = B.idx_latent_attention(*args, stream=side)
+        side.synchronize()
+        assert torch.equal(other, first)
     call.keep[4].zero_()
     g = torch.cuda.CUDAGraph()
     torch.cuda.synchronize()

@@ -87,7 +87,7 @@ def test_gather_refusals():
 
 
 def test_attention_refusals():
-    base = [FAKE, 64 * 576, 576, FAKE, 41472, 10, 64, 1, FAKE, FAKE, 100, 4, 64, 512, 64, 0.1, FAKE,
+    base = [FAKE, 64 * 576, 576, FAKE, 41472, 10, 64, 1, FAKE, FAKE, 1000, 4, 64, 512, 64, 0.1, FAKE,
             64 * 512, 512, FAKE, 64, FAKE, 1 << 30, None]
     p = dict(q=0, qr=1, qh=2, pages=3, stride=4, np=5, P=6, fmt=7, slots=8, indptr=9, ns=10, R=11, H=12,
              L=13, rope=14, scale=15, out=16, outr=17, oh=18, lse=19, ldl=20, ws=21, wsb=22)
@@ -100,7 +100,7 @@ def test_attention_refusals():
     for kw in (dict(H=129, ldl=129), dict(L=256), dict(rope=0), dict(q=FAKE + 2), dict(qr=64 * 576 + 4),
                dict(qh=580), dict(out=FAKE + 8), dict(outr=4), dict(pages=FAKE + 8)):
         assert call(**kw) == UNSUPPORTED, kw
-    assert call(ws=None) == WORKSPACE and call(wsb=0) == WORKSPACE
+    assert call(ws=None) == WORKSPACE and call(wsb=0) == WORKSPACE and call(ws=FAKE + 8) == WORKSPACE
 
 
 def test_paged_attention_refusals():
@@ -117,7 +117,7 @@ def test_paged_attention_refusals():
 
 def test_prefill_refusals():
     base = [FAKE, 64 * 192, 192, FAKE, 64 * 256, 256, FAKE, 576, FAKE, 64 * 256, 256, FAKE, FAKE, 2, 100,
-            100, 64, 128, 64, 128, 0.1, 1, FAKE, 64 * 128, 128, FAKE, 64, FAKE, 1 << 30, None]
+            1000, 64, 128, 64, 128, 0.1, 1, FAKE, 64 * 128, 128, FAKE, 64, FAKE, 1 << 30, None]
     p = dict(q=0, qr=1, qh=2, k=3, kr=4, kh=5, rope=6, ldr=7, v=8, vr=9, vh=10, cq=11, ck=12, B=13, Tq=14,
              Tk=15, H=16, dn=17, dr=18, dv=19, scale=20, out=22, outr=23, oh=24, lse=25, ldl=26, ws=27, wsb=28)
     call = _caller("idx_latent_prefill", base, p)
@@ -171,5 +171,5 @@ def test_binding_refusals():
 def test_workspace_size_of_nothing():
     f = B.lib().idx_latent_attention_workspace_size
     g = B.lib().idx_latent_prefill_workspace_size
-    assert g(0, 64) == 0 and g(4, 0) == 0 and g(1, 1) > 0
-    assert f(0, 64) == 0 and f(4, 0) == 0 and isinstance(f(1, 1), int) and ctypes.sizeof(ctypes.c_size_t) == 8
+    assert g(0, 999, 64) == 0 and g(4, 999, 0) == 0 and g(9, 64, 4) == 0 and g(1, 999, 1) > 0
+    assert f(0, 64, 999) == 0 and f(4, 0, 999) == 0 and f(4, 64, 64) == 0 and isinstance(f(1, 1, 999), int) and ctypes.sizeof(ctypes.c_size_t) == 8

@@ -245,13 +245,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&full[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&tail[i], 1);
-            mbar_init(&k_free[i], 1);
+            mbar_init(&k_free[i], 4);
             mbar_init(&v_free[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], 4);
             mbar_init(&pv_done[i], 1);
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_free[i], 1);
+            mbar_init(&q_free[i], 4);
         }
         mbar_init(drain, 1);
         *abort_flag = 0;
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t col_s = tmem + lanes + kColS + q * 128, col_o = tmem + lanes + kColO + q * 128;
         const float sl = a.scale_log2;
-        int i = 0;  // tiles of this query tile so far
+        int i = 0, n = 0, segs = 0;  // tiles of this query tile, of both, its segments so far
         for (int seg = 0; next_seg(a, cq, ck, w, s); ++seg) {
             const int row = s.k.i * kRows + q * kTile + (tid & 127);
             // rows past the sequence's queries take part with no key
@@ -388,6 +388,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 (void)mbar_wait_here(&s_full[q], i & 1, abort_flag, a.status);
                 __syncwarp();
                 tc_fence_after();
+                // the keys are free after the tile's last S, the queries after
+                // the segment's
+                if (lane == 0 && (q == 1 || s.nt[1] <= j))
+                    mbar_arrive(&k_free[(n + j - s.t0) & 1]);
+                if (lane == 0 && j + 1 == t1)
+                    mbar_arrive(&q_free[q]);
                 uint32_t r[4][32];
                 #pragma unroll
                 for (int c = 0; c < 4; ++c)
@@ -418,9 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = nm;
                     l *= al;
                     if (j > s.t0) {
-                        (void)mbar_wait_here(&pv_done[q], (i - 1) & 1, abort_flag, a.status);
-                        __syncwarp();
-                        tc_fence_after();
+                        // O is complete: S was issued after its last product, and
+                        // a commit covers all that its thread issued before
                         #pragma unroll 1
                         for (int c = 0; c < 128; c += 16) {
                             uint32_t o[16];
@@ -461,8 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the segment's sums
             const bool some = t1 > s.t0;
+            n += max(0, min(s.t1, max(s.nt[0], s.nt[1])) - s.t0);
             if (some) {
-                (void)mbar_wait_here(&pv_done[q], (i - 1) & 1, abort_flag, a.status);
+                (void)mbar_wait_here(&pv_done[q], segs & 1, abort_flag, a.status);
+                ++segs;
                 __syncwarp();
                 tc_fence_after();
             }
@@ -635,9 +642,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n0 = 0;            // tiles before the segment
         int fills = 0;         // parity of the segments that each query tile had, a bit each
         int done0 = 0, done1 = 0;  // tiles of each query tile before the segment
-        // S of query tile q and the segment's k-th key tile; the last query tile
-        // of a key tile frees it
-        const auto scores = [&](int q, int k, bool first, bool last, bool end) {
+        // S of query tile q and the segment's k-th key tile.  Commits cost the
+        // issuing warp about a hundred cycles each: there are no more than needed.
+        const auto scores = [&](int q, int k, bool first) {
             const int n = n0 + k, slot = n * kPieces;
             const uint32_t qd = desc_lo(sbase + q * kQPieces * kPiece);
             #pragma unroll
@@ -655,11 +662,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             kDescHiSw128, id_s, c + e > 0 ? 1u : 0u, one);
             }
             mma_commit_if(&s_full[q], one);
-            mma_commit_if(&k_free[n & 1], one && last);
-            mma_commit_if(&q_free[q], one && end);
             return true;
         };
-        const auto values = [&](int q, int k, int done, bool first, bool last) {
+        // O += P V; the last query tile of a key tile frees its values
+        const auto values = [&](int q, int k, int done, bool first, bool last, bool end) {
             const int n = n0 + k, slot = n * kPieces + kQPieces;
             if (!mbar_wait_here(&p_full[q], (done + k) & 1, abort_flag, a.status))
                 return false;
@@ -677,8 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mma_f16_ts(tmem + kColO + q * 128 + 64 * c, tmem + kColS + q * 128 + 8 * e,
                                vd + e * (2048 >> 4), kDescHiSw128, id_v, k + e > 0 ? 1u : 0u, one);
             }
-            mma_commit_if(&pv_done[q], one);
-            mma_commit_if(&v_free[n & 1], one && last);
+            if (last)
+                mma_commit_if(&v_free[n & 1], one);
+            if (end)
+                mma_commit_if(&pv_done[q], one);
             return true;
         };
         bool ok = true;
@@ -695,17 +703,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = mbar_wait_here(&q_full[q], (fills >> q) & 1, abort_flag, a.status);
                 fills ^= 1 << q;
                 if (ok)
-                    ok = scores(q, 0, q == 0 || c0 <= 0, q == 1 || c1 <= 0, cnt == 1);
+                    ok = scores(q, 0, q == 0 || c0 <= 0);
             }
             for (int k = 0; ok && k < most; ++k) {
                 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int cnt = q ? c1 : c0;
                     if (ok && k < cnt)
-                        ok = values(q, k, q ? done1 : done0, q == 0 || c0 <= k, q == 1 || c1 <= k);
+                        ok = values(q, k, q ? done1 : done0, q == 0 || c0 <= k, q == 1 || c1 <= k,
+                                    k + 1 == cnt);
                     if (ok && k + 1 < cnt)
-                        ok = scores(q, k + 1, q == 0 || c0 <= k + 1, q == 1 || c1 <= k + 1,
-                                    k + 2 == cnt);
+                        ok = scores(q, k + 1, q == 0 || c0 <= k + 1);
                 }
             }
             n0 += most;

@@ -203,8 +203,9 @@ __device__ __forceinline__ int reduce_rows(float (&v)[CNT], int lane, Op op)
 template <int N>
 struct Cfg {
     static constexpr int Q_BYTES = kChunks * N * 128;
-    // 64 tokens a head row; the epilogue turns 1 KB a warp over in it
-    static constexpr int P_BYTES = N * 128 > 4096 ? N * 128 : 4096;
+    // 64 tokens a head row; the epilogue turns 1 KB a warp over in it, twice
+    static constexpr int P_BYTES = 8192;
+    static_assert(N <= 64, "a head row is 128 bytes");
     static constexpr int OFF_Q = 2 * kStageBytes;
     static constexpr int OFF_P = OFF_Q + Q_BYTES;
     static constexpr int OFF_MAX = OFF_P + P_BYTES;     // [4][N] floats
@@ -829,11 +830,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // 32 latents (this warp's) x 16 heads at a time, turned over in
                 // the warp's part of the P buffer (free: the last product is in)
                 // so that four lanes store 64 bytes of a head
-                const uint32_t turn = p_addr + warp * 1024;
+                const uint32_t turn0 = p_addr + warp * 2048;
                 uint16_t *to = a.out + (int64_t)s.r * a.next * a.ldo_row + 32 * warp +
                                8 * (lane & 3);
-                #pragma unroll 1
+                #pragma unroll 2
                 for (int q = 0; q < 4 * N; q += 16) {
+                    const uint32_t turn = turn0 + (q & 16) * 64;
                     uint32_t o[2][8];
                     tmem_ld_16x256b<2>(tmem + lanes + q, o[0]);
                     tmem_ld_16x256b<2>(tmem + lanes + (16u << 16) + q, o[1]);

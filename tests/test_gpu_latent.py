@@ -471,3 +471,125 @@ def test_prefill_peaked_and_graph():
     g.replay()
     _clean()
     assert torch.equal(call.keep[6], first)
+
+
+# --------------------------------------------------- sizes where the lists end
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_sparse_more_rows_than_threads(fmt):
+    """The share scan's threads take several rows each; one row is cut."""
+    rng = np.random.default_rng(41)
+    lens = np.concatenate([rng.integers(0, 9, 1100), [700], rng.integers(0, 9, 300)])
+    pool, slots, indptr, qt, q = _sparse_case(rng, fmt, lens, 8, 64)
+    out, lse = B.idx_latent_attention(qt, _dev(pool), 64, fmt, _dev(slots), _dev(indptr), SCALE)
+    _clean()
+    _check_sparse(pool, fmt, 64, slots, indptr, q, out, lse, rows=list(range(0, 1401, 37)) + [1100])
+
+
+def test_sparse_bounds_past_the_slots():
+    """Row bounds outside the listed slots are clamped to them."""
+    rng = np.random.default_rng(42)
+    pool, slots, indptr, qt, q = _sparse_case(rng, ref.FP8, [100, 90, 60], 16, 64)
+    wrong = np.array([-5, 100, 10 ** 9, 2 ** 31 - 1], np.int32)
+    out, lse = B.idx_latent_attention(qt, _dev(pool), 64, ref.FP8, _dev(slots), _dev(wrong), SCALE)
+    _clean()
+    _check_sparse(pool, ref.FP8, 64, slots, np.array([0, 100, 250, 250]), q, out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_sparse_heads_before_rows(fmt):
+    """Queries and outputs laid out [H, R, ..]: the head stride is the larger."""
+    rng = np.random.default_rng(43)
+    pool, slots, indptr, _, _ = _sparse_case(rng, fmt, [300, 5, 64], 20, 64)
+    t, q = _bf16(rng.standard_normal((20, 3, 576)))
+    o = torch.empty(20, 3, 512, dtype=torch.bfloat16, device="cuda")
+    out, lse = B.idx_latent_attention(t.transpose(0, 1), _dev(pool), 64, fmt, _dev(slots), _dev(indptr), SCALE,
+                                      out=o.transpose(0, 1))
+    _clean()
+    _check_sparse(pool, fmt, 64, slots, indptr, q.transpose(1, 0, 2), out, lse)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("next_n,H", [(3, 24), (2, 40), (5, 16), (4, 1)])
+def test_paged_rows_sharing_columns(fmt, next_n, H):
+    """Groups of columns that hold some of a sequence's rows, the last one fewer."""
+    rng = np.random.default_rng(next_n * H)
+    ctx, page = [next_n - 1, 130, 1100], 64
+    pool, bt, slots = _paged_case(rng, fmt, ctx, page)
+    qt, q = _bf16(rng.standard_normal((len(ctx) * next_n, H, 576)))
+    out, lse = B.idx_paged_latent_attention(qt, _dev(pool), page, fmt, _dev(bt), _dev(np.array(ctx, np.int32)),
+                                            next_n, SCALE, max(ctx))
+    _clean()
+    out, lse = _np(out), _np(lse)
+    for b, c in enumerate(ctx):
+        tok = ref.read_tokens(pool, fmt, page, slots[b])
+        for j in range(next_n):
+            t = tok[:max(0, c - next_n + j + 1)]
+            ref.check(out[b * next_n + j], lse[b * next_n + j], ref.attend(q[b * next_n + j], t, t[:, :512], SCALE))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_cache_beyond_four_gigabytes(fmt):
+    """Store, read-back and attention at byte offsets past 2^32."""
+    rng = np.random.default_rng(44)
+    page, stride = 64, ref.page_stride(fmt, 64)
+    pages = (2 ** 32 + 2 ** 30) // stride
+    pool = torch.empty(pages, stride, dtype=torch.uint8, device="cuda")
+    slots = np.concatenate([np.arange(100), pages * page - 200 + np.arange(200)]).astype(np.int64)
+    t, x = _bf16(rng.standard_normal((300, 576)))
+    B.idx_latent_store(t, None, None, None, 0.0, pool, page, _dev(slots), fmt)
+    bt = np.array([[0, 1, pages - 4, pages - 3, pages - 2, pages - 1]], np.int32)
+    back = torch.empty(6 * page, 576, dtype=torch.bfloat16, device="cuda")
+    B.idx_latent_gather(pool, page, fmt, _dev(bt), _dev(np.array([0, 6 * page], np.int32)), back)
+    _clean()
+    got = _np(back)
+    at = np.concatenate([np.arange(100), 6 * page - 200 + np.arange(200)])
+    tol = 0 if fmt == ref.BF16 else 2.0 ** -4 * np.abs(x) + 2.0 ** -10
+    assert (np.abs(got[at] - x) <= tol).all()
+    qt, q = _bf16(rng.standard_normal((1, 16, 576)))
+    out, lse = B.idx_latent_attention(qt, pool, page, fmt, _dev(slots.astype(np.int32)),
+                                      _dev(np.array([0, 300], np.int32)), SCALE)
+    _clean()
+    ref.check(_np(out)[0], _np(lse)[0], ref.attend(q[0], got[at], got[at][:, :512], SCALE))
+
+
+@pytest.mark.parametrize("count", [200, 900])
+def test_prefill_many_sequences(count):
+    """More sequences than the kernel keeps bounds for, and than it has threads."""
+    rng = np.random.default_rng(count)
+    lq = rng.integers(0, 4, count).tolist()
+    lk = [a + int(b) for a, b in zip(lq, rng.integers(0, 3, count))]
+    lq[count // 2], lk[count // 2] = 300, 700
+    cq, ck, qt, q, kvt, kv, latt, lat = _prefill_case(rng, lq, lk, 2)
+    out, lse = B.idx_latent_prefill(qt, kvt[..., :128], latt[:, 512:], kvt[..., 128:], _dev(cq), _dev(ck), SCALE)
+    _clean()
+    _check_prefill(cq, ck, q, kv, lat[:, 512:], out, lse, True)
+
+
+def test_prefill_without_keys_and_one_long_row():
+    z = torch.zeros(0, 2, 128, dtype=torch.bfloat16, device="cuda")
+    q = torch.ones(5, 2, 192, dtype=torch.bfloat16, device="cuda")
+    cu = lambda *a: _dev(np.array(a, np.int32))  # noqa: E731
+    out, lse = B.idx_latent_prefill(q, z, z[:, 0, :64], z, cu(0, 5), cu(0, 0), SCALE)
+    _clean()
+    assert (out == 0).all() and (lse == -float("inf")).all()
+    # one query on many keys: cut over the whole GPU
+    rng = np.random.default_rng(45)
+    cq, ck, qt, qn, kvt, kv, latt, lat = _prefill_case(rng, [1], [40000], 1)
+    out, lse = B.idx_latent_prefill(qt, kvt[..., :128], latt[:, 512:], kvt[..., 128:], _dev(cq), _dev(ck), SCALE)
+    _clean()
+    _check_prefill(cq, ck, qn, kv, lat[:, 512:], out, lse, True)
+
+
+def test_nothing_to_do():
+    bf = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool = torch.zeros(2, 64 * 648, dtype=torch.uint8, device="cuda")
+    B.idx_latent_store(bf(0, 576), None, None, None, 0.0, pool, 64, torch.zeros(0, dtype=torch.int64, device="cuda"), 1)
+    B.idx_latent_gather(pool, 64, 1, i32(1, 2), i32(2), bf(0, 576))
+    out, lse = B.idx_latent_attention(bf(0, 4, 576), pool, 64, 1, i32(0), i32(1), SCALE)
+    assert out.shape == (0, 4, 512) and lse.shape == (0, 4)
+    out, lse = B.idx_latent_prefill(bf(0, 4, 192), bf(3, 4, 128), bf(3, 64), bf(3, 4, 128), i32(2), i32(2), SCALE)
+    assert out.shape == (0, 4, 128)
+    _clean()

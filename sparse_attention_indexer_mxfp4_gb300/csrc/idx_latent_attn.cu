@@ -1214,8 +1214,10 @@ idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int shares, cud
     cudaError_t e = launch_pdl(kern, dim3(a.groups, shares), dim3(kThreads), C::SMEM, s, tm, a);
     if (e == cudaSuccess && shares > 1 && !a.uncut) {
         const int entries = a.by_row ? a.rows : shares - 1;
-        // teams from about eight pieces a row on
-        if (shares >= 8 * a.rows)
+        // Teams while their blocks, of which an SM holds two, run at once: at
+        // 2048 keys 16 columns x 4 rows 13.3 us (without teams 20.6), x 12 18.3
+        // (19.2), x 28 24.0 (21.3); 64 columns x 2 14.9 (18.5), x 16 37.7 (22.5).
+        if (entries * N * a.groups <= 2 * sm_count())
             e = launch_pdl(latent_join_kernel<N, true>, dim3(entries, N, a.groups),
                            dim3(128 * kTeams), 0, s, a);
         else
@@ -1275,9 +1277,11 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
     const int shares =
         (int)std::min<int64_t>(sm_count() / a.groups, most);
     a.by_row = a.rows < shares;
-    // the end of a row (its sums, its output, the next row's first scores) costs
-    // a CTA about as much as this many tiles; short shares are left equal
-    a.charge = most >= 8ll * shares ? (n == 64 ? 3 : 2) : 0;
+    // The end of a row (its sums, its output, the next row's first scores) costs
+    // a CTA about as much as this many tiles: 64 columns 24 rows of 2048 keys
+    // 24.1 us (uncharged 27.7), 64 rows 45.4 (47.3).  Shares of one tile are left
+    // equal: 8 rows of 512 keys 15.2 us charged, 13.6 uncharged.
+    a.charge = most <= shares ? 0 : n == 64 ? 2 : 1;
     CUtensorMap tm;
     // bytes of a head row, heads, rows; a stride over one element is free
     const uint64_t dims[3] = {2 * kLatTok, (uint64_t)a.H, (uint64_t)R};

@@ -51,12 +51,12 @@ class LatentLayer:
         last 64 rotated) over their sequences' num_tokens = cu_k[-1] cached
         tokens.  Returns (out [Tq, H, 128], lse)."""
         n = num_tokens
-        tokens = torch.empty(n, LATENT + ROPE, dtype=torch.bfloat16, device=q.device)
-        B.idx_latent_gather(self.pages, self.page_size, self.fmt, block_table, cu_k, tokens,
-                            stream=stream)
-        kv = torch.matmul(tokens[:, :LATENT], self.w_up).view(n, self.heads, NOPE + VDIM)
-        return B.idx_latent_prefill(q, kv[..., :NOPE], tokens[:, LATENT:], kv[..., NOPE:], cu_q,
-                                    cu_k, self.scale, stream=stream)
+        with B._on(stream):  # the products between the calls too
+            tokens = torch.empty(n, LATENT + ROPE, dtype=torch.bfloat16, device=q.device)
+            B.idx_latent_gather(self.pages, self.page_size, self.fmt, block_table, cu_k, tokens)
+            kv = torch.matmul(tokens[:, :LATENT], self.w_up).view(n, self.heads, NOPE + VDIM)
+            return B.idx_latent_prefill(q, kv[..., :NOPE], tokens[:, LATENT:], kv[..., NOPE:], cu_q,
+                                        cu_k, self.scale)
 
     def absorb(self, q):
         """q bf16 [R, H, 192] with the key projection taken into it: [R, H, 576]."""
@@ -69,16 +69,18 @@ class LatentLayer:
 
     def decode_slots(self, q, slots, indptr, stream=None):
         """Absorbed attention over ragged slots (an indexer step's)."""
-        out, lse = B.idx_latent_attention(self.absorb(q), self.pages, self.page_size, self.fmt,
-                                          slots, indptr, self.scale, stream=stream)
-        return self.project(out), lse
+        with B._on(stream):
+            out, lse = B.idx_latent_attention(self.absorb(q), self.pages, self.page_size, self.fmt,
+                                              slots, indptr, self.scale)
+            return self.project(out), lse
 
     def decode_paged(self, q, block_table, context_lens, next_n, max_model_len, stream=None):
         """Absorbed attention over whole contexts."""
-        out, lse = B.idx_paged_latent_attention(self.absorb(q), self.pages, self.page_size,
-                                                self.fmt, block_table, context_lens, next_n,
-                                                self.scale, max_model_len, stream=stream)
-        return self.project(out), lse
+        with B._on(stream):
+            out, lse = B.idx_paged_latent_attention(self.absorb(q), self.pages, self.page_size,
+                                                    self.fmt, block_table, context_lens, next_n,
+                                                    self.scale, max_model_len)
+            return self.project(out), lse
 
 
 class SparseDecodeStep:

@@ -93,3 +93,31 @@ def test_decode_step_over_an_indexers_slots():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(step.out, first)
+
+
+def test_layer_on_another_stream():
+    """Every part of a call runs on the stream it is given, the library products
+    between the kernels among them: the current stream is kept busy meanwhile."""
+    rng = np.random.default_rng(33)
+    lens, heads, page = [130, 70], 16, 64
+    layer = _layer(rng, heads, 8, page, ref.FP8)
+    bt, pos, slots = _prompt(rng, layer, lens, page)
+    cu = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device="cuda")
+    ctx = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    flat = torch.from_numpy(np.concatenate(slots).astype(np.int32)).cuda()
+    q = torch.from_numpy(rng.standard_normal((sum(lens), heads, 192))).bfloat16().cuda()
+    last = q[(cu[1:] - 1).long()]
+    calls = [lambda s: layer.prefill(q, cu, bt, cu, sum(lens), stream=s),
+             lambda s: layer.decode_slots(last, flat, cu, stream=s),
+             lambda s: layer.decode_paged(last, bt, ctx, 1, max(lens), stream=s)]
+    want = [[x.clone() for x in c(None)] for c in calls]
+    side = torch.cuda.Stream()
+    for c, (out, lse) in zip(calls, want):
+        torch.cuda.synchronize()
+        torch.cuda._sleep(200_000_000)  # a tenth of a second
+        got = c(side)
+        side.synchronize()
+        with torch.cuda.stream(side):
+            same = torch.equal(got[0], out) and torch.equal(got[1], lse)
+        torch.cuda.synchronize()
+        assert same

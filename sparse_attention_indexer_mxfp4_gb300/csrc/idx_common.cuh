@@ -585,6 +585,48 @@ IDX_DEVFN float ex2(float x)
     return y;
 }
 
+// Pairs of floats, one instruction for both.
+IDX_DEVFN uint64_t pack_x2(uint32_t lo, uint32_t hi)
+{
+    uint64_t v;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+    return v;
+}
+
+IDX_DEVFN uint64_t pack_x2(float lo, float hi)
+{
+    return pack_x2(__float_as_uint(lo), __float_as_uint(hi));
+}
+
+IDX_DEVFN float low_x2(uint64_t v)
+{
+    return __uint_as_float((uint32_t)v);
+}
+
+IDX_DEVFN float high_x2(uint64_t v)
+{
+    return __uint_as_float((uint32_t)(v >> 32));
+}
+
+IDX_DEVFN uint64_t fma_x2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+IDX_DEVFN uint64_t add_x2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+IDX_DEVFN uint64_t ex2_x2(uint64_t x)
+{
+    return pack_x2(ex2(low_x2(x)), ex2(high_x2(x)));
+}
+
 // Four 8x8 blocks of 16-bit elements from fragment registers to shared
 // memory, each transposed; lane l gives the address of row l % 8 of block
 // l / 8.

@@ -10,8 +10,14 @@
 // The two tiles take turns: while the softmax warps of one work, the tensor
 // cores do the other's products, and both read each key tile once.  Scores,
 // weights and sums stay in tensor memory: S (128 columns) is overwritten by P
-// in bf16, which the second product takes as its A operand from there.  The
-// tensor cores bound it: 1280 cycles a tile pair against 1024 of exponentials.
+// in bf16, which the second product takes as its A operand from there.  Bounds:
+// the tensor cores need 2610 cycles for both tiles' products with a key tile
+// (12 of 65 and 16 of 33 each), a tile's softmax 1150, by its instructions
+// (pairs of scores share them where they can; exponentials by polynomial beside
+// the special-function unit's cost more of them and time).  Measured: 3030
+// cycles; 2048 queries x 64 heads at the end of 8192 tokens 372 to 380 us, 1600
+// TFLOP/s, where the GPU's power limit holds it whatever the kernel saves; 7 whole
+// prompts of 65 to 1500 tokens x 16 heads 54.8 us.
 //
 // Keys and values come by TMA in pieces of 64 elements of 128 tokens (16 KB,
 // 128-byte swizzled), five a tile (three of K, the last shared by all heads,
@@ -23,12 +29,15 @@
 // Work is the flat list of (head, block, key tile); every CTA (one per SM)
 // takes an equal contiguous share of it, so causal blocks of any length fill
 // the GPU evenly and few queries on many keys are spread over it; a block
-// counts a tile more than it has, for the end of the one before.  The next
-// block's queries and keys come in while the last one's epilogue runs.  A block
+// counts a tile more than it has, for the end of the one before (the prompts
+// 54.8 us; none 58.8, two 55.0).  The products go from block to block without a
+// pause: a query tile's next scores follow its last values at once, in the next
+// block while the other tile still works on this one (62.9 us with a pause), as
+// its place and the keys' come free.  A block
 // that shares cut leaves unnormalised sums in scratch for a second kernel.
 //
 // Warps: 0-3 and 4-7 softmax of the two tiles, a thread a query; 8 issues TMA;
-// 9 issues the products.
+// 9 issues the products; 10 clears values past a sequence's end.
 #include <algorithm>
 #include <atomic>
 #include <cuda_bf16.h>
@@ -44,16 +53,16 @@ constexpr int kTile = 128;                      // queries and keys of a tile
 constexpr int kPiece = kTile * 128;             // bytes of 64 elements of a tile's tokens
 constexpr int kQPieces = kQk / 64, kVPieces = kV / 64, kPieces = kQPieces + kVPieces;
 constexpr int kRing = 8;
-constexpr int kWarpLoad = 8, kWarpMma = 9;
-constexpr int kThreads = 384;  // whole warpgroups: two warps only help to start
+constexpr int kWarpLoad = 8, kWarpMma = 9, kWarpTail = 10;
+constexpr int kThreads = 384;  // whole warpgroups: the last warp only helps to start
 // Registers of a thread: as launched, then of the two softmax warpgroups (a
 // row of scores each thread) and of the third.
-constexpr int kRegs = 168, kRegsSoft = 216, kRegsRest = 72;
+constexpr int kRegs = 168, kRegsSoft = 200, kRegsRest = 104;
 static_assert(2 * kRegsSoft + kRegsRest <= 3 * kRegs && kRegs * kThreads <= 65536,
               "the warpgroups' registers come from the launch's");
 constexpr int kOffRing = 2 * kQPieces * kPiece;
 constexpr int kOffBar = kOffRing + kRing * kPiece;
-constexpr int kBars = kRing + 18;
+constexpr int kBars = kRing + 20;
 constexpr int kOffMisc = kOffBar + 8 * kBars;  // tmem base, abort flag, the share's place, sizes
 constexpr int kOffCu = kOffMisc + 80;          // the sequences' bounds, where they fit
 constexpr int kMaxCu = 128;
@@ -233,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // were read by their last product
     uint64_t *full = bar, *k_free = bar + kRing, *v_free = k_free + 2;
     uint64_t *s_full = k_free + 4, *p_full = k_free + 6, *pv_done = k_free + 8;
-    uint64_t *q_full = k_free + 10, *q_free = k_free + 12, *tail = k_free + 14;  // tail[2]
-    uint64_t *drain = k_free + 16;
+    uint64_t *q_full = k_free + 10, *q_free = k_free + 12, *drain = k_free + 14;
+    uint64_t *tail = k_free + 15;  // cut values came in: [even and odd cut tiles][pieces]
     int *misc = reinterpret_cast<int *>(smem + kOffMisc);
     volatile int *abort_flag = misc + 1;
     const int tid = threadIdx.x, lane = tid & 31;
@@ -244,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < kRing; ++i)
             mbar_init(&full[i], 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&tail[i], 1);
+            mbar_init(&tail[2 * i], 1);
+            mbar_init(&tail[2 * i + 1], 1);
             mbar_init(&k_free[i], 4);
             mbar_init(&v_free[i], 1);
             mbar_init(&s_full[i], 1);
@@ -374,7 +384,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t col_s = tmem + lanes + kColS + q * 128, col_o = tmem + lanes + kColO + q * 128;
         const float sl = a.scale_log2;
         int i = 0, n = 0, segs = 0;  // tiles of this query tile, of both, its segments so far
-        for (int seg = 0; next_seg(a, cq, ck, w, s); ++seg) {
+        Seg ahead;
+        bool more = next_seg(a, cq, ck, w, s);
+        for (int seg = 0; more; ++seg, s = ahead) {
             const int row = s.k.i * kRows + q * kTile + (tid & 127);
             // rows past the sequence's queries take part with no key
             const int seen = row < s.k.nq ? keys_seen(a, s.k, row) : 0;
@@ -440,24 +452,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const float nm = m == -INFINITY ? 0.0f : -m;
-                float sum[4] = {};
+                const uint64_t sl2 = pack_x2(sl, sl), nm2 = pack_x2(nm, nm);
+                uint64_t sum[2] = {};
                 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     // weights as bf16 (half a step of 2^-8 each), two a column
                     uint32_t v[32];
                     #pragma unroll
                     for (int e = 0; e < 32; ++e) {
-                        const int at2 = 2 * e & 31;
-                        const float x = ex2(fmaf(__uint_as_float(r[2 * c + (e >> 4)][at2]), sl, nm));
-                        const float y =
-                            ex2(fmaf(__uint_as_float(r[2 * c + (e >> 4)][at2 + 1]), sl, nm));
-                        sum[e & 3] += x + y;
-                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+                        const uint32_t *at = &r[2 * c + (e >> 4)][2 * e & 31];
+                        const uint64_t x = ex2_x2(fma_x2(pack_x2(at[0], at[1]), sl2, nm2));
+                        sum[e & 1] = add_x2(sum[e & 1], x);
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(low_x2(x), high_x2(x));
                         v[e] = *reinterpret_cast<const uint32_t *>(&b2);
                     }
                     tmem_st_32x32b_x32(col_s + 32 * c, v);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                sum[0] = add_x2(sum[0], sum[1]);
+                l += low_x2(sum[0]) + high_x2(sum[0]);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -467,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the segment's sums
             const bool some = t1 > s.t0;
             n += max(0, min(s.t1, max(s.nt[0], s.nt[1])) - s.t0);
+            more = next_seg(a, cq, ck, w, ahead);  // while the last products run
             if (some) {
                 (void)mbar_wait_here(&pv_done[q], segs & 1, abort_flag, a.status);
                 ++segs;
@@ -550,15 +563,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         int loads[2] = {0, 0};    // of each query tile
         bool ok = true;
         while (ok && next_seg(a, cq, ck, w, s)) {
-            #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (!ok || s.nt[q] <= s.t0)
-                    continue;
-                // the last segment's products have read the queries before
+            // Query tile 0's queries, the first keys, tile 1's queries, the first
+            // values: in the order in which the segment before frees their places.
+            const auto queries = [&](int q) {
+                // the last segment's products have read the ones before
                 if (loads[q] > 0)
                     ok = mbar_wait_here(&q_free[q], (loads[q] - 1) & 1, abort_flag, a.status);
                 if (!ok)
-                    continue;
+                    return;
                 __syncwarp();
                 if (one) {
                     mbar_arrive_expect_tx(&q_full[q], kQPieces * kPiece);
@@ -568,7 +580,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     s.k.head, s.k.seq_q + s.k.i * kRows + q * kTile);
                 }
                 ++loads[q];
-            }
+            };
+            if (s.nt[0] > s.t0)
+                queries(0);
             const int most = min(s.t1, max(s.nt[0], s.nt[1]));
             for (int j = s.t0; ok && j < most; ++j, ++n) {
                 const int t0 = s.k.seq_k + j * kTile, rem = s.k.nk - j * kTile;
@@ -579,6 +593,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // n - 2's keys (c = 0), its values (1, 2), tile n - 1's first
                     // keys (3, 4).
                     const int m = n * kPieces + c, slot = m & (kRing - 1);
+                    if (c == kQPieces && j == s.t0 && s.nt[1] > s.t0) {
+                        queries(1);
+                        if (!ok)
+                            break;
+                    }
                     if (c == 0 && n >= 2)
                         ok = mbar_wait_here(&k_free[n & 1], ((n >> 1) - 1) & 1, abort_flag,
                                             a.status);
@@ -593,7 +612,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     uint8_t *to = smem + kOffRing + slot * kPiece;
                     if (one) {
-                        uint64_t *b = cut && c >= kQPieces ? &tail[c - kQPieces] : &full[slot];
+                        uint64_t *b = cut && c >= kQPieces ? &tail[2 * (tails & 1) + c - kQPieces]
+                                                           : &full[slot];
                         mbar_arrive_expect_tx(b, kPiece);
                         if (c < 2)
                             tma_load_3d(to, &tm_k, b, 128 * c, s.k.head, t0);
@@ -604,22 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     pieces = m + 1;
                 }
-                __syncwarp();
-                // a weight of zero does not hide what is not finite: another
-                // sequence's values become zeros here
-                #pragma unroll 1
-                for (int c = 0; ok && cut && c < kVPieces; ++c) {
-                    ok = mbar_wait_here(&tail[c], tails & 1, abort_flag, a.status);
-                    const int slot = (n * kPieces + kQPieces + c) & (kRing - 1);
-                    const uint32_t to = smem_u32(smem + kOffRing + slot * kPiece);
-                    for (int e = rem * 8 + lane; e < kTile * 8; e += 32)
-                        st_shared_v4(to + 16 * e, 0, 0, 0, 0);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&full[slot]);
-                }
-                tails += cut;
+                tails += cut && ok;
             }
         }
         if (*abort_flag) {
@@ -628,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 2; ++q)
                 if (loads[q] > 0)
                     (void)mbar_drain_here(&q_full[q], (loads[q] - 1) & 1);
-            for (int c = 0; c < kVPieces; ++c)
-                if (tails > 0)
-                    (void)mbar_drain_here(&tail[c], (tails - 1) & 1);
+            for (int t = max(0, tails - 2); t < tails; ++t)
+                for (int c = 0; c < kVPieces; ++c)
+                    (void)mbar_drain_here(&tail[2 * (t & 1) + c], (t >> 1) & 1);
             for (int i = max(0, pieces - kRing); i < pieces; ++i)
                 (void)mbar_drain_here(&full[i & (kRing - 1)], (i >> 3) & 1);
         }
@@ -639,7 +644,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t one = elect_one();
         const uint32_t id_s = idesc_bf16(kTile, kTile, false, false);
         const uint32_t id_v = idesc_bf16(kTile, 64, false, true);
-        int n0 = 0;            // tiles before the segment
+        int n0 = -1;           // tiles before the segment
         int fills = 0;         // parity of the segments that each query tile had, a bit each
         int done0 = 0, done1 = 0;  // tiles of each query tile before the segment
         // S of query tile q and the segment's k-th key tile.  Commits cost the
@@ -689,41 +694,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_commit_if(&pv_done[q], one);
             return true;
         };
-        bool ok = true;
-        while (ok && next_seg(a, cq, ck, w, s)) {
-            // tiles of the segment that each query tile takes
-            const int c0 = max(0, min(s.t1, s.nt[0]) - s.t0);
-            const int c1 = max(0, min(s.t1, s.nt[1]) - s.t0);
-            const int most = max(c0, c1);
-            #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int cnt = q ? c1 : c0;
-                if (!ok || cnt == 0)
-                    continue;
-                ok = mbar_wait_here(&q_full[q], (fills >> q) & 1, abort_flag, a.status);
-                fills ^= 1 << q;
-                if (ok)
-                    ok = scores(q, 0, q == 0 || c0 <= 0);
+        // Tile by tile: its products of each query tile, each followed by the next
+        // tile's scores of the same one, in the next segment as in this.  Before
+        // the first segment stands one of a tile that none takes.
+        int c0 = 0, c1 = 0;  // the segment's tiles for each query tile
+        bool ok = true, more = true;
+        while (ok && more) {
+            int x0 = 0, x1 = 0;  // the next segment's
+            while (max(x0, x1) == 0 && (more = next_seg(a, cq, ck, w, s))) {
+                x0 = max(0, min(s.t1, s.nt[0]) - s.t0);
+                x1 = max(0, min(s.t1, s.nt[1]) - s.t0);
             }
+            const int most = max(1, max(c0, c1));
+            #pragma unroll 1
             for (int k = 0; ok && k < most; ++k) {
+                const bool last = k + 1 == most;
                 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     const int cnt = q ? c1 : c0;
                     if (ok && k < cnt)
                         ok = values(q, k, q ? done1 : done0, q == 0 || c0 <= k, q == 1 || c1 <= k,
                                     k + 1 == cnt);
-                    if (ok && k + 1 < cnt)
-                        ok = scores(q, k + 1, q == 0 || c0 <= k + 1);
+                    const bool fresh = last && (q ? x1 : x0) > 0;
+                    if (ok && fresh) {
+                        ok = mbar_wait_here(&q_full[q], (fills >> q) & 1, abort_flag, a.status);
+                        fills ^= 1 << q;
+                    }
+                    if (ok && (fresh || k + 1 < cnt))
+                        ok = scores(q, k + 1, q == 0 || (last ? x0 : c0 - k - 1) <= 0);
                 }
             }
             n0 += most;
             done0 += c0;
             done1 += c1;
+            c0 = x0;
+            c1 = x1;
         }
         if (*abort_flag) {
             mma_commit_if(drain, one);
             __syncwarp();
             (void)mbar_drain_here(drain, 0);
+        }
+    }
+    else if (warp == kWarpTail) {
+        // ---------------------------------------------- values of a cut tile
+        // A weight of zero does not hide what is not finite: another sequence's
+        // values become zeros here.
+        int n = 0, tails = 0;
+        bool ok = true;
+        while (ok && next_seg(a, cq, ck, w, s)) {
+            const int most = min(s.t1, max(s.nt[0], s.nt[1]));
+            const int j = s.k.nk / kTile, rem = s.k.nk % kTile;
+            if (rem > 0 && j >= s.t0 && j < most) {
+                #pragma unroll 1
+                for (int c = 0; c < kVPieces; ++c) {
+                    ok = mbar_wait_here(&tail[2 * (tails & 1) + c], (tails >> 1) & 1, abort_flag,
+                                        a.status);
+                    if (!ok)
+                        break;
+                    const int slot = ((n + j - s.t0) * kPieces + kQPieces + c) & (kRing - 1);
+                    const uint32_t to = smem_u32(smem + kOffRing + slot * kPiece);
+                    #pragma unroll 1
+                    for (int e = rem * 8 + lane; e < kTile * 8; e += 32)
+                        st_shared_v4(to + 16 * e, 0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&full[slot]);
+                }
+                ++tails;
+            }
+            n += max(0, most - s.t0);
         }
     }
     tc_fence_before();

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libidx.so (include/idx.h).
+"""Thin binding of libidx.so (include/idx.h): ctypes, and for the latent calls
+an extension that does the same natively (csrc/bind_latent.cpp).
 
 Argument marshalling only: every function takes torch CUDA tensors, checks
 dtype / shape / device, and passes raw device pointers, sizes and the current
@@ -10,6 +11,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -34,6 +37,7 @@ SLOT_DIRECT_ROWS = 4096  # above it the slot map runs a third (scan) kernel
 TOPK_CLUSTER_MAX_LEN = 262144  # rows the one-cluster-per-row top-k holds (8 x 32768 keys)
 
 _lib = None
+_calls = None
 _lock = threading.Lock()
 
 _P, _I, _L, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
@@ -171,16 +175,9 @@ class Prepared:
         _check(self.fn(*self.args, _stream(stream)), self.name)
 
 
-def _run(name, args, stream):
-    """A call made once: what Prepared does, without the object."""
-    rc = getattr(_lib or lib(), name)(*args, _stream(stream))
-    if rc != IDX_OK:
-        _check(rc, name)
-
-
 def _on(stream):
-    """The context a call's outputs and scratch are made in: memory of the
-    current stream may still be in use there when another stream writes it."""
+    """The context in which what a call makes is made on its stream: memory of
+    the current stream may still be in use there when another writes it."""
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
@@ -615,69 +612,23 @@ def latent_page_bytes(page_size, fmt) -> int:
     return -(-page_size * token // 16) * 16
 
 
-def _need_pages(t):
-    """The number of pages and the bytes between them."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != torch.uint8 or len(shape) != 2 or stride[1] != 1:
-        raise ValueError("kv_pages must be uint8 [num_pages, page_stride] with unit byte stride")
-    return shape[0], stride[0]
-
-
-def _need_heads(t, dims, dim, name):
-    """bf16, `dims` dimensions, the last one of `dim` contiguous elements."""
-    shape, stride = t.shape, t.stride()
-    if t.dtype != torch.bfloat16 or len(shape) != dims or shape[-1] != dim or stride[-1] != 1:
-        raise ValueError(f"{name} must be bfloat16 [..., {dim}] of {dims} dimensions with unit "
-                         "last stride")
-    return shape, stride
-
-
-def _out_lse(out, lse, rows, heads, dim, device):
-    """The outputs of an attention call, made here unless given (lse False:
-    none), and their strides: row and head of out, row of lse."""
-    if out is None:
-        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=device)
-        ldo = (heads * dim, dim)
-    else:
-        shape, ldo = _need_heads(out, 3, dim, "out")
-        if shape[0] != rows or shape[1] != heads:
-            raise ValueError(f"out must be [{rows}, {heads}, {dim}]")
-    if lse is False:
-        return out, None, ldo[0], ldo[1], 0
-    if lse is None:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=device)
-        return out, lse, ldo[0], ldo[1], heads
-    if lse.dtype != torch.float32 or lse.shape != (rows, heads) or lse.stride(1) != 1:
-        raise ValueError(f"lse must be float32 [{rows}, {heads}] with unit column stride")
-    return out, lse, ldo[0], ldo[1], lse.stride(0)
-
-
-def _latent_store_args(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
-                         slot_mapping, fmt):
-    (T, _), (ld_kv, _) = _need_heads(kv, 2, LATENT_DIM + LATENT_ROPE, "kv")
-    _need(slot_mapping, torch.int64, "slot_mapping")
-    pages, stride = _need_pages(kv_pages)
-    if slot_mapping.numel() != T:
-        raise ValueError(f"slot_mapping must hold {T} entries")
-    if (cos_sin is None) != (positions is None):
-        raise ValueError("positions and cos_sin come together")
-    rows, ld = 0, 0
-    if cos_sin is not None:
-        _need(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError(f"positions must hold {T} entries")
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or cos_sin.stride(1) != 1 or (
-                cos_sin.shape[1] < LATENT_ROPE):
-            raise ValueError(f"cos_sin must be float32 [positions, {LATENT_ROPE}]")
-        rows, ld = cos_sin.shape[0], cos_sin.stride(0)
-    if norm_weight is not None:
-        _need(norm_weight, torch.float32, "norm_weight")
-        if norm_weight.numel() != LATENT_DIM:
-            raise ValueError(f"norm_weight must hold {LATENT_DIM} entries")
-    args = (_ptr(kv), ld_kv, _ptr(positions), _ptr(cos_sin), ld, rows, _ptr(norm_weight), eps, T,
-            LATENT_DIM, LATENT_ROPE, fmt, _ptr(kv_pages), stride, pages, page_size,
-            _ptr(slot_mapping))
-    return args, (kv, positions, cos_sin, norm_weight, kv_pages, slot_mapping), 1
+def _latent_calls():
+    """The latent calls' extension, bound to the loaded library."""
+    global _calls
+    if _calls is None:
+        L = lib()
+        if not os.path.exists(_build.CALLS):
+            raise IndexerError(f"{_build.CALLS} is missing: build the library first")
+        loader = importlib.machinery.ExtensionFileLoader("_latent_calls", _build.CALLS)
+        mod = importlib.util.module_from_spec(
+            importlib.util.spec_from_file_location("_latent_calls", _build.CALLS, loader=loader))
+        loader.exec_module(mod)
+        mod.bind(_check, *(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            "idx_latent_store", "idx_latent_gather", "idx_latent_attention",
+            "idx_paged_latent_attention", "idx_latent_prefill",
+            "idx_latent_attention_workspace_size", "idx_latent_prefill_workspace_size")))
+        _calls = mod
+    return _calls
 
 
 def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
@@ -687,33 +638,18 @@ def prepare_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, pag
     [P, 64] (both None: stored as they are); norm_weight fp32 [512] (None: no
     norm); slot_mapping int64 [T], negative skips."""
     return Prepared("idx_latent_store",
-                    *_latent_store_args(kv, positions, cos_sin, norm_weight, eps, kv_pages,
-                                        page_size, slot_mapping, fmt))
+                    *_latent_calls().store(True, kv, positions, cos_sin, norm_weight, eps, kv_pages,
+                                           page_size, slot_mapping, fmt))
 
 
 def idx_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size, slot_mapping,
                      fmt, stream=None):
-    _run("idx_latent_store", _latent_store_args(kv, positions, cos_sin, norm_weight, eps, kv_pages,
-                                                page_size, slot_mapping, fmt)[0], stream)
-
-
-def _latent_gather_args(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None):
-    pages, stride = _need_pages(kv_pages)
-    (rows, _), (ld_out, _) = _need_heads(out, 2, LATENT_DIM + LATENT_ROPE, "out")
-    _need(block_table, torch.int32, "block_table")
-    _need(cu_lens, torch.int32, "cu_lens")
-    B_ = cu_lens.numel() - 1
-    table = block_table.shape
-    if len(table) != 2 or table[0] < B_ or B_ < 0:
-        raise ValueError("block_table must be [B, blocks] and cu_lens [B + 1]")
-    if seq_starts is not None:
-        _need(seq_starts, torch.int32, "seq_starts")
-        if seq_starts.numel() != B_:
-            raise ValueError(f"seq_starts must hold {B_} entries")
-    args = (_ptr(kv_pages), stride, pages, page_size, fmt, LATENT_DIM, LATENT_ROPE,
-            _ptr(block_table), table[1], table[1], _ptr(cu_lens), _ptr(seq_starts), B_, rows,
-            _ptr(out), ld_out)
-    return args, (kv_pages, block_table, cu_lens, seq_starts, out), 1
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return idx_latent_store(kv, positions, cos_sin, norm_weight, eps, kv_pages, page_size,
+                                    slot_mapping, fmt)
+    return (_calls or _latent_calls()).store(False, kv, positions, cos_sin, norm_weight, eps,
+                                             kv_pages, page_size, slot_mapping, fmt)
 
 
 def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None):
@@ -721,15 +657,18 @@ def prepare_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, s
     rows cu_lens[b] .. cu_lens[b + 1] are sequence b's tokens from
     seq_starts[b] (None: 0) on.  cu_lens int32 [B + 1], seq_starts int32 [B]."""
     return Prepared("idx_latent_gather",
-                    *_latent_gather_args(kv_pages, page_size, fmt, block_table, cu_lens, out,
-                                         seq_starts))
+                    *_latent_calls().gather(True, kv_pages, page_size, fmt, block_table, cu_lens,
+                                            out, seq_starts))
 
 
 def idx_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out, seq_starts=None,
                       stream=None):
-    _run("idx_latent_gather", _latent_gather_args(kv_pages, page_size, fmt, block_table, cu_lens,
-                                                  out, seq_starts)[0], stream)
-    return out
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return idx_latent_gather(kv_pages, page_size, fmt, block_table, cu_lens, out,
+                                     seq_starts)
+    return (_calls or _latent_calls()).gather(False, kv_pages, page_size, fmt, block_table, cu_lens,
+                                              out, seq_starts)
 
 
 def latent_attention_workspace_size(rows, heads, max_keys) -> int:
@@ -743,33 +682,6 @@ def latent_prefill_workspace_size(rows, keys, heads) -> int:
     return int(lib().idx_latent_prefill_workspace_size(rows, keys, heads))
 
 
-def _latent_ws(workspace, size, device):
-    """The scratch of an attention call and its bytes."""
-    if workspace is True:
-        return (torch.empty(size, dtype=torch.uint8, device=device), size) if size else (None, 0)
-    return workspace, 0 if workspace is None else workspace.numel() * workspace.element_size()
-
-
-def _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
-                           workspace=True):
-    (R, H, _), (ldq, ldqh, _) = _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
-    pages, stride = _need_pages(kv_pages)
-    _need(slots, torch.int32, "slots")
-    _need(indptr, torch.int32, "indptr")
-    if indptr.numel() != R + 1:
-        raise ValueError(f"indptr must hold {R + 1} entries")
-    device = q.device
-    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
-    n = slots.numel()
-    size = lib().idx_latent_attention_workspace_size(R, H, n)
-    ws, ws_bytes = _latent_ws(workspace, size, device)
-    args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(slots),
-            _ptr(indptr), n, R, H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo,
-            ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
-    # the attention, and with scratch the joining kernel
-    return args, (q, kv_pages, slots, indptr, out, lse, ws), 2 if size else 1
-
-
 def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
                              workspace=True):
     """Absorbed latent attention over ragged slots.  q bf16 [R, H, 576] (row
@@ -778,44 +690,19 @@ def prepare_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, 
     none).  workspace: True allocates the scratch here, or a uint8 tensor of
     latent_attention_workspace_size(R, H, slots.numel()) bytes."""
     return Prepared("idx_latent_attention",
-                    *_latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale, out,
-                                            lse, workspace))
+                    *_latent_calls().attention(True, q, kv_pages, page_size, fmt, slots, indptr,
+                                               scale, out, lse, workspace))
 
 
 def idx_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out=None, lse=None,
                          workspace=True, stream=None):
     """(out, lse) of the absorbed attention over ragged slots."""
-    with _on(stream):
-        args, keep, _ = _latent_attention_args(q, kv_pages, page_size, fmt, slots, indptr, scale,
-                                               out, lse, workspace)
-        _run("idx_latent_attention", args, None)
-    return keep[4], keep[5]
-
-
-def _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
-                                 scale, max_model_len, ctx_per_row=False, out=None, lse=None,
-                                 workspace=True):
-    (R, H, _), (ldq, ldqh, _) = _need_heads(q, 3, LATENT_DIM + LATENT_ROPE, "q")
-    pages, stride = _need_pages(kv_pages)
-    _need(block_table, torch.int32, "block_table")
-    _need(context_lens, torch.int32, "context_lens")
-    if next_n <= 0 or R % next_n:
-        raise ValueError("q must hold B * next_n rows")
-    B_ = R // next_n
-    want = R if ctx_per_row else B_
-    if context_lens.numel() != want:
-        raise ValueError(f"context_lens must hold {want} entries")
-    if block_table.dim() != 2 or block_table.shape[0] < B_:
-        raise ValueError(f"block_table must be [{B_}, blocks]")
-    device = q.device
-    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, R, H, LATENT_DIM, device)
-    size = lib().idx_latent_attention_workspace_size(R, H, max_model_len)
-    ws, ws_bytes = _latent_ws(workspace, size, device)
-    args = (_ptr(q), ldq, ldqh, _ptr(kv_pages), stride, pages, page_size, fmt, _ptr(block_table),
-            block_table.shape[1], _ptr(context_lens), int(ctx_per_row), B_, next_n, max_model_len,
-            H, LATENT_DIM, LATENT_ROPE, scale, _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws),
-            ws_bytes)
-    return args, (q, kv_pages, block_table, context_lens, out, lse, ws), 2 if size else 1
+    if stream is not None:  # outputs and scratch are made on the call's stream
+        with torch.cuda.stream(stream):
+            return idx_latent_attention(q, kv_pages, page_size, fmt, slots, indptr, scale, out, lse,
+                                        workspace)
+    return (_calls or _latent_calls()).attention(False, q, kv_pages, page_size, fmt, slots, indptr,
+                                                 scale, out, lse, workspace)
 
 
 def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
@@ -825,44 +712,24 @@ def prepare_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, con
     b attends to its first context_lens[b] - next_n + j + 1 tokens (or
     context_lens[row] with ctx_per_row).  q bf16 [B * next_n, H, 576]."""
     return Prepared("idx_paged_latent_attention",
-                    *_paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table,
-                                                  context_lens, next_n, scale, max_model_len,
-                                                  ctx_per_row, out, lse, workspace))
+                    *_latent_calls().paged_attention(True, q, kv_pages, page_size, fmt, block_table,
+                                                     context_lens, next_n, scale, max_model_len,
+                                                     ctx_per_row, out, lse, workspace))
 
 
 def idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table, context_lens, next_n,
                                scale, max_model_len, ctx_per_row=False, out=None, lse=None,
                                workspace=True, stream=None):
     """(out, lse) of the absorbed attention over whole paged contexts."""
-    with _on(stream):
-        args, keep, _ = _paged_latent_attention_args(q, kv_pages, page_size, fmt, block_table,
-                                                     context_lens, next_n, scale, max_model_len,
-                                                     ctx_per_row, out, lse, workspace)
-        _run("idx_paged_latent_attention", args, None)
-    return keep[4], keep[5]
-
-
-def _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
-                         workspace=True):
-    (Tq, H, _), (ldq, ldqh, _) = _need_heads(q, 3, 192, "q")
-    (Tk, Hk, _), (ldk, ldkh, _) = _need_heads(k, 3, 128, "k")
-    (Tr, _), (ldr, _) = _need_heads(k_rope, 2, LATENT_ROPE, "k_rope")
-    (Tv, Hv, _), (ldv, ldvh, _) = _need_heads(v, 3, 128, "v")
-    _need(cu_q, torch.int32, "cu_q")
-    _need(cu_k, torch.int32, "cu_k")
-    if Hk != H or Hv != H or Tv != Tk or Tr != Tk:
-        raise ValueError("k, k_rope and v must hold the same tokens, and the heads of q")
-    B_ = cu_q.numel() - 1
-    if cu_k.numel() != B_ + 1 or B_ < 0:
-        raise ValueError("cu_q and cu_k must both hold B + 1 entries")
-    device = q.device
-    out, lse, ldo, ldoh, ldl = _out_lse(out, lse, Tq, H, 128, device)
-    size = lib().idx_latent_prefill_workspace_size(Tq, Tk, H)
-    ws, ws_bytes = _latent_ws(workspace, size, device)
-    args = (_ptr(q), ldq, ldqh, _ptr(k), ldk, ldkh, _ptr(k_rope), ldr, _ptr(v), ldv, ldvh,
-            _ptr(cu_q), _ptr(cu_k), B_, Tq, Tk, H, 128, LATENT_ROPE, 128, scale, int(causal),
-            _ptr(out), ldo, ldoh, _ptr(lse), ldl, _ptr(ws), ws_bytes)
-    return args, (q, k, k_rope, v, cu_q, cu_k, out, lse, ws), 2 if size else 1
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return idx_paged_latent_attention(q, kv_pages, page_size, fmt, block_table,
+                                              context_lens, next_n, scale, max_model_len,
+                                              ctx_per_row, out, lse, workspace)
+    return (_calls or _latent_calls()).paged_attention(False, q, kv_pages, page_size, fmt,
+                                                       block_table, context_lens, next_n, scale,
+                                                       max_model_len, ctx_per_row, out, lse,
+                                                       workspace)
 
 
 def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
@@ -873,18 +740,19 @@ def prepare_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=
     [Tq, H, 128], lse fp32 [Tq, H] and workspace as in prepare_latent_attention
     (the size is latent_prefill_workspace_size(Tq, Tk, H))."""
     return Prepared("idx_latent_prefill",
-                    *_latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
-                                          workspace))
+                    *_latent_calls().prefill(True, q, k, k_rope, v, cu_q, cu_k, scale, causal, out,
+                                             lse, workspace))
 
 
 def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
                        workspace=True, stream=None):
     """(out, lse) of the expanded attention of ragged sequences."""
-    with _on(stream):
-        args, keep, _ = _latent_prefill_args(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
-                                             workspace)
-        _run("idx_latent_prefill", args, None)
-    return keep[6], keep[7]
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal, out, lse,
+                                      workspace)
+    return (_calls or _latent_calls()).prefill(False, q, k, k_rope, v, cu_q, cu_k, scale, causal,
+                                               out, lse, workspace)
 
 
 def idx_debug_wait_expiry(which: int, limit_ns: int, stream=None):

@@ -1,8 +1,10 @@
-"""Builds libidx.so (the C ABI of the indexer) in-tree with nvcc for sm_103a.
+"""Builds libidx.so (the C ABI of the indexer) in-tree with nvcc for sm_103a,
+and the host extension of the latent calls.
 
 The translation units are compiled in parallel and linked into
-``sparse_attention_indexer_mxfp4_gb300/_build/libidx.so``.  Rebuilds only when
-a source or header is newer than the library.
+``sparse_attention_indexer_mxfp4_gb300/_build/libidx.so``; the extension, which
+needs torch's headers, becomes ``_latent_calls.so`` beside it.  Rebuilds only
+when a source or header is newer than the two.
 """
 from __future__ import annotations
 
@@ -11,12 +13,16 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+from importlib.util import find_spec
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libidx.so")
+CALLS = os.path.join(BUILD, "_latent_calls.so")
+CALLS_SRC = os.path.join(CSRC, "bind_latent.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
          "-Xptxas", "-v"]
@@ -34,15 +40,25 @@ def sources() -> list[str]:
 
 
 def _inputs() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+    return (sources() + [CALLS_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) +
             glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "idx.h")])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(p) <= t for p in _inputs())
+
+
+def _calls_command(out: str) -> list[str]:
+    torch = os.path.dirname(find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    include = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"],
+               os.path.join(torch, "include"), os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", *(f"-I{i}" for i in include), CALLS_SRC,
+            "-o", out, "-L" + os.path.join(torch, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu",
+            "-ltorch_cuda", "-ltorch_python"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -50,7 +66,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
-    procs = []
+    calls = CALLS + f".{os.getpid()}.tmp"
+    procs = [(CALLS_SRC, subprocess.Popen(_calls_command(calls), stdout=subprocess.PIPE,
+                                          stderr=subprocess.STDOUT, text=True))]
     objs = []
     for src in sources():
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
@@ -66,10 +84,11 @@ def build(force: bool = False, verbose: bool = False) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError(f"nvcc failed on {failed}")
+        raise RuntimeError(f"the compiler failed on {failed}")
     tmp = LIB + f".{os.getpid()}.tmp"
     subprocess.check_call([nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    os.replace(calls, CALLS)
     return LIB
 
 

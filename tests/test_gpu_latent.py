@@ -593,3 +593,42 @@ def test_nothing_to_do():
     out, lse = B.idx_latent_prefill(bf(0, 4, 192), bf(3, 4, 128), bf(3, 64), bf(3, 4, 128), i32(2), i32(2), SCALE)
     assert out.shape == (0, 4, 128)
     _clean()
+
+
+@pytest.mark.parametrize("H,rows,mix", [(16, 700, (0, 3)), (16, 160, (0, 200)), (64, 153, (0, 130)), (64, 40, (60, 70)),
+                                        (128, 90, (1, 500)), (24, 19, (300, 2000)), (64, 9, (1000, 1100)),
+                                        (3, 2, (5000, 9000))])
+def test_sparse_random_lists(H, rows, mix):
+    """Shares that begin and end anywhere in a list of rows, within what a row
+    is charged too; the bits do not change from call to call."""
+    rng = np.random.default_rng(rows + H)
+    lens = rng.integers(mix[0], mix[1] + 1, rows)
+    pool, slots, indptr, q, qv = _sparse_case(rng, ref.FP8, lens, H, 64)
+    args = _dev(pool), 64, ref.FP8, _dev(slots), _dev(indptr), SCALE
+    out, lse = B.idx_latent_attention(q, *args)
+    _clean()
+    some = rng.choice(rows, min(rows, 12), replace=False)
+    _check_sparse(pool, ref.FP8, 64, slots, indptr, qv, out, lse, rows=some)
+    again, lse2 = B.idx_latent_attention(q, *args)
+    _clean()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+
+
+@pytest.mark.parametrize("H,seqs,longest", [(1, 40, 300), (3, 12, 700), (5, 7, 1500), (16, 3, 900), (2, 150, 140)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_random_packs(H, seqs, longest, causal):
+    """Blocks of one and two query tiles in every order, cut by shares and not,
+    with contexts before some of the prompts and rows without keys."""
+    rng = np.random.default_rng(H * 1000 + seqs)
+    lq = rng.integers(0, longest, seqs)
+    lk = np.maximum(0, lq + rng.integers(-60, 300, seqs))
+    cq, ck, qt, q, kvt, kv, latt, lat = _prefill_case(rng, lq, lk, H)
+    call = lambda: B.idx_latent_prefill(qt, kvt[..., :128], latt[:, 512:], kvt[..., 128:], _dev(cq), _dev(ck),  # noqa: E731
+                                        SCALE, causal=causal)
+    out, lse = call()
+    _clean()
+    picked = sorted(rng.choice(seqs, min(seqs, 6), replace=False))
+    _check_prefill(cq, ck, q, kv, lat[:, 512:], out, lse, causal, seqs=picked)
+    again, lse2 = call()
+    _clean()
+    assert torch.equal(out, again) and torch.equal(lse, lse2)

@@ -188,26 +188,30 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
 // halving the values a lane carries at every step (CNT - 1 exchanges, not 3
 // CNT).  Lane l is left with CNT / 8 results (one, for fewer than eight) in
 // v[0 ..]; returns which value v[0] is.
+template <int O, int CNT, int SIZE, typename Op>
+__device__ __forceinline__ int reduce_step(float (&v)[SIZE], int lane, Op op)
+{
+    if constexpr (O < 4) {
+        return 0;
+    } else if constexpr (CNT > 1) {
+        constexpr int H = CNT / 2;
+        const bool up = lane & O;
+        #pragma unroll
+        for (int e = 0; e < H; ++e) {
+            const float got = __shfl_xor_sync(0xffffffffu, up ? v[e] : v[e + H], O);
+            v[e] = op(up ? v[e + H] : v[e], got);
+        }
+        return (up ? H : 0) + reduce_step<O / 2, H>(v, lane, op);
+    } else {
+        v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], O));
+        return reduce_step<O / 2, 1>(v, lane, op);
+    }
+}
+
 template <int CNT, typename Op>
 __device__ __forceinline__ int reduce_rows(float (&v)[CNT], int lane, Op op)
 {
-    int base = 0;
-    #pragma unroll
-    for (int o = 16, n = CNT; o >= 4; o >>= 1) {
-        if (n > 1) {
-            n >>= 1;
-            const bool up = lane & o;
-            #pragma unroll
-            for (int e = 0; e < n; ++e) {
-                const float got = __shfl_xor_sync(0xffffffffu, up ? v[e] : v[e + n], o);
-                v[e] = op(up ? v[e + n] : v[e], got);
-            }
-            base += up ? n : 0;
-        } else {
-            v[0] = op(v[0], __shfl_xor_sync(0xffffffffu, v[0], o));
-        }
-    }
-    return base;
+    return reduce_step<16, CNT>(v, lane, op);
 }
 
 template <int N>

@@ -1088,9 +1088,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 // blockIdx.x: the row's entry of ws_cut; blockIdx.y: a quad of columns (MANY:
 // and 128 latents); blockIdx.z: the group.  The pieces lie in L2, a thousand
 // cycles away or more, so a thread asks for four pieces at once, a thread a
-// latent (of all four tiles of them), and where a row has many, eight teams of
-// threads take four pieces each.
-constexpr int kTeams = 8;
+// latent (of all four tiles of them), and where a row has many, four teams of
+// threads take four pieces each in turn (one row of 16 heads on 2048 keys 11.0 us
+// in all; with eight teams, whose threads have half the registers, 11.7; two
+// 14.9).
+constexpr int kTeams = 4;
 
 template <int N, bool MANY>
 __global__ void __launch_bounds__(MANY ? 128 * kTeams : 128) latent_join_kernel(const AttnArgs a)
@@ -1229,10 +1231,11 @@ idx_status launch_attn(const CUtensorMap &tm, const AttnArgs &a, int shares, cud
     cudaError_t e = launch_pdl(kern, dim3(a.groups, shares), dim3(kThreads), C::SMEM, s, tm, a);
     if (e == cudaSuccess && shares > 1 && !a.uncut) {
         const int entries = a.by_row ? a.rows : shares - 1;
-        // Teams while their blocks, of which an SM holds two, run at once: at
-        // 2048 keys 16 columns x 4 rows 13.3 us (without teams 20.6), x 12 18.3
-        // (19.2), x 28 24.0 (21.3); 64 columns x 2 14.9 (18.5), x 16 37.7 (22.5).
-        if (entries * N * a.groups <= 2 * sm_count())
+        // Teams up to three blocks of them an SM, one at a time; us with and
+        // without: at 2048 keys 16 columns x 4 rows 12.0 and 20.6, 32 columns x 12
+        // 19.0 and 20.4, x 16 21.0 and 19.7; 64 columns x 6 20.7 and 24.0, x 10 24.0
+        // and 21.1.
+        if (entries * N * a.groups <= 3 * sm_count())
             e = launch_pdl(latent_join_kernel<N, true>, dim3(entries, N, a.groups),
                            dim3(128 * kTeams), 0, s, a);
         else

@@ -24,13 +24,13 @@
 // share are finished there; the others leave unnormalised sums with their
 // maximum in scratch and a second kernel joins them in share order.
 //
-// What bounds it: with 64 columns shared memory's data path, about 3300 of 3350
+// What bounds it: with 64 columns shared memory's data path, about 3250 of 3350
 // cycles a tile of 8-bit tokens (wavefronts: 36 x 32 and 16 x 48 of the products'
 // operands, 700 of stores, 700 of loads and shuffles): 2048 rows x 64 heads x
-// 2048 slots 814 us, 720 TFLOP/s, the tensor pipe 47 % busy.  With 16 columns
+// 2048 slots 799 us, 730 TFLOP/s, the tensor pipe 47 % busy.  With 16 columns
 // the same path (2450 of 2700 cycles) and DRAM share it: 32 contexts of 4 to 32
 // thousand 8-bit tokens 104 us, 4.0 TB/s.  Bf16 tokens need no widening: four
-// contexts of 100 to 131 thousand, 32 columns, 104 us with the joining kernel,
+// contexts of 100 to 131 thousand, 32 columns, 102 us with the joining kernel,
 // 5.6 TB/s while this one runs.  Few rows wait: about 9 thousand cycles until a
 // CTA has its first tokens, twice a table and then what it names.
 //
@@ -186,7 +186,8 @@ __device__ __forceinline__ bool next_seg(const AttnArgs &a, Walk &w, Seg &s)
 
 // Reduces each of CNT values over the eight lanes that differ in bits 2-4,
 // halving the values a lane carries at every step (CNT - 1 exchanges, not 3
-// CNT).  Lane l is left with CNT / 8 results (one, for fewer than eight) in
+// CNT).  Steps are instances of their own: as a loop whose count halves, the
+// values went through local memory (64 columns 3 % slower).  Lane l is left with CNT / 8 results (one, for fewer than eight) in
 // v[0 ..]; returns which value v[0] is.
 template <int O, int CNT, int SIZE, typename Op>
 __device__ __forceinline__ int reduce_step(float (&v)[SIZE], int lane, Op op)

@@ -610,7 +610,9 @@ idx_status idx_latent_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_
  * idx_paged_mqa_logits (context_lens, ctx_per_row), clamped to
  * [0, max_model_len]; token t is in page block_table[b, t / page_size],
  * bt_stride >= ceil(max_model_len / page_size).  Tokens of a page outside
- * the pool are left out and set IDX_DEV_BAD_PAGE.
+ * the pool are left out and set IDX_DEV_BAD_PAGE.  Tokens at or past ke take
+ * no part in row j, whatever they hold and whichever row of the sequence sees
+ * them.
  * Supported: as above, and next_n * ceil(H / 64) at most the SMs (152).
  * ---------------------------------------------------------------------- */
 idx_status idx_paged_latent_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,

@@ -41,3 +41,97 @@ def test_nan_code_shows(code, latent, scale, H):
                         _dev(np.array([0, page], np.int32)), back)
     _clean()
     assert torch.isnan(back[s % page, latent]) and torch.isnan(back[s % page, :512]).sum() == 1
+
+
+# ------------------------------------------- tokens that a row is not to see
+
+
+def _token_put(pool, fmt, page, slot, what):
+    """Makes one cached token NaN, or infinite in latent 7."""
+    line, o = pool[slot // page], slot % page
+    if fmt == ref.BF16:
+        word = {"nan": 0x7fc0, "inf": 0x7f80, "-inf": 0xff80}[what]
+        line[o * 1152 + 14:o * 1152 + 16] = word & 255, word >> 8
+    elif what == "nan":
+        line[page * 640 + o * 8 + 3] = 255  # latents 192 .. 255
+    else:
+        line[o * 512:o * 512 + 64] = 0
+        line[o * 512 + 7] = {"inf": 0x7e, "-inf": 0xfe}[what]  # 448 * 2^127 is past bf16
+        line[page * 640 + o * 8] = 254
+
+
+def _attend_ieee(q, tok, seen):
+    """The formula with IEEE's rules: a NaN score or an infinite one at the top
+    makes the row NaN; a weight of zero times an infinity is NaN."""
+    t = tok[:seen].copy()
+    t[np.isinf(t) | (np.abs(t) > 3.39e38)] *= np.inf
+    with np.errstate(invalid="ignore"):
+        s = q @ t.T
+    every = np.isnan(s).any(1) | (s == np.inf).any(1)
+    lost = ~np.isfinite(t[:, :512]).all(0)  # latents
+    keep = np.isfinite(t).all(1)
+    return every, lost, ref.attend(q, t[keep], t[keep][:, :512], SCALE)
+
+
+def _check_hidden(out, lse, q, tok, ends):
+    for r, end in enumerate(ends):
+        every, lost, want = _attend_ieee(q[r], tok, end)
+        assert np.isnan(out[r][every]).all() and np.isnan(lse[r][every]).all()
+        o, l, pv, mag = (x[~every] for x in want)
+        assert np.isnan(out[r][~every][:, lost]).all()
+        ref.check(out[r][~every][:, ~lost], lse[r][~every], (o[:, ~lost], l, pv[:, ~lost], mag))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("what", ["nan", "inf", "-inf"])
+@pytest.mark.parametrize("ctx,next_n,H", [(130, 2, 16), (65, 2, 64), (66, 3, 8), (3, 3, 16), (64, 4, 1), (128, 2, 128),
+                                          (2000, 2, 24), (2, 2, 40)])
+def test_paged_tokens_past_a_rows_end(fmt, what, ctx, next_n, H):
+    """The newest tokens of a sequence are not finite: rows that end before them are as if they were not there."""
+    rng = np.random.default_rng(ctx + H)
+    pool, bt, slots = _paged_case(rng, fmt, [ctx, 70], 64)
+    for k in {0, next_n - 2}:  # the last token, and the oldest that some row does not see
+        _token_put(pool, fmt, 64, slots[0][ctx - 1 - k], what)
+    qt, q = _bf16(rng.standard_normal((2 * next_n, H, 576)))
+    out, lse = B.idx_paged_latent_attention(qt, _dev(pool), 64, fmt, _dev(bt), _dev(np.array([ctx, 70], np.int32)),
+                                            next_n, SCALE, max(ctx, 70))
+    _clean()
+    out, lse = _np(out), _np(lse)
+    for b, c in enumerate([ctx, 70]):
+        rows = slice(b * next_n, (b + 1) * next_n)
+        tok = ref.read_tokens(pool, fmt, 64, slots[b])
+        _check_hidden(out[rows], lse[rows], q[rows], tok, [max(0, c - next_n + j + 1) for j in range(next_n)])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("what", ["nan", "inf"])
+@pytest.mark.parametrize("per_row,bad,H", [([0, 130, 64, 1], [64], 16), ([0, 130, 64, 1], [0], 64), ([0, 1], [0], 16),
+                                           ([700, 3000, 2001], [700, 2000, 2999], 16), ([-4, 5000], [1, 3000], 128),
+                                           ([64, 64, 200], [100, 150], 8)])
+def test_paged_lengths_per_row_hide_tokens(fmt, what, per_row, bad, H):
+    """Lengths given row by row, far apart: a row of none stays zeros, a short one its own."""
+    rng = np.random.default_rng(sum(per_row) + H)
+    longest = max(per_row)
+    pool, bt, slots = _paged_case(rng, fmt, [longest], 64)
+    for t in bad:
+        _token_put(pool, fmt, 64, slots[0][t], what)
+    qt, q = _bf16(rng.standard_normal((len(per_row), H, 576)))
+    out, lse = B.idx_paged_latent_attention(qt, _dev(pool), 64, fmt, _dev(bt), _dev(np.array(per_row, np.int32)),
+                                            len(per_row), SCALE, longest, ctx_per_row=True)
+    _clean()
+    _check_hidden(_np(out), _np(lse), q, ref.read_tokens(pool, fmt, 64, slots[0]), [max(0, n) for n in per_row])
+
+
+def test_paged_hidden_nan_code():
+    """A NaN code past a row's end, among the largest finite ones."""
+    rng = np.random.default_rng(4)
+    pool, bt, slots = _paged_case(rng, ref.FP8, [100], 64)
+    for s in slots[0]:
+        pool[s // 64, (s % 64) * 512:][:512:5] = rng.choice([0x7e, 0xfe, 0x77, 0xf7, 0x6f], 103)
+    s = slots[0][99]
+    pool[s // 64, (s % 64) * 512 + 9] = 0xff
+    qt, q = _bf16(0.01 * rng.standard_normal((2, 16, 576)))
+    out, lse = B.idx_paged_latent_attention(qt, _dev(pool), 64, ref.FP8, _dev(bt), _dev(np.array([100], np.int32)), 2,
+                                            SCALE, 100)
+    _clean()
+    _check_hidden(_np(out), _np(lse), q, ref.read_tokens(pool, ref.FP8, 64, slots[0]), [99, 100])

@@ -160,18 +160,25 @@ def version() -> str:
 
 class Prepared:
     """One validated library call with its arguments already marshalled;
-    calling it launches on the given (or current) stream."""
+    calling it launches on the given (or current) stream, which is one of the
+    device that the call was prepared for (None: not checked)."""
 
-    __slots__ = ("fn", "args", "name", "keep", "kernels")
+    __slots__ = ("fn", "args", "name", "keep", "kernels", "device")
 
-    def __init__(self, name, args, keep, kernels=1):
+    def __init__(self, name, args, keep, kernels=1, device=None):
         self.fn = getattr(lib(), name)
         self.name = name
         self.args = tuple(args)
         self.keep = keep  # tensors that must outlive the call
         self.kernels = kernels  # kernel launches per call
+        self.device = device
 
     def __call__(self, stream=None):
+        if self.device is not None:
+            on = torch.cuda.current_device()
+            if on != self.device or (stream is not None and stream.device_index != on):
+                raise ValueError(f"{self.name} was prepared for cuda:{self.device}: the current "
+                                 "device and the stream have to be its")
         _check(self.fn(*self.args, _stream(stream)), self.name)
 
 

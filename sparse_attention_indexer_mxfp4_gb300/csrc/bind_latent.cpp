@@ -8,11 +8,13 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <climits>
+#include <initializer_list>
 #include <optional>
 #include <string>
 
@@ -65,11 +67,29 @@ float float_of(PyObject *o)
     return (float)v;
 }
 
+// Every tensor of a call lives on one device, and it is the current one: the
+// stream, the scratch's size and the launch are the current device's.
+void on_one_device(std::initializer_list<const at::Tensor *> tensors)
+{
+    const at::Tensor &first = **tensors.begin();
+    for (const at::Tensor *t : tensors) {
+        if (!t->defined())
+            continue;
+        if (!t->is_cuda())
+            refuse("indexer tensors must live on a CUDA device");
+        if (t->device() != first.device())
+            refuse("tensors of one call are on " + first.device().str() + " and " +
+                   t->device().str());
+    }
+    const int current = c10::cuda::current_device();
+    if (first.device().index() != current)
+        refuse("tensors on " + first.device().str() + ", but the current device is cuda:" +
+               std::to_string(current));
+}
+
 template <typename T>
 T *address(const at::Tensor &t)
 {
-    if (!t.is_cuda())
-        refuse("indexer tensors must live on a CUDA device");
     return static_cast<T *>(t.data_ptr());
 }
 
@@ -129,8 +149,7 @@ struct Outputs {
     int64_t ld_row, ld_head, ld_lse = 0;
     size_t ws_bytes = 0;
 
-    Outputs(PyObject *out_o, PyObject *lse_o, PyObject *ws_o, const at::Tensor &q, int64_t dim,
-            size_t size)
+    Outputs(PyObject *out_o, PyObject *lse_o, PyObject *ws_o, const at::Tensor &q, int64_t dim)
     {
         const int64_t R = q.size(0), H = q.size(1);
         if (out_o != Py_None) {
@@ -150,8 +169,12 @@ struct Outputs {
             ws = tensor_of(ws_o, "workspace");
             ws_bytes = ws.numel() * ws.element_size();
         }
-        address<void>(q);
-        if (out_o == Py_None)
+    }
+    // The ones that were not given, once the device is known to be good.
+    void make(PyObject *lse_o, PyObject *ws_o, const at::Tensor &q, int64_t dim, size_t size)
+    {
+        const int64_t R = q.size(0), H = q.size(1);
+        if (!out.defined())
             out = empty({R, H, dim}, at::kBFloat16, q.device());
         if (lse_o == Py_None)
             lse = empty({R, H}, at::kFloat, q.device());
@@ -224,12 +247,13 @@ PyObject *arguments(A... args)
 }
 
 // Launches (returns `result`), or with prepare returns (arguments, tensors to
-// keep, launches of the call).
+// keep, launches of the call, device).
 template <typename F, typename R, typename K, typename... A>
 PyObject *call(bool prepare, F f, const char *name, int launches, R result, K kept, A... args)
 {
     if (prepare)
-        return Py_BuildValue("(NNi)", arguments(args...), kept(), launches);
+        return Py_BuildValue("(NNii)", arguments(args...), kept(), launches,
+                             (int)c10::cuda::current_device());
     launch(f, name, args...);
     return result();
 }
@@ -242,25 +266,26 @@ PyObject *store(PyObject *, PyObject *const *a, Py_ssize_t)
     need_count(slots, T, "slot_mapping");
     if ((a[2] == Py_None) != (a[3] == Py_None))
         refuse("positions and cos_sin come together");
-    const int32_t *positions = nullptr;
-    const float *cos_sin = nullptr, *weight = nullptr;
+    at::Tensor p, c, w;
     int rows = 0;
     int64_t ld = 0;
     if (a[3] != Py_None) {
-        const at::Tensor &p = need(a[2], at::kInt, "positions"), &c = tensor_of(a[3], "cos_sin");
+        p = need(a[2], at::kInt, "positions");
+        c = tensor_of(a[3], "cos_sin");
         need_count(p, T, "positions");
         if (c.scalar_type() != at::kFloat || c.dim() != 2 || c.stride(1) != 1 || c.size(1) < kRope)
             refuse("cos_sin must be float32 [positions, " + std::to_string(kRope) + "]");
-        positions = address<int32_t>(p);
-        cos_sin = address<float>(c);
         rows = count(c.size(0), "cos_sin");
         ld = c.stride(0);
     }
     if (a[4] != Py_None) {
-        const at::Tensor &w = need(a[4], at::kFloat, "norm_weight");
+        w = need(a[4], at::kFloat, "norm_weight");
         need_count(w, kLatent, "norm_weight");
-        weight = address<float>(w);
     }
+    on_one_device({&kv, &pages, &slots, &p, &c, &w});
+    const int32_t *positions = c.defined() ? address<int32_t>(p) : nullptr;
+    const float *cos_sin = c.defined() ? address<float>(c) : nullptr;
+    const float *weight = w.defined() ? address<float>(w) : nullptr;
     return call(
         a[0] == Py_True, f_store, "idx_latent_store", 1, [] { Py_RETURN_NONE; },
         [&] {
@@ -281,12 +306,13 @@ PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t)
     const int64_t B = cu.numel() - 1;
     if (table.dim() != 2 || table.size(0) < B || B < 0)
         refuse("block_table must be [B, blocks] and cu_lens [B + 1]");
-    const int32_t *starts = nullptr;
+    at::Tensor s;
     if (a[7] != Py_None) {
-        const at::Tensor &s = need(a[7], at::kInt, "seq_starts");
+        s = need(a[7], at::kInt, "seq_starts");
         need_count(s, B, "seq_starts");
-        starts = address<int32_t>(s);
     }
+    on_one_device({&pages, &out, &table, &cu, &s});
+    const int32_t *starts = s.defined() ? address<int32_t>(s) : nullptr;
     return call(
         a[0] == Py_True, f_gather, "idx_latent_gather", 1, [&] { return keep(a[6]); },
         [&] {
@@ -306,8 +332,10 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t)
     const at::Tensor &slots = need(a[5], at::kInt, "slots"), &indptr = need(a[6], at::kInt, "indptr");
     const int R = count(q.size(0), "q"), H = count(q.size(1), "q");
     need_count(indptr, (int64_t)R + 1, "indptr");
+    Outputs o(a[8], a[9], a[10], q, kLatent);
+    on_one_device({&q, &pages, &slots, &indptr, &o.out, &o.lse, &o.ws});
     const size_t size = f_attention_size(R, H, slots.numel());
-    const Outputs o(a[8], a[9], a[10], q, kLatent, size);
+    o.make(a[9], a[10], q, kLatent, size);
     // the attention, and with scratch the joining kernel
     return call(
         a[0] == Py_True, f_attention, "idx_latent_attention", size ? 2 : 1,
@@ -338,8 +366,10 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t)
     if (table.dim() != 2 || table.size(0) < B)
         refuse("block_table must be [" + std::to_string(B) + ", blocks]");
     const int longest = int_of(a[9], "max_model_len");
+    Outputs o(a[11], a[12], a[13], q, kLatent);
+    on_one_device({&q, &pages, &table, &lens, &o.out, &o.lse, &o.ws});
     const size_t size = f_attention_size(R, H, longest);
-    const Outputs o(a[11], a[12], a[13], q, kLatent, size);
+    o.make(a[12], a[13], q, kLatent, size);
     return call(
         a[0] == Py_True, f_paged, "idx_paged_latent_attention", size ? 2 : 1,
         [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
@@ -369,8 +399,10 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t)
     const int64_t B = cu_q.numel() - 1;
     if (cu_k.numel() != B + 1 || B < 0)
         refuse("cu_q and cu_k must both hold B + 1 entries");
+    Outputs o(a[9], a[10], a[11], q, kV);
+    on_one_device({&q, &k, &rope, &v, &cu_q, &cu_k, &o.out, &o.lse, &o.ws});
     const size_t size = f_prefill_size(Tq, Tk, H);
-    const Outputs o(a[9], a[10], a[11], q, kV, size);
+    o.make(a[10], a[11], q, kV, size);
     return call(
         a[0] == Py_True, f_prefill, "idx_latent_prefill", size ? 2 : 1,
         [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },

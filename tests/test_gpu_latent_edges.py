@@ -7,7 +7,10 @@ import torch
 
 import latent_ref as ref
 from sparse_attention_indexer_mxfp4_gb300 import _binding as B
-from test_gpu_latent import SCALE, _bf16, _check_prefill, _check_sparse, _clean, _dev, _np, _paged_case, _prefill_case, _sparse_case
+from test_gpu_latent import (SCALE, _bf16, _check_prefill, _check_sparse, _clean, _dev, _np, _paged_case,
+                             _prefill_case, _sparse_case)
+from test_latent_calls_host import CALLS
+from test_latent_edges_host import Elsewhere
 
 pytestmark = pytest.mark.gpu
 FMTS = [ref.BF16, ref.FP8]
@@ -135,3 +138,16 @@ def test_paged_hidden_nan_code():
                                             SCALE, 100)
     _clean()
     _check_hidden(_np(out), _np(lse), q, ref.read_tokens(pool, ref.FP8, 64, slots[0]), [99, 100])
+
+
+# ------------------------------------------------------------------- devices
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_tensors_of_a_device_that_is_not_current(name):
+    """Refused before a pointer is taken: the tensors have no storage."""
+    call, prepare, good = CALLS[name]
+    args = [Elsewhere(x.shape, x.dtype, "cuda:1") if torch.is_tensor(x) else x for x in good()]
+    for f in (call, prepare):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            f(*args)

@@ -1,0 +1,76 @@
+"""Host checks of the latent calls where a wrong argument would reach the
+device: tensors of several devices, scratch that is not one piece, prepared
+calls under another device.  The devices are those of tensors without storage."""
+import pytest
+import torch
+
+from sparse_attention_indexer_mxfp4_gb300 import _binding as B
+from test_latent_calls_host import CALLS
+
+BF, U8 = torch.bfloat16, torch.uint8
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on a device, without storage."""
+
+    @staticmethod
+    def __new__(cls, shape, dtype, device):
+        return torch.Tensor._make_wrapper_subclass(cls, shape, dtype=dtype, device=device)
+
+    @classmethod
+    def __torch_dispatch__(cls, func, types, args=(), kwargs=None):
+        raise RuntimeError("a tensor without storage was computed with")
+
+
+def _on(device, t):
+    return Elsewhere(t.shape, t.dtype, device)
+
+
+def _good(name, device="cuda:0"):
+    return [_on(device, x) if torch.is_tensor(x) else x for x in CALLS[name][2]()]
+
+
+@pytest.mark.parametrize("name", sorted(CALLS))
+def test_tensors_of_two_devices(name):
+    call, prepare, _ = CALLS[name]
+    tensors = [i for i, x in enumerate(_good(name)) if torch.is_tensor(x)]
+    for f in (call, prepare):
+        for i in tensors:
+            args = _good(name)
+            args[i] = _on("cuda:1", args[i])
+            with pytest.raises(ValueError, match="cuda:0 and cuda:1|cuda:1 and cuda:0"):
+                f(*args)
+
+
+@pytest.mark.parametrize("name,out", [("attention", (3, 16, 512)), ("paged", (4, 16, 512)), ("prefill", (5, 4, 128))])
+def test_outputs_and_scratch_of_another_device(name, out):
+    call, prepare, _ = CALLS[name]
+    for f in (call, prepare):
+        for more in (dict(out=_on("cuda:1", torch.empty(out, dtype=BF))),
+                     dict(lse=_on("cuda:1", torch.empty(out[:2]))),
+                     dict(workspace=_on("cuda:1", torch.empty(64, dtype=U8)))):
+            with pytest.raises(ValueError, match="cuda:0 and cuda:1"):
+                f(*_good(name), **more)
+
+
+class _Stream:
+    def __init__(self, device):
+        self.device_index, self.cuda_stream = device, 7
+
+
+@pytest.mark.parametrize("current,stream,launches", [(0, None, True), (1, None, False), (0, 0, True), (0, 1, False),
+                                                     (1, 0, False), (1, 1, False)])
+def test_prepared_call_under_another_device(monkeypatch, current, stream, launches):
+    made = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current)
+    monkeypatch.setattr(B, "_raw_stream", lambda device: 5)
+    p = B.Prepared("idx_latent_store", (1, 2), None, 1, 0)
+    p.fn = lambda *a: made.append(a) or 0
+    s = None if stream is None else _Stream(stream)
+    if launches:
+        p(s)
+        assert made == [(1, 2, 5 if s is None else 7)]
+    else:
+        with pytest.raises(ValueError, match="prepared for cuda:0"):
+            p(s)
+        assert not made

@@ -167,6 +167,8 @@ struct Outputs {
         }
         if (ws_o != Py_True && ws_o != Py_None) {
             ws = tensor_of(ws_o, "workspace");
+            if (!ws.is_contiguous())  // its bytes are counted, and have to be there
+                refuse("workspace must be contiguous");
             ws_bytes = ws.numel() * ws.element_size();
         }
     }

@@ -74,3 +74,13 @@ def test_prepared_call_under_another_device(monkeypatch, current, stream, launch
         with pytest.raises(ValueError, match="prepared for cuda:0"):
             p(s)
         assert not made
+
+
+@pytest.mark.parametrize("name", ["attention", "paged", "prefill"])
+@pytest.mark.parametrize("ws", [torch.zeros(1, dtype=U8).expand(1 << 24), torch.zeros(1 << 20, dtype=U8)[::2]])
+def test_scratch_that_is_not_one_piece(name, ws):
+    """Its elements would be counted as bytes that lie one after another."""
+    call, prepare, good = CALLS[name]
+    for f in (call, prepare):
+        with pytest.raises(ValueError, match="workspace must be contiguous"):
+            f(*good(), workspace=ws)

@@ -67,6 +67,7 @@ typedef enum {
 #define IDX_DEV_BAD_CANDIDATE 2u /* reserved: candidate ids are range-checked and ignored */
 #define IDX_DEV_TIMEOUT 4u       /* a bounded pipeline wait ran out; outputs undefined */
 #define IDX_DEV_BAD_POSITION 8u  /* a producer's position outside its cos/sin table */
+#define IDX_DEV_BAD_BOUNDS 16u   /* bounds of sequences that their tensors do not hold */
 
 /* ------------------------------------------------------------------------
  * idx_mqa_logits -- non-paged logits for one key sequence.
@@ -558,7 +559,9 @@ idx_status idx_latent_store(const uint16_t *kv, int64_t ld_kv, const int32_t *po
  *               cu_lens[b + 1]) of out are the tokens seq_starts[b],
  *               seq_starts[b] + 1, ... of sequence b.
  *   seq_starts  int32 [B] or NULL (0).
- *   N           rows of out; rows at or past cu_lens[B] are not written.
+ *   N           rows of out; rows at or past cu_lens[B] are not written, and
+ *               a cu_lens[B] past N sets IDX_DEV_BAD_BOUNDS (the N rows are
+ *               written).
  *   out         bf16 bits [N, ld_out], ld_out >= 576 a multiple of 8,
  *               16-byte aligned: latents, then the rotated elements.
  * A token whose page is outside the table or the pool is written as zeros
@@ -643,7 +646,9 @@ size_t idx_latent_attention_workspace_size(int R, int H, int64_t max_keys);
  *   cu_q, cu_k  int32 [B + 1], ascending from 0, ends at most Tq and Tk: the
  *           rows of each sequence.  causal: query i of a sequence with Lq
  *           queries and Lk keys attends to keys [0, i + Lk - Lq], so the
- *           last query sees every key; otherwise to all Lk.
+ *           last query sees every key; otherwise to all Lk.  Bounds that
+ *           descend or leave [0, Tq] or [0, Tk] are clamped and set
+ *           IDX_DEV_BAD_BOUNDS.
  *   out     bf16 bits [Tq, H, 128], strides ldo_row, ldo_head.
  *   lse     fp32 [Tq, ld_lse] (ld_lse >= H) or NULL, as idx_latent_attention.
  *           A query with no key gets zeros and -inf; rows of q outside every

@@ -5,6 +5,7 @@ hand-written sm_103a CUDA kernels in ``csrc/``; this package only builds it,
 loads it and marshals torch tensors into its calls.
 """
 from ._binding import (  # noqa: F401
+    DEV_BAD_BOUNDS,
     DEV_BAD_PAGE,
     DEV_TIMEOUT,
     FMT_FP8,

@@ -33,6 +33,7 @@ _ERRORS = {1: "IDX_ERR_INVALID_ARG", 2: "IDX_ERR_UNSUPPORTED", 3: "IDX_ERR_WORKS
 DEV_BAD_PAGE = 1
 DEV_TIMEOUT = 4
 DEV_BAD_POSITION = 8
+DEV_BAD_BOUNDS = 16
 SLOT_DIRECT_ROWS = 4096  # above it the slot map runs a third (scan) kernel
 TOPK_CLUSTER_MAX_LEN = 262144  # rows the one-cluster-per-row top-k holds (8 x 32768 keys)
 

@@ -12,6 +12,7 @@ namespace idx {
 
 constexpr unsigned kDevBadPage = 1u;
 constexpr unsigned kDevTimeout = 4u;
+constexpr unsigned kDevBadBounds = 16u;
 
 IDX_DEVFN uint32_t smem_u32(const void *p)
 {

@@ -217,7 +217,9 @@ __global__ void __launch_bounds__(kCacheThreads)
     pdl_launch_dependents();
     const int lane = lane_id();
     const long long step = (long long)gridDim.x * (kCacheThreads / 32) * kGatherRows;
-    const int total = min(N, cu_lens[B]);
+    const int rows = cu_lens[B], total = min(N, rows);
+    if (rows > N && blockIdx.x == 0 && threadIdx.x == 0)
+        atomicOr(status, kDevBadBounds);
     for (long long first = ((long long)blockIdx.x * (kCacheThreads / 32) + (threadIdx.x >> 5)) *
                            kGatherRows;
          first < total; first += step) {

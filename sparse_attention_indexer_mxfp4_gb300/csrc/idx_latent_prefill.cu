@@ -295,6 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (b >= a.B)
             return 0;
         block_seq(a, cq, ck, k);
+        if (blockIdx.x == 0 && (cq[b] < 0 || cq[b + 1] < cq[b] || cq[b + 1] > a.Tq || ck[b] < 0 ||
+                                ck[b + 1] < ck[b] || ck[b + 1] > a.Tk))
+            atomicOr(a.status, kDevBadBounds);
         return tiles_of_seq(a, k.nq, k.nk);
     };
     int head_tiles = 0, mine, before;

@@ -49,7 +49,8 @@ class LatentLayer:
     def prefill(self, q, cu_q, block_table, cu_k, num_tokens, stream=None):
         """Expanded causal attention of prompt rows q bf16 [Tq, H, 192] (the
         last 64 rotated) over their sequences' num_tokens = cu_k[-1] cached
-        tokens.  Returns (out [Tq, H, 128], lse)."""
+        tokens (fewer set IDX_DEV_BAD_BOUNDS in the device status).  Returns
+        (out [Tq, H, 128], lse)."""
         n = num_tokens
         with B._on(stream):  # the products between the calls too
             tokens = torch.empty(n, LATENT + ROPE, dtype=torch.bfloat16, device=q.device)

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import latent_ref as ref
+from sparse_attention_indexer_mxfp4_gb300 import LatentLayer
 from sparse_attention_indexer_mxfp4_gb300 import _binding as B
 from test_gpu_latent import (SCALE, _bf16, _check_prefill, _check_sparse, _clean, _dev, _np, _paged_case,
                              _prefill_case, _sparse_case)
@@ -151,3 +152,44 @@ def test_tensors_of_a_device_that_is_not_current(name):
     for f in (call, prepare):
         with pytest.raises(ValueError, match="current device is cuda:0"):
             f(*args)
+
+
+# ------------------------------------------------------ bounds past the tensors
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_gather_tells_of_rows_that_do_not_fit(fmt):
+    rng = np.random.default_rng(2)
+    pool = ref.make_pool(rng, fmt, 3, 64)
+    out = torch.full((100, 576), 7.0, dtype=torch.bfloat16, device="cuda")
+    B.idx_latent_gather(_dev(pool), 64, fmt, _dev(np.array([[2, 1]], np.int32)), _dev(np.array([0, 101], np.int32)), out)
+    torch.cuda.synchronize()
+    assert B.idx_get_device_status() == B.DEV_BAD_BOUNDS
+    want = ref.read_tokens(pool, fmt, 64, np.concatenate([128 + np.arange(64), 64 + np.arange(36)]))
+    assert np.array_equal(_np(out), want)
+
+
+@pytest.mark.parametrize("cu_q,cu_k", [([0, 5, 11], [0, 9, 20]), ([0, 5, 10], [0, 9, 21]), ([0, 5, 10], [-1, 9, 20]),
+                                       ([0, 11, 10], [0, 9, 20])])
+def test_prefill_tells_of_bounds_past_its_tensors(cu_q, cu_k):
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    B.idx_latent_prefill(z(10, 2, 192), z(20, 2, 128), z(20, 64), z(20, 2, 128), _dev(np.array(cu_q, np.int32)),
+                         _dev(np.array(cu_k, np.int32)), SCALE)
+    torch.cuda.synchronize()
+    assert B.idx_get_device_status() == B.DEV_BAD_BOUNDS
+
+
+def test_layer_tells_of_too_few_tokens():
+    """A prefill told of fewer cached tokens than its bounds have is not silently cut."""
+    rng = np.random.default_rng(5)
+    t = lambda *s: torch.from_numpy(rng.standard_normal(s)).bfloat16().cuda()  # noqa: E731
+    layer = LatentLayer(t(2, 128, 512), t(2, 128, 512), torch.ones(512, device="cuda"),
+                        torch.ones(64, 64, device="cuda"), 4, 64)
+    layer.store(t(60, 576), torch.arange(60, dtype=torch.int32, device="cuda"), torch.arange(60, device="cuda"))
+    cu = torch.tensor([0, 60], dtype=torch.int32, device="cuda")
+    table = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    layer.prefill(t(60, 2, 192), cu, table, cu, 60)
+    _clean()
+    layer.prefill(t(60, 2, 192), cu, table, cu, 59)
+    torch.cuda.synchronize()
+    assert B.idx_get_device_status() == B.DEV_BAD_BOUNDS

@@ -583,6 +583,8 @@ idx_status idx_latent_gather(const uint8_t *kv_pages, int64_t page_stride_bytes,
  *   slots     int32, num_slots of them; row r attends to slots[indptr[r]]
  *             .. slots[indptr[r + 1] - 1] (a slot listed twice counts twice).
  *   indptr    int32 [R + 1], ascending; values are clamped to [0, num_slots].
+ *             One that descends, and lists 2^37 tokens or more by that, sets
+ *             IDX_DEV_BAD_BOUNDS and nothing is written.
  *   scale     multiplies the scores, > 0.
  *   out       bf16 bits [R, H, 512] with strides ldo_row, ldo_head (multiples
  *             of 8, 16-byte aligned).

@@ -618,26 +618,33 @@ __global__ void __launch_bounds__(kThreads, 1)
     // counts besides, over the threads
     const int chunk = (a.rows + kThreads - 1) / kThreads;
     const int r0 = min(a.rows, tid * chunk), r1 = min(a.rows, r0 + chunk);
-    int mine = 0;
+    // Rows of an ascending list have at most INT32_MAX / 4 tiles and two charges
+    // each together; one that descends can name its slots any number of times.
+    constexpr uint32_t kTooMany = INT32_MAX;
+    const auto plus = [](uint32_t x, uint32_t y) { return min(x + y, kTooMany); };
+    uint32_t own = 0;
     #pragma unroll 1
     for (int r = r0; r < r1; ++r)
-        mine += tiles_of(row_of(a, r).n) + a.charge;
-    int upto = mine;
+        own = plus(own, tiles_of(row_of(a, r).n) + a.charge);
+    const int mine = own;
+    uint32_t upto = own;
     #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, upto, o);
-        upto += lane >= o ? v : 0;
+        const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        upto = plus(upto, lane >= o ? v : 0);
     }
     int *wsum = reinterpret_cast<int *>(smax);
     if (lane == 31)
         wsum[warp] = upto;
     __syncthreads();
-    int total = 0, before = upto - mine;
+    uint32_t all = 0, lower = upto - own;
     #pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) {
-        total += wsum[i];
-        before += i < warp ? wsum[i] : 0;
+        all = plus(all, wsum[i]);
+        lower = plus(lower, i < warp ? wsum[i] : 0);
     }
+    const bool too_many = all == kTooMany;  // no CTA has a share
+    const int total = too_many ? 1 : all, before = lower;
     // equal shares, the first ones a tile longer
     const Group group = group_of(a, blockIdx.x);
     const int p = blockIdx.y, shares = min((int)gridDim.y, total);
@@ -673,9 +680,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!a.by_row && !a.uncut && blockIdx.x == 0 && tid == 0)
         a.ws_cut[p] = make_int4(-1, 0, 0, 0);
+    if (too_many && blockIdx.x == 0 && p == 0) {
+        if (tid == 0)
+            atomicOr(a.status, kDevBadBounds);
+        if (a.by_row && !a.uncut && tid < a.rows)  // fewer than SMs
+            a.ws_cut[tid] = make_int4(-1, 0, 0, 0);
+    }
     __syncthreads();
     const int tiles1 = p + 1 < shares ? (int)misc[3] : total - a.rows * a.charge;
-    const int left = p < shares ? tiles1 - (int)misc[2] : 0;
+    const int left = p < shares && !too_many ? tiles1 - (int)misc[2] : 0;
     if (a.hpg * a.rpg < N) {
         // columns without a head: their query rows are zeros
         #pragma unroll 1

@@ -193,3 +193,26 @@ def test_layer_tells_of_too_few_tokens():
     layer.prefill(t(60, 2, 192), cu, table, cu, 59)
     torch.cuda.synchronize()
     assert B.idx_get_device_status() == B.DEV_BAD_BOUNDS
+
+
+def test_list_that_descends():
+    """Rows named again by bounds that descend are computed while the list can be counted; a list that cannot is left
+    alone, told of, and harms no later call."""
+    rng = np.random.default_rng(43)
+    pool, slots, _, qt, q = _sparse_case(rng, ref.FP8, [700], 16, 64)
+    qt, q = _bf16(rng.standard_normal((5, 16, 576)))
+    falls = np.array([0, 700, 0, 300, 100, 650], np.int32)
+    args = _dev(pool), 64, ref.FP8, _dev(slots)
+    out, lse = B.idx_latent_attention(qt, *args, _dev(falls), SCALE)
+    _clean()
+    _check_sparse(pool, ref.FP8, 64, slots, falls, q, out, lse)
+    rows, n = 1 << 18, 1 << 20  # half of the rows name all of a million slots
+    far = torch.zeros(rows + 1, dtype=torch.int32, device="cuda")
+    far[1::2] = n
+    many = torch.zeros(n, dtype=torch.int32, device="cuda")
+    B.idx_latent_attention(torch.zeros(rows, 1, 576, dtype=torch.bfloat16, device="cuda"), *args[:3], many, far, SCALE)
+    torch.cuda.synchronize()
+    assert B.idx_get_device_status() == B.DEV_BAD_BOUNDS
+    again, _ = B.idx_latent_attention(qt, *args, _dev(falls), SCALE)
+    _clean()
+    assert torch.equal(again, out)

@@ -661,7 +661,9 @@ size_t idx_latent_attention_workspace_size(int R, int H, int64_t max_keys);
  * aligned.  Keys and values past a sequence's end (another sequence's) never
  * enter its results, whatever they hold; within a sequence a value that is
  * not finite may reach queries that the causal mask hides it from.
- * Supported: d_nope = d_v = 128, d_rope = 64, H <= 65535.
+ * Supported: d_nope = d_v = 128, d_rope = 64, H <= 65535, Tq and Tk up to
+ * 2^31 - 513; a list of 2^36 tiles (256 queries of a head x 128 keys) or more
+ * sets IDX_DEV_BAD_BOUNDS and nothing is written.
  * ---------------------------------------------------------------------- */
 idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
                               const uint16_t *k, int64_t ldk_row, int64_t ldk_head,

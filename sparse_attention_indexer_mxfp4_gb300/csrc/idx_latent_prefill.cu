@@ -64,7 +64,8 @@ constexpr int kOffRing = 2 * kQPieces * kPiece;
 constexpr int kOffBar = kOffRing + kRing * kPiece;
 constexpr int kBars = kRing + 20;
 constexpr int kOffMisc = kOffBar + 8 * kBars;  // tmem base, abort flag, the share's place, sizes
-constexpr int kOffCu = kOffMisc + 80;          // the sequences' bounds, where they fit
+constexpr int kOffSum = kOffMisc + 32;         // a sum of each warp
+constexpr int kOffCu = kOffSum + kThreads / 4; // the sequences' bounds, where they fit
 constexpr int kMaxCu = 128;
 constexpr int kSmem = kOffCu + 8 * (kMaxCu + 1) + 1024;  // the base is aligned to 1024
 static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -92,6 +93,7 @@ constexpr int kRows = 2 * kTile;                        // queries of a block
 constexpr int kPartTile = kTile * kV + 2 * kTile;       // floats of a query tile's partial result
 constexpr int kMaxShares = 152;
 constexpr int kCharge = 1;  // tiles that a block counts besides its own
+constexpr int64_t kMaxHeadTiles = (int64_t)1 << 36;  // of all heads: a share's fit 32 bits
 // Blocks of few keys are not cut: up to four tiles a CTA more cost less than
 // the joining kernel (6.6 us whole, 8.1 cut, for 2 sequences of 50 rows, 3
 // heads).
@@ -143,21 +145,22 @@ __device__ __forceinline__ int key_tiles(const PrefillArgs &a, const Block &k, i
 }
 
 // Tiles of the first n blocks of a sequence, its last not among them; a block
-// counts at least one, its outputs are written (causal: block i sees kRows / kTile (i + 1) + ceil((nk - nq) /
-// kTile) tiles).
-__device__ __forceinline__ int tiles_before(const PrefillArgs &a, int nq, int nk, int n)
+// counts at least one, its outputs are written (causal: block i sees kRows /
+// kTile (i + 1) + ceil((nk - nq) / kTile) tiles).  Lists are counted in 64
+// bits, shares in 32.
+__device__ __forceinline__ int64_t tiles_before(const PrefillArgs &a, int nq, int nk, int n)
 {
     if (!a.causal)
-        return n * max(1, (nk + kTile - 1) / kTile);
+        return (int64_t)n * max(1, (nk + kTile - 1) / kTile);
     constexpr int rho = kRows / kTile;
     const int d = nk - nq;
     const int delta = d >= 0 ? (d + kTile - 1) / kTile : -(-d / kTile);
     const int z = min(n, max(0, -delta / rho));  // blocks that see nothing
-    return z + rho * (n * (n + 1) - z * (z + 1)) / 2 + delta * (n - z);
+    return z + rho * ((int64_t)n * (n + 1) - (int64_t)z * (z + 1)) / 2 + (int64_t)delta * (n - z);
 }
 
-// All of a sequence's tiles and its blocks' charges.
-__device__ __forceinline__ int tiles_of_seq(const PrefillArgs &a, int nq, int nk)
+// All of a sequence's tiles and its blocks' charges: below 2^48.
+__device__ __forceinline__ int64_t tiles_of_seq(const PrefillArgs &a, int nq, int nk)
 {
     if (nq <= 0)
         return 0;
@@ -288,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     if (tid == 0 && !a.uncut)
         a.ws_cut[2 * blockIdx.x] = make_int4(0, 0, 0, 0);
-    int *wsum = misc + 4;
-    const auto seq_tiles = [&](int b) {
+    int64_t *wsum = reinterpret_cast<int64_t *>(smem + kOffSum);
+    const auto seq_tiles = [&](int b) -> int64_t {
         Block k;
         k.b = b;
         if (b >= a.B)
@@ -300,13 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             atomicOr(a.status, kDevBadBounds);
         return tiles_of_seq(a, k.nq, k.nk);
     };
-    int head_tiles = 0, mine, before;
+    int64_t head_tiles = 0, mine, before;
     const auto scan = [&](int b0) {  // of sequences b0 + thread; adds up head_tiles
         mine = seq_tiles(b0 + tid);
-        int upto = mine;
+        int64_t upto = mine;
         #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, upto, o);
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
             upto += lane >= o ? v : 0;
         }
         __syncthreads();
@@ -319,35 +322,45 @@ __global__ void __launch_bounds__(kThreads, 1)
             before += i < warp ? wsum[i] : 0;
             head_tiles += wsum[i];
         }
+        head_tiles = min(head_tiles, kMaxHeadTiles);
     };
     for (int b0 = 0; b0 < a.B; b0 += kThreads)
         scan(b0);
-    const int total = head_tiles * a.H;
-    // two tiles a share at least: a cut costs about as much as a tile
-    const int p = blockIdx.x, shares = max(1, min((int)gridDim.x, total / 2));
-    const int each = total / shares, more = total - each * shares;
-    if (tid == 0) {
-        misc[16] = each;
-        misc[17] = more;
+    // A list that no device lives to the end of (of bounds that descend: its
+    // sequences hold tokens again) is left alone.
+    const bool too_many = head_tiles >= kMaxHeadTiles / a.H;
+    if (too_many) {
+        if (blockIdx.x == 0 && tid == 0)
+            atomicOr(a.status, kDevBadBounds);
+        head_tiles = 0;
     }
-    const int u0 = p * each + min(p, more);
+    const int64_t total = head_tiles * a.H;
+    // two tiles a share at least: a cut costs about as much as a tile
+    const int p = blockIdx.x, shares = (int)max((int64_t)1, min((int64_t)gridDim.x, total / 2));
+    const int each = (int)(total / shares), more = (int)(total - (int64_t)each * shares);
+    if (tid == 0) {
+        misc[4] = each;
+        misc[5] = more;
+    }
+    const int64_t u0 = (int64_t)p * each + min(p, more);
     Walk w;
     w.left = p < shares && total > 0 ? each + (p < more) : 0;
-    w.k.head = w.left > 0 ? u0 / head_tiles : 0;
-    const int at = u0 - w.k.head * head_tiles;
-    if (a.B > kThreads) {
+    w.k.head = w.left > 0 ? (int)(u0 / head_tiles) : 0;
+    const int64_t at = u0 - w.k.head * head_tiles;
+    int64_t *rest_at = reinterpret_cast<int64_t *>(misc + 2);
+    if (a.B > kThreads && !too_many) {
         // many sequences: the chunk that holds the place, once more
         head_tiles = 0;
         for (int b0 = 0; b0 < a.B; b0 += kThreads) {
             scan(b0);
             if (w.left > 0 && at >= before && at < before + mine) {
-                misc[2] = b0 + tid;
-                misc[3] = at - before;
+                misc[6] = b0 + tid;
+                *rest_at = at - before;
             }
         }
     } else if (w.left > 0 && at >= before && at < before + mine) {
-        misc[2] = tid;
-        misc[3] = at - before;
+        misc[6] = tid;
+        *rest_at = at - before;
     }
     __syncthreads();
     tc_fence_after();
@@ -355,19 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, misc[0], 0);
     w.t = w.pay = 0;
     if (w.left > 0) {
-        w.k.b = __shfl_sync(0xffffffffu, misc[2], 0);
-        int rest = __shfl_sync(0xffffffffu, misc[3], 0);
+        w.k.b = __shfl_sync(0xffffffffu, misc[6], 0);
+        const int64_t place = __shfl_sync(0xffffffffu, *rest_at, 0);
         block_seq(a, cq, ck, w.k);
         int lo = 0, hi = (w.k.nq + kRows - 1) / kRows - 1;  // the last i with tiles_before <= rest
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
-            if (tiles_before(a, w.k.nq, w.k.nk, mid) + mid * kCharge <= rest)
+            if (tiles_before(a, w.k.nq, w.k.nk, mid) + mid * kCharge <= place)
                 lo = mid;
             else
                 hi = mid - 1;
         }
         w.k.i = lo;
-        rest -= tiles_before(a, w.k.nq, w.k.nk, lo) + lo * kCharge;
+        const int rest = (int)(place - (tiles_before(a, w.k.nq, w.k.nk, lo) + lo * kCharge));
         w.t = max(0, rest - kCharge);
         w.pay = max(0, kCharge - rest);
         if (a.uncut && rest > 0) {
@@ -507,8 +520,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (tid == 0 && s.t0 == 0) {
                     // the shares that hold the rest: `more - p - 1` longer ones first
-                    const int size = misc[16], longer = max(0, misc[17] - (int)blockIdx.x - 1);
-                    const int rest = s.tiles - s.t1, in = min(rest, longer * (size + 1));
+                    const int size = misc[4], longer = max(0, misc[5] - (int)blockIdx.x - 1);
+                    const int rest = s.tiles - s.t1;
+                    const int in = (int)min((int64_t)rest, (int64_t)longer * (size + 1));
                     a.ws_cut[2 * blockIdx.x] = make_int4(
                         s.k.head, s.k.b, s.k.i,
                         1 + (in + size) / (size + 1) + (rest - in + size - 1) / size);
@@ -898,10 +912,8 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
     const size_t need = idx_latent_prefill_workspace_size(Tq, Tk, H);
     if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need))
         return IDX_ERR_WORKSPACE;
-    // an upper bound of the list: every block and the most keys it may see
-    const int64_t bound = ((int64_t)Tq / kRows + B) * ((int64_t)Tk / kTile + 1 + kCharge) * H;
-    if (bound > INT32_MAX || Tq / kRows > 32768)
-        return IDX_ERR_UNSUPPORTED;
+    if (Tq > INT32_MAX - 2 * kRows || Tk > INT32_MAX - 2 * kTile)
+        return IDX_ERR_UNSUPPORTED;  // rows and tiles are counted past the end
     CUtensorMap tq, tk, tr, tv;
     const uint64_t rdims[2] = {2 * kRope, (uint64_t)Tk};
     const uint64_t rstr[1] = {(uint64_t)(Tk > 1 ? 2 * ld_rope : 2 * kRope)};
@@ -947,8 +959,12 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
             return IDX_ERR_CUDA;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int shares =
-        (int)std::min<int64_t>(std::min(sm_count(), kMaxShares), std::max<int64_t>(1, bound / 2));
+    // few blocks on few keys: no more CTAs than tiles and charges in pairs
+    const int64_t blocks = (int64_t)Tq / kRows + B, tiles = (int64_t)Tk / kTile + 1 + kCharge;
+    const int most = std::min(sm_count(), kMaxShares);
+    const int shares = blocks > most || tiles > 2 * most || H > most
+                           ? most
+                           : (int)std::min<int64_t>(most, std::max<int64_t>(1, blocks * tiles * H / 2));
     cudaError_t e = launch_pdl(latent_prefill_kernel, dim3(shares), dim3(kThreads), kSmem,
                                (cudaStream_t)stream, tq, tk, tr, tv, a);
     if (e == cudaSuccess && shares > 1 && !a.uncut)

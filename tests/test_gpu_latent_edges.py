@@ -216,3 +216,42 @@ def test_list_that_descends():
     again, _ = B.idx_latent_attention(qt, *args, _dev(falls), SCALE)
     _clean()
     assert torch.equal(again, out)
+
+
+# --------------------------------------------------------- long lists of work
+
+
+def test_prefill_pack_of_many_sequences_and_heads():
+    """20000 sequences of 70 heads: every block times all keys is past 32 bits, the list is not."""
+    B_, H, lk = 20000, 70, 10
+    g = torch.Generator(device="cuda").manual_seed(3)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda", dtype=torch.bfloat16)  # noqa: E731
+    q, kv, lat = r(B_, H, 192), r(B_ * lk, H, 256), r(B_ * lk, 64)
+    cu_q = torch.arange(B_ + 1, dtype=torch.int32, device="cuda")
+    cu_k = cu_q * lk
+    out, lse = B.idx_latent_prefill(q, kv[..., :128], lat, kv[..., 128:], cu_q, cu_k, SCALE)
+    _clean()
+    for b in [0, 1, 383, 384, 9999, 12345, 19999]:
+        k = slice(b * lk, b * lk + lk)
+        _check_prefill(np.array([0, 1]), np.array([0, lk]), _np(q[b:b + 1]), _np(kv[k]), _np(lat[k]), out[b:b + 1],
+                       lse[b:b + 1], True)
+    # each of the equal sequences is computed: none has kept what was in memory
+    assert torch.isfinite(out).all() and (out.abs().amax(-1) > 0).all()
+
+
+def test_prefill_list_that_cannot_be_counted():
+    """Bounds that descend name the same tokens again and again: told of, and no later call is harmed."""
+    n, H, seqs = 1 << 16, 64, 1 << 15
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    q, k, rope = z(n, H, 192), z(n, H, 128), z(n, 64)
+    far = torch.zeros(seqs + 1, dtype=torch.int32, device="cuda")
+    far[1::2] = n
+    B.idx_latent_prefill(q, k, rope, k, far, far, SCALE, causal=False)
+    torch.cuda.synchronize()
+    assert B.idx_get_device_status() == B.DEV_BAD_BOUNDS
+    del q, k
+    rng = np.random.default_rng(9)
+    cq, ck, qt, qv, kvt, kv, latt, lat = _prefill_case(rng, [300], [900], 2)
+    out, lse = B.idx_latent_prefill(qt, kvt[..., :128], latt[:, 512:], kvt[..., 128:], _dev(cq), _dev(ck), SCALE)
+    _clean()
+    _check_prefill(cq, ck, qv, kv, lat[:, 512:], out, lse, True)

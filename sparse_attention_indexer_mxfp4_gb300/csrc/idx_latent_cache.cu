@@ -56,6 +56,19 @@ __device__ __forceinline__ float group_inverse(int bits)
     return bits == 255 ? 0.0f : __uint_as_float((uint32_t)(254 - bits) << 23);
 }
 
+// Of a token's latents, sixteen a lane.
+__device__ __forceinline__ float sum_of_squares(const float (&y)[16])
+{
+    float ss = 0.0f;
+    #pragma unroll
+    for (int i = 0; i < 16; ++i)
+        ss = fmaf(y[i], y[i], ss);
+    #pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    return ss;
+}
+
 // Lane l holds latents 8 l .. 8 l + 7 of both halves of 256 (16-byte loads,
 // 512 contiguous bytes a warp), so a group of 64 is eight lanes, and the pair
 // 2 l, 2 l + 1 of the rotated elements.
@@ -107,14 +120,18 @@ __global__ void __launch_bounds__(kCacheThreads)
             }
         }
         if (norm_w) {
-            float ss = 0.0f;
-            #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                ss = fmaf(y[i], y[i], ss);
-            #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = 1.0f / sqrtf(ss * (1.0f / kLatent) + eps);
+            float ss = sum_of_squares(y), e = eps;
+            if (!(ss <= 1e36f) || (ss < 1e-30f && eps < 1e-30f)) {
+                // squares leave 32 bits' range: x / sqrt(mean(x^2) + eps) is the
+                // same of 2^k x and 2^2k eps (uniform in the warp)
+                const float up = ss < 1.0f ? 0x1p80f : 0x1p-80f;
+                #pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    y[i] *= up;
+                ss = sum_of_squares(y);
+                e = eps * up * up;
+            }
+            const float r = 1.0f / sqrtf(ss * (1.0f / kLatent) + e);
             #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float4 w = *reinterpret_cast<const float4 *>(norm_w + (q >> 1) * 256 +

@@ -255,3 +255,33 @@ def test_prefill_list_that_cannot_be_counted():
     out, lse = B.idx_latent_prefill(qt, kvt[..., :128], latt[:, 512:], kvt[..., 128:], _dev(cq), _dev(ck), SCALE)
     _clean()
     _check_prefill(cq, ck, qv, kv, lat[:, 512:], out, lse, True)
+
+
+# --------------------------------------------------- values at the types' ends
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("eps", [0.0, 1e-38, 1e-6, 4.0])
+def test_store_norm_of_large_and_small_tokens(fmt, eps):
+    """Squares past 32 bits' range on either side: the norm is the formula's."""
+    rng = np.random.default_rng(6)
+    size = np.array([3e38, 1e30, 1e19, 1e17, 1.0, 1e-12, 1e-15, 1e-18, 1e-25, 1e-36])
+    x = np.clip(rng.standard_normal((len(size), 576)), -1, 1) * size[:, None]
+    x[:, 512:] = 0
+    t, v = _bf16(x)
+    w = (1 + 0.1 * rng.standard_normal(512)).astype(np.float32)
+    page = 16
+    pool = torch.zeros(1, ref.page_stride(fmt, page), dtype=torch.uint8, device="cuda")
+    slots = np.arange(len(size))
+    B.idx_latent_store(t, None, None, _dev(w), eps, pool, page, _dev(slots), fmt)
+    _clean()
+    y = v[:, :512] / np.sqrt((v[:, :512] ** 2).mean(1, keepdims=True) + eps) * w
+    got = ref.read_tokens(pool.cpu().numpy(), fmt, page, slots)[:, :512]
+    if fmt == ref.BF16:
+        # half a step, subnormal ones among them, and a few units of the 32-bit norm
+        assert (np.abs(got - y) <= (ref.HALF_BF16 + 2.0 ** -20) * np.abs(y) + 2.0 ** -133).all()
+    else:
+        amax = np.repeat(np.abs(y).reshape(-1, 8, 64).max(-1), 64, 1).reshape(y.shape)
+        # the group's step is at most amax / 224, or the least scale's
+        step = np.maximum(amax / 224, 2.0 ** -127)
+        assert (np.abs(got - y) <= (2.0 ** -4 + 1e-5) * np.abs(y) + (2.0 ** -10 + 1e-5) * step).all()

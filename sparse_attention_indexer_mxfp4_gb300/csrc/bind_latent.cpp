@@ -129,6 +129,18 @@ const at::Tensor &need_pages(PyObject *o)
     return t;
 }
 
+// The stride of dimension d in elements; over one element any stride will do,
+// and a tensor may have one without meaning there.
+int64_t ld(const at::Tensor &t, int64_t d, int64_t natural)
+{
+    return t.size(d) > 1 ? t.stride(d) : natural;
+}
+
+int64_t page_stride(const at::Tensor &pages)
+{
+    return ld(pages, 0, (pages.size(1) + 15) / 16 * 16);
+}
+
 // What a launch counts in 32 bits.
 int count(int64_t n, const char *name)
 {
@@ -161,7 +173,7 @@ struct Outputs {
         if (lse_o != Py_None && lse_o != Py_False) {
             lse = tensor_of(lse_o, "lse");
             if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != R ||
-                lse.size(1) != H || lse.stride(1) != 1)
+                lse.size(1) != H || ld(lse, 1, 1) != 1)
                 refuse("lse must be float32 [" + std::to_string(R) + ", " + std::to_string(H) +
                        "] with unit column stride");
         }
@@ -184,10 +196,10 @@ struct Outputs {
             ws = empty({(int64_t)size}, at::kByte, q.device());
             ws_bytes = size;
         }
-        ld_row = out.stride(0);
-        ld_head = out.stride(1);
+        ld_row = ld(out, 0, H * dim);
+        ld_head = ld(out, 1, dim);
         if (lse.defined())
-            ld_lse = lse.stride(0);
+            ld_lse = ld(lse, 0, H);
     }
     uint16_t *out_at() const { return address<uint16_t>(out); }
     float *lse_at() const { return lse.defined() ? address<float>(lse) : nullptr; }
@@ -270,7 +282,7 @@ PyObject *store(PyObject *, PyObject *const *a, Py_ssize_t)
         refuse("positions and cos_sin come together");
     at::Tensor p, c, w;
     int rows = 0;
-    int64_t ld = 0;
+    int64_t ld_cs = 0;
     if (a[3] != Py_None) {
         p = need(a[2], at::kInt, "positions");
         c = tensor_of(a[3], "cos_sin");
@@ -278,7 +290,7 @@ PyObject *store(PyObject *, PyObject *const *a, Py_ssize_t)
         if (c.scalar_type() != at::kFloat || c.dim() != 2 || c.stride(1) != 1 || c.size(1) < kRope)
             refuse("cos_sin must be float32 [positions, " + std::to_string(kRope) + "]");
         rows = count(c.size(0), "cos_sin");
-        ld = c.stride(0);
+        ld_cs = ld(c, 0, kRope);
     }
     if (a[4] != Py_None) {
         w = need(a[4], at::kFloat, "norm_weight");
@@ -293,9 +305,10 @@ PyObject *store(PyObject *, PyObject *const *a, Py_ssize_t)
         [&] {
             return Py_BuildValue("(OOOOOO)", a[1], a[2], a[3], a[4], a[6], a[8]);
         },
-        (const uint16_t *)address<uint16_t>(kv), kv.stride(0), positions, cos_sin, ld, rows, weight,
+        (const uint16_t *)address<uint16_t>(kv), ld(kv, 0, kLatent + kRope), positions, cos_sin,
+        ld_cs, rows, weight,
         float_of(a[5]), count(T, "kv"), (int)kLatent, (int)kRope,
-        (idx_latent_format)int_of(a[9], "fmt"), address<uint8_t>(pages), pages.stride(0),
+        (idx_latent_format)int_of(a[9], "fmt"), address<uint8_t>(pages), page_stride(pages),
         count(pages.size(0), "kv_pages"), int_of(a[7], "page_size"),
         (const int64_t *)address<int64_t>(slots));
 }
@@ -320,11 +333,12 @@ PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t)
         [&] {
             return Py_BuildValue("(OOOOO)", a[1], a[4], a[5], a[7], a[6]);
         },
-        (const uint8_t *)address<uint8_t>(pages), pages.stride(0), count(pages.size(0), "kv_pages"),
+        (const uint8_t *)address<uint8_t>(pages), page_stride(pages), count(pages.size(0), "kv_pages"),
         int_of(a[2], "page_size"), (idx_latent_format)int_of(a[3], "fmt"), (int)kLatent, (int)kRope,
         (const int32_t *)address<int32_t>(table), table.size(1),
         count(table.size(1), "block_table"), (const int32_t *)address<int32_t>(cu), starts,
-        count(B, "cu_lens"), count(out.size(0), "out"), address<uint16_t>(out), out.stride(0));
+        count(B, "cu_lens"), count(out.size(0), "out"), address<uint16_t>(out),
+        ld(out, 0, kLatent + kRope));
 }
 
 PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t)
@@ -346,8 +360,9 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t)
             return Py_BuildValue("(OOOONNN)", a[1], a[2], a[5], a[6], wrap(o.out), wrap(o.lse),
                                  wrap(o.ws));
         },
-        (const uint16_t *)address<uint16_t>(q), q.stride(0), q.stride(1),
-        (const uint8_t *)address<uint8_t>(pages), pages.stride(0), count(pages.size(0), "kv_pages"),
+        (const uint16_t *)address<uint16_t>(q), ld(q, 0, H * (kLatent + kRope)),
+        ld(q, 1, kLatent + kRope), (const uint8_t *)address<uint8_t>(pages), page_stride(pages),
+        count(pages.size(0), "kv_pages"),
         int_of(a[3], "page_size"), (idx_latent_format)int_of(a[4], "fmt"),
         (const int32_t *)address<int32_t>(slots), (const int32_t *)address<int32_t>(indptr),
         slots.numel(), R, H, (int)kLatent, (int)kRope, float_of(a[7]), o.out_at(), o.ld_row,
@@ -379,8 +394,9 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t)
             return Py_BuildValue("(OOOONNN)", a[1], a[2], a[5], a[6], wrap(o.out), wrap(o.lse),
                                  wrap(o.ws));
         },
-        (const uint16_t *)address<uint16_t>(q), q.stride(0), q.stride(1),
-        (const uint8_t *)address<uint8_t>(pages), pages.stride(0), count(pages.size(0), "kv_pages"),
+        (const uint16_t *)address<uint16_t>(q), ld(q, 0, H * (kLatent + kRope)),
+        ld(q, 1, kLatent + kRope), (const uint8_t *)address<uint8_t>(pages), page_stride(pages),
+        count(pages.size(0), "kv_pages"),
         int_of(a[3], "page_size"), (idx_latent_format)int_of(a[4], "fmt"),
         (const int32_t *)address<int32_t>(table), table.size(1),
         (const int32_t *)address<int32_t>(lens), per_row, B, next, longest, H, (int)kLatent,
@@ -412,10 +428,10 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t)
             return Py_BuildValue("(OOOOOONNN)", a[1], a[2], a[3], a[4], a[5], a[6], wrap(o.out),
                                  wrap(o.lse), wrap(o.ws));
         },
-        (const uint16_t *)address<uint16_t>(q), q.stride(0), q.stride(1),
-        (const uint16_t *)address<uint16_t>(k), k.stride(0), k.stride(1),
-        (const uint16_t *)address<uint16_t>(rope), rope.stride(0),
-        (const uint16_t *)address<uint16_t>(v), v.stride(0), v.stride(1),
+        (const uint16_t *)address<uint16_t>(q), ld(q, 0, H * (kNope + kRope)), ld(q, 1, kNope + kRope),
+        (const uint16_t *)address<uint16_t>(k), ld(k, 0, H * kNope), ld(k, 1, kNope),
+        (const uint16_t *)address<uint16_t>(rope), ld(rope, 0, kRope),
+        (const uint16_t *)address<uint16_t>(v), ld(v, 0, H * kV), ld(v, 1, kV),
         (const int32_t *)address<int32_t>(cu_q), (const int32_t *)address<int32_t>(cu_k),
         count(B, "cu_q"), Tq, Tk, H, (int)kNope, (int)kRope, (int)kV, float_of(a[7]),
         PyObject_IsTrue(a[8]), o.out_at(), o.ld_row, o.ld_head, o.lse_at(), o.ld_lse, o.ws_at(),

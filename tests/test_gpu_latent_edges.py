@@ -285,3 +285,44 @@ def test_store_norm_of_large_and_small_tokens(fmt, eps):
         # the group's step is at most amax / 224, or the least scale's
         step = np.maximum(amax / 224, 2.0 ** -127)
         assert (np.abs(got - y) <= (2.0 ** -4 + 1e-5) * np.abs(y) + (2.0 ** -10 + 1e-5) * step).all()
+
+
+# ------------------------------------------------- layouts of one row, one head
+
+
+def _odd(t, *dims):
+    """The same tensor with strides of no meaning where it has one element."""
+    strides = list(t.stride())
+    for d in dims:
+        assert t.shape[d] == 1
+        strides[d] = 1
+    return t.as_strided(t.shape, strides)
+
+
+def test_strides_over_one_element_are_free():
+    rng = np.random.default_rng(8)
+    pool, slots, indptr, qt, q = _sparse_case(rng, ref.FP8, [70], 1, 128)
+    dev = _dev(pool)
+    one = _odd(dev[:1], 0)
+    o, l = torch.empty(1, 1, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(1, 1, device="cuda")
+    out, lse = B.idx_latent_attention(_odd(qt, 0, 1), dev, 128, ref.FP8, _dev(slots), _dev(indptr), SCALE,
+                                      out=_odd(o, 0, 1), lse=_odd(l, 0))
+    _clean()
+    _check_sparse(pool, ref.FP8, 128, slots, indptr, q, out, lse)
+    # one token stored into a pool of one page, and read back
+    kv, x = _bf16(rng.standard_normal((1, 576)))
+    cs = torch.ones(1, 64, device="cuda")
+    pos = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.idx_latent_store(_odd(kv, 0), pos, _odd(cs, 0), None, 0.0, one, 128, _dev(np.array([5])), ref.FP8)
+    back = torch.empty(1, 576, dtype=torch.bfloat16, device="cuda")
+    B.idx_latent_gather(one, 128, ref.FP8, _dev(np.zeros((1, 1), np.int32)), _dev(np.array([0, 1], np.int32)),
+                        _odd(back, 0), seq_starts=_dev(np.array([5], np.int32)))
+    _clean()
+    assert (np.abs(_np(back)[:, :512] - x[:, :512]) <= 2.0 ** -4 * np.abs(x[:, :512]) + 2.0 ** -10).all()
+    # one query on one key
+    cq, ck, qt, q, kvt, kv, latt, lat = _prefill_case(rng, [1], [1], 1, tail=0)
+    o = torch.empty(1, 1, 128, dtype=torch.bfloat16, device="cuda")
+    out, lse = B.idx_latent_prefill(_odd(qt, 0, 1), _odd(kvt[..., :128], 0, 1), _odd(latt[:, 512:], 0),
+                                    _odd(kvt[..., 128:], 0, 1), _dev(cq), _dev(ck), SCALE, out=_odd(o, 0, 1))
+    _clean()
+    _check_prefill(cq, ck, q, kv, lat[:, 512:], out, lse, True)

@@ -67,6 +67,14 @@ float float_of(PyObject *o)
     return (float)v;
 }
 
+bool truth_of(PyObject *o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0)
+        throw python_error();
+    return v != 0;
+}
+
 // Every tensor of a call lives on one device, and it is the current one: the
 // stream, the scratch's size and the launch are the current device's.
 void on_one_device(std::initializer_list<const at::Tensor *> tensors)
@@ -378,7 +386,7 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t)
     const int R = count(q.size(0), "q"), H = count(q.size(1), "q"), next = int_of(a[7], "next_n");
     if (next <= 0 || R % next)
         refuse("q must hold B * next_n rows");
-    const int B = R / next, per_row = PyObject_IsTrue(a[10]);
+    const int B = R / next, per_row = truth_of(a[10]);
     need_count(lens, per_row ? R : B, "context_lens");
     if (table.dim() != 2 || table.size(0) < B)
         refuse("block_table must be [" + std::to_string(B) + ", blocks]");
@@ -412,6 +420,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t)
     const at::Tensor &v = need_heads(a[4], 3, kV, "v");
     const at::Tensor &cu_q = need(a[5], at::kInt, "cu_q"), &cu_k = need(a[6], at::kInt, "cu_k");
     const int Tq = count(q.size(0), "q"), H = count(q.size(1), "q"), Tk = count(k.size(0), "k");
+    const int causal = truth_of(a[8]);
     if (k.size(1) != H || v.size(1) != H || v.size(0) != Tk || rope.size(0) != Tk)
         refuse("k, k_rope and v must hold the same tokens, and the heads of q");
     const int64_t B = cu_q.numel() - 1;
@@ -434,7 +443,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t)
         (const uint16_t *)address<uint16_t>(v), ld(v, 0, H * kV), ld(v, 1, kV),
         (const int32_t *)address<int32_t>(cu_q), (const int32_t *)address<int32_t>(cu_k),
         count(B, "cu_q"), Tq, Tk, H, (int)kNope, (int)kRope, (int)kV, float_of(a[7]),
-        PyObject_IsTrue(a[8]), o.out_at(), o.ld_row, o.ld_head, o.lse_at(), o.ld_lse, o.ws_at(),
+        causal, o.out_at(), o.ld_row, o.ld_head, o.lse_at(), o.ld_lse, o.ws_at(),
         o.ws_bytes);
 }
 

@@ -84,3 +84,13 @@ def test_scratch_that_is_not_one_piece(name, ws):
     for f in (call, prepare):
         with pytest.raises(ValueError, match="workspace must be contiguous"):
             f(*good(), workspace=ws)
+
+
+@pytest.mark.parametrize("name,flag", [("paged", "ctx_per_row"), ("prefill", "causal")])
+def test_flag_without_a_truth_value(name, flag):
+    """Its own error comes through, and before anything is launched."""
+    call, prepare, good = CALLS[name]
+    for f in (call, prepare):
+        for args in (good(), _good(name)):
+            with pytest.raises(RuntimeError, match="Boolean value"):
+                f(*args, **{flag: torch.zeros(2)})

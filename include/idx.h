@@ -635,6 +635,10 @@ idx_status idx_paged_latent_attention(const uint16_t *q, int64_t ldq_row, int64_
  * are so few that rows are not split. */
 size_t idx_latent_attention_workspace_size(int R, int H, int64_t max_keys);
 
+/* Kernels that such a call launches, R rows in all, next_n of them a sequence
+ * (1: ragged slots). */
+int idx_latent_attention_launches(int R, int next_n, int H, int64_t max_keys);
+
 /* ------------------------------------------------------------------------
  * idx_latent_prefill -- the expanded form: attention of ragged sequences
  * with keys of 128 own elements a head and 64 rotated ones shared by all

@@ -110,6 +110,8 @@ def lib() -> ctypes.CDLL:
             L.idx_topk_workspace_size.restype = _S
             L.idx_latent_attention_workspace_size.argtypes = [_I, _I, _L]
             L.idx_latent_attention_workspace_size.restype = _S
+            L.idx_latent_attention_launches.argtypes = [_I, _I, _I, _L]
+            L.idx_latent_attention_launches.restype = _I
             L.idx_latent_prefill_workspace_size.argtypes = [_I, _I, _I]
             L.idx_latent_prefill_workspace_size.restype = _S
             L.idx_paged_mqa_logits_workspace_size.argtypes = [_I, _I, _I, _I]
@@ -634,7 +636,8 @@ def _latent_calls():
         mod.bind(_check, *(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
             "idx_latent_store", "idx_latent_gather", "idx_latent_attention",
             "idx_paged_latent_attention", "idx_latent_prefill",
-            "idx_latent_attention_workspace_size", "idx_latent_prefill_workspace_size")))
+            "idx_latent_attention_workspace_size", "idx_latent_prefill_workspace_size",
+            "idx_latent_attention_launches")))
         _calls = mod
     return _calls
 

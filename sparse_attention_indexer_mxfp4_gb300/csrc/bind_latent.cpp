@@ -31,6 +31,7 @@ decltype(&idx_paged_latent_attention) f_paged;
 decltype(&idx_latent_prefill) f_prefill;
 decltype(&idx_latent_attention_workspace_size) f_attention_size;
 decltype(&idx_latent_prefill_workspace_size) f_prefill_size;
+decltype(&idx_latent_attention_launches) f_attention_launches;
 PyObject *g_check;  // check(status, name) raises
 
 struct Refusal {
@@ -309,7 +310,7 @@ PyObject *store(PyObject *, PyObject *const *a, Py_ssize_t)
     const float *cos_sin = c.defined() ? address<float>(c) : nullptr;
     const float *weight = w.defined() ? address<float>(w) : nullptr;
     return call(
-        a[0] == Py_True, f_store, "idx_latent_store", 1, [] { Py_RETURN_NONE; },
+        a[0] == Py_True, f_store, "idx_latent_store", T > 0, [] { Py_RETURN_NONE; },
         [&] {
             return Py_BuildValue("(OOOOOO)", a[1], a[2], a[3], a[4], a[6], a[8]);
         },
@@ -337,7 +338,8 @@ PyObject *gather(PyObject *, PyObject *const *a, Py_ssize_t)
     on_one_device({&pages, &out, &table, &cu, &s});
     const int32_t *starts = s.defined() ? address<int32_t>(s) : nullptr;
     return call(
-        a[0] == Py_True, f_gather, "idx_latent_gather", 1, [&] { return keep(a[6]); },
+        a[0] == Py_True, f_gather, "idx_latent_gather", B > 0 && out.size(0) > 0,
+        [&] { return keep(a[6]); },
         [&] {
             return Py_BuildValue("(OOOOO)", a[1], a[4], a[5], a[7], a[6]);
         },
@@ -360,9 +362,9 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t)
     on_one_device({&q, &pages, &slots, &indptr, &o.out, &o.lse, &o.ws});
     const size_t size = f_attention_size(R, H, slots.numel());
     o.make(a[9], a[10], q, kLatent, size);
-    // the attention, and with scratch the joining kernel
     return call(
-        a[0] == Py_True, f_attention, "idx_latent_attention", size ? 2 : 1,
+        a[0] == Py_True, f_attention, "idx_latent_attention",
+        f_attention_launches(R, 1, H, slots.numel()),
         [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
         [&] {
             return Py_BuildValue("(OOOONNN)", a[1], a[2], a[5], a[6], wrap(o.out), wrap(o.lse),
@@ -396,7 +398,8 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t)
     const size_t size = f_attention_size(R, H, longest);
     o.make(a[12], a[13], q, kLatent, size);
     return call(
-        a[0] == Py_True, f_paged, "idx_paged_latent_attention", size ? 2 : 1,
+        a[0] == Py_True, f_paged, "idx_paged_latent_attention",
+        f_attention_launches(R, next, H, longest),
         [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
         [&] {
             return Py_BuildValue("(OOOONNN)", a[1], a[2], a[5], a[6], wrap(o.out), wrap(o.lse),
@@ -431,7 +434,7 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t)
     const size_t size = f_prefill_size(Tq, Tk, H);
     o.make(a[10], a[11], q, kV, size);
     return call(
-        a[0] == Py_True, f_prefill, "idx_latent_prefill", size ? 2 : 1,
+        a[0] == Py_True, f_prefill, "idx_latent_prefill", Tq == 0 || B == 0 ? 0 : size ? 2 : 1,
         [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
         [&] {
             return Py_BuildValue("(OOOOOONNN)", a[1], a[2], a[3], a[4], a[5], a[6], wrap(o.out),
@@ -468,9 +471,10 @@ PyObject *entry(PyObject *self, PyObject *const *a, Py_ssize_t n)
 // bind(check, addresses of the library's functions)
 PyObject *bind(PyObject *, PyObject *args)
 {
-    unsigned long long p[7];
+    unsigned long long p[8];
     PyObject *check;
-    if (!PyArg_ParseTuple(args, "OKKKKKKK", &check, p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6))
+    if (!PyArg_ParseTuple(args, "OKKKKKKKK", &check, p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6,
+                          p + 7))
         return nullptr;
     f_store = reinterpret_cast<decltype(f_store)>(p[0]);
     f_gather = reinterpret_cast<decltype(f_gather)>(p[1]);
@@ -479,6 +483,7 @@ PyObject *bind(PyObject *, PyObject *args)
     f_prefill = reinterpret_cast<decltype(f_prefill)>(p[4]);
     f_attention_size = reinterpret_cast<decltype(f_attention_size)>(p[5]);
     f_prefill_size = reinterpret_cast<decltype(f_prefill_size)>(p[6]);
+    f_attention_launches = reinterpret_cast<decltype(f_attention_launches)>(p[7]);
     Py_INCREF(check);
     Py_XSETREF(g_check, check);
     Py_RETURN_NONE;

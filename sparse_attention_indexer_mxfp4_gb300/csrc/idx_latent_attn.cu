@@ -1363,6 +1363,22 @@ idx_status check_attn(const uint16_t *q, int64_t ldq_row, int64_t ldq_head, int 
     return IDX_OK;
 }
 
+// Groups of columns: `hpg` heads of `rpg` query rows each.
+struct Columns {
+    int hpg, rpg, hgroups, groups;
+};
+
+Columns columns_for(int H, int next)
+{
+    Columns c;
+    // up to 64 heads, and as many query rows of them as 64 hold
+    c.hpg = std::min(H, 64);
+    c.rpg = std::min(next, 64 / c.hpg);
+    c.hgroups = (H + c.hpg - 1) / c.hpg;
+    c.groups = c.hgroups * ((next + c.rpg - 1) / c.rpg);
+    return c;
+}
+
 // Rows of few keys are not cut: up to four tiles a CTA more cost less than
 // the joining kernel (7.0 us whole, 8.6 cut, for 4 rows of 64 keys).
 constexpr int64_t kUncutKeys = 4 * kTile;
@@ -1380,12 +1396,12 @@ idx_status run_attn(AttnArgs &a, const uint16_t *q, int64_t ldq_row, int64_t ldq
     a.status = device_status_ptr();
     if (!a.status)
         return IDX_ERR_CUDA;
-    // columns: up to 64 heads, and as many query rows of them as 64 hold
-    a.hpg = std::min(a.H, 64);
-    a.rpg = std::min(a.next, 64 / a.hpg);
+    const Columns c = columns_for(a.H, a.next);
+    a.hpg = c.hpg;
+    a.rpg = c.rpg;
     a.inv_hpg = 65536 / a.hpg + 1;
-    a.hgroups = (a.H + a.hpg - 1) / a.hpg;
-    a.groups = a.hgroups * ((a.next + a.rpg - 1) / a.rpg);
+    a.hgroups = c.hgroups;
+    a.groups = c.groups;
     // places in out are kept in units of eight elements, in 32 bits
     const int64_t span = (a.next - 1) * a.ldo_row + (a.H - 1) * a.ldo_head;
     if (a.groups > sm_count() || most > INT32_MAX / 4 || a.pool.stride > INT32_MAX ||
@@ -1433,6 +1449,14 @@ extern "C" size_t idx_latent_attention_workspace_size(int R, int H, int64_t max_
     // rows of a sequence share whatever H is)
     const int64_t columns = columns_of((int)std::min<int64_t>(64, (int64_t)R * H));
     return cut_bytes() + (size_t)(2 * sm_count() * (kLatent + 2) * columns) * sizeof(float);
+}
+
+extern "C" int idx_latent_attention_launches(int R, int next_n, int H, int64_t max_keys)
+{
+    if (R <= 0 || next_n <= 0 || H <= 0)
+        return 0;
+    // rows are cut where a group of columns has two CTAs or more
+    return max_keys > kUncutKeys && sm_count() / columns_for(H, next_n).groups > 1 ? 2 : 1;
 }
 
 extern "C" idx_status idx_latent_attention(

@@ -326,3 +326,29 @@ def test_strides_over_one_element_are_free():
                                     _odd(kvt[..., 128:], 0, 1), _dev(cq), _dev(ck), SCALE, out=_odd(o, 0, 1))
     _clean()
     _check_prefill(cq, ck, q, kv, lat[:, 512:], out, lse, True)
+
+
+# ----------------------------------------------------- launches that are counted
+
+
+def test_launches_of_prepared_calls():
+    """The joining kernel is counted where rows are cut, and nothing where nothing is to do."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    bf = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+    pool = torch.zeros(2, 64 * 648, dtype=torch.uint8, device="cuda")
+    slots = lambda R, n: B.prepare_latent_attention(bf(R, 4, 576), pool, 64, 1, i32(n), i32(R + 1), SCALE).kernels  # noqa: E731
+    assert [slots(0, 0), slots(3, 256), slots(3, 257)] == [0, 1, 2]
+    for next_n in (1, sms // 2, sms // 2 + 1, sms):  # 64 heads: a group of columns a row
+        call = B.prepare_paged_latent_attention(bf(next_n, 64, 576), pool, 64, 1, i32(1, 20), i32(1), next_n, SCALE,
+                                                1000)
+        assert call.kernels == (2 if 2 * next_n <= sms else 1), next_n
+        call()
+    _clean()
+    pre = lambda q, k, b: B.prepare_latent_prefill(bf(q, 2, 192), bf(k, 2, 128), bf(k, 64), bf(k, 2, 128), i32(b + 1),  # noqa: E731
+                                                   i32(b + 1), SCALE).kernels
+    assert [pre(0, 9, 1), pre(4, 512, 1), pre(4, 513, 1), pre(4, 513, 0)] == [0, 1, 2, 0]
+    out = lambda n, b: B.prepare_latent_gather(pool, 64, 1, i32(max(b, 1), 2), i32(b + 1), bf(n, 576)).kernels  # noqa: E731
+    assert [out(0, 1), out(5, 0), out(5, 1)] == [0, 0, 1]
+    put = lambda n: B.prepare_latent_store(bf(n, 576), None, None, None, 0.0, pool, 64, i32(n).long(), 1).kernels  # noqa: E731
+    assert [put(0), put(3)] == [0, 1]

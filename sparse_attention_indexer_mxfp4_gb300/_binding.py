@@ -95,7 +95,7 @@ def lib() -> ctypes.CDLL:
         return _lib
     with _lock:
         if _lib is None:
-            path = _build.build() if not os.environ.get("IDX_NO_BUILD") else _build.LIB
+            path = _build.build_library() if not os.environ.get("IDX_NO_BUILD") else _build.LIB
             if not os.path.exists(path):
                 raise IndexerError(f"indexer library missing: {path}")
             L = ctypes.CDLL(path)
@@ -623,22 +623,26 @@ def latent_page_bytes(page_size, fmt) -> int:
 
 
 def _latent_calls():
-    """The latent calls' extension, bound to the loaded library."""
+    """The latent calls' extension (building it first if its sources are
+    newer), bound to the loaded library."""
     global _calls
-    if _calls is None:
-        L = lib()
-        if not os.path.exists(_build.CALLS):
-            raise IndexerError(f"{_build.CALLS} is missing: build the library first")
-        loader = importlib.machinery.ExtensionFileLoader("_latent_calls", _build.CALLS)
-        mod = importlib.util.module_from_spec(
-            importlib.util.spec_from_file_location("_latent_calls", _build.CALLS, loader=loader))
-        loader.exec_module(mod)
-        mod.bind(_check, *(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
-            "idx_latent_store", "idx_latent_gather", "idx_latent_attention",
-            "idx_paged_latent_attention", "idx_latent_prefill",
-            "idx_latent_attention_workspace_size", "idx_latent_prefill_workspace_size",
-            "idx_latent_attention_launches")))
-        _calls = mod
+    L = lib()
+    with _lock:
+        if _calls is None:
+            if not os.environ.get("IDX_NO_BUILD"):
+                _build.build_calls()
+            if not os.path.exists(_build.CALLS):
+                raise IndexerError(f"{_build.CALLS} is missing: build the package first")
+            loader = importlib.machinery.ExtensionFileLoader("_latent_calls", _build.CALLS)
+            mod = importlib.util.module_from_spec(
+                importlib.util.spec_from_file_location("_latent_calls", _build.CALLS, loader=loader))
+            loader.exec_module(mod)
+            mod.bind(_check, *(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+                "idx_latent_store", "idx_latent_gather", "idx_latent_attention",
+                "idx_paged_latent_attention", "idx_latent_prefill",
+                "idx_latent_attention_workspace_size", "idx_latent_prefill_workspace_size",
+                "idx_latent_attention_launches")))
+            _calls = mod
     return _calls
 
 

@@ -31,6 +31,9 @@ class LatentLayer:
 
     def __init__(self, w_uk, w_uv, norm_weight, cos_sin, num_pages, page_size,
                  fmt=B.LATENT_FP8, eps=1e-6, scale=None):
+        for w in (w_uk, w_uv):
+            if w.dtype != torch.bfloat16 or w.shape != (w_uk.shape[0], NOPE, LATENT):
+                raise ValueError(f"w_uk and w_uv must be bfloat16 [H, {NOPE}, {LATENT}]")
         self.w_uk, self.w_uv = w_uk.contiguous(), w_uv.contiguous()
         # one product makes both, side by side for each head: [512, H * 256]
         self.w_up = torch.cat([w_uk, w_uv], 1).reshape(-1, LATENT).t().contiguous()
@@ -90,6 +93,9 @@ class SparseDecodeStep:
     indexer's (synth.PagedCase); its block table places the latent cache too."""
 
     def __init__(self, case, layer: LatentLayer, q, device="cuda"):
+        if case.page_size != layer.page_size or case.num_pages > layer.pages.shape[0]:
+            raise ValueError(f"the indexer's {case.num_pages} pages of {case.page_size} tokens are not "
+                             f"the layer's {layer.pages.shape[0]} pages of {layer.page_size}")
         self.indexer = IndexerStep(case, device=device)
         self.layer = layer
         self.q = layer.absorb(q)  # a query's products belong to the layers before

@@ -352,3 +352,97 @@ def test_launches_of_prepared_calls():
     assert [out(0, 1), out(5, 0), out(5, 1)] == [0, 0, 1]
     put = lambda n: B.prepare_latent_store(bf(n, 576), None, None, None, 0.0, pool, 64, i32(n).long(), 1).kernels  # noqa: E731
     assert [put(0), put(3)] == [0, 1]
+
+
+# ------------------------------- scratch and outputs that are given, rows that are cut
+
+
+class _Scratch:
+    """Scratch of exactly n bytes between guards, all of it NaN in 32 bits before the call."""
+
+    def __init__(self, n):
+        assert n > 0
+        self.n, self.all = n, torch.full((n + 4096,), 255, dtype=torch.uint8, device="cuda")
+
+    def __call__(self, less=0):
+        return self.all[2048:2048 + self.n - less]
+
+    def check(self):
+        torch.cuda.synchronize()
+        assert (self.all[:2048] == 255).all() and (self.all[2048 + self.n:] == 255).all()
+        assert (self.all != 255).any()  # it was used
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lens,H", [([2000, 0, 700], 24), ([1, 5000], 128), ([300] * 200 + [1500], 8), ([2048] * 20, 64)])
+def test_sparse_given_scratch_and_outputs_of_cut_rows(fmt, lens, H):
+    rng = np.random.default_rng(sum(lens) + H)
+    R = len(lens)
+    pool, slots, indptr, _, _ = _sparse_case(rng, fmt, lens, H, 64)
+    big, q = _bf16(rng.standard_normal((R, H + 6, 584)))
+    o = torch.full((R, H + 6, 520), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((R, H + 4), 3.0, device="cuda")
+    ws = _Scratch(B.latent_attention_workspace_size(R, H, len(slots)))
+    args = big[:, 2:2 + H, :576], _dev(pool), 64, fmt, _dev(slots), _dev(indptr), SCALE
+    with pytest.raises(B.IndexerError, match="WORKSPACE"):
+        B.idx_latent_attention(*args, workspace=ws(16))
+    got, gl = B.idx_latent_attention(*args, out=o[:, 3:3 + H, :512], lse=lse[:, :H], workspace=ws())
+    _clean()
+    ws.check()
+    some = sorted({0, 1, R // 2, R - 1})
+    _check_sparse(pool, fmt, 64, slots, indptr, q[:, 2:2 + H, :576], got, gl, rows=some)
+    made, ml = B.idx_latent_attention(*args)
+    assert torch.equal(made, got) and torch.equal(ml, gl)
+    assert (o[:, :3] == 3).all() and (o[:, 3 + H:] == 3).all() and (o[..., 512:] == 3).all() and (lse[:, H:] == 3).all()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_paged_given_scratch_and_outputs_of_cut_rows(fmt):
+    rng = np.random.default_rng(51)
+    ctx, next_n, H = [1800, 3, 900], 2, 24
+    pool, bt, slots = _paged_case(rng, fmt, ctx, 64)
+    qt, q = _bf16(rng.standard_normal((6, H, 576)))
+    o = torch.full((H + 1, 6, 520), 3.0, dtype=torch.bfloat16, device="cuda")  # heads before rows
+    lse = torch.full((6, H + 4), 3.0, device="cuda")
+    ws = _Scratch(B.latent_attention_workspace_size(6, H, 2000))
+    out, gl = B.idx_paged_latent_attention(qt, _dev(pool), 64, fmt, _dev(bt), _dev(np.array(ctx, np.int32)), next_n, SCALE,
+                                           1800, out=o[:H, :, :512].transpose(0, 1), lse=lse[:, :H], workspace=ws())
+    _clean()
+    ws.check()
+    out, gl = _np(out), _np(gl)
+    for b, c in enumerate(ctx):
+        tok = ref.read_tokens(pool, fmt, 64, slots[b])
+        for j in range(next_n):
+            t = tok[:max(0, c - next_n + j + 1)]
+            ref.check(out[2 * b + j], gl[2 * b + j], ref.attend(q[2 * b + j], t, t[:, :512], SCALE))
+    assert (o[H:] == 3).all() and (o[..., 512:] == 3).all() and (lse[:, H:] == 3).all()
+
+
+@pytest.mark.parametrize("lq,lk,H,causal", [([300, 70, 200], [1300, 150, 900], 3, True), ([16], [20000], 1, True),
+                                            ([1, 40, 5], [3000, 90, 4000], 2, False), ([700, 1, 257], [700, 900, 257], 5, True)])
+def test_prefill_given_scratch_and_outputs_of_cut_blocks(lq, lk, H, causal):
+    """The middle sequence, where there is one, is NaN; rows past the last one and what lies beside a head stay as they were."""
+    rng = np.random.default_rng(sum(lq) + H)
+    cq, ck, _, _, kvt, kv, latt, lat = _prefill_case(rng, lq, lk, H)
+    if len(lq) > 1:
+        kvt[ck[1]:ck[2]] = float("nan")
+        latt[ck[1]:ck[2]] = float("nan")
+    n = sum(lq)
+    big, q = _bf16(rng.standard_normal((n + 6, H + 2, 200)))
+    o = torch.full((n + 6, H + 2, 136), 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((n + 6, H + 1), 3.0, device="cuda")
+    args = big[:, 1:1 + H, :192], kvt[..., :128], latt[:, 512:], kvt[..., 128:], _dev(cq), _dev(ck), SCALE
+    ws = _Scratch(B.latent_prefill_workspace_size(n + 6, sum(lk) + 5, H))
+    with pytest.raises(B.IndexerError, match="WORKSPACE"):
+        B.idx_latent_prefill(*args, workspace=ws(16))
+    got, gl = B.idx_latent_prefill(*args, causal=causal, out=o[:, 2:, :128], lse=lse[:, :H], workspace=ws())
+    _clean()
+    ws.check()
+    seqs = [0, 2] if len(lq) > 1 else [0]
+    _check_prefill(cq, ck, q[:, 1:1 + H, :192], kv, lat[:, 512:], got, gl, causal, seqs=seqs)
+    if len(lq) > 1:
+        assert torch.isnan(got[cq[1]:cq[2]]).all() and torch.isnan(gl[cq[1]:cq[2]]).all()
+    assert (o[n:] == 3).all() and (o[:, :2] == 3).all() and (o[..., 128:] == 3).all()
+    assert (lse[n:] == 3).all() and (lse[:, H] == 3).all()
+    made, ml = B.idx_latent_prefill(*args, causal=causal)
+    assert torch.equal(made[:n].nan_to_num(7), got[:n].nan_to_num(7)) and torch.equal(ml[:n].nan_to_num(7), gl[:n].nan_to_num(7))

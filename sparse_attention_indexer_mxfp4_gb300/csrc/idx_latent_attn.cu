@@ -1354,7 +1354,7 @@ idx_status check_attn(const uint16_t *q, int64_t ldq_row, int64_t ldq_head, int 
                       int64_t ldo_head, const float *lse, int64_t ld_lse)
 {
     if (!q || !out || ldq_head < (int64_t)L + rope_dim || ldq_row < 0 || ldo_head < L ||
-        ldo_row < 0 || !(scale > 0.0f) || !(scale <= 3.4e38f) || (lse && ld_lse < H))
+        ldo_row < 0 || !(scale > 0.0f) || !(scale * kLog2e <= 3.4e38f) || (lse && ld_lse < H))
         return IDX_ERR_INVALID_ARG;
     if (L != kLatent || rope_dim != kLatRope || H > kMaxHeads || !aligned16(q) ||
         !aligned16(out) || ldq_row % 8 != 0 || ldq_head % 8 != 0 || ldo_row % 8 != 0 ||

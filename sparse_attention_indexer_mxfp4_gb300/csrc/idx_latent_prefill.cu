@@ -900,7 +900,7 @@ extern "C" idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int
     if (B == 0 || Tq == 0)
         return IDX_OK;
     if (!q || !cu_q || !cu_k || !out || (Tk > 0 && (!k || !k_rope || !v)) || !(scale > 0.0f) ||
-        !(scale <= 3.4e38f) || ldq_head < (int64_t)d_nope + d_rope || ldq_row < 0 ||
+        !(scale * kLog2e <= 3.4e38f) || ldq_head < (int64_t)d_nope + d_rope || ldq_row < 0 ||
         ldk_head < d_nope || ldk_row < 0 || ld_rope < d_rope || ldv_head < d_v || ldv_row < 0 ||
         ldo_head < d_v || ldo_row < 0 || (lse && ld_lse < H))
         return IDX_ERR_INVALID_ARG;

@@ -94,3 +94,23 @@ def test_flag_without_a_truth_value(name, flag):
         for args in (good(), _good(name)):
             with pytest.raises(RuntimeError, match="Boolean value"):
                 f(*args, **{flag: torch.zeros(2)})
+
+
+def test_scale_past_its_power_of_two():
+    """The kernels take the scale times log2(e), which has to be a number."""
+    call = {"idx_latent_attention": 15, "idx_paged_latent_attention": 18, "idx_latent_prefill": 20}
+    fake = 0x10000
+    base = {
+        "idx_latent_attention": [fake, 64 * 576, 576, fake, 41472, 10, 64, 1, fake, fake, 1000, 4, 64, 512, 64, 0.1, fake,
+                                 64 * 512, 512, fake, 64, None, 0, None],
+        "idx_paged_latent_attention": [fake, 64 * 576, 576, fake, 41472, 10, 64, 1, fake, 16, fake, 0, 2, 2, 1000, 64, 512,
+                                       64, 0.1, fake, 64 * 512, 512, None, 0, None, 0, None],
+        "idx_latent_prefill": [fake, 64 * 192, 192, fake, 64 * 256, 256, fake, 576, fake, 64 * 256, 256, fake, fake, 2, 100,
+                               1000, 64, 128, 64, 128, 0.1, 1, fake, 64 * 128, 128, fake, 64, None, 0, None],
+    }
+    invalid, workspace = 1, 3
+    for name, at in call.items():
+        for scale, want in ((2.3e38, workspace), (2.4e38, invalid), (3.4e38, invalid)):
+            args = list(base[name])
+            args[at] = scale
+            assert getattr(B.lib(), name)(*args) == want, (name, scale)

@@ -596,8 +596,12 @@ idx_status idx_latent_gather(const uint8_t *kv_pages, int64_t page_stride_bytes,
  *             share one ws must not overlap in time.
  * A slot outside the pool is left out of its row and sets IDX_DEV_BAD_PAGE.
  * The sums run in fp32, the weights enter the second product in bf16; the
- * order of the sums depends on the arguments and the lengths alone.
- * Supported: L = 512, rope_dim = 64, 1 <= H <= 128.
+ * order of the sums depends on the arguments and the lengths alone.  A weight
+ * may stand 2^40 over the first token's before the sums are rescaled: values
+ * up to 2^70 in magnitude keep them in range.
+ * Supported: L = 512, rope_dim = 64, 1 <= H <= 128, num_slots / 64 + R up to
+ * 2^29 (the paged form: B * ceil(max_model_len / 64)), pages of less than 2^31
+ * bytes, scale * log2(e) finite.
  * Errors: IDX_ERR_INVALID_ARG, IDX_ERR_UNSUPPORTED (sizes, alignment),
  * IDX_ERR_WORKSPACE (ws missing or too small), IDX_ERR_CUDA.
  * ---------------------------------------------------------------------- */
@@ -655,6 +659,7 @@ int idx_latent_attention_launches(int R, int next_n, int H, int64_t max_keys);
  *           last query sees every key; otherwise to all Lk.  Bounds that
  *           descend or leave [0, Tq] or [0, Tk] are clamped and set
  *           IDX_DEV_BAD_BOUNDS.
+ *   scale   as idx_latent_attention, and the values' magnitude.
  *   out     bf16 bits [Tq, H, 128], strides ldo_row, ldo_head.
  *   lse     fp32 [Tq, ld_lse] (ld_lse >= H) or NULL, as idx_latent_attention.
  *           A query with no key gets zeros and -inf; rows of q outside every

@@ -3,7 +3,7 @@
 //
 // A decode step's call is a few microseconds of GPU time; attribute look-ups,
 // three allocations and 24 converted arguments in Python took 16 to 22 us of
-// host time on a Grace core.  The functions come as addresses of the loaded
+// host time on a Grace core (here 7 to 8).  The functions come as addresses of the loaded
 // library (bind), so there is one copy of it in the process.
 #include <Python.h>
 

@@ -24,15 +24,16 @@
 // share are finished there; the others leave unnormalised sums with their
 // maximum in scratch and a second kernel joins them in share order.
 //
-// What bounds it: with 64 columns shared memory's data path, about 3250 of 3350
-// cycles a tile of 8-bit tokens (wavefronts: 36 x 32 and 16 x 48 of the products'
-// operands, 700 of stores, 700 of loads and shuffles): 2048 rows x 64 heads x
-// 2048 slots 799 us, 730 TFLOP/s, the tensor pipe 47 % busy.  With 16 columns
-// the same path (2450 of 2700 cycles) and DRAM share it: 32 contexts of 4 to 32
-// thousand 8-bit tokens 104 us, 4.0 TB/s.  Bf16 tokens need no widening: four
-// contexts of 100 to 131 thousand, 32 columns, 102 us with the joining kernel,
-// 5.6 TB/s while this one runs.  Few rows wait: about 9 thousand cycles until a
-// CTA has its first tokens, twice a table and then what it names.
+// What bounds it: with 64 columns shared memory's data path.  Of 3600 cycles a
+// tile of 8-bit tokens the products' operands take 1920 wavefronts (36 x 32 and
+// 16 x 48), loads, stores and shuffles 1930 (the counters overlap a little):
+// 2048 rows x 64 heads x 2048 slots 802 us, 728 TFLOP/s, the tensor pipe 47 %
+// busy.  With 16 columns it is the same path (1300 and 1590 of 2920 cycles) and
+// DRAM beside it: 32 contexts of 4 to 32 thousand 8-bit tokens 107 us, 3.8 TB/s.
+// Bf16 tokens need no widening: four contexts of 100 to 131 thousand, 32 columns,
+// 102 us with the joining kernel, 5.6 TB/s while this one runs.  Few rows wait:
+// about 9 thousand cycles until a CTA has its first tokens, twice a table and
+// then what it names.
 //
 // Warps: 0-3 softmax and epilogue; 4-11 bring tokens in (slot -> page ->
 // global loads; 8-bit codes are widened to bf16 on the way, exactly, by moving

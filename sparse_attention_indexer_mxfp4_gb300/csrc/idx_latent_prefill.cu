@@ -15,9 +15,10 @@
 // (12 of 65 and 16 of 33 each), a tile's softmax 1150, by its instructions
 // (pairs of scores share them where they can; exponentials by polynomial beside
 // the special-function unit's cost more of them and time).  Measured: 3030
-// cycles; 2048 queries x 64 heads at the end of 8192 tokens 372 to 380 us, 1600
-// TFLOP/s, where the GPU's power limit holds it whatever the kernel saves; 7 whole
-// prompts of 65 to 1500 tokens x 16 heads 54.8 us.
+// cycles; 2048 queries x 64 heads at the end of 8192 tokens 380 to 397 us in
+// short bursts (1500 to 1580 TFLOP/s) and 432 to 444 in calls that go on, where
+// the GPU's power limit holds it whatever the kernel saves; 7 whole prompts of
+// 65 to 1500 tokens x 16 heads 55 us.
 //
 // Keys and values come by TMA in pieces of 64 elements of 128 tokens (16 KB,
 // 128-byte swizzled), five a tile (three of K, the last shared by all heads,

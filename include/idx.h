@@ -688,6 +688,191 @@ idx_status idx_latent_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_he
 size_t idx_latent_prefill_workspace_size(int Tq, int Tk, int H);
 
 /* ------------------------------------------------------------------------
+ * Grouped-head attention over a 4-bit cache: H query heads share kv_heads key
+ * and value heads of D = 128 elements, head h that of h / (H / kv_heads).  The
+ * slots and block tables are the indexer's.  These calls have no counterpart in
+ * the pages; layouts and conventions follow the latent calls'.
+ *
+ * Cached elements are e2m1 (element 2i the low nibble of byte i) with one e8m0
+ * scale for each 32: the value of a code is code * 2^(scale - 127), 255 is NaN.
+ * Block-flat pages, page p at kv_pages + p * page_stride_bytes (16-byte aligned,
+ * stride a multiple of 16 and at least page_size * kv_heads * 136):
+ *     K codes  [kv_heads][page_size][64]      V codes  [kv_heads][page_size][64]
+ *     K scales [kv_heads][page_size][4]       V scales [kv_heads][page_size][4]
+ * A call's D is the heads' dimension: 128 is supported.  Pages hold less than
+ * 2^31 slots in all.
+ * ---------------------------------------------------------------------- */
+
+/* ------------------------------------------------------------------------
+ * idx_grouped_prefill -- attention of ragged sequences before anything is cached
+ * in 4 bits (or after idx_kv4_gather).
+ *
+ *   q       bf16 bits [Tq, H, 128], strides ldq_row, ldq_head.
+ *   k, v    bf16 bits [Tk, kv_heads, 128], strides ldk_*, ldv_*.
+ *   The rest as idx_latent_prefill (bounds, causal, scale, out, lse, rows that see
+ *   nothing, values that are not finite, ws of
+ *   idx_grouped_prefill_workspace_size bytes).
+ * Supported: D = 128, H a multiple of kv_heads, H <= 65535.
+ * ---------------------------------------------------------------------- */
+idx_status idx_grouped_prefill(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                               const uint16_t *k, int64_t ldk_row, int64_t ldk_head,
+                               const uint16_t *v, int64_t ldv_row, int64_t ldv_head,
+                               const int32_t *cu_q, const int32_t *cu_k, int B, int Tq, int Tk,
+                               int H, int kv_heads, int D, float scale, int causal, uint16_t *out,
+                               int64_t ldo_row, int64_t ldo_head, float *lse, int64_t ld_lse,
+                               void *ws, size_t ws_bytes, idx_stream_t stream);
+
+size_t idx_grouped_prefill_workspace_size(int Tq, int Tk, int H);
+
+/* ------------------------------------------------------------------------
+ * idx_kv4_store -- quantise new tokens into their cache slots.
+ *
+ *   k, v        bf16 bits [T, kv_heads, 128] as the attention sees them (rotated),
+ *               strides ldk_row, ldk_head, ldv_row, ldv_head (multiples of 8),
+ *               16-byte aligned.
+ *   slot_mapping [T] int64: page * page_size + offset; negative skips.
+ *   One exponent per 32 elements, bits = clamp(ceil(log2(max(amax, 2^-126) / 6))
+ *   + 127, 0, 254), codes of x * 2^(127 - bits) to nearest even; a group holding a
+ *   NaN or an infinity gets the e8m0 NaN (255) and codes of zero.
+ * A slot outside the pool sets IDX_DEV_BAD_PAGE; its token is skipped.  Two tokens
+ * with one slot race.
+ * ---------------------------------------------------------------------- */
+idx_status idx_kv4_store(const uint16_t *k, int64_t ldk_row, int64_t ldk_head, const uint16_t *v,
+                         int64_t ldv_row, int64_t ldv_head, int T, int kv_heads, int D,
+                         uint8_t *kv_pages, int64_t page_stride_bytes, int num_pages,
+                         int page_size, const int64_t *slot_mapping, idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_kv4_gather -- read cached tokens back as rows of bf16 (which holds every
+ * value of magnitude below 2^128 exactly), for a later chunk of a prompt.
+ * block_table, max_blocks, cu_lens, seq_starts, N and the errors as
+ * idx_latent_gather; k_out, v_out bf16 bits [N, kv_heads, 128] with strides
+ * (multiples of 8), 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_stride_bytes, int num_pages,
+                          int page_size, int kv_heads, int D, const int32_t *block_table,
+                          int64_t bt_stride, int max_blocks, const int32_t *cu_lens,
+                          const int32_t *seq_starts, int B, int N, uint16_t *k_out,
+                          int64_t ldk_row, int64_t ldk_head, uint16_t *v_out, int64_t ldv_row,
+                          int64_t ldv_head, idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_kv4_attention -- attention over ragged slots (the output of
+ * idx_topk_ragged_slots):
+ *     s = scale * (q[r, h, :] . k),   out[r, h, :] = sum softmax(s) v
+ *
+ *   q         bf16 bits [R, H, 128] with strides ldq_row, ldq_head (elements,
+ *             multiples of 8; 16-byte aligned).
+ *   slots, indptr, num_slots, scale, out (bf16 bits [R, H, 128]), lse and rows
+ *             without a token as idx_latent_attention.
+ *   ws, ws_bytes  device scratch, 16-byte aligned, of at least
+ *             idx_kv4_attention_workspace_size(R, 1, H, kv_heads, num_slots) bytes
+ *             (the paged form: R = B * next_n, next_n, max_model_len); NULL where
+ *             that is 0.  Calls that share one ws must not overlap in time.
+ * A slot outside the pool is left out of its row and sets IDX_DEV_BAD_PAGE; an
+ * indptr that descends, and lists more tiles than num_slots tokens in R rows have,
+ * sets IDX_DEV_BAD_BOUNDS and nothing is written.
+ * Queries, keys and weights enter the products in 16 bits that hold queries and
+ * codes exactly (a query element 2^29 under its row's largest loses bits); scores,
+ * maxima and sums are held in 32.  The order of the sums depends on the arguments
+ * and the lengths alone.  Values up to 2^70 in magnitude keep the sums in range.
+ * Supported: D = 128, H a multiple of kv_heads, up to 2^31 tiles (128 tokens of a
+ * row and key head), scale * log2(e) finite.
+ * ---------------------------------------------------------------------- */
+idx_status idx_kv4_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                             const uint8_t *kv_pages, int64_t page_stride_bytes, int num_pages,
+                             int page_size, const int32_t *slots, const int32_t *indptr,
+                             int64_t num_slots, int R, int H, int kv_heads, int D, float scale,
+                             uint16_t *out, int64_t ldo_row, int64_t ldo_head, float *lse,
+                             int64_t ld_lse, void *ws, size_t ws_bytes, idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_paged_kv4_attention -- the same over whole contexts: row j of sequence b
+ * attends to its tokens [0, ke), block_table, context_lens, ctx_per_row, next_n
+ * and max_model_len as idx_paged_latent_attention.  Tokens of a page outside the
+ * pool are left out and set IDX_DEV_BAD_PAGE.
+ * ---------------------------------------------------------------------- */
+idx_status idx_paged_kv4_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                                   const uint8_t *kv_pages, int64_t page_stride_bytes,
+                                   int num_pages, int page_size, const int32_t *block_table,
+                                   int64_t bt_stride, const int32_t *context_lens,
+                                   int ctx_per_row, int B, int next_n, int max_model_len, int H,
+                                   int kv_heads, int D, float scale, uint16_t *out,
+                                   int64_t ldo_row, int64_t ldo_head, float *lse, int64_t ld_lse,
+                                   void *ws, size_t ws_bytes, idx_stream_t stream);
+
+/* Bytes of ws for R rows, next_n of them a sequence, of at most max_keys keys, on
+ * the current device; 0 where they are so few that rows are not split. */
+size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int kv_heads, int64_t max_keys);
+
+/* ------------------------------------------------------------------------
+ * idx_paged_kv4_weights -- what an attention gave each cached token:
+ *     out[b, g, t] = mass[b, g, t] + sum over the rows j of sequence b and the
+ *                    heads h of key head g of exp(scale * (q[j, h, :] . k) - lse[j, h])
+ * over the rows that see token t; columns that none sees get mass.
+ *
+ *   q, the cache, block_table, context_lens, next_n, scale, max_model_len  as
+ *             idx_paged_kv4_attention.
+ *   lse       fp32 [B * next_n, ld_lse]: that call's (-inf, a row that saw
+ *             nothing, counts as 0).
+ *   mass      fp32, mass[b * ld_batch + g * ld_head + t], t in [0, width); NULL
+ *             stands for zeros.  width >= max_model_len.
+ *   out       the same shape, strides ldo_batch, ldo_head; may be mass.
+ * Sums are in 32 bits, in an order that the arguments alone decide.
+ * ---------------------------------------------------------------------- */
+idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                                 const uint8_t *kv_pages, int64_t page_stride_bytes,
+                                 int num_pages, int page_size, const int32_t *block_table,
+                                 int64_t bt_stride, const int32_t *context_lens, int ctx_per_row,
+                                 int B, int next_n, int max_model_len, int H, int kv_heads, int D,
+                                 float scale, const float *lse, int64_t ld_lse, const float *mass,
+                                 int64_t ld_batch, int64_t ld_head, int width, float *out,
+                                 int64_t ldo_batch, int64_t ldo_head, idx_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * idx_kv4_evict -- shrink sequences to their heaviest tokens: of sequence b's n =
+ * context_lens[b] tokens the last `recent` stay, and of the others the
+ * budget - recent of most weight (ties: the lower position; NaN counts as the
+ * least), all of them where n <= budget.  They go, in their order, to positions 0,
+ * 1, ... of the pages of new_table.
+ *
+ *   mass      fp32, mass[b * ld_batch + g * ld_head + t], t in [0, ld_mass): the
+ *             tokens' weights.  A context past ld_mass is cut there and sets
+ *             IDX_DEV_BAD_BOUNDS.
+ *   budget, recent  0 <= recent <= budget.
+ *   whole_tokens  0: each key head keeps its own tokens.  Otherwise a token stays
+ *             or goes with all its heads, by the sum of their weights (in 64 bits,
+ *             rounded to 32), so that positions stay aligned with the indexer's.
+ *   kv_pages  read through block_table and written through new_table (max_blocks
+ *             and new_blocks columns valid; new_blocks * page_size >= the smaller
+ *             of budget and ld_mass).  The pages that new_table names for kept
+ *             tokens must not be among those being read.
+ *   keep      int32 [B, lists, budget], lists = whole_tokens ? 1 : kv_heads: the
+ *             positions that stayed, ascending, then -1.
+ *   new_lens  int32 [B]: min(n, budget).
+ *   new_mass  fp32 [B, kv_heads, budget]: their weights, then zeros.
+ *   ws        device scratch of idx_kv4_evict_workspace_size bytes (0: NULL).
+ * A page outside the pool sets IDX_DEV_BAD_PAGE: tokens from it become zeros,
+ * tokens to it are dropped.
+ * Supported: D = 128, B * lists <= 65535.
+ * ---------------------------------------------------------------------- */
+idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t ld_head, int ld_mass,
+                         const int32_t *context_lens, int B, int kv_heads, int D, int budget,
+                         int recent, int whole_tokens, uint8_t *kv_pages,
+                         int64_t page_stride_bytes, int num_pages, int page_size,
+                         const int32_t *block_table, int64_t bt_stride, int max_blocks,
+                         const int32_t *new_table, int64_t new_stride, int new_blocks,
+                         int32_t *keep, int32_t *new_lens, float *new_mass, void *ws,
+                         size_t ws_bytes, idx_stream_t stream);
+
+size_t idx_kv4_evict_workspace_size(int B, int kv_heads, int ld_mass, int budget, int recent,
+                                    int whole_tokens);
+
+/* Kernels that such a call launches on the current device. */
+int idx_kv4_evict_launches(int B, int kv_heads, int ld_mass, int budget, int recent,
+                           int whole_tokens);
+
+/* ------------------------------------------------------------------------
  * idx_get_device_status -- read and clear the sticky device status word of
  * the current device (IDX_DEV_* bits).  Synchronises `stream`; it is the
  * only call that does.  *out receives the bits.

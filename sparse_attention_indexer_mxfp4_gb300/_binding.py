@@ -26,6 +26,7 @@ LATENT_BF16 = 0
 LATENT_FP8 = 1
 LATENT_DIM = 512  # latents of a cached token
 LATENT_ROPE = 64  # its rotated elements
+KV4_DIM = 128  # elements of a cached token's keys and values, of one key head
 
 IDX_OK = 0
 _ERRORS = {1: "IDX_ERR_INVALID_ARG", 2: "IDX_ERR_UNSUPPORTED", 3: "IDX_ERR_WORKSPACE",
@@ -73,6 +74,19 @@ _SIGNATURES = {
                                    _I, _I, ctypes.c_float, _P, _L, _L, _P, _L, _P, _S, _P],
     "idx_latent_prefill": [_P, _L, _L, _P, _L, _L, _P, _L, _P, _L, _L, _P, _P, _I, _I, _I, _I, _I,
                            _I, _I, ctypes.c_float, _I, _P, _L, _L, _P, _L, _P, _S, _P],
+    "idx_grouped_prefill": [_P, _L, _L, _P, _L, _L, _P, _L, _L, _P, _P, _I, _I, _I, _I, _I, _I,
+                            ctypes.c_float, _I, _P, _L, _L, _P, _L, _P, _S, _P],
+    "idx_kv4_store": [_P, _L, _L, _P, _L, _L, _I, _I, _I, _P, _L, _I, _I, _P, _P],
+    "idx_kv4_gather": [_P, _L, _I, _I, _I, _I, _P, _L, _I, _P, _P, _I, _I, _P, _L, _L, _P, _L, _L,
+                       _P],
+    "idx_kv4_attention": [_P, _L, _L, _P, _L, _I, _I, _P, _P, _L, _I, _I, _I, _I, ctypes.c_float,
+                          _P, _L, _L, _P, _L, _P, _S, _P],
+    "idx_paged_kv4_attention": [_P, _L, _L, _P, _L, _I, _I, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I,
+                                ctypes.c_float, _P, _L, _L, _P, _L, _P, _S, _P],
+    "idx_paged_kv4_weights": [_P, _L, _L, _P, _L, _I, _I, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I,
+                              ctypes.c_float, _P, _L, _P, _L, _L, _I, _P, _L, _L, _P],
+    "idx_kv4_evict": [_P, _L, _L, _I, _P, _I, _I, _I, _I, _I, _I, _P, _L, _I, _I, _P, _L, _I, _P, _L,
+                      _I, _P, _P, _P, _P, _S, _P],
     "idx_get_device_status": [_P, ctypes.POINTER(ctypes.c_uint32)],
     "idx_debug_wait_expiry": [_I, ctypes.c_uint64, _P],
     "idx_row_ends": [_P, _I, _I, _I, _I, _P, _P],
@@ -114,6 +128,14 @@ def lib() -> ctypes.CDLL:
             L.idx_latent_attention_launches.restype = _I
             L.idx_latent_prefill_workspace_size.argtypes = [_I, _I, _I]
             L.idx_latent_prefill_workspace_size.restype = _S
+            L.idx_grouped_prefill_workspace_size.argtypes = [_I, _I, _I]
+            L.idx_grouped_prefill_workspace_size.restype = _S
+            L.idx_kv4_attention_workspace_size.argtypes = [_I, _I, _I, _I, _L]
+            L.idx_kv4_attention_workspace_size.restype = _S
+            L.idx_kv4_evict_workspace_size.argtypes = [_I] * 6
+            L.idx_kv4_evict_workspace_size.restype = _S
+            L.idx_kv4_evict_launches.argtypes = [_I] * 6
+            L.idx_kv4_evict_launches.restype = _I
             L.idx_paged_mqa_logits_workspace_size.argtypes = [_I, _I, _I, _I]
             L.idx_paged_mqa_logits_workspace_size.restype = _S
             _lib = L
@@ -637,11 +659,15 @@ def _latent_calls():
             mod = importlib.util.module_from_spec(
                 importlib.util.spec_from_file_location("_latent_calls", _build.CALLS, loader=loader))
             loader.exec_module(mod)
-            mod.bind(_check, *(ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
+            mod.bind(_check, {name: ctypes.cast(getattr(L, name), ctypes.c_void_p).value for name in (
                 "idx_latent_store", "idx_latent_gather", "idx_latent_attention",
                 "idx_paged_latent_attention", "idx_latent_prefill",
                 "idx_latent_attention_workspace_size", "idx_latent_prefill_workspace_size",
-                "idx_latent_attention_launches")))
+                "idx_latent_attention_launches", "idx_grouped_prefill",
+                "idx_grouped_prefill_workspace_size", "idx_kv4_store", "idx_kv4_gather",
+                "idx_kv4_attention", "idx_paged_kv4_attention", "idx_kv4_attention_workspace_size",
+                "idx_paged_kv4_weights", "idx_kv4_evict", "idx_kv4_evict_workspace_size",
+                "idx_kv4_evict_launches")})
             _calls = mod
     return _calls
 
@@ -768,6 +794,190 @@ def idx_latent_prefill(q, k, k_rope, v, cu_q, cu_k, scale, causal=True, out=None
                                       workspace)
     return (_calls or _latent_calls()).prefill(False, q, k, k_rope, v, cu_q, cu_k, scale, causal,
                                                out, lse, workspace)
+
+
+def kv4_page_bytes(page_size, kv_heads) -> int:
+    """Bytes of a page of the 4-bit cache, rounded up to the 16 bytes a page stride needs."""
+    return -(-page_size * kv_heads * 2 * (KV4_DIM // 2 + KV4_DIM // 32) // 16) * 16
+
+
+def grouped_prefill_workspace_size(rows, keys, heads) -> int:
+    """Bytes of device scratch of the grouped prefill (0: none needed)."""
+    return int(lib().idx_grouped_prefill_workspace_size(rows, keys, heads))
+
+
+def kv4_attention_workspace_size(rows, heads, kv_heads, max_keys, next_n=1) -> int:
+    """Bytes of device scratch of the attention over the 4-bit cache on the current device, for
+    rows of at most max_keys keys, next_n of them a sequence (0: none needed)."""
+    return int(lib().idx_kv4_attention_workspace_size(rows, next_n, heads, kv_heads, max_keys))
+
+
+def kv4_evict_workspace_size(batch, kv_heads, columns, budget, recent, whole_tokens) -> int:
+    """Bytes of device scratch of an eviction (0: none needed)."""
+    return int(lib().idx_kv4_evict_workspace_size(batch, kv_heads, columns, budget, recent,
+                                                  int(whole_tokens)))
+
+
+def prepare_grouped_prefill(q, k, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                            workspace=True):
+    """Attention of ragged sequences with grouped heads.  q bf16 [Tq, H, 128], k and v bf16
+    [Tk, kv_heads, 128] (row and head strides free), query head h with key head
+    h // (H // kv_heads); cu_q, cu_k int32 [B + 1].  out bf16 [Tq, H, 128] and lse fp32 [Tq, H]
+    are made here when None (lse False: none).  workspace: True allocates the scratch here, or a
+    uint8 tensor of grouped_prefill_workspace_size(Tq, Tk, H) bytes."""
+    return Prepared("idx_grouped_prefill",
+                    *_latent_calls().grouped_prefill(True, q, k, v, cu_q, cu_k, scale, causal, out,
+                                                     lse, workspace))
+
+
+def idx_grouped_prefill(q, k, v, cu_q, cu_k, scale, causal=True, out=None, lse=None,
+                        workspace=True, stream=None):
+    """(out, lse) of the attention of ragged sequences with grouped heads."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_grouped_prefill(q, k, v, cu_q, cu_k, scale, causal, out, lse, workspace)
+    return (_calls or _latent_calls()).grouped_prefill(False, q, k, v, cu_q, cu_k, scale, causal,
+                                                       out, lse, workspace)
+
+
+def prepare_kv4_store(k, v, kv_pages, page_size, slot_mapping):
+    """New tokens into the 4-bit cache.  k and v bf16 [T, kv_heads, 128] as the attention sees
+    them (row and head strides free); slot_mapping int64 [T], negative skips."""
+    return Prepared("idx_kv4_store",
+                    *_latent_calls().kv4_store(True, k, v, kv_pages, page_size, slot_mapping))
+
+
+def idx_kv4_store(k, v, kv_pages, page_size, slot_mapping, stream=None):
+    """Quantise new tokens' keys and values into their slots."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_kv4_store(k, v, kv_pages, page_size, slot_mapping)
+    return (_calls or _latent_calls()).kv4_store(False, k, v, kv_pages, page_size, slot_mapping)
+
+
+def prepare_kv4_gather(kv_pages, page_size, block_table, cu_lens, k_out, v_out, seq_starts=None):
+    """Cached tokens back as rows of k_out and v_out (bf16 [N, kv_heads, 128], row and head
+    strides free): rows cu_lens[b] .. cu_lens[b + 1] are sequence b's tokens from seq_starts[b]
+    (None: 0) on."""
+    return Prepared("idx_kv4_gather",
+                    *_latent_calls().kv4_gather(True, kv_pages, page_size, block_table, cu_lens,
+                                                k_out, v_out, seq_starts))
+
+
+def idx_kv4_gather(kv_pages, page_size, block_table, cu_lens, k_out, v_out, seq_starts=None,
+                   stream=None):
+    """(k_out, v_out), filled with cached tokens."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_kv4_gather(kv_pages, page_size, block_table, cu_lens, k_out, v_out,
+                                  seq_starts)
+    return (_calls or _latent_calls()).kv4_gather(False, kv_pages, page_size, block_table, cu_lens,
+                                                  k_out, v_out, seq_starts)
+
+
+def prepare_kv4_attention(q, kv_pages, page_size, kv_heads, slots, indptr, scale, out=None,
+                          lse=None, workspace=True):
+    """Attention over ragged slots of the 4-bit cache.  q bf16 [R, H, 128] (row and head strides
+    free); slots int32, indptr int32 [R + 1]; out bf16 [R, H, 128], lse fp32 [R, H] and workspace
+    as in prepare_grouped_prefill (the size is kv4_attention_workspace_size(R, H, kv_heads,
+    slots.numel()))."""
+    return Prepared("idx_kv4_attention",
+                    *_latent_calls().kv4_attention(True, q, kv_pages, page_size, kv_heads, slots,
+                                                   indptr, scale, out, lse, workspace))
+
+
+def idx_kv4_attention(q, kv_pages, page_size, kv_heads, slots, indptr, scale, out=None, lse=None,
+                      workspace=True, stream=None):
+    """(out, lse) of the attention over ragged slots of the 4-bit cache."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_kv4_attention(q, kv_pages, page_size, kv_heads, slots, indptr, scale, out,
+                                     lse, workspace)
+    return (_calls or _latent_calls()).kv4_attention(False, q, kv_pages, page_size, kv_heads,
+                                                     slots, indptr, scale, out, lse, workspace)
+
+
+def prepare_paged_kv4_attention(q, kv_pages, page_size, kv_heads, block_table, context_lens,
+                                next_n, scale, max_model_len, ctx_per_row=False, out=None,
+                                lse=None, workspace=True):
+    """Attention over whole contexts of the 4-bit cache: row j of sequence b attends to its
+    first context_lens[b] - next_n + j + 1 tokens (or context_lens[row] with ctx_per_row).  q bf16
+    [B * next_n, H, 128]."""
+    return Prepared("idx_paged_kv4_attention",
+                    *_latent_calls().paged_kv4_attention(True, q, kv_pages, page_size, kv_heads,
+                                                         block_table, context_lens, next_n, scale,
+                                                         max_model_len, ctx_per_row, out, lse,
+                                                         workspace))
+
+
+def idx_paged_kv4_attention(q, kv_pages, page_size, kv_heads, block_table, context_lens, next_n,
+                            scale, max_model_len, ctx_per_row=False, out=None, lse=None,
+                            workspace=True, stream=None):
+    """(out, lse) of the attention over whole contexts of the 4-bit cache."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_paged_kv4_attention(q, kv_pages, page_size, kv_heads, block_table,
+                                           context_lens, next_n, scale, max_model_len, ctx_per_row,
+                                           out, lse, workspace)
+    return (_calls or _latent_calls()).paged_kv4_attention(False, q, kv_pages, page_size, kv_heads,
+                                                           block_table, context_lens, next_n,
+                                                           scale, max_model_len, ctx_per_row, out,
+                                                           lse, workspace)
+
+
+def prepare_paged_kv4_weights(q, kv_pages, page_size, kv_heads, block_table, context_lens, next_n,
+                              scale, max_model_len, lse, mass=None, out=None, ctx_per_row=False):
+    """The weights that idx_paged_kv4_attention gave the cached tokens, summed over a sequence's
+    rows and a key head's query heads and added to mass (fp32 [B, kv_heads, columns >=
+    max_model_len]; None: zeros).  lse: that call's.  out None: mass itself, or a new tensor of
+    max_model_len columns."""
+    return Prepared("idx_paged_kv4_weights",
+                    *_latent_calls().paged_kv4_weights(True, q, kv_pages, page_size, kv_heads,
+                                                       block_table, context_lens, next_n, scale,
+                                                       max_model_len, lse, mass, out, ctx_per_row))
+
+
+def idx_paged_kv4_weights(q, kv_pages, page_size, kv_heads, block_table, context_lens, next_n,
+                          scale, max_model_len, lse, mass=None, out=None, ctx_per_row=False,
+                          stream=None):
+    """mass (or out) with the weights of the cached tokens added."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_paged_kv4_weights(q, kv_pages, page_size, kv_heads, block_table,
+                                         context_lens, next_n, scale, max_model_len, lse, mass,
+                                         out, ctx_per_row)
+    return (_calls or _latent_calls()).paged_kv4_weights(False, q, kv_pages, page_size, kv_heads,
+                                                         block_table, context_lens, next_n, scale,
+                                                         max_model_len, lse, mass, out,
+                                                         ctx_per_row)
+
+
+def prepare_kv4_evict(mass, context_lens, budget, recent, kv_pages, page_size, block_table,
+                      new_table, whole_tokens=False, keep=None, new_lens=None, new_mass=None,
+                      workspace=True):
+    """Sequences shrunk to the last `recent` tokens and the budget - recent heaviest of the
+    others (mass fp32 [B, kv_heads, columns]), each key head its own, or whole_tokens by the sum
+    over the heads; they move to the pages of new_table, which are read by no other part of the
+    call.  keep int32 [B, kv_heads or 1, budget] (positions, ascending, then -1), new_lens int32
+    [B] and new_mass fp32 [B, kv_heads, budget] are made here when None."""
+    return Prepared("idx_kv4_evict",
+                    *_latent_calls().kv4_evict(True, mass, context_lens, budget, recent, kv_pages,
+                                               page_size, block_table, new_table, whole_tokens,
+                                               keep, new_lens, new_mass, workspace))
+
+
+def idx_kv4_evict(mass, context_lens, budget, recent, kv_pages, page_size, block_table, new_table,
+                  whole_tokens=False, keep=None, new_lens=None, new_mass=None, workspace=True,
+                  stream=None):
+    """(keep, new_lens, new_mass) of sequences shrunk to their heaviest tokens."""
+    if stream is not None:  # what the call makes is made on its stream
+        with torch.cuda.stream(stream):
+            return idx_kv4_evict(mass, context_lens, budget, recent, kv_pages, page_size,
+                                 block_table, new_table, whole_tokens, keep, new_lens, new_mass,
+                                 workspace)
+    return (_calls or _latent_calls()).kv4_evict(False, mass, context_lens, budget, recent,
+                                                 kv_pages, page_size, block_table, new_table,
+                                                 whole_tokens, keep, new_lens, new_mass, workspace)
 
 
 def idx_debug_wait_expiry(which: int, limit_ns: int, stream=None):

@@ -1,5 +1,5 @@
-// bind_latent.cpp -- the latent calls from Python: checks of the tensors, their
-// outputs and scratch, and the call, as one extension function each.
+// bind_latent.cpp -- the latent and the grouped-head calls from Python: checks of the
+// tensors, their outputs and scratch, and the call, as one extension function each.
 //
 // A decode step's call is a few microseconds of GPU time; attribute look-ups,
 // three allocations and 24 converted arguments in Python took 16 to 22 us of
@@ -13,10 +13,12 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <climits>
 #include <initializer_list>
 #include <optional>
 #include <string>
+#include <type_traits>
 
 #include "idx.h"
 
@@ -32,6 +34,17 @@ decltype(&idx_latent_prefill) f_prefill;
 decltype(&idx_latent_attention_workspace_size) f_attention_size;
 decltype(&idx_latent_prefill_workspace_size) f_prefill_size;
 decltype(&idx_latent_attention_launches) f_attention_launches;
+decltype(&idx_grouped_prefill) f_grouped;
+decltype(&idx_grouped_prefill_workspace_size) f_grouped_size;
+decltype(&idx_kv4_store) f_kv4_store;
+decltype(&idx_kv4_gather) f_kv4_gather;
+decltype(&idx_kv4_attention) f_kv4;
+decltype(&idx_paged_kv4_attention) f_paged_kv4;
+decltype(&idx_kv4_attention_workspace_size) f_kv4_size;
+decltype(&idx_paged_kv4_weights) f_kv4_weights;
+decltype(&idx_kv4_evict) f_kv4_evict;
+decltype(&idx_kv4_evict_workspace_size) f_kv4_evict_size;
+decltype(&idx_kv4_evict_launches) f_kv4_evict_launches;
 PyObject *g_check;  // check(status, name) raises
 
 struct Refusal {
@@ -450,6 +463,295 @@ PyObject *prefill(PyObject *, PyObject *const *a, Py_ssize_t)
         o.ws_bytes);
 }
 
+// ------------------------------------------------------- grouped heads, 4-bit cache
+
+constexpr int64_t kHead = 128;
+
+// Key heads that a call names, which its query heads are a multiple of.
+int key_heads(PyObject *o, int64_t H)
+{
+    const int g = int_of(o, "kv_heads");
+    if (g <= 0 || H % g)
+        refuse("q's heads must be a multiple of kv_heads");
+    return g;
+}
+
+// fp32 [B, heads, columns] with contiguous columns.
+const at::Tensor &need_mass(PyObject *o, int64_t B, int64_t heads, int64_t least, const char *name)
+{
+    const at::Tensor &t = tensor_of(o, name);
+    if (t.scalar_type() != at::kFloat || t.dim() != 3 || (B >= 0 && t.size(0) != B) ||
+        (heads >= 0 && t.size(1) != heads) || t.size(2) < least || ld(t, 2, 1) != 1)
+        refuse(std::string(name) + " must be float32 [B, kv_heads, columns] with unit column "
+               "stride, a column for each token");
+    return t;
+}
+
+const at::Tensor &need_table(PyObject *o, int64_t B, const char *name)
+{
+    const at::Tensor &t = need(o, at::kInt, name);
+    if (t.dim() != 2 || t.size(0) < B)
+        refuse(std::string(name) + " must be [" + std::to_string(B) + ", blocks]");
+    return t;
+}
+
+PyObject *grouped_prefill(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const at::Tensor &q = need_heads(a[1], 3, kHead, "q");
+    const at::Tensor &k = need_heads(a[2], 3, kHead, "k");
+    const at::Tensor &v = need_heads(a[3], 3, kHead, "v");
+    const at::Tensor &cu_q = need(a[4], at::kInt, "cu_q"), &cu_k = need(a[5], at::kInt, "cu_k");
+    const int Tq = count(q.size(0), "q"), H = count(q.size(1), "q"), Tk = count(k.size(0), "k");
+    const int G = count(k.size(1), "k"), causal = truth_of(a[7]);
+    if (v.size(0) != Tk || v.size(1) != G)
+        refuse("k and v must hold the same tokens and heads");
+    if (G == 0 || H % G)
+        refuse("q's heads must be a multiple of k's");
+    const int64_t B = cu_q.numel() - 1;
+    if (cu_k.numel() != B + 1 || B < 0)
+        refuse("cu_q and cu_k must both hold B + 1 entries");
+    Outputs o(a[8], a[9], a[10], q, kHead);
+    on_one_device({&q, &k, &v, &cu_q, &cu_k, &o.out, &o.lse, &o.ws});
+    const size_t size = f_grouped_size(Tq, Tk, H);
+    o.make(a[9], a[10], q, kHead, size);
+    return call(
+        a[0] == Py_True, f_grouped, "idx_grouped_prefill", Tq == 0 || B == 0 ? 0 : size ? 2 : 1,
+        [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
+        [&] {
+            return Py_BuildValue("(OOOOONNN)", a[1], a[2], a[3], a[4], a[5], wrap(o.out),
+                                 wrap(o.lse), wrap(o.ws));
+        },
+        (const uint16_t *)address<uint16_t>(q), ld(q, 0, H * kHead), ld(q, 1, kHead),
+        (const uint16_t *)address<uint16_t>(k), ld(k, 0, G * kHead), ld(k, 1, kHead),
+        (const uint16_t *)address<uint16_t>(v), ld(v, 0, G * kHead), ld(v, 1, kHead),
+        (const int32_t *)address<int32_t>(cu_q), (const int32_t *)address<int32_t>(cu_k),
+        count(B, "cu_q"), Tq, Tk, H, G, (int)kHead, float_of(a[6]), causal, o.out_at(), o.ld_row,
+        o.ld_head, o.lse_at(), o.ld_lse, o.ws_at(), o.ws_bytes);
+}
+
+PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const at::Tensor &k = need_heads(a[1], 3, kHead, "k"), &v = need_heads(a[2], 3, kHead, "v");
+    const int64_t T = k.size(0), G = k.size(1);
+    if (v.size(0) != T || v.size(1) != G)
+        refuse("k and v must hold the same tokens and heads");
+    const at::Tensor &pages = need_pages(a[3]), &slots = need(a[5], at::kLong, "slot_mapping");
+    need_count(slots, T, "slot_mapping");
+    on_one_device({&k, &v, &pages, &slots});
+    return call(
+        a[0] == Py_True, f_kv4_store, "idx_kv4_store", T > 0, [] { Py_RETURN_NONE; },
+        [&] { return Py_BuildValue("(OOOO)", a[1], a[2], a[3], a[5]); },
+        (const uint16_t *)address<uint16_t>(k), ld(k, 0, G * kHead), ld(k, 1, kHead),
+        (const uint16_t *)address<uint16_t>(v), ld(v, 0, G * kHead), ld(v, 1, kHead),
+        count(T, "k"), count(G, "k"), (int)kHead, address<uint8_t>(pages), page_stride(pages),
+        count(pages.size(0), "kv_pages"), int_of(a[4], "page_size"),
+        (const int64_t *)address<int64_t>(slots));
+}
+
+PyObject *kv4_gather(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const at::Tensor &pages = need_pages(a[1]);
+    const at::Tensor &cu = need(a[4], at::kInt, "cu_lens");
+    const int64_t B = cu.numel() - 1;
+    if (B < 0)
+        refuse("cu_lens must hold B + 1 entries");
+    const at::Tensor &table = need_table(a[3], B, "block_table");
+    const at::Tensor &k = need_heads(a[5], 3, kHead, "k_out"), &v = need_heads(a[6], 3, kHead, "v_out");
+    const int64_t N = k.size(0), G = k.size(1);
+    if (v.size(0) != N || v.size(1) != G)
+        refuse("k_out and v_out must hold the same tokens and heads");
+    at::Tensor s;
+    if (a[7] != Py_None) {
+        s = need(a[7], at::kInt, "seq_starts");
+        need_count(s, B, "seq_starts");
+    }
+    on_one_device({&pages, &table, &cu, &k, &v, &s});
+    const int32_t *starts = s.defined() ? address<int32_t>(s) : nullptr;
+    return call(
+        a[0] == Py_True, f_kv4_gather, "idx_kv4_gather", B > 0 && N > 0,
+        [&] { return Py_BuildValue("(OO)", a[5], a[6]); },
+        [&] { return Py_BuildValue("(OOOOOO)", a[1], a[3], a[4], a[5], a[6], a[7]); },
+        (const uint8_t *)address<uint8_t>(pages), page_stride(pages), count(pages.size(0), "kv_pages"),
+        int_of(a[2], "page_size"), count(G, "k_out"), (int)kHead,
+        (const int32_t *)address<int32_t>(table), table.size(1),
+        count(table.size(1), "block_table"), (const int32_t *)address<int32_t>(cu), starts,
+        count(B, "cu_lens"), count(N, "k_out"), address<uint16_t>(k), ld(k, 0, G * kHead),
+        ld(k, 1, kHead), address<uint16_t>(v), ld(v, 0, G * kHead), ld(v, 1, kHead));
+}
+
+PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const at::Tensor &q = need_heads(a[1], 3, kHead, "q");
+    const at::Tensor &pages = need_pages(a[2]);
+    const at::Tensor &slots = need(a[5], at::kInt, "slots"), &indptr = need(a[6], at::kInt, "indptr");
+    const int R = count(q.size(0), "q"), H = count(q.size(1), "q"), G = key_heads(a[4], H);
+    need_count(indptr, (int64_t)R + 1, "indptr");
+    Outputs o(a[8], a[9], a[10], q, kHead);
+    on_one_device({&q, &pages, &slots, &indptr, &o.out, &o.lse, &o.ws});
+    const size_t size = f_kv4_size(R, 1, H, G, slots.numel());
+    o.make(a[9], a[10], q, kHead, size);
+    return call(
+        a[0] == Py_True, f_kv4, "idx_kv4_attention", R == 0 ? 0 : size ? 2 : 1,
+        [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
+        [&] {
+            return Py_BuildValue("(OOOONNN)", a[1], a[2], a[5], a[6], wrap(o.out), wrap(o.lse),
+                                 wrap(o.ws));
+        },
+        (const uint16_t *)address<uint16_t>(q), ld(q, 0, H * kHead), ld(q, 1, kHead),
+        (const uint8_t *)address<uint8_t>(pages), page_stride(pages),
+        count(pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
+        (const int32_t *)address<int32_t>(slots), (const int32_t *)address<int32_t>(indptr),
+        slots.numel(), R, H, G, (int)kHead, float_of(a[7]), o.out_at(), o.ld_row, o.ld_head,
+        o.lse_at(), o.ld_lse, o.ws_at(), o.ws_bytes);
+}
+
+// What the paged calls share.
+struct Paged {
+    const at::Tensor &q, &pages, &table, &lens;
+    int R, H, G, next, B, per_row, longest;
+
+    Paged(PyObject *const *a, PyObject *per)
+        : q(need_heads(a[1], 3, kHead, "q")), pages(need_pages(a[2])),
+          table(need(a[5], at::kInt, "block_table")), lens(need(a[6], at::kInt, "context_lens"))
+    {
+        R = count(q.size(0), "q");
+        H = count(q.size(1), "q");
+        G = key_heads(a[4], H);
+        next = int_of(a[7], "next_n");
+        if (next <= 0 || R % next)
+            refuse("q must hold B * next_n rows");
+        B = R / next;
+        per_row = truth_of(per);
+        need_count(lens, per_row ? R : B, "context_lens");
+        need_table(a[5], B, "block_table");
+        longest = int_of(a[9], "max_model_len");
+    }
+};
+
+PyObject *paged_kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const Paged p(a, a[10]);
+    Outputs o(a[11], a[12], a[13], p.q, kHead);
+    on_one_device({&p.q, &p.pages, &p.table, &p.lens, &o.out, &o.lse, &o.ws});
+    const size_t size = f_kv4_size(p.R, p.next, p.H, p.G, p.longest);
+    o.make(a[12], a[13], p.q, kHead, size);
+    return call(
+        a[0] == Py_True, f_paged_kv4, "idx_paged_kv4_attention", p.R == 0 ? 0 : size ? 2 : 1,
+        [&] { return Py_BuildValue("(NN)", wrap(o.out), wrap(o.lse)); },
+        [&] {
+            return Py_BuildValue("(OOOONNN)", a[1], a[2], a[5], a[6], wrap(o.out), wrap(o.lse),
+                                 wrap(o.ws));
+        },
+        (const uint16_t *)address<uint16_t>(p.q), ld(p.q, 0, p.H * kHead), ld(p.q, 1, kHead),
+        (const uint8_t *)address<uint8_t>(p.pages), page_stride(p.pages),
+        count(p.pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
+        (const int32_t *)address<int32_t>(p.table), p.table.size(1),
+        (const int32_t *)address<int32_t>(p.lens), p.per_row, p.B, p.next, p.longest, p.H, p.G,
+        (int)kHead, float_of(a[8]), o.out_at(), o.ld_row, o.ld_head, o.lse_at(), o.ld_lse,
+        o.ws_at(), o.ws_bytes);
+}
+
+PyObject *paged_kv4_weights(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const Paged p(a, a[13]);
+    const at::Tensor &lse = tensor_of(a[10], "lse");
+    if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != p.R ||
+        lse.size(1) != p.H || ld(lse, 1, 1) != 1)
+        refuse("lse must be float32 [" + std::to_string(p.R) + ", " + std::to_string(p.H) +
+               "] with unit column stride");
+    at::Tensor mass, out;
+    if (a[11] != Py_None)
+        mass = need_mass(a[11], p.B, p.G, p.longest, "mass");
+    if (a[12] != Py_None)
+        out = need_mass(a[12], p.B, p.G, p.longest, "out");
+    if (mass.defined() && out.defined() && mass.size(2) != out.size(2))
+        refuse("mass and out must have the same columns");
+    on_one_device({&p.q, &p.pages, &p.table, &p.lens, &lse, &mass, &out});
+    if (!out.defined())
+        out = mass.defined() ? mass : empty({p.B, p.G, p.longest}, at::kFloat, p.q.device());
+    const int64_t width = out.size(2);
+    return call(
+        a[0] == Py_True, f_kv4_weights, "idx_paged_kv4_weights", p.B > 0 && width > 0,
+        [&] { return wrap(out); },
+        [&] {
+            return Py_BuildValue("(OOOOONN)", a[1], a[2], a[5], a[6], a[10], wrap(mass), wrap(out));
+        },
+        (const uint16_t *)address<uint16_t>(p.q), ld(p.q, 0, p.H * kHead), ld(p.q, 1, kHead),
+        (const uint8_t *)address<uint8_t>(p.pages), page_stride(p.pages),
+        count(p.pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
+        (const int32_t *)address<int32_t>(p.table), p.table.size(1),
+        (const int32_t *)address<int32_t>(p.lens), p.per_row, p.B, p.next, p.longest, p.H, p.G,
+        (int)kHead, float_of(a[8]), (const float *)address<float>(lse), ld(lse, 0, p.H),
+        mass.defined() ? (const float *)address<float>(mass) : nullptr,
+        mass.defined() ? ld(mass, 0, p.G * width) : (int64_t)0,
+        mass.defined() ? ld(mass, 1, width) : (int64_t)0, count(width, "out"),
+        address<float>(out), ld(out, 0, p.G * width), ld(out, 1, width));
+}
+
+PyObject *kv4_evict(PyObject *, PyObject *const *a, Py_ssize_t)
+{
+    const at::Tensor &mass = need_mass(a[1], -1, -1, 0, "mass");
+    const at::Tensor &lens = need(a[2], at::kInt, "context_lens"), &pages = need_pages(a[5]);
+    const int B = count(mass.size(0), "mass"), G = count(mass.size(1), "mass");
+    const int columns = count(mass.size(2), "mass");
+    need_count(lens, B, "context_lens");
+    if (G == 0)
+        refuse("mass must have key heads");
+    const int budget = int_of(a[3], "budget"), recent = int_of(a[4], "recent");
+    if (recent < 0 || budget < recent)
+        refuse("budget and recent must be 0 <= recent <= budget");
+    const at::Tensor &table = need_table(a[7], B, "block_table");
+    const at::Tensor &fresh = need_table(a[8], B, "new_table");
+    const int whole = truth_of(a[9]), lists = whole ? 1 : G, page_size = int_of(a[6], "page_size");
+    if (page_size > 0 && fresh.size(1) * page_size < std::min(budget, columns))
+        refuse("new_table has no room for the tokens that stay");
+    at::Tensor keep_t, new_lens, new_mass, ws;
+    const auto exact = [&](PyObject *o, at::ScalarType type, at::IntArrayRef shape, const char *name) {
+        const at::Tensor &t = need(o, type, name);
+        if (t.sizes() != shape)
+            refuse(std::string(name) + " has another shape");
+        return t;
+    };
+    if (a[10] != Py_None)
+        keep_t = exact(a[10], at::kInt, {B, lists, budget}, "keep");
+    if (a[11] != Py_None)
+        new_lens = exact(a[11], at::kInt, {B}, "new_lens");
+    if (a[12] != Py_None)
+        new_mass = exact(a[12], at::kFloat, {B, G, budget}, "new_mass");
+    if (a[13] != Py_True && a[13] != Py_None) {
+        ws = tensor_of(a[13], "workspace");
+        if (!ws.is_contiguous())
+            refuse("workspace must be contiguous");
+    }
+    on_one_device({&mass, &lens, &pages, &table, &fresh, &keep_t, &new_lens, &new_mass, &ws});
+    const auto device = mass.device();
+    if (!keep_t.defined())
+        keep_t = empty({B, lists, budget}, at::kInt, device);
+    if (!new_lens.defined())
+        new_lens = empty({B}, at::kInt, device);
+    if (!new_mass.defined())
+        new_mass = empty({B, G, budget}, at::kFloat, device);
+    const size_t size = f_kv4_evict_size(B, G, columns, budget, recent, whole);
+    if (a[13] == Py_True && size > 0)
+        ws = empty({(int64_t)size}, at::kByte, device);
+    const size_t ws_bytes = ws.defined() ? ws.numel() * ws.element_size() : 0;
+    return call(
+        a[0] == Py_True, f_kv4_evict, "idx_kv4_evict",
+        f_kv4_evict_launches(B, G, columns, budget, recent, whole),
+        [&] { return Py_BuildValue("(NNN)", wrap(keep_t), wrap(new_lens), wrap(new_mass)); },
+        [&] {
+            return Py_BuildValue("(OOOOONNNN)", a[1], a[2], a[5], a[7], a[8], wrap(keep_t),
+                                 wrap(new_lens), wrap(new_mass), wrap(ws));
+        },
+        (const float *)address<float>(mass), ld(mass, 0, (int64_t)G * columns), ld(mass, 1, columns),
+        columns, (const int32_t *)address<int32_t>(lens), B, G, (int)kHead, budget, recent, whole,
+        address<uint8_t>(pages), page_stride(pages), count(pages.size(0), "kv_pages"), page_size,
+        (const int32_t *)address<int32_t>(table), table.size(1), count(table.size(1), "block_table"),
+        (const int32_t *)address<int32_t>(fresh), fresh.size(1), count(fresh.size(1), "new_table"),
+        address<int32_t>(keep_t), address<int32_t>(new_lens), address<float>(new_mass),
+        ws.defined() ? address<void>(ws) : (void *)nullptr, ws_bytes);
+}
+
 // Errors as Python's: refusals are ValueErrors.
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t), int N>
 PyObject *entry(PyObject *self, PyObject *const *a, Py_ssize_t n)
@@ -468,22 +770,43 @@ PyObject *entry(PyObject *self, PyObject *const *a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// bind(check, addresses of the library's functions)
+// bind(check, addresses of the library's functions by name)
 PyObject *bind(PyObject *, PyObject *args)
 {
-    unsigned long long p[8];
-    PyObject *check;
-    if (!PyArg_ParseTuple(args, "OKKKKKKKK", &check, p, p + 1, p + 2, p + 3, p + 4, p + 5, p + 6,
-                          p + 7))
+    PyObject *check, *names;
+    if (!PyArg_ParseTuple(args, "OO!", &check, &PyDict_Type, &names))
         return nullptr;
-    f_store = reinterpret_cast<decltype(f_store)>(p[0]);
-    f_gather = reinterpret_cast<decltype(f_gather)>(p[1]);
-    f_attention = reinterpret_cast<decltype(f_attention)>(p[2]);
-    f_paged = reinterpret_cast<decltype(f_paged)>(p[3]);
-    f_prefill = reinterpret_cast<decltype(f_prefill)>(p[4]);
-    f_attention_size = reinterpret_cast<decltype(f_attention_size)>(p[5]);
-    f_prefill_size = reinterpret_cast<decltype(f_prefill_size)>(p[6]);
-    f_attention_launches = reinterpret_cast<decltype(f_attention_launches)>(p[7]);
+    bool ok = true;
+    const auto at = [&](const char *name, auto &f) {
+        PyObject *o = ok ? PyDict_GetItemString(names, name) : nullptr;
+        void *p = o ? PyLong_AsVoidPtr(o) : nullptr;
+        ok = ok && p;
+        f = reinterpret_cast<std::decay_t<decltype(f)>>(p);
+    };
+    at("idx_latent_store", f_store);
+    at("idx_latent_gather", f_gather);
+    at("idx_latent_attention", f_attention);
+    at("idx_paged_latent_attention", f_paged);
+    at("idx_latent_prefill", f_prefill);
+    at("idx_latent_attention_workspace_size", f_attention_size);
+    at("idx_latent_prefill_workspace_size", f_prefill_size);
+    at("idx_latent_attention_launches", f_attention_launches);
+    at("idx_grouped_prefill", f_grouped);
+    at("idx_grouped_prefill_workspace_size", f_grouped_size);
+    at("idx_kv4_store", f_kv4_store);
+    at("idx_kv4_gather", f_kv4_gather);
+    at("idx_kv4_attention", f_kv4);
+    at("idx_paged_kv4_attention", f_paged_kv4);
+    at("idx_kv4_attention_workspace_size", f_kv4_size);
+    at("idx_paged_kv4_weights", f_kv4_weights);
+    at("idx_kv4_evict", f_kv4_evict);
+    at("idx_kv4_evict_workspace_size", f_kv4_evict_size);
+    at("idx_kv4_evict_launches", f_kv4_evict_launches);
+    if (!ok) {
+        if (!PyErr_Occurred())
+            PyErr_SetString(PyExc_KeyError, "an address of the library is missing");
+        return nullptr;
+    }
     Py_INCREF(check);
     Py_XSETREF(g_check, check);
     Py_RETURN_NONE;
@@ -498,6 +821,13 @@ PyMethodDef methods[] = {
     IDX_ENTRY(attention, 11),
     IDX_ENTRY(paged_attention, 14),
     IDX_ENTRY(prefill, 12),
+    IDX_ENTRY(grouped_prefill, 11),
+    IDX_ENTRY(kv4_store, 6),
+    IDX_ENTRY(kv4_gather, 8),
+    IDX_ENTRY(kv4_attention, 11),
+    IDX_ENTRY(paged_kv4_attention, 14),
+    IDX_ENTRY(paged_kv4_weights, 14),
+    IDX_ENTRY(kv4_evict, 14),
     {nullptr, nullptr, 0, nullptr},
 };
 

@@ -1,0 +1,1347 @@
+// idx_kv4_attn.cu -- attention of grouped heads over the 4-bit cache, by ragged
+// slots or whole paged contexts, and the weights it gives the cached tokens.
+//
+// For one key head, the columns are the query heads that share it (of all rows
+// of a sequence), in blocks of 8, 16 or 32; tokens are the other side:
+//
+//     S^T [32 tokens x cols] = K [32 x 128] . Q^T,   O^T [128 x cols] += V^T . P^T
+//
+// What bounds it is reading the cache, 136 bytes a token and head, and widening
+// it: 7 TB/s are 47 elements a clock and SM.  So the codes are widened in
+// registers, straight into the operand fragments of warp-level products, and
+// never pass through shared memory a second time (a widened tile would take 94
+// of its 128 bytes a clock to write, and as many to read): tokens are the
+// products' 16 rows, so that 8 columns fill an instruction.
+//
+//  * The hardware's conversion gives a pair of e2m1 as f16, exactly.  Queries
+//    become f16 under a power of two of their own, which bf16's 8 bits survive.
+//  * A key's scale stands for 32 elements, two product steps: their sum is
+//    scaled in 32 bits.
+//  * A value's scale goes to the weight: P_g = P 2^(e_g - E_g), E_g the largest
+//    exponent met, as f16 pairs (O follows E_g like the running maximum).  Tokens
+//    over 2^19 under E_g, and NaN scales, take a second form of the product with
+//    bf16 weights, which have an exponent to spare.
+//  * Values lie with pairs of elements in a byte, and the product wants pairs of
+//    tokens: the nibbles of two tokens change places before they are widened,
+//    four instructions for sixteen elements.
+//
+// Every warp walks 32 tokens of each tile of 128 with a running maximum and sum
+// of its own and a ring of its own, filled by asynchronous copies (16 bytes, the
+// pieces of a row turned by its number so that fragments are read without bank
+// conflicts); warps meet where a segment of a row ends.  Work is the flat list
+// of (row or sequence, key head, tile); CTAs take equal contiguous shares of it
+// and a second kernel joins what they cut.
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <float.h>
+
+#include "idx_kv4.cuh"
+
+namespace idx {
+namespace {
+
+constexpr int kThreads = 128, kWarps = 4;
+constexpr int kSub = 32;                // tokens of a warp's step
+constexpr int kTile = kWarps * kSub;    // of a CTA's
+constexpr int kSubCodes = kSub * kKv4Codes;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 4.0f;           // a score may exceed its running maximum by 2^4
+constexpr int kBias = 6;                // weights are held 2^6 larger: up to 2^10 in f16
+constexpr int kScaleUp = 5;             // and scaled values' up to 2^5 more
+constexpr int kScaleRange = 19;         // f16 holds 2^5 to 2^-14 without loss
+// Rows of few keys are not cut: no scratch and no joining kernel.
+constexpr int kUncutKeys = 4 * kTile;
+constexpr int kJoinThreads = 256;
+
+struct Kv4Args {
+    const uint16_t *q;
+    int64_t ldq_row, ldq_head;
+    Kv4Pool pool;
+    int group;        // query heads of a key head
+    int cols;         // columns of a unit: rows of a sequence x group
+    int blocks;       // blocks of columns
+    // ragged slots
+    const int32_t *slots, *indptr;
+    int64_t num_slots;
+    // whole contexts
+    const int32_t *table;
+    int64_t bt_stride;
+    const int32_t *ctx;
+    int ctx_per_row, next_n, max_len;
+    int B;            // rows or sequences
+    float scale_log2;
+    uint16_t *out;
+    int64_t ldo_row, ldo_head;
+    float *lse;
+    int64_t ld_lse;
+    int uncut;        // units are not cut
+    int4 *ws_cut;     // a share: the unit it begins and leaves to the next (sequence, key head and
+                      // block of columns, pieces; no pieces: none), whether a segment lies before
+    float *ws_part;   // two segments a share: O, maxima, sums
+    unsigned int *status;
+    // weights of tokens
+    const float *lse_in;
+    int64_t ld_lse_in;
+    const float *mass;
+    int64_t ld_batch, ld_head;
+    int width;
+    float *mass_out;
+    int64_t ldo_batch, ldo_mass_head;
+};
+
+// ------------------------------------------------------------------- pieces
+
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma16_bf(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// An 8 x 8 block of 16-bit elements in fragment registers, transposed.
+__device__ __forceinline__ uint32_t turn8(uint32_t v)
+{
+    uint32_t t;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+    return t;
+}
+
+__device__ __forceinline__ uint32_t as_u32(__half2 v)
+{
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t as_u32(__nv_bfloat162 v)
+{
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ __half2 as_h2(uint32_t v)
+{
+    return *reinterpret_cast<const __half2 *>(&v);
+}
+
+__device__ __forceinline__ __nv_bfloat162 as_b2(uint32_t v)
+{
+    return *reinterpret_cast<const __nv_bfloat162 *>(&v);
+}
+
+// f16 pairs that bf16 holds (e2m1 values).
+__device__ __forceinline__ uint32_t to_bf16x2(uint32_t h)
+{
+    const float2 f = __half22float2(as_h2(h));
+    return as_u32(__floats2bfloat162_rn(f.x, f.y));
+}
+
+__device__ __forceinline__ void cp_async4(uint32_t saddr, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(saddr),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+
+// 2^x of a float's exponent field and beyond it (underflow gives 0).
+__device__ __forceinline__ float pow2i(int x)
+{
+    return ex2((float)x);
+}
+
+// ------------------------------------------------------------------ the list
+
+// A unit's tokens: the longest of its rows.
+template <bool kPaged>
+__device__ __forceinline__ int unit_len(const Kv4Args &a, int b)
+{
+    if constexpr (kPaged) {
+        int n = a.ctx_per_row ? 0 : a.ctx[b];
+        if (a.ctx_per_row)
+            for (int j = 0; j < a.next_n; ++j)
+                n = max(n, a.ctx[(int64_t)b * a.next_n + j]);
+        return min(max(n, 0), a.max_len);
+    } else {
+        const int64_t lo = min((int64_t)max(a.indptr[b], 0), a.num_slots);
+        const int64_t hi = min((int64_t)max(a.indptr[b + 1], 0), a.num_slots);
+        return (int)max((int64_t)0, hi - lo);
+    }
+}
+
+// Tokens that row j of the unit sees.
+template <bool kPaged>
+__device__ __forceinline__ int row_end(const Kv4Args &a, int b, int j, int len)
+{
+    if constexpr (!kPaged)
+        return len;
+    const int n = a.ctx_per_row ? a.ctx[(int64_t)b * a.next_n + j]
+                                : (int)max((int64_t)a.ctx[b] - a.next_n + j + 1, (int64_t)0);
+    return min(max(n, 0), a.max_len);
+}
+
+// Every sequence counts a tile at least: its outputs are written.
+template <bool kPaged>
+__device__ __forceinline__ int64_t unit_tiles(const Kv4Args &a, int b)
+{
+    return a.uncut ? 1 : max(1, (int)(((int64_t)unit_len<kPaged>(a, b) + kTile - 1) / kTile));
+}
+
+// A share of the list: segments of units' tiles.  Sequences lie behind one
+// another, each with its key heads and blocks of columns.
+struct Share {
+    int b, hc;       // sequence; key head x blocks of columns
+    int tiles, len;  // of the sequence
+    int t;           // next tile
+    int left;        // tiles left
+    int each, more;  // of all shares: size, how many have one more
+};
+
+// Sums over the block, for every thread: upto and including its own, and of all.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *wsum, int64_t &all)
+{
+    const int lane = lane_id(), warp = threadIdx.x >> 5;
+    #pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, v, o);
+        v += lane >= o ? up : 0;
+    }
+    __syncthreads();
+    if (lane == 31)
+        wsum[warp] = v;
+    __syncthreads();
+    all = 0;
+    #pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        v += i < warp ? wsum[i] : 0;
+        all += wsum[i];
+    }
+    return v;
+}
+
+// This CTA's share; false where it has none.  limit: tiles that a list may have.
+template <bool kPaged>
+__device__ __forceinline__ bool find_share(const Kv4Args &a, int heads, int64_t limit, Share &s)
+{
+    __shared__ int64_t wsum[kWarps];
+    __shared__ int found[2];
+    const int tid = threadIdx.x;
+    int64_t total = 0, mine = 0, upto = 0;
+    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        int64_t all;
+        mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
+        upto = total + block_scan(mine, wsum, all);
+        total += all;
+    }
+    if (total > limit) {
+        if (blockIdx.x == 0 && tid == 0)
+            atomicOr(a.status, kDevBadBounds);
+        return false;
+    }
+    total *= heads;
+    const int p = blockIdx.x, shares = (int)min((int64_t)gridDim.x, total);
+    if (p >= shares)
+        return false;
+    s.each = (int)(total / shares);
+    s.more = (int)(total - (int64_t)s.each * shares);
+    s.left = s.each + (p < s.more);
+    const int64_t u0 = (int64_t)p * s.each + min(p, s.more);
+    const auto look = [&](int b) {
+        const int64_t before = (upto - mine) * heads;
+        if (u0 >= before && u0 < before + mine * heads) {
+            found[0] = b;
+            found[1] = (int)(u0 - before);
+        }
+    };
+    if (a.B <= kThreads) {
+        look(tid);
+    } else {
+        int64_t sum = 0, all;
+        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+            mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
+            upto = sum + block_scan(mine, wsum, all);
+            sum += all;
+            look(b0 + tid);
+        }
+    }
+    __syncthreads();
+    s.b = found[0];
+    s.len = unit_len<kPaged>(a, s.b);
+    s.tiles = (int)unit_tiles<kPaged>(a, s.b);
+    s.hc = found[1] / s.tiles;
+    s.t = found[1] - s.hc * s.tiles;
+    return true;
+}
+
+// A segment: tiles [t0, t1) of a unit.
+struct Seg {
+    int b, hc, len, t0, t1, tiles;
+};
+
+template <bool kPaged>
+__device__ __forceinline__ bool next_seg(const Kv4Args &a, int heads, Share &s, Seg &g)
+{
+    if (s.left <= 0)
+        return false;
+    if (s.t == s.tiles) {
+        s.t = 0;
+        if (++s.hc == heads) {
+            s.hc = 0;
+            ++s.b;
+            s.len = unit_len<kPaged>(a, s.b);
+            s.tiles = (int)unit_tiles<kPaged>(a, s.b);
+        }
+    }
+    const int n = min(s.left, s.tiles - s.t);
+    g = {s.b, s.hc, s.len, s.t, s.t + n, s.tiles};
+    s.t += n;
+    s.left -= n;
+    if (a.uncut)
+        g.t1 = g.tiles = max(1, (s.len + kTile - 1) / kTile);
+    return true;
+}
+
+// ------------------------------------------------------------------- a ring
+//
+// A warp's tokens on their way in: codes of the keys (and values), scales, and
+// which tokens are there.
+template <bool kPaged, bool kValues, int kStages>
+struct Ring {
+    static constexpr int kCodes = (kValues ? 2 : 1) * kSubCodes;
+    static constexpr int kScales = (kValues ? 2 : 1) * 4 * kSub;
+    static constexpr int kStage = kCodes + kScales;
+    static constexpr int kBytes = kStages * kStage + (kValues ? 8 * kSub : 0) + 16 * ((kStages + 3) / 4);
+
+    uint8_t *mem;
+    int32_t ahead;       // the next step's slot, or its page
+    int64_t first;       // slots: of the row's first token; pages: of the table's row
+    int head, len, tok;  // tok: this lane's next token
+
+    __device__ __forceinline__ uint8_t *stage(int i) const { return mem + i * kStage; }
+    __device__ __forceinline__ uint2 *turned() const
+    {
+        return reinterpret_cast<uint2 *>(mem + kStages * kStage);
+    }
+    __device__ __forceinline__ uint32_t *masks() const
+    {
+        return reinterpret_cast<uint32_t *>(mem + kStages * kStage + (kValues ? 8 * kSub : 0));
+    }
+    __device__ __forceinline__ void look(const Kv4Args &a)
+    {
+        ahead = -1;
+        if (tok < len) {
+            if constexpr (kPaged)
+                ahead = a.table[first + page_of(a.pool.p, tok)];
+            else
+                ahead = a.slots[first + tok];
+        }
+    }
+    // Tokens from tok0 on, every kTile of them.
+    __device__ __forceinline__ void start(const Kv4Args &a, int b, int key_head, int length, int tok0)
+    {
+        head = key_head;
+        len = length;
+        tok = tok0 + lane_id();
+        if constexpr (kPaged)
+            first = b * a.bt_stride;
+        else
+            first = min((int64_t)max(a.indptr[b], 0), a.num_slots);
+        look(a);
+    }
+    __device__ __forceinline__ void fill(const Kv4Args &a, int st)
+    {
+        const int lane = lane_id();
+        int page = ahead, off = 0;
+        bool good = tok < len;
+        if constexpr (kPaged) {
+            off = tok - page_of(a.pool.p, tok) * a.pool.p.page_size;
+        } else if (page >= 0) {
+            const int slot = page;
+            page = page_of(a.pool.p, slot);
+            off = slot - page * a.pool.p.page_size;
+        }
+        if (good && (page < 0 || page >= a.pool.p.num_pages)) {
+            good = false;
+            atomicOr(a.status, kDevBadPage);
+        }
+        tok += kTile;
+        look(a);
+        const uint32_t there = __ballot_sync(0xffffffffu, good);
+        if (lane == 0)
+            masks()[st] = there;
+        const uint32_t to = smem_u32(stage(st));
+        const int64_t at = kv4_codes_at(a.pool, page, head, off);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2), c = lane & 3;
+            const int64_t from = __shfl_sync(0xffffffffu, at, row);
+            if (there >> row & 1) {
+                const uint32_t d = to + row * kKv4Codes + 16 * (c ^ (row >> 1 & 3));
+                cp_async16(d, a.pool.p.base + from + 16 * c);
+                if constexpr (kValues)
+                    cp_async16(d + kSubCodes, a.pool.p.base + from + a.pool.side + 16 * c);
+            }
+        }
+        if (good) {
+            const uint8_t *s = a.pool.p.base + kv4_scales_at(a.pool, page, head, off);
+            cp_async4(to + kCodes + 4 * lane, s);
+            if constexpr (kValues)
+                cp_async4(to + kCodes + 4 * (kSub + lane), s + a.pool.scale_side);
+        }
+    }
+};
+
+// ------------------------------------------------------------------- queries
+
+// Query fragments of a block of columns, as f16 under a power of two for each
+// column; slc brings scores to units of log2 (columns 2 c, 2 c + 1 of each
+// eight).
+template <int NT>
+__device__ __forceinline__ void load_queries(const Kv4Args &a, int b, int key_head, int cb,
+                                             uint32_t (&qf)[NT][4][4], float (&slc)[NT][2])
+{
+    const int lane = lane_id(), g = lane >> 2, c = lane & 3;
+    #pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int col = (cb * NT + n) * 8 + g, j = col / a.group;
+        uint4 raw[4] = {};
+        if (col < a.cols) {
+            const uint16_t *src = a.q + ((int64_t)b * a.next_n + j) * a.ldq_row +
+                                  (int64_t)(key_head * a.group + col - j * a.group) * a.ldq_head;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i)
+                raw[i] = *reinterpret_cast<const uint4 *>(src + 32 * i + 8 * c);
+        }
+        uint32_t top = 0;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                top = max(top, max((w[e] << 16) & 0x7fffffffu, w[e] & 0x7fff0000u));
+        }
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest to [2^14, 2^15); infinities and NaN stay what they are
+        const int e = (int)(top >> 23);
+        const int up = e == 0 || e == 255 ? 0 : min(max(141 - e, -100), 100);
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        const float back = __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2;
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            #pragma unroll
+            for (int x = 0; x < 4; ++x)
+                qf[n][i][x] = as_u32(__floats2half2_rn(__uint_as_float(w[x] << 16) * f,
+                                                       __uint_as_float(w[x] & 0xffff0000u) * f));
+        }
+        #pragma unroll
+        for (int i = 0; i < 2; ++i)
+            slc[n][i] = __shfl_sync(0xffffffffu, back, (2 * c + i) * 4);
+    }
+}
+
+// Scores of 32 tokens: s[m][n][0, 1] of token 16 m + g, [2, 3] of the one 8
+// further, columns 2 c and 2 c + 1.
+template <int NT>
+__device__ __forceinline__ void score_tile(const uint8_t *codes, const uint32_t *scales,
+                                           const uint32_t (&qf)[NT][4][4], float (&s)[2][NT][4])
+{
+    const int lane = lane_id(), g = lane >> 2, c = lane & 3;
+    #pragma unroll
+    for (int m = 0; m < 2; ++m) {
+        const uint8_t *row = codes + (16 * m + g) * kKv4Codes + 4 * c;
+        float sa[4], sb[4];
+        e8m0_to_float(scales[16 * m + g], sa);
+        e8m0_to_float(scales[16 * m + g + 8], sb);
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int at = (i ^ (g >> 1 & 3)) << 4;
+            uint32_t ka[4], kb[4];
+            e2m1_to_f16x2(*reinterpret_cast<const uint32_t *>(row + at), ka);
+            e2m1_to_f16x2(*reinterpret_cast<const uint32_t *>(row + 8 * kKv4Codes + at), kb);
+            const uint32_t a0[4] = {ka[0], kb[0], ka[1], kb[1]};
+            const uint32_t a1[4] = {ka[2], kb[2], ka[3], kb[3]};
+            #pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float d[4] = {};
+                mma16(d, a0, qf[n][i][0], qf[n][i][1]);
+                mma16(d, a1, qf[n][i][2], qf[n][i][3]);
+                #pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    s[m][n][x] = i == 0 ? d[x] * (x < 2 ? sa[0] : sb[0])
+                                        : fmaf(d[x], x < 2 ? sa[i] : sb[i], s[m][n][x]);
+            }
+        }
+    }
+}
+
+// Scores of places where there is no token, or none that the column sees, are
+// -inf.  tok0: the first token; ends of columns 2 c, 2 c + 1.
+template <int NT>
+__device__ __forceinline__ void mask_tile(float (&s)[2][NT][4], uint32_t there, int tok0,
+                                          const int (&end)[NT][2])
+{
+    const int g = lane_id() >> 2;
+    #pragma unroll
+    for (int m = 0; m < 2; ++m)
+        #pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int r = 16 * m + g + 8 * (x >> 1);
+            const bool here = there >> r & 1;
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                s[m][n][x] = here && tok0 + r < end[n][x & 1] ? s[m][n][x] : -INFINITY;
+        }
+}
+
+// ----------------------------------------------------------------- attention
+
+template <int NT>
+struct Shape {
+    static constexpr int kCols = 8 * NT;
+    static constexpr int kStages = NT == 1 ? 3 : 4;
+    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;  // of an SM
+    static constexpr int kPart = kCols * (kKv4Dim + 2);  // floats of a partial result
+    // the warps' sums where they meet: rows of 128 elements, padded so that a
+    // quad's columns fall into different banks
+    static constexpr int kRow = kKv4Dim + 4;
+    static constexpr int kMeet = kWarps * kCols * (kRow + 2) * 4;
+    template <bool kPaged>
+    static constexpr int smem()
+    {
+        const int ring = kWarps * Ring<kPaged, true, kStages>::kBytes;
+        return ring > kMeet ? ring : kMeet;
+    }
+};
+
+template <bool kPaged, int NT>
+__global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
+    kv4_attention_kernel(const __grid_constant__ Kv4Args a)
+{
+    using S = Shape<NT>;
+    using R = Ring<kPaged, true, S::kStages>;
+    constexpr int kStages = S::kStages, kCols = S::kCols;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int tid = threadIdx.x, lane = lane_id(), g = lane >> 2, c = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int heads = a.pool.heads * a.blocks;
+    const int64_t limit = kPaged || a.uncut ? INT64_MAX / INT_MAX : a.num_slots / kTile + a.B;
+    if (tid == 0 && !a.uncut)
+        a.ws_cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    Share share;
+    if (!find_share<kPaged>(a, heads, limit, share))
+        return;
+    R ring;
+    ring.mem = smem + warp * R::kBytes;
+    Seg seg;
+    for (int nth = 0; next_seg<kPaged>(a, heads, share, seg); ++nth) {
+        const int head = seg.hc / a.blocks, cb = seg.hc - head * a.blocks;
+        const int tok0 = seg.t0 * kTile + warp * kSub;
+        const int upto = (int)min((int64_t)seg.t1 * kTile, (int64_t)seg.len);
+        const int steps = tok0 < upto ? (upto - tok0 + kTile - 1) / kTile : 0;
+        ring.start(a, seg.b, head, upto, tok0);
+        #pragma unroll
+        for (int i = 0; i < kStages - 1; ++i) {
+            if (i < steps)
+                ring.fill(a, i);
+            cp_async_commit();
+        }
+        uint32_t qf[NT][4][4];
+        float slc[NT][2];
+        load_queries<NT>(a, seg.b, head, cb, qf, slc);
+        int end[NT][2], least = INT_MAX;
+        #pragma unroll
+        for (int n = 0; n < NT; ++n)
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = cb * kCols + n * 8 + 2 * c + i;
+                end[n][i] = col < a.cols ? row_end<kPaged>(a, seg.b, col / a.group, seg.len) : 0;
+                if (col < a.cols)
+                    least = min(least, end[n][i]);
+            }
+        least = __reduce_min_sync(0xffffffffu, least);
+
+        float o[8][NT][4] = {};  // element tiles: rows 32 (t / 2) + 4 g + 2 (t % 2) and the next
+        float m[NT][2], l[NT][2];
+        #pragma unroll
+        for (int n = 0; n < NT; ++n)
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                m[n][i] = -FLT_MAX;
+                l[n][i] = 0.0f;
+            }
+        uint32_t top_e = 0;  // the largest exponents, a byte a group
+        int st = 0;
+        #pragma unroll 1
+        for (int k = 0; k < steps; ++k) {
+            cp_async_wait<kStages - 2>();
+            __syncwarp();
+            {
+                const int to = st == 0 ? kStages - 1 : st - 1;
+                if (k + kStages - 1 < steps)
+                    ring.fill(a, to);
+                cp_async_commit();
+            }
+            const uint8_t *mem = ring.stage(st);
+            const uint32_t *scales = reinterpret_cast<const uint32_t *>(mem + R::kCodes);
+            const uint32_t there = ring.masks()[st];
+            const int tok = tok0 + k * kTile;
+            st = st + 1 == kStages ? 0 : st + 1;
+            float s[2][NT][4];
+            score_tile<NT>(mem, scales, qf, s);
+            if (there != 0xffffffffu || tok + kSub > least)
+                mask_tile<NT>(s, there, tok, end);
+
+            // ---- the running maximum
+            bool over = false;
+            float mx[NT][2];
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    mx[n][i] = fmaxf(fmaxf(s[0][n][i], s[0][n][i + 2]),
+                                     fmaxf(s[1][n][i], s[1][n][i + 2])) * slc[n][i];
+                    over |= mx[n][i] > m[n][i] + kLazy;
+                }
+            if (__any_sync(0xffffffffu, over)) {
+                #pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    #pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float t = mx[n][i];
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
+                        t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
+                        const float nm = fmaxf(m[n][i], t);
+                        const float al = nm == m[n][i] ? 1.0f : ex2(m[n][i] - nm);
+                        m[n][i] = nm;
+                        l[n][i] *= al;
+                        #pragma unroll
+                        for (int x = 0; x < 8; ++x) {
+                            o[x][n][i] *= al;
+                            o[x][n][i + 2] *= al;
+                        }
+                    }
+            }
+            // ---- weights
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float z = (float)kBias - m[n][i];
+                    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        s[h][n][i] = ex2(fmaf(s[h][n][i], slc[n][i], z));
+                        s[h][n][i + 2] = ex2(fmaf(s[h][n][i + 2], slc[n][i], z));
+                        l[n][i] += s[h][n][i] + s[h][n][i + 2];
+                    }
+                }
+
+            // ---- exponents of the values: a lane a token
+            const bool here = there >> lane & 1;
+            const uint32_t word = here ? scales[kSub + lane] : top_e;
+            const auto in_range = [&] {
+                // top - word bytewise, at most kScaleRange (and nothing over the top)
+                const uint32_t d = top_e - word;
+                const bool low = ((((d & 0x7f7f7f7fu) + 0x01010101u * (127 - kScaleRange)) | d) &
+                                  0x80808080u) == 0;
+                return __vmaxu4(word, top_e) == top_e && low;
+            };
+            bool fast = __all_sync(0xffffffffu, in_range());
+            if (!fast) {
+                // raise the tops over this tile's (one more, so that the next need not), NaN apart
+                uint32_t t = here ? word & ~__vcmpeq4(word, 0xffffffffu) : 0u;
+                #pragma unroll
+                for (int x = 16; x > 0; x >>= 1)
+                    t = __vmaxu4(t, __shfl_xor_sync(0xffffffffu, t, x));
+                uint32_t next = 0;
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int was = top_e >> (8 * i) & 255, now = t >> (8 * i) & 255;
+                    const int e = now > was ? min(now + 1, 254) : was;
+                    next |= (uint32_t)e << (8 * i);
+                    const float f = pow2i(was - e);
+                    #pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        #pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            o[2 * i][n][x] *= f;
+                            o[2 * i + 1][n][x] *= f;
+                        }
+                }
+                const bool was_there = here;
+                top_e = next;
+                const uint32_t d = top_e - (was_there ? word : top_e);
+                const uint32_t w = was_there ? word : top_e;
+                const bool low = ((((d & 0x7f7f7f7fu) + 0x01010101u * (127 - kScaleRange)) | d) &
+                                  0x80808080u) == 0;
+                fast = __all_sync(0xffffffffu, __vmaxu4(w, top_e) == top_e && low);
+            }
+            const uint8_t *val = mem + kSubCodes;
+            // element pairs of groups 2 y and 2 y + 1 of four tokens, widened: rows of the
+            // products' left side, two tiles a group
+            const auto widen = [&](int h, int y, uint32_t (&w)[4][4]) {
+                uint32_t r[4];
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint8_t *at = val + (16 * h + 2 * c + (i & 1) + 8 * (i >> 1)) * kKv4Codes + 2 * g;
+                    const uint32_t u0 = *reinterpret_cast<const uint16_t *>(at + (((2 * y) ^ c) << 4));
+                    const uint32_t u1 = *reinterpret_cast<const uint16_t *>(at + (((2 * y + 1) ^ c) << 4));
+                    r[i] = __byte_perm(u0, u1, 0x5410);
+                }
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t x0 = r[2 * i], x1 = r[2 * i + 1];
+                    uint32_t f[4];
+                    e2m1_to_f16x2((x0 & 0x0f0f0f0fu) | (x1 << 4 & 0xf0f0f0f0u), f);
+                    #pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        w[t][2 * i] = f[t];
+                    e2m1_to_f16x2((x0 >> 4 & 0x0f0f0f0fu) | (x1 & 0xf0f0f0f0u), f);
+                    #pragma unroll
+                    for (int t = 0; t < 4; ++t)
+                        w[t][2 * i + 1] = f[t];
+                }
+            };
+            if (fast) {
+                // a lane its token's scales as f16, 2^(e - top + 5) by their exponent bits:
+                // groups 0 and 2, then 1 and 3
+                const uint32_t w = here ? word : top_e;
+                const uint32_t f = (0x01010101u * (15 + kScaleUp) - (top_e - w)) << 2;
+                ring.turned()[lane] = make_uint2((f & 0x00ff00ffu) << 8, f & 0xff00ff00u);
+                __syncwarp();
+                #pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[NT][2];
+                    #pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            p[n][i] = turn8(as_u32(__floats2half2_rn(s[h][n][2 * i], s[h][n][2 * i + 1])));
+                    const uint4 e0 = *reinterpret_cast<const uint4 *>(ring.turned() + 16 * h + 2 * c);
+                    const uint4 e1 = *reinterpret_cast<const uint4 *>(ring.turned() + 16 * h + 2 * c + 8);
+                    #pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t v[4][4];
+                        widen(h, y, v);
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            // group 2 y + i of tokens 2 c, 2 c + 1 and of those 8 further
+                            const uint32_t f0 = __byte_perm(i ? e0.y : e0.x, i ? e0.w : e0.z, y ? 0x7632 : 0x5410);
+                            const uint32_t f1 = __byte_perm(i ? e1.y : e1.x, i ? e1.w : e1.z, y ? 0x7632 : 0x5410);
+                            #pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                const uint32_t b0 = as_u32(__hmul2(as_h2(p[n][0]), as_h2(f0)));
+                                const uint32_t b1 = as_u32(__hmul2(as_h2(p[n][1]), as_h2(f1)));
+                                mma16(o[4 * y + 2 * i][n], v[2 * i], b0, b1);
+                                mma16(o[4 * y + 2 * i + 1][n], v[2 * i + 1], b0, b1);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+            } else {
+                // weights and scales in bf16; a column that does not see a token has no part
+                // in a scale that is not finite
+                #pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t p[NT][2], seen[NT] = {};
+                    #pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float x = h ? s[1][n][2 * i] : s[0][n][2 * i];
+                            const float y = h ? s[1][n][2 * i + 1] : s[0][n][2 * i + 1];
+                            p[n][i] = turn8(as_u32(__floats2bfloat162_rn(x, y)));
+                        }
+                        const int col = cb * kCols + n * 8 + g;
+                        const int last = col < a.cols ? row_end<kPaged>(a, seg.b, col / a.group, seg.len) : 0;
+                        #pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const int r = 16 * h + 2 * c + (x & 1) + 8 * (x >> 1);
+                            seen[n] |= (uint32_t)((there >> r & 1) && tok + r < last) << x;
+                        }
+                    }
+                    #pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        uint32_t v[4][4];
+                        widen(h, y, v);
+                        #pragma unroll
+                        for (int t = 0; t < 4; ++t)
+                            #pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                v[t][x] = to_bf16x2(v[t][x]);
+                        #pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const int grp = 2 * y + i;
+                            float f[4];
+                            #pragma unroll
+                            for (int x = 0; x < 4; ++x) {
+                                const int r = 16 * h + 2 * c + (x & 1) + 8 * (x >> 1);
+                                const int e = scales[kSub + r] >> (8 * grp) & 255;
+                                const int d = e - (int)(top_e >> (8 * grp) & 255) + kScaleUp;
+                                f[x] = e == 255 ? NAN : pow2i(d);
+                            }
+                            #pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                uint32_t b[2];
+                                #pragma unroll
+                                for (int x = 0; x < 2; ++x) {
+                                    const float2 pf = __bfloat1622float2(as_b2(p[n][x]));
+                                    b[x] = as_u32(__floats2bfloat162_rn(
+                                        seen[n] >> (2 * x) & 1 ? pf.x * f[2 * x] : 0.0f,
+                                        seen[n] >> (2 * x + 1) & 1 ? pf.y * f[2 * x + 1] : 0.0f));
+                                }
+                                mma16_bf(o[4 * y + 2 * i][n], v[2 * i], b[0], b[1]);
+                                mma16_bf(o[4 * y + 2 * i + 1][n], v[2 * i + 1], b[0], b[1]);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+        cp_async_wait<0>();
+        __syncthreads();  // the rings are read
+
+        // ---- the warps meet
+        float *sums = reinterpret_cast<float *>(smem) + warp * kCols * S::kRow;
+        float *stat = reinterpret_cast<float *>(smem) + kWarps * kCols * S::kRow;  // [warp][m, l][col]
+        #pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = pow2i((int)(top_e >> (8 * i) & 255) - 127 - kScaleUp - kBias);
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int x = 0; x < 2; ++x)
+                    *reinterpret_cast<float4 *>(sums + (8 * n + 2 * c + x) * S::kRow + 32 * i + 4 * g) =
+                        make_float4(o[2 * i][n][x] * f, o[2 * i][n][x + 2] * f, o[2 * i + 1][n][x] * f,
+                                    o[2 * i + 1][n][x + 2] * f);
+        }
+        #pragma unroll
+        for (int n = 0; n < NT; ++n)
+            #pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                float t = l[n][i];
+                t += __shfl_xor_sync(0xffffffffu, t, 4);
+                t += __shfl_xor_sync(0xffffffffu, t, 8);
+                t += __shfl_xor_sync(0xffffffffu, t, 16);
+                if (g == 0) {
+                    stat[(2 * warp) * kCols + 8 * n + 2 * c + i] = m[n][i];
+                    stat[(2 * warp + 1) * kCols + 8 * n + 2 * c + i] = t * pow2i(-kBias);
+                }
+            }
+        __syncthreads();
+        const bool part = seg.t0 > 0 || seg.t1 < seg.tiles;
+        float *to = a.ws_part + (int64_t)(2 * blockIdx.x + (nth > 0)) * S::kPart;
+        if (part && seg.t0 == 0 && tid == 0) {
+            // the shares that hold the rest: `more - p - 1` longer ones first
+            const int64_t longer = max(0, share.more - (int)blockIdx.x - 1);
+            const int rest = seg.tiles - seg.t1;
+            const int in = (int)min((int64_t)rest, longer * (share.each + 1));
+            a.ws_cut[blockIdx.x] = make_int4(
+                seg.b, seg.hc, 1 + (in + share.each) / (share.each + 1) +
+                                   (rest - in + share.each - 1) / share.each, nth > 0);
+        }
+        const float *all = reinterpret_cast<const float *>(smem);
+        #pragma unroll 1
+        for (int col = 0; col < min(kCols, a.cols - cb * kCols); ++col) {
+            float mw[kWarps], top = -FLT_MAX, sum = 0.0f, acc = 0.0f;
+            #pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                mw[w] = stat[2 * w * kCols + col];
+                top = fmaxf(top, mw[w]);
+            }
+            #pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(mw[w] - top);
+                sum = fmaf(f, stat[(2 * w + 1) * kCols + col], sum);
+                acc = fmaf(f, all[(w * kCols + col) * S::kRow + tid], acc);
+            }
+            if (part) {
+                to[col * kKv4Dim + tid] = acc;
+                if (tid == 0) {
+                    to[kCols * kKv4Dim + col] = top;
+                    to[kCols * kKv4Dim + kCols + col] = sum;
+                }
+            } else {
+                const int at = cb * kCols + col, j = at / a.group;
+                const int64_t row = (int64_t)seg.b * a.next_n + j;
+                const int h = head * a.group + at - j * a.group;
+                const float v = sum == 0.0f ? 0.0f : acc / sum;
+                reinterpret_cast<__nv_bfloat16 *>(a.out)[row * a.ldo_row + h * a.ldo_head + tid] =
+                    __float2bfloat16_rn(v);
+                if (a.lse && tid == 0)
+                    a.lse[row * a.ld_lse + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+            }
+        }
+        __syncthreads();  // before the rings fill again
+    }
+}
+
+// Joins the pieces of a unit that several shares hold: blockIdx.x is the share
+// that begins it, blockIdx.y the column.  A warp a piece, four in flight.
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, int kCols)
+{
+    constexpr int kTeams = kJoinThreads / 32;
+    __shared__ float4 meet[kTeams][32];
+    __shared__ float meet_sum[kTeams], meet_top[kTeams];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int4 cut = a.ws_cut[blockIdx.x];
+    const int pieces = cut.z, col = blockIdx.y;
+    const int head = cut.y / a.blocks, cb = cut.y - head * a.blocks;
+    const int at = cb * kCols + col;
+    if (pieces < 2 || at >= a.cols)
+        return;
+    const int team = threadIdx.x >> 5, lane = lane_id();
+    const int64_t step = 2 * (int64_t)kCols * (kKv4Dim + 2);
+    const float *rest = a.ws_part + blockIdx.x * step;
+    const float *first = rest + cut.w * (step / 2);
+    const int stat = kCols * kKv4Dim + col;
+    float top = -FLT_MAX;
+    for (int i = threadIdx.x; i < pieces; i += kJoinThreads)
+        top = fmaxf(top, (i == 0 ? first : rest + i * step)[stat]);
+    #pragma unroll
+    for (int x = 16; x > 0; x >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    if (lane == 0)
+        meet_top[team] = top;
+    __syncthreads();
+    #pragma unroll
+    for (int i = 0; i < kTeams; ++i)
+        top = fmaxf(top, meet_top[i]);
+    float sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    #pragma unroll 4
+    for (int i = team; i < pieces; i += kTeams) {
+        const float *f = i == 0 ? first : rest + i * step;
+        const float w = ex2(f[stat] - top);
+        const float4 v = *reinterpret_cast<const float4 *>(f + col * kKv4Dim + 4 * lane);
+        sum = fmaf(w, f[stat + kCols], sum);
+        acc.x = fmaf(w, v.x, acc.x);
+        acc.y = fmaf(w, v.y, acc.y);
+        acc.z = fmaf(w, v.z, acc.z);
+        acc.w = fmaf(w, v.w, acc.w);
+    }
+    meet[team][lane] = acc;
+    if (lane == 0)
+        meet_sum[team] = sum;
+    __syncthreads();
+    if (team > 0)
+        return;
+    #pragma unroll
+    for (int i = 1; i < kTeams; ++i) {
+        const float4 v = meet[i][lane];
+        acc.x += v.x;
+        acc.y += v.y;
+        acc.z += v.z;
+        acc.w += v.w;
+        sum += meet_sum[i];
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int j = at / a.group, h = head * a.group + at - j * a.group;
+    const int64_t row = (int64_t)cut.x * a.next_n + j;
+    *reinterpret_cast<uint2 *>(a.out + row * a.ldo_row + h * a.ldo_head + 4 * lane) =
+        make_uint2(as_u32(__floats2bfloat162_rn(acc.x * inv, acc.y * inv)),
+                   as_u32(__floats2bfloat162_rn(acc.z * inv, acc.w * inv)));
+    if (a.lse && lane == 0)
+        a.lse[row * a.ld_lse + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+}
+
+// ------------------------------------------------------------ tokens' weights
+//
+// The scores once more, without values: exp(s - lse) summed over the columns.
+// Half the cache's bytes, and 8 of the weights.  Where there are more columns than a
+// block, a segment is walked for each and the same lane adds to what it wrote.
+template <int NT>
+__global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4)
+    kv4_weights_kernel(const __grid_constant__ Kv4Args a)
+{
+    constexpr int kStages = 4, kCols = 8 * NT;
+    using R = Ring<true, false, kStages>;
+    __shared__ __align__(16) uint8_t smem[kWarps * R::kBytes];
+    const int tid = threadIdx.x, lane = lane_id(), c = lane & 3;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    pdl_wait();
+    pdl_launch_dependents();
+    const int heads = a.pool.heads;
+    Share share;
+    share.left = 0;
+    find_share<true>(a, heads, INT64_MAX / INT_MAX, share);
+    R ring;
+    ring.mem = smem + warp * R::kBytes;
+    Seg seg;
+    while (next_seg<true>(a, heads, share, seg)) {
+        const int head = seg.hc;
+        const int tok0 = seg.t0 * kTile + warp * kSub;
+        const int upto = (int)min((int64_t)seg.t1 * kTile, (int64_t)seg.len);
+        const int steps = tok0 < upto ? (upto - tok0 + kTile - 1) / kTile : 0;
+        const float *mass = a.mass ? a.mass + seg.b * a.ld_batch + head * a.ld_head : nullptr;
+        float *out = a.mass_out + seg.b * a.ldo_batch + head * a.ldo_mass_head;
+        #pragma unroll 1
+        for (int cb = 0; cb < a.blocks; ++cb) {
+            ring.start(a, seg.b, head, upto, tok0);
+            #pragma unroll
+            for (int i = 0; i < kStages - 1; ++i) {
+                if (i < steps)
+                    ring.fill(a, i);
+                cp_async_commit();
+            }
+            uint32_t qf[NT][4][4];
+            float slc[NT][2], z[NT][2];
+            load_queries<NT>(a, seg.b, head, cb, qf, slc);
+            int end[NT][2], least = INT_MAX;
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int col = cb * kCols + n * 8 + 2 * c + i, j = col / a.group;
+                    end[n][i] = 0;
+                    z[n][i] = -INFINITY;  // a column that is not there weighs nothing
+                    if (col < a.cols) {
+                        end[n][i] = row_end<true>(a, seg.b, j, seg.len);
+                        const float v = a.lse_in[((int64_t)seg.b * a.next_n + j) * a.ld_lse_in +
+                                                 head * a.group + col - j * a.group];
+                        z[n][i] = v == -INFINITY ? 0.0f : -v * kLog2e;
+                        least = min(least, end[n][i]);
+                    }
+                }
+            least = __reduce_min_sync(0xffffffffu, least);
+            int st = 0;
+            #pragma unroll 1
+            for (int k = 0; k < steps; ++k) {
+                cp_async_wait<kStages - 2>();
+                __syncwarp();
+                {
+                    const int to = st == 0 ? kStages - 1 : st - 1;
+                    if (k + kStages - 1 < steps)
+                        ring.fill(a, to);
+                    cp_async_commit();
+                }
+                // this lane's token of the sums: 16 (c / 2) + 8 (c % 2) + g
+                const int tok = tok0 + k * kTile;
+                const int mine = tok + 16 * (c >> 1) + 8 * (c & 1) + (lane >> 2);
+                float before = 0.0f;
+                if (mine < upto) {
+                    if (cb > 0)
+                        before = out[mine];
+                    else if (mass)
+                        before = mass[mine];
+                }
+                const uint8_t *mem = ring.stage(st);
+                const uint32_t there = ring.masks()[st];
+                st = st + 1 == kStages ? 0 : st + 1;
+                float s[2][NT][4];
+                score_tile<NT>(mem, reinterpret_cast<const uint32_t *>(mem + R::kCodes), qf, s);
+                if (there != 0xffffffffu || tok + kSub > least)
+                    mask_tile<NT>(s, there, tok, end);
+                float v[4] = {};
+                #pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        #pragma unroll
+                        for (int x = 0; x < 2; ++x)
+                            v[i] += ex2(fmaf(s[i >> 1][n][2 * (i & 1) + x], slc[n][x], z[n][x]));
+                // the quad's lanes hold two columns of each eight: a lane ends with one of the
+                // four tokens
+                float w[2];
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float give = c & 1 ? v[2 * i] : v[2 * i + 1];
+                    w[i] = (c & 1 ? v[2 * i + 1] : v[2 * i]) + __shfl_xor_sync(0xffffffffu, give, 1);
+                }
+                const float give = c & 2 ? w[0] : w[1];
+                const float sum = (c & 2 ? w[1] : w[0]) + __shfl_xor_sync(0xffffffffu, give, 2);
+                if (mine < upto)
+                    out[mine] = before + sum;
+            }
+            cp_async_wait<0>();
+            __syncwarp();
+        }
+    }
+    // ---- columns past the contexts
+    if (a.mass == a.mass_out)
+        return;
+    constexpr int kChunk = 8 * kThreads;
+    const int chunks = (a.width + kChunk - 1) / kChunk;
+    for (int64_t i = blockIdx.x; i < (int64_t)a.B * heads * chunks; i += gridDim.x) {
+        const int bh = (int)(i / chunks), at = (int)(i - (int64_t)bh * chunks) * kChunk;
+        const int b = bh / heads, head = bh - b * heads;
+        const int from = max(at, unit_len<true>(a, b)), to = min((int64_t)at + kChunk, (int64_t)a.width);
+        const float *mass = a.mass ? a.mass + b * a.ld_batch + head * a.ld_head : nullptr;
+        float *out = a.mass_out + b * a.ldo_batch + head * a.ldo_mass_head;
+        for (int t = from + tid; t < to; t += kThreads)
+            out[t] = mass ? mass[t] : 0.0f;
+    }
+}
+
+// ---------------------------------------------------------------------- host
+
+// Columns of a block: 8, 16 or 32.
+int tiles_of(int cols)
+{
+    return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+}
+
+int ctas_of(int nt)
+{
+    return nt == 1 ? Shape<1>::kCtas : nt == 2 ? Shape<2>::kCtas : Shape<4>::kCtas;
+}
+
+int part_of(int nt)
+{
+    return nt == 1 ? Shape<1>::kPart : nt == 2 ? Shape<2>::kPart : Shape<4>::kPart;
+}
+
+size_t cut_bytes(int shares)
+{
+    return ((size_t)shares * sizeof(int4) + 255) / 256 * 256;
+}
+
+template <bool kPaged, int NT>
+idx_status launch_attention(const Kv4Args &a, int shares, cudaStream_t stream)
+{
+    constexpr int smem = Shape<NT>::template smem<kPaged>();
+    static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return IDX_ERR_CUDA;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        if (cudaFuncSetAttribute(kv4_attention_kernel<kPaged, NT>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+            return IDX_ERR_CUDA;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaError_t e = launch_pdl(kv4_attention_kernel<kPaged, NT>, dim3(shares), dim3(kThreads), smem,
+                               stream, a);
+    if (e == cudaSuccess && shares > 1 && !a.uncut)
+        e = launch_pdl(kv4_join_kernel, dim3(shares - 1, std::min(a.cols, 8 * NT)),
+                       dim3(kJoinThreads), 0, stream, a, 8 * NT);
+    return launch_status(e);
+}
+
+// Checks that the calls share; keys: of a row at most.
+idx_status check_attention(const void *q, int64_t ldq_row, int64_t ldq_head, int H, int kv_heads,
+                           int D, float scale)
+{
+    if (!q || !(scale > 0.0f) || !(scale * kLog2e <= 3.4e38f) || ldq_head < D || ldq_row < 0)
+        return IDX_ERR_INVALID_ARG;
+    if (H % kv_heads != 0 || D != kKv4Dim || !aligned16(q) || (ldq_row | ldq_head) % 8 != 0)
+        return IDX_ERR_UNSUPPORTED;
+    return IDX_OK;
+}
+
+// Fills in what a launch needs and launches; rows: of all sequences.
+template <bool kPaged>
+idx_status run_attention(Kv4Args &a, int64_t keys, int64_t most_tiles, void *ws, size_t ws_bytes,
+                         int H, idx_stream_t stream)
+{
+    const int nt = tiles_of(a.cols);
+    a.blocks = (a.cols + 8 * nt - 1) / (8 * nt);
+    a.uncut = keys <= kUncutKeys;
+    const int64_t units = (int64_t)a.B * a.pool.heads * a.blocks;
+    const int64_t tiles = a.uncut ? units : most_tiles * a.pool.heads * a.blocks;
+    if ((int64_t)a.pool.heads * a.blocks > INT32_MAX / 2 || most_tiles > INT32_MAX / ((int64_t)a.pool.heads * a.blocks))
+        return IDX_ERR_UNSUPPORTED;
+    const size_t need = idx_kv4_attention_workspace_size(a.B * a.next_n, a.next_n, H, a.pool.heads, keys);
+    if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need))
+        return IDX_ERR_WORKSPACE;
+    a.status = device_status_ptr();
+    if (!a.status)
+        return IDX_ERR_CUDA;
+    const int most = sm_count() * ctas_of(nt);
+    const int shares = (int)std::min<int64_t>(most, std::max<int64_t>(1, tiles));
+    a.ws_cut = static_cast<int4 *>(ws);
+    a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + cut_bytes(most));
+    const cudaStream_t s = (cudaStream_t)stream;
+    return nt == 1 ? launch_attention<kPaged, 1>(a, shares, s)
+         : nt == 2 ? launch_attention<kPaged, 2>(a, shares, s)
+                   : launch_attention<kPaged, 4>(a, shares, s);
+}
+
+} // namespace
+} // namespace idx
+
+using namespace idx;
+
+extern "C" size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int kv_heads,
+                                                   int64_t max_keys)
+{
+    if (R <= 0 || next_n <= 0 || H <= 0 || kv_heads <= 0 || max_keys <= kUncutKeys)
+        return 0;
+    const int64_t cols = (int64_t)next_n * (H / kv_heads);
+    const int nt = tiles_of((int)std::min<int64_t>(cols, 32)), most = sm_count() * ctas_of(nt);
+    return cut_bytes(most) + (size_t)2 * most * part_of(nt) * sizeof(float);
+}
+
+extern "C" idx_status idx_kv4_attention(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
+                                        const uint8_t *kv_pages, int64_t page_stride_bytes,
+                                        int num_pages, int page_size, const int32_t *slots,
+                                        const int32_t *indptr, int64_t num_slots, int R, int H,
+                                        int kv_heads, int D, float scale, uint16_t *out,
+                                        int64_t ldo_row, int64_t ldo_head, float *lse,
+                                        int64_t ld_lse, void *ws, size_t ws_bytes,
+                                        idx_stream_t stream)
+{
+    IDX_NVTX_RANGE("idx_kv4_attention");
+    if (R < 0 || H <= 0 || kv_heads <= 0 || D <= 0 || num_slots < 0)
+        return IDX_ERR_INVALID_ARG;
+    if (R == 0)
+        return IDX_OK;
+    if (!indptr || (num_slots > 0 && !slots) || !out || ldo_head < D || ldo_row < 0 ||
+        (lse && ld_lse < H))
+        return IDX_ERR_INVALID_ARG;
+    idx_status ok = check_attention(q, ldq_row, ldq_head, H, kv_heads, D, scale);
+    if (ok == IDX_OK)
+        ok = check_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
+    if (ok != IDX_OK)
+        return ok;
+    if (!aligned16(out) || (ldo_row | ldo_head) % 8 != 0 || num_slots > INT32_MAX - 4 * kTile)
+        return IDX_ERR_UNSUPPORTED;
+    Kv4Args a = {};
+    a.q = q;
+    a.ldq_row = ldq_row;
+    a.ldq_head = ldq_head;
+    a.pool = make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
+    a.group = a.cols = H / kv_heads;
+    a.next_n = 1;
+    a.slots = slots;
+    a.indptr = indptr;
+    a.num_slots = num_slots;
+    a.B = R;
+    a.scale_log2 = scale * kLog2e;
+    a.out = out;
+    a.ldo_row = ldo_row;
+    a.ldo_head = ldo_head;
+    a.lse = lse;
+    a.ld_lse = ld_lse;
+    return run_attention<false>(a, num_slots, num_slots / kTile + R, ws, ws_bytes, H, stream);
+}
+
+extern "C" idx_status idx_paged_kv4_attention(
+    const uint16_t *q, int64_t ldq_row, int64_t ldq_head, const uint8_t *kv_pages,
+    int64_t page_stride_bytes, int num_pages, int page_size, const int32_t *block_table,
+    int64_t bt_stride, const int32_t *context_lens, int ctx_per_row, int B, int next_n,
+    int max_model_len, int H, int kv_heads, int D, float scale, uint16_t *out, int64_t ldo_row,
+    int64_t ldo_head, float *lse, int64_t ld_lse, void *ws, size_t ws_bytes, idx_stream_t stream)
+{
+    IDX_NVTX_RANGE("idx_paged_kv4_attention");
+    if (B < 0 || next_n <= 0 || H <= 0 || kv_heads <= 0 || D <= 0 || max_model_len < 0)
+        return IDX_ERR_INVALID_ARG;
+    if (B == 0)
+        return IDX_OK;
+    if (!context_lens || (max_model_len > 0 && !block_table) || !out || ldo_head < D ||
+        ldo_row < 0 || (lse && ld_lse < H))
+        return IDX_ERR_INVALID_ARG;
+    idx_status ok = check_attention(q, ldq_row, ldq_head, H, kv_heads, D, scale);
+    if (ok == IDX_OK)
+        ok = check_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
+    if (ok != IDX_OK)
+        return ok;
+    if (bt_stride < ((int64_t)max_model_len + page_size - 1) / page_size)
+        return IDX_ERR_INVALID_ARG;
+    const int64_t cols = (int64_t)next_n * (H / kv_heads);
+    if (!aligned16(out) || (ldo_row | ldo_head) % 8 != 0 || cols > INT32_MAX / 2 ||
+        (int64_t)B * next_n > INT32_MAX || max_model_len > INT32_MAX - 4 * kTile)
+        return IDX_ERR_UNSUPPORTED;
+    Kv4Args a = {};
+    a.q = q;
+    a.ldq_row = ldq_row;
+    a.ldq_head = ldq_head;
+    a.pool = make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
+    a.group = H / kv_heads;
+    a.cols = (int)cols;
+    a.next_n = next_n;
+    a.table = block_table;
+    a.bt_stride = bt_stride;
+    a.ctx = context_lens;
+    a.ctx_per_row = ctx_per_row != 0;
+    a.max_len = max_model_len;
+    a.B = B;
+    a.scale_log2 = scale * kLog2e;
+    a.out = out;
+    a.ldo_row = ldo_row;
+    a.ldo_head = ldo_head;
+    a.lse = lse;
+    a.ld_lse = ld_lse;
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)max_model_len + kTile - 1) / kTile);
+    return run_attention<true>(a, max_model_len, B * tiles, ws, ws_bytes, H, stream);
+}
+
+extern "C" idx_status idx_paged_kv4_weights(
+    const uint16_t *q, int64_t ldq_row, int64_t ldq_head, const uint8_t *kv_pages,
+    int64_t page_stride_bytes, int num_pages, int page_size, const int32_t *block_table,
+    int64_t bt_stride, const int32_t *context_lens, int ctx_per_row, int B, int next_n,
+    int max_model_len, int H, int kv_heads, int D, float scale, const float *lse, int64_t ld_lse,
+    const float *mass, int64_t ld_batch, int64_t ld_head, int width, float *out, int64_t ldo_batch,
+    int64_t ldo_head, idx_stream_t stream)
+{
+    IDX_NVTX_RANGE("idx_paged_kv4_weights");
+    if (B < 0 || next_n <= 0 || H <= 0 || kv_heads <= 0 || D <= 0 || max_model_len < 0 ||
+        width < max_model_len)
+        return IDX_ERR_INVALID_ARG;
+    if (B == 0 || width == 0)
+        return IDX_OK;
+    if (!context_lens || (max_model_len > 0 && !block_table) || !lse || ld_lse < H || !out ||
+        ld_batch < 0 || ld_head < 0 || ldo_batch < 0 || ldo_head < 0)
+        return IDX_ERR_INVALID_ARG;
+    idx_status ok = check_attention(q, ldq_row, ldq_head, H, kv_heads, D, scale);
+    if (ok == IDX_OK)
+        ok = check_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
+    if (ok != IDX_OK)
+        return ok;
+    if (bt_stride < ((int64_t)max_model_len + page_size - 1) / page_size ||
+        (mass == out && (ld_batch != ldo_batch || ld_head != ldo_head)))
+        return IDX_ERR_INVALID_ARG;
+    const int64_t cols = (int64_t)next_n * (H / kv_heads);
+    const int64_t tiles = std::max<int64_t>(1, ((int64_t)max_model_len + kTile - 1) / kTile) * B;
+    if (cols > INT32_MAX / 2 || (int64_t)B * next_n > INT32_MAX || width > INT32_MAX - 4 * kTile ||
+        kv_heads > INT32_MAX / 2 || tiles > INT32_MAX / kv_heads)
+        return IDX_ERR_UNSUPPORTED;
+    Kv4Args a = {};
+    a.q = q;
+    a.ldq_row = ldq_row;
+    a.ldq_head = ldq_head;
+    a.pool = make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
+    a.group = H / kv_heads;
+    a.cols = (int)cols;
+    a.next_n = next_n;
+    a.table = block_table;
+    a.bt_stride = bt_stride;
+    a.ctx = context_lens;
+    a.ctx_per_row = ctx_per_row != 0;
+    a.max_len = max_model_len;
+    a.B = B;
+    a.scale_log2 = scale * kLog2e;
+    a.lse_in = lse;
+    a.ld_lse_in = ld_lse;
+    a.mass = mass;
+    a.ld_batch = ld_batch;
+    a.ld_head = ld_head;
+    a.width = width;
+    a.mass_out = out;
+    a.ldo_batch = ldo_batch;
+    a.ldo_mass_head = ldo_head;
+    a.status = device_status_ptr();
+    if (!a.status)
+        return IDX_ERR_CUDA;
+    const int nt = tiles_of(a.cols);
+    a.blocks = (a.cols + 8 * nt - 1) / (8 * nt);
+    auto kern = nt == 1 ? kv4_weights_kernel<1> : nt == 2 ? kv4_weights_kernel<2>
+                                                          : kv4_weights_kernel<4>;
+    const int grid = (int)std::min<int64_t>((int64_t)sm_count() * (nt == 4 ? 3 : 4),
+                                            tiles * kv_heads);
+    return launch_status(launch_pdl(kern, dim3(grid), dim3(kThreads), 0, (cudaStream_t)stream, a));
+}

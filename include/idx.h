@@ -699,8 +699,8 @@ size_t idx_latent_prefill_workspace_size(int Tq, int Tk, int H);
  * stride a multiple of 16 and at least page_size * kv_heads * 136):
  *     K codes  [kv_heads][page_size][64]      V codes  [kv_heads][page_size][64]
  *     K scales [kv_heads][page_size][4]       V scales [kv_heads][page_size][4]
- * A call's D is the heads' dimension: 128 is supported.  Pages hold less than
- * 2^31 slots in all.
+ * A call's D is the heads' dimension: 128 is supported.  Pages are of less than
+ * 2^31 bytes and hold less than 2^31 slots in all.
  * ---------------------------------------------------------------------- */
 
 /* ------------------------------------------------------------------------

@@ -50,7 +50,9 @@ inline idx_status check_kv4_pool(const uint8_t *base, int64_t stride, int num_pa
     if ((int64_t)page_size * heads > INT64_MAX / (2 * kKv4TokBytes) ||
         stride < (int64_t)page_size * heads * kKv4TokBytes)
         return IDX_ERR_INVALID_ARG;
-    if ((int64_t)num_pages * page_size > INT32_MAX || !aligned16(base) || stride % 16 != 0)
+    // slots are int32, and so are places within a page
+    if ((int64_t)num_pages * page_size > INT32_MAX || !aligned16(base) || stride % 16 != 0 ||
+        stride > INT32_MAX)
         return IDX_ERR_UNSUPPORTED;
     return IDX_OK;
 }

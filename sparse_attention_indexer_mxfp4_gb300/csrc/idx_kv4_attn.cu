@@ -28,9 +28,10 @@
 // Every warp walks 32 tokens of each tile of 128 with a running maximum and sum
 // of its own and a ring of its own, filled by asynchronous copies (16 bytes, the
 // pieces of a row turned by its number so that fragments are read without bank
-// conflicts); warps meet where a segment of a row ends.  Work is the flat list
-// of (row or sequence, key head, tile); CTAs take equal contiguous shares of it
-// and a second kernel joins what they cut.
+// conflicts).  Work is the flat list of (row or sequence, key head, tile); CTAs
+// take equal contiguous shares of it and a second kernel joins what they cut.  The
+// ring runs on over the ends of a share's segments; there the warps hand their sums
+// on in fragments, through the one place of the ring that is free.
 #include <algorithm>
 #include <atomic>
 #include <climits>
@@ -53,6 +54,7 @@ constexpr int kScaleRange = 19;         // f16 holds 2^5 to 2^-14 without loss
 // Rows of few keys are not cut: no scratch and no joining kernel.
 constexpr int kUncutKeys = 4 * kTile;
 constexpr int kJoinThreads = 256;
+constexpr int kJoinFew = 8;  // pieces of a unit that one warp joins
 
 struct Kv4Args {
     const uint16_t *q;
@@ -100,6 +102,16 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// The same on sums of zero.
+__device__ __forceinline__ void mma16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
+        " {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 __device__ __forceinline__ void mma16_bf(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                          uint32_t b1)
 {
@@ -144,11 +156,44 @@ __device__ __forceinline__ uint32_t to_bf16x2(uint32_t h)
     return as_u32(__floats2bfloat162_rn(f.x, f.y));
 }
 
-__device__ __forceinline__ void cp_async4(uint32_t saddr, const void *src)
+// Copies of scattered pieces: 64 bytes are fetched for one and no more (64 rows x
+// 64 heads x 2048 slots 56 us, with the usual granularity 71).
+__device__ __forceinline__ void cp_async16_alone(uint32_t saddr, const void *src)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(saddr),
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16;" ::"r"(saddr),
                  "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
+}
+
+__device__ __forceinline__ void cp_async4_alone(uint32_t saddr, const void *src)
+{
+    asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], 4;" ::"r"(saddr),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
+
+// Loads from shared memory by address, so that what varies is added once a step.
+__device__ __forceinline__ uint32_t lds32(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t lds16(uint32_t at)
+{
+    uint16_t v;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(at));
+    return v;
+}
+
+__device__ __forceinline__ float4 lds128f(uint32_t at)
+{
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(at));
+    return v;
 }
 
 // 2^x of a float's exponent field and beyond it (underflow gives 0).
@@ -158,6 +203,10 @@ __device__ __forceinline__ float pow2i(int x)
 }
 
 // ------------------------------------------------------------------ the list
+
+// How tokens are found: by slots, by pages of any size, by pages that hold whole
+// steps of 32 tokens.
+enum Mode { kSlots, kPages, kWholePages };
 
 // A unit's tokens: the longest of its rows.
 template <bool kPaged>
@@ -205,6 +254,7 @@ struct Share {
 };
 
 // Sums over the block, for every thread: upto and including its own, and of all.
+template <int kAllWarps>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *wsum, int64_t &all)
 {
     const int lane = lane_id(), warp = threadIdx.x >> 5;
@@ -219,65 +269,71 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *wsum, int64_t 
     __syncthreads();
     all = 0;
     #pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
+    for (int i = 0; i < kAllWarps; ++i) {
         v += i < warp ? wsum[i] : 0;
         all += wsum[i];
     }
     return v;
 }
 
-// This CTA's share; false where it has none.  limit: tiles that a list may have.
-template <bool kPaged>
-__device__ __forceinline__ bool find_share(const Kv4Args &a, int heads, int64_t limit, Share &s)
+// The share of this thread's group of kWarps warps (left: 0 where it has none);
+// group i of a CTA takes share i * gridDim.x + blockIdx.x, so that few shares
+// spread over the SMs.  limit: tiles that a list may have.
+template <bool kPaged, int kGroups>
+__device__ __forceinline__ void find_share(const Kv4Args &a, int heads, int64_t limit, Share &s)
 {
-    __shared__ int64_t wsum[kWarps];
-    __shared__ int found[2];
-    const int tid = threadIdx.x;
+    constexpr int kAll = kGroups * kThreads;
+    __shared__ int64_t wsum[kGroups * kWarps];
+    __shared__ int2 found[kGroups];
+    const int tid = threadIdx.x, group = tid / kThreads;
     int64_t total = 0, mine = 0, upto = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+    for (int b0 = 0; b0 < a.B; b0 += kAll) {
         int64_t all;
         mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
-        upto = total + block_scan(mine, wsum, all);
+        upto = total + block_scan<kGroups * kWarps>(mine, wsum, all);
         total += all;
     }
+    s.left = s.each = s.more = 0;
     if (total > limit) {
         if (blockIdx.x == 0 && tid == 0)
             atomicOr(a.status, kDevBadBounds);
-        return false;
+        return;
     }
     total *= heads;
-    const int p = blockIdx.x, shares = (int)min((int64_t)gridDim.x, total);
-    if (p >= shares)
-        return false;
+    const int shares = (int)min((int64_t)gridDim.x * kGroups, total);
     s.each = (int)(total / shares);
     s.more = (int)(total - (int64_t)s.each * shares);
-    s.left = s.each + (p < s.more);
-    const int64_t u0 = (int64_t)p * s.each + min(p, s.more);
+    const auto begin = [&](int p) { return (int64_t)p * s.each + min(p, s.more); };
     const auto look = [&](int b) {
-        const int64_t before = (upto - mine) * heads;
-        if (u0 >= before && u0 < before + mine * heads) {
-            found[0] = b;
-            found[1] = (int)(u0 - before);
+        const int64_t before = (upto - mine) * heads, after = before + mine * heads;
+        #pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            const int64_t u = begin(i * gridDim.x + blockIdx.x);
+            if (u >= before && u < after)
+                found[i] = make_int2(b, (int)(u - before));
         }
     };
-    if (a.B <= kThreads) {
+    if (a.B <= kAll) {
         look(tid);
     } else {
         int64_t sum = 0, all;
-        for (int b0 = 0; b0 < a.B; b0 += kThreads) {
+        for (int b0 = 0; b0 < a.B; b0 += kAll) {
             mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
-            upto = sum + block_scan(mine, wsum, all);
+            upto = sum + block_scan<kGroups * kWarps>(mine, wsum, all);
             sum += all;
             look(b0 + tid);
         }
     }
     __syncthreads();
-    s.b = found[0];
+    const int p = group * gridDim.x + blockIdx.x;
+    if (p >= shares)
+        return;
+    s.left = s.each + (p < s.more);
+    s.b = found[group].x;
     s.len = unit_len<kPaged>(a, s.b);
     s.tiles = (int)unit_tiles<kPaged>(a, s.b);
-    s.hc = found[1] / s.tiles;
-    s.t = found[1] - s.hc * s.tiles;
-    return true;
+    s.hc = found[group].y / s.tiles;
+    s.t = found[group].y - s.hc * s.tiles;
 }
 
 // A segment: tiles [t0, t1) of a unit.
@@ -311,101 +367,231 @@ __device__ __forceinline__ bool next_seg(const Kv4Args &a, int heads, Share &s, 
 // ------------------------------------------------------------------- a ring
 //
 // A warp's tokens on their way in: codes of the keys (and values), scales, and
-// which tokens are there.
-template <bool kPaged, bool kValues, int kStages>
+// which tokens are there.  It is filled ahead of the walk, over the ends of
+// segments; the walk that fills is a second one, in shared memory but for the
+// segment at hand.  One place is always free: the one that was read last.
+template <int kMode, bool kValues, int kStages>
 struct Ring {
+    static constexpr bool kPaged = kMode != kSlots;
     static constexpr int kCodes = (kValues ? 2 : 1) * kSubCodes;
     static constexpr int kScales = (kValues ? 2 : 1) * 4 * kSub;
     static constexpr int kStage = kCodes + kScales;
-    static constexpr int kBytes = kStages * kStage + (kValues ? 8 * kSub : 0) + 16 * ((kStages + 3) / 4);
+    // behind the stages: scales of the keys in 32 bits, of the values in 16, the second walk, and
+    // which tokens are there
+    static constexpr int kOffKeys = kStages * kStage;
+    static constexpr int kOffValues = kOffKeys + 16 * kSub;
+    static constexpr int kOffWalk = kOffValues + (kValues ? 8 * kSub : 0);
+    static constexpr int kOffMasks = kOffWalk + 48;
+    static constexpr int kBytes = (kOffMasks + 4 * kStages + 63) / 64 * 64;  // places lie at multiples of 64
 
     uint8_t *mem;
-    int32_t ahead;       // the next step's slot, or its page
-    int64_t first;       // slots: of the row's first token; pages: of the table's row
-    int head, len, tok;  // tok: this lane's next token
+    int32_t ahead;         // the next step's slot, or its page
+    int off;               // its tokens' place in the page
+    const int32_t *from;   // the row's slots, or the sequence's pages
+    int head, len;         // of the segment at hand
+    int tok;               // slots, pages: this lane's next token; whole pages: the step's first
+    int left;              // steps of the segment; negative: no more
 
     __device__ __forceinline__ uint8_t *stage(int i) const { return mem + i * kStage; }
-    __device__ __forceinline__ uint2 *turned() const
+    __device__ __forceinline__ float4 *key_scales() const
     {
-        return reinterpret_cast<uint2 *>(mem + kStages * kStage);
+        return reinterpret_cast<float4 *>(mem + kOffKeys);
+    }
+    __device__ __forceinline__ uint2 *value_scales() const
+    {
+        return reinterpret_cast<uint2 *>(mem + kOffValues);
     }
     __device__ __forceinline__ uint32_t *masks() const
     {
-        return reinterpret_cast<uint32_t *>(mem + kStages * kStage + (kValues ? 8 * kSub : 0));
+        return reinterpret_cast<uint32_t *>(mem + kOffMasks);
+    }
+    __device__ __forceinline__ Share *walk() const
+    {
+        return reinterpret_cast<Share *>(mem + kOffWalk);
     }
     __device__ __forceinline__ void look(const Kv4Args &a)
     {
         ahead = -1;
         if (tok < len) {
-            if constexpr (kPaged)
-                ahead = a.table[first + page_of(a.pool.p, tok)];
-            else
-                ahead = a.slots[first + tok];
-        }
-    }
-    // Tokens from tok0 on, every kTile of them.
-    __device__ __forceinline__ void start(const Kv4Args &a, int b, int key_head, int length, int tok0)
-    {
-        head = key_head;
-        len = length;
-        tok = tok0 + lane_id();
-        if constexpr (kPaged)
-            first = b * a.bt_stride;
-        else
-            first = min((int64_t)max(a.indptr[b], 0), a.num_slots);
-        look(a);
-    }
-    __device__ __forceinline__ void fill(const Kv4Args &a, int st)
-    {
-        const int lane = lane_id();
-        int page = ahead, off = 0;
-        bool good = tok < len;
-        if constexpr (kPaged) {
-            off = tok - page_of(a.pool.p, tok) * a.pool.p.page_size;
-        } else if (page >= 0) {
-            const int slot = page;
-            page = page_of(a.pool.p, slot);
-            off = slot - page * a.pool.p.page_size;
-        }
-        if (good && (page < 0 || page >= a.pool.p.num_pages)) {
-            good = false;
-            atomicOr(a.status, kDevBadPage);
-        }
-        tok += kTile;
-        look(a);
-        const uint32_t there = __ballot_sync(0xffffffffu, good);
-        if (lane == 0)
-            masks()[st] = there;
-        const uint32_t to = smem_u32(stage(st));
-        const int64_t at = kv4_codes_at(a.pool, page, head, off);
-        #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = 8 * i + (lane >> 2), c = lane & 3;
-            const int64_t from = __shfl_sync(0xffffffffu, at, row);
-            if (there >> row & 1) {
-                const uint32_t d = to + row * kKv4Codes + 16 * (c ^ (row >> 1 & 3));
-                cp_async16(d, a.pool.p.base + from + 16 * c);
-                if constexpr (kValues)
-                    cp_async16(d + kSubCodes, a.pool.p.base + from + a.pool.side + 16 * c);
+            if constexpr (kPaged) {
+                const int block = page_of(a.pool.p, tok);
+                ahead = from[block];
+                off = tok - block * a.pool.p.page_size;
+            } else {
+                ahead = from[tok];
             }
         }
-        if (good) {
-            const uint8_t *s = a.pool.p.base + kv4_scales_at(a.pool, page, head, off);
-            cp_async4(to + kCodes + 4 * lane, s);
-            if constexpr (kValues)
-                cp_async4(to + kCodes + 4 * (kSub + lane), s + a.pool.scale_side);
+    }
+    // The next segment of the second walk that has a step for this warp.
+    __device__ __forceinline__ void advance(const Kv4Args &a, int heads, int blocks, int warp)
+    {
+        Share s = *walk();
+        Seg g;
+        do {
+            left = -1;
+            if (!next_seg<kPaged>(a, heads, s, g))
+                break;
+            const int tok0 = g.t0 * kTile + warp * kSub;
+            len = (int)min((int64_t)g.t1 * kTile, (int64_t)g.len);
+            left = tok0 < len ? (len - tok0 + kTile - 1) / kTile : 0;
+            tok = tok0 + (kMode == kWholePages ? 0 : lane_id());
+        } while (left == 0);
+        __syncwarp();
+        if (lane_id() == 0)
+            *walk() = s;
+        __syncwarp();
+        if (left < 0)
+            return;
+        head = g.hc / blocks;
+        off = 0;
+        if constexpr (kPaged)
+            from = a.table + g.b * a.bt_stride;
+        else
+            from = a.slots + min((int64_t)max(a.indptr[g.b], 0), a.num_slots);
+        look(a);
+    }
+    __device__ __forceinline__ void start(const Kv4Args &a, const Share &s, int heads, int blocks,
+                                          int warp)
+    {
+        if (lane_id() == 0)
+            *walk() = s;
+        __syncwarp();
+        left = 0;
+        advance(a, heads, blocks, warp);
+    }
+    // One more step into place st, if there is one; a group of copies is committed in any case.
+    __device__ __forceinline__ void fill(const Kv4Args &a, int heads, int blocks, int warp, int st)
+    {
+        if (left == 0)
+            advance(a, heads, blocks, warp);
+        if (left > 0) {
+            --left;
+            copy(a, st);
         }
+        cp_async_commit();
+    }
+    __device__ __forceinline__ void copy(const Kv4Args &a, int st)
+    {
+        const int lane = lane_id();
+        const uint32_t to = smem_u32(mem) + st * kStage;
+        const uint32_t d = to + (lane >> 2) * kKv4Codes + 16 * ((lane & 3) ^ (lane >> 3));
+        int page = ahead, o = off;
+        if constexpr (kMode == kWholePages) {
+            // 32 tokens side by side; those past the context lie in its last page too
+            const int rows = len - tok;
+            tok += kTile;
+            look(a);
+            const bool good = (uint32_t)page < (uint32_t)a.pool.p.num_pages;
+            const uint32_t there = rows >= kSub ? 0xffffffffu : (1u << rows) - 1u;
+            if (lane == 0)
+                masks()[st] = good ? there : 0u;
+            if (good) {
+                const uint8_t *base = a.pool.p.base + (uint64_t)(uint32_t)page * (uint32_t)a.pool.p.stride;
+                const uint32_t token = (uint32_t)head * a.pool.p.page_size + o;
+                const uint8_t *keys = base + (token * kKv4Codes + 16 * lane);
+                #pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    cp_async16(d + i * 8 * kKv4Codes, keys + i * 8 * kKv4Codes);
+                if constexpr (kValues) {
+                    const uint8_t *vals = keys + a.pool.side;
+                    #pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        cp_async16(d + kSubCodes + i * 8 * kKv4Codes, vals + i * 8 * kKv4Codes);
+                }
+                if (lane < (kValues ? 16 : 8))
+                    cp_async16(to + kCodes + 16 * lane,
+                               base + (a.pool.scales + token * kKv4Groups +
+                                       (lane >> 3) * (uint32_t)a.pool.scale_side + 16 * (lane & 7)));
+            } else if (lane == 0) {
+                atomicOr(a.status, kDevBadPage);
+            }
+        } else {
+            bool good = tok < len;
+            if constexpr (!kPaged) {
+                if (page >= 0) {
+                    const int slot = page;
+                    page = page_of(a.pool.p, slot);
+                    o = slot - page * a.pool.p.page_size;
+                }
+            }
+            if (good && (page < 0 || page >= a.pool.p.num_pages)) {
+                good = false;
+                atomicOr(a.status, kDevBadPage);
+            }
+            tok += kTile;
+            look(a);
+            const uint32_t there = __ballot_sync(0xffffffffu, good);
+            if (lane == 0)
+                masks()[st] = there;
+            const int64_t base = (uint64_t)(uint32_t)page * (uint32_t)a.pool.p.stride;
+            const uint32_t token = (uint32_t)head * a.pool.p.page_size + o;
+            const int64_t code = base + token * kKv4Codes;
+            #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 8 * i + (lane >> 2);
+                const uint8_t *keys = a.pool.p.base + __shfl_sync(0xffffffffu, code, row) + 16 * (lane & 3);
+                if (there >> row & 1) {
+                    cp_async16_alone(d + i * 8 * kKv4Codes, keys);
+                    if constexpr (kValues)
+                        cp_async16_alone(d + kSubCodes + i * 8 * kKv4Codes, keys + a.pool.side);
+                }
+            }
+            if (good) {
+                const uint8_t *sc = a.pool.p.base + base + (a.pool.scales + token * kKv4Groups);
+                cp_async4_alone(to + kCodes + 4 * lane, sc);
+                if constexpr (kValues)
+                    cp_async4_alone(to + kCodes + 4 * (kSub + lane), sc + a.pool.scale_side);
+            }
+        }
+    }
+    // The scales of a step's keys in 32 bits, a lane a token (a warp's barrier follows).
+    __device__ __forceinline__ void widen_key_scales(int st) const
+    {
+        float f[4];
+        e8m0_to_float(reinterpret_cast<const uint32_t *>(stage(st) + kCodes)[lane_id()], f);
+        key_scales()[lane_id()] = make_float4(f[0], f[1], f[2], f[3]);
     }
 };
 
 // ------------------------------------------------------------------- queries
 
 // Query fragments of a block of columns, as f16 under a power of two for each
-// column; slc brings scores to units of log2 (columns 2 c, 2 c + 1 of each
-// eight).
+// column: eight columns' in registers, more in shared memory (16 columns on 16
+// registers each of the sums' 64 and the step's own spill).
+template <int NT>
+struct Queries {
+    static constexpr int kBytes = NT == 1 ? 0 : NT * 4 * 512;
+    uint32_t r[NT == 1 ? 4 : 1][4];
+    uint32_t at;  // shared memory: this lane's place
+
+    __device__ __forceinline__ void put(int n, int i, const uint32_t (&v)[4])
+    {
+        if constexpr (NT == 1) {
+            #pragma unroll
+            for (int x = 0; x < 4; ++x)
+                r[i][x] = v[x];
+        } else {
+            st_shared_v4(at + (4 * n + i) * 512, v[0], v[1], v[2], v[3]);
+        }
+    }
+    __device__ __forceinline__ void get(int n, int i, uint32_t (&v)[4]) const
+    {
+        if constexpr (NT == 1) {
+            #pragma unroll
+            for (int x = 0; x < 4; ++x)
+                v[x] = r[i][x];
+        } else {
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                         : "r"(at + (4 * n + i) * 512));
+        }
+    }
+};
+
+// slc brings scores to units of log2 (columns 2 c, 2 c + 1 of each eight).
 template <int NT>
 __device__ __forceinline__ void load_queries(const Kv4Args &a, int b, int key_head, int cb,
-                                             uint32_t (&qf)[NT][4][4], float (&slc)[NT][2])
+                                             Queries<NT> &q, float (&slc)[NT][2])
 {
     const int lane = lane_id(), g = lane >> 2, c = lane & 3;
     #pragma unroll
@@ -437,10 +623,12 @@ __device__ __forceinline__ void load_queries(const Kv4Args &a, int b, int key_he
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+            uint32_t v[4];
             #pragma unroll
             for (int x = 0; x < 4; ++x)
-                qf[n][i][x] = as_u32(__floats2half2_rn(__uint_as_float(w[x] << 16) * f,
-                                                       __uint_as_float(w[x] & 0xffff0000u) * f));
+                v[x] = as_u32(__floats2half2_rn(__uint_as_float(w[x] << 16) * f,
+                                                __uint_as_float(w[x] & 0xffff0000u) * f));
+            q.put(n, i, v);
         }
         #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -451,33 +639,52 @@ __device__ __forceinline__ void load_queries(const Kv4Args &a, int b, int key_he
 // Scores of 32 tokens: s[m][n][0, 1] of token 16 m + g, [2, 3] of the one 8
 // further, columns 2 c and 2 c + 1.
 template <int NT>
-__device__ __forceinline__ void score_tile(const uint8_t *codes, const uint32_t *scales,
-                                           const uint32_t (&qf)[NT][4][4], float (&s)[2][NT][4])
+__device__ __forceinline__ void score_tile(uint32_t codes, uint32_t scales, const Queries<NT> &q,
+                                           float (&s)[2][NT][4])
 {
     const int lane = lane_id(), g = lane >> 2, c = lane & 3;
+    // (pieces of 16 bytes are turned by the row's number: places are multiples of 64)
+    const uint32_t row = codes + g * kKv4Codes + 4 * c + ((g >> 1 & 3) << 4);
+    float sc[2][2][4];  // of the two tiles' rows
     #pragma unroll
-    for (int m = 0; m < 2; ++m) {
-        const uint8_t *row = codes + (16 * m + g) * kKv4Codes + 4 * c;
-        float sa[4], sb[4];
-        e8m0_to_float(scales[16 * m + g], sa);
-        e8m0_to_float(scales[16 * m + g + 8], sb);
+    for (int m = 0; m < 2; ++m)
         #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int at = (i ^ (g >> 1 & 3)) << 4;
+        for (int h = 0; h < 2; ++h) {
+            const float4 v = lds128f(scales + 16 * g + 256 * m + 128 * h);
+            sc[m][h][0] = v.x;
+            sc[m][h][1] = v.y;
+            sc[m][h][2] = v.z;
+            sc[m][h][3] = v.w;
+        }
+    #pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t a0[2][4], a1[2][4];
+        #pragma unroll
+        for (int m = 0; m < 2; ++m) {
             uint32_t ka[4], kb[4];
-            e2m1_to_f16x2(*reinterpret_cast<const uint32_t *>(row + at), ka);
-            e2m1_to_f16x2(*reinterpret_cast<const uint32_t *>(row + 8 * kKv4Codes + at), kb);
-            const uint32_t a0[4] = {ka[0], kb[0], ka[1], kb[1]};
-            const uint32_t a1[4] = {ka[2], kb[2], ka[3], kb[3]};
+            e2m1_to_f16x2(lds32((row ^ (16 * i)) + 16 * m * kKv4Codes), ka);
+            e2m1_to_f16x2(lds32((row ^ (16 * i)) + (16 * m + 8) * kKv4Codes), kb);
             #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float d[4] = {};
-                mma16(d, a0, qf[n][i][0], qf[n][i][1]);
-                mma16(d, a1, qf[n][i][2], qf[n][i][3]);
+            for (int x = 0; x < 2; ++x) {
+                a0[m][2 * x] = ka[x];
+                a0[m][2 * x + 1] = kb[x];
+                a1[m][2 * x] = ka[2 + x];
+                a1[m][2 * x + 1] = kb[2 + x];
+            }
+        }
+        #pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            uint32_t b[4];
+            q.get(n, i, b);
+            #pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float d[4];
+                mma16_first(d, a0[m], b[0], b[1]);
+                mma16(d, a1[m], b[2], b[3]);
                 #pragma unroll
                 for (int x = 0; x < 4; ++x)
-                    s[m][n][x] = i == 0 ? d[x] * (x < 2 ? sa[0] : sb[0])
-                                        : fmaf(d[x], x < 2 ? sa[i] : sb[i], s[m][n][x]);
+                    s[m][n][x] = i == 0 ? d[x] * sc[m][x >> 1][i]
+                                        : fmaf(d[x], sc[m][x >> 1][i], s[m][n][x]);
             }
         }
     }
@@ -507,58 +714,121 @@ __device__ __forceinline__ void mask_tile(float (&s)[2][NT][4], uint32_t there, 
 template <int NT>
 struct Shape {
     static constexpr int kCols = 8 * NT;
-    static constexpr int kStages = NT == 1 ? 3 : 4;
-    static constexpr int kCtas = NT == 1 ? 4 : NT == 2 ? 3 : 2;  // of an SM
+    static constexpr int kStages = NT == 4 ? 5 : 3;
+    // Groups of kWarps warps with shares of their own: an SM has one CTA of as many as
+    // registers and shared memory hold.
+    static constexpr int kGroups = NT == 1 ? 4 : NT == 2 ? 3 : 2;
     static constexpr int kPart = kCols * (kKv4Dim + 2);  // floats of a partial result
-    // the warps' sums where they meet: rows of 128 elements, padded so that a
-    // quad's columns fall into different banks
-    static constexpr int kRow = kKv4Dim + 4;
-    static constexpr int kMeet = kWarps * kCols * (kRow + 2) * 4;
-    template <bool kPaged>
+    template <int kMode>
     static constexpr int smem()
     {
-        const int ring = kWarps * Ring<kPaged, true, kStages>::kBytes;
-        return ring > kMeet ? ring : kMeet;
+        return kGroups * (kWarps * Ring<kMode, true, kStages>::kBytes + 2 * Queries<NT>::kBytes);
     }
 };
 
-template <bool kPaged, int NT>
-__global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
+// A warp's sums: O in absolute units, of element tiles x columns, maxima, sums of
+// the weights.
+template <int NT>
+struct Sums {
+    float o[8][NT][4], m[NT][2], l[NT][2];
+};
+
+// Sums go from one warp to another through the first one's free place, a block of
+// eight columns at a time, with a barrier of the two before and after it is read.
+template <int NT>
+__device__ __forceinline__ void give_sums(const Sums<NT> &s, uint8_t *place, int barrier)
+{
+    const int lane = lane_id();
+    float4 *to = reinterpret_cast<float4 *>(place);
+    #pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        #pragma unroll
+        for (int x = 0; x < 8; ++x)
+            to[32 * x + lane] = make_float4(s.o[x][n][0], s.o[x][n][1], s.o[x][n][2], s.o[x][n][3]);
+        if (lane < 4)  // the columns' maxima and sums are the quads' alike
+            to[256 + lane] = make_float4(s.m[n][0], s.m[n][1], s.l[n][0], s.l[n][1]);
+        named_bar_sync(barrier, 64);
+        named_bar_sync(barrier, 64);  // it was read
+    }
+}
+
+template <int NT, typename Place>
+__device__ __forceinline__ void take_sums(Sums<NT> &s, Place place, int warp, int barrier)
+{
+    const int lane = lane_id();
+    #pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        named_bar_sync(barrier, 64);
+        const float4 *from = reinterpret_cast<const float4 *>(place(warp));
+        const float4 st = from[256 + (lane & 3)];
+        const float m[2] = {st.x, st.y}, l[2] = {st.z, st.w};
+        float mine[2], theirs[2];
+        #pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float top = fmaxf(s.m[n][i], m[i]);
+            mine[i] = ex2(s.m[n][i] - top);
+            theirs[i] = ex2(m[i] - top);
+            s.m[n][i] = top;
+            s.l[n][i] = s.l[n][i] * mine[i] + l[i] * theirs[i];
+        }
+        #pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const float4 v = from[32 * x + lane];
+            const float o[4] = {v.x, v.y, v.z, v.w};
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                s.o[x][n][e] = s.o[x][n][e] * mine[e & 1] + o[e] * theirs[e & 1];
+        }
+        named_bar_sync(barrier, 64);
+    }
+}
+
+template <int kMode, int NT>
+__global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     kv4_attention_kernel(const __grid_constant__ Kv4Args a)
 {
     using S = Shape<NT>;
-    using R = Ring<kPaged, true, S::kStages>;
-    constexpr int kStages = S::kStages, kCols = S::kCols;
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int tid = threadIdx.x, lane = lane_id(), g = lane >> 2, c = lane & 3;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    using R = Ring<kMode, true, S::kStages>;
+    constexpr bool kPaged = kMode != kSlots;
+    constexpr int kStages = S::kStages, kCols = S::kCols, kGroups = S::kGroups;
+    static_assert(R::kStage >= 257 * 16 && R::kStage % 64 == 0, "a place takes sums");
+    static_assert(sizeof(Share) <= 48, "the second walk's place");
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ volatile int places[kGroups * kWarps];  // the warps' free places, where they give sums
+    const int lane = lane_id(), g = lane >> 2, c = lane & 3;
+    const int all_warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
+    const int group = all_warp / kWarps, warp = all_warp % kWarps;  // of the group
+    const int p = group * gridDim.x + blockIdx.x;                   // the group's share
     pdl_wait();
     pdl_launch_dependents();
     const int heads = a.pool.heads * a.blocks;
     const int64_t limit = kPaged || a.uncut ? INT64_MAX / INT_MAX : a.num_slots / kTile + a.B;
-    if (tid == 0 && !a.uncut)
-        a.ws_cut[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (warp == 0 && lane == 0 && !a.uncut)
+        a.ws_cut[p] = make_int4(0, 0, 0, 0);
     Share share;
-    if (!find_share<kPaged>(a, heads, limit, share))
-        return;
+    find_share<kPaged, kGroups>(a, heads, limit, share);
     R ring;
-    ring.mem = smem + warp * R::kBytes;
+    ring.mem = smem + all_warp * R::kBytes;
+    ring.start(a, share, heads, a.blocks, warp);
+    #pragma unroll
+    for (int i = 0; i < kStages - 1; ++i)
+        ring.fill(a, heads, a.blocks, warp, i);
+    int st = 0;            // the next place to read
+    int spare = kStages - 1;  // the free one
     Seg seg;
     for (int nth = 0; next_seg<kPaged>(a, heads, share, seg); ++nth) {
         const int head = seg.hc / a.blocks, cb = seg.hc - head * a.blocks;
         const int tok0 = seg.t0 * kTile + warp * kSub;
         const int upto = (int)min((int64_t)seg.t1 * kTile, (int64_t)seg.len);
         const int steps = tok0 < upto ? (upto - tok0 + kTile - 1) / kTile : 0;
-        ring.start(a, seg.b, head, upto, tok0);
-        #pragma unroll
-        for (int i = 0; i < kStages - 1; ++i) {
-            if (i < steps)
-                ring.fill(a, i);
-            cp_async_commit();
-        }
-        uint32_t qf[NT][4][4];
+        // A group's warps write the same fragments.  They are a segment apart at most: by turns
+        // into two places.
+        Queries<NT> qf;
+        qf.at = smem_u32(smem) + kGroups * kWarps * R::kBytes +
+                (2 * group + (nth & 1)) * Queries<NT>::kBytes + 16 * lane;
         float slc[NT][2];
         load_queries<NT>(a, seg.b, head, cb, qf, slc);
+        __syncwarp();
         int end[NT][2], least = INT_MAX;
         #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -571,34 +841,92 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
             }
         least = __reduce_min_sync(0xffffffffu, least);
 
-        float o[8][NT][4] = {};  // element tiles: rows 32 (t / 2) + 4 g + 2 (t % 2) and the next
-        float m[NT][2], l[NT][2];
+        Sums<NT> sum;
+        // element tiles: rows 32 (t / 2) + 4 g + 2 (t % 2) and the next
+        auto &o = sum.o;
+        auto &m = sum.m;
+        auto &l = sum.l;
         #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NT; ++n) {
+            #pragma unroll
+            for (int x = 0; x < 8; ++x)
+                #pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    o[x][n][i] = 0.0f;
             #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 m[n][i] = -FLT_MAX;
                 l[n][i] = 0.0f;
             }
+        }
         uint32_t top_e = 0;  // the largest exponents, a byte a group
-        int st = 0;
         #pragma unroll 1
         for (int k = 0; k < steps; ++k) {
             cp_async_wait<kStages - 2>();
             __syncwarp();
-            {
-                const int to = st == 0 ? kStages - 1 : st - 1;
-                if (k + kStages - 1 < steps)
-                    ring.fill(a, to);
-                cp_async_commit();
-            }
+            ring.fill(a, heads, a.blocks, warp, spare);
+            ring.widen_key_scales(st);
             const uint8_t *mem = ring.stage(st);
-            const uint32_t *scales = reinterpret_cast<const uint32_t *>(mem + R::kCodes);
+            const uint32_t *scales = reinterpret_cast<const uint32_t *>(mem + R::kCodes) + kSub;
             const uint32_t there = ring.masks()[st];
             const int tok = tok0 + k * kTile;
+            spare = st;
             st = st + 1 == kStages ? 0 : st + 1;
+
+            // ---- exponents of the values: a lane a token, two groups a word (0 and 2, 1 and 3)
+            const bool here = there >> lane & 1;
+            const uint32_t word = here ? scales[lane] : top_e;
+            uint32_t under[2];  // the tops less them
+            const auto in_range = [&](uint32_t w) {
+                // 256 + top - e: bit 8 is clear where e is over the top
+                under[0] = (top_e & 0x00ff00ffu) + 0x01000100u - (w & 0x00ff00ffu);
+                under[1] = (top_e >> 8 & 0x00ff00ffu) + 0x01000100u - (w >> 8 & 0x00ff00ffu);
+                constexpr uint32_t over = 0x00010001u * (255 - kScaleRange);
+                const bool good = (((under[0] & under[1]) & 0x01000100u) == 0x01000100u) &
+                                  (((under[0] + over) | (under[1] + over)) & 0x02000200u) == 0;
+                under[0] -= 0x01000100u;
+                under[1] -= 0x01000100u;
+                return good;
+            };
+            bool fast = __all_sync(0xffffffffu, in_range(word));
+            if (!fast) {
+                // raise the tops over this step's (one more, so that the next need not), NaN apart
+                uint32_t t = here ? word & ~__vcmpeq4(word, 0xffffffffu) : 0u;
+                #pragma unroll
+                for (int x = 16; x > 0; x >>= 1)
+                    t = __vmaxu4(t, __shfl_xor_sync(0xffffffffu, t, x));
+                uint32_t next = 0;
+                #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int was = top_e >> (8 * i) & 255, now = t >> (8 * i) & 255;
+                    const int e = now > was ? min(now + 1, 254) : was;
+                    next |= (uint32_t)e << (8 * i);
+                    const float f = pow2i(was - e);
+                    #pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        #pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            o[2 * i][n][x] *= f;
+                            o[2 * i + 1][n][x] *= f;
+                        }
+                }
+                top_e = next;
+                fast = __all_sync(0xffffffffu, in_range(here ? word : top_e));
+            }
+            {
+                // the token's scales as f16, 2^(e - top + 5) by their exponent bits; two lanes
+                // change halves, so that pairs of tokens lie together
+                const uint32_t f0 = 0x00010001u * ((15 + kScaleUp) << 10) - (under[0] << 10);
+                const uint32_t f1 = 0x00010001u * ((15 + kScaleUp) << 10) - (under[1] << 10);
+                const bool odd = lane & 1;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? f0 : f1, 1);
+                const uint32_t x = odd ? got : f0, y = odd ? f1 : got;
+                ring.value_scales()[lane] = make_uint2(__byte_perm(x, y, 0x5410), __byte_perm(x, y, 0x7632));
+            }
+            __syncwarp();
+
             float s[2][NT][4];
-            score_tile<NT>(mem, scales, qf, s);
+            score_tile<NT>(smem_u32(mem), smem_u32(ring.key_scales()), qf, s);
             if (there != 0xffffffffu || tok + kSub > least)
                 mask_tile<NT>(s, there, tok, end);
 
@@ -647,57 +975,15 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
                     }
                 }
 
-            // ---- exponents of the values: a lane a token
-            const bool here = there >> lane & 1;
-            const uint32_t word = here ? scales[kSub + lane] : top_e;
-            const auto in_range = [&] {
-                // top - word bytewise, at most kScaleRange (and nothing over the top)
-                const uint32_t d = top_e - word;
-                const bool low = ((((d & 0x7f7f7f7fu) + 0x01010101u * (127 - kScaleRange)) | d) &
-                                  0x80808080u) == 0;
-                return __vmaxu4(word, top_e) == top_e && low;
-            };
-            bool fast = __all_sync(0xffffffffu, in_range());
-            if (!fast) {
-                // raise the tops over this tile's (one more, so that the next need not), NaN apart
-                uint32_t t = here ? word & ~__vcmpeq4(word, 0xffffffffu) : 0u;
-                #pragma unroll
-                for (int x = 16; x > 0; x >>= 1)
-                    t = __vmaxu4(t, __shfl_xor_sync(0xffffffffu, t, x));
-                uint32_t next = 0;
-                #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int was = top_e >> (8 * i) & 255, now = t >> (8 * i) & 255;
-                    const int e = now > was ? min(now + 1, 254) : was;
-                    next |= (uint32_t)e << (8 * i);
-                    const float f = pow2i(was - e);
-                    #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        #pragma unroll
-                        for (int x = 0; x < 4; ++x) {
-                            o[2 * i][n][x] *= f;
-                            o[2 * i + 1][n][x] *= f;
-                        }
-                }
-                const bool was_there = here;
-                top_e = next;
-                const uint32_t d = top_e - (was_there ? word : top_e);
-                const uint32_t w = was_there ? word : top_e;
-                const bool low = ((((d & 0x7f7f7f7fu) + 0x01010101u * (127 - kScaleRange)) | d) &
-                                  0x80808080u) == 0;
-                fast = __all_sync(0xffffffffu, __vmaxu4(w, top_e) == top_e && low);
-            }
-            const uint8_t *val = mem + kSubCodes;
             // element pairs of groups 2 y and 2 y + 1 of four tokens, widened: rows of the
             // products' left side, two tiles a group
+            const uint32_t val = smem_u32(mem) + kSubCodes + 2 * c * kKv4Codes + 2 * g + (c << 4);
             const auto widen = [&](int h, int y, uint32_t (&w)[4][4]) {
                 uint32_t r[4];
                 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint8_t *at = val + (16 * h + 2 * c + (i & 1) + 8 * (i >> 1)) * kKv4Codes + 2 * g;
-                    const uint32_t u0 = *reinterpret_cast<const uint16_t *>(at + (((2 * y) ^ c) << 4));
-                    const uint32_t u1 = *reinterpret_cast<const uint16_t *>(at + (((2 * y + 1) ^ c) << 4));
-                    r[i] = __byte_perm(u0, u1, 0x5410);
+                    const int at = (16 * h + (i & 1) + 8 * (i >> 1)) * kKv4Codes;
+                    r[i] = __byte_perm(lds16((val ^ (32 * y)) + at), lds16((val ^ (32 * y + 16)) + at), 0x5410);
                 }
                 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -714,12 +1000,6 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
                 }
             };
             if (fast) {
-                // a lane its token's scales as f16, 2^(e - top + 5) by their exponent bits:
-                // groups 0 and 2, then 1 and 3
-                const uint32_t w = here ? word : top_e;
-                const uint32_t f = (0x01010101u * (15 + kScaleUp) - (top_e - w)) << 2;
-                ring.turned()[lane] = make_uint2((f & 0x00ff00ffu) << 8, f & 0xff00ff00u);
-                __syncwarp();
                 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint32_t p[NT][2];
@@ -728,28 +1008,26 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
                         #pragma unroll
                         for (int i = 0; i < 2; ++i)
                             p[n][i] = turn8(as_u32(__floats2half2_rn(s[h][n][2 * i], s[h][n][2 * i + 1])));
-                    const uint4 e0 = *reinterpret_cast<const uint4 *>(ring.turned() + 16 * h + 2 * c);
-                    const uint4 e1 = *reinterpret_cast<const uint4 *>(ring.turned() + 16 * h + 2 * c + 8);
+                    // groups 0, 2, 1, 3 of tokens 2 c, 2 c + 1 and of those 8 further
+                    const uint4 e0 = *reinterpret_cast<const uint4 *>(ring.value_scales() + 16 * h + 2 * c);
+                    const uint4 e1 = *reinterpret_cast<const uint4 *>(ring.value_scales() + 16 * h + 2 * c + 8);
+                    const uint32_t fa[4] = {e0.x, e0.z, e0.y, e0.w}, fb[4] = {e1.x, e1.z, e1.y, e1.w};
                     #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         uint32_t v[4][4];
                         widen(h, y, v);
                         #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            // group 2 y + i of tokens 2 c, 2 c + 1 and of those 8 further
-                            const uint32_t f0 = __byte_perm(i ? e0.y : e0.x, i ? e0.w : e0.z, y ? 0x7632 : 0x5410);
-                            const uint32_t f1 = __byte_perm(i ? e1.y : e1.x, i ? e1.w : e1.z, y ? 0x7632 : 0x5410);
                             #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                const uint32_t b0 = as_u32(__hmul2(as_h2(p[n][0]), as_h2(f0)));
-                                const uint32_t b1 = as_u32(__hmul2(as_h2(p[n][1]), as_h2(f1)));
+                                const uint32_t b0 = as_u32(__hmul2(as_h2(p[n][0]), as_h2(fa[2 * y + i])));
+                                const uint32_t b1 = as_u32(__hmul2(as_h2(p[n][1]), as_h2(fb[2 * y + i])));
                                 mma16(o[4 * y + 2 * i][n], v[2 * i], b0, b1);
                                 mma16(o[4 * y + 2 * i + 1][n], v[2 * i + 1], b0, b1);
                             }
                         }
                     }
                 }
-                __syncwarp();
             } else {
                 // weights and scales in bf16; a column that does not see a token has no part
                 // in a scale that is not finite
@@ -788,7 +1066,7 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
                             #pragma unroll
                             for (int x = 0; x < 4; ++x) {
                                 const int r = 16 * h + 2 * c + (x & 1) + 8 * (x >> 1);
-                                const int e = scales[kSub + r] >> (8 * grp) & 255;
+                                const int e = scales[r] >> (8 * grp) & 255;
                                 const int d = e - (int)(top_e >> (8 * grp) & 255) + kScaleUp;
                                 f[x] = e == 255 ? NAN : pow2i(d);
                             }
@@ -810,22 +1088,17 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
                 }
             }
         }
-        cp_async_wait<0>();
-        __syncthreads();  // the rings are read
-
-        // ---- the warps meet
-        float *sums = reinterpret_cast<float *>(smem) + warp * kCols * S::kRow;
-        float *stat = reinterpret_cast<float *>(smem) + kWarps * kCols * S::kRow;  // [warp][m, l][col]
+        // ---- the warps' sums, in absolute units, from 1 to 0 and 3 to 2, then 2 to 0
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const float f = pow2i((int)(top_e >> (8 * i) & 255) - 127 - kScaleUp - kBias);
             #pragma unroll
             for (int n = 0; n < NT; ++n)
                 #pragma unroll
-                for (int x = 0; x < 2; ++x)
-                    *reinterpret_cast<float4 *>(sums + (8 * n + 2 * c + x) * S::kRow + 32 * i + 4 * g) =
-                        make_float4(o[2 * i][n][x] * f, o[2 * i][n][x + 2] * f, o[2 * i + 1][n][x] * f,
-                                    o[2 * i + 1][n][x + 2] * f);
+                for (int x = 0; x < 4; ++x) {
+                    o[2 * i][n][x] *= f;
+                    o[2 * i + 1][n][x] *= f;
+                }
         }
         #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -835,95 +1108,119 @@ __global__ void __launch_bounds__(kThreads, Shape<NT>::kCtas)
                 t += __shfl_xor_sync(0xffffffffu, t, 4);
                 t += __shfl_xor_sync(0xffffffffu, t, 8);
                 t += __shfl_xor_sync(0xffffffffu, t, 16);
-                if (g == 0) {
-                    stat[(2 * warp) * kCols + 8 * n + 2 * c + i] = m[n][i];
-                    stat[(2 * warp + 1) * kCols + 8 * n + 2 * c + i] = t * pow2i(-kBias);
-                }
+                l[n][i] = t * pow2i(-kBias);
             }
-        __syncthreads();
+        __syncwarp();  // the last step's place is read, and free
+        if (warp > 0 && lane == 0)
+            places[all_warp] = spare;
+        if (warp & 1) {
+            give_sums<NT>(sum, ring.stage(spare), 3 * group + 1 + (warp >> 1));
+            continue;
+        }
+        // (a place's number is written before the barrier that tells of it)
+        const auto place = [&](int w) {
+            return smem + w * R::kBytes + places[w] * R::kStage;
+        };
+        take_sums<NT>(sum, place, all_warp + 1, 3 * group + 1 + (warp >> 1));
+        if (warp == 2) {
+            give_sums<NT>(sum, ring.stage(spare), 3 * group + 3);
+            continue;
+        }
+        take_sums<NT>(sum, place, all_warp + 2, 3 * group + 3);
+
+        // ---- warp 0 has the segment's
         const bool part = seg.t0 > 0 || seg.t1 < seg.tiles;
-        float *to = a.ws_part + (int64_t)(2 * blockIdx.x + (nth > 0)) * S::kPart;
-        if (part && seg.t0 == 0 && tid == 0) {
+        float *to = a.ws_part + (int64_t)(2 * p + (nth > 0)) * S::kPart;
+        if (part && seg.t0 == 0 && lane == 0) {
             // the shares that hold the rest: `more - p - 1` longer ones first
-            const int64_t longer = max(0, share.more - (int)blockIdx.x - 1);
+            const int64_t longer = max(0, share.more - p - 1);
             const int rest = seg.tiles - seg.t1;
             const int in = (int)min((int64_t)rest, longer * (share.each + 1));
-            a.ws_cut[blockIdx.x] = make_int4(
+            a.ws_cut[p] = make_int4(
                 seg.b, seg.hc, 1 + (in + share.each) / (share.each + 1) +
                                    (rest - in + share.each - 1) / share.each, nth > 0);
         }
-        const float *all = reinterpret_cast<const float *>(smem);
-        #pragma unroll 1
-        for (int col = 0; col < min(kCols, a.cols - cb * kCols); ++col) {
-            float mw[kWarps], top = -FLT_MAX, sum = 0.0f, acc = 0.0f;
+        #pragma unroll
+        for (int n = 0; n < NT; ++n)
             #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                mw[w] = stat[2 * w * kCols + col];
-                top = fmaxf(top, mw[w]);
-            }
-            #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2(mw[w] - top);
-                sum = fmaf(f, stat[(2 * w + 1) * kCols + col], sum);
-                acc = fmaf(f, all[(w * kCols + col) * S::kRow + tid], acc);
-            }
-            if (part) {
-                to[col * kKv4Dim + tid] = acc;
-                if (tid == 0) {
-                    to[kCols * kKv4Dim + col] = top;
-                    to[kCols * kKv4Dim + kCols + col] = sum;
+            for (int i = 0; i < 2; ++i) {
+                const int col = n * 8 + 2 * c + i, at = cb * kCols + col;
+                if (at >= a.cols)
+                    continue;
+                const float all = l[n][i];
+                if (part) {
+                    #pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        *reinterpret_cast<float4 *>(to + col * kKv4Dim + 32 * y + 4 * g) =
+                            make_float4(o[2 * y][n][i], o[2 * y][n][i + 2], o[2 * y + 1][n][i],
+                                        o[2 * y + 1][n][i + 2]);
+                    if (g == 0) {
+                        to[kCols * kKv4Dim + col] = m[n][i];
+                        to[kCols * kKv4Dim + kCols + col] = all;
+                    }
+                } else {
+                    const int j = at / a.group, h = head * a.group + at - j * a.group;
+                    const int64_t row = (int64_t)seg.b * a.next_n + j;
+                    const float inv = all == 0.0f ? 0.0f : 1.0f / all;
+                    uint16_t *out = a.out + row * a.ldo_row + h * a.ldo_head + 4 * g;
+                    #pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        *reinterpret_cast<uint2 *>(out + 32 * y) = make_uint2(
+                            as_u32(__floats2bfloat162_rn(o[2 * y][n][i] * inv, o[2 * y][n][i + 2] * inv)),
+                            as_u32(__floats2bfloat162_rn(o[2 * y + 1][n][i] * inv,
+                                                         o[2 * y + 1][n][i + 2] * inv)));
+                    if (a.lse && g == 0)
+                        a.lse[row * a.ld_lse + h] =
+                            all == 0.0f ? -INFINITY : (m[n][i] + log2f(all)) * kLn2;
                 }
-            } else {
-                const int at = cb * kCols + col, j = at / a.group;
-                const int64_t row = (int64_t)seg.b * a.next_n + j;
-                const int h = head * a.group + at - j * a.group;
-                const float v = sum == 0.0f ? 0.0f : acc / sum;
-                reinterpret_cast<__nv_bfloat16 *>(a.out)[row * a.ldo_row + h * a.ldo_head + tid] =
-                    __float2bfloat16_rn(v);
-                if (a.lse && tid == 0)
-                    a.lse[row * a.ld_lse + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
             }
-        }
-        __syncthreads();  // before the rings fill again
     }
+    cp_async_wait<0>();
 }
 
 // Joins the pieces of a unit that several shares hold: blockIdx.x is the share
-// that begins it, blockIdx.y the column.  A warp a piece, four in flight.
-__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, int kCols)
+// that begins it.  A block's warps take a column each, or all of them one column
+// and every eighth piece; four pieces in flight a warp.
+__global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, int kCols, int together)
 {
     constexpr int kTeams = kJoinThreads / 32;
     __shared__ float4 meet[kTeams][32];
     __shared__ float meet_sum[kTeams], meet_top[kTeams];
+    const int warp = threadIdx.x >> 5, lane = lane_id();
+    const int team = together ? warp : 0, teams = together ? kTeams : 1;
+    const int col = together ? blockIdx.y : blockIdx.y * kTeams + warp;
     pdl_wait();
     pdl_launch_dependents();
     const int4 cut = a.ws_cut[blockIdx.x];
-    const int pieces = cut.z, col = blockIdx.y;
+    const int pieces = cut.z;
+    if (pieces < 2)
+        return;
     const int head = cut.y / a.blocks, cb = cut.y - head * a.blocks;
     const int at = cb * kCols + col;
-    if (pieces < 2 || at >= a.cols)
+    if (col >= kCols || at >= a.cols)
         return;
-    const int team = threadIdx.x >> 5, lane = lane_id();
     const int64_t step = 2 * (int64_t)kCols * (kKv4Dim + 2);
     const float *rest = a.ws_part + blockIdx.x * step;
     const float *first = rest + cut.w * (step / 2);
     const int stat = kCols * kKv4Dim + col;
     float top = -FLT_MAX;
-    for (int i = threadIdx.x; i < pieces; i += kJoinThreads)
+    for (int i = 32 * team + lane; i < pieces; i += 32 * teams)
         top = fmaxf(top, (i == 0 ? first : rest + i * step)[stat]);
     #pragma unroll
     for (int x = 16; x > 0; x >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (lane == 0)
-        meet_top[team] = top;
-    __syncthreads();
-    #pragma unroll
-    for (int i = 0; i < kTeams; ++i)
-        top = fmaxf(top, meet_top[i]);
+    if (together) {
+        if (lane == 0)
+            meet_top[team] = top;
+        __syncthreads();
+        #pragma unroll
+        for (int i = 0; i < kTeams; ++i)
+            top = fmaxf(top, meet_top[i]);
+    }
     float sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     #pragma unroll 4
-    for (int i = team; i < pieces; i += kTeams) {
+    for (int i = team; i < pieces; i += teams) {
         const float *f = i == 0 ? first : rest + i * step;
         const float w = ex2(f[stat] - top);
         const float4 v = *reinterpret_cast<const float4 *>(f + col * kKv4Dim + 4 * lane);
@@ -933,20 +1230,22 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
         acc.z = fmaf(w, v.z, acc.z);
         acc.w = fmaf(w, v.w, acc.w);
     }
-    meet[team][lane] = acc;
-    if (lane == 0)
-        meet_sum[team] = sum;
-    __syncthreads();
-    if (team > 0)
-        return;
-    #pragma unroll
-    for (int i = 1; i < kTeams; ++i) {
-        const float4 v = meet[i][lane];
-        acc.x += v.x;
-        acc.y += v.y;
-        acc.z += v.z;
-        acc.w += v.w;
-        sum += meet_sum[i];
+    if (together) {
+        meet[team][lane] = acc;
+        if (lane == 0)
+            meet_sum[team] = sum;
+        __syncthreads();
+        if (team > 0)
+            return;
+        #pragma unroll
+        for (int i = 1; i < kTeams; ++i) {
+            const float4 v = meet[i][lane];
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+            sum += meet_sum[i];
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int j = at / a.group, h = head * a.group + at - j * a.group;
@@ -964,22 +1263,35 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
 // Half the cache's bytes, and 8 of the weights.  Where there are more columns than a
 // block, a segment is walked for each and the same lane adds to what it wrote.
 template <int NT>
-__global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4)
+struct WeightShape {
+    static constexpr int kStages = 4;
+    static constexpr int kGroups = NT == 4 ? 3 : 4;
+    template <int kMode>
+    static constexpr int smem()
+    {
+        return kGroups * kWarps * (Ring<kMode, false, kStages>::kBytes + Queries<NT>::kBytes);
+    }
+};
+
+template <int kMode, int NT>
+__global__ void __launch_bounds__(WeightShape<NT>::kGroups * kThreads, 1)
     kv4_weights_kernel(const __grid_constant__ Kv4Args a)
 {
-    constexpr int kStages = 4, kCols = 8 * NT;
-    using R = Ring<true, false, kStages>;
-    __shared__ __align__(16) uint8_t smem[kWarps * R::kBytes];
-    const int tid = threadIdx.x, lane = lane_id(), c = lane & 3;
-    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    constexpr int kStages = WeightShape<NT>::kStages, kGroups = WeightShape<NT>::kGroups;
+    constexpr int kCols = 8 * NT;
+    using R = Ring<kMode, false, kStages>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = lane_id(), c = lane & 3;
+    const int all_warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), warp = all_warp % kWarps;
     pdl_wait();
     pdl_launch_dependents();
     const int heads = a.pool.heads;
     Share share;
-    share.left = 0;
-    find_share<true>(a, heads, INT64_MAX / INT_MAX, share);
+    find_share<true, kGroups>(a, heads, INT64_MAX / INT_MAX, share);
     R ring;
-    ring.mem = smem + warp * R::kBytes;
+    ring.mem = smem + all_warp * R::kBytes;
+    Queries<NT> qf;
+    qf.at = smem_u32(smem) + kGroups * kWarps * R::kBytes + all_warp * Queries<NT>::kBytes + 16 * lane;
     Seg seg;
     while (next_seg<true>(a, heads, share, seg)) {
         const int head = seg.hc;
@@ -988,18 +1300,17 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4)
         const int steps = tok0 < upto ? (upto - tok0 + kTile - 1) / kTile : 0;
         const float *mass = a.mass ? a.mass + seg.b * a.ld_batch + head * a.ld_head : nullptr;
         float *out = a.mass_out + seg.b * a.ldo_batch + head * a.ldo_mass_head;
+        // a walk of this segment alone
+        Share one = {seg.b, seg.hc, seg.tiles, seg.len, seg.t0, seg.t1 - seg.t0, 0, 0};
         #pragma unroll 1
         for (int cb = 0; cb < a.blocks; ++cb) {
-            ring.start(a, seg.b, head, upto, tok0);
+            ring.start(a, one, heads, 1, warp);
             #pragma unroll
-            for (int i = 0; i < kStages - 1; ++i) {
-                if (i < steps)
-                    ring.fill(a, i);
-                cp_async_commit();
-            }
-            uint32_t qf[NT][4][4];
+            for (int i = 0; i < kStages - 1; ++i)
+                ring.fill(a, heads, 1, warp, i);
             float slc[NT][2], z[NT][2];
             load_queries<NT>(a, seg.b, head, cb, qf, slc);
+            __syncwarp();
             int end[NT][2], least = INT_MAX;
             #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -1017,32 +1328,27 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4)
                     }
                 }
             least = __reduce_min_sync(0xffffffffu, least);
+            // this lane's token of a step's sums: 16 (c / 2) + 8 (c % 2) + g; what it adds to
+            // comes a step ahead
+            int mine = tok0 + 16 * (c >> 1) + 8 * (c & 1) + (lane >> 2);
+            const float *base = cb > 0 ? out : mass;
+            float next = base && mine < upto ? base[mine] : 0.0f;
             int st = 0;
             #pragma unroll 1
-            for (int k = 0; k < steps; ++k) {
+            for (int k = 0; k < steps; ++k, mine += kTile) {
+                const float before = next;
+                next = base && mine < upto - kTile ? base[mine + kTile] : 0.0f;
                 cp_async_wait<kStages - 2>();
                 __syncwarp();
-                {
-                    const int to = st == 0 ? kStages - 1 : st - 1;
-                    if (k + kStages - 1 < steps)
-                        ring.fill(a, to);
-                    cp_async_commit();
-                }
-                // this lane's token of the sums: 16 (c / 2) + 8 (c % 2) + g
+                ring.fill(a, heads, 1, warp, st == 0 ? kStages - 1 : st - 1);
+                ring.widen_key_scales(st);
                 const int tok = tok0 + k * kTile;
-                const int mine = tok + 16 * (c >> 1) + 8 * (c & 1) + (lane >> 2);
-                float before = 0.0f;
-                if (mine < upto) {
-                    if (cb > 0)
-                        before = out[mine];
-                    else if (mass)
-                        before = mass[mine];
-                }
                 const uint8_t *mem = ring.stage(st);
                 const uint32_t there = ring.masks()[st];
                 st = st + 1 == kStages ? 0 : st + 1;
+                __syncwarp();
                 float s[2][NT][4];
-                score_tile<NT>(mem, reinterpret_cast<const uint32_t *>(mem + R::kCodes), qf, s);
+                score_tile<NT>(smem_u32(mem), smem_u32(ring.key_scales()), qf, s);
                 if (there != 0xffffffffu || tok + kSub > least)
                     mask_tile<NT>(s, there, tok, end);
                 float v[4] = {};
@@ -1070,19 +1376,31 @@ __global__ void __launch_bounds__(kThreads, NT == 4 ? 3 : 4)
             __syncwarp();
         }
     }
-    // ---- columns past the contexts
+    // ---- columns past the contexts, sixteen a lane at once
     if (a.mass == a.mass_out)
         return;
-    constexpr int kChunk = 8 * kThreads;
+    constexpr int kEach = 16, kChunk = 32 * kEach;
     const int chunks = (a.width + kChunk - 1) / kChunk;
-    for (int64_t i = blockIdx.x; i < (int64_t)a.B * heads * chunks; i += gridDim.x) {
+    const int64_t all = (int64_t)a.B * heads * chunks, step = (int64_t)gridDim.x * kGroups * kWarps;
+    for (int64_t i = (int64_t)blockIdx.x * kGroups * kWarps + all_warp; i < all; i += step) {
         const int bh = (int)(i / chunks), at = (int)(i - (int64_t)bh * chunks) * kChunk;
-        const int b = bh / heads, head = bh - b * heads;
-        const int from = max(at, unit_len<true>(a, b)), to = min((int64_t)at + kChunk, (int64_t)a.width);
+        const int b = bh / heads, head = bh - b * heads, len = unit_len<true>(a, b);
+        if (at + kChunk <= len)
+            continue;
         const float *mass = a.mass ? a.mass + b * a.ld_batch + head * a.ld_head : nullptr;
         float *out = a.mass_out + b * a.ldo_batch + head * a.ldo_mass_head;
-        for (int t = from + tid; t < to; t += kThreads)
-            out[t] = mass ? mass[t] : 0.0f;
+        float v[kEach];
+        #pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+            const int t = at + 32 * x + lane;
+            v[x] = mass && t >= len && t < a.width ? mass[t] : 0.0f;
+        }
+        #pragma unroll
+        for (int x = 0; x < kEach; ++x) {
+            const int t = at + 32 * x + lane;
+            if (t >= len && t < a.width)
+                out[t] = v[x];
+        }
     }
 }
 
@@ -1094,9 +1412,9 @@ int tiles_of(int cols)
     return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
 }
 
-int ctas_of(int nt)
+int groups_of(int nt)
 {
-    return nt == 1 ? Shape<1>::kCtas : nt == 2 ? Shape<2>::kCtas : Shape<4>::kCtas;
+    return nt == 1 ? Shape<1>::kGroups : nt == 2 ? Shape<2>::kGroups : Shape<4>::kGroups;
 }
 
 int part_of(int nt)
@@ -1109,27 +1427,56 @@ size_t cut_bytes(int shares)
     return ((size_t)shares * sizeof(int4) + 255) / 256 * 256;
 }
 
-template <bool kPaged, int NT>
-idx_status launch_attention(const Kv4Args &a, int shares, cudaStream_t stream)
+// A kernel's shared memory is raised once a device.
+template <typename F>
+bool raise_smem(F kernel, int smem, std::atomic<uint64_t> &ready)
 {
-    constexpr int smem = Shape<NT>::template smem<kPaged>();
-    static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
-        return IDX_ERR_CUDA;
+        return false;
     const uint64_t bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_relaxed) & bit)) {
-        if (cudaFuncSetAttribute(kv4_attention_kernel<kPaged, NT>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-            return IDX_ERR_CUDA;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return false;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    cudaError_t e = launch_pdl(kv4_attention_kernel<kPaged, NT>, dim3(shares), dim3(kThreads), smem,
-                               stream, a);
-    if (e == cudaSuccess && shares > 1 && !a.uncut)
-        e = launch_pdl(kv4_join_kernel, dim3(shares - 1, std::min(a.cols, 8 * NT)),
-                       dim3(kJoinThreads), 0, stream, a, 8 * NT);
+    return true;
+}
+
+template <int kMode, int NT>
+idx_status launch_attention(const Kv4Args &a, int64_t tiles, cudaStream_t stream)
+{
+    const int ctas = (int)std::min<int64_t>(sm_count(), tiles);
+    const int shares = ctas * Shape<NT>::kGroups;
+    constexpr int smem = Shape<NT>::template smem<kMode>();
+    static_assert(smem <= 226 * 1024, "shared memory of a CTA");
+    static std::atomic<uint64_t> ready{0};
+    if (!raise_smem(kv4_attention_kernel<kMode, NT>, smem, ready))
+        return IDX_ERR_CUDA;
+    cudaError_t e = launch_pdl(kv4_attention_kernel<kMode, NT>, dim3(ctas),
+                               dim3(Shape<NT>::kGroups * kThreads), smem, stream, a);
+    if (e == cudaSuccess && !a.uncut) {
+        // many pieces of few units: a block's warps share a column's
+        const int cols = std::min(a.cols, 8 * NT), warps = kJoinThreads / 32;
+        const int together = (int64_t)a.B * a.pool.heads * a.blocks * kJoinFew < shares;
+        e = launch_pdl(kv4_join_kernel, dim3(shares - 1, together ? cols : (cols + warps - 1) / warps),
+                       dim3(kJoinThreads), 0, stream, a, 8 * NT, together);
+    }
     return launch_status(e);
+}
+
+template <int kMode, int NT>
+idx_status launch_weights(const Kv4Args &a, int64_t tiles, cudaStream_t stream)
+{
+    constexpr int smem = WeightShape<NT>::template smem<kMode>();
+    static_assert(smem <= 226 * 1024, "shared memory of a CTA");
+    static std::atomic<uint64_t> ready{0};
+    if (!raise_smem(kv4_weights_kernel<kMode, NT>, smem, ready))
+        return IDX_ERR_CUDA;
+    return launch_status(launch_pdl(kv4_weights_kernel<kMode, NT>,
+                                    dim3((int)std::min<int64_t>(sm_count(), tiles)),
+                                    dim3(WeightShape<NT>::kGroups * kThreads), smem, stream, a));
 }
 
 // Checks that the calls share; keys: of a row at most.
@@ -1143,7 +1490,15 @@ idx_status check_attention(const void *q, int64_t ldq_row, int64_t ldq_head, int
     return IDX_OK;
 }
 
-// Fills in what a launch needs and launches; rows: of all sequences.
+template <int kMode>
+idx_status launch_columns(const Kv4Args &a, int nt, int64_t tiles, cudaStream_t s)
+{
+    return nt == 1 ? launch_attention<kMode, 1>(a, tiles, s)
+         : nt == 2 ? launch_attention<kMode, 2>(a, tiles, s)
+                   : launch_attention<kMode, 4>(a, tiles, s);
+}
+
+// Fills in what a launch needs and launches.
 template <bool kPaged>
 idx_status run_attention(Kv4Args &a, int64_t keys, int64_t most_tiles, void *ws, size_t ws_bytes,
                          int H, idx_stream_t stream)
@@ -1161,14 +1516,14 @@ idx_status run_attention(Kv4Args &a, int64_t keys, int64_t most_tiles, void *ws,
     a.status = device_status_ptr();
     if (!a.status)
         return IDX_ERR_CUDA;
-    const int most = sm_count() * ctas_of(nt);
-    const int shares = (int)std::min<int64_t>(most, std::max<int64_t>(1, tiles));
+    const int most = sm_count() * groups_of(nt);
     a.ws_cut = static_cast<int4 *>(ws);
     a.ws_part = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + cut_bytes(most));
     const cudaStream_t s = (cudaStream_t)stream;
-    return nt == 1 ? launch_attention<kPaged, 1>(a, shares, s)
-         : nt == 2 ? launch_attention<kPaged, 2>(a, shares, s)
-                   : launch_attention<kPaged, 4>(a, shares, s);
+    if constexpr (!kPaged)
+        return launch_columns<kSlots>(a, nt, tiles, s);
+    return a.pool.p.page_size % kSub == 0 ? launch_columns<kWholePages>(a, nt, tiles, s)
+                                          : launch_columns<kPages>(a, nt, tiles, s);
 }
 
 } // namespace
@@ -1182,7 +1537,7 @@ extern "C" size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int
     if (R <= 0 || next_n <= 0 || H <= 0 || kv_heads <= 0 || max_keys <= kUncutKeys)
         return 0;
     const int64_t cols = (int64_t)next_n * (H / kv_heads);
-    const int nt = tiles_of((int)std::min<int64_t>(cols, 32)), most = sm_count() * ctas_of(nt);
+    const int nt = tiles_of((int)std::min<int64_t>(cols, 32)), most = sm_count() * groups_of(nt);
     return cut_bytes(most) + (size_t)2 * most * part_of(nt) * sizeof(float);
 }
 
@@ -1339,9 +1694,16 @@ extern "C" idx_status idx_paged_kv4_weights(
         return IDX_ERR_CUDA;
     const int nt = tiles_of(a.cols);
     a.blocks = (a.cols + 8 * nt - 1) / (8 * nt);
-    auto kern = nt == 1 ? kv4_weights_kernel<1> : nt == 2 ? kv4_weights_kernel<2>
-                                                          : kv4_weights_kernel<4>;
-    const int grid = (int)std::min<int64_t>((int64_t)sm_count() * (nt == 4 ? 3 : 4),
-                                            tiles * kv_heads);
-    return launch_status(launch_pdl(kern, dim3(grid), dim3(kThreads), 0, (cudaStream_t)stream, a));
+    // the tiles of the contexts, and at least a warp for 512 columns past them
+    const int64_t work = std::max<int64_t>(tiles * kv_heads,
+                                           (int64_t)B * kv_heads * ((width + 511) / 512) / kWarps);
+    const int mode = page_size % kSub == 0 ? kWholePages : kPages;
+    const cudaStream_t st = (cudaStream_t)stream;
+    return mode == kWholePages
+               ? nt == 1 ? launch_weights<kWholePages, 1>(a, work, st)
+                 : nt == 2 ? launch_weights<kWholePages, 2>(a, work, st)
+                           : launch_weights<kWholePages, 4>(a, work, st)
+               : nt == 1 ? launch_weights<kPages, 1>(a, work, st)
+                 : nt == 2 ? launch_weights<kPages, 2>(a, work, st)
+                           : launch_weights<kPages, 4>(a, work, st);
 }

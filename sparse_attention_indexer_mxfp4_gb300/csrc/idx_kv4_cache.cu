@@ -1,9 +1,11 @@
 // idx_kv4_cache.cu -- the 4-bit cache's writer, its read-back and the eviction
 // that moves the tokens that stay to other pages.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 
 #include "idx_kv4.cuh"
+#include "idx_topk_cluster.cuh"
 
 namespace idx {
 namespace {
@@ -61,7 +63,7 @@ struct Kv4Rows {
 };
 
 __global__ void __launch_bounds__(kThreads)
-    kv4_store_kernel(const Kv4Rows in, int64_t items, const Kv4Pool pool,
+    kv4_store_kernel(const Kv4Rows in, uint32_t items, const Kv4Pool pool,
                      const int64_t *__restrict__ slots, unsigned int *status)
 {
     pdl_wait();
@@ -70,19 +72,18 @@ __global__ void __launch_bounds__(kThreads)
     const uint16_t *src = side ? in.v : in.k;
     const int64_t ld_row = side ? in.ldv_row : in.ldk_row;
     const int64_t ld_head = side ? in.ldv_head : in.ldk_head;
-    const int64_t step = (int64_t)gridDim.x * kWarps * kItems;
-    for (int64_t i0 = ((int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5)) * kItems; i0 < items;
-         i0 += step) {
+    const uint32_t step = gridDim.x * kWarps * kItems;
+    for (uint32_t i0 = (blockIdx.x * kWarps + (threadIdx.x >> 5)) * kItems; i0 < items; i0 += step) {
         uint4 raw[kItems];
         int64_t slot[kItems];
+        int head[kItems];
         #pragma unroll
         for (int i = 0; i < kItems; ++i) {
-            const int64_t it = i0 + i;
+            const uint32_t it = i0 + i, t = it / (uint32_t)pool.heads;
+            const int h = head[i] = (int)(it - t * pool.heads);
             slot[i] = -1;
             raw[i] = make_uint4(0u, 0u, 0u, 0u);
             if (it < items) {
-                const int64_t t = it / pool.heads;
-                const int h = (int)(it - t * pool.heads);
                 slot[i] = slots[t];
                 raw[i] = *reinterpret_cast<const uint4 *>(src + t * ld_row + h * ld_head + 8 * piece);
             }
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(kThreads)
             }
             const int page = page_of(pool.p, (int)slot[i]);
             const int off = (int)slot[i] - page * pool.p.page_size;
-            const int h = (int)((i0 + i) % pool.heads);
+            const int h = head[i];
             uint8_t *base = const_cast<uint8_t *>(pool.p.base);
             *reinterpret_cast<uint32_t *>(base + kv4_codes_at(pool, page, h, off) +
                                           side * pool.side + 4 * piece) = codes;
@@ -134,11 +135,10 @@ __global__ void __launch_bounds__(kThreads)
         atomicOr(status, kDevBadBounds);
     const int rows = min(N, end);
     // a warp has the heads of a row, kItems at a time
-    const int parts = (pool.heads + kItems - 1) / kItems;
-    const int64_t step = (int64_t)gridDim.x * kWarps;
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < (int64_t)rows * parts;
-         i += step) {
-        const int n = (int)(i / parts), h0 = (int)(i - (int64_t)n * parts) * kItems;
+    const uint32_t parts = (pool.heads + kItems - 1) / kItems;
+    const uint32_t step = gridDim.x * kWarps;
+    for (uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < rows * parts; i += step) {
+        const int n = (int)(i / parts), h0 = (int)(i - n * parts) * kItems;
         int lo = 0, hi = B - 1;  // the first sequence that ends past row n
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -193,10 +193,16 @@ __global__ void __launch_bounds__(kThreads)
 
 // -------------------------------------------------------------- the eviction
 //
-// Scores (a token's weight, of its head or summed over the heads in 64 bits and
-// rounded once), the top-k of those that are not recent, then the tokens that
-// stay go to their new places.  Tokens move to pages of their own: the old ones
-// may belong to other sequences too.
+// A cluster of CTAs a list selects among the tokens that are not recent: the
+// cluster form of the top-k on weights, of a head or summed over the heads, which
+// stay in its shared memory.  Then the tokens that stay go to their new places.
+// Tokens move to pages of their own: the old ones may belong to other sequences
+// too.  Bound: the weights once, the tokens that stay read and written (136 bytes).
+//
+// A sum over heads is of pairs of floats (sum and what it lost to rounding, 48 bits
+// together), rounded once; 64-bit additions are so few a clock that they bounded the
+// selection (32 contexts x 8 heads 31 us).  Longer contexts than a cluster holds
+// take scores in scratch and the general top-k.
 
 struct EvictArgs {
     const float *mass;
@@ -230,6 +236,122 @@ __device__ __forceinline__ float orderly(float x)
     return x != x ? -most : fminf(fmaxf(x, -most), most);
 }
 
+// a + b as a float and what the float lacks.
+__device__ __forceinline__ void add_pair(float &hi, float &lo, float b)
+{
+    const float sum = hi + b, part = sum - hi;
+    lo += (hi - (sum - part)) + (b - part);
+    hi = sum;
+}
+
+__device__ __forceinline__ float of_pair(float hi, float lo)
+{
+    return isfinite(hi) ? hi + lo : hi;  // (infinities leave NaN behind)
+}
+
+// Weight of token t of a list.
+__device__ __forceinline__ float evict_weight(const EvictArgs &a, const float *m, int t)
+{
+    if (a.lists == a.heads)
+        return m[t];
+    float hi = 0.0f, lo = 0.0f;
+    #pragma unroll 8
+    for (int h = 0; h < a.heads; ++h)
+        add_pair(hi, lo, m[h * a.ld_head + t]);
+    return of_pair(hi, lo);
+}
+
+// The keys of a list for the top-k's cluster form.
+struct Weights {
+    static constexpr bool kRuns = true;
+    EvictArgs a;
+    int vec_ok;  // four columns side by side are one load
+
+    __device__ __forceinline__ int len(int row) const
+    {
+        const int n = evict_len(a, row / a.lists);
+        return n > a.budget ? n - a.recent : 0;
+    }
+    __device__ __forceinline__ void run(int row, int base, int at, int end, uint32_t (&key)[4]) const
+    {
+        const int b = row / a.lists, g = row - b * a.lists;
+        const float *m = a.mass + b * a.ld_batch + g * a.ld_head + base;
+        float x[4] = {};
+        if (vec_ok && at + 4 <= end) {
+            const int heads = a.lists == a.heads ? 1 : a.heads;
+            float lo[4] = {};
+            for (int h0 = 0; h0 < heads; h0 += 4) {
+                float4 v[4];
+                #pragma unroll
+                for (int h = 0; h < 4; ++h)
+                    v[h] = h0 + h < heads
+                               ? __ldg(reinterpret_cast<const float4 *>(m + (h0 + h) * a.ld_head + at))
+                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                #pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    add_pair(x[0], lo[0], v[h].x);
+                    add_pair(x[1], lo[1], v[h].y);
+                    add_pair(x[2], lo[2], v[h].z);
+                    add_pair(x[3], lo[3], v[h].w);
+                }
+            }
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                x[e] = of_pair(x[e], lo[e]);
+        } else {
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (at + e < end)
+                    x[e] = evict_weight(a, m, at + e);
+        }
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+            key[e] = at + e < end ? order_key(orderly(x[e])) : 0u;
+    }
+};
+
+// Short lists of single heads: a CTA each, the keys in its registers (4 sequences
+// x 8 heads of up to 8192 tokens to 2048 in clusters 16.9 us, here 10.4).
+__global__ void __launch_bounds__(topk_short::kThreads, 3)
+    evict_short_kernel(const Weights src, int k, int32_t *__restrict__ out, int64_t ld_out)
+{
+    namespace T = topk_short;
+    __shared__ __align__(16) regsel::Shared<T::kThreads, T::kSteps> sh;
+    const int row = blockIdx.x, tid = threadIdx.x;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int len = src.len(row), nrun = (len + 4 * T::kThreads - 1) / (4 * T::kThreads);
+    const EvictArgs &a = src.a;
+    const float *m = a.mass + row / a.heads * a.ld_batch + row % a.heads * a.ld_head;
+    float4 v[T::kSteps];
+    #pragma unroll
+    for (int s = 0; s < T::kSteps; ++s) {
+        const int at = 4 * (s * T::kThreads + tid);
+        v[s] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (src.vec_ok && at + 4 <= len) {
+            v[s] = __ldg(reinterpret_cast<const float4 *>(m + at));
+        } else {
+            v[s].x = at < len ? __ldg(m + at) : 0.0f;
+            v[s].y = at + 1 < len ? __ldg(m + at + 1) : 0.0f;
+            v[s].z = at + 2 < len ? __ldg(m + at + 2) : 0.0f;
+            v[s].w = at + 3 < len ? __ldg(m + at + 3) : 0.0f;
+        }
+    }
+    uint32_t key[T::kSteps][4];
+    #pragma unroll
+    for (int s = 0; s < T::kSteps; ++s) {
+        const int at = 4 * (s * T::kThreads + tid);
+        const float x[4] = {v[s].x, v[s].y, v[s].z, v[s].w};
+        #pragma unroll
+        for (int e = 0; e < 4; ++e)
+            key[s][e] = at + e < len ? order_key(orderly(x[e])) : 0u;
+    }
+    regsel::select_write<T::kThreads, T::kSteps>(
+        sh, key, k, out + (size_t)row * ld_out,
+        [&](int s, int e) -> int32_t { return s * 4 * T::kThreads + 4 * tid + e; }, nrun);
+}
+
+// The same in scratch.
 __global__ void __launch_bounds__(kThreads) evict_score_kernel(const EvictArgs a)
 {
     pdl_wait();
@@ -239,33 +361,23 @@ __global__ void __launch_bounds__(kThreads) evict_score_kernel(const EvictArgs a
     if (blockIdx.x == 0 && threadIdx.x == 0)
         a.lengths[row] = old;
     const float *m = a.mass + b * a.ld_batch + g * a.ld_head;
-    for (int t = blockIdx.x * kThreads + threadIdx.x; t < old; t += gridDim.x * kThreads) {
-        float x;
-        if (a.lists == a.heads) {
-            x = m[t];
-        } else {
-            double sum = 0.0;
-            #pragma unroll 8
-            for (int h = 0; h < a.heads; ++h)
-                sum += (double)m[h * a.ld_head + t];
-            x = (float)sum;
-        }
-        a.score[row * a.ld_score + t] = orderly(x);
-    }
+    for (int t = blockIdx.x * kThreads + threadIdx.x; t < old; t += gridDim.x * kThreads)
+        a.score[row * a.ld_score + t] = orderly(evict_weight(a, m, t));
 }
 
-// Eight tokens of a head a warp: four lanes a token's 64 bytes of keys, then of
-// values; a lane each its scales and weight.
+// 32 tokens of a head a warp: a lane looks a token up, four lanes move its 64
+// bytes of keys, then of values (eight tokens at once, all loads before the first
+// store: 4 KB in flight a warp), a lane each its scales and weight.
 __global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a, const Kv4Pool pool)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = lane_id();
-    const int parts = max(1, (a.budget + 7) / 8);
-    const int64_t all = (int64_t)a.B * a.heads * parts, step = (int64_t)gridDim.x * kWarps;
+    const uint32_t parts = max(1, (a.budget + 31) / 32);
+    const uint32_t all = a.B * a.heads * parts, step = gridDim.x * kWarps;
     uint8_t *base = const_cast<uint8_t *>(pool.p.base);
-    for (int64_t i = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); i < all; i += step) {
-        const int bh = (int)(i / parts), j0 = (int)(i - (int64_t)bh * parts) * 8;
+    for (uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < all; i += step) {
+        const int bh = (int)(i / parts), j0 = (int)(i - bh * parts) * 32;
         const int b = bh / a.heads, h = bh - b * a.heads, g = a.lists == 1 ? 0 : h;
         const int n = evict_len(a, b), kept = min(n, a.budget), chosen = a.budget - a.recent;
         if (h == 0 && j0 == 0 && lane == 0) {
@@ -273,20 +385,22 @@ __global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a,
             if (a.ctx[b] < 0 || a.ctx[b] > a.ld)
                 atomicOr(a.status, kDevBadBounds);
         }
-        // lanes 0 to 7: the place of a token, and its new one
-        const int j = j0 + (lane & 7);
+        // this lane's token: its place and its new one
+        const int j = j0 + lane;
         int32_t *list = a.keep + ((int64_t)b * a.lists + g) * a.budget;
+        const bool listed = n > a.budget && j < chosen;  // by the top-k
         int src = -1;
         if (j < kept)
-            src = n <= a.budget ? j : j < chosen ? list[j] : n - a.recent + (j - chosen);
-        const bool listed = n > a.budget && j < chosen;  // by the top-k
-        if (lane < 8 && j < a.budget && !listed && h == g)
+            src = n <= a.budget ? j : listed ? list[j] : n - a.recent + (j - chosen);
+        if (j < a.budget && !listed && h == g)
             list[j] = src;
         int64_t from = -1, to = -1, sc_from = 0, sc_to = 0;
+        float m = 0.0f;
         if (src >= 0) {
             const int sb = page_of(pool.p, src), db = page_of(pool.p, j);
             const int sp = sb < a.blocks ? a.table[b * a.bt_stride + sb] : -1;
             const int dp = db < a.new_blocks ? a.new_table[b * a.new_stride + db] : -1;
+            m = a.mass[b * a.ld_batch + h * a.ld_head + src];
             if (sp >= 0 && sp < pool.p.num_pages) {
                 from = kv4_codes_at(pool, sp, h, src - sb * pool.p.page_size);
                 sc_from = kv4_scales_at(pool, sp, h, src - sb * pool.p.page_size);
@@ -295,31 +409,82 @@ __global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a,
                 to = kv4_codes_at(pool, dp, h, j - db * pool.p.page_size);
                 sc_to = kv4_scales_at(pool, dp, h, j - db * pool.p.page_size);
             }
-            if ((from < 0 || to < 0) && lane < 8)
+            if (from < 0 || to < 0)
                 atomicOr(a.status, kDevBadPage);
         }
-        const int64_t from4 = __shfl_sync(0xffffffffu, from, lane >> 2),
-                      to4 = __shfl_sync(0xffffffffu, to, lane >> 2);
-        uint4 kv[2] = {};
-        uint32_t sc = 0;
-        float m = 0.0f;
-        if (from4 >= 0) {
-            kv[0] = *reinterpret_cast<const uint4 *>(base + from4 + 16 * (lane & 3));
-            kv[1] = *reinterpret_cast<const uint4 *>(base + from4 + pool.side + 16 * (lane & 3));
+        uint4 kv[4][2] = {};
+        uint32_t sc[2] = {};
+        #pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int64_t at = __shfl_sync(0xffffffffu, from, 8 * x + (lane >> 2));
+            if (at >= 0) {
+                kv[x][0] = *reinterpret_cast<const uint4 *>(base + at + 16 * (lane & 3));
+                kv[x][1] = *reinterpret_cast<const uint4 *>(base + at + pool.side + 16 * (lane & 3));
+            }
         }
-        if (lane < 16 && from >= 0)
-            sc = *reinterpret_cast<const uint32_t *>(base + sc_from + (lane >> 3) * pool.scale_side);
-        if (lane < 8 && src >= 0)
-            m = a.mass[b * a.ld_batch + h * a.ld_head + src];
-        if (to4 >= 0) {
-            *reinterpret_cast<uint4 *>(base + to4 + 16 * (lane & 3)) = kv[0];
-            *reinterpret_cast<uint4 *>(base + to4 + pool.side + 16 * (lane & 3)) = kv[1];
+        if (from >= 0) {
+            sc[0] = *reinterpret_cast<const uint32_t *>(base + sc_from);
+            sc[1] = *reinterpret_cast<const uint32_t *>(base + sc_from + pool.scale_side);
         }
-        if (lane < 16 && to >= 0)
-            *reinterpret_cast<uint32_t *>(base + sc_to + (lane >> 3) * pool.scale_side) = sc;
-        if (lane < 8 && j < a.budget)
+        #pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int64_t at = __shfl_sync(0xffffffffu, to, 8 * x + (lane >> 2));
+            if (at >= 0) {
+                *reinterpret_cast<uint4 *>(base + at + 16 * (lane & 3)) = kv[x][0];
+                *reinterpret_cast<uint4 *>(base + at + pool.side + 16 * (lane & 3)) = kv[x][1];
+            }
+        }
+        if (to >= 0) {
+            *reinterpret_cast<uint32_t *>(base + sc_to) = sc[0];
+            *reinterpret_cast<uint32_t *>(base + sc_to + pool.scale_side) = sc[1];
+        }
+        if (j < a.budget)
             a.new_mass[(int64_t)bh * a.budget + j] = m;
     }
+}
+
+// Selection without scratch.  The cluster form has as many CTAs a list as there are
+// SMs for, and at least enough to hold it; none with less than half a run of keys
+// (2048).
+cudaError_t select_on_chip(const EvictArgs &a, int chosen, cudaStream_t stream)
+{
+    namespace T = topk_cluster;
+    const int rows = a.B * a.lists;
+    const int vec_ok = (a.ld_batch | a.ld_head) % 4 == 0 && aligned16(a.mass);
+    if (a.lists == a.heads && a.ld <= topk_short::kMaxLen)
+        return launch_pdl(evict_short_kernel, dim3(rows), dim3(topk_short::kThreads), 0, stream,
+                          Weights{a, vec_ok}, chosen, a.keep, (int64_t)a.budget);
+    const int least = (a.ld + T::kChunk - 1) / T::kChunk, most = (a.ld + 2047) / 2048;
+    const int C = std::max(least, std::min({T::kMaxCluster, most, sm_count() / rows}));
+    static std::atomic<uint64_t> ready{0};  // devices whose attribute is set
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(T::topk_cluster_kernel<Weights>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(T::Shared));
+        if (e != cudaSuccess)
+            return e;
+        ready.fetch_or(bit, std::memory_order_relaxed);
+    }
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * C));
+    cfg.blockDim = dim3(T::kThreads);
+    cfg.dynamicSmemBytes = sizeof(T::Shared);
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, T::topk_cluster_kernel<Weights>, Weights{a, vec_ok}, rows, chosen,
+                              a.keep, (int64_t)a.budget, SlotCount{});
 }
 
 // CTAs for so many warps of work, at most a full SM of warps each.
@@ -369,15 +534,16 @@ extern "C" idx_status idx_kv4_store(const uint16_t *k, int64_t ldk_row, int64_t 
     const idx_status ok = check_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
     if (ok != IDX_OK)
         return ok;
-    if (!aligned16(k) || !aligned16(v) || (ldk_row | ldk_head | ldv_row | ldv_head) % 8 != 0)
+    const int64_t items = (int64_t)T * kv_heads;
+    if (!aligned16(k) || !aligned16(v) || (ldk_row | ldk_head | ldv_row | ldv_head) % 8 != 0 ||
+        items > INT32_MAX)
         return IDX_ERR_UNSUPPORTED;
     unsigned int *status = device_status_ptr();
     if (!status)
         return IDX_ERR_CUDA;
-    const int64_t items = (int64_t)T * kv_heads;
     return launch_status(launch_pdl(
         kv4_store_kernel, dim3(grid_of((items + kItems - 1) / kItems)), dim3(kThreads), 0,
-        (cudaStream_t)stream, Kv4Rows{k, v, ldk_row, ldk_head, ldv_row, ldv_head}, items,
+        (cudaStream_t)stream, Kv4Rows{k, v, ldk_row, ldk_head, ldv_row, ldv_head}, (uint32_t)items,
         make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads), slot_mapping,
         status));
 }
@@ -404,7 +570,7 @@ extern "C" idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_strid
     if (ok != IDX_OK)
         return ok;
     if (!aligned16(k_out) || !aligned16(v_out) ||
-        (ldk_row | ldk_head | ldv_row | ldv_head) % 8 != 0)
+        (ldk_row | ldk_head | ldv_row | ldv_head) % 8 != 0 || (int64_t)N * kv_heads > INT32_MAX)
         return IDX_ERR_UNSUPPORTED;
     unsigned int *status = device_status_ptr();
     if (!status)
@@ -420,8 +586,10 @@ extern "C" idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_strid
 extern "C" size_t idx_kv4_evict_workspace_size(int B, int kv_heads, int ld_mass, int budget,
                                                int recent, int whole_tokens)
 {
-    if (B <= 0 || kv_heads <= 0 || ld_mass <= budget || budget <= recent)
-        return 0;  // nothing is chosen
+    // nothing is chosen, or a cluster holds what it is chosen from
+    if (B <= 0 || kv_heads <= 0 || ld_mass <= budget || budget <= recent ||
+        ld_mass <= topk_cluster::kMaxLen)
+        return 0;
     return EvictScratch(B, whole_tokens ? 1 : kv_heads, ld_mass, budget - recent).all;
 }
 
@@ -430,16 +598,13 @@ extern "C" int idx_kv4_evict_launches(int B, int kv_heads, int ld_mass, int budg
 {
     if (B <= 0 || kv_heads <= 0)
         return 0;
-    if (idx_kv4_evict_workspace_size(B, kv_heads, ld_mass, budget, recent, whole_tokens) == 0)
+    if (ld_mass <= budget || budget <= recent)
         return 1;
+    if (ld_mass <= topk_cluster::kMaxLen)
+        return 2;
     const int lists = whole_tokens ? 1 : kv_heads;
     const EvictScratch at(B, lists, ld_mass, budget - recent);
-    // the top-k is one kernel where rows fit a CTA's registers or a wave of clusters, or
-    // without scratch of its own
-    const int64_t clusters = (at.ld_score + 32767) / 32768;
-    const bool chunked = at.ld_score > 8192 && at.all > at.topk &&
-                         (at.ld_score > 262144 || (int64_t)B * lists * clusters > sm_count());
-    return chunked ? 4 : 3;
+    return at.all > at.topk ? 4 : 3;  // the top-k with scratch of its own is two kernels
 }
 
 extern "C" idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t ld_head,
@@ -470,7 +635,8 @@ extern "C" idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t
         return IDX_ERR_INVALID_ARG;  // no room for what stays
     const int lists = whole_tokens ? 1 : kv_heads;
     // rows are a grid's second dimension
-    if ((int64_t)B * lists > 65535 || ld_mass > INT32_MAX - 3)
+    if ((int64_t)B * lists > 65535 || ld_mass > INT32_MAX - 3 ||
+        (int64_t)B * kv_heads > INT32_MAX / ((int64_t)budget + 32))
         return IDX_ERR_UNSUPPORTED;
     const size_t need =
         idx_kv4_evict_workspace_size(B, kv_heads, ld_mass, budget, recent, whole_tokens);
@@ -500,8 +666,13 @@ extern "C" idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t
     if (!a.status)
         return IDX_ERR_CUDA;
     const Kv4Pool pool = make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads);
-    if (need > 0) {
-        const int rows = B * lists, chosen = budget - recent;
+    const int chosen = budget - recent;
+    if (need == 0 && chosen > 0 && ld_mass > budget) {
+        const cudaError_t e = select_on_chip(a, chosen, (cudaStream_t)stream);
+        if (e != cudaSuccess)
+            return launch_status(e);
+    } else if (need > 0) {
+        const int rows = B * lists;
         const EvictScratch at(B, lists, ld_mass, chosen);
         uint8_t *w = static_cast<uint8_t *>(ws);
         a.score = reinterpret_cast<float *>(w);
@@ -521,6 +692,6 @@ extern "C" idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t
             return st;
     }
     return launch_status(launch_pdl(
-        evict_move_kernel, dim3(grid_of((int64_t)B * kv_heads * std::max(1, (budget + 7) / 8))),
+        evict_move_kernel, dim3(grid_of((int64_t)B * kv_heads * std::max(1, (budget + 31) / 32))),
         dim3(kThreads), 0, (cudaStream_t)stream, a, pool));
 }

@@ -476,7 +476,7 @@ idx_status topk_launch_cluster(const float *logits, int64_t ld, int rows, const 
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
         return IDX_ERR_CUDA;
     if (!configured[dev]) {
-        if (cudaFuncSetAttribute(T::topk_cluster_kernel,
+        if (cudaFuncSetAttribute(T::topk_cluster_kernel<T::Logits>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)smem) != cudaSuccess)
             return IDX_ERR_CUDA;
@@ -498,7 +498,7 @@ idx_status topk_launch_cluster(const float *logits, int64_t ld, int rows, const 
     cfg.numAttrs = 1;
     if (!resident[dev][C]) {
         int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, T::topk_cluster_kernel, &cfg);
+        const cudaError_t e = cudaOccupancyMaxActiveClusters(&n, T::topk_cluster_kernel<T::Logits>, &cfg);
         if (e != cudaSuccess)
             (void)cudaGetLastError();
         resident[dev][C] = e == cudaSuccess && n > 0 ? 1 : -1;
@@ -507,8 +507,9 @@ idx_status topk_launch_cluster(const float *logits, int64_t ld, int rows, const 
         return IDX_ERR_UNSUPPORTED;
     cfg.numAttrs = 2;  // launched programmatically after the kernel before it
     SlotCount none = {};
-    return launch_status(cudaLaunchKernelEx(&cfg, T::topk_cluster_kernel, logits, ld, rows,
-                                            lengths, k, out, ld_out, vec_ok, sc ? *sc : none));
+    return launch_status(cudaLaunchKernelEx(&cfg, T::topk_cluster_kernel<T::Logits>,
+                                            T::Logits{logits, ld, lengths, vec_ok}, rows, k, out,
+                                            ld_out, sc ? *sc : none));
 }
 
 } // namespace

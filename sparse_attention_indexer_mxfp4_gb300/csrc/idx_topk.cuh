@@ -197,7 +197,7 @@ __device__ __forceinline__ void find_bin(Shared &sh, const uint32_t *h, int nb, 
     __syncthreads();
 }
 
-__global__ void __launch_bounds__(kThreads, 2)
+static __global__ void __launch_bounds__(kThreads, 2)
     topk_kernel(const float *__restrict__ logits, int64_t ld, int rows,
                 const int32_t *__restrict__ lengths, int k, int32_t *__restrict__ out,
                 int64_t ld_out, int vec_ok)

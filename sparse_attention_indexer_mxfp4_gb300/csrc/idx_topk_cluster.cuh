@@ -89,10 +89,25 @@ __device__ __forceinline__ void find_bin_cluster(cg::cluster_group &cl, Shared &
         nb, krem, sh.wbin[digit], sh.sel[digit]);
 }
 
+// Where a row's keys come from: logits, every finite one of [0, lengths[row]).
+// Another source (kRuns) gives a thread four keys of a run at a time.
+struct Logits {
+    static constexpr bool kRuns = false;
+    const float *__restrict__ logits;
+    int64_t ld;
+    const int32_t *__restrict__ lengths;
+    int vec_ok;
+
+    __device__ __forceinline__ int len(int row) const
+    {
+        return max(0, min(lengths[row], (int)ld));
+    }
+};
+
+template <typename Source>
 __global__ void __launch_bounds__(kThreads, 1)
-    topk_cluster_kernel(const float *__restrict__ logits, int64_t ld, int rows,
-                        const int32_t *__restrict__ lengths, int k, int32_t *__restrict__ out,
-                        int64_t ld_out, int vec_ok, const SlotCount sc)
+    topk_cluster_kernel(const Source src, int rows, int k, int32_t *__restrict__ out,
+                        int64_t ld_out, const SlotCount sc)
 {
     extern __shared__ __align__(16) uint8_t dsm[];
     Shared &sh = *reinterpret_cast<Shared *>(dsm);
@@ -110,14 +125,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // by the cluster barriers between)
     if (sc.bt && live && rank == 0 && tid == 0)
         sc.lens[row] = 0;
-    const int len = live ? max(0, min(lengths[row], (int)ld)) : 0;
+    const int len = live ? src.len(row) : 0;
     // the row's keys spread evenly over the cluster, whole quads per CTA (the
     // chunk starts stay 16-byte aligned for vector loads)
     const int per = min(kChunk, ((len + C - 1) / C + 3) & ~3);
     const int base = rank * per;
     const int end = max(0, min(len - base, per));        // keys of this CTA's chunk
     const int nrun = (end + 4 * kThreads - 1) / (4 * kThreads);  // runs holding them
-    const float *rowp = logits + (size_t)(live ? row : 0) * ld + base;
     // (slot count) the block-table entries of the chunk's pages go to shared
     // memory while the keys load, when they fit (-1 past max_blocks)
     const int seq = sc.bt && live ? (sc.row_to_seq ? __ldg(sc.row_to_seq + row) : row / sc.next_n)
@@ -139,9 +153,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     // keys of this chunk into shared memory, the local digit-1 histogram
     // from them as they are formed (the histograms were cleared above)
     uint32_t nvalid = 0;
-    {
+    if constexpr (Source::kRuns) {
+        __syncthreads();
+        for (int s = 0; s < nrun; ++s) {
+            uint32_t key[4];
+            src.run(row, base, 4 * (s * kThreads + tid), end, key);
+            sh.keys[s * kThreads + tid] = make_uint4(key[0], key[1], key[2], key[3]);
+            #pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (key[e]) {
+                    ++nvalid;
+                    atomicAdd(&sh.h1[key[e] >> 21], 1u);
+                }
+        }
+    } else {
+        const float *rowp = src.logits + (size_t)(live ? row : 0) * src.ld + base;
         uint32_t key[kSteps][4];
-        topk_detail::load_keys<kSteps>(rowp, 4 * tid, 4 * kThreads, end, vec_ok != 0, key, nrun);
+        topk_detail::load_keys<kSteps>(rowp, 4 * tid, 4 * kThreads, end, src.vec_ok != 0, key, nrun);
         __syncthreads();
         #pragma unroll
         for (int s = 0; s < kSteps; ++s) {

@@ -317,7 +317,7 @@ constexpr int kSteps = 8;                       // runs of four keys per thread
 constexpr int kMaxLen = kSteps * kThreads * 4;  // 8192
 
 // Rows of at most 8192 keys; thread t holds elements 1024 s + 4 t + e.
-__global__ void __launch_bounds__(kThreads, 3)
+static __global__ void __launch_bounds__(kThreads, 3)
     topk_short_kernel(const float *__restrict__ logits, int64_t ld, int rows,
                       const int32_t *__restrict__ lengths, int k, int32_t *__restrict__ out,
                       int64_t ld_out, int vec_ok)

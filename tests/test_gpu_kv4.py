@@ -516,6 +516,29 @@ def test_evict(whole, ctx, budget, recent, heads, page):
     assert np.array_equal(pool.cpu().numpy(), moved)
 
 
+@pytest.mark.parametrize("whole", [False, True])
+@pytest.mark.parametrize("columns,batch,recent", [(262144, 1, 0), (262148, 1, 5), (300001, 2, 64), (9001, 40, 64)])
+def test_evict_from_long_contexts(whole, columns, batch, recent):
+    """Lists that a cluster just holds, longer ones, and more of them than fit the SMs at once."""
+    rng = np.random.default_rng(columns)
+    page, heads, budget = 64, 2, 700
+    ctx = [columns - 3 * i for i in range(batch)]
+    new = -(-budget // page)
+    blocks = -(-columns // page)
+    # all sequences share the old pages
+    bt = np.tile(rng.permutation(blocks).astype(np.int32), (batch, 1))
+    nt = (blocks + np.arange(batch * new, dtype=np.int32)).reshape(batch, new)
+    pool = torch.zeros(blocks + batch * new, ref.page_stride(page, heads), dtype=torch.uint8, device="cuda")
+    mass = rng.random((batch, heads, columns), dtype=np.float32)
+    mass[:, :, ::3] = 0.75  # ties
+    keep, lens, got = B.idx_kv4_evict(_dev(mass), _dev(np.array(ctx, np.int32)), budget, recent, pool, page, _dev(bt),
+                                      _dev(nt), whole_tokens=whole)
+    _clean()
+    assert np.array_equal(keep.cpu().numpy(), _evict_reference(mass, ctx, budget, recent, whole))
+    want = np.take_along_axis(mass, np.broadcast_to(keep.cpu().numpy().astype(np.int64), (batch, heads, budget)), 2)
+    assert np.array_equal(got.cpu().numpy(), want) and lens.tolist() == [budget] * batch
+
+
 def test_evict_past_the_columns_and_the_pool():
     pool = torch.ones(6, ref.page_stride(16, 1), dtype=torch.uint8, device="cuda")
     mass = torch.rand(2, 1, 40, device="cuda")

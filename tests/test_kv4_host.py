@@ -131,7 +131,7 @@ def test_evict_refusals():
                              dict(nt=None), dict(keep=None), dict(lens=None), dict(nm=None), dict(pages=None),
                              dict(stride=100), dict(lh=-1)))
     _refused(call, UNSUPPORTED, (dict(D=64), dict(B=60000), dict(pages=FAKE + 8)))
-    _refused(call, WORKSPACE, (dict(ws=None), dict(wsb=8), dict(ws=FAKE + 8)))
+    _refused(call, WORKSPACE, (dict(ld=300000, ws=None), dict(ld=300000, wsb=8), dict(ld=300000, ws=FAKE + 8)))
 
 
 def test_grouped_prefill_refusals():
@@ -155,8 +155,10 @@ def test_scratch_of_nothing():
     assert f(0, 1, 64, 8, 9999) == 0 and f(4, 1, 64, 8, 512) == 0 and f(4, 1, 64, 8, 513) > 0
     assert f(4, 4, 64, 8, 513) > f(4, 1, 64, 8, 513)  # wider blocks of columns
     assert g(0, 999, 64) == 0 and g(4, 512, 64) == 0 and g(4, 513, 64) > 0
-    assert e(0, 8, 99, 9, 1, 0) == 0 and e(2, 8, 99, 99, 1, 0) == 0 and e(2, 8, 99, 9, 9, 0) == 0
-    assert e(2, 8, 99, 9, 1, 0) > e(2, 8, 99, 9, 1, 1) > 0
+    # what a cluster holds needs none
+    n = 1 << 19
+    assert e(0, 8, n, 9, 1, 0) == 0 and e(2, 8, n, n, 1, 0) == 0 and e(2, 8, n, 9, 9, 0) == 0
+    assert e(2, 8, 262144, 9, 1, 0) == 0 and e(2, 8, n, 9, 1, 0) > e(2, 8, n, 9, 1, 1) > 0
 
 
 # ------------------------------------------------------------------- the binding

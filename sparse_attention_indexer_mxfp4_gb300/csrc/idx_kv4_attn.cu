@@ -19,7 +19,7 @@
 //    scaled in 32 bits.
 //  * A value's scale goes to the weight: P_g = P 2^(e_g - E_g), E_g the largest
 //    exponent met, as f16 pairs (O follows E_g like the running maximum).  Tokens
-//    over 2^19 under E_g, and NaN scales, take a second form of the product with
+//    over 2^15 under E_g, and NaN scales, take a second form of the product with
 //    bf16 weights, which have an exponent to spare.
 //  * Values lie with pairs of elements in a byte, and the product wants pairs of
 //    tokens: the nibbles of two tokens change places before they are widened,
@@ -48,9 +48,9 @@ constexpr int kTile = kWarps * kSub;    // of a CTA's
 constexpr int kSubCodes = kSub * kKv4Codes;
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 4.0f;           // a score may exceed its running maximum by 2^4
-constexpr int kBias = 6;                // weights are held 2^6 larger: up to 2^10 in f16
-constexpr int kScaleUp = 5;             // and scaled values' up to 2^5 more
-constexpr int kScaleRange = 19;         // f16 holds 2^5 to 2^-14 without loss
+constexpr int kBias = 10;               // weights are held 2^10 larger: up to 2^14 in f16
+constexpr int kScaleUp = 1;             // and scaled values' up to 2 more
+constexpr int kScaleRange = 15;         // f16 holds 2 to 2^-14 without loss
 // Rows of few keys are not cut: no scratch and no joining kernel.
 constexpr int kUncutKeys = 4 * kTile;
 constexpr int kJoinThreads = 256;
@@ -391,6 +391,9 @@ struct Ring {
     int head, len;         // of the segment at hand
     int tok;               // slots, pages: this lane's next token; whole pages: the step's first
     int left;              // steps of the segment; negative: no more
+    // whole pages: this lane's first piece of a page's keys and of its scales; the last
+    // steps' pages outside the pool, a bit each
+    uint32_t code_at, scale_at, bad;
 
     __device__ __forceinline__ uint8_t *stage(int i) const { return mem + i * kStage; }
     __device__ __forceinline__ float4 *key_scales() const
@@ -444,6 +447,12 @@ struct Ring {
             return;
         head = g.hc / blocks;
         off = 0;
+        if constexpr (kMode == kWholePages) {
+            const uint32_t token = (uint32_t)head * a.pool.p.page_size, lane = lane_id();
+            code_at = token * kKv4Codes + 16 * lane;
+            scale_at = (uint32_t)a.pool.scales + token * kKv4Groups +
+                       (lane >> 3) * (uint32_t)a.pool.scale_side + 16 * (lane & 7);
+        }
         if constexpr (kPaged)
             from = a.table + g.b * a.bt_stride;
         else
@@ -457,6 +466,7 @@ struct Ring {
             *walk() = s;
         __syncwarp();
         left = 0;
+        bad = 0;
         advance(a, heads, blocks, warp);
     }
     // One more step into place st, if there is one; a group of copies is committed in any case.
@@ -464,11 +474,23 @@ struct Ring {
     {
         if (left == 0)
             advance(a, heads, blocks, warp);
+        bad <<= 1;
         if (left > 0) {
             --left;
             copy(a, st);
         }
         cp_async_commit();
+    }
+    // Which tokens of the step that is read next are there; rows: of the segment from its first
+    // on.  (kStages - 1 steps were filled after it.)
+    __device__ __forceinline__ uint32_t there(int st, int rows) const
+    {
+        if constexpr (kMode == kWholePages) {
+            const uint32_t all = rows >= kSub ? 0xffffffffu : (1u << rows) - 1u;
+            return bad >> (kStages - 1) & 1 ? 0u : all;
+        } else {
+            return masks()[st];
+        }
     }
     __device__ __forceinline__ void copy(const Kv4Args &a, int st)
     {
@@ -478,32 +500,26 @@ struct Ring {
         int page = ahead, o = off;
         if constexpr (kMode == kWholePages) {
             // 32 tokens side by side; those past the context lie in its last page too
-            const int rows = len - tok;
             tok += kTile;
             look(a);
-            const bool good = (uint32_t)page < (uint32_t)a.pool.p.num_pages;
-            const uint32_t there = rows >= kSub ? 0xffffffffu : (1u << rows) - 1u;
-            if (lane == 0)
-                masks()[st] = good ? there : 0u;
-            if (good) {
+            if ((uint32_t)page < (uint32_t)a.pool.p.num_pages) {
                 const uint8_t *base = a.pool.p.base + (uint64_t)(uint32_t)page * (uint32_t)a.pool.p.stride;
-                const uint32_t token = (uint32_t)head * a.pool.p.page_size + o;
-                const uint8_t *keys = base + (token * kKv4Codes + 16 * lane);
+                const uint8_t *keys = base + (code_at + o * kKv4Codes);
                 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     cp_async16(d + i * 8 * kKv4Codes, keys + i * 8 * kKv4Codes);
                 if constexpr (kValues) {
-                    const uint8_t *vals = keys + a.pool.side;
+                    const uint8_t *vals = keys + (uint32_t)a.pool.side;
                     #pragma unroll
                     for (int i = 0; i < 4; ++i)
                         cp_async16(d + kSubCodes + i * 8 * kKv4Codes, vals + i * 8 * kKv4Codes);
                 }
                 if (lane < (kValues ? 16 : 8))
-                    cp_async16(to + kCodes + 16 * lane,
-                               base + (a.pool.scales + token * kKv4Groups +
-                                       (lane >> 3) * (uint32_t)a.pool.scale_side + 16 * (lane & 7)));
-            } else if (lane == 0) {
-                atomicOr(a.status, kDevBadPage);
+                    cp_async16(to + kCodes + 16 * lane, base + (scale_at + o * kKv4Groups));
+            } else {
+                bad |= 1;
+                if (lane == 0)
+                    atomicOr(a.status, kDevBadPage);
             }
         } else {
             bool good = tok < len;
@@ -656,36 +672,56 @@ __device__ __forceinline__ void score_tile(uint32_t codes, uint32_t scales, cons
             sc[m][h][2] = v.z;
             sc[m][h][3] = v.w;
         }
+    // A group's products are scaled, two columns at once, while the next one's run.
+    float d[2][2][NT][4];
     #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t a0[2][4], a1[2][4];
-        #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            uint32_t ka[4], kb[4];
-            e2m1_to_f16x2(lds32((row ^ (16 * i)) + 16 * m * kKv4Codes), ka);
-            e2m1_to_f16x2(lds32((row ^ (16 * i)) + (16 * m + 8) * kKv4Codes), kb);
-            #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                a0[m][2 * x] = ka[x];
-                a0[m][2 * x + 1] = kb[x];
-                a1[m][2 * x] = ka[2 + x];
-                a1[m][2 * x + 1] = kb[2 + x];
-            }
-        }
-        #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            uint32_t b[4];
-            q.get(n, i, b);
+    for (int i = 0; i < 5; ++i) {
+        uint32_t a0[2][4], a1[2][4], b[NT][4];
+        if (i < 4) {
             #pragma unroll
             for (int m = 0; m < 2; ++m) {
-                float d[4];
-                mma16_first(d, a0[m], b[0], b[1]);
-                mma16(d, a1[m], b[2], b[3]);
+                uint32_t ka[4], kb[4];
+                e2m1_to_f16x2(lds32((row ^ (16 * i)) + 16 * m * kKv4Codes), ka);
+                e2m1_to_f16x2(lds32((row ^ (16 * i)) + (16 * m + 8) * kKv4Codes), kb);
                 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    s[m][n][x] = i == 0 ? d[x] * sc[m][x >> 1][i]
-                                        : fmaf(d[x], sc[m][x >> 1][i], s[m][n][x]);
+                for (int x = 0; x < 2; ++x) {
+                    a0[m][2 * x] = ka[x];
+                    a0[m][2 * x + 1] = kb[x];
+                    a1[m][2 * x] = ka[2 + x];
+                    a1[m][2 * x + 1] = kb[2 + x];
+                }
             }
+            #pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                q.get(n, i, b[n]);
+                #pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    mma16_first(d[i & 1][m][n], a0[m], b[n][0], b[n][1]);
+            }
+        }
+        if (i > 0) {
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    #pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float f = sc[m][h][i - 1];
+                        const float *v = d[~i & 1][m][n] + 2 * h;
+                        const float2 t = i == 1
+                            ? __fmul2_rn(make_float2(v[0], v[1]), make_float2(f, f))
+                            : fma2(make_float2(v[0], v[1]), make_float2(f, f),
+                                   make_float2(s[m][n][2 * h], s[m][n][2 * h + 1]));
+                        s[m][n][2 * h] = t.x;
+                        s[m][n][2 * h + 1] = t.y;
+                    }
+        }
+        if (i < 4) {
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int m = 0; m < 2; ++m)
+                    mma16(d[i & 1][m][n], a1[m], b[n][2], b[n][3]);
         }
     }
 }
@@ -714,7 +750,7 @@ __device__ __forceinline__ void mask_tile(float (&s)[2][NT][4], uint32_t there, 
 template <int NT>
 struct Shape {
     static constexpr int kCols = 8 * NT;
-    static constexpr int kStages = NT == 4 ? 5 : 3;
+    static constexpr int kStages = 2;  // (three: no faster, and less of L1)
     // Groups of kWarps warps with shares of their own: an SM has one CTA of as many as
     // registers and shared memory hold.
     static constexpr int kGroups = NT == 1 ? 4 : NT == 2 ? 3 : 2;
@@ -868,25 +904,21 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
             ring.widen_key_scales(st);
             const uint8_t *mem = ring.stage(st);
             const uint32_t *scales = reinterpret_cast<const uint32_t *>(mem + R::kCodes) + kSub;
-            const uint32_t there = ring.masks()[st];
             const int tok = tok0 + k * kTile;
+            const uint32_t there = ring.there(st, upto - tok);
             spare = st;
             st = st + 1 == kStages ? 0 : st + 1;
 
             // ---- exponents of the values: a lane a token, two groups a word (0 and 2, 1 and 3)
             const bool here = there >> lane & 1;
             const uint32_t word = here ? scales[lane] : top_e;
-            uint32_t under[2];  // the tops less them
+            uint32_t under[2];  // the tops less them, in halves
             const auto in_range = [&](uint32_t w) {
-                // 256 + top - e: bit 8 is clear where e is over the top
-                under[0] = (top_e & 0x00ff00ffu) + 0x01000100u - (w & 0x00ff00ffu);
-                under[1] = (top_e >> 8 & 0x00ff00ffu) + 0x01000100u - (w >> 8 & 0x00ff00ffu);
-                constexpr uint32_t over = 0x00010001u * (255 - kScaleRange);
-                const bool good = (((under[0] & under[1]) & 0x01000100u) == 0x01000100u) &
-                                  (((under[0] + over) | (under[1] + over)) & 0x02000200u) == 0;
-                under[0] -= 0x01000100u;
-                under[1] -= 0x01000100u;
-                return good;
+                // (one over the top is negative, which shows in its upper bits)
+                under[0] = (top_e & 0x00ff00ffu) - (w & 0x00ff00ffu);
+                under[1] = (top_e >> 8 & 0x00ff00ffu) - (w >> 8 & 0x00ff00ffu);
+                static_assert(kScaleRange == 15, "four bits");
+                return ((under[0] | under[1]) & 0xfff0fff0u) == 0;
             };
             bool fast = __all_sync(0xffffffffu, in_range(word));
             if (!fast) {
@@ -914,10 +946,10 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
                 fast = __all_sync(0xffffffffu, in_range(here ? word : top_e));
             }
             {
-                // the token's scales as f16, 2^(e - top + 5) by their exponent bits; two lanes
+                // the token's scales as f16, 2^(e - top + 1) by their exponent bits; two lanes
                 // change halves, so that pairs of tokens lie together
-                const uint32_t f0 = 0x00010001u * ((15 + kScaleUp) << 10) - (under[0] << 10);
-                const uint32_t f1 = 0x00010001u * ((15 + kScaleUp) << 10) - (under[1] << 10);
+                const uint32_t f0 = 0x00010001u * ((15 + kScaleUp) << 10) - under[0] * 1024u;
+                const uint32_t f1 = 0x00010001u * ((15 + kScaleUp) << 10) - under[1] * 1024u;
                 const bool odd = lane & 1;
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? f0 : f1, 1);
                 const uint32_t x = odd ? got : f0, y = odd ? f1 : got;
@@ -963,17 +995,23 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
             }
             // ---- weights
             #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NT; ++n) {
+                const float2 f = make_float2(slc[n][0], slc[n][1]);
+                const float2 z = make_float2((float)kBias - m[n][0], (float)kBias - m[n][1]);
+                float2 all = make_float2(l[n][0], l[n][1]);
                 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float z = (float)kBias - m[n][i];
+                for (int h = 0; h < 2; ++h)
                     #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        s[h][n][i] = ex2(fmaf(s[h][n][i], slc[n][i], z));
-                        s[h][n][i + 2] = ex2(fmaf(s[h][n][i + 2], slc[n][i], z));
-                        l[n][i] += s[h][n][i] + s[h][n][i + 2];
+                    for (int x = 0; x < 4; x += 2) {
+                        float2 t = fma2(make_float2(s[h][n][x], s[h][n][x + 1]), f, z);
+                        t = make_float2(ex2(t.x), ex2(t.y));
+                        s[h][n][x] = t.x;
+                        s[h][n][x + 1] = t.y;
+                        all = __fadd2_rn(all, t);
                     }
-                }
+                l[n][0] = all.x;
+                l[n][1] = all.y;
+            }
 
             // element pairs of groups 2 y and 2 y + 1 of four tokens, widened: rows of the
             // products' left side, two tiles a group
@@ -1344,7 +1382,7 @@ __global__ void __launch_bounds__(WeightShape<NT>::kGroups * kThreads, 1)
                 ring.widen_key_scales(st);
                 const int tok = tok0 + k * kTile;
                 const uint8_t *mem = ring.stage(st);
-                const uint32_t there = ring.masks()[st];
+                const uint32_t there = ring.there(st, upto - tok);
                 st = st + 1 == kStages ? 0 : st + 1;
                 __syncwarp();
                 float s[2][NT][4];

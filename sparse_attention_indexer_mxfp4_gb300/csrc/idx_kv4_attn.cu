@@ -78,8 +78,12 @@ struct Kv4Args {
     float *lse;
     int64_t ld_lse;
     int uncut;        // units are not cut
-    int4 *ws_cut;     // a share: the unit it begins and leaves to the next (sequence, key head and
-                      // block of columns, pieces; no pieces: none), whether a segment lies before
+    // A unit (a sequence's key head and block of columns) that is begun: sequence, head and
+    // block, pieces, and twice the share that has the first, plus one where that is not the
+    // share's first segment.  By unit, or where there are more of them than shares by the
+    // share that begins a unit and leaves it to the next (none: no pieces).
+    int4 *ws_cut;
+    int by_unit;
     float *ws_part;   // two segments a share: O, maxima, sums
     unsigned int *status;
     // weights of tokens
@@ -282,58 +286,98 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t *wsum, int64_t 
 template <bool kPaged, int kGroups>
 __device__ __forceinline__ void find_share(const Kv4Args &a, int heads, int64_t limit, Share &s)
 {
-    constexpr int kAll = kGroups * kThreads;
-    __shared__ int64_t wsum[kGroups * kWarps];
-    __shared__ int2 found[kGroups];
-    const int tid = threadIdx.x, group = tid / kThreads;
-    int64_t total = 0, mine = 0, upto = 0;
-    for (int b0 = 0; b0 < a.B; b0 += kAll) {
-        int64_t all;
-        mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
-        upto = total + block_scan<kGroups * kWarps>(mine, wsum, all);
-        total += all;
-    }
+    constexpr int kAll = kGroups * kThreads, kFew = 128;
+    const int tid = threadIdx.x, lane = lane_id(), group = tid / kThreads;
+    const int p = group * gridDim.x + blockIdx.x;
     s.left = s.each = s.more = 0;
-    if (total > limit) {
-        if (blockIdx.x == 0 && tid == 0)
-            atomicOr(a.status, kDevBadBounds);
-        return;
-    }
-    total *= heads;
-    const int shares = (int)min((int64_t)gridDim.x * kGroups, total);
-    s.each = (int)(total / shares);
-    s.more = (int)(total - (int64_t)s.each * shares);
-    const auto begin = [&](int p) { return (int64_t)p * s.each + min(p, s.more); };
-    const auto look = [&](int b) {
-        const int64_t before = (upto - mine) * heads, after = before + mine * heads;
-        #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            const int64_t u = begin(i * gridDim.x + blockIdx.x);
-            if (u >= before && u < after)
-                found[i] = make_int2(b, (int)(u - before));
+    // tiles of all heads as one list, once it is known to be no longer than it may
+    int shares = 0;
+    const auto divide = [&](int64_t tiles) {
+        if (tiles > limit) {
+            if (blockIdx.x == 0 && tid == 0)
+                atomicOr(a.status, kDevBadBounds);
+            return false;
         }
+        const uint32_t total = (uint32_t)(tiles * heads);
+        shares = min(gridDim.x * kGroups, total);
+        s.each = total / shares;
+        s.more = total - s.each * shares;
+        return true;
     };
-    if (a.B <= kAll) {
-        look(tid);
+    const auto begin = [&](int share) { return (int64_t)share * s.each + min(share, s.more); };
+    int place;  // of the share's first tile among its sequence's
+    if (a.B <= kFew) {
+        // every warp by itself, four sequences a lane
+        int n[kFew / 32];
+        int64_t upto = 0;
+        #pragma unroll
+        for (int i = 0; i < kFew / 32; ++i) {
+            const int b = kFew / 32 * lane + i;
+            n[i] = b < a.B ? (int)unit_tiles<kPaged>(a, b) : 0;
+            upto += n[i];
+        }
+        const int64_t mine = upto;
+        #pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? up : 0;
+        }
+        if (!divide(__shfl_sync(0xffffffffu, upto, 31)) || p >= shares)
+            return;
+        int64_t at = begin(p) - (upto - mine) * heads;
+        const uint32_t here = __ballot_sync(0xffffffffu, at >= 0 && at < mine * heads);
+        int b = kFew / 32 * lane;
+        #pragma unroll
+        for (int i = 0; i + 1 < kFew / 32; ++i)
+            if (at >= (int64_t)n[i] * heads && b == kFew / 32 * lane + i) {
+                at -= (int64_t)n[i] * heads;
+                ++b;
+            }
+        const int who = __ffs(here) - 1;
+        s.b = __shfl_sync(0xffffffffu, b, who);
+        place = __shfl_sync(0xffffffffu, (int)at, who);
     } else {
-        int64_t sum = 0, all;
+        __shared__ int64_t wsum[kGroups * kWarps];
+        __shared__ int2 found[kGroups];
+        int64_t total = 0, mine = 0, upto = 0, all;
         for (int b0 = 0; b0 < a.B; b0 += kAll) {
             mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
-            upto = sum + block_scan<kGroups * kWarps>(mine, wsum, all);
-            sum += all;
-            look(b0 + tid);
+            upto = total + block_scan<kGroups * kWarps>(mine, wsum, all);
+            total += all;
         }
+        if (!divide(total))
+            return;
+        const auto look = [&](int b) {
+            const int64_t before = (upto - mine) * heads, after = before + mine * heads;
+            #pragma unroll
+            for (int i = 0; i < kGroups; ++i) {
+                const int64_t u = begin(i * gridDim.x + blockIdx.x);
+                if (u >= before && u < after)
+                    found[i] = make_int2(b, (int)(u - before));
+            }
+        };
+        if (a.B <= kAll) {
+            look(tid);
+        } else {
+            int64_t sum = 0;
+            for (int b0 = 0; b0 < a.B; b0 += kAll) {
+                mine = b0 + tid < a.B ? unit_tiles<kPaged>(a, b0 + tid) : 0;
+                upto = sum + block_scan<kGroups * kWarps>(mine, wsum, all);
+                sum += all;
+                look(b0 + tid);
+            }
+        }
+        __syncthreads();
+        if (p >= shares)
+            return;
+        s.b = found[group].x;
+        place = found[group].y;
     }
-    __syncthreads();
-    const int p = group * gridDim.x + blockIdx.x;
-    if (p >= shares)
-        return;
     s.left = s.each + (p < s.more);
-    s.b = found[group].x;
     s.len = unit_len<kPaged>(a, s.b);
     s.tiles = (int)unit_tiles<kPaged>(a, s.b);
-    s.hc = found[group].y / s.tiles;
-    s.t = found[group].y - s.hc * s.tiles;
+    s.hc = place / s.tiles;
+    s.t = place - s.hc * s.tiles;
 }
 
 // A segment: tiles [t0, t1) of a unit.
@@ -839,10 +883,13 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     pdl_launch_dependents();
     const int heads = a.pool.heads * a.blocks;
     const int64_t limit = kPaged || a.uncut ? INT64_MAX / INT_MAX : a.num_slots / kTile + a.B;
-    if (warp == 0 && lane == 0 && !a.uncut)
+    if (warp == 0 && lane == 0 && !a.uncut && !a.by_unit)
         a.ws_cut[p] = make_int4(0, 0, 0, 0);
     Share share;
     find_share<kPaged, kGroups>(a, heads, limit, share);
+    // a list that is left alone (shares of nothing) has nothing to join
+    if (warp == 0 && lane == 0 && a.by_unit && !a.uncut && share.each == 0 && p < a.B * heads)
+        a.ws_cut[p] = make_int4(0, 0, 0, 0);
     R ring;
     ring.mem = smem + all_warp * R::kBytes;
     ring.start(a, share, heads, a.blocks, warp);
@@ -1169,14 +1216,13 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
         // ---- warp 0 has the segment's
         const bool part = seg.t0 > 0 || seg.t1 < seg.tiles;
         float *to = a.ws_part + (int64_t)(2 * p + (nth > 0)) * S::kPart;
-        if (part && seg.t0 == 0 && lane == 0) {
+        if ((part || a.by_unit) && !a.uncut && seg.t0 == 0 && lane == 0) {
             // the shares that hold the rest: `more - p - 1` longer ones first
-            const int64_t longer = max(0, share.more - p - 1);
-            const int rest = seg.tiles - seg.t1;
-            const int in = (int)min((int64_t)rest, longer * (share.each + 1));
-            a.ws_cut[p] = make_int4(
+            const int longer = max(0, share.more - p - 1), rest = seg.tiles - seg.t1;
+            const int in = (int)min((int64_t)rest, (int64_t)longer * (share.each + 1));
+            a.ws_cut[a.by_unit ? seg.b * heads + seg.hc : p] = make_int4(
                 seg.b, seg.hc, 1 + (in + share.each) / (share.each + 1) +
-                                   (rest - in + share.each - 1) / share.each, nth > 0);
+                                   (rest - in + share.each - 1) / share.each, 2 * p + (nth > 0));
         }
         #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -1216,14 +1262,14 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     cp_async_wait<0>();
 }
 
-// Joins the pieces of a unit that several shares hold: blockIdx.x is the share
-// that begins it.  A block's warps take a column each, or all of them one column
-// and every eighth piece; four pieces in flight a warp.
+// Joins the pieces of a unit that several shares hold, blockIdx.x its entry.  A
+// block's warps take a column each, or all of them one column and every eighth
+// piece; four pieces at once, under a running maximum.
 __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a, int kCols, int together)
 {
-    constexpr int kTeams = kJoinThreads / 32;
+    constexpr int kTeams = kJoinThreads / 32, kAtOnce = 4;
     __shared__ float4 meet[kTeams][32];
-    __shared__ float meet_sum[kTeams], meet_top[kTeams];
+    __shared__ float2 meet_stat[kTeams];
     const int warp = threadIdx.x >> 5, lane = lane_id();
     const int team = together ? warp : 0, teams = together ? kTeams : 1;
     const int col = together ? blockIdx.y : blockIdx.y * kTeams + warp;
@@ -1238,52 +1284,49 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_join_kernel(const Kv4Args a,
     if (col >= kCols || at >= a.cols)
         return;
     const int64_t step = 2 * (int64_t)kCols * (kKv4Dim + 2);
-    const float *rest = a.ws_part + blockIdx.x * step;
-    const float *first = rest + cut.w * (step / 2);
-    const int stat = kCols * kKv4Dim + col;
-    float top = -FLT_MAX;
-    for (int i = 32 * team + lane; i < pieces; i += 32 * teams)
-        top = fmaxf(top, (i == 0 ? first : rest + i * step)[stat]);
-    #pragma unroll
-    for (int x = 16; x > 0; x >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-    if (together) {
-        if (lane == 0)
-            meet_top[team] = top;
-        __syncthreads();
-        #pragma unroll
-        for (int i = 0; i < kTeams; ++i)
-            top = fmaxf(top, meet_top[i]);
-    }
-    float sum = 0.0f;
+    const float *rest = a.ws_part + (cut.w >> 1) * step;
+    const float *first = rest + (cut.w & 1) * (step / 2);
+    float top = -FLT_MAX, sum = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    #pragma unroll 4
-    for (int i = team; i < pieces; i += teams) {
-        const float *f = i == 0 ? first : rest + i * step;
-        const float w = ex2(f[stat] - top);
-        const float4 v = *reinterpret_cast<const float4 *>(f + col * kKv4Dim + 4 * lane);
-        sum = fmaf(w, f[stat + kCols], sum);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+    const auto add = [&](float m, float l, float4 v) {
+        const float up = fmaxf(top, m), mine = ex2(top - up), w = ex2(m - up);
+        top = up;
+        sum = sum * mine + l * w;
+        acc.x = acc.x * mine + v.x * w;
+        acc.y = acc.y * mine + v.y * w;
+        acc.z = acc.z * mine + v.z * w;
+        acc.w = acc.w * mine + v.w * w;
+    };
+    for (int i0 = team; i0 < pieces; i0 += kAtOnce * teams) {
+        float m[kAtOnce], l[kAtOnce];
+        float4 v[kAtOnce];
+        #pragma unroll
+        for (int x = 0; x < kAtOnce; ++x) {
+            const int i = i0 + x * teams;
+            const float *f = (i == 0 ? first : rest + i * step) + col * kKv4Dim;
+            m[x] = -FLT_MAX;
+            l[x] = 0.0f;
+            v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (i < pieces) {
+                m[x] = f[kCols * kKv4Dim - col * (kKv4Dim - 1)];
+                l[x] = f[kCols * (kKv4Dim + 1) - col * (kKv4Dim - 1)];
+                v[x] = *reinterpret_cast<const float4 *>(f + 4 * lane);
+            }
+        }
+        #pragma unroll
+        for (int x = 0; x < kAtOnce; ++x)
+            add(m[x], l[x], v[x]);
     }
     if (together) {
         meet[team][lane] = acc;
         if (lane == 0)
-            meet_sum[team] = sum;
+            meet_stat[team] = make_float2(top, sum);
         __syncthreads();
         if (team > 0)
             return;
         #pragma unroll
-        for (int i = 1; i < kTeams; ++i) {
-            const float4 v = meet[i][lane];
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
-            sum += meet_sum[i];
-        }
+        for (int i = 1; i < kTeams; ++i)
+            add(meet_stat[i].x, meet_stat[i].y, meet[i][lane]);
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int j = at / a.group, h = head * a.group + at - j * a.group;
@@ -1483,7 +1526,7 @@ bool raise_smem(F kernel, int smem, std::atomic<uint64_t> &ready)
 }
 
 template <int kMode, int NT>
-idx_status launch_attention(const Kv4Args &a, int64_t tiles, cudaStream_t stream)
+idx_status launch_attention(Kv4Args &a, int64_t tiles, cudaStream_t stream)
 {
     const int ctas = (int)std::min<int64_t>(sm_count(), tiles);
     const int shares = ctas * Shape<NT>::kGroups;
@@ -1492,13 +1535,16 @@ idx_status launch_attention(const Kv4Args &a, int64_t tiles, cudaStream_t stream
     static std::atomic<uint64_t> ready{0};
     if (!raise_smem(kv4_attention_kernel<kMode, NT>, smem, ready))
         return IDX_ERR_CUDA;
+    const int64_t units = (int64_t)a.B * a.pool.heads * a.blocks;
+    a.by_unit = units < shares;
     cudaError_t e = launch_pdl(kv4_attention_kernel<kMode, NT>, dim3(ctas),
                                dim3(Shape<NT>::kGroups * kThreads), smem, stream, a);
     if (e == cudaSuccess && !a.uncut) {
         // many pieces of few units: a block's warps share a column's
         const int cols = std::min(a.cols, 8 * NT), warps = kJoinThreads / 32;
-        const int together = (int64_t)a.B * a.pool.heads * a.blocks * kJoinFew < shares;
-        e = launch_pdl(kv4_join_kernel, dim3(shares - 1, together ? cols : (cols + warps - 1) / warps),
+        const int together = units * kJoinFew < shares;
+        const int entries = a.by_unit ? (int)units : shares - 1;
+        e = launch_pdl(kv4_join_kernel, dim3(entries, together ? cols : (cols + warps - 1) / warps),
                        dim3(kJoinThreads), 0, stream, a, 8 * NT, together);
     }
     return launch_status(e);
@@ -1529,7 +1575,7 @@ idx_status check_attention(const void *q, int64_t ldq_row, int64_t ldq_head, int
 }
 
 template <int kMode>
-idx_status launch_columns(const Kv4Args &a, int nt, int64_t tiles, cudaStream_t s)
+idx_status launch_columns(Kv4Args &a, int nt, int64_t tiles, cudaStream_t s)
 {
     return nt == 1 ? launch_attention<kMode, 1>(a, tiles, s)
          : nt == 2 ? launch_attention<kMode, 2>(a, tiles, s)

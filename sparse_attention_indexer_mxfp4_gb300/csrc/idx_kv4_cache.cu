@@ -11,9 +11,10 @@ namespace idx {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-// Items (a token's keys and values of one head) whose loads a warp has in
-// flight.
-constexpr int kItems = 4;
+// Items (a token's keys and values of one head) whose loads a warp has in flight
+// (8191 tokens x 8 heads written and read back: four 21.2 us, eight 27.1, two 25.7);
+// where there are fewer than fill the SMs, one (128 tokens 5.0 -> 4.3 us).
+constexpr int kItemsMany = 4;
 
 // ----------------------------------------------------------------- the store
 //
@@ -62,6 +63,7 @@ struct Kv4Rows {
     int64_t ldk_row, ldk_head, ldv_row, ldv_head;
 };
 
+template <int kItems>
 __global__ void __launch_bounds__(kThreads)
     kv4_store_kernel(const Kv4Rows in, uint32_t items, const Kv4Pool pool,
                      const int64_t *__restrict__ slots, unsigned int *status)
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(kThreads)
 // out.  A code times a power of two has two significant bits, so bf16 holds it
 // exactly.
 
+template <int kItems>
 __global__ void __launch_bounds__(kThreads)
     kv4_gather_kernel(const Kv4Pool pool, const int32_t *__restrict__ table, int64_t bt_stride,
                       int max_blocks, const int32_t *__restrict__ cu,
@@ -367,16 +370,18 @@ __global__ void __launch_bounds__(kThreads) evict_score_kernel(const EvictArgs a
 
 // 32 tokens of a head a warp: a lane looks a token up, four lanes move its 64
 // bytes of keys, then of values (eight tokens at once, all loads before the first
-// store: 4 KB in flight a warp), a lane each its scales and weight.
+// store: 4 KB in flight a warp), a lane each its scales and weight.  A warp each: CTAs
+// that walk on instead took 136 us where these take 130, with the next tokens looked
+// up ahead 142 (32 contexts x 8 heads to 8192 tokens, selection and all).
 __global__ void __launch_bounds__(kThreads) evict_move_kernel(const EvictArgs a, const Kv4Pool pool)
 {
     pdl_wait();
     pdl_launch_dependents();
     const int lane = lane_id();
     const uint32_t parts = max(1, (a.budget + 31) / 32);
-    const uint32_t all = a.B * a.heads * parts, step = gridDim.x * kWarps;
     uint8_t *base = const_cast<uint8_t *>(pool.p.base);
-    for (uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5); i < all; i += step) {
+    const uint32_t i = blockIdx.x * kWarps + (threadIdx.x >> 5);
+    if (i < a.B * a.heads * parts) {
         const int bh = (int)(i / parts), j0 = (int)(i - bh * parts) * 32;
         const int b = bh / a.heads, h = bh - b * a.heads, g = a.lists == 1 ? 0 : h;
         const int n = evict_len(a, b), kept = min(n, a.budget), chosen = a.budget - a.recent;
@@ -493,6 +498,12 @@ int grid_of(int64_t warps)
     return (int)std::min<int64_t>((warps + kWarps - 1) / kWarps, (int64_t)sm_count() * 8);
 }
 
+// Items a warp for so many of them.
+int items_of(int64_t items)
+{
+    return items > (int64_t)sm_count() * 4 * kWarps ? kItemsMany : 1;
+}
+
 // Where the parts of the eviction's scratch begin.
 struct EvictScratch {
     int64_t ld_score;
@@ -541,8 +552,10 @@ extern "C" idx_status idx_kv4_store(const uint16_t *k, int64_t ldk_row, int64_t 
     unsigned int *status = device_status_ptr();
     if (!status)
         return IDX_ERR_CUDA;
+    const int each = items_of(items);
     return launch_status(launch_pdl(
-        kv4_store_kernel, dim3(grid_of((items + kItems - 1) / kItems)), dim3(kThreads), 0,
+        each == 1 ? kv4_store_kernel<1> : kv4_store_kernel<kItemsMany>,
+        dim3(grid_of((items + each - 1) / each)), dim3(kThreads), 0,
         (cudaStream_t)stream, Kv4Rows{k, v, ldk_row, ldk_head, ldv_row, ldv_head}, (uint32_t)items,
         make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads), slot_mapping,
         status));
@@ -575,9 +588,10 @@ extern "C" idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_strid
     unsigned int *status = device_status_ptr();
     if (!status)
         return IDX_ERR_CUDA;
+    const int each = items_of((int64_t)N * kv_heads);
     return launch_status(launch_pdl(
-        kv4_gather_kernel, dim3(grid_of((int64_t)N * ((kv_heads + kItems - 1) / kItems))),
-        dim3(kThreads), 0, (cudaStream_t)stream,
+        each == 1 ? kv4_gather_kernel<1> : kv4_gather_kernel<kItemsMany>,
+        dim3(grid_of((int64_t)N * ((kv_heads + each - 1) / each))), dim3(kThreads), 0, (cudaStream_t)stream,
         make_kv4_pool(kv_pages, page_stride_bytes, num_pages, page_size, kv_heads), block_table,
         bt_stride, max_blocks, cu_lens, seq_starts, B, N, k_out, ldk_row, ldk_head, v_out, ldv_row,
         ldv_head, status));
@@ -692,6 +706,7 @@ extern "C" idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t
             return st;
     }
     return launch_status(launch_pdl(
-        evict_move_kernel, dim3(grid_of((int64_t)B * kv_heads * std::max(1, (budget + 31) / 32))),
+        evict_move_kernel,
+        dim3((unsigned)(((int64_t)B * kv_heads * std::max(1, (budget + 31) / 32) + kWarps - 1) / kWarps)),
         dim3(kThreads), 0, (cudaStream_t)stream, a, pool));
 }

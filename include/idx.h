@@ -813,8 +813,8 @@ size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int kv_heads, 
  *
  *   q, the cache, block_table, context_lens, next_n, scale, max_model_len  as
  *             idx_paged_kv4_attention.
- *   lse       fp32 [B * next_n, ld_lse]: that call's (-inf, a row that saw
- *             nothing, counts as 0).
+ *   lse       fp32, lse[row * ld_lse + head * ld_lse_head]: that call's (-inf, a
+ *             row that saw nothing, counts as 0).
  *   mass      fp32, mass[b * ld_batch + g * ld_head + t], t in [0, width); NULL
  *             stands for zeros.  width >= max_model_len.
  *   out       the same shape, strides ldo_batch, ldo_head; may be mass.
@@ -825,8 +825,8 @@ idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq
                                  int num_pages, int page_size, const int32_t *block_table,
                                  int64_t bt_stride, const int32_t *context_lens, int ctx_per_row,
                                  int B, int next_n, int max_model_len, int H, int kv_heads, int D,
-                                 float scale, const float *lse, int64_t ld_lse, const float *mass,
-                                 int64_t ld_batch, int64_t ld_head, int width, float *out,
+                                 float scale, const float *lse, int64_t ld_lse,
+                                 int64_t ld_lse_head, const float *mass, int64_t ld_batch, int64_t ld_head, int width, float *out,
                                  int64_t ldo_batch, int64_t ldo_head, idx_stream_t stream);
 
 /* ------------------------------------------------------------------------

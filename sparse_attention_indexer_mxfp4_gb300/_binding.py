@@ -84,7 +84,7 @@ _SIGNATURES = {
     "idx_paged_kv4_attention": [_P, _L, _L, _P, _L, _I, _I, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I,
                                 ctypes.c_float, _P, _L, _L, _P, _L, _P, _S, _P],
     "idx_paged_kv4_weights": [_P, _L, _L, _P, _L, _I, _I, _P, _L, _P, _I, _I, _I, _I, _I, _I, _I,
-                              ctypes.c_float, _P, _L, _P, _L, _L, _I, _P, _L, _L, _P],
+                              ctypes.c_float, _P, _L, _L, _P, _L, _L, _I, _P, _L, _L, _P],
     "idx_kv4_evict": [_P, _L, _L, _I, _P, _I, _I, _I, _I, _I, _I, _P, _L, _I, _I, _P, _L, _I, _P, _L,
                       _I, _P, _P, _P, _P, _S, _P],
     "idx_get_device_status": [_P, ctypes.POINTER(ctypes.c_uint32)],

@@ -656,9 +656,8 @@ PyObject *paged_kv4_weights(PyObject *, PyObject *const *a, Py_ssize_t)
     const Paged p(a, a[13]);
     const at::Tensor &lse = tensor_of(a[10], "lse");
     if (lse.scalar_type() != at::kFloat || lse.dim() != 2 || lse.size(0) != p.R ||
-        lse.size(1) != p.H || ld(lse, 1, 1) != 1)
-        refuse("lse must be float32 [" + std::to_string(p.R) + ", " + std::to_string(p.H) +
-               "] with unit column stride");
+        lse.size(1) != p.H)
+        refuse("lse must be float32 [" + std::to_string(p.R) + ", " + std::to_string(p.H) + "]");
     at::Tensor mass, out;
     if (a[11] != Py_None)
         mass = need_mass(a[11], p.B, p.G, p.longest, "mass");
@@ -681,7 +680,7 @@ PyObject *paged_kv4_weights(PyObject *, PyObject *const *a, Py_ssize_t)
         count(p.pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
         (const int32_t *)address<int32_t>(p.table), p.table.size(1),
         (const int32_t *)address<int32_t>(p.lens), p.per_row, p.B, p.next, p.longest, p.H, p.G,
-        (int)kHead, float_of(a[8]), (const float *)address<float>(lse), ld(lse, 0, p.H),
+        (int)kHead, float_of(a[8]), (const float *)address<float>(lse), ld(lse, 0, p.H), ld(lse, 1, 1),
         mass.defined() ? (const float *)address<float>(mass) : nullptr,
         mass.defined() ? ld(mass, 0, p.G * width) : (int64_t)0,
         mass.defined() ? ld(mass, 1, width) : (int64_t)0, count(width, "out"),

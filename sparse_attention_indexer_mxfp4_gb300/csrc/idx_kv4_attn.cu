@@ -29,12 +29,14 @@
 // of its own and a ring of its own, filled by asynchronous copies (16 bytes, the
 // pieces of a row turned by its number so that fragments are read without bank
 // conflicts).  Work is the flat list of (row or sequence, key head, tile); CTAs
-// take equal contiguous shares of it and a second kernel joins what they cut.  The
-// ring runs on over the ends of a share's segments; there the warps hand their sums
+// take equal contiguous shares of it and a second kernel joins what they cut.  Few
+// units of few tiles go to a cluster of CTAs each instead, which joins its sums through
+// its shared memory: no second kernel.  The ring runs on over the ends of a share's segments; there the warps hand their sums
 // on in fragments, through the one place of the ring that is free.
 #include <algorithm>
 #include <atomic>
 #include <climits>
+#include <cooperative_groups.h>
 #include <float.h>
 
 #include "idx_kv4.cuh"
@@ -53,6 +55,9 @@ constexpr int kScaleUp = 1;             // and scaled values' up to 2 more
 constexpr int kScaleRange = 15;         // f16 holds 2 to 2^-14 without loss
 // Rows of few keys are not cut: no scratch and no joining kernel.
 constexpr int kUncutKeys = 4 * kTile;
+// Teams: CTAs of a cluster that share a unit, for up to kTeamTiles tiles a group, and
+// kTeamLeast in all.
+constexpr int kTeamMost = 8, kTeamTiles = 5, kTeamLeast = 256;
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 8;  // pieces of a unit that one warp joins
 
@@ -78,6 +83,7 @@ struct Kv4Args {
     float *lse;
     int64_t ld_lse;
     int uncut;        // units are not cut
+    int team;         // CTAs that share a unit (0: shares of the list)
     // A unit (a sequence's key head and block of columns) that is begun: sequence, head and
     // block, pieces, and twice the share that has the first, plus one where that is not the
     // share's first segment.  By unit, or where there are more of them than shares by the
@@ -88,7 +94,7 @@ struct Kv4Args {
     unsigned int *status;
     // weights of tokens
     const float *lse_in;
-    int64_t ld_lse_in;
+    int64_t ld_lse_in, ld_lse_head;
     const float *mass;
     int64_t ld_batch, ld_head;
     int width;
@@ -378,6 +384,33 @@ __device__ __forceinline__ void find_share(const Kv4Args &a, int heads, int64_t 
     s.tiles = (int)unit_tiles<kPaged>(a, s.b);
     s.hc = place / s.tiles;
     s.t = place - s.hc * s.tiles;
+}
+
+// The share of a group of a team: of one unit's tiles, by its number among the team's.
+// False where the rows list more than they may (there are no more rows than SMs).
+template <bool kPaged, int kGroups>
+__device__ __forceinline__ bool team_share(const Kv4Args &a, int heads, int64_t limit, Share &s)
+{
+    const int unit = blockIdx.x / a.team, groups = a.team * kGroups;
+    const int nth = (blockIdx.x - unit * a.team) * kGroups + threadIdx.x / kThreads;
+    s.b = unit / heads;
+    s.hc = unit - s.b * heads;
+    s.len = unit_len<kPaged>(a, s.b);
+    s.tiles = max(1, (s.len + kTile - 1) / kTile);
+    s.t = (int)((int64_t)s.tiles * nth / groups);
+    s.left = (int)((int64_t)s.tiles * (nth + 1) / groups) - s.t;
+    s.each = s.more = 0;
+    if (kPaged || a.B == 1)
+        return true;
+    uint32_t tiles = 0;
+    for (int b = lane_id(); b < a.B; b += 32)
+        tiles += (uint32_t)unit_tiles<kPaged>(a, b);
+    if (__reduce_add_sync(0xffffffffu, tiles) <= limit)
+        return true;
+    if (blockIdx.x == 0 && threadIdx.x == 0)
+        atomicOr(a.status, kDevBadBounds);
+    s.left = 0;
+    return false;
 }
 
 // A segment: tiles [t0, t1) of a unit.
@@ -677,7 +710,7 @@ __device__ __forceinline__ void load_queries(const Kv4Args &a, int b, int key_he
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // the largest to [2^14, 2^15); infinities and NaN stay what they are
         const int e = (int)(top >> 23);
-        const int up = e == 0 || e == 255 ? 0 : min(max(141 - e, -100), 100);
+        const int up = e == 0 || e == 255 ? 0 : min(141 - e, 126);
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
         const float back = __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2;
         #pragma unroll
@@ -799,6 +832,8 @@ struct Shape {
     // registers and shared memory hold.
     static constexpr int kGroups = NT == 1 ? 4 : NT == 2 ? 3 : 2;
     static constexpr int kPart = kCols * (kKv4Dim + 2);  // floats of a partial result
+    static constexpr int kRow = kKv4Dim + 4;  // of a column in a team's shared memory: a quad's columns
+                                              // fall into different banks
     template <int kMode>
     static constexpr int smem()
     {
@@ -863,7 +898,71 @@ __device__ __forceinline__ void take_sums(Sums<NT> &s, Place place, int warp, in
     }
 }
 
-template <int kMode, int NT>
+// A team's sums, joined by its CTAs, a column a warp; idle: this thread's group had no tile.
+template <int NT, int kRingBytes>
+__device__ __forceinline__ void join_team(const Kv4Args &a, uint8_t *smem, int b, int hc, bool idle)
+{
+    namespace cg = cooperative_groups;
+    using S = Shape<NT>;
+    constexpr int kCols = S::kCols, kGroups = S::kGroups, kAtOnce = 8;
+    const int lane = lane_id(), warp = threadIdx.x >> 5, group = warp / kWarps;
+    float *all = reinterpret_cast<float *>(smem);
+    constexpr int kStep = kWarps * kRingBytes / 4;  // floats between groups
+    constexpr int kStat = kCols * S::kRow;
+    if (idle && warp % kWarps == 0 && lane < kCols) {
+        all[group * kStep + kStat + lane] = -FLT_MAX;
+        all[group * kStep + kStat + kCols + lane] = 0.0f;
+    }
+    cg::cluster_group team = cg::this_cluster();
+    team.sync();
+    const int head = hc / a.blocks, cb = hc - head * a.blocks;
+    const int rank = (int)team.block_rank(), groups = a.team * kGroups;
+    for (int col = rank + a.team * warp; col < min(kCols, a.cols - cb * kCols);
+         col += a.team * kGroups * kWarps) {
+        float top = -FLT_MAX, sum = 0.0f;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int i0 = 0; i0 < groups; i0 += kAtOnce) {
+            float m[kAtOnce], l[kAtOnce];
+            float4 v[kAtOnce];
+            #pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                const int i = i0 + x;
+                m[x] = -FLT_MAX;
+                l[x] = 0.0f;
+                v[x] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i < groups) {
+                    const float *f = team.map_shared_rank(all, i / kGroups) + i % kGroups * kStep;
+                    m[x] = f[kStat + col];
+                    l[x] = f[kStat + kCols + col];
+                    v[x] = *reinterpret_cast<const float4 *>(f + col * S::kRow + 4 * lane);
+                }
+            }
+            #pragma unroll
+            for (int x = 0; x < kAtOnce; ++x) {
+                if (l[x] == 0.0f)  // no sums were written
+                    continue;
+                const float up = fmaxf(top, m[x]), mine = ex2(top - up), w = ex2(m[x] - up);
+                top = up;
+                sum = sum * mine + l[x] * w;
+                acc.x = acc.x * mine + v[x].x * w;
+                acc.y = acc.y * mine + v[x].y * w;
+                acc.z = acc.z * mine + v[x].z * w;
+                acc.w = acc.w * mine + v[x].w * w;
+            }
+        }
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int at = cb * kCols + col, j = at / a.group, h = head * a.group + at - j * a.group;
+        const int64_t row = (int64_t)b * a.next_n + j;
+        *reinterpret_cast<uint2 *>(a.out + row * a.ldo_row + h * a.ldo_head + 4 * lane) =
+            make_uint2(as_u32(__floats2bfloat162_rn(acc.x * inv, acc.y * inv)),
+                       as_u32(__floats2bfloat162_rn(acc.z * inv, acc.w * inv)));
+        if (a.lse && lane == 0)
+            a.lse[row * a.ld_lse + h] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    team.sync();  // the sums are read
+}
+
+template <int kMode, int NT, bool kTeam>
 __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     kv4_attention_kernel(const __grid_constant__ Kv4Args a)
 {
@@ -883,12 +982,18 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     pdl_launch_dependents();
     const int heads = a.pool.heads * a.blocks;
     const int64_t limit = kPaged || a.uncut ? INT64_MAX / INT_MAX : a.num_slots / kTile + a.B;
-    if (warp == 0 && lane == 0 && !a.uncut && !a.by_unit)
+    const bool cuts = !kTeam && !a.uncut;
+    if (warp == 0 && lane == 0 && cuts && !a.by_unit)
         a.ws_cut[p] = make_int4(0, 0, 0, 0);
     Share share;
-    find_share<kPaged, kGroups>(a, heads, limit, share);
+    bool good = true;
+    if constexpr (kTeam)
+        good = team_share<kPaged, kGroups>(a, heads, limit, share);
+    else
+        find_share<kPaged, kGroups>(a, heads, limit, share);
+    const int unit_b = share.b, unit_hc = share.hc;  // a team's
     // a list that is left alone (shares of nothing) has nothing to join
-    if (warp == 0 && lane == 0 && a.by_unit && !a.uncut && share.each == 0 && p < a.B * heads)
+    if (warp == 0 && lane == 0 && a.by_unit && cuts && share.each == 0 && p < a.B * heads)
         a.ws_cut[p] = make_int4(0, 0, 0, 0);
     R ring;
     ring.mem = smem + all_warp * R::kBytes;
@@ -899,6 +1004,7 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     int st = 0;            // the next place to read
     int spare = kStages - 1;  // the free one
     Seg seg;
+    const bool idle = share.left == 0;
     for (int nth = 0; next_seg<kPaged>(a, heads, share, seg); ++nth) {
         const int head = seg.hc / a.blocks, cb = seg.hc - head * a.blocks;
         const int tok0 = seg.t0 * kTile + warp * kSub;
@@ -1214,9 +1320,29 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
         take_sums<NT>(sum, place, all_warp + 2, 3 * group + 3);
 
         // ---- warp 0 has the segment's
+        if constexpr (kTeam) {
+            // (the group's rings are read, and nothing is in flight)
+            float *mine = reinterpret_cast<float *>(smem + group * kWarps * R::kBytes);
+            #pragma unroll
+            for (int n = 0; n < NT; ++n)
+                #pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int col = n * 8 + 2 * c + i;
+                    #pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        *reinterpret_cast<float4 *>(mine + col * S::kRow + 32 * y + 4 * g) =
+                            make_float4(o[2 * y][n][i], o[2 * y][n][i + 2], o[2 * y + 1][n][i],
+                                        o[2 * y + 1][n][i + 2]);
+                    if (g == 0) {
+                        mine[kCols * S::kRow + col] = m[n][i];
+                        mine[kCols * (S::kRow + 1) + col] = l[n][i];
+                    }
+                }
+            continue;
+        }
         const bool part = seg.t0 > 0 || seg.t1 < seg.tiles;
         float *to = a.ws_part + (int64_t)(2 * p + (nth > 0)) * S::kPart;
-        if ((part || a.by_unit) && !a.uncut && seg.t0 == 0 && lane == 0) {
+        if ((part || a.by_unit) && cuts && seg.t0 == 0 && lane == 0) {
             // the shares that hold the rest: `more - p - 1` longer ones first
             const int longer = max(0, share.more - p - 1), rest = seg.tiles - seg.t1;
             const int in = (int)min((int64_t)rest, (int64_t)longer * (share.each + 1));
@@ -1260,6 +1386,9 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
             }
     }
     cp_async_wait<0>();
+    if constexpr (kTeam)
+        if (good)  // (one answer for all CTAs)
+            join_team<NT, R::kBytes>(a, smem, unit_b, unit_hc, idle);
 }
 
 // Joins the pieces of a unit that several shares hold, blockIdx.x its entry.  A
@@ -1403,7 +1532,7 @@ __global__ void __launch_bounds__(WeightShape<NT>::kGroups * kThreads, 1)
                     if (col < a.cols) {
                         end[n][i] = row_end<true>(a, seg.b, j, seg.len);
                         const float v = a.lse_in[((int64_t)seg.b * a.next_n + j) * a.ld_lse_in +
-                                                 head * a.group + col - j * a.group];
+                                                 (head * a.group + col - j * a.group) * a.ld_lse_head];
                         z[n][i] = v == -INFINITY ? 0.0f : -v * kLog2e;
                         least = min(least, end[n][i]);
                     }
@@ -1503,6 +1632,21 @@ int part_of(int nt)
     return nt == 1 ? Shape<1>::kPart : nt == 2 ? Shape<2>::kPart : Shape<4>::kPart;
 }
 
+// CTAs of a team for so many units of at most so many tiles: enough for a tile a group,
+// as far as the SMs go; 0 where groups would have too many, or all tiles are so few
+// that their pieces are joined sooner than a cluster starts (us, list and teams: 28
+// tiles 8.4 and 9.3, 256 11.5 and 11.1, 512 14.6 and 13.0, 648 14.5 and 11.8).
+int team_of(int64_t units, int64_t tiles, int nt)
+{
+    const int sms = sm_count(), groups = groups_of(nt);
+    if (units > sms || units * tiles < kTeamLeast)
+        return 0;
+    int team = 1;
+    while (team < kTeamMost && 2 * team * units <= sms && tiles > (int64_t)team * groups)
+        team *= 2;
+    return tiles <= (int64_t)kTeamTiles * team * groups ? team : 0;
+}
+
 size_t cut_bytes(int shares)
 {
     return ((size_t)shares * sizeof(int4) + 255) / 256 * 256;
@@ -1526,18 +1670,44 @@ bool raise_smem(F kernel, int smem, std::atomic<uint64_t> &ready)
 }
 
 template <int kMode, int NT>
+idx_status launch_team(const Kv4Args &a, cudaStream_t stream)
+{
+    constexpr int smem = Shape<NT>::template smem<kMode>();
+    static std::atomic<uint64_t> ready{0};
+    if (!raise_smem(kv4_attention_kernel<kMode, NT, true>, smem, ready))
+        return IDX_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)a.team;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.B * a.pool.heads * a.blocks * a.team));
+    cfg.blockDim = dim3(Shape<NT>::kGroups * kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return launch_status(cudaLaunchKernelEx(&cfg, kv4_attention_kernel<kMode, NT, true>, a));
+}
+
+template <int kMode, int NT>
 idx_status launch_attention(Kv4Args &a, int64_t tiles, cudaStream_t stream)
 {
-    const int ctas = (int)std::min<int64_t>(sm_count(), tiles);
-    const int shares = ctas * Shape<NT>::kGroups;
     constexpr int smem = Shape<NT>::template smem<kMode>();
     static_assert(smem <= 226 * 1024, "shared memory of a CTA");
+    if (a.team)
+        return launch_team<kMode, NT>(a, stream);
     static std::atomic<uint64_t> ready{0};
-    if (!raise_smem(kv4_attention_kernel<kMode, NT>, smem, ready))
+    if (!raise_smem(kv4_attention_kernel<kMode, NT, false>, smem, ready))
         return IDX_ERR_CUDA;
     const int64_t units = (int64_t)a.B * a.pool.heads * a.blocks;
+    const int ctas = (int)std::min<int64_t>(sm_count(), tiles);
+    const int shares = ctas * Shape<NT>::kGroups;
     a.by_unit = units < shares;
-    cudaError_t e = launch_pdl(kv4_attention_kernel<kMode, NT>, dim3(ctas),
+    cudaError_t e = launch_pdl(kv4_attention_kernel<kMode, NT, false>, dim3(ctas),
                                dim3(Shape<NT>::kGroups * kThreads), smem, stream, a);
     if (e == cudaSuccess && !a.uncut) {
         // many pieces of few units: a block's warps share a column's
@@ -1589,8 +1759,9 @@ idx_status run_attention(Kv4Args &a, int64_t keys, int64_t most_tiles, void *ws,
 {
     const int nt = tiles_of(a.cols);
     a.blocks = (a.cols + 8 * nt - 1) / (8 * nt);
-    a.uncut = keys <= kUncutKeys;
     const int64_t units = (int64_t)a.B * a.pool.heads * a.blocks;
+    a.team = team_of(units, (keys + kTile - 1) / kTile, nt);
+    a.uncut = !a.team && keys <= kUncutKeys;
     const int64_t tiles = a.uncut ? units : most_tiles * a.pool.heads * a.blocks;
     if ((int64_t)a.pool.heads * a.blocks > INT32_MAX / 2 || most_tiles > INT32_MAX / ((int64_t)a.pool.heads * a.blocks))
         return IDX_ERR_UNSUPPORTED;
@@ -1622,6 +1793,9 @@ extern "C" size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int
         return 0;
     const int64_t cols = (int64_t)next_n * (H / kv_heads);
     const int nt = tiles_of((int)std::min<int64_t>(cols, 32)), most = sm_count() * groups_of(nt);
+    const int64_t units = (int64_t)(R / next_n) * kv_heads * ((cols + 8 * nt - 1) / (8 * nt));
+    if (team_of(units, (max_keys + kTile - 1) / kTile, nt))
+        return 0;
     return cut_bytes(most) + (size_t)2 * most * part_of(nt) * sizeof(float);
 }
 
@@ -1724,7 +1898,7 @@ extern "C" idx_status idx_paged_kv4_weights(
     int64_t page_stride_bytes, int num_pages, int page_size, const int32_t *block_table,
     int64_t bt_stride, const int32_t *context_lens, int ctx_per_row, int B, int next_n,
     int max_model_len, int H, int kv_heads, int D, float scale, const float *lse, int64_t ld_lse,
-    const float *mass, int64_t ld_batch, int64_t ld_head, int width, float *out, int64_t ldo_batch,
+    int64_t ld_lse_head, const float *mass, int64_t ld_batch, int64_t ld_head, int width, float *out, int64_t ldo_batch,
     int64_t ldo_head, idx_stream_t stream)
 {
     IDX_NVTX_RANGE("idx_paged_kv4_weights");
@@ -1733,7 +1907,7 @@ extern "C" idx_status idx_paged_kv4_weights(
         return IDX_ERR_INVALID_ARG;
     if (B == 0 || width == 0)
         return IDX_OK;
-    if (!context_lens || (max_model_len > 0 && !block_table) || !lse || ld_lse < H || !out ||
+    if (!context_lens || (max_model_len > 0 && !block_table) || !lse || ld_lse < 0 || ld_lse_head < 0 || !out ||
         ld_batch < 0 || ld_head < 0 || ldo_batch < 0 || ldo_head < 0)
         return IDX_ERR_INVALID_ARG;
     idx_status ok = check_attention(q, ldq_row, ldq_head, H, kv_heads, D, scale);
@@ -1766,6 +1940,7 @@ extern "C" idx_status idx_paged_kv4_weights(
     a.scale_log2 = scale * kLog2e;
     a.lse_in = lse;
     a.ld_lse_in = ld_lse;
+    a.ld_lse_head = ld_lse_head;
     a.mass = mass;
     a.ld_batch = ld_batch;
     a.ld_head = ld_head;

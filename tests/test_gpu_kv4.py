@@ -371,6 +371,35 @@ def test_strides_outputs_and_scratch():
         assert torch.equal(again, first[0]) and torch.equal(again, out)
 
 
+def test_few_units_need_no_scratch():
+    """A cluster's shared memory holds the sums of few units of few tiles."""
+    f = B.kv4_attention_workspace_size
+    assert f(1, 16, 2, 20000) == 0 and f(1, 16, 2, 200000) > 0 and f(200, 16, 2, 2048) > 0
+    assert f(1, 16, 2, 600) > 0  # too few to pay for a cluster
+
+
+@pytest.mark.parametrize("n", [129, 640, 2049, 5000, 16384])
+@pytest.mark.parametrize("rows,heads,group", [(1, 1, 1), (3, 2, 8), (2, 8, 16), (1, 3, 40), (30, 4, 2)])
+def test_units_shared_by_teams(n, rows, heads, group):
+    """Every size of a cluster, groups of it with a tile and without, rows without tokens among them."""
+    rng = np.random.default_rng(n + rows)
+    lens = [n] + [int(x) for x in rng.integers(0, min(n, 600), rows - 1)]
+    if rows > 2:
+        lens[1] = 0
+    page = 64
+    pool = ref.make_pool(rng, 40, page, heads, 0, 2)
+    sets = [rng.integers(0, 40 * page, m) for m in lens]
+    q, q64 = _bf16(rng.standard_normal((rows, heads * group, 128)) * 2)
+    indptr = _dev(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    args = (q, _dev(pool), page, heads, _dev(np.concatenate(sets).astype(np.int32)), indptr, SCALE)
+    out, lse = B.idx_kv4_attention(*args)
+    _clean()
+    some = sorted({0, min(1, rows - 1), rows - 1})
+    _check_rows(out[some], lse[some], q64[some], pool, page, heads, [sets[r] for r in some])
+    again = B.idx_kv4_attention(*args)
+    assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
 def test_many_sequences():
     """More sequences than a block has threads, most of them empty or short."""
     rng = np.random.default_rng(15)
@@ -415,6 +444,7 @@ def test_weights(ctx, next_n, heads, group):
     ends = [max(0, c - next_n + 1 + j) for c in ctx for j in range(next_n)]
     args = (q, _dev(pool), page, heads, _dev(bt), _dev(np.array(ctx, np.int32)), next_n, SCALE, bt.shape[1] * page)
     _, lse = B.idx_paged_kv4_attention(*args)
+    lse = torch.stack([lse.t(), lse.t()], 1)[:, 0].t()  # any strides
     wide = torch.rand(len(ctx), heads, width + 2, device="cuda")
     mass = wide[:, :, 1:-1]
     before = _np(mass)

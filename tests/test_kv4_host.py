@@ -82,7 +82,7 @@ def test_gather_refusals():
 
 
 def test_attention_refusals():
-    base = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, FAKE, 1000, 4, 64, 8, 128, 0.1, FAKE, 8192, 128, FAKE, 64, FAKE,
+    base = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, FAKE, 90000, 4, 64, 8, 128, 0.1, FAKE, 8192, 128, FAKE, 64, FAKE,
             1 << 40, None]
     p = dict(q=0, qr=1, qh=2, pages=3, stride=4, np=5, P=6, slots=7, indptr=8, ns=9, R=10, H=11, G=12, D=13, scale=14, out=15,
              outr=16, oh=17, ldl=19, ws=20, wsb=21)
@@ -98,24 +98,25 @@ def test_attention_refusals():
 
 
 def test_paged_refusals():
-    base = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, 16, FAKE, 0, 2, 2, 1000, 64, 8, 128, 0.1, FAKE, 8192, 128, None, 0,
-            FAKE, 1 << 40, None]
+    base = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, 1600, FAKE, 0, 2, 2, 100000, 64, 8, 128, 0.1, FAKE, 8192, 128, None,
+            0, FAKE, 1 << 40, None]
     p = dict(q=0, bt=7, bts=8, ctx=9, B=11, n=12, mml=13, H=14, G=15, out=18, ws=23, wsb=24)
     call = _caller("idx_paged_kv4_attention", base, p)
     assert call(B=0) == 0
-    _refused(call, INVALID, (dict(B=-1), dict(n=0), dict(mml=-1), dict(bts=15), dict(bt=None), dict(ctx=None), dict(q=None)))
+    _refused(call, INVALID, (dict(B=-1), dict(n=0), dict(mml=-1), dict(bts=1562), dict(bt=None), dict(ctx=None), dict(q=None)))
     _refused(call, UNSUPPORTED, (dict(B=2 ** 30, n=4), dict(H=20), dict(out=FAKE + 2)))
     assert call(wsb=0) == WORKSPACE
 
 
 def test_weights_refusals():
-    base = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, 16, FAKE, 0, 2, 2, 1000, 64, 8, 128, 0.1, FAKE, 64, FAKE, 9000, 1000,
-            1000, FAKE + 64, 9000, 1000, None]
-    p = dict(q=0, bts=8, ctx=9, B=11, n=12, mml=13, H=14, lse=18, ldl=19, mass=20, lb=21, lh=22, width=23, out=24, ob=25, oh=26)
+    base = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, 16, FAKE, 0, 2, 2, 1000, 64, 8, 128, 0.1, FAKE, 64, 1, FAKE, 9000,
+            1000, 1000, FAKE + 64, 9000, 1000, None]
+    p = dict(q=0, bts=8, ctx=9, B=11, n=12, mml=13, H=14, lse=18, ldl=19, ldlh=20, mass=21, lb=22, lh=23, width=24, out=25,
+             ob=26, oh=27)
     call = _caller("idx_paged_kv4_weights", base, p)
     assert call(B=0) == 0
-    _refused(call, INVALID, (dict(B=-1), dict(n=0), dict(width=999), dict(bts=15), dict(lse=None), dict(ldl=63),
-                             dict(out=None), dict(lb=-1), dict(oh=-1), dict(mass=FAKE + 64, lb=9001)))
+    _refused(call, INVALID, (dict(B=-1), dict(n=0), dict(width=999), dict(bts=15), dict(lse=None), dict(ldl=-1),
+                             dict(ldlh=-1), dict(out=None), dict(lb=-1), dict(oh=-1), dict(mass=FAKE + 64, lb=9001)))
     _refused(call, UNSUPPORTED, (dict(H=20), dict(q=FAKE + 4), dict(B=2 ** 30, n=4)))
 
 
@@ -152,8 +153,8 @@ def test_grouped_prefill_refusals():
 def test_scratch_of_nothing():
     L = B.lib()
     f, g, e = L.idx_kv4_attention_workspace_size, L.idx_grouped_prefill_workspace_size, L.idx_kv4_evict_workspace_size
-    assert f(0, 1, 64, 8, 9999) == 0 and f(4, 1, 64, 8, 512) == 0 and f(4, 1, 64, 8, 513) > 0
-    assert f(4, 4, 64, 8, 513) > f(4, 1, 64, 8, 513)  # wider blocks of columns
+    assert f(0, 1, 64, 8, 9999) == 0 and f(400, 1, 64, 8, 512) == 0 and f(400, 1, 64, 8, 513) > 0
+    assert f(400, 4, 64, 8, 513) > f(400, 1, 64, 8, 513)  # wider blocks of columns
     assert g(0, 999, 64) == 0 and g(4, 512, 64) == 0 and g(4, 513, 64) > 0
     # what a cluster holds needs none
     n = 1 << 19

@@ -15,6 +15,7 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 // (8191 tokens x 8 heads written and read back: four 21.2 us, eight 27.1, two 25.7);
 // where there are fewer than fill the SMs, one (128 tokens 5.0 -> 4.3 us).
 constexpr int kItemsMany = 4;
+constexpr int kShortSum = 2048;  // columns of a summed list that one CTA selects from
 
 // ----------------------------------------------------------------- the store
 //
@@ -313,8 +314,10 @@ struct Weights {
     }
 };
 
-// Short lists of single heads: a CTA each, the keys in its registers (4 sequences
-// x 8 heads of up to 8192 tokens to 2048 in clusters 16.9 us, here 10.4).
+// Short lists, of single heads or (kSum) summed over them: a CTA each, the keys in
+// its registers (4 sequences x 8 heads of up to 8192 tokens to 2048 in clusters 16.9
+// us, here 10.4).
+template <bool kSum>
 __global__ void __launch_bounds__(topk_short::kThreads, 3)
     evict_short_kernel(const Weights src, int k, int32_t *__restrict__ out, int64_t ld_out)
 {
@@ -325,6 +328,19 @@ __global__ void __launch_bounds__(topk_short::kThreads, 3)
     pdl_launch_dependents();
     const int len = src.len(row), nrun = (len + 4 * T::kThreads - 1) / (4 * T::kThreads);
     const EvictArgs &a = src.a;
+    uint32_t key[T::kSteps][4];
+    if constexpr (kSum) {
+        #pragma unroll
+        for (int s = 0; s < T::kSteps; ++s) {
+            key[s][0] = key[s][1] = key[s][2] = key[s][3] = 0u;
+            if (s < nrun)
+                src.run(row, 0, 4 * (s * T::kThreads + tid), len, key[s]);
+        }
+        regsel::select_write<T::kThreads, T::kSteps>(
+            sh, key, k, out + (size_t)row * ld_out,
+            [&](int s, int e) -> int32_t { return s * 4 * T::kThreads + 4 * tid + e; }, nrun);
+        return;
+    }
     const float *m = a.mass + row / a.heads * a.ld_batch + row % a.heads * a.ld_head;
     float4 v[T::kSteps];
     #pragma unroll
@@ -340,7 +356,6 @@ __global__ void __launch_bounds__(topk_short::kThreads, 3)
             v[s].w = at + 3 < len ? __ldg(m + at + 3) : 0.0f;
         }
     }
-    uint32_t key[T::kSteps][4];
     #pragma unroll
     for (int s = 0; s < T::kSteps; ++s) {
         const int at = 4 * (s * T::kThreads + tid);
@@ -457,7 +472,11 @@ cudaError_t select_on_chip(const EvictArgs &a, int chosen, cudaStream_t stream)
     const int rows = a.B * a.lists;
     const int vec_ok = (a.ld_batch | a.ld_head) % 4 == 0 && aligned16(a.mass);
     if (a.lists == a.heads && a.ld <= topk_short::kMaxLen)
-        return launch_pdl(evict_short_kernel, dim3(rows), dim3(topk_short::kThreads), 0, stream,
+        return launch_pdl(evict_short_kernel<false>, dim3(rows), dim3(topk_short::kThreads), 0, stream,
+                          Weights{a, vec_ok}, chosen, a.keep, (int64_t)a.budget);
+    // (a CTA alone reads a run of a few heads' weights in about a microsecond)
+    if (a.ld <= kShortSum)
+        return launch_pdl(evict_short_kernel<true>, dim3(rows), dim3(topk_short::kThreads), 0, stream,
                           Weights{a, vec_ok}, chosen, a.keep, (int64_t)a.budget);
     const int least = (a.ld + T::kChunk - 1) / T::kChunk, most = (a.ld + 2047) / 2048;
     const int C = std::max(least, std::min({T::kMaxCluster, most, sm_count() / rows}));

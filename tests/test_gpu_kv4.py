@@ -220,7 +220,8 @@ def _paged_sets(bt, ends, page, next_n):
 
 
 @pytest.mark.parametrize("ctx", [[1], [0, 40, 129], [512, 513, 2, 1000], [3000, 65]])
-@pytest.mark.parametrize("next_n,heads,group,page", [(1, 2, 8, 64), (2, 1, 5, 16), (4, 2, 8, 64), (3, 1, 16, 100), (1, 8, 4, 128)])
+@pytest.mark.parametrize("next_n,heads,group,page", [(1, 2, 8, 64), (2, 1, 5, 16), (4, 2, 8, 64), (3, 1, 16, 100), (1, 8, 4, 128),
+                                                       (2, 3, 3, 32), (1, 2, 12, 96)])
 def test_whole_contexts(ctx, next_n, heads, group, page):
     rng = np.random.default_rng(sum(ctx) + next_n)
     bt, pages, _ = _table(rng, ctx, page)
@@ -400,6 +401,54 @@ def test_units_shared_by_teams(n, rows, heads, group):
     assert torch.equal(again[0], out) and torch.equal(again[1], lse)
 
 
+def test_teams_captured_and_beside_one_another():
+    """A cluster's calls captured and replayed, and two of them at once on two streams."""
+    rng = np.random.default_rng(50)
+    page, heads, n = 64, 2, 9000
+    bt, pages, _ = _table(rng, [n, 7000], page)
+    pool = _dev(ref.make_pool(rng, pages, page, heads))
+    ctx, table = _dev(np.array([n, 7000], np.int32)), _dev(bt)
+    qs = [_bf16(rng.standard_normal((2, 16, 128)))[0] for _ in range(2)]
+    call = lambda q, s=None: B.idx_paged_kv4_attention(q, pool, page, heads, table, ctx, 1, SCALE, n, stream=s)  # noqa: E731
+    assert B.kv4_attention_workspace_size(2, 16, heads, n) == 0
+    want = [call(q) for q in qs]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in qs]
+    got = [[call(q, s) for q, s in zip(qs, sides)] for _ in range(20)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for turn in got for g, w in zip(turn, want) for x, y in zip(g, w))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(qs[0])
+    for x in out:
+        x.zero_()
+    graph.replay()
+    _clean()
+    assert all(torch.equal(x, y) for x, y in zip(out, want[0]))
+
+
+def test_calls_beside_one_another():
+    """Cut rows on two streams, each with scratch of its own, and one scratch for calls in turn."""
+    rng = np.random.default_rng(51)
+    page, heads = 64, 4
+    pool = _dev(ref.make_pool(rng, 60, page, heads))
+    slots = _dev(rng.integers(0, 60 * page, 60 * 700).astype(np.int32))
+    indptr = _dev((700 * np.arange(61)).astype(np.int32))
+    qs = [_bf16(rng.standard_normal((60, 16, 128)))[0] for _ in range(2)]
+    size = B.kv4_attention_workspace_size(60, 16, heads, slots.numel())
+    assert size > 0
+    args = (pool, page, heads, slots, indptr, SCALE)
+    want = [B.idx_kv4_attention(q, *args) for q in qs]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in qs]
+    got = [[B.idx_kv4_attention(q, *args, stream=s) for q, s in zip(qs, sides)] for _ in range(20)]
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    turns = [B.idx_kv4_attention(q, *args, workspace=ws) for q in qs for _ in range(3)]
+    _clean()
+    assert all(torch.equal(x, y) for turn in got for g, w in zip(turn, want) for x, y in zip(g, w))
+    assert all(torch.equal(x, y) for g, w in zip(turns, [want[0]] * 3 + [want[1]] * 3) for x, y in zip(g, w))
+
+
 def test_many_sequences():
     """More sequences than a block has threads, most of them empty or short."""
     rng = np.random.default_rng(15)
@@ -433,10 +482,10 @@ def test_pages_past_32_bits():
 # ---------------------------------------------------------------------- weights
 
 
+@pytest.mark.parametrize("page", [64, 16, 100])
 @pytest.mark.parametrize("ctx,next_n,heads,group", [([1], 1, 1, 1), ([0, 40, 700], 2, 2, 4), ([513], 4, 1, 20), ([300, 129], 1, 3, 8)])
-def test_weights(ctx, next_n, heads, group):
+def test_weights(ctx, next_n, heads, group, page):
     rng = np.random.default_rng(sum(ctx) + group)
-    page = 64
     bt, pages, _ = _table(rng, ctx, page)
     pool = ref.make_pool(rng, pages, page, heads)
     width = bt.shape[1] * page + 30

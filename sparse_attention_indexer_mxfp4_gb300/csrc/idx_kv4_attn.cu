@@ -2,7 +2,7 @@
 // slots or whole paged contexts, and the weights it gives the cached tokens.
 //
 // For one key head, the columns are the query heads that share it (of all rows
-// of a sequence), in blocks of 8, 16 or 32; tokens are the other side:
+// of a sequence), in blocks of 8 or 16; tokens are the other side:
 //
 //     S^T [32 tokens x cols] = K [32 x 128] . Q^T,   O^T [128 x cols] += V^T . P^T
 //
@@ -830,7 +830,7 @@ struct Shape {
     static constexpr int kStages = 2;  // (three: no faster, and less of L1)
     // Groups of kWarps warps with shares of their own: an SM has one CTA of as many as
     // registers and shared memory hold.
-    static constexpr int kGroups = NT == 1 ? 4 : NT == 2 ? 3 : 2;
+    static constexpr int kGroups = NT == 1 ? 4 : 3;
     static constexpr int kPart = kCols * (kKv4Dim + 2);  // floats of a partial result
     static constexpr int kRow = kKv4Dim + 4;  // of a column in a team's shared memory: a quad's columns
                                               // fall into different banks
@@ -1616,20 +1616,21 @@ __global__ void __launch_bounds__(WeightShape<NT>::kGroups * kThreads, 1)
 
 // ---------------------------------------------------------------------- host
 
-// Columns of a block: 8, 16 or 32.
+// Columns of a block, in eights (32 sequences of 4 key heads: 32 columns as two
+// blocks of 16 182 us, as one of 32, which spills, 189; 24 180 and 186).
 int tiles_of(int cols)
 {
-    return cols <= 8 ? 1 : cols <= 16 ? 2 : 4;
+    return cols <= 8 ? 1 : 2;
 }
 
 int groups_of(int nt)
 {
-    return nt == 1 ? Shape<1>::kGroups : nt == 2 ? Shape<2>::kGroups : Shape<4>::kGroups;
+    return nt == 1 ? Shape<1>::kGroups : Shape<2>::kGroups;
 }
 
 int part_of(int nt)
 {
-    return nt == 1 ? Shape<1>::kPart : nt == 2 ? Shape<2>::kPart : Shape<4>::kPart;
+    return nt == 1 ? Shape<1>::kPart : Shape<2>::kPart;
 }
 
 // CTAs of a team for so many units of at most so many tiles: enough for a tile a group,
@@ -1747,9 +1748,7 @@ idx_status check_attention(const void *q, int64_t ldq_row, int64_t ldq_head, int
 template <int kMode>
 idx_status launch_columns(Kv4Args &a, int nt, int64_t tiles, cudaStream_t s)
 {
-    return nt == 1 ? launch_attention<kMode, 1>(a, tiles, s)
-         : nt == 2 ? launch_attention<kMode, 2>(a, tiles, s)
-                   : launch_attention<kMode, 4>(a, tiles, s);
+    return nt == 1 ? launch_attention<kMode, 1>(a, tiles, s) : launch_attention<kMode, 2>(a, tiles, s);
 }
 
 // Fills in what a launch needs and launches.
@@ -1951,7 +1950,9 @@ extern "C" idx_status idx_paged_kv4_weights(
     a.status = device_status_ptr();
     if (!a.status)
         return IDX_ERR_CUDA;
-    const int nt = tiles_of(a.cols);
+    // (without values there are registers for 32: 32 sequences of 4 key heads 111 us, as two
+    // blocks 117)
+    const int nt = a.cols <= 8 ? 1 : a.cols <= 16 ? 2 : 4;
     a.blocks = (a.cols + 8 * nt - 1) / (8 * nt);
     // the tiles of the contexts, and at least a warp for 512 columns past them
     const int64_t work = std::max<int64_t>(tiles * kv_heads,

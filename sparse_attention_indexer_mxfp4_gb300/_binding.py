@@ -1,4 +1,4 @@
-"""Thin binding of libidx.so (include/idx.h): ctypes, and for the latent calls
+"""Thin binding of libidx.so (include/idx.h): ctypes, and for the latent and grouped calls
 an extension that does the same natively (csrc/bind_latent.cpp).
 
 Argument marshalling only: every function takes torch CUDA tensors, checks

@@ -31,8 +31,14 @@
 // conflicts).  Work is the flat list of (row or sequence, key head, tile); CTAs
 // take equal contiguous shares of it and a second kernel joins what they cut.  Few
 // units of few tiles go to a cluster of CTAs each instead, which joins its sums through
-// its shared memory: no second kernel.  The ring runs on over the ends of a share's segments; there the warps hand their sums
-// on in fragments, through the one place of the ring that is free.
+// its shared memory: no second kernel.  The ring runs on over the ends of a share's
+// segments; there the warps hand their sums on in fragments, through the one place of
+// the ring that is free.
+//
+// Measured: 32 contexts of 4096 to 32768 tokens x 8 key heads, 4 columns, 125 us (690
+// MB, 0.81 of the copy rate; 0.64 instructions a cycle and scheduler bound it); 4 of 100 to 131
+// thousand, 16 columns, 139; 64 rows x 2048 slots x 8 key heads 50 to 57.  Rings filled
+// by bulk tensor copies and barriers took 134 and 154 for the first two.
 #include <algorithm>
 #include <atomic>
 #include <climits>

@@ -746,8 +746,9 @@ idx_status idx_kv4_store(const uint16_t *k, int64_t ldk_row, int64_t ldk_head, c
  * idx_kv4_gather -- read cached tokens back as rows of bf16 (which holds every
  * value of magnitude below 2^128 exactly), for a later chunk of a prompt.
  * block_table, max_blocks, cu_lens, seq_starts, N and the errors as
- * idx_latent_gather; k_out, v_out bf16 bits [N, kv_heads, 128] with strides
- * (multiples of 8), 16-byte aligned.
+ * idx_latent_gather (and a cu_lens[B] below zero sets IDX_DEV_BAD_BOUNDS, nothing is
+ * written); k_out, v_out bf16 bits [N, kv_heads, 128] with strides (multiples of 8),
+ * 16-byte aligned.
  * ---------------------------------------------------------------------- */
 idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_stride_bytes, int num_pages,
                           int page_size, int kv_heads, int D, const int32_t *block_table,

@@ -135,9 +135,10 @@ __global__ void __launch_bounds__(kThreads)
     uint16_t *dst = side ? v_out : k_out;
     const int64_t ld_row = side ? ldv_row : ldk_row, ld_head = side ? ldv_head : ldk_head;
     const int end = cu[B];
-    if (blockIdx.x == 0 && threadIdx.x == 0 && end > N)
+    if (blockIdx.x == 0 && threadIdx.x == 0 && (end < 0 || end > N))
         atomicOr(status, kDevBadBounds);
-    const int rows = min(N, end);
+    // (products with parts are unsigned: a bound below zero would wrap)
+    const uint32_t rows = max(0, min(N, end));
     // a warp has the heads of a row, kItems at a time
     const uint32_t parts = (pool.heads + kItems - 1) / kItems;
     const uint32_t step = gridDim.x * kWarps;

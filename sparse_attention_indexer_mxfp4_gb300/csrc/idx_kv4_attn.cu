@@ -392,6 +392,45 @@ __device__ __forceinline__ void find_share(const Kv4Args &a, int heads, int64_t 
     s.t = place - s.hc * s.tiles;
 }
 
+// The tiles that rows which are not cut list, though their shares count a unit each: of
+// few rows four a lane, whose bounds are read beside the first look-ups and added up later.
+struct Listed {
+    static constexpr int kFew = 128, kEach = kFew / 32;
+    int bound[kEach + 1];
+
+    __device__ __forceinline__ void look(const Kv4Args &a)
+    {
+        if (a.B <= kFew)
+            #pragma unroll
+            for (int i = 0; i <= kEach; ++i)
+                bound[i] = a.indptr[min(kEach * lane_id() + i, a.B)];
+    }
+    // Whether they are more than num_slots tokens in B rows have: one answer for all threads
+    // of all CTAs.
+    template <int kGroups>
+    __device__ __forceinline__ bool too_many(const Kv4Args &a) const
+    {
+        const auto tiles = [&](int lo, int hi) {
+            const int most = (int)a.num_slots;
+            return max(1, (min(max(hi, 0), most) - min(max(lo, 0), most) + kTile - 1) / kTile);
+        };
+        const int64_t limit = a.num_slots / kTile + a.B;
+        if (a.B <= kFew) {
+            uint32_t n = 0;
+            #pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                n += kEach * lane_id() + i < a.B ? tiles(bound[i], bound[i + 1]) : 0;
+            return __reduce_add_sync(0xffffffffu, n) > limit;
+        }
+        __shared__ int64_t wsum[kGroups * kWarps];
+        int64_t n = 0, all;
+        for (int b = threadIdx.x; b < a.B; b += kGroups * kThreads)
+            n += tiles(a.indptr[b], a.indptr[b + 1]);
+        block_scan<kGroups * kWarps>(n, wsum, all);
+        return all > limit;
+    }
+};
+
 // The share of a group of a team: of one unit's tiles, by its number among the team's.
 // False where the rows list more than they may (there are no more rows than SMs).
 template <bool kPaged, int kGroups>
@@ -968,7 +1007,9 @@ __device__ __forceinline__ void join_team(const Kv4Args &a, uint8_t *smem, int b
     team.sync();  // the sums are read
 }
 
-template <int kMode, int NT, bool kTeam>
+// kListed: rows by slots that are not cut, whose tiles are counted against the slots' (an
+// instance of its own: the count costs calls that go without it 0.2 us).
+template <int kMode, int NT, bool kTeam, bool kListed>
 __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     kv4_attention_kernel(const __grid_constant__ Kv4Args a)
 {
@@ -991,6 +1032,9 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     const bool cuts = !kTeam && !a.uncut;
     if (warp == 0 && lane == 0 && cuts && !a.by_unit)
         a.ws_cut[p] = make_int4(0, 0, 0, 0);
+    Listed listed;
+    if constexpr (kListed)
+        listed.look(a);
     Share share;
     bool good = true;
     if constexpr (kTeam)
@@ -1007,6 +1051,12 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
     #pragma unroll
     for (int i = 0; i < kStages - 1; ++i)
         ring.fill(a, heads, a.blocks, warp, i);
+    if constexpr (kListed)
+        if (listed.too_many<kGroups>(a)) {  // (the first copies are on their way)
+            if (blockIdx.x == 0 && threadIdx.x == 0)
+                atomicOr(a.status, kDevBadBounds);
+            share.left = 0;
+        }
     int st = 0;            // the next place to read
     int spare = kStages - 1;  // the free one
     Seg seg;
@@ -1681,7 +1731,7 @@ idx_status launch_team(const Kv4Args &a, cudaStream_t stream)
 {
     constexpr int smem = Shape<NT>::template smem<kMode>();
     static std::atomic<uint64_t> ready{0};
-    if (!raise_smem(kv4_attention_kernel<kMode, NT, true>, smem, ready))
+    if (!raise_smem(kv4_attention_kernel<kMode, NT, true, false>, smem, ready))
         return IDX_ERR_CUDA;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1697,7 +1747,7 @@ idx_status launch_team(const Kv4Args &a, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return launch_status(cudaLaunchKernelEx(&cfg, kv4_attention_kernel<kMode, NT, true>, a));
+    return launch_status(cudaLaunchKernelEx(&cfg, kv4_attention_kernel<kMode, NT, true, false>, a));
 }
 
 template <int kMode, int NT>
@@ -1707,14 +1757,17 @@ idx_status launch_attention(Kv4Args &a, int64_t tiles, cudaStream_t stream)
     static_assert(smem <= 226 * 1024, "shared memory of a CTA");
     if (a.team)
         return launch_team<kMode, NT>(a, stream);
-    static std::atomic<uint64_t> ready{0};
-    if (!raise_smem(kv4_attention_kernel<kMode, NT, false>, smem, ready))
+    static std::atomic<uint64_t> ready[2]{};
+    const bool listed = kMode == kSlots && a.uncut;
+    const auto kernel = listed ? kv4_attention_kernel<kMode, NT, false, kMode == kSlots>
+                               : kv4_attention_kernel<kMode, NT, false, false>;
+    if (!raise_smem(kernel, smem, ready[listed]))
         return IDX_ERR_CUDA;
     const int64_t units = (int64_t)a.B * a.pool.heads * a.blocks;
     const int ctas = (int)std::min<int64_t>(sm_count(), tiles);
     const int shares = ctas * Shape<NT>::kGroups;
     a.by_unit = units < shares;
-    cudaError_t e = launch_pdl(kv4_attention_kernel<kMode, NT, false>, dim3(ctas),
+    cudaError_t e = launch_pdl(kernel, dim3(ctas),
                                dim3(Shape<NT>::kGroups * kThreads), smem, stream, a);
     if (e == cudaSuccess && !a.uncut) {
         // many pieces of few units: a block's warps share a column's

@@ -27,3 +27,27 @@ def test_gather_bounds_below_zero(heads, rows, last):
                      out[:rows, :, 1])
     assert _status() == (B.DEV_BAD_BOUNDS if last < 0 else 0)
     assert (out == 9).all()
+
+
+@pytest.mark.parametrize("rows", [3, 20, 300])
+def test_short_lists_that_descend(rows):
+    """A list of few slots whose bounds descend is told of and left alone like a long one."""
+    rng = np.random.default_rng(rows)
+    pool = ref.make_pool(rng, 8, 64, 1)
+    slots = rng.integers(0, 512, 500)
+    q, q64 = _bf16(rng.standard_normal((rows, 2, 128)))
+    out = torch.full((rows, 2, 128), 5.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows, 2), 5.0, device="cuda")
+    args = (q, _dev(pool), 64, 1, _dev(slots.astype(np.int32)))
+    bounds = np.array(([0, 500] * rows)[:rows + 1], np.int32)
+    listed = sum(max(1, -(-int(b - a) // 128)) for a, b in zip(bounds, bounds[1:]))
+    assert listed > 500 // 128 + rows
+    B.idx_kv4_attention(*args, _dev(bounds), SCALE, out=out, lse=lse)
+    assert _status() == B.DEV_BAD_BOUNDS and (out == 5).all() and (lse == 5).all()
+    # one that ascends, full and clipped rows among its rows, is computed
+    cuts = np.sort(rng.integers(0, 500, rows - 1))
+    bounds = np.concatenate([[-7], cuts, [900]]).astype(np.int32)
+    B.idx_kv4_attention(*args, _dev(bounds), SCALE, out=out, lse=lse)
+    _clean()
+    cut = np.clip(bounds, 0, 500)
+    _check_rows(out, lse, q64, pool, 64, 1, [slots[a:b] for a, b in zip(cut, cut[1:])])

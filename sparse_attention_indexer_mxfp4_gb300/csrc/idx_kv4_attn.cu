@@ -753,9 +753,12 @@ __device__ __forceinline__ void load_queries(const Kv4Args &a, int b, int key_he
         }
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // the largest to [2^14, 2^15); infinities and NaN stay what they are
+        // the largest to [2^14, 2^15), as far as the power's inverse times the scale is a
+        // normal number (zero times the -inf of a masked score would be NaN; the queries that
+        // stop short of it score nothing); infinities and NaN stay what they are
         const int e = (int)(top >> 23);
-        const int up = e == 0 || e == 255 ? 0 : min(141 - e, 126);
+        const int most = max((int)(__float_as_uint(a.scale_log2) >> 23) - 1, 0);
+        const int up = e == 0 || e == 255 ? 0 : min(141 - e, min(most, 126));
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
         const float back = __uint_as_float((uint32_t)(127 - up) << 23) * a.scale_log2;
         #pragma unroll

@@ -51,3 +51,36 @@ def test_short_lists_that_descend(rows):
     _clean()
     cut = np.clip(bounds, 0, 500)
     _check_rows(out, lse, q64, pool, 64, 1, [slots[a:b] for a, b in zip(cut, cut[1:])])
+
+
+@pytest.mark.parametrize("factor,scale", [(1e-37, 1e-12), (1e-37, 1e-39), (1.0, 1e-40), (1e30, 1e-45), (0.0, 1e-12)])
+@pytest.mark.parametrize("n", [40, 700])
+def test_factors_whose_product_leaves_the_range(factor, scale, n):
+    """Queries and factors so small that every score is zero: tokens that are there weigh alike,
+    those that are not weigh nothing."""
+    rng = np.random.default_rng(n)
+    bt, pages, _ = _table(rng, [n], 64)
+    pool = ref.make_pool(rng, pages, 64, 2)
+    slots = _slots(bt, 0, n, 64)
+    q, q64 = _bf16(rng.choice([-1.0, 1.0], (2, 8, 128)) * factor)
+    ctx = _dev(np.array([n], np.int32))
+    paged = (q, _dev(pool), 64, 2, _dev(bt), ctx, 2, scale, n)
+    out, lse = B.idx_paged_kv4_attention(*paged)
+    weights = B.idx_paged_kv4_weights(*paged, lse)
+    listed, ll = B.idx_kv4_attention(q[1:], _dev(pool), 64, 2, _dev(slots.astype(np.int32)), _dev(np.array([0, n], np.int32)),
+                                     scale)
+    _clean()
+    for h in range(2):
+        k, v = ref.read(pool, 64, 2, slots, h)
+        hs = slice(4 * h, 4 * h + 4)
+        for j in range(2):
+            m = n - 1 + j
+            want = ref.attend(q64[j, hs], k[:m], v[:m], float(np.float32(scale)))
+            ref.check(_np(out[j, hs]), _np(lse[j, hs]), want, m, vmax=np.abs(v).max())
+        ref.check(_np(listed[0, hs]), _np(ll[0, hs]), want, n, vmax=np.abs(v).max())
+        # each weight is 1 / m by at most the errors of its logarithm and its exponential, and of
+        # sums of eight
+        got = _np(weights[0, h])
+        wish = np.full(n, 4 / n)
+        wish[:n - 1] += 4 / (n - 1)
+        assert (np.abs(got - wish) <= wish * (2.0 ** -19 + 2.0 ** -21 * np.log(n))).all()

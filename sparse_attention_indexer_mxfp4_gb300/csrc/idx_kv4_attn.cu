@@ -1341,7 +1341,12 @@ __global__ void __launch_bounds__(Shape<NT>::kGroups * kThreads, 1)
         // ---- the warps' sums, in absolute units, from 1 to 0 and 3 to 2, then 2 to 0
         #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float f = pow2i((int)(top_e >> (8 * i) & 255) - 127 - kScaleUp - kBias);
+            // 2^(e - 127) less what the weights were raised by, by its bits: it may lie under the
+            // least normal number, where the instruction for powers gives zero
+            constexpr int kRaised = kScaleUp + kBias;
+            const int e = top_e >> (8 * i) & 255;
+            const float f = __uint_as_float(e > kRaised ? (uint32_t)(e - kRaised) << 23
+                                                        : 0x400000u >> (kRaised - e));
             #pragma unroll
             for (int n = 0; n < NT; ++n)
                 #pragma unroll

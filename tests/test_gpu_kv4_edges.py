@@ -84,3 +84,26 @@ def test_factors_whose_product_leaves_the_range(factor, scale, n):
         wish = np.full(n, 4 / n)
         wish[:n - 1] += 4 / (n - 1)
         assert (np.abs(got - wish) <= wish * (2.0 ** -19 + 2.0 ** -21 * np.log(n))).all()
+
+
+@pytest.mark.parametrize("n", [300, 700, 9000])
+@pytest.mark.parametrize("bits", [2, 9])
+def test_values_near_the_least(n, bits):
+    """Values near the least that 32 bits hold come out as they are, not as zeros."""
+    rng = np.random.default_rng(n + bits)
+    bt, pages, _ = _table(rng, [n], 64)
+    pool = ref.make_pool(rng, pages, 64, 1)
+    m = 64
+    pool[:, m * 132:m * 136] = rng.integers(bits - 2, bits + 3, (pages, m * 4)).astype(np.uint8)
+    q, q64 = _bf16(rng.standard_normal((1, 8, 128)))
+    out, _ = B.idx_paged_kv4_attention(q, _dev(pool), 64, 1, _dev(bt), _dev(np.array([n], np.int32)), 1, SCALE, n)
+    _clean()
+    k, v = ref.read(pool, 64, 1, _slots(bt, 0, n, 64), 0)
+    o, _, pv, mag = ref.attend(q64[0], k, v, SCALE)
+    # the bounds of kv4_ref.check; sums in 32 bits' least steps (2^-149) a token and a joining, the
+    # result in bf16's (2^-133)
+    ds = 136 * 2.0 ** -23 * mag + 2.0 ** -20
+    tol = (ref.HALF_BF16 * np.abs(o) + (ref.HALF_F16 * 1.01 + 2 * ds[:, None]) * pv * (1 + ref.HALF_BF16)
+           + n * 2.0 ** -26 * np.abs(v).max() + 64 * 2.0 ** -149 + 2.0 ** -134)
+    assert (np.abs(_np(out[0]) - o) <= tol).all()
+    assert np.abs(o).max() > 8 * tol.max()  # (zeros would show)

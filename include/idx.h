@@ -833,9 +833,10 @@ idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq
 /* ------------------------------------------------------------------------
  * idx_kv4_evict -- shrink sequences to their heaviest tokens: of sequence b's n =
  * context_lens[b] tokens the last `recent` stay, and of the others the
- * budget - recent of most weight (ties: the lower position; NaN counts as the
- * least), all of them where n <= budget.  They go, in their order, to positions 0,
- * 1, ... of the pages of new_table.
+ * budget - recent of most weight (ties: the lower position), all of them where n <=
+ * budget.  They go, in their order, to positions 0, 1, ... of the pages of new_table.
+ * Infinite weights count as the largest and the least finite number, NaN as the
+ * least, and zeros of either sign are alike.
  *
  *   mass      fp32, mass[b * ld_batch + g * ld_head + t], t in [0, ld_mass): the
  *             tokens' weights.  A context past ld_mass is cut there and sets

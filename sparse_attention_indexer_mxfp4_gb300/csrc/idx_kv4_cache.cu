@@ -234,11 +234,12 @@ __device__ __forceinline__ int evict_len(const EvictArgs &a, int b)
     return min(max(a.ctx[b], 0), a.ld);
 }
 
-// What the top-k orders by: every number counts, NaN as the least.
+// What the top-k orders by: finite numbers (it passes over others), infinities as the
+// largest and the least of them, NaN as the least, zeros of either sign as one.
 __device__ __forceinline__ float orderly(float x)
 {
     constexpr float most = 3.402823466e38f;
-    return x != x ? -most : fminf(fmaxf(x, -most), most);
+    return x != x ? -most : fminf(fmaxf(x, -most), most) + 0.0f;
 }
 
 // a + b as a float and what the float lacks.

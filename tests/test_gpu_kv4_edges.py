@@ -107,3 +107,48 @@ def test_values_near_the_least(n, bits):
            + n * 2.0 ** -26 * np.abs(v).max() + 64 * 2.0 ** -149 + 2.0 ** -134)
     assert (np.abs(_np(out[0]) - o) <= tol).all()
     assert np.abs(o).max() > 8 * tol.max()  # (zeros would show)
+
+
+# --------------------------------------------------------------- eviction's order
+
+
+def _evicted(mass, budget, recent, whole):
+    """keep [B, lists, budget] of whole contexts on one page a token, which nothing depends on."""
+    nb, heads, n = mass.shape
+    page = 4096
+    blocks, new = -(-n // page), -(-budget // page)
+    pool = torch.zeros(blocks + nb * new, ref.page_stride(page, heads), dtype=torch.uint8, device="cuda")
+    bt = torch.arange(blocks, dtype=torch.int32, device="cuda").expand(nb, blocks).contiguous()
+    nt = (blocks + torch.arange(nb * new, dtype=torch.int32, device="cuda")).view(nb, new)
+    ctx = torch.full((nb,), n, dtype=torch.int32, device="cuda")
+    keep, _, _ = B.idx_kv4_evict(mass, ctx, budget, recent, pool, page, bt, nt, whole_tokens=whole)
+    _clean()
+    return keep.cpu().numpy()
+
+
+@pytest.mark.parametrize("columns", [37, 300, 2500, 9003, 262149])
+@pytest.mark.parametrize("whole", [False, True])
+def test_zeros_of_either_sign_weigh_alike(columns, whole):
+    rng = np.random.default_rng(columns)
+    heads = 2
+    mass = np.where(rng.random((2, heads, columns)) < 0.5, -0.0, 0.0).astype(np.float32)
+    budget = min(columns // 2, 1000)
+    keep = _evicted(_dev(mass), budget, 3, whole)
+    want = np.concatenate([np.arange(budget - 3), np.arange(columns - 3, columns)])
+    assert (keep == want).all()
+
+
+@pytest.mark.parametrize("columns", [37, 300, 2500, 9003, 262149])
+@pytest.mark.parametrize("whole", [False, True])
+def test_infinities_count_as_the_largest_numbers(columns, whole):
+    """As the header says: infinities as the largest and the least float, NaN as the least."""
+    rng = np.random.default_rng(columns + 1)
+    most = np.float32(3.4028235e38)
+    x = rng.choice(np.array([np.inf, most, 1, 0, -1, -most, -np.inf, np.nan], np.float32), columns)
+    mass = np.zeros((1, 2, columns), np.float32)
+    mass[0, 0] = x
+    mass[0, 1] = 0 if whole else x
+    budget = min(columns // 2, 1500)
+    keep = _evicted(_dev(mass), budget, 0, whole)
+    y = np.clip(np.where(np.isnan(x), -most, x), -most, most).astype(np.float64)
+    assert (keep == np.sort(np.lexsort((np.arange(columns), -y))[:budget])).all()

@@ -843,8 +843,11 @@ idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq
  *             IDX_DEV_BAD_BOUNDS.
  *   budget, recent  0 <= recent <= budget.
  *   whole_tokens  0: each key head keeps its own tokens.  Otherwise a token stays
- *             or goes with all its heads, by the sum of their weights (in 64 bits,
- *             rounded to 32), so that positions stay aligned with the indexer's.
+ *             or goes with all its heads, by the sum of their weights (head by head
+ *             in pairs of floats, some 48 bits, rounded once; one that leaves the
+ *             range of 32 bits on its way is infinite).  Its new position is then
+ *             the same in every head.  An indexer's own keys are not moved: the
+ *             slots that it selects do not follow.
  *   kv_pages  read through block_table and written through new_table (max_blocks
  *             and new_blocks columns valid; new_blocks * page_size >= the smaller
  *             of budget and ld_mass).  The pages that new_table names for kept

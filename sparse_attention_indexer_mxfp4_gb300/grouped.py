@@ -75,6 +75,7 @@ class GroupedLayer:
     def evict(self, mass, context_lens, budget, recent, block_table, new_table, whole_tokens=False,
               stream=None):
         """Sequences shrunk to `budget` tokens on the pages of new_table (not those they are on).
+        An indexer's own keys are not moved with them: decode_paged is the step that follows.
         Returns (keep, new context_lens, new mass)."""
         if mass.dim() != 3 or mass.shape[1] != self.kv_heads:
             raise ValueError(f"mass must be [sequences, {self.kv_heads}, columns]")
@@ -85,7 +86,7 @@ class GroupedLayer:
 class GroupedDecodeStep:
     """One decode step of a layer: the indexer's logits, top-k and slot map, then the layer's
     attention over exactly those slots.  ``case`` is the indexer's (synth.PagedCase); its block
-    table places the layer's cache too."""
+    table places the layer's cache too, so it is of sequences that were not evicted from."""
 
     def __init__(self, case, layer: GroupedLayer, q, device="cuda"):
         if case.page_size != layer.page_size or case.num_pages > layer.pages.shape[0]:

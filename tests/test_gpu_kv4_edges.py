@@ -152,3 +152,25 @@ def test_infinities_count_as_the_largest_numbers(columns, whole):
     keep = _evicted(_dev(mass), budget, 0, whole)
     y = np.clip(np.where(np.isnan(x), -most, x), -most, most).astype(np.float64)
     assert (keep == np.sort(np.lexsort((np.arange(columns), -y))[:budget])).all()
+
+
+@pytest.mark.parametrize("heads", [3, 5, 8, 11])
+@pytest.mark.parametrize("columns", [300, 2048, 9003, 262149])
+def test_sums_over_heads_are_rounded_once(heads, columns):
+    """Tokens whose heads share the same weights in different orders have one sum, and one bit more
+    in a head's weight counts: sums in 32 bits would part the first and miss the second.  (Weights
+    are multiples of 2^-30 below 1: their sums are exact in 64 bits and in pairs of floats.)"""
+    rng = np.random.default_rng(heads * columns)
+    one = rng.integers(1, 1 << 24, heads) * 2.0 ** -30
+    one[0] = 0.75 + 2.0 ** -24
+    mass = rng.permuted(np.tile(one, (columns, 1)), axis=1).T.astype(np.float32)[None]
+    ulp = np.spacing(np.float32(one.sum()))
+    heavy = rng.random(columns) < 0.1
+    mass[0, :, heavy] = one
+    for t in np.flatnonzero(heavy):  # the least weight more by the sum's own step
+        mass[0, -1, t] = np.float32(one[-1] + ulp)
+    total = mass[0].astype(np.float64).sum(0).astype(np.float32)
+    assert len(np.unique(total)) == 2 and (total[heavy] > total[~heavy].max()).all()
+    for budget in (min(heavy.sum() // 2, 1000), min(heavy.sum() + columns // 3, 4000)):
+        want = np.sort(np.lexsort((np.arange(columns), -total.astype(np.float64)))[:budget])
+        assert (_evicted(_dev(mass), int(budget), 0, True) == want).all()

@@ -40,9 +40,8 @@ __device__ __forceinline__ uint32_t quantise8(uint4 raw, int &bits)
         return 0;
     }
     bits = max(0, (int)(top >> 23) - 2 + ((top & 0x7fffffu) > 0x400000u));
-    // 2^(127 - bits)
-    const float inv = bits < 254 ? __uint_as_float((uint32_t)(254 - bits) << 23)
-                                 : __uint_as_float(0x400000u);
+    // 2^(127 - bits) (the largest finite magnitude has 253)
+    const float inv = __uint_as_float((uint32_t)(254 - bits) << 23);
     uint32_t out = 0;
     #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -700,7 +700,9 @@ size_t idx_latent_prefill_workspace_size(int Tq, int Tk, int H);
  *     K codes  [kv_heads][page_size][64]      V codes  [kv_heads][page_size][64]
  *     K scales [kv_heads][page_size][4]       V scales [kv_heads][page_size][4]
  * A call's D is the heads' dimension: 128 is supported.  Pages are of less than
- * 2^31 bytes and hold less than 2^31 slots in all.
+ * 2^31 bytes and hold less than 2^31 slots in all.  A written tensor whose rows or
+ * heads overlap by their strides is IDX_ERR_INVALID_ARG (one stride has to pass over
+ * all that the other covers).
  * ---------------------------------------------------------------------- */
 
 /* ------------------------------------------------------------------------
@@ -818,7 +820,8 @@ size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int kv_heads, 
  *             row that saw nothing, counts as 0).
  *   mass      fp32, mass[b * ld_batch + g * ld_head + t], t in [0, width); NULL
  *             stands for zeros.  width >= max_model_len.
- *   out       the same shape, strides ldo_batch, ldo_head; may be mass.
+ *   out       the same shape, strides ldo_batch, ldo_head; mass itself, or no
+ *             element of it (where their ranges meet the strides are the same).
  * Sums are in 32 bits, in an order that the arguments alone decide.
  * ---------------------------------------------------------------------- */
 idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
@@ -857,6 +860,8 @@ idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq
  *   new_lens  int32 [B]: min(n, budget).
  *   new_mass  fp32 [B, kv_heads, budget]: their weights, then zeros.
  *   ws        device scratch of idx_kv4_evict_workspace_size bytes (0: NULL).
+ * keep, new_lens and new_mass share no memory with one another, nor with mass,
+ * context_lens or the tables.
  * A page outside the pool sets IDX_DEV_BAD_PAGE: tokens from it become zeros,
  * tokens to it are dropped.
  * Supported: D = 128, B * lists <= 65535.

@@ -37,6 +37,8 @@ extern "C" idx_status idx_grouped_prefill(const uint16_t *q, int64_t ldq_row, in
         return IDX_ERR_WORKSPACE;
     if (Tq > INT32_MAX - 2 * kRows || Tk > INT32_MAX - 2 * kTile)
         return IDX_ERR_UNSUPPORTED;  // rows and tiles are counted past the end
+    if (!lie_apart({out, Tq, ldo_row, H, ldo_head, D, 2}))
+        return IDX_ERR_INVALID_ARG;
     CUtensorMap tq, tk, tv;
     if (!encode_rows(&tq, q, kV, H, Tq, ldq_row, ldq_head))
         return IDX_ERR_UNSUPPORTED;

@@ -1889,6 +1889,8 @@ extern "C" idx_status idx_kv4_attention(const uint16_t *q, int64_t ldq_row, int6
         return ok;
     if (!aligned16(out) || (ldo_row | ldo_head) % 8 != 0 || num_slots > INT32_MAX - 4 * kTile)
         return IDX_ERR_UNSUPPORTED;
+    if (!lie_apart({out, R, ldo_row, H, ldo_head, D, 2}))
+        return IDX_ERR_INVALID_ARG;
     Kv4Args a = {};
     a.q = q;
     a.ldq_row = ldq_row;
@@ -1935,6 +1937,8 @@ extern "C" idx_status idx_paged_kv4_attention(
     if (!aligned16(out) || (ldo_row | ldo_head) % 8 != 0 || cols > INT32_MAX / 2 ||
         (int64_t)B * next_n > INT32_MAX || max_model_len > INT32_MAX - 4 * kTile)
         return IDX_ERR_UNSUPPORTED;
+    if (!lie_apart({out, (int64_t)B * next_n, ldo_row, H, ldo_head, D, 2}))
+        return IDX_ERR_INVALID_ARG;
     Kv4Args a = {};
     a.q = q;
     a.ldq_row = ldq_row;
@@ -1989,6 +1993,10 @@ extern "C" idx_status idx_paged_kv4_weights(
     if (cols > INT32_MAX / 2 || (int64_t)B * next_n > INT32_MAX || width > INT32_MAX - 4 * kTile ||
         kv_heads > INT32_MAX / 2 || tiles > INT32_MAX / kv_heads)
         return IDX_ERR_UNSUPPORTED;
+    const Strided sums = {out, B, ldo_batch, kv_heads, ldo_head, width, 4};
+    if (!lie_apart(sums) ||
+        (mass && mass != out && !lie_apart(sums, {mass, B, ld_batch, kv_heads, ld_head, width, 4})))
+        return IDX_ERR_INVALID_ARG;
     Kv4Args a = {};
     a.q = q;
     a.ldq_row = ldq_row;

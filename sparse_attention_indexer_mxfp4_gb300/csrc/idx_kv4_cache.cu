@@ -605,6 +605,10 @@ extern "C" idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_strid
     if (!aligned16(k_out) || !aligned16(v_out) ||
         (ldk_row | ldk_head | ldv_row | ldv_head) % 8 != 0 || (int64_t)N * kv_heads > INT32_MAX)
         return IDX_ERR_UNSUPPORTED;
+    const Strided keys = {k_out, N, ldk_row, kv_heads, ldk_head, D, 2};
+    const Strided values = {v_out, N, ldv_row, kv_heads, ldv_head, D, 2};
+    if (!lie_apart(keys) || !lie_apart(values) || !lie_apart(keys, values))
+        return IDX_ERR_INVALID_ARG;
     unsigned int *status = device_status_ptr();
     if (!status)
         return IDX_ERR_CUDA;
@@ -676,6 +680,23 @@ extern "C" idx_status idx_kv4_evict(const float *mass, int64_t ld_batch, int64_t
         idx_kv4_evict_workspace_size(B, kv_heads, ld_mass, budget, recent, whole_tokens);
     if (need > 0 && (!ws || !aligned16(ws) || ws_bytes < need))
         return IDX_ERR_WORKSPACE;
+    // every part of the call reads the inputs while others write: no output may be one of them
+    struct Bytes {
+        const void *p;
+        __int128 n;
+    };
+    const Bytes parts[] = {
+        {keep, (__int128)4 * B * lists * budget},
+        {new_lens, (__int128)4 * B},
+        {new_mass, (__int128)4 * B * kv_heads * budget},
+        {mass, span({mass, B, ld_batch, kv_heads, ld_head, ld_mass, 4})},
+        {context_lens, (__int128)4 * B},
+        {block_table, span({block_table, B, bt_stride, 1, 0, max_blocks, 4})},
+        {new_table, span({new_table, B, new_stride, 1, 0, new_blocks, 4})}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 7; ++j)
+            if (meet(parts[i].p, parts[i].n, parts[j].p, parts[j].n))
+                return IDX_ERR_INVALID_ARG;
     EvictArgs a = {};
     a.mass = mass;
     a.ld_batch = ld_batch;

@@ -174,3 +174,61 @@ def test_sums_over_heads_are_rounded_once(heads, columns):
     for budget in (min(heavy.sum() // 2, 1000), min(heavy.sum() + columns // 3, 4000)):
         want = np.sort(np.lexsort((np.arange(columns), -total.astype(np.float64)))[:budget])
         assert (_evicted(_dev(mass), int(budget), 0, True) == want).all()
+
+
+# ------------------------------------------------------------- written views
+
+
+def test_views_beside_one_another():
+    """Sums and read-back rows that share storage, not elements, and outputs whose heads are
+    outermost; views that share elements are refused before anything is launched."""
+    rng = np.random.default_rng(60)
+    page, heads, ctx = 64, 2, [70, 300]
+    bt, pages, _ = _table(rng, ctx, page)
+    pool = _dev(ref.make_pool(rng, pages, page, heads))
+    lens = _dev(np.array(ctx, np.int32))
+    q, _ = _bf16(rng.standard_normal((2, 8, 128)))
+    paged = (q, pool, page, heads, _dev(bt), lens, 1, SCALE, 320)
+    out, lse = B.idx_paged_kv4_attention(*paged)
+    turned = torch.zeros(8, 2, 128, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    B.idx_paged_kv4_attention(*paged, out=turned)
+    mass = torch.rand(2, heads, 330, device="cuda")
+    want = B.idx_paged_kv4_weights(*paged, lse, mass, torch.empty_like(mass))
+    for shape, at in [((2, 2, heads, 330), lambda t, i: t[:, i]), ((2, heads, 2, 330), lambda t, i: t[:, :, i]),
+                      ((2, heads, 660), lambda t, i: t[..., 330 * i:330 * i + 330]),
+                      ((heads, 2, 2, 330), lambda t, i: t[:, i].transpose(0, 1))]:
+        both = torch.zeros(shape, device="cuda")
+        for i in (0, 1):
+            both.zero_()
+            at(both, i).copy_(mass)
+            got = B.idx_paged_kv4_weights(*paged, lse, at(both, i), at(both, 1 - i))
+            assert torch.equal(got, want) and torch.equal(at(both, i), mass)
+    # one row of sums read for all heads, written elsewhere
+    one = mass[:, :1].expand(2, heads, 330)
+    assert torch.equal(B.idx_paged_kv4_weights(*paged, lse, one, torch.empty_like(mass)),
+                       B.idx_paged_kv4_weights(*paged, lse, one.contiguous()))
+    cu = _dev(np.array([0, 70, 370], np.int32))
+    rows = [torch.zeros(370, heads, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    B.idx_kv4_gather(pool, page, _dev(bt), cu, *rows)
+    for shape, at in [((370, heads, 2, 128), lambda t, i: t[:, :, i]), ((370, 2, heads, 128), lambda t, i: t[:, i]),
+                      ((2, heads, 370, 128), lambda t, i: t[i].transpose(0, 1)), ((heads, 370, 256), lambda t, i: t.transpose(0, 1)[..., 128 * i:128 * i + 128])]:
+        both = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
+        B.idx_kv4_gather(pool, page, _dev(bt), cu, at(both, 0), at(both, 1))
+        assert torch.equal(at(both, 0), rows[0]) and torch.equal(at(both, 1), rows[1])
+    _clean()
+    assert torch.equal(turned, out)
+    wide, held = torch.zeros(2, heads, 331, device="cuda"), torch.zeros(2, 1, 330, device="cuda")
+    spot = torch.zeros(370, 1, 128, dtype=torch.bfloat16, device="cuda")
+    new = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+    for call in [lambda: B.idx_paged_kv4_weights(*paged, lse, held.expand(2, heads, 330)),
+                 lambda: B.idx_paged_kv4_weights(*paged, lse, mass, held.expand(2, heads, 330)),
+                 lambda: B.idx_paged_kv4_weights(*paged, lse, wide[..., :-1], wide[..., 1:]),
+                 lambda: B.idx_paged_kv4_attention(*paged, out=spot[:2].expand(2, 8, 128)),
+                 lambda: B.idx_kv4_gather(pool, page, _dev(bt), cu, spot.expand(370, heads, 128), rows[1]),
+                 lambda: B.idx_kv4_gather(pool, page, _dev(bt), cu, rows[0], rows[0]),
+                 lambda: B.idx_kv4_evict(mass, lens, 60, 4, pool, page, _dev(bt), new, new_lens=lens),
+                 lambda: B.idx_kv4_evict(mass, lens, 330, 4, pool, page, _dev(bt), new.expand(2, 6).contiguous(), new_mass=mass)]:
+        with pytest.raises(B.IndexerError, match="INVALID"):
+            call()
+    torch.cuda.synchronize()
+    assert lens.tolist() == ctx and not wide.any() and not held.any() and not spot.any()

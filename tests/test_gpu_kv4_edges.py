@@ -109,6 +109,75 @@ def test_values_near_the_least(n, bits):
     assert np.abs(o).max() > 8 * tol.max()  # (zeros would show)
 
 
+# ------------------------------------------------------ shares of several tiles
+
+
+@pytest.mark.parametrize("page", [64, 100])
+@pytest.mark.parametrize("group,next_n", [(1, 1), (4, 2), (40, 1)])
+@pytest.mark.parametrize("bad", [False, True])
+def test_shares_of_several_tiles(page, group, next_n, bad):
+    """Lists with several times more tiles than shares, sequences that end inside shares, pages
+    outside the pool among them; weights into a tensor of their own and in place."""
+    rng = np.random.default_rng(page + group + bad)
+    heads = 8
+    ctx = [0, 1, 63] + [int(x) for x in rng.integers(3000, 9001, 12)]
+    bt, pages, _ = _table(rng, ctx, page)
+    pool = ref.make_pool(rng, pages, page, heads)
+    slots = [_slots(bt, b, n, page) for b, n in enumerate(ctx)]
+    wrong, there = bt.copy(), [np.ones(n, bool) for n in ctx]
+    if bad:
+        for b in (4, 9):
+            for at, p in ((0, -1), (17, pages), (ctx[b] // page, -5)):
+                wrong[b, at] = p
+                there[b][at * page:(at + 1) * page] = False
+    q, q64 = _bf16(rng.standard_normal((len(ctx) * next_n, heads * group, 128)))
+    longest = bt.shape[1] * page
+    args = (q, _dev(pool), page, heads, _dev(wrong), _dev(np.array(ctx, np.int32)), next_n, SCALE, longest)
+    out, lse = B.idx_paged_kv4_attention(*args)
+    wide = torch.rand(len(ctx), heads, longest + 5, device="cuda")
+    mass = wide[:, :, 2:-2]
+    before = _np(mass)
+    own = torch.full_like(wide, 7.0)[:, :, 2:-2]
+    B.idx_paged_kv4_weights(*args, lse, mass, own)
+    edges = wide[:, :, [0, 1, -2, -1]].clone()
+    B.idx_paged_kv4_weights(*args, lse, mass)
+    assert _status() == (B.DEV_BAD_PAGE if bad else 0)
+    assert torch.equal(mass, own) and torch.equal(wide[:, :, [0, 1, -2, -1]], edges)
+    got, blocks = _np(own), -(-group * next_n // 32)
+    # each page is read through kv4_ref once a sampled head
+    for b, h in [(0, 0), (1, 5), (2, 7), (3, 0), (4, 3), (9, 7), (9, 2), (14, 7)]:
+        k, v = ref.read(pool, page, heads, slots[b], h)
+        hs = slice(h * group, (h + 1) * group)
+        want, most = np.zeros(longest + 1), 0.0
+        for j in range(next_n):
+            r, end = b * next_n + j, max(0, ctx[b] - next_n + 1 + j)
+            seen = there[b][:end]
+            ref.check(_np(out[r, hs]), _np(lse[r, hs]), ref.attend(q64[r, hs], k[:end][seen], v[:end][seen], SCALE), end,
+                      vmax=np.abs(v).max() if v.size else 0)
+            if seen.any():
+                s = q64[r, hs] @ k[:end].T * SCALE
+                want[:end] += np.where(seen, np.exp(s - _np(lse[r, hs])[:, None]), 0).sum(0)
+                most = max(most, (np.abs(q64[r, hs]) @ np.abs(k).T).max() * SCALE)
+        # as for short contexts, and a rounding of the sum so far for each block of columns
+        ds = 136 * 2.0 ** -23 * most + 2.0 ** -20 + next_n * group * 2.0 ** -24
+        base = before[b, h]
+        assert (np.abs(got[b, h] - base - want) <= 1.1 * ds * want + (blocks + 1) * 2.0 ** -24 * (base + want)).all(), (b, h)
+
+
+@pytest.mark.parametrize("page", [64, 100])
+def test_teams_of_several_steps(page):
+    """Few long contexts, which clusters share, several tiles a group."""
+    rng = np.random.default_rng(page)
+    ctx, heads = [9000, 7001], 2
+    assert B.kv4_attention_workspace_size(4, 16, heads, 9000, next_n=2) == 0
+    bt, pages, _ = _table(rng, ctx, page)
+    pool = ref.make_pool(rng, pages, page, heads)
+    q, q64 = _bf16(rng.standard_normal((4, 16, 128)))
+    out, lse = B.idx_paged_kv4_attention(q, _dev(pool), page, heads, _dev(bt), _dev(np.array(ctx, np.int32)), 2, SCALE, 9000)
+    _clean()
+    _check_rows(out, lse, q64, pool, page, heads, [_slots(bt, b, n, page)[:n - 1 + j] for b, n in enumerate(ctx) for j in (0, 1)])
+
+
 # --------------------------------------------------------------- eviction's order
 
 

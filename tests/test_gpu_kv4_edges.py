@@ -178,6 +178,31 @@ def test_teams_of_several_steps(page):
     _check_rows(out, lse, q64, pool, page, heads, [_slots(bt, b, n, page)[:n - 1 + j] for b, n in enumerate(ctx) for j in (0, 1)])
 
 
+@pytest.mark.parametrize("page", [64, 48])
+def test_weights_with_a_length_for_each_row(page):
+    """Rows of one sequence that see more, fewer and none of its tokens, past the limit among them."""
+    rng = np.random.default_rng(page)
+    bt, pages, _ = _table(rng, [900, 700], page)
+    pool = ref.make_pool(rng, pages, page, 2)
+    q, q64 = _bf16(rng.standard_normal((6, 8, 128)))
+    per, most = np.array([900, 3, 0, 650, 700, -2], np.int32), 800
+    args = (q, _dev(pool), page, 2, _dev(bt), _dev(per), 3, SCALE, most)
+    _, lse = B.idx_paged_kv4_attention(*args, ctx_per_row=True)
+    got = B.idx_paged_kv4_weights(*args, lse, ctx_per_row=True)
+    _clean()
+    want, mag = np.zeros((2, 2, most)), 0.0
+    for r, end in enumerate(np.clip(per, 0, most)):
+        for h in range(2):
+            if end:
+                k, _ = ref.read(pool, page, 2, _slots(bt, r // 3, end, page), h)
+                hs = slice(4 * h, 4 * h + 4)
+                want[r // 3, h, :end] += np.exp(q64[r, hs] @ k.T * SCALE - _np(lse[r, hs])[:, None]).sum(0)
+                mag = max(mag, (np.abs(q64[r, hs]) @ np.abs(k).T).max() * SCALE)
+    # each weight by its score's and its exponential's errors, sums of twelve
+    ds = 136 * 2.0 ** -23 * mag + 2.0 ** -20 + 12 * 2.0 ** -24
+    assert (np.abs(_np(got) - want) <= 1.1 * ds * want + 2.0 ** -23 * want).all()
+
+
 # --------------------------------------------------------------- eviction's order
 
 

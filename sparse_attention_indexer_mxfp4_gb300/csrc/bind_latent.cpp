@@ -476,6 +476,17 @@ int key_heads(PyObject *o, int64_t H)
     return g;
 }
 
+// A pool whose rows hold a page (a row's bytes may be fewer than the stride tells).
+const at::Tensor &need_kv4_pages(PyObject *o, int page_size, int64_t heads)
+{
+    const at::Tensor &t = need_pages(o);
+    const int64_t least = std::max(page_size, 0) * heads * 2 * (kHead / 2 + kHead / 32);
+    if (t.size(0) > 0 && t.size(1) < least)
+        refuse("kv_pages must hold " + std::to_string(least) + " bytes a page, got " +
+               std::to_string(t.size(1)));
+    return t;
+}
+
 // fp32 [B, heads, columns] with contiguous columns.
 const at::Tensor &need_mass(PyObject *o, int64_t B, int64_t heads, int64_t least, const char *name)
 {
@@ -535,7 +546,9 @@ PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t)
     const int64_t T = k.size(0), G = k.size(1);
     if (v.size(0) != T || v.size(1) != G)
         refuse("k and v must hold the same tokens and heads");
-    const at::Tensor &pages = need_pages(a[3]), &slots = need(a[5], at::kLong, "slot_mapping");
+    const int page_size = int_of(a[4], "page_size");
+    const at::Tensor &pages = need_kv4_pages(a[3], page_size, G);
+    const at::Tensor &slots = need(a[5], at::kLong, "slot_mapping");
     need_count(slots, T, "slot_mapping");
     on_one_device({&k, &v, &pages, &slots});
     return call(
@@ -544,13 +557,11 @@ PyObject *kv4_store(PyObject *, PyObject *const *a, Py_ssize_t)
         (const uint16_t *)address<uint16_t>(k), ld(k, 0, G * kHead), ld(k, 1, kHead),
         (const uint16_t *)address<uint16_t>(v), ld(v, 0, G * kHead), ld(v, 1, kHead),
         count(T, "k"), count(G, "k"), (int)kHead, address<uint8_t>(pages), page_stride(pages),
-        count(pages.size(0), "kv_pages"), int_of(a[4], "page_size"),
-        (const int64_t *)address<int64_t>(slots));
+        count(pages.size(0), "kv_pages"), page_size, (const int64_t *)address<int64_t>(slots));
 }
 
 PyObject *kv4_gather(PyObject *, PyObject *const *a, Py_ssize_t)
 {
-    const at::Tensor &pages = need_pages(a[1]);
     const at::Tensor &cu = need(a[4], at::kInt, "cu_lens");
     const int64_t B = cu.numel() - 1;
     if (B < 0)
@@ -560,6 +571,8 @@ PyObject *kv4_gather(PyObject *, PyObject *const *a, Py_ssize_t)
     const int64_t N = k.size(0), G = k.size(1);
     if (v.size(0) != N || v.size(1) != G)
         refuse("k_out and v_out must hold the same tokens and heads");
+    const int page_size = int_of(a[2], "page_size");
+    const at::Tensor &pages = need_kv4_pages(a[1], page_size, G);
     at::Tensor s;
     if (a[7] != Py_None) {
         s = need(a[7], at::kInt, "seq_starts");
@@ -572,7 +585,7 @@ PyObject *kv4_gather(PyObject *, PyObject *const *a, Py_ssize_t)
         [&] { return Py_BuildValue("(OO)", a[5], a[6]); },
         [&] { return Py_BuildValue("(OOOOOO)", a[1], a[3], a[4], a[5], a[6], a[7]); },
         (const uint8_t *)address<uint8_t>(pages), page_stride(pages), count(pages.size(0), "kv_pages"),
-        int_of(a[2], "page_size"), count(G, "k_out"), (int)kHead,
+        page_size, count(G, "k_out"), (int)kHead,
         (const int32_t *)address<int32_t>(table), table.size(1),
         count(table.size(1), "block_table"), (const int32_t *)address<int32_t>(cu), starts,
         count(B, "cu_lens"), count(N, "k_out"), address<uint16_t>(k), ld(k, 0, G * kHead),
@@ -582,10 +595,11 @@ PyObject *kv4_gather(PyObject *, PyObject *const *a, Py_ssize_t)
 PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t)
 {
     const at::Tensor &q = need_heads(a[1], 3, kHead, "q");
-    const at::Tensor &pages = need_pages(a[2]);
     const at::Tensor &slots = need(a[5], at::kInt, "slots"), &indptr = need(a[6], at::kInt, "indptr");
     const int R = count(q.size(0), "q"), H = count(q.size(1), "q"), G = key_heads(a[4], H);
     need_count(indptr, (int64_t)R + 1, "indptr");
+    const int page_size = int_of(a[3], "page_size");
+    const at::Tensor &pages = need_kv4_pages(a[2], page_size, G);
     Outputs o(a[8], a[9], a[10], q, kHead);
     on_one_device({&q, &pages, &slots, &indptr, &o.out, &o.lse, &o.ws});
     const size_t size = f_kv4_size(R, 1, H, G, slots.numel());
@@ -599,7 +613,7 @@ PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t)
         },
         (const uint16_t *)address<uint16_t>(q), ld(q, 0, H * kHead), ld(q, 1, kHead),
         (const uint8_t *)address<uint8_t>(pages), page_stride(pages),
-        count(pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
+        count(pages.size(0), "kv_pages"), page_size,
         (const int32_t *)address<int32_t>(slots), (const int32_t *)address<int32_t>(indptr),
         slots.numel(), R, H, G, (int)kHead, float_of(a[7]), o.out_at(), o.ld_row, o.ld_head,
         o.lse_at(), o.ld_lse, o.ws_at(), o.ws_bytes);
@@ -608,7 +622,7 @@ PyObject *kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t)
 // What the paged calls share.
 struct Paged {
     const at::Tensor &q, &pages, &table, &lens;
-    int R, H, G, next, B, per_row, longest;
+    int R, H, G, next, B, per_row, longest, page_size;
 
     Paged(PyObject *const *a, PyObject *per)
         : q(need_heads(a[1], 3, kHead, "q")), pages(need_pages(a[2])),
@@ -625,6 +639,8 @@ struct Paged {
         need_count(lens, per_row ? R : B, "context_lens");
         need_table(a[5], B, "block_table");
         longest = int_of(a[9], "max_model_len");
+        page_size = int_of(a[3], "page_size");
+        need_kv4_pages(a[2], page_size, G);
     }
 };
 
@@ -644,7 +660,7 @@ PyObject *paged_kv4_attention(PyObject *, PyObject *const *a, Py_ssize_t)
         },
         (const uint16_t *)address<uint16_t>(p.q), ld(p.q, 0, p.H * kHead), ld(p.q, 1, kHead),
         (const uint8_t *)address<uint8_t>(p.pages), page_stride(p.pages),
-        count(p.pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
+        count(p.pages.size(0), "kv_pages"), p.page_size,
         (const int32_t *)address<int32_t>(p.table), p.table.size(1),
         (const int32_t *)address<int32_t>(p.lens), p.per_row, p.B, p.next, p.longest, p.H, p.G,
         (int)kHead, float_of(a[8]), o.out_at(), o.ld_row, o.ld_head, o.lse_at(), o.ld_lse,
@@ -677,7 +693,7 @@ PyObject *paged_kv4_weights(PyObject *, PyObject *const *a, Py_ssize_t)
         },
         (const uint16_t *)address<uint16_t>(p.q), ld(p.q, 0, p.H * kHead), ld(p.q, 1, kHead),
         (const uint8_t *)address<uint8_t>(p.pages), page_stride(p.pages),
-        count(p.pages.size(0), "kv_pages"), int_of(a[3], "page_size"),
+        count(p.pages.size(0), "kv_pages"), p.page_size,
         (const int32_t *)address<int32_t>(p.table), p.table.size(1),
         (const int32_t *)address<int32_t>(p.lens), p.per_row, p.B, p.next, p.longest, p.H, p.G,
         (int)kHead, float_of(a[8]), (const float *)address<float>(lse), ld(lse, 0, p.H), ld(lse, 1, 1),
@@ -690,7 +706,7 @@ PyObject *paged_kv4_weights(PyObject *, PyObject *const *a, Py_ssize_t)
 PyObject *kv4_evict(PyObject *, PyObject *const *a, Py_ssize_t)
 {
     const at::Tensor &mass = need_mass(a[1], -1, -1, 0, "mass");
-    const at::Tensor &lens = need(a[2], at::kInt, "context_lens"), &pages = need_pages(a[5]);
+    const at::Tensor &lens = need(a[2], at::kInt, "context_lens");
     const int B = count(mass.size(0), "mass"), G = count(mass.size(1), "mass");
     const int columns = count(mass.size(2), "mass");
     need_count(lens, B, "context_lens");
@@ -702,6 +718,7 @@ PyObject *kv4_evict(PyObject *, PyObject *const *a, Py_ssize_t)
     const at::Tensor &table = need_table(a[7], B, "block_table");
     const at::Tensor &fresh = need_table(a[8], B, "new_table");
     const int whole = truth_of(a[9]), lists = whole ? 1 : G, page_size = int_of(a[6], "page_size");
+    const at::Tensor &pages = need_kv4_pages(a[5], page_size, G);
     if (page_size > 0 && fresh.size(1) * page_size < std::min(budget, columns))
         refuse("new_table has no room for the tokens that stay");
     at::Tensor keep_t, new_lens, new_mass, ws;

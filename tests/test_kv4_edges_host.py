@@ -1,9 +1,10 @@
 """Refusals of tensors whose elements overlap where they are written, by the C entry points (every
-call here fails its host checks, so no pointer is followed)."""
+call here fails its host checks, so no pointer is followed), and of views of a pool that do not
+hold its pages, by the binding."""
 import pytest
 
 from sparse_attention_indexer_mxfp4_gb300 import _binding as B
-from test_kv4_host import FAKE, INVALID, STRIDE
+from test_kv4_host import CALLS, FAKE, INVALID, STRIDE, U8, _z
 
 FAR = FAKE << 16
 ATTENTION = [FAKE, 8192, 128, FAKE, STRIDE, 10, 64, FAKE, FAKE, 90000, 4, 64, 8, 128, 0.1, FAR, 8192, 128, FAKE, 64, FAKE,
@@ -46,3 +47,17 @@ def test_written_elements_overlap(name, args, changes):
     for at, value in changes.items():
         a[at] = value
     assert getattr(B.lib(), name)(*a) == INVALID
+
+
+@pytest.mark.parametrize("name,at", [("store", 2), ("gather", 0), ("attention", 1), ("paged", 1), ("weights", 1), ("evict", 4)])
+def test_rows_narrower_than_a_page(name, at):
+    """The stride of such a view is a page's, its rows are not: bytes outside it were touched."""
+    call, prepare, good = CALLS[name]
+    for f in (call, prepare):
+        args = good()
+        args[at] = _z(4, B.kv4_page_bytes(64, 2), d=U8)[:, :64 * 2 * 136 - 1]
+        with pytest.raises(ValueError, match="bytes a page"):
+            f(*args)
+        args[at] = _z(4, B.kv4_page_bytes(64, 2) + 48, d=U8)[:, :64 * 2 * 136]
+        with pytest.raises(ValueError, match="CUDA"):  # wide enough: the next check
+            f(*args)

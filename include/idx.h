@@ -776,9 +776,12 @@ idx_status idx_kv4_gather(const uint8_t *kv_pages, int64_t page_stride_bytes, in
  * indptr that descends, and lists more tiles than num_slots tokens in R rows have,
  * sets IDX_DEV_BAD_BOUNDS and nothing is written.
  * Queries, keys and weights enter the products in 16 bits that hold queries and
- * codes exactly (a query element 2^29 under its row's largest loses bits); scores,
- * maxima and sums are held in 32.  The order of the sums depends on the arguments
- * and the lengths alone.  Values up to 2^70 in magnitude keep the sums in range.
+ * codes exactly (a query element 2^29 under its row's largest loses bits); weights
+ * are rounded to f16, and to bf16 beside a value scale that is NaN or over 2^15 under
+ * the largest met; scores, maxima and sums are held in 32.  The order of the sums
+ * depends on the arguments and the lengths alone.  Keys and values up to 2^70 in
+ * magnitude keep scores and sums in range; values 2^120 under the largest scale of
+ * their 32 elements in the list may count as zero.
  * Supported: D = 128, H a multiple of kv_heads, up to 2^31 tiles (128 tokens of a
  * row and key head), scale * log2(e) finite.
  * ---------------------------------------------------------------------- */

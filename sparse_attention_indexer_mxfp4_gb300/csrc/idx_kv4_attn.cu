@@ -1700,7 +1700,9 @@ int part_of(int nt)
 // CTAs of a team for so many units of at most so many tiles: enough for a tile a group,
 // as far as the SMs go; 0 where groups would have too many, or all tiles are so few
 // that their pieces are joined sooner than a cluster starts (us, list and teams: 28
-// tiles 8.4 and 9.3, 256 11.5 and 11.1, 512 14.6 and 13.0, 648 14.5 and 11.8).
+// tiles 8.4 and 9.3, 256 11.5 and 11.1, 512 14.6 and 13.0, 648 14.5 and 11.8; one to
+// three sequences).  Of ragged slots the host knows the list's length, not its rows', and
+// takes that for the longest: batches of rows mostly go without teams.
 int team_of(int64_t units, int64_t tiles, int nt)
 {
     const int sms = sm_count(), groups = groups_of(nt);

@@ -825,7 +825,8 @@ size_t idx_kv4_attention_workspace_size(int R, int next_n, int H, int kv_heads, 
  *             stands for zeros.  width >= max_model_len.
  *   out       the same shape, strides ldo_batch, ldo_head; mass itself, or no
  *             element of it (where their ranges meet the strides are the same).
- * Sums are in 32 bits, in an order that the arguments alone decide.
+ * Sums are in 32 bits, in an order that the arguments alone decide; a weight under
+ * 2^-126 counts as zero.
  * ---------------------------------------------------------------------- */
 idx_status idx_paged_kv4_weights(const uint16_t *q, int64_t ldq_row, int64_t ldq_head,
                                  const uint8_t *kv_pages, int64_t page_stride_bytes,
